@@ -405,6 +405,118 @@ m3_status m3scan_bwd_noalloc(const m3_dims* dims, m3_dtype act,
                              float* d_a_log, float* dD,
                              m3_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm over the last dimension, with the f32 residual stream of a
+ * pre-norm block:
+ *
+ *   r = x + residual,  y = (r - mean) * rstd * weight + bias
+ *   mean = sum r / dim,  rstd = 1 / sqrt(sum (r - mean)^2 / dim + eps)
+ *
+ *   x, y, dy, dx                        : [rows, dim]  activation dtype
+ *   residual, residual_out, d_residual_out, d_residual : [rows, dim]  float32
+ *   weight, bias, d_weight, d_bias      : [dim]        float32
+ *   mean, rstd                          : [rows]       float32
+ *
+ * Statistics and sums are f32.  dim up to 16384 when it is a multiple of 8
+ * (then rows that start on 16 bytes run the vector kernels; other pointers
+ * up to 8192 columns), up to 8192 otherwise.  The parameter gradients are
+ * fixed-order sums: identical bits on every call.
+ */
+typedef struct {
+    int64_t rows, dim;
+    float eps;                      /* >= 0 */
+    int32_t accumulate_param_grads; /* 1: d_weight, d_bias are added to; 0: overwritten */
+} m3_norm_dims;
+
+typedef struct {
+    int64_t workspace_bytes;        /* of m3scan_norm_bwd */
+} m3_norm_plan;
+
+m3_status m3scan_norm_plan(const m3_norm_dims* dims, m3_dtype act, m3_norm_plan* out);
+
+/* residual NULL: r = x.  bias NULL: none.  residual_out (r, the stream the
+ * block adds to), mean and rstd are written where they are not NULL; the
+ * backward needs mean, rstd and r. */
+m3_status m3scan_norm_fwd(const m3_norm_dims* dims, m3_dtype act, const void* x,
+                          const float* residual, const float* weight, const float* bias, void* y,
+                          float* residual_out, float* mean, float* rstd, m3_stream_t stream);
+
+/* normed: what the forward normalised, of normed_dtype: r (M3_F32), or x in
+ * the activation dtype when there was no residual.  d_residual_out (NULL =
+ * zero) is the gradient that reaches r past the norm; the sum of both is
+ * written to dx (activation dtype) and, where it is not NULL, to d_residual
+ * (float32).  d_weight and d_bias may be NULL. */
+m3_status m3scan_norm_bwd(const m3_norm_dims* dims, m3_dtype act, const void* dy,
+                          const void* normed, m3_dtype normed_dtype, const float* weight,
+                          const float* mean, const float* rstd, const float* d_residual_out,
+                          void* dx, float* d_residual, float* d_weight, float* d_bias,
+                          void* workspace, size_t workspace_bytes, m3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: a linear recurrence whose state S [head_k, head_v] per
+ * (batch row, value head) forgets by exp(g) and replaces what it holds under
+ * the key k_t by a blend with v_t:
+ *
+ *   S'  = exp(g_t) S_{t-1}
+ *   u   = beta_t (v_t - S'^T k_t)
+ *   S_t = S' + k_t u^T
+ *   o_t = scale S_t^T q_t
+ *
+ * with q and k divided by sqrt(sum of squares + 1e-6) first when qk_l2norm
+ * is 1.  Value head h uses key head h / (v_heads / k_heads).
+ *
+ *   q, k, dq, dk  : [batch, seq_len, k_heads, head_k]  activation dtype
+ *   v, dv         : [batch, seq_len, v_heads, head_v]  activation dtype
+ *   o, d_o        : the same, dense
+ *   g, beta, dg, dbeta : [batch, seq_len, v_heads]     activation dtype, dense
+ *   state, state_out, d_state, d_state_out : [batch, v_heads, head_k, head_v] float32
+ *   ckpt          : [batch, v_heads, n_chunks, head_k, head_v] float32, the
+ *                   state before step c * chunk (opaque to the caller)
+ *
+ * g is a log decay: normally <= 0; -inf forgets everything.  head_k and
+ * head_v are multiples of 8 up to 128.  Activation and state pointers are
+ * 16-byte aligned.  All results are the same bits on every call.
+ */
+typedef struct {
+    int64_t batch, seq_len, k_heads, v_heads, head_k, head_v;
+    /* Elements between consecutive tokens of q, k, v and of dq, dk, dv (the
+       rows of a batch row follow each other at the same stride); 0 = dense.
+       A larger stride lets them be columns of one projection's output and of
+       its gradient.  stride x element size must be a multiple of 16. */
+    int64_t q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
+    float scale;       /* 0 = 1 / sqrt(head_k) */
+    int32_t qk_l2norm; /* 1: q and k are normalised in the kernels */
+} m3_delta_dims;
+
+typedef struct {
+    int64_t chunk, n_chunks;
+    int64_t ckpt_bytes, workspace_bytes;
+    int32_t fwd_launches, bwd_launches;
+} m3_delta_plan;
+
+m3_status m3scan_delta_plan(const m3_delta_dims* dims, m3_dtype act, m3_delta_plan* out);
+
+/* state NULL = zero.  state_out and ckpt are written where they are not
+ * NULL; m3scan_delta_bwd needs ckpt. */
+m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta, const float* state,
+                           void* o, float* state_out, float* ckpt, void* workspace,
+                           size_t workspace_bytes, m3_stream_t stream);
+
+/* The derivative of sum(d_o * o) + sum(d_state_out * state_out).
+ * d_state_out NULL = zero; d_state is written where it is not NULL. */
+m3_status m3scan_delta_bwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta, const float* ckpt,
+                           const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,
+                           void* dg, void* dbeta, float* d_state, void* workspace,
+                           size_t workspace_bytes, m3_stream_t stream);
+
+/* A short window (typically one token) from the carried state, which is
+ * updated in place; no workspace. */
+m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                              const void* v, const void* g, const void* beta, float* state,
+                              void* o, m3_stream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char* m3scan_status_string(m3_status status);
 

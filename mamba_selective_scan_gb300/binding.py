@@ -35,7 +35,8 @@ STATUS_BYTES = 256
 EXPORTS = ("m3scan_plan", "m3scan_fwd", "m3scan_bwd", "m3scan_fwd_state", "m3scan_bwd_state",
            "m3scan_bwd_scan", "m3scan_conv_bwd", "m3scan_decode", "m3scan_bwd_noalloc", "m3scan_status_string", "m3scan_last_cuda_error",
            "m3scan_version", "m3scan_get_status", "m3scan_device_status",
-           "m3scan_selftest_wait_timeout")
+           "m3scan_selftest_wait_timeout", "m3scan_norm_plan", "m3scan_norm_fwd", "m3scan_norm_bwd",
+           "m3scan_delta_plan", "m3scan_delta_fwd", "m3scan_delta_bwd", "m3scan_delta_decode")
 
 # size of the library's own scratch array used by m3scan_bwd_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -85,6 +86,28 @@ class M3BwdState(ctypes.Structure):
     _fields_ = [("conv_state", ctypes.c_void_p), ("d_ssm_state_out", ctypes.c_void_p),
                 ("d_conv_state_out", ctypes.c_void_p), ("d_ssm_state", ctypes.c_void_p),
                 ("d_conv_state", ctypes.c_void_p)]
+
+
+class M3NormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("accumulate_param_grads", ctypes.c_int32)]
+
+
+class M3NormPlan(ctypes.Structure):
+    _fields_ = [("workspace_bytes", ctypes.c_int64)]
+
+
+class M3DeltaDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "seq_len", "k_heads", "v_heads", "head_k", "head_v", "q_stride", "k_stride",
+        "v_stride", "dq_stride", "dk_stride", "dv_stride")] + [
+            ("scale", ctypes.c_float), ("qk_l2norm", ctypes.c_int32)]
+
+
+class M3DeltaPlan(ctypes.Structure):
+    _fields_ = [("chunk", ctypes.c_int64), ("n_chunks", ctypes.c_int64),
+                ("ckpt_bytes", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+                ("fwd_launches", ctypes.c_int32), ("bwd_launches", ctypes.c_int32)]
 
 
 _LIB = None
@@ -156,6 +179,18 @@ def _lib_handle(build_if_missing: bool = True):
             lib.m3scan_get_status.argtypes = [_vp, _vp, ctypes.POINTER(ctypes.c_int)]
             lib.m3scan_selftest_wait_timeout.restype = ctypes.c_int
             lib.m3scan_selftest_wait_timeout.argtypes = [_vp, _vp]
+            pn, pd = ctypes.POINTER(M3NormDims), ctypes.POINTER(M3DeltaDims)
+            ci, sz = ctypes.c_int, ctypes.c_size_t
+            for name, args in (
+                    ("m3scan_norm_plan", [pn, ci, ctypes.POINTER(M3NormPlan)]),
+                    ("m3scan_norm_fwd", [pn, ci] + [_vp] * 9),
+                    ("m3scan_norm_bwd", [pn, ci, _vp, _vp, ci] + [_vp] * 9 + [sz, _vp]),
+                    ("m3scan_delta_plan", [pd, ci, ctypes.POINTER(M3DeltaPlan)]),
+                    ("m3scan_delta_fwd", [pd, ci] + [_vp] * 10 + [sz, _vp]),
+                    ("m3scan_delta_bwd", [pd, ci] + [_vp] * 15 + [sz, _vp]),
+                    ("m3scan_delta_decode", [pd, ci] + [_vp] * 8)):
+                getattr(lib, name).restype = ctypes.c_int
+                getattr(lib, name).argtypes = args
             _LIB = lib
     return _LIB
 
@@ -608,4 +643,243 @@ def m3scan_bwd_two_phase(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log
                      st, ws.ptr, ws.nbytes, h)
     if r != 0:
         raise M3Error(r, "m3scan_conv_bwd")
+    return o
+
+
+# ---------------------------------------------------------------------------
+# block operators: layer norm and the gated delta rule
+# ---------------------------------------------------------------------------
+
+def m3scan_norm_plan(dims: M3NormDims, act: int) -> M3NormPlan:
+    out = M3NormPlan()
+    st = _lib_handle().m3scan_norm_plan(ctypes.byref(dims), int(act), ctypes.byref(out))
+    if st != 0:
+        raise M3Error(st, "m3scan_norm_plan")
+    return out
+
+
+def m3scan_delta_plan(dims: M3DeltaDims, act: int) -> M3DeltaPlan:
+    out = M3DeltaPlan()
+    st = _lib_handle().m3scan_delta_plan(ctypes.byref(dims), int(act), ctypes.byref(out))
+    if st != 0:
+        raise M3Error(st, "m3scan_delta_plan")
+    return out
+
+
+def _shape(t, name, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residual_out=None,
+                    mean=None, rstd=None, want_stats=True, stream=None):
+    """Layer norm over the last dimension of ``x`` [..., dim], of x + residual
+    when the f32 ``residual`` stream is given.  Returns (y, residual_out,
+    mean, rstd): ``residual_out`` (f32) is x + residual, None without a
+    residual unless a tensor for it is passed; ``mean`` and ``rstd`` (f32
+    [...]) are None when ``want_stats`` is False."""
+    torch = _torch()
+    dev, shape = x.device, tuple(x.shape)
+    dim = shape[-1]
+    code = _act_code(x)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    if want_stats and mean is None:
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    if want_stats and rstd is None:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _check(x, "x", None, dev)
+    _check(y, "y", x.dtype, dev)
+    _shape(y, "y", shape)
+    for n, t, s in (("weight", weight, (dim,)), ("bias", bias, (dim,)), ("residual", residual, shape),
+                    ("residual_out", residual_out, shape), ("mean", mean, shape[:-1]),
+                    ("rstd", rstd, shape[:-1])):
+        _check(t, n, torch.float32, dev)
+        _shape(t, n, s)
+    dims = M3NormDims(x.numel() // dim if dim else 0, dim, float(eps), 0)
+    st = _lib_handle().m3scan_norm_fwd(ctypes.byref(dims), code, _ptr(x), _ptr(residual), _ptr(weight),
+                                       _ptr(bias), _ptr(y), _ptr(residual_out), _ptr(mean), _ptr(rstd),
+                                       _stream_handle(stream))
+    if st != 0:
+        raise M3Error(st, "m3scan_norm_fwd")
+    return y, residual_out, mean, rstd
+
+
+def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want_bias=True,
+                    accumulate_param_grads=False, out=None, workspace=None, stream=None):
+    """Backward of ``m3scan_norm_fwd``.  ``normed`` is its ``residual_out``
+    (f32), or x when it had no residual; ``d_residual_out`` (f32) is the
+    gradient reaching the residual stream past the norm.  Returns a dict:
+    ``dx`` (dtype of dy), ``d_residual`` (f32; None without
+    ``d_residual_out`` unless passed in ``out``), ``d_weight``, ``d_bias``."""
+    torch = _torch()
+    dev, shape = dy.device, tuple(dy.shape)
+    dim = shape[-1]
+    code, ncode = _act_code(dy), _act_code(normed)
+    o = dict(out or {})
+    if o.get("dx") is None:
+        o["dx"] = torch.empty_like(dy)
+    if o.get("d_residual") is None:
+        o["d_residual"] = torch.empty_like(d_residual_out) if d_residual_out is not None else None
+    new = torch.zeros if accumulate_param_grads else torch.empty
+    if o.get("d_weight") is None:
+        o["d_weight"] = new((dim,), dtype=torch.float32, device=dev)
+    if o.get("d_bias") is None:
+        o["d_bias"] = new((dim,), dtype=torch.float32, device=dev) if want_bias else None
+    _check(dy, "dy", None, dev)
+    _check(normed, "normed", None, dev)
+    _shape(normed, "normed", shape)
+    _check(o["dx"], "dx", dy.dtype, dev)
+    _shape(o["dx"], "dx", shape)
+    for n, t, s in (("weight", weight, (dim,)), ("mean", mean, shape[:-1]), ("rstd", rstd, shape[:-1]),
+                    ("d_residual_out", d_residual_out, shape), ("d_residual", o["d_residual"], shape),
+                    ("d_weight", o["d_weight"], (dim,)), ("d_bias", o["d_bias"], (dim,))):
+        _check(t, n, torch.float32, dev)
+        _shape(t, n, s)
+    dims = M3NormDims(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)))
+    if workspace is None:
+        workspace = Workspace(m3scan_norm_plan(dims, code).workspace_bytes, dev)
+    st = _lib_handle().m3scan_norm_bwd(ctypes.byref(dims), code, _ptr(dy), _ptr(normed), ncode, _ptr(weight),
+                                       _ptr(mean), _ptr(rstd), _ptr(d_residual_out), _ptr(o["dx"]),
+                                       _ptr(o["d_residual"]), _ptr(o["d_weight"]), _ptr(o["d_bias"]),
+                                       workspace.ptr, workspace.nbytes, _stream_handle(stream))
+    if st != 0:
+        raise M3Error(st, "m3scan_norm_bwd")
+    return o
+
+
+def _token_stride(t, name, dtype, dev):
+    """Elements between tokens of a [B, T, H, D] tensor whose heads are dense
+    and whose batch rows follow each other at that stride (a column view of a
+    projection's output)."""
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return 0
+    B, T, H, D = t.shape
+    sb, stk, sh, sd = t.stride()
+    if T <= 1:
+        stk = sb if B > 1 else H * D
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 0 and sb != T * stk):
+        raise ValueError(f"{name}: heads must be dense and batch rows T token strides apart, got strides {t.stride()}")
+    return stk
+
+
+def _delta_dims(q, k, v, g, beta, scale, qk_l2norm):
+    torch = _torch()
+    for n, t, nd in (("q", q, 4), ("k", k, 4), ("v", v, 4), ("g", g, 3), ("beta", beta, 3)):
+        if t.dim() != nd:
+            raise ValueError(f"{n} must have {nd} dimensions, got {tuple(t.shape)}")
+    dev, dt = v.device, v.dtype
+    B, T, Hv, dv = v.shape
+    Hk, dk = k.shape[2:]
+    _shape(k, "k", (B, T, Hk, dk))
+    _shape(q, "q", (B, T, Hk, dk))
+    for n, t in (("g", g), ("beta", beta)):
+        _check(t, n, dt, dev)
+        _shape(t, n, (B, T, Hv))
+    return M3DeltaDims(B, T, Hk, Hv, dk, dv, _token_stride(q, "q", dt, dev), _token_stride(k, "k", dt, dev),
+                       _token_stride(v, "v", dt, dev), 0, 0, 0, float(scale), int(bool(qk_l2norm)))
+
+
+def _state_check(t, name, dims, dev):
+    _check(t, name, _torch().float32, dev)
+    _shape(t, name, (dims.batch, dims.v_heads, dims.head_k, dims.head_v))
+
+
+def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False, want_state=True,
+                     want_ckpt=False, o=None, state_out=None, ckpt=None, workspace=None, stream=None):
+    """Gated delta rule over a sequence.  q, k [B, T, Hk, dk], v [B, T, Hv,
+    dv] (column views of a projection's output are fine), g (log decay) and
+    beta [B, T, Hv], all bf16 or f32; ``state`` [B, Hv, dk, dv] f32 or None
+    (zero).  Returns (o, state_out or None, ckpt or None); the backward needs
+    ``want_ckpt=True``."""
+    torch = _torch()
+    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
+    dev, code = v.device, _act_code(v)
+    pl = m3scan_delta_plan(dims, code)
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    sshape = (dims.batch, dims.v_heads, dims.head_k, dims.head_v)
+    if want_state and state_out is None:
+        state_out = torch.empty(sshape, dtype=torch.float32, device=dev)
+    cshape = (dims.batch, dims.v_heads, pl.n_chunks, dims.head_k, dims.head_v)
+    if want_ckpt and ckpt is None:
+        ckpt = torch.empty(cshape, dtype=torch.float32, device=dev)
+    _check(o, "o", v.dtype, dev)
+    _shape(o, "o", v.shape)
+    _state_check(state, "state", dims, dev)
+    _state_check(state_out, "state_out", dims, dev)
+    _check(ckpt, "ckpt", torch.float32, dev)
+    _shape(ckpt, "ckpt", cshape)
+    if workspace is None:
+        workspace = Workspace(pl.workspace_bytes, dev)
+    st = _lib_handle().m3scan_delta_fwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                        _ptr(beta), _ptr(state), _ptr(o), _ptr(state_out), _ptr(ckpt),
+                                        workspace.ptr, workspace.nbytes, _stream_handle(stream))
+    if st != 0:
+        raise M3Error(st, "m3scan_delta_fwd")
+    return o, state_out, ckpt
+
+
+def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_state=False, scale=0.0,
+                     qk_l2norm=False, out=None, workspace=None, stream=None):
+    """Backward of ``m3scan_delta_fwd`` (same q, k, v, g, beta, scale and
+    qk_l2norm, its ``ckpt``).  Returns a dict: dq, dk, dv, dg, dbeta
+    (activation dtype) and d_state (f32, None unless wanted).  dq, dk and dv
+    in ``out`` may be column views of a projection's gradient."""
+    torch = _torch()
+    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
+    dev, dt, code = v.device, v.dtype, _act_code(v)
+    r = dict(out or {})
+    for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
+        if r.get(n) is None:
+            r[n] = torch.empty(t.shape, dtype=dt, device=dev)
+        _shape(r[n], n, t.shape)
+    for n in ("dg", "dbeta"):
+        _check(r[n], n, dt, dev)
+    for n in ("dq", "dk", "dv"):
+        setattr(dims, n + "_stride", _token_stride(r[n], n, dt, dev))
+    pl = m3scan_delta_plan(dims, code)
+    if r.get("d_state") is None:
+        r["d_state"] = torch.empty((dims.batch, dims.v_heads, dims.head_k, dims.head_v), dtype=torch.float32,
+                                   device=dev) if want_d_state else None
+    _state_check(d_state_out, "d_state_out", dims, dev)
+    _state_check(r["d_state"], "d_state", dims, dev)
+    _check(d_o, "d_o", dt, dev)
+    _shape(d_o, "d_o", v.shape)
+    _check(ckpt, "ckpt", torch.float32, dev)
+    _shape(ckpt, "ckpt", (dims.batch, dims.v_heads, pl.n_chunks, dims.head_k, dims.head_v))
+    if workspace is None:
+        workspace = Workspace(pl.workspace_bytes, dev)
+    st = _lib_handle().m3scan_delta_bwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                        _ptr(beta), _ptr(ckpt), _ptr(d_o), _ptr(d_state_out), _ptr(r["dq"]),
+                                        _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dg"]), _ptr(r["dbeta"]),
+                                        _ptr(r["d_state"]), workspace.ptr, workspace.nbytes,
+                                        _stream_handle(stream))
+    if st != 0:
+        raise M3Error(st, "m3scan_delta_bwd")
+    return r
+
+
+def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, o=None, stream=None):
+    """A short window (typically one token: T = 1) from the carried ``state``
+    [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""
+    torch = _torch()
+    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
+    dev = v.device
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _check(o, "o", v.dtype, dev)
+    _shape(o, "o", v.shape)
+    _state_check(state, "state", dims, dev)
+    st = _lib_handle().m3scan_delta_decode(ctypes.byref(dims), _act_code(v), _ptr(q), _ptr(k), _ptr(v),
+                                           _ptr(g), _ptr(beta), _ptr(state), _ptr(o),
+                                           _stream_handle(stream))
+    if st != 0:
+        raise M3Error(st, "m3scan_delta_decode")
     return o

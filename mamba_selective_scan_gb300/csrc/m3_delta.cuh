@@ -1,0 +1,56 @@
+// m3_delta.cuh -- gated delta rule: argument structs, the launch plan and the
+// entry points the translation units provide to each other.
+//
+// Per batch row and value head, S in R^{head_k x head_v}:
+//
+//   S' = exp(g_t) S_{t-1};  u = beta_t (v_t - S'^T k_t);  S_t = S' + k_t u^T
+//   o_t = scale S_t^T q_t
+//
+// Over a chunk of C tokens with gam = cumsum(g), D_ij = exp(gam_i - gam_j):
+//
+//   A_ij = beta_i D_ij k_i.k_j (j < i),  T = (I + A)^-1
+//   E = V - exp(gam) (K S0),  U = T (beta E)
+//   O = scale (exp(gam) (Q S0) + (D o Q K^T) U)
+//   S_end = exp(gam_C) S0 + (exp(gam_C - gam) K)^T U
+#pragma once
+
+#include "m3_common.cuh"
+
+namespace m3 {
+
+constexpr int DMAX = 128;          // head_k and head_v, at most
+constexpr float DELTA_L2_EPS = 1e-6f;  // added to the sum of squares of q and of k
+constexpr float G_MIN = -110.0f;       // exp(-110) is 0 in f32: lower log decays (and -inf) count as this
+
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta, *d_o;
+  const float *s_in, *ckpt_in, *ds_out;  // state in, checkpoints and d(state out) of the backward
+  void *o, *dq, *dk, *dv, *dg, *dbeta;
+  float *s_out, *ckpt, *ds_in;
+  float *pdq, *pdk;  // shared heads: per-value-head shares of dq, dk [B, T, Hv, dk]
+  int64_t qs, ks, vs, dqs, dks, dvs;  // elements between tokens
+  int B, T, Hk, Hv, DK, DV, share;
+  int chunk, nc;
+  float scale;
+  int l2;
+  unsigned* status;
+};
+
+struct DeltaPlan {
+  int B, T, Hk, Hv, DK, DV, chunk, nc;
+  size_t ckpt_bytes, ws_bytes;
+  size_t o_pdq, o_pdk;  // workspace offsets
+  int fwd_launches, bwd_launches;
+};
+
+__device__ __forceinline__ float clamp_g(float g) { return fmaxf(g, G_MIN); }
+
+// Forward by the recurrence itself, token after token (any length and type;
+// decoding): provided by m3_delta_rec.cu
+template <typename T> cudaError_t launch_delta_rec(const DeltaArgs& a, cudaStream_t st, int sms);
+// Backward from the checkpoints in f32 arithmetic: m3_delta_bwd.cu
+template <typename T> cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st);
+// Sum of the per-value-head shares of dq and dk
+template <typename T> cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl);
+
+}  // namespace m3

@@ -1,0 +1,199 @@
+// m3_delta_api.cu -- the C entry points of the gated delta rule: validation,
+// the launch plan and the launch sequences.
+#include <math.h>
+
+#include <initializer_list>
+
+#include "m3_delta.cuh"
+
+namespace m3 {
+namespace {
+
+m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
+  if (!d) return M3_ERR_NULL;
+  if (act != M3_F32 && act != M3_BF16) return M3_ERR_UNSUPPORTED;
+  if (d->batch < 0 || d->seq_len < 0 || d->k_heads < 1 || d->v_heads < 1) return M3_ERR_DIMS;
+  if (d->batch > 65535 || d->seq_len > (int64_t)1 << 30 || d->v_heads > 65535) return M3_ERR_DIMS;
+  if (d->batch * d->v_heads > (int64_t)1 << 24) return M3_ERR_DIMS;
+  if (d->batch * d->seq_len > (int64_t)1 << 33) return M3_ERR_DIMS;
+  if (d->v_heads % d->k_heads != 0) return M3_ERR_UNSUPPORTED;
+  if (d->head_k < 8 || d->head_v < 8 || d->head_k > DMAX || d->head_v > DMAX || d->head_k % 8 || d->head_v % 8)
+    return M3_ERR_UNSUPPORTED;
+  if (!isfinite(d->scale)) return M3_ERR_DIMS;
+  if (d->qk_l2norm != 0 && d->qk_l2norm != 1) return M3_ERR_DIMS;
+  const int es = act == M3_BF16 ? 2 : 4;
+  const int64_t kw = d->k_heads * d->head_k, vw = d->v_heads * d->head_v;
+  const struct { int64_t stride, width; } rows[] = {{d->q_stride, kw}, {d->k_stride, kw}, {d->v_stride, vw},
+                                                    {d->dq_stride, kw}, {d->dk_stride, kw}, {d->dv_stride, vw}};
+  for (const auto& r : rows) {
+    if (r.stride != 0 && (r.stride < r.width || r.stride > (int64_t)1 << 24)) return M3_ERR_DIMS;
+    if (r.stride * es % 16 != 0) return M3_ERR_ALIGN;
+  }
+  return M3_OK;
+}
+
+m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
+  const m3_status st = delta_validate(d, act);
+  if (st != M3_OK) return st;
+  p->B = (int)d->batch; p->T = (int)d->seq_len;
+  p->Hk = (int)d->k_heads; p->Hv = (int)d->v_heads;
+  p->DK = (int)d->head_k; p->DV = (int)d->head_v;
+  p->chunk = 32;
+  p->nc = (p->T + p->chunk - 1) / p->chunk;
+  p->ckpt_bytes = (size_t)p->B * p->Hv * p->nc * p->DK * p->DV * 4;
+  size_t off = STATUS_BYTES;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const bool shared = p->Hv != p->Hk;
+  const size_t share_bytes = shared ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
+  p->o_pdq = take(share_bytes);
+  p->o_pdk = take(share_bytes);
+  p->ws_bytes = off;
+  const bool empty = p->B == 0 || p->T == 0;
+  p->fwd_launches = empty ? 0 : 1;
+  p->bwd_launches = empty ? 0 : shared ? 2 : 1;
+  return M3_OK;
+}
+
+DeltaArgs delta_args(const m3_delta_dims* d, const DeltaPlan& p) {
+  DeltaArgs a{};
+  a.B = p.B; a.T = p.T; a.Hk = p.Hk; a.Hv = p.Hv; a.DK = p.DK; a.DV = p.DV;
+  a.share = p.Hv / p.Hk;
+  a.chunk = p.chunk; a.nc = p.nc;
+  const int64_t kw = (int64_t)p.Hk * p.DK, vw = (int64_t)p.Hv * p.DV;
+  a.qs = d->q_stride ? d->q_stride : kw;
+  a.ks = d->k_stride ? d->k_stride : kw;
+  a.vs = d->v_stride ? d->v_stride : vw;
+  a.dqs = d->dq_stride ? d->dq_stride : kw;
+  a.dks = d->dk_stride ? d->dk_stride : kw;
+  a.dvs = d->dv_stride ? d->dv_stride : vw;
+  a.scale = d->scale != 0.0f ? d->scale : 1.0f / sqrtf((float)p.DK);
+  a.l2 = d->qk_l2norm;
+  return a;
+}
+
+// `aligned` for a list; NULL passes (presence is checked apart)
+bool all_aligned(std::initializer_list<const void*> ptrs, size_t n) {
+  for (const void* q : ptrs)
+    if (q && !aligned(q, n)) return false;
+  return true;
+}
+
+m3_status sm_count(int* sms) {
+  int dev = 0;
+  if (note(cudaGetDevice(&dev)) != cudaSuccess ||
+      note(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return M3_ERR_CUDA;
+  return M3_OK;
+}
+
+// No tokens: the state passes through (zero where there is none)
+m3_status pass_state(const float* in, float* out, size_t bytes, cudaStream_t s) {
+  if (!out || bytes == 0 || in == out) return M3_OK;
+  const cudaError_t e = in ? cudaMemcpyAsync(out, in, bytes, cudaMemcpyDeviceToDevice, s)
+                           : cudaMemsetAsync(out, 0, bytes, s);
+  return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) return M3_ERR_WORKSPACE;
+  return aligned(ws, 256) ? M3_OK : M3_ERR_ALIGN;
+}
+
+}  // namespace
+}  // namespace m3
+
+using namespace m3;
+
+extern "C" {
+
+m3_status m3scan_delta_plan(const m3_delta_dims* dims, m3_dtype act, m3_delta_plan* out) {
+  if (!out) return M3_ERR_NULL;
+  DeltaPlan p;
+  const m3_status st = delta_plan(dims, act, &p);
+  if (st != M3_OK) return st;
+  out->chunk = p.chunk;
+  out->n_chunks = p.nc;
+  out->ckpt_bytes = (int64_t)p.ckpt_bytes;
+  out->workspace_bytes = (int64_t)p.ws_bytes;
+  out->fwd_launches = p.fwd_launches;
+  out->bwd_launches = p.bwd_launches;
+  return M3_OK;
+}
+
+m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta, const float* state,
+                           void* o, float* state_out, float* ckpt, void* workspace,
+                           size_t workspace_bytes, m3_stream_t stream) {
+  DeltaPlan p;
+  m3_status st = delta_plan(dims, act, &p);
+  if (st != M3_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!all_aligned({q, k, v, o, state, state_out, ckpt}, 16) || !all_aligned({g, beta}, act == M3_BF16 ? 2 : 4))
+    return M3_ERR_ALIGN;
+  if (p.B == 0 || p.T == 0)
+    return pass_state(state, state_out, (size_t)p.B * p.Hv * p.DK * p.DV * 4, s);
+  if (!q || !k || !v || !g || !beta || !o) return M3_ERR_NULL;
+  st = check_workspace(workspace, workspace_bytes, p.ws_bytes);
+  if (st != M3_OK) return st;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != M3_OK) return st;
+  DeltaArgs a = delta_args(dims, p);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state;
+  a.o = o; a.s_out = state_out; a.ckpt = ckpt;
+  const cudaError_t e = act == M3_BF16 ? launch_delta_rec<__nv_bfloat16>(a, s, sms) : launch_delta_rec<float>(a, s, sms);
+  return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                              const void* v, const void* g, const void* beta, float* state, void* o,
+                              m3_stream_t stream) {
+  DeltaPlan p;
+  m3_status st = delta_plan(dims, act, &p);
+  if (st != M3_OK) return st;
+  if (!all_aligned({q, k, v, o, state}, 16) || !all_aligned({g, beta}, act == M3_BF16 ? 2 : 4)) return M3_ERR_ALIGN;
+  if (p.B == 0 || p.T == 0) return M3_OK;
+  if (!q || !k || !v || !g || !beta || !o || !state) return M3_ERR_NULL;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != M3_OK) return st;
+  DeltaArgs a = delta_args(dims, p);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state; a.s_out = state; a.o = o;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = act == M3_BF16 ? launch_delta_rec<__nv_bfloat16>(a, s, sms) : launch_delta_rec<float>(a, s, sms);
+  return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+m3_status m3scan_delta_bwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
+                           const void* v, const void* g, const void* beta, const float* ckpt,
+                           const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,
+                           void* dg, void* dbeta, float* d_state, void* workspace,
+                           size_t workspace_bytes, m3_stream_t stream) {
+  DeltaPlan p;
+  m3_status st = delta_plan(dims, act, &p);
+  if (st != M3_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (!all_aligned({q, k, v, ckpt, d_o, d_state_out, dq, dk, dv, d_state}, 16) ||
+      !all_aligned({g, beta, dg, dbeta}, act == M3_BF16 ? 2 : 4))
+    return M3_ERR_ALIGN;
+  if (p.B == 0 || p.T == 0)
+    return pass_state(d_state_out, d_state, (size_t)p.B * p.Hv * p.DK * p.DV * 4, s);
+  if (!q || !k || !v || !g || !beta || !ckpt || !d_o || !dq || !dk || !dv || !dg || !dbeta) return M3_ERR_NULL;
+  st = check_workspace(workspace, workspace_bytes, p.ws_bytes);
+  if (st != M3_OK) return st;
+  DeltaArgs a = delta_args(dims, p);
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.ckpt_in = ckpt; a.d_o = d_o; a.ds_out = d_state_out;
+  a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.ds_in = d_state;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.status = static_cast<unsigned*>(workspace);
+  a.pdq = reinterpret_cast<float*>(ws + p.o_pdq);
+  a.pdk = reinterpret_cast<float*>(ws + p.o_pdk);
+  cudaError_t e = act == M3_BF16 ? launch_delta_bwd<__nv_bfloat16>(a, s) : launch_delta_bwd<float>(a, s);
+  if (e == cudaSuccess && a.share > 1)
+    e = act == M3_BF16 ? launch_delta_share<__nv_bfloat16>(a, s, true) : launch_delta_share<float>(a, s, true);
+  return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+}
+
+}  // extern "C"

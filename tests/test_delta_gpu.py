@@ -1,0 +1,214 @@
+"""Gated delta rule on the GPU against the float64 recurrence and its
+autograd gradients.
+
+Tolerances (2-norm of the difference over the 2-norm of the result), from the
+arithmetic: an output rounded to bf16 is off by at most 2^-9 per element
+(1.95e-3; about 1.7e-3 in the 2-norm), and what happens before the rounding
+may add as much again: 4e-3.  f32 outputs come from sums of f32-grade products
+over up to a few hundred terms: 2e-5."""
+
+import pytest
+import torch
+
+from delta_util import delta_inputs, delta_ref_grads, rel
+from mamba_selective_scan_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+TOL = {torch.bfloat16: 4e-3, torch.float32: 2e-5}
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mamba_selective_scan_gb300 import build
+    build.build()
+
+
+def _check_all(got, ref, names):
+    bad = {}
+    for n in names:
+        e = rel(got[n], ref[n])
+        if not e <= TOL[got[n].dtype]:
+            bad[n] = e
+    assert not bad, bad
+
+
+def _run(x, l2norm, scale=0.0):
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    o, st, ck = binding.m3scan_delta_fwd(*args, state=x["state"], qk_l2norm=l2norm, scale=scale, want_ckpt=True)
+    r = binding.m3scan_delta_bwd(*args, ck, x["d_o"], d_state_out=x["d_state_out"],
+                                 want_d_state=x["state"] is not None, qk_l2norm=l2norm, scale=scale)
+    r.update(o=o, state_out=st)
+    return r
+
+
+CASES = [
+    # B, T, Hk, Hv, dk, dv, dtype, state, packed
+    (1, 1, 1, 1, 8, 8, "bf16", True, False),
+    (2, 3, 1, 2, 16, 24, "bf16", False, False),
+    (2, 31, 2, 2, 64, 64, "bf16", True, False),
+    (1, 32, 2, 2, 128, 128, "bf16", True, False),
+    (1, 33, 1, 3, 128, 128, "bf16", True, True),
+    (2, 63, 2, 4, 80, 72, "bf16", True, True),
+    (1, 64, 2, 2, 128, 128, "bf16", False, False),
+    (2, 65, 2, 2, 128, 128, "bf16", True, False),
+    (1, 127, 1, 1, 128, 64, "bf16", True, False),
+    (1, 128, 2, 2, 64, 128, "bf16", True, True),
+    (3, 129, 1, 2, 96, 128, "bf16", True, False),
+    (1, 300, 2, 2, 128, 128, "bf16", True, False),
+    (1, 1, 2, 2, 128, 128, "f32", True, False),
+    (2, 33, 1, 2, 40, 128, "f32", True, True),
+    (1, 130, 2, 2, 128, 128, "f32", True, False),
+    (2, 200, 2, 2, 128, 56, "f32", False, False),
+]
+
+
+@pytest.mark.parametrize("l2norm", [True, False])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+def test_forward_and_gradients(case, l2norm):
+    B, T, Hk, Hv, dk, dv, dt, state, packed = case
+    x = delta_inputs(B, T, Hk, Hv, dk, dv, DT[dt], seed=T + dk, device="cuda", state=state, packed=packed)
+    if not l2norm:  # unnormalised keys: short enough that beta |k|^2 stays below 2
+        for n in ("q", "k"):
+            x[n] = (x[n].float() * (0.8 / dk ** 0.5)).to(DT[dt])
+    got = _run(x, l2norm)
+    ref = delta_ref_grads(x, dk ** -0.5, l2norm)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta"] + (["d_state"] if state else []))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_extreme_gates(dt):
+    """-inf and very negative log decays forget the state; beta 0 writes
+    nothing; a zero key row is normalised to zero."""
+    x = delta_inputs(1, 150, 1, 2, 128, 128, DT[dt], seed=5, device="cuda")
+    x["g"][:, 3::17] = float("-inf")
+    x["g"][:, 7::31] = -500.0
+    x["g"][:, 11::13] = 0.0
+    x["beta"][:, 5::7] = 0.0
+    x["beta"][:, 6::7] = 1.0
+    x["k"][:, 9::19] = 0.0
+    got = _run(x, True)
+    y = dict(x)
+    y["g"] = x["g"].clamp(min=-800.0)  # exp(-800) is 0 in float64
+    ref = delta_ref_grads(y, 128 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_repeated_keys(dt):
+    """The same key every token, beta 1, no decay: the inverse's entries do
+    not shrink away from the diagonal."""
+    x = delta_inputs(1, 100, 1, 1, 64, 64, DT[dt], seed=8, device="cuda")
+    x["k"] = x["k"][:, :1].expand(-1, 100, -1, -1).contiguous()
+    x["beta"][:] = 1.0
+    x["g"][:] = 0.0
+    got = _run(x, True)
+    ref = delta_ref_grads(x, 64 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dv"])
+
+
+def test_scale_argument():
+    x = delta_inputs(1, 70, 1, 1, 64, 64, torch.bfloat16, seed=2, device="cuda")
+    got = _run(x, True, scale=0.37)
+    ref = delta_ref_grads(x, 0.37, True)
+    _check_all(got, ref, ["o", "dq", "dk", "dv", "d_state"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [0, 1, 64, 130])
+def test_windows_chain(dt, T):
+    """A sequence cut in two windows, the state carried: the same as one."""
+    x = delta_inputs(2, T + 67, 1, 2, 64, 128, DT[dt], seed=T, device="cuda")
+    names = ("q", "k", "v", "g", "beta")
+    whole, st, _ = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=True)
+    a, mid, _ = binding.m3scan_delta_fwd(*[x[n][:, :T].contiguous() for n in names], state=x["state"], qk_l2norm=True)
+    b, end, _ = binding.m3scan_delta_fwd(*[x[n][:, T:].contiguous() for n in names], state=mid, qk_l2norm=True)
+    assert rel(torch.cat([a, b], 1), whole.double().cpu()) <= TOL[DT[dt]]
+    assert rel(end, st.double().cpu()) <= 2e-5
+
+
+@pytest.mark.parametrize("B,Hk,Hv,dk,dv,dt", [(1, 1, 1, 8, 8, "bf16"), (1, 2, 4, 128, 128, "bf16"), (40, 4, 16, 64, 96, "bf16"),
+                                             (3, 2, 2, 128, 128, "f32"), (16, 5, 40, 128, 128, "bf16")])
+def test_decode_continues_prefill(B, Hk, Hv, dk, dv, dt):
+    """Single tokens from a carried state, updated in place."""
+    x = delta_inputs(B, 5, Hk, Hv, dk, dv, DT[dt], seed=B, device="cuda")
+    ref = delta_ref_grads(x, dk ** -0.5, True)
+    S = x["state"].clone()
+    outs = []
+    for t in range(5):
+        outs.append(binding.m3scan_delta_decode(*[x[n][:, t:t + 1].contiguous() for n in ("q", "k", "v", "g", "beta")], S,
+                                                qk_l2norm=True))
+    assert rel(torch.cat(outs, 1), ref["o"]) <= TOL[DT[dt]]
+    assert rel(S, ref["state_out"]) <= 2e-5
+
+
+def test_same_bits_every_call():
+    x = delta_inputs(2, 333, 2, 4, 128, 128, torch.bfloat16, seed=1, device="cuda")
+    a, b = _run(x, True), _run(x, True)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_on_another_stream():
+    x = delta_inputs(1, 200, 1, 2, 128, 128, torch.bfloat16, seed=4, device="cuda")
+    want = _run(x, True)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        got = _run(x, True)
+    s.synchronize()
+    for n in want:
+        assert torch.equal(want[n], got[n]), n
+
+
+def test_gradient_views_of_one_buffer():
+    """dq, dk and dv written into columns of one projection's gradient leave
+    its other columns alone."""
+    B, T, Hk, Hv, dk, dv = 2, 70, 2, 4, 64, 64
+    x = delta_inputs(B, T, Hk, Hv, dk, dv, torch.bfloat16, seed=6, device="cuda", packed=True)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    _, _, ck = binding.m3scan_delta_fwd(*args, state=x["state"], qk_l2norm=True, want_ckpt=True)
+    plain = binding.m3scan_delta_bwd(*args, ck, x["d_o"], qk_l2norm=True)
+    row = torch.full((B, T, 2 * Hk * dk + Hv * dv + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    q, k, v, rest = row.split([Hk * dk, Hk * dk, Hv * dv, 16], -1)
+    out = {"dq": q.unflatten(2, (Hk, dk)), "dk": k.unflatten(2, (Hk, dk)), "dv": v.unflatten(2, (Hv, dv))}
+    binding.m3scan_delta_bwd(*args, ck, x["d_o"], qk_l2norm=True, out=out)
+    for n in out:
+        assert torch.equal(out[n], plain[n]), n
+    assert (rest == 7.0).all()
+
+
+def test_gradients_against_differences():
+    """Central differences of the f32 forward along random directions."""
+    x = delta_inputs(1, 70, 1, 2, 32, 32, torch.float32, seed=9, device="cuda")
+    got = _run(x, True)
+
+    def loss(y):
+        o, st, _ = binding.m3scan_delta_fwd(y["q"], y["k"], y["v"], y["g"], y["beta"], state=y["state"], qk_l2norm=True)
+        return ((o.double() * x["d_o"].double()).sum() + (st.double() * x["d_state_out"].double()).sum()).item()
+
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    for n in ("q", "k", "v", "g", "beta", "state"):
+        d = torch.randn(x[n].shape, generator=gen, device="cuda")
+        d *= x[n].norm() / d.norm()
+        eps = 1e-3
+        num = (loss({**x, n: x[n] + eps * d}) - loss({**x, n: x[n] - eps * d})) / (2 * eps)
+        ana = (got["d_" + n if n == "state" else "d" + n].double() * d.double()).sum().item()
+        size = (got["d_" + n if n == "state" else "d" + n].double().norm() * d.double().norm()).item() / d.numel() ** 0.5
+        # truncation ~ eps^2, and the f32 forward's rounding (1e-6 of the loss's terms) over eps
+        assert abs(num - ana) <= 2e-2 * max(abs(ana), size), n
+
+
+def test_nan_stays_in_its_row():
+    """A NaN in one head's values reaches that head's outputs only."""
+    x = delta_inputs(1, 80, 2, 2, 64, 64, torch.bfloat16, seed=3, device="cuda")
+    clean = _run(x, True)
+    x["v"][0, 40, 1, 3] = float("nan")
+    got = _run(x, True)
+    assert torch.equal(got["o"][:, :, 0], clean["o"][:, :, 0])
+    assert torch.equal(got["o"][:, :40], clean["o"][:, :40])
+    assert torch.isnan(got["o"][0, 40, 1, 3])
+    assert torch.equal(got["dv"][:, :, 0], clean["dv"][:, :, 0])
