@@ -18,6 +18,7 @@
 
 namespace m3 {
 
+constexpr size_t TC_CKPT = 98304;  // bytes per chunk and head: S^T hi, lo [128][128], U^T hi, lo [128][64], bf16
 constexpr int DMAX = 128;          // head_k and head_v, at most
 constexpr float DELTA_L2_EPS = 1e-6f;  // added to the sum of squares of q and of k
 constexpr float G_MIN = -110.0f;       // exp(-110) is 0 in f32: lower log decays (and -inf) count as this
@@ -33,13 +34,16 @@ struct DeltaArgs {
   int chunk, nc;
   float scale;
   int l2;
+  int segs, seg_chunks;  // time segments of the tensor-core kernels, chunks per segment
+  float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
   unsigned* status;
 };
 
 struct DeltaPlan {
   int B, T, Hk, Hv, DK, DV, chunk, nc;
   size_t ckpt_bytes, ws_bytes;
-  size_t o_pdq, o_pdk;  // workspace offsets
+  size_t o_pdq, o_pdk, o_end, o_phi, o_start;  // workspace offsets
+  int segs, seg_chunks;  // forward time segments
   int fwd_launches, bwd_launches;
 };
 
@@ -52,5 +56,12 @@ template <typename T> cudaError_t launch_delta_rec(const DeltaArgs& a, cudaStrea
 template <typename T> cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st);
 // Sum of the per-value-head shares of dq and dk
 template <typename T> cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl);
+
+// Forward of bf16 activations by chunks of 64 on the tensor cores
+cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st);
+// Tensor map of a [B, T, H, D] bf16 tensor (`stride` elements between
+// tokens) read in tiles of 64 tokens x 64 columns, 128-byte swizzle
+bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, int64_t B, int64_t stride);
+cudaError_t take_delta_fwd_status(unsigned* out);
 
 }  // namespace m3

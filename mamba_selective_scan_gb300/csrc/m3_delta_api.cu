@@ -32,6 +32,31 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
   return M3_OK;
 }
 
+// Time segments of the tensor-core forward.  A block per (head, segment) runs
+// one chunk in a unit of time (about 2 us); with S segments, first the S - 1
+// earlier ones run twice without outputs (from zero and from the identity,
+// about 3/4 of a unit per chunk), then a kernel chains them (about half a
+// unit per segment and three for its launch), then all S run.  The count
+// with the least total is taken, with at least four chunks per segment.
+void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
+  constexpr int64_t SMS = 152;
+  double best = 0.0;
+  *segs = 1;
+  *seg_chunks = nc < 1 ? 1 : nc;
+  for (int want = 1; want <= 64 && want * 4 <= (nc > 4 ? nc : 4); ++want) {
+    const int m = (nc + want - 1) / want;
+    if (m < 1) break;
+    const int S = (nc + m - 1) / m;
+    const double fin = (double)((heads * S + SMS - 1) / SMS) * m;
+    const double agg = S > 1 ? (double)((heads * (S - 1) * 2 + SMS - 1) / SMS) * m * 0.75 + 0.5 * S + 3.0 : 0.0;
+    if (want == 1 || fin + agg < best - 1e-9) {
+      best = fin + agg;
+      *segs = S;
+      *seg_chunks = m;
+    }
+  }
+}
+
 m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   const m3_status st = delta_validate(d, act);
   if (st != M3_OK) return st;
@@ -51,6 +76,11 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   const size_t share_bytes = shared ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
   p->o_pdq = take(share_bytes);
   p->o_pdk = take(share_bytes);
+  delta_segments((int64_t)p->B * p->Hv, (p->T + 63) / 64, &p->segs, &p->seg_chunks);
+  const size_t seg_bytes = p->segs > 1 ? (size_t)p->B * p->Hv * p->segs * DMAX * DMAX * 4 : 0;
+  p->o_end = take(seg_bytes);
+  p->o_phi = take(seg_bytes);
+  p->o_start = take(seg_bytes);
   p->ws_bytes = off;
   const bool empty = p->B == 0 || p->T == 0;
   p->fwd_launches = empty ? 0 : 1;
@@ -144,7 +174,21 @@ m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   DeltaArgs a = delta_args(dims, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state;
   a.o = o; a.s_out = state_out; a.ckpt = ckpt;
-  const cudaError_t e = act == M3_BF16 ? launch_delta_rec<__nv_bfloat16>(a, s, sms) : launch_delta_rec<float>(a, s, sms);
+  cudaError_t e;
+  if (act == M3_F32) {
+    e = launch_delta_rec<float>(a, s, sms);
+  } else if (ckpt) {
+    e = launch_delta_rec<__nv_bfloat16>(a, s, sms);
+  } else {
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.nc = (p.T + 63) / 64;
+    a.segs = p.segs; a.seg_chunks = p.seg_chunks;
+    a.status = static_cast<unsigned*>(workspace);
+    a.seg_end = reinterpret_cast<float*>(ws + p.o_end);
+    a.seg_phi = reinterpret_cast<float*>(ws + p.o_phi);
+    a.seg_start = reinterpret_cast<float*>(ws + p.o_start);
+    e = launch_delta_tc_fwd(a, s);
+  }
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 

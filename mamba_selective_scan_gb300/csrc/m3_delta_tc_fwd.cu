@@ -1,0 +1,494 @@
+// m3_delta_tc_fwd.cu -- the gated delta rule's forward on the tensor cores:
+// bf16 activations, chunks of 64 tokens, f32-grade sums.
+#include "m3_delta_tc.cuh"
+
+namespace m3 {
+
+// nonzero once a kernel here gave up waiting
+__device__ unsigned int g_delta_fwd_status;
+
+cudaError_t take_delta_fwd_status(unsigned* out) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_delta_fwd_status, sizeof(v));
+  if (e == cudaSuccess && v) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(g_delta_fwd_status, &zero, sizeof(zero));
+  }
+  *out = v;
+  return e;
+}
+
+namespace {
+
+constexpr int THREADS = 384;  // 8 warps on the state, 4 on T and P
+constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), V (2 tiles)
+
+struct Smem {  // after two stages
+  TcTP tp[2];
+  TcVec vec[2];
+  TcWork work;
+  int bad[2][128];
+  uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbq, mbu, mbd, mbo;
+  uint32_t tmem;
+};
+constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
+
+// tensor-memory columns
+constexpr uint32_t T_S = 0;     // S as hi (64) and lo (64); also the 128 columns of U'^T K
+constexpr uint32_t T_X = 128;   // S K^T, then U
+constexpr uint32_t T_Q = 192;   // S Q^T
+constexpr uint32_t T_R = 256;   // R as hi, lo (32 + 32), then U' = U e^{gam_C - gam}
+constexpr uint32_t T_U = 320;   // U as hi, lo
+constexpr uint32_t T_O = 384;   // U P^T
+constexpr uint32_t T_K = 448;   // K over Q times K^T
+
+}  // namespace
+
+// One block per (batch row, value head, time segment) walks its chunks.  The
+// state is held transposed, S^T [head_v][head_k], one row per tensor-memory
+// lane, so that every product of the chain has the state's rows (M = 128) as
+// its A operand in tensor memory and token tiles as B in shared memory, and
+// every per-token factor is a column factor:
+//
+//   X = S^T K^T          R = beta V^T - bfx X        (N = 64 tokens)
+//   U = R T^T            U' = U fu
+//   S^T = e^{gam_C} S^T + U' K                       (N = head_k)
+//   O^T = fq (S^T Q^T) + U P^T
+//
+// Operands that are not bf16 inputs (S, R, U, T, P) enter as hi + lo, two
+// bf16 terms: 2 MMAs against an input, 3 against another pair (lo x lo is
+// below f32's own rounding of these sums).  The state itself stays f32 in
+// registers, half a row per thread.
+//
+// Roles: warps 0-7 the chain above (a row's columns in two halves), warps
+// 8-11 T and P of the chunk ahead (tc_make_tp); thread 0 also issues the MMAs
+// and the copies, two stages.  A chunk is a chain of four dependent products, bound by their
+// latency and the register work between them, not by HBM.
+//
+// AGG: the segment's effect on the state instead of outputs: blockIdx.z 0
+// from a zero state, blockIdx.z 1 from the identity with V = 0 (the rows of
+// the state's transition), both written to seg.
+template <bool AGG, bool L2>
+__global__ void __launch_bounds__(THREADS, 1)
+m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  extern __shared__ unsigned char raw[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
+  const int seg = blockIdx.y;
+  const int c_begin = seg * a.seg_chunks, c_end = min(a.nc, c_begin + a.seg_chunks);
+  const bool ident = AGG && blockIdx.z == 1;
+  const uint32_t st0 = smem_u32(base);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.tp_full[i], 1);
+      mbar_init(&s.tp_empty[i], 1);
+    }
+    mbar_init(&s.mbk, 1); mbar_init(&s.mbx, 1); mbar_init(&s.mbq, 1);
+    mbar_init(&s.mbu, 1); mbar_init(&s.mbd, 1); mbar_init(&s.mbo, 1);
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(&s.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = s.tmem;
+  TcWait wait;
+
+  // one chunk's copies (thread 0, once the stage is free)
+  int issued = 0;
+  auto load = [&](int c) {
+    if (c >= c_end || !wait.ok) return;
+    const int g = issued++ & 1;
+    const uint32_t st = st0 + g * STAGE;
+    mbar_expect_tx(&s.kv_full[g], STAGE);
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+      tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+      tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+      tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, c * TC, b, &s.kv_full[g]);
+    }
+  };
+
+  if (warp >= 8) {
+    const int pt = tid - 256;
+    const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.g) + (int64_t)b * a.T * a.Hv + h;
+    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + (int64_t)b * a.T * a.Hv + h;
+    auto gate = [&](const __nv_bfloat16* p, int c) {
+      const int t = c * TC + pt;
+      return pt < TC && t < a.T ? __bfloat162float(p[(int64_t)t * a.Hv]) : 0.0f;
+    };
+    float g = gate(gp, c_begin), beta = gate(bp, c_begin);
+    for (int c = c_begin; c < c_end; ++c) {
+      const int n = c - c_begin, i = n & 1;
+      const float gn = c + 1 < c_end ? gate(gp, c + 1) : 0.0f, bn = c + 1 < c_end ? gate(bp, c + 1) : 0.0f;
+      wait(&s.kv_full[i], (n >> 1) & 1);
+      tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
+                     &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
+      if (pt == 0) mbar_arrive(&s.tp_full[i]);
+      g = gn;
+      beta = bn;
+    }
+  } else {
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // row: the state's head_v index
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool live = row < a.DV;
+    float S[64];  // S^T[row][64 half + k]
+    if (AGG) {
+#pragma unroll
+      for (int k = 0; k < 64; ++k) S[k] = ident && half * 64 + k == row ? 1.0f : 0.0f;
+    } else {
+      // the segment's start: the carried state, or what the segments before left
+      const float* src = seg == 0 ? a.s_in ? a.s_in + (size_t)bh * a.DK * a.DV : nullptr
+                                  : a.seg_start + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+      const int ld = seg == 0 ? a.DV : DMAX;
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        const int kk = half * 64 + k;
+        S[k] = src && (seg > 0 || (live && kk < a.DK)) ? src[(size_t)kk * ld + row] : 0.0f;
+      }
+    }
+    const int64_t obase = ((int64_t)b * a.T * a.Hv + h) * a.DV + row;
+    uint32_t hi[32], lo[32];
+    bool nan_row = false;
+
+    auto put_state = [&](int c) {  // S as hi, lo into tensor memory (and the chunk's checkpoint)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) split2(S[2 * k], S[2 * k + 1], hi[k], lo[k]);
+      tc_st16(tl + T_S + half * 32, hi);
+      tc_st16(tl + T_S + half * 32 + 16, hi + 16);
+      tc_st16(tl + T_S + 64 + half * 32, lo);
+      tc_st16(tl + T_S + 64 + half * 32 + 16, lo + 16);
+      if (!AGG && a.ckpt && c < c_end) {
+        unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + row * 256 + half * 128;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 32768 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
+      }
+      tmem_wait_st();
+      tmem_fence_before_sync();
+    };
+    // MMAs of the A operand at column ta (hi; lo at ta + 8 ksteps) against a K-major tile pair
+    auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc_mma_ts(tm + d, tm + T_S + p * 64 + ks * 8, tc_desc(bt + (ks >> 2) * 2 * TILE + (ks & 3) * 32, 16, 1024),
+                    tc_idesc(128, 64, false, false), p + ks > 0);
+    };
+    auto mma_tokens = [&](uint32_t d, uint32_t ta, uint32_t bhi, uint32_t blo) {  // (hi, lo) x (hi, lo), K = 64
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma_ts(tm + d, tm + ta + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? blo : bhi) + ks * 32, 16, 1024),
+                    tc_idesc(128, 64, false, false), p + ks > 0);
+    };
+    auto outputs = [&](int c) {  // O of chunk c from T_Q and T_O
+      const int n = c - c_begin, i = n & 1;
+      float q[32], o[32];
+      wait(&s.mbq, n & 1);
+      wait(&s.mbo, n & 1);
+      tmem_fence_after_sync();
+      tc_ld32(tl + T_Q + half * 32, q);
+      tc_ld32(tl + T_O + half * 32, o);
+      tmem_fence_before_sync();
+      const int t0 = c * TC + half * 32;
+      const int bad = min(s.bad[0][row], s.bad[1][row]) - half * 32;
+      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) + obase + (int64_t)t0 * a.Hv * a.DV;
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 fq = *reinterpret_cast<const float4*>(&s.vec[i].fq[half * 32 + j]);
+        const float f[4] = {fq.x, fq.y, fq.z, fq.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float v = fmaf(f[m], q[j + m], o[j + m]);
+          if (j + m >= bad) v = __int_as_float(0x7FFFFFFF);
+          if (live && t0 + j + m < a.T) op[(int64_t)(j + m) * a.Hv * a.DV] = __float2bfloat16_rn(v);
+        }
+      }
+    };
+
+    if (tid == 0) {
+      load(c_begin);
+      load(c_begin + 1);
+    }
+    __syncwarp();
+    put_state(c_begin);
+    bar_sync(1, 256);
+    for (int c = c_begin; c < c_end; ++c) {
+      const int n = c - c_begin, i = n & 1;
+      const uint32_t st = st0 + i * STAGE;
+      const uint32_t par = n & 1;
+      if (tid == 0) {
+        wait(&s.kv_full[i], (n >> 1) & 1);
+        tmem_fence_after_sync();
+        if (wait.ok) {
+          mma_state(T_X, st);
+          tc_commit(&s.mbx);
+        }
+      }
+      __syncwarp();
+      if (AGG) {
+        if (tid == 0 && n > 0) load(c + 1);
+      } else {
+        if (n > 0) outputs(c - 1);
+        bar_sync(1, 256);  // T_Q and T_O are read
+        if (tid == 0) {
+          if (n > 0) {  // every MMA of the last chunk is done and its V is read
+            mbar_arrive(&s.tp_empty[(n - 1) & 1]);
+            load(c + 1);
+          }
+          tmem_fence_after_sync();
+          if (wait.ok) {
+            mma_state(T_Q, st + TILE);
+            tc_commit(&s.mbq);
+          }
+        }
+        __syncwarp();
+      }
+      // R = beta V - bfx X
+      wait(&s.tp_full[i], (n >> 1) & 1);
+      wait(&s.kv_full[i], (n >> 1) & 1);
+      wait(&s.mbx, par);
+      tmem_fence_after_sync();
+      float x[32];
+      tc_ld32(tl + T_X + half * 32, x);
+      {
+        int bad = TC;
+        const uint32_t vt = st + (4 + (row >> 6)) * TILE;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 be = *reinterpret_cast<const float4*>(&s.vec[i].beta[half * 32 + j]);
+          const float4 bx = *reinterpret_cast<const float4*>(&s.vec[i].bfx[half * 32 + j]);
+          const float bv[4] = {be.x, be.y, be.z, be.w}, xv[4] = {bx.x, bx.y, bx.z, bx.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int t = half * 32 + j + m;
+            uint16_t vr;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(t, (row & 63) >> 3) + (row & 7) * 2));
+            const float v = ident ? 0.0f : __uint_as_float((uint32_t)vr << 16);
+            float r = fmaf(-xv[m], x[j + m], bv[m] * v);
+            // a value that is not finite must not reach earlier tokens
+            // through the zeros of T: it is taken out, and every output
+            // from its token on becomes NaN
+            if (!(fabsf(r) <= FINITE_MAX)) {
+              r = 0.0f;
+              bad = min(bad, t);
+            }
+            x[j + m] = r;
+          }
+        }
+        s.bad[half][row] = bad;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      tc_st16(tl + T_R + half * 16, hi);
+      tc_st16(tl + T_R + 32 + half * 16, lo);
+      tmem_wait_st();
+      tmem_fence_before_sync();
+      bar_sync(1, 256);
+      if (tid == 0 && wait.ok) {
+        tmem_fence_after_sync();
+        mma_tokens(T_X, T_R, smem_u32(s.tp[i].t_hi), smem_u32(s.tp[i].t_lo));
+        tc_commit(&s.mbu);
+      }
+      __syncwarp();
+      nan_row = nan_row || min(s.bad[0][row], s.bad[1][row]) < TC;
+      wait(&s.mbu, par);
+      tmem_fence_after_sync();
+      tc_ld32(tl + T_X + half * 32, x);
+      if (!AGG) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+        tc_st16(tl + T_U + half * 16, hi);
+        tc_st16(tl + T_U + 32 + half * 16, lo);
+        if (a.ckpt) {
+          unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 65536 + row * 128 + half * 64;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + 16384 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 fu = *reinterpret_cast<const float4*>(&s.vec[i].fu[half * 32 + j]);
+        x[j] *= fu.x; x[j + 1] *= fu.y; x[j + 2] *= fu.z; x[j + 3] *= fu.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      tc_st16(tl + T_R + half * 16, hi);
+      tc_st16(tl + T_R + 32 + half * 16, lo);
+      tmem_wait_st();
+      tmem_fence_before_sync();
+      const float ec = s.vec[i].ec;
+      bar_sync(1, 256);
+      if (tid == 0) {
+        if (!AGG) wait(&s.mbq, par);  // S is read: its columns may be overwritten
+        tmem_fence_after_sync();
+        if (wait.ok) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
+                        tc_idesc(128, 128, false, true), p + ks > 0);
+          tc_commit(&s.mbd);
+          if (!AGG) {
+            mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
+            tc_commit(&s.mbo);
+          } else {
+            tc_commit(&s.tp_empty[i]);
+          }
+        }
+      }
+      __syncwarp();
+      wait(&s.mbd, par);
+      tmem_fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        tc_ld32(tl + T_S + half * 64 + q * 32, x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) S[q * 32 + k] = fmaf(ec, S[q * 32 + k], x[k]);
+      }
+      if (nan_row) {
+#pragma unroll
+        for (int k = 0; k < 64; ++k) S[k] = __int_as_float(0x7FFFFFFF);
+      }
+      tmem_fence_before_sync();
+      bar_sync(1, 256);  // every column of U'^T K is read
+      tmem_fence_after_sync();
+      put_state(c + 1);
+      bar_sync(1, 256);
+    }
+    if (!AGG) outputs(c_end - 1);
+    // the state's way out
+    float* dst = nullptr;
+    int ld = a.DV;
+    if (AGG) {
+      dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+      ld = DMAX;
+    } else if (a.s_out && c_end == a.nc) {
+      dst = a.s_out + (size_t)bh * a.DK * a.DV;
+    }
+    if (dst) {
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        const int kk = half * 64 + k;
+        if (AGG || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = S[k];
+      }
+    }
+  }
+  if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
+  // after a wait ran out, copies still in flight land before the block's
+  // shared memory is given up (bounded)
+  if (tid == 0 && !wait.ok)
+    for (int i = 0; i < 2; ++i)
+      if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, int64_t B, int64_t stride) {
+  typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2, (cuuint64_t)T * stride * 2};
+  const cuuint32_t box[4] = {64, 1, TC, 1}, one[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
+// start[s], 32 columns of the state per block, f32.
+__global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a) {
+  __shared__ __align__(16) float S[DMAX][32];
+  __shared__ __align__(16) float P[32][DMAX + 4];
+  grid_dep_wait();
+  const int tid = threadIdx.x, bh = blockIdx.x, v0 = blockIdx.y * 32;
+  const int kq = (tid >> 3) * 4, vq = (tid & 7) * 4;  // 4 rows k x 4 columns per thread
+  for (int i = tid; i < DMAX * 32; i += 256) {
+    const int k = i >> 5, v = v0 + (i & 31);
+    S[k][i & 31] = a.s_in && k < a.DK && v < a.DV ? a.s_in[((size_t)bh * a.DK + k) * a.DV + v] : 0.0f;
+  }
+  for (int sg = 0; sg + 1 < a.segs; ++sg) {
+    const size_t at = ((size_t)bh * a.segs + sg) * DMAX * DMAX;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 n = *reinterpret_cast<const float4*>(a.seg_end + at + (size_t)(kq + i) * DMAX + v0 + vq);
+      acc[i][0] = n.x; acc[i][1] = n.y; acc[i][2] = n.z; acc[i][3] = n.w;
+    }
+    for (int r0 = 0; r0 < DMAX; r0 += 32) {  // Phi[r][k] is stored [k][r]
+      __syncthreads();
+      for (int i = tid; i < 32 * DMAX; i += 256) P[i & 31][i >> 5] = a.seg_phi[at + (size_t)(i >> 5) * DMAX + r0 + (i & 31)];
+      __syncthreads();
+#pragma unroll 8
+      for (int r = 0; r < 32; ++r) {
+        const float4 p = *reinterpret_cast<const float4*>(&P[r][kq]);
+        const float4 x = *reinterpret_cast<const float4*>(&S[r0 + r][vq]);
+        const float pv[4] = {p.x, p.y, p.z, p.w}, xv[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(pv[i], xv[j], acc[i][j]);
+      }
+    }
+    __syncthreads();
+    float* dst = a.seg_start + ((size_t)bh * a.segs + sg + 1) * DMAX * DMAX;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 r = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(&S[kq + i][vq]) = r;
+      *reinterpret_cast<float4*>(dst + (size_t)(kq + i) * DMAX + v0 + vq) = r;
+    }
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
+      !delta_tile_map(&mv, a.v, a.DV, a.Hv, a.T, a.B, a.vs))
+    return cudaErrorInvalidValue;
+  auto go = [&](auto agg, auto fin) {
+    cudaError_t e = cudaSuccess;
+    const unsigned heads = (unsigned)(a.B * a.Hv);
+    if (a.segs > 1) {
+      e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+      if (e == cudaSuccess)
+        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv);
+      if (e == cudaSuccess) e = launch_k(m3_delta_seg_kernel, dim3(heads, 4), 256, 0, st, false, a);
+    }
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = launch_k(fin, dim3(heads, (unsigned)a.segs), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv);
+    return e;
+  };
+  return a.l2 ? go(m3_delta_tc_fwd_kernel<true, true>, m3_delta_tc_fwd_kernel<false, true>)
+              : go(m3_delta_tc_fwd_kernel<true, false>, m3_delta_tc_fwd_kernel<false, false>);
+}
+
+}  // namespace m3
