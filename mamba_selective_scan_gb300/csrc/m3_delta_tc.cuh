@@ -46,26 +46,27 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// one lane of a converged warp, the same one every time (lane 0 on a full warp)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// 32 columns of the calling thread's tensor-memory lane, as f32 or raw words
-__device__ __forceinline__ void tc_ld32(uint32_t t, float (&v)[32]) {
+// 16 columns of the calling thread's tensor-memory lane
+__device__ __forceinline__ void tc_ld16(uint32_t t, float (&v)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
       : "r"(t) : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]) : "memory");
+__device__ __forceinline__ void tc_st8(uint32_t t, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"r"(t), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
@@ -96,12 +97,33 @@ struct TcVec {
 struct TcTP {  // one chunk's T and P, each as bf16 hi and lo [64][64]
   unsigned char t_hi[TILE], t_lo[TILE], p_hi[TILE], p_lo[TILE];
 };
-struct TcWork {  // scratch of the warpgroup that makes T and P
+struct TcWork {  // scratch of the warps that make T and P
   float A[TC][TC + 4];
   float M[32][36];
-  float gam[TC], n[2 * TC], beta[TC];
+  float gam[TC], ss[2][2 * TC], beta[TC], nk[TC], nq[TC];
   float tot;
 };
+constexpr int TP_THREADS = 256;
+
+// mbar_wait of m3_common.cuh for the short waits of these kernels' chains:
+// the clock is looked at every 64th try only.
+__device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(a), "r"(parity) : "memory");
+    if (done) return true;
+    if ((i & 63) == 63) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > 1000000000ull) return false;
+    }
+  }
+}
 
 // What a kernel's roles share about giving up: a role that ran out of
 // patience at a wait goes on without waiting (and without issuing copies or
@@ -109,28 +131,66 @@ struct TcWork {  // scratch of the warpgroup that makes T and P
 struct TcWait {
   bool ok = true;
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    if (ok) ok = mbar_wait(bar, parity);
+    if (ok) ok = mbar_wait_fast(bar, parity);
   }
 };
 
-// A chunk's T = (I + A)^-1 and P = scale D o (Q K^T), by 128 threads.
+__device__ __forceinline__ float exp_neg(float d) { return ex2(d * LOG2E); }
+// D (16 x 8) += A (16 x K) B (K x 8) by one warp, f32 in shared memory, each
+// operand as two bf16 terms (three products; these blocks are far too small
+// for a tcgen05 product and its way through tensor memory)
+__device__ __forceinline__ void warp_mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <int K>
+__device__ __forceinline__ void warp_mma_split(float (&d)[4], const float* A, int lda, const float* B, int ldb, int lane) {
+  const int g = lane >> 2, t = (lane & 3) * 2;
+#pragma unroll
+  for (int k = 0; k < K; k += 16) {
+    uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 x = *reinterpret_cast<const float2*>(A + (g + (q & 1) * 8) * lda + k + t + (q >> 1) * 8);
+      split2(x.x, x.y, ah[q], al[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float* p = B + (k + t + q * 8) * ldb + g;
+      split2(p[0], p[ldb], bh[q], bl[q]);
+    }
+    warp_mma(d, ah, bh);
+    warp_mma(d, al, bh);
+    warp_mma(d, ah, bl);
+  }
+}
+__device__ __forceinline__ void warp_mma_store(const float (&d)[4], float* o, int ld, int lane, float sign) {
+  const int g = lane >> 2, t = (lane & 3) * 2;
+  *reinterpret_cast<float2*>(o + g * ld + t) = make_float2(sign * d[0], sign * d[1]);
+  *reinterpret_cast<float2*>(o + (g + 8) * ld + t) = make_float2(sign * d[2], sign * d[3]);
+}
+
+// A chunk's T = (I + A)^-1 and P = scale D o (Q K^T), by 256 threads.
 //
-// K over Q times K^T is one 128 x 64 MMA; a thread then has a row of K K^T
-// (threads 0-63) or of Q K^T (64-127).  I + A is inverted by blocks: the four
-// 16 x 16 diagonal blocks by forward substitution (a column per thread), then
-// 16 -> 32 -> 64 with [[P, 0], [-R C P, R]].  All of it f32; T and P are
-// stored as two bf16 terms, 17 bits of mantissa, so that what they multiply
-// keeps f32-grade sums.
+// K over Q times K^T is one 128 x 64 MMA; a thread then has half a row of
+// K K^T (rows 0-63) or of Q K^T (64-127).  I + A is inverted by blocks: the
+// eight 8 x 8 diagonal blocks by forward substitution (a column per thread),
+// then 8 -> 16 -> 32 -> 64 with [[P, 0], [-R C P, R]], the last two steps as
+// warp products of two bf16 terms.  T and P are stored as two bf16 terms, 17
+// bits of mantissa, so that what they multiply keeps f32-grade sums.
 //   kq: the stage's K/Q tiles;  acc: 64 tensor-memory columns (all lanes)
 //   g, beta: this thread's token's (threads 0-63; 0 past the sequence)
-//   empty: completes (parity ep) when tp and vec may be overwritten
+//   empty: completes (parity epar) when tp and vec may be overwritten
 template <bool L2>
 __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, TcVec& vec, TcWork& w, float g,
                                            float beta, float scale, int pt, uint64_t* mbk, uint32_t kpar,
                                            uint64_t* empty, uint32_t epar, bool wait_empty, TcWait& wait) {
   constexpr int BAR = 2;
-  const int lane = pt & 31, wp = pt >> 5;
-  if (pt == 0 && wait.ok) {
+  const int lane = pt & 31, wp = __shfl_sync(~0u, pt >> 5, 0);
+  const int row = (wp & 3) * 32 + lane, ch = wp >> 2;  // row of K over Q, half of its columns
+  if (wp == 0 && elect_one() && wait.ok) {
     tmem_fence_after_sync();
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -141,28 +201,23 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
     tc_commit(mbk);
   }
   __syncwarp();
-  // norms: thread r < 64 has row r of K, r >= 64 row r - 64 of Q
-  float nrm = 1.0f;
-  if (L2) {
+  if (L2) {  // sums of squares, half a row per thread
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
+    for (int u = 0; u < 8; ++u) {
+      uint4 x;
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                   : "r"(kq + ch * (2 * TILE) + sw(row, u)));
+      const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(kq + blk * (2 * TILE) + sw(pt, u)));
-        const uint32_t q[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float lo = __uint_as_float(q[j] << 16), hi = __uint_as_float(q[j] & 0xFFFF0000u);
-          s0 = fmaf(lo, lo, s0);
-          s1 = fmaf(hi, hi, s1);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float lo = __uint_as_float(q[j] << 16), hi = __uint_as_float(q[j] & 0xFFFF0000u);
+        s0 = fmaf(lo, lo, s0);
+        s1 = fmaf(hi, hi, s1);
       }
-    nrm = rsqrtf(s0 + s1 + DELTA_L2_EPS);
+    }
+    w.ss[ch][row] = s0 + s1;
   }
-  w.n[pt] = nrm;
   float gam = clamp_g(g);
   if (wp < 2) {
 #pragma unroll
@@ -173,59 +228,61 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
     if (pt == 31) w.tot = gam;
     w.beta[pt] = beta;
   }
-  bar_sync(BAR, 128);
+  bar_sync(BAR, TP_THREADS);
   if (wp < 2) {
     if (wp == 1) gam += w.tot;
     w.gam[pt] = gam;
+    w.nk[pt] = L2 ? rsqrtf(w.ss[0][pt] + w.ss[1][pt] + DELTA_L2_EPS) : 1.0f;
+    w.nq[pt] = L2 ? rsqrtf(w.ss[0][TC + pt] + w.ss[1][TC + pt] + DELTA_L2_EPS) : 1.0f;
   }
-  bar_sync(BAR, 128);
+  bar_sync(BAR, TP_THREADS);
   if (wait_empty) wait(empty, epar);
   if (wp < 2) {
-    const float gc = w.gam[TC - 1], eg = expf(gam);
+    const float gc = w.gam[TC - 1], eg = exp_neg(gam);
     vec.beta[pt] = beta;
-    vec.bfx[pt] = beta * eg * nrm;
-    vec.fu[pt] = expf(gc - gam) * nrm;
-    vec.fq[pt] = scale * eg * w.n[TC + pt];
-    if (pt == 0) vec.ec = expf(gc);
+    vec.bfx[pt] = beta * eg * w.nk[pt];
+    vec.fu[pt] = exp_neg(gc - gam) * w.nk[pt];
+    vec.fq[pt] = scale * eg * w.nq[pt];
+    if (pt == 0) vec.ec = exp_neg(gc);
   }
   wait(mbk, kpar);
   tmem_fence_after_sync();
   {
-    const int i = pt & (TC - 1);
-    const bool isA = wp < 2;
+    const int i = row & (TC - 1);
+    const bool isA = (wp & 3) < 2;
     const float gi = w.gam[i];
-    const float f = isA ? w.beta[i] * nrm : scale * nrm;
-    float v[32];
+    const float f = isA ? w.beta[i] * w.nk[i] : scale * w.nq[i];
+    const int last = isA ? i - 1 : i;  // last column that counts
+    const bool any = ch == 0 || (wp & 1);  // rows 0-31 have nothing in the second half
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      // columns past this warp's last row are zero (rows 0-31: half 1)
-      const bool any = half == 0 || (wp & 1);
-      if (any) tc_ld32(acc + ((uint32_t)(wp * 32) << 16) + half * 32, v);
+    for (int q = 0; q < 2; ++q) {
+      const int c0 = ch * 32 + q * 16;
+      float v[16];
+      if (any) tc_ld16(acc + ((uint32_t)((wp & 3) * 32) << 16) + c0, v);
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const int j = half * 32 + c;
-        const float4 gj = *reinterpret_cast<const float4*>(&w.gam[j]);
-        const float4 nj = *reinterpret_cast<const float4*>(&w.n[j]);
+      for (int c = 0; c < 16; c += 4) {
+        const float4 gj = *reinterpret_cast<const float4*>(&w.gam[c0 + c]);
+        const float4 nj = *reinterpret_cast<const float4*>(&w.nk[c0 + c]);
         const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, nv[4] = {nj.x, nj.y, nj.z, nj.w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const bool in = any && (isA ? j + m < i : j + m <= i);
-          v[c + m] = in ? f * nv[m] * expf(gi - gv[m]) * v[c + m] : 0.0f;
+          const float r = f * nv[m] * exp_neg(gi - gv[m]) * v[c + m];
+          v[c + m] = any && c0 + c + m <= last ? r : 0.0f;
         }
       }
       if (isA) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4)
-          *reinterpret_cast<float4*>(&w.A[i][half * 32 + c]) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        for (int c = 0; c < 16; c += 4)
+          *reinterpret_cast<float4*>(&w.A[i][c0 + c]) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
       } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
           uint4 h, l;
           split2(v[8 * u], v[8 * u + 1], h.x, l.x);
           split2(v[8 * u + 2], v[8 * u + 3], h.y, l.y);
           split2(v[8 * u + 4], v[8 * u + 5], h.z, l.z);
           split2(v[8 * u + 6], v[8 * u + 7], h.w, l.w);
-          const uint32_t at = sw(i, half * 4 + u);
+          const uint32_t at = sw(i, (c0 >> 3) + u);
           *reinterpret_cast<uint4*>(tp.p_hi + at) = h;
           *reinterpret_cast<uint4*>(tp.p_lo + at) = l;
         }
@@ -233,80 +290,67 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
     }
   }
   tmem_fence_before_sync();  // the accumulator is read: the next chunk's MMA may overwrite it
-  bar_sync(BAR, 128);
-  if (pt < TC) {  // diagonal blocks
-    const int d = (pt >> 4) * 16, c = pt & 15;
-    float x[16];
+  bar_sync(BAR, TP_THREADS);
+  if (pt < TC) {  // 8 x 8 diagonal blocks, a column per thread
+    const int d = pt & ~7, c = pt & 7;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s[4] = {i == c ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 8; ++i) {
+      float s0 = i == c ? 1.0f : 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int l = 0; l < i; l += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(&w.A[d + i][d + l]);
-        s[0] = fmaf(-a.x, x[l], s[0]);
-        if (l + 1 < i) s[1] = fmaf(-a.y, x[l + 1], s[1]);
-        if (l + 2 < i) s[2] = fmaf(-a.z, x[l + 2], s[2]);
-        if (l + 3 < i) s[3] = fmaf(-a.w, x[l + 3], s[3]);
-      }
-      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+      for (int l = 0; l < i; ++l) (l & 1 ? s1 : s0) = fmaf(-w.A[d + i][d + l], x[l], l & 1 ? s1 : s0);
+      x[i] = s0 + s1;
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w.A[d + i][d + c] = x[i];
+    for (int i = 0; i < 8; ++i) w.A[d + i][d + c] = x[i];
   }
-  bar_sync(BAR, 128);
-  {  // 16 -> 32: two blocks of 64 threads, four columns of a row each
-    const int d = (pt >> 6) * 32, r = (pt >> 2) & 15, c = (pt & 3) * 4;
-    float4 m = make_float4(0, 0, 0, 0);
+  bar_sync(BAR, TP_THREADS);
+  {  // 8 -> 16: four blocks of 64 threads, an element each
+    const int d = (pt >> 6) * 16, r = (pt >> 3) & 7, c = pt & 7;
+    float m = 0.0f;
 #pragma unroll
-    for (int l = 0; l < 16; ++l) {
-      const float a = w.A[d + 16 + r][d + l];
-      const float4 t = *reinterpret_cast<const float4*>(&w.A[d + l][d + c]);
-      m.x = fmaf(a, t.x, m.x); m.y = fmaf(a, t.y, m.y); m.z = fmaf(a, t.z, m.z); m.w = fmaf(a, t.w, m.w);
-    }
-    float* M = &w.M[(pt >> 6) * 16][0];
-    *reinterpret_cast<float4*>(M + r * 36 + c) = m;
-    bar_sync(BAR, 128);
-    m = make_float4(0, 0, 0, 0);
+    for (int l = 0; l < 8; ++l) m = fmaf(w.A[d + 8 + r][d + l], w.A[d + l][d + c], m);
+    float* M = &w.M[(pt >> 6) * 8][0];
+    M[r * 36 + c] = m;
+    bar_sync(BAR, TP_THREADS);
+    m = 0.0f;
 #pragma unroll
-    for (int l = 0; l < 16; ++l) {
-      const float a = -w.A[d + 16 + r][d + 16 + l];
-      const float4 t = *reinterpret_cast<const float4*>(M + l * 36 + c);
-      m.x = fmaf(a, t.x, m.x); m.y = fmaf(a, t.y, m.y); m.z = fmaf(a, t.z, m.z); m.w = fmaf(a, t.w, m.w);
-    }
-    *reinterpret_cast<float4*>(&w.A[d + 16 + r][d + c]) = m;
+    for (int l = 0; l < 8; ++l) m = fmaf(-w.A[d + 8 + r][d + 8 + l], M[l * 36 + c], m);
+    w.A[d + 8 + r][d + c] = m;
   }
-  bar_sync(BAR, 128);
-  {  // 32 -> 64: eight columns of a row per thread
-    const int r = pt >> 2, c = (pt & 3) * 8;
-    float m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 8
-    for (int l = 0; l < 32; ++l) {
-      const float a = w.A[32 + r][l];
-      const float4 t = *reinterpret_cast<const float4*>(&w.A[l][c]), q = *reinterpret_cast<const float4*>(&w.A[l][c + 4]);
-      m[0] = fmaf(a, t.x, m[0]); m[1] = fmaf(a, t.y, m[1]); m[2] = fmaf(a, t.z, m[2]); m[3] = fmaf(a, t.w, m[3]);
-      m[4] = fmaf(a, q.x, m[4]); m[5] = fmaf(a, q.y, m[5]); m[6] = fmaf(a, q.z, m[6]); m[7] = fmaf(a, q.w, m[7]);
+  bar_sync(BAR, TP_THREADS);
+  // 16 -> 32: four tiles of 16 x 8, a warp each
+  {
+    const int d = (wp >> 1 & 1) * 32, c = (wp & 1) * 8;
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (wp < 4) {
+      warp_mma_split<16>(m, &w.A[d + 16][d], TC + 4, &w.A[d][d + c], TC + 4, lane);
+      warp_mma_store(m, &w.M[d >> 1][c], 36, lane, 1.0f);
     }
-    *reinterpret_cast<float4*>(&w.M[r][c]) = make_float4(m[0], m[1], m[2], m[3]);
-    *reinterpret_cast<float4*>(&w.M[r][c + 4]) = make_float4(m[4], m[5], m[6], m[7]);
-    bar_sync(BAR, 128);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m[e] = 0.0f;
-#pragma unroll 8
-    for (int l = 0; l < 32; ++l) {
-      const float a = -w.A[32 + r][32 + l];
-      const float4 t = *reinterpret_cast<const float4*>(&w.M[l][c]), q = *reinterpret_cast<const float4*>(&w.M[l][c + 4]);
-      m[0] = fmaf(a, t.x, m[0]); m[1] = fmaf(a, t.y, m[1]); m[2] = fmaf(a, t.z, m[2]); m[3] = fmaf(a, t.w, m[3]);
-      m[4] = fmaf(a, q.x, m[4]); m[5] = fmaf(a, q.y, m[5]); m[6] = fmaf(a, q.z, m[6]); m[7] = fmaf(a, q.w, m[7]);
+    bar_sync(BAR, TP_THREADS);
+    if (wp < 4) {
+      m[0] = m[1] = m[2] = m[3] = 0.0f;
+      warp_mma_split<16>(m, &w.A[d + 16][d + 16], TC + 4, &w.M[d >> 1][c], 36, lane);
+      warp_mma_store(m, &w.A[d + 16][d + c], TC + 4, lane, -1.0f);
     }
-    *reinterpret_cast<float4*>(&w.A[32 + r][c]) = make_float4(m[0], m[1], m[2], m[3]);
-    *reinterpret_cast<float4*>(&w.A[32 + r][c + 4]) = make_float4(m[4], m[5], m[6], m[7]);
   }
-  bar_sync(BAR, 128);
-  {  // T as hi and lo: half a row per thread
-    const int r = pt >> 1, u0 = (pt & 1) * 4;
+  bar_sync(BAR, TP_THREADS);
+  {  // 32 -> 64: eight tiles of 16 x 8
+    const int r = (wp & 1) * 16, c = (wp >> 1) * 8;
+    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    warp_mma_split<32>(m, &w.A[32 + r][0], TC + 4, &w.A[0][c], TC + 4, lane);
+    warp_mma_store(m, &w.M[r][c], 36, lane, 1.0f);
+    bar_sync(BAR, TP_THREADS);
+    m[0] = m[1] = m[2] = m[3] = 0.0f;
+    warp_mma_split<32>(m, &w.A[32 + r][32], TC + 4, &w.M[0][c], 36, lane);
+    warp_mma_store(m, &w.A[32 + r][c], TC + 4, lane, -1.0f);
+  }
+  bar_sync(BAR, TP_THREADS);
+  {  // T as hi and lo: a quarter row per thread
+    const int r = pt >> 2, u0 = (pt & 3) * 2;
 #pragma unroll
-    for (int u = u0; u < u0 + 4; ++u) {
+    for (int u = u0; u < u0 + 2; ++u) {
       const float4 a = *reinterpret_cast<const float4*>(&w.A[r][u * 8]), b = *reinterpret_cast<const float4*>(&w.A[r][u * 8 + 4]);
       uint4 h, l;
       split2(a.x, a.y, h.x, l.x);
@@ -319,7 +363,7 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
     }
   }
   fence_proxy_async();
-  bar_sync(BAR, 128);
+  bar_sync(BAR, TP_THREADS);
 }
 
 // One chunk's tiles of a [B, T, H, D] tensor as [64 tokens][64 columns],

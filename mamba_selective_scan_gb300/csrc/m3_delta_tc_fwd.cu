@@ -1,5 +1,7 @@
 // m3_delta_tc_fwd.cu -- the gated delta rule's forward on the tensor cores:
 // bf16 activations, chunks of 64 tokens, f32-grade sums.
+#include <initializer_list>
+
 #include "m3_delta_tc.cuh"
 
 namespace m3 {
@@ -20,21 +22,23 @@ cudaError_t take_delta_fwd_status(unsigned* out) {
 
 namespace {
 
-constexpr int THREADS = 384;  // 8 warps on the state, 4 on T and P
+constexpr int CHAIN = 512;                   // threads on the state: a row's columns in quarters
+constexpr int THREADS = CHAIN + TP_THREADS + 32;  // those on T and P, and the warp that issues
 constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), V (2 tiles)
 
 struct Smem {  // after two stages
   TcTP tp[2];
   TcVec vec[2];
   TcWork work;
-  int bad[2][128];
+  int bad[128];
   uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbq, mbu, mbd, mbo;
+  uint64_t rdy_s, rdy_o, rdy_r, rdy_u;  // one arrival per chain warp
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
 
 // tensor-memory columns
-constexpr uint32_t T_S = 0;     // S as hi (64) and lo (64); also the 128 columns of U'^T K
+constexpr uint32_t T_S = 0;     // S: per 16 columns k, 8 of hi and 8 of lo; also the 128 columns of U'^T K
 constexpr uint32_t T_X = 128;   // S K^T, then U
 constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_R = 256;   // R as hi, lo (32 + 32), then U' = U e^{gam_C - gam}
@@ -58,11 +62,13 @@ constexpr uint32_t T_K = 448;   // K over Q times K^T
 // Operands that are not bf16 inputs (S, R, U, T, P) enter as hi + lo, two
 // bf16 terms: 2 MMAs against an input, 3 against another pair (lo x lo is
 // below f32's own rounding of these sums).  The state itself stays f32 in
-// registers, half a row per thread.
+// registers, a quarter row per thread.
 //
-// Roles: warps 0-7 the chain above (a row's columns in two halves), warps
-// 8-11 T and P of the chunk ahead (tc_make_tp); thread 0 also issues the MMAs
-// and the copies, two stages.  A chunk is a chain of four dependent products, bound by their
+// Roles: warps 0-15 the chain above (a row's columns in quarters), warps
+// 16-23 T and P of the chunk ahead (tc_make_tp), warp 24 issues the MMAs and
+// the copies (two stages), so that a full MMA queue stops nobody else.  The
+// columns of U'^T K that a thread reads are those its part of S goes back
+// to, so the chain needs no barrier among its warps.  A chunk is a chain of four dependent products, bound by their
 // latency and the register work between them, not by HBM.
 //
 // AGG: the segment's effect on the state instead of outputs: blockIdx.z 0
@@ -73,9 +79,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   extern __shared__ unsigned char raw[];
-  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
   const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
   const int seg = blockIdx.y;
   const int c_begin = seg * a.seg_chunks, c_end = min(a.nc, c_begin + a.seg_chunks);
@@ -90,32 +97,104 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     }
     mbar_init(&s.mbk, 1); mbar_init(&s.mbx, 1); mbar_init(&s.mbq, 1);
     mbar_init(&s.mbu, 1); mbar_init(&s.mbd, 1); mbar_init(&s.mbo, 1);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_o, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
-  const uint32_t tm = s.tmem;
+  const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   TcWait wait;
 
-  // one chunk's copies (thread 0, once the stage is free)
-  int issued = 0;
-  auto load = [&](int c) {
-    if (c >= c_end || !wait.ok) return;
-    const int g = issued++ & 1;
-    const uint32_t st = st0 + g * STAGE;
-    mbar_expect_tx(&s.kv_full[g], STAGE);
+  if (warp == (CHAIN + TP_THREADS) / 32) {
+    if (elect_one()) {
+      int issued = 0;
+      auto load = [&](int c) {  // one chunk's copies, once the stage is free
+        if (c >= c_end || !wait.ok) return;
+        const int g = issued++ & 1;
+        const uint32_t st = st0 + g * STAGE;
+        mbar_expect_tx(&s.kv_full[g], STAGE);
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
-      tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-      tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-      tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, c * TC, b, &s.kv_full[g]);
+        for (int blk = 0; blk < 2; ++blk) {
+          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, c * TC, b, &s.kv_full[g]);
+        }
+      };
+      auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tc_mma_ts(tm + d, tm + T_S + ks * 16 + p * 8, tc_desc(bt + (ks >> 2) * 2 * TILE + (ks & 3) * 32, 16, 1024),
+                      tc_idesc(128, 64, false, false), p + ks > 0);
+      };
+      auto mma_tokens = [&](uint32_t d, uint32_t ta, uint32_t bhi, uint32_t blo) {  // (hi, lo) x (hi, lo), K = 64
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma_ts(tm + d, tm + ta + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? blo : bhi) + ks * 32, 16, 1024),
+                      tc_idesc(128, 64, false, false), p + ks > 0);
+      };
+      load(c_begin);
+      load(c_begin + 1);
+      for (int c = c_begin; c < c_end; ++c) {
+        const int n = c - c_begin, i = n & 1;
+        const uint32_t st = st0 + i * STAGE, par = n & 1;
+        wait(&s.kv_full[i], (n >> 1) & 1);
+        wait(&s.rdy_s, par);  // S is in tensor memory
+        tmem_fence_after_sync();
+        if (wait.ok) {
+          mma_state(T_X, st);
+          tc_commit(&s.mbx);
+        }
+        if (!AGG) {
+          wait(&s.rdy_o, par);  // the last chunk's outputs, V and factors are read
+          if (n > 0) mbar_arrive(&s.tp_empty[i ^ 1]);
+        }
+        if (n > 0) load(c + 1);
+        if (!AGG && wait.ok) {
+          tmem_fence_after_sync();
+          mma_state(T_Q, st + TILE);
+          tc_commit(&s.mbq);
+        }
+        wait(&s.tp_full[i], (n >> 1) & 1);
+        wait(&s.rdy_r, par);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          mma_tokens(T_X, T_R, smem_u32(s.tp[i].t_hi), smem_u32(s.tp[i].t_lo));
+          tc_commit(&s.mbu);
+        }
+        wait(&s.rdy_u, par);
+        if (!AGG) wait(&s.mbq, par);  // S is read: its columns may be overwritten
+        if (wait.ok) {
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
+                        tc_idesc(128, 128, false, true), p + ks > 0);
+          tc_commit(&s.mbd);
+          if (AGG) {
+            tc_commit(&s.tp_empty[i]);
+          } else {
+            mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
+            tc_commit(&s.mbo);
+          }
+        }
+      }
+      // after a wait ran out, copies still in flight land before the block's
+      // shared memory is given up (bounded)
+      if (!wait.ok)
+        for (int i = 0; i < 2; ++i)
+          if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
     }
-  };
-
-  if (warp >= 8) {
-    const int pt = tid - 256;
+    __syncwarp();
+  } else if (warp >= CHAIN / 32) {
+    const int pt = tid - CHAIN;
     const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.g) + (int64_t)b * a.T * a.Hv + h;
     const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + (int64_t)b * a.T * a.Hv + h;
     auto gate = [&](const __nv_bfloat16* p, int c) {
@@ -134,241 +213,188 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       beta = bn;
     }
   } else {
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;  // row: the state's head_v index
+    const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const bool live = row < a.DV;
-    float S[64];  // S^T[row][64 half + k]
+    float S[32];  // S^T[row][32 qt + k]
     if (AGG) {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) S[k] = ident && half * 64 + k == row ? 1.0f : 0.0f;
+      for (int k = 0; k < 32; ++k) S[k] = ident && qt * 32 + k == row ? 1.0f : 0.0f;
     } else {
       // the segment's start: the carried state, or what the segments before left
       const float* src = seg == 0 ? a.s_in ? a.s_in + (size_t)bh * a.DK * a.DV : nullptr
                                   : a.seg_start + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
       const int ld = seg == 0 ? a.DV : DMAX;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        const int kk = half * 64 + k;
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
         S[k] = src && (seg > 0 || (live && kk < a.DK)) ? src[(size_t)kk * ld + row] : 0.0f;
       }
     }
-    const int64_t obase = ((int64_t)b * a.T * a.Hv + h) * a.DV + row;
-    uint32_t hi[32], lo[32];
+    const int64_t ostep = (int64_t)a.Hv * a.DV;
+    __nv_bfloat16* const ob = static_cast<__nv_bfloat16*>(a.o) + ((int64_t)b * a.T * a.Hv + h) * a.DV + row;
     bool nan_row = false;
+    if (qt == 0) s.bad[row] = TC;
 
-    auto put_state = [&](int c) {  // S as hi, lo into tensor memory (and the chunk's checkpoint)
-#pragma unroll
-      for (int k = 0; k < 32; ++k) split2(S[2 * k], S[2 * k + 1], hi[k], lo[k]);
-      tc_st16(tl + T_S + half * 32, hi);
-      tc_st16(tl + T_S + half * 32 + 16, hi + 16);
-      tc_st16(tl + T_S + 64 + half * 32, lo);
-      tc_st16(tl + T_S + 64 + half * 32 + 16, lo + 16);
-      if (!AGG && a.ckpt && c < c_end) {
-        unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + row * 256 + half * 128;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(ck + 32768 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-        }
-      }
+    auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
       tmem_wait_st();
       tmem_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
     };
-    // MMAs of the A operand at column ta (hi; lo at ta + 8 ksteps) against a K-major tile pair
-    auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
+    auto put_state = [&](int c) {  // S as hi, lo into tensor memory (and the chunk's checkpoint)
+      unsigned char* ck = nullptr;
+      if (!AGG && a.ckpt && c < c_end)
+        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + row * 256 + qt * 64;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < 2; ++p) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_ts(tm + d, tm + T_S + p * 64 + ks * 8, tc_desc(bt + (ks >> 2) * 2 * TILE + (ks & 3) * 32, 16, 1024),
-                    tc_idesc(128, 64, false, false), p + ks > 0);
+        for (int k = 0; k < 8; ++k) split2(S[16 * p + 2 * k], S[16 * p + 2 * k + 1], hi[k], lo[k]);
+        tc_st8(tl + T_S + qt * 32 + p * 16, hi);
+        tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
+        if (ck) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            *reinterpret_cast<uint4*>(ck + p * 32 + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + 32768 + p * 32 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          }
+        }
+      }
+      ready(&s.rdy_s);
     };
-    auto mma_tokens = [&](uint32_t d, uint32_t ta, uint32_t bhi, uint32_t blo) {  // (hi, lo) x (hi, lo), K = 64
+    // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns)
+    auto put_tokens = [&](uint32_t ta, const float (&x)[16], unsigned char* ck) {
+      uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int p = 0; p < 3; ++p)
+      for (int k = 0; k < 8; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      tc_st8(tl + ta + qt * 8, hi);
+      tc_st8(tl + ta + 32 + qt * 8, lo);
+      if (ck) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc_mma_ts(tm + d, tm + ta + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? blo : bhi) + ks * 32, 16, 1024),
-                    tc_idesc(128, 64, false, false), p + ks > 0);
+        for (int u = 0; u < 2; ++u) {
+          *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 16384 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
+      }
     };
     auto outputs = [&](int c) {  // O of chunk c from T_Q and T_O
       const int n = c - c_begin, i = n & 1;
-      float q[32], o[32];
+      float q[16], o[16];
       wait(&s.mbq, n & 1);
       wait(&s.mbo, n & 1);
       tmem_fence_after_sync();
-      tc_ld32(tl + T_Q + half * 32, q);
-      tc_ld32(tl + T_O + half * 32, o);
+      tc_ld16(tl + T_Q + qt * 16, q);
+      tc_ld16(tl + T_O + qt * 16, o);
       tmem_fence_before_sync();
-      const int t0 = c * TC + half * 32;
-      const int bad = min(s.bad[0][row], s.bad[1][row]) - half * 32;
-      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) + obase + (int64_t)t0 * a.Hv * a.DV;
+      const int t0 = c * TC + qt * 16;
+      const int bad = s.bad[row] - qt * 16;
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 fq = *reinterpret_cast<const float4*>(&s.vec[i].fq[half * 32 + j]);
-        const float f[4] = {fq.x, fq.y, fq.z, fq.w};
+      for (int j = 0; j < 16; j += 4) {
+        const float4 fq = *reinterpret_cast<const float4*>(&s.vec[i].fq[qt * 16 + j]);
+        o[j] = fmaf(fq.x, q[j], o[j]); o[j + 1] = fmaf(fq.y, q[j + 1], o[j + 1]);
+        o[j + 2] = fmaf(fq.z, q[j + 2], o[j + 2]); o[j + 3] = fmaf(fq.w, q[j + 3], o[j + 3]);
+      }
+      if (bad < 16) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          float v = fmaf(f[m], q[j + m], o[j + m]);
-          if (j + m >= bad) v = __int_as_float(0x7FFFFFFF);
-          if (live && t0 + j + m < a.T) op[(int64_t)(j + m) * a.Hv * a.DV] = __float2bfloat16_rn(v);
+        for (int j = 0; j < 16; ++j)
+          if (j >= bad) o[j] = __int_as_float(0x7FFFFFFF);
+      }
+      if (live) {
+        __nv_bfloat16* op = ob + t0 * ostep;
+        if (t0 + 16 <= a.T) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, op += ostep) *op = __float2bfloat16_rn(o[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j, op += ostep)
+            if (t0 + j < a.T) *op = __float2bfloat16_rn(o[j]);
         }
       }
     };
 
-    if (tid == 0) {
-      load(c_begin);
-      load(c_begin + 1);
-    }
-    __syncwarp();
+    bar_sync(1, CHAIN);  // s.bad is set
     put_state(c_begin);
-    bar_sync(1, 256);
     for (int c = c_begin; c < c_end; ++c) {
       const int n = c - c_begin, i = n & 1;
       const uint32_t st = st0 + i * STAGE;
       const uint32_t par = n & 1;
-      if (tid == 0) {
-        wait(&s.kv_full[i], (n >> 1) & 1);
-        tmem_fence_after_sync();
-        if (wait.ok) {
-          mma_state(T_X, st);
-          tc_commit(&s.mbx);
-        }
-      }
-      __syncwarp();
-      if (AGG) {
-        if (tid == 0 && n > 0) load(c + 1);
-      } else {
+      if (!AGG) {
         if (n > 0) outputs(c - 1);
-        bar_sync(1, 256);  // T_Q and T_O are read
-        if (tid == 0) {
-          if (n > 0) {  // every MMA of the last chunk is done and its V is read
-            mbar_arrive(&s.tp_empty[(n - 1) & 1]);
-            load(c + 1);
-          }
-          tmem_fence_after_sync();
-          if (wait.ok) {
-            mma_state(T_Q, st + TILE);
-            tc_commit(&s.mbq);
-          }
-        }
-        __syncwarp();
+        ready(&s.rdy_o);
       }
       // R = beta V - bfx X
       wait(&s.tp_full[i], (n >> 1) & 1);
       wait(&s.kv_full[i], (n >> 1) & 1);
-      wait(&s.mbx, par);
-      tmem_fence_after_sync();
-      float x[32];
-      tc_ld32(tl + T_X + half * 32, x);
+      float x[16];
       {
-        int bad = TC;
-        const uint32_t vt = st + (4 + (row >> 6)) * TILE;
+        const uint32_t vt = st + (4 + (row >> 6)) * TILE + (row & 7) * 2;
+        uint32_t v[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 be = *reinterpret_cast<const float4*>(&s.vec[i].beta[half * 32 + j]);
-          const float4 bx = *reinterpret_cast<const float4*>(&s.vec[i].bfx[half * 32 + j]);
+        for (int j = 0; j < 16; ++j) {
+          uint16_t vr;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(qt * 16 + j, (row & 63) >> 3)));
+          v[j] = vr;
+        }
+        wait(&s.mbx, par);
+        tmem_fence_after_sync();
+        tc_ld16(tl + T_X + qt * 16, x);
+        float chk = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 be = *reinterpret_cast<const float4*>(&s.vec[i].beta[qt * 16 + j]);
+          const float4 bx = *reinterpret_cast<const float4*>(&s.vec[i].bfx[qt * 16 + j]);
           const float bv[4] = {be.x, be.y, be.z, be.w}, xv[4] = {bx.x, bx.y, bx.z, bx.w};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            const int t = half * 32 + j + m;
-            uint16_t vr;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(t, (row & 63) >> 3) + (row & 7) * 2));
-            const float v = ident ? 0.0f : __uint_as_float((uint32_t)vr << 16);
-            float r = fmaf(-xv[m], x[j + m], bv[m] * v);
-            // a value that is not finite must not reach earlier tokens
-            // through the zeros of T: it is taken out, and every output
-            // from its token on becomes NaN
-            if (!(fabsf(r) <= FINITE_MAX)) {
-              r = 0.0f;
-              bad = min(bad, t);
+            const float vv = ident ? 0.0f : __uint_as_float(v[j + m] << 16);
+            x[j + m] = fmaf(-xv[m], x[j + m], bv[m] * vv);
+            chk = fmaf(x[j + m], 0.0f, chk);  // 0 unless a value is not finite
+          }
+        }
+        // a value that is not finite must not reach earlier tokens through
+        // the zeros of T: it is taken out, and every output from its token
+        // on becomes NaN
+        if (!(chk == 0.0f)) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (!(fabsf(x[j]) <= FINITE_MAX)) {
+              x[j] = 0.0f;
+              atomicMin(&s.bad[row], qt * 16 + j);
             }
-            x[j + m] = r;
-          }
         }
-        s.bad[half][row] = bad;
       }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
-      tc_st16(tl + T_R + half * 16, hi);
-      tc_st16(tl + T_R + 32 + half * 16, lo);
-      tmem_wait_st();
-      tmem_fence_before_sync();
-      bar_sync(1, 256);
-      if (tid == 0 && wait.ok) {
-        tmem_fence_after_sync();
-        mma_tokens(T_X, T_R, smem_u32(s.tp[i].t_hi), smem_u32(s.tp[i].t_lo));
-        tc_commit(&s.mbu);
-      }
-      __syncwarp();
-      nan_row = nan_row || min(s.bad[0][row], s.bad[1][row]) < TC;
+      put_tokens(T_R, x, nullptr);
+      ready(&s.rdy_r);
       wait(&s.mbu, par);
+      nan_row = s.bad[row] < TC;
       tmem_fence_after_sync();
-      tc_ld32(tl + T_X + half * 32, x);
-      if (!AGG) {
+      tc_ld16(tl + T_X + qt * 16, x);
+      if (!AGG)
+        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 65536 +
+                                        row * 128 + qt * 32
+                                  : nullptr);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
-        tc_st16(tl + T_U + half * 16, hi);
-        tc_st16(tl + T_U + 32 + half * 16, lo);
-        if (a.ckpt) {
-          unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 65536 + row * 128 + half * 64;
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-            *reinterpret_cast<uint4*>(ck + 16384 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 fu = *reinterpret_cast<const float4*>(&s.vec[i].fu[half * 32 + j]);
+      for (int j = 0; j < 16; j += 4) {
+        const float4 fu = *reinterpret_cast<const float4*>(&s.vec[i].fu[qt * 16 + j]);
         x[j] *= fu.x; x[j + 1] *= fu.y; x[j + 2] *= fu.z; x[j + 3] *= fu.w;
       }
-#pragma unroll
-      for (int k = 0; k < 16; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
-      tc_st16(tl + T_R + half * 16, hi);
-      tc_st16(tl + T_R + 32 + half * 16, lo);
-      tmem_wait_st();
-      tmem_fence_before_sync();
+      put_tokens(T_R, x, nullptr);
       const float ec = s.vec[i].ec;
-      bar_sync(1, 256);
-      if (tid == 0) {
-        if (!AGG) wait(&s.mbq, par);  // S is read: its columns may be overwritten
-        tmem_fence_after_sync();
-        if (wait.ok) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
-                        tc_idesc(128, 128, false, true), p + ks > 0);
-          tc_commit(&s.mbd);
-          if (!AGG) {
-            mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
-            tc_commit(&s.mbo);
-          } else {
-            tc_commit(&s.tp_empty[i]);
-          }
-        }
-      }
-      __syncwarp();
+      ready(&s.rdy_u);
       wait(&s.mbd, par);
       tmem_fence_after_sync();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        tc_ld32(tl + T_S + half * 64 + q * 32, x);
+        tc_ld16(tl + T_S + qt * 32 + q * 16, x);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) S[q * 32 + k] = fmaf(ec, S[q * 32 + k], x[k]);
+        for (int k = 0; k < 16; ++k) S[q * 16 + k] = fmaf(ec, S[q * 16 + k], x[k]);
       }
       if (nan_row) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) S[k] = __int_as_float(0x7FFFFFFF);
+        for (int k = 0; k < 32; ++k) S[k] = __int_as_float(0x7FFFFFFF);
       }
-      tmem_fence_before_sync();
-      bar_sync(1, 256);  // every column of U'^T K is read
-      tmem_fence_after_sync();
       put_state(c + 1);
-      bar_sync(1, 256);
     }
     if (!AGG) outputs(c_end - 1);
     // the state's way out
@@ -382,18 +408,13 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     }
     if (dst) {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) {
-        const int kk = half * 64 + k;
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
         if (AGG || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = S[k];
       }
     }
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
-  // after a wait ran out, copies still in flight land before the block's
-  // shared memory is given up (bounded)
-  if (tid == 0 && !wait.ok)
-    for (int i = 0; i < 2; ++i)
-      if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
