@@ -470,8 +470,8 @@ m3_status m3scan_norm_bwd(const m3_norm_dims* dims, m3_dtype act, const void* dy
  *   o, d_o        : the same, dense
  *   g, beta, dg, dbeta : [batch, seq_len, v_heads]     activation dtype, dense
  *   state, state_out, d_state, d_state_out : [batch, v_heads, head_k, head_v] float32
- *   ckpt          : [batch, v_heads, n_chunks, head_k, head_v] float32, the
- *                   state before step c * chunk (opaque to the caller)
+ *   ckpt          : ckpt_bytes of m3scan_delta_plan, opaque to the caller
+ *                   (per chunk and head what the backward starts from)
  *
  * g is a log decay: normally <= 0; -inf forgets everything.  head_k and
  * head_v are multiples of 8 up to 128.  Activation and state pointers are

@@ -807,15 +807,14 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     sshape = (dims.batch, dims.v_heads, dims.head_k, dims.head_v)
     if want_state and state_out is None:
         state_out = torch.empty(sshape, dtype=torch.float32, device=dev)
-    cshape = (dims.batch, dims.v_heads, pl.n_chunks, dims.head_k, dims.head_v)
     if want_ckpt and ckpt is None:
-        ckpt = torch.empty(cshape, dtype=torch.float32, device=dev)
+        ckpt = torch.empty(pl.ckpt_bytes // 4, dtype=torch.float32, device=dev)
     _check(o, "o", v.dtype, dev)
     _shape(o, "o", v.shape)
     _state_check(state, "state", dims, dev)
     _state_check(state_out, "state_out", dims, dev)
     _check(ckpt, "ckpt", torch.float32, dev)
-    _shape(ckpt, "ckpt", cshape)
+    _shape(ckpt, "ckpt", (pl.ckpt_bytes // 4,))
     if workspace is None:
         workspace = Workspace(pl.workspace_bytes, dev)
     st = _lib_handle().m3scan_delta_fwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
@@ -853,7 +852,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _check(d_o, "d_o", dt, dev)
     _shape(d_o, "d_o", v.shape)
     _check(ckpt, "ckpt", torch.float32, dev)
-    _shape(ckpt, "ckpt", (dims.batch, dims.v_heads, pl.n_chunks, dims.head_k, dims.head_v))
+    _shape(ckpt, "ckpt", (pl.ckpt_bytes // 4,))
     if workspace is None:
         workspace = Workspace(pl.workspace_bytes, dev)
     st = _lib_handle().m3scan_delta_bwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),

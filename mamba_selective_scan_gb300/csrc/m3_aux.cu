@@ -1,6 +1,6 @@
 // m3_aux.cu -- the conv backward of the two-phase backward and the decode
 // kernels, and their launch.
-#include "m3_common.cuh"
+#include "m3_delta.cuh"
 
 namespace m3 {
 
@@ -14,7 +14,11 @@ cudaError_t take_aux_status(unsigned* out) {
     const unsigned zero = 0;
     e = cudaMemcpyToSymbol(g_aux_status, &zero, sizeof(zero));
   }
-  *out = v;
+  // the gated delta rule's units report through this one
+  unsigned f = 0, b = 0;
+  if (e == cudaSuccess) e = take_delta_fwd_status(&f);
+  if (e == cudaSuccess) e = take_delta_bwd_status(&b);
+  *out = v | f | b;
   return e;
 }
 

@@ -18,7 +18,10 @@
 
 namespace m3 {
 
-constexpr size_t TC_CKPT = 98304;  // bytes per chunk and head: S^T hi, lo [128][128], U^T hi, lo [128][64], bf16
+// Per chunk and head, bf16 tiles of 128 rows (head_v) x 64 in the swizzle of
+// shared-memory operands, so that one bulk copy brings them in ready to use:
+constexpr size_t TC_CKPT = 65536;  // the forward's: S^T (head_k in two tiles), U^T hi, U^T lo
+constexpr size_t TC_BWD = 98304;   // the reverse pass's: dS^T hi, lo (two tiles each), dR^T hi, dR^T lo
 constexpr int DMAX = 128;          // head_k and head_v, at most
 constexpr float DELTA_L2_EPS = 1e-6f;  // added to the sum of squares of q and of k
 constexpr float G_MIN = -110.0f;       // exp(-110) is 0 in f32: lower log decays (and -inf) count as this
@@ -36,13 +39,14 @@ struct DeltaArgs {
   int l2;
   int segs, seg_chunks;  // time segments of the tensor-core kernels, chunks per segment
   float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
+  unsigned char* bwd;  // [B Hv][nc][TC_BWD]
   unsigned* status;
 };
 
 struct DeltaPlan {
   int B, T, Hk, Hv, DK, DV, chunk, nc;
   size_t ckpt_bytes, ws_bytes;
-  size_t o_pdq, o_pdk, o_end, o_phi, o_start;  // workspace offsets
+  size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd;  // workspace offsets
   int segs, seg_chunks;  // forward time segments
   int fwd_launches, bwd_launches;
 };
@@ -52,8 +56,8 @@ __device__ __forceinline__ float clamp_g(float g) { return fmaxf(g, G_MIN); }
 // Forward by the recurrence itself, token after token (any length and type;
 // decoding): provided by m3_delta_rec.cu
 template <typename T> cudaError_t launch_delta_rec(const DeltaArgs& a, cudaStream_t st, int sms);
-// Backward from the checkpoints in f32 arithmetic: m3_delta_bwd.cu
-template <typename T> cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st);
+// Backward of f32 activations from the checkpoints: m3_delta_bwd.cu
+cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st);
 // Sum of the per-value-head shares of dq and dk
 template <typename T> cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl);
 
@@ -62,6 +66,11 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st);
 // Tensor map of a [B, T, H, D] bf16 tensor (`stride` elements between
 // tokens) read in tiles of 64 tokens x 64 columns, 128-byte swizzle
 bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, int64_t B, int64_t stride);
+cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st);
 cudaError_t take_delta_fwd_status(unsigned* out);
+// Its backward: the reverse pass over the chunks, then every chunk's gradients
+cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st);
+cudaError_t launch_delta_tc_grad(const DeltaArgs& a, cudaStream_t st);
+cudaError_t take_delta_bwd_status(unsigned* out);
 
 }  // namespace m3

@@ -63,9 +63,11 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->B = (int)d->batch; p->T = (int)d->seq_len;
   p->Hk = (int)d->k_heads; p->Hv = (int)d->v_heads;
   p->DK = (int)d->head_k; p->DV = (int)d->head_v;
-  p->chunk = 32;
+  const bool tc = act == M3_BF16;  // the tensor-core kernels
+  p->chunk = tc ? 64 : 32;
   p->nc = (p->T + p->chunk - 1) / p->chunk;
-  p->ckpt_bytes = (size_t)p->B * p->Hv * p->nc * p->DK * p->DV * 4;
+  const size_t chunks = (size_t)p->B * p->Hv * p->nc;
+  p->ckpt_bytes = chunks * (tc ? TC_CKPT : (size_t)p->DK * p->DV * 4);
   size_t off = STATUS_BYTES;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -76,15 +78,18 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   const size_t share_bytes = shared ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
   p->o_pdq = take(share_bytes);
   p->o_pdk = take(share_bytes);
-  delta_segments((int64_t)p->B * p->Hv, (p->T + 63) / 64, &p->segs, &p->seg_chunks);
+  p->segs = 1;
+  p->seg_chunks = p->nc;
+  if (tc) delta_segments((int64_t)p->B * p->Hv, p->nc, &p->segs, &p->seg_chunks);
   const size_t seg_bytes = p->segs > 1 ? (size_t)p->B * p->Hv * p->segs * DMAX * DMAX * 4 : 0;
   p->o_end = take(seg_bytes);
   p->o_phi = take(seg_bytes);
   p->o_start = take(seg_bytes);
+  p->o_bwd = take(tc ? chunks * TC_BWD : 0);
   p->ws_bytes = off;
   const bool empty = p->B == 0 || p->T == 0;
-  p->fwd_launches = empty ? 0 : 1;
-  p->bwd_launches = empty ? 0 : shared ? 2 : 1;
+  p->fwd_launches = empty ? 0 : p->segs > 1 ? 3 : 1;
+  p->bwd_launches = empty ? 0 : p->fwd_launches + (tc ? 1 : 0) + (shared ? 1 : 0);
   return M3_OK;
 }
 
@@ -103,6 +108,19 @@ DeltaArgs delta_args(const m3_delta_dims* d, const DeltaPlan& p) {
   a.scale = d->scale != 0.0f ? d->scale : 1.0f / sqrtf((float)p.DK);
   a.l2 = d->qk_l2norm;
   return a;
+}
+
+// The workspace's parts
+void delta_ws(DeltaArgs& a, const DeltaPlan& p, void* workspace) {
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  a.status = static_cast<unsigned*>(workspace);
+  a.pdq = reinterpret_cast<float*>(ws + p.o_pdq);
+  a.pdk = reinterpret_cast<float*>(ws + p.o_pdk);
+  a.segs = p.segs; a.seg_chunks = p.seg_chunks;
+  a.seg_end = reinterpret_cast<float*>(ws + p.o_end);
+  a.seg_phi = reinterpret_cast<float*>(ws + p.o_phi);
+  a.seg_start = reinterpret_cast<float*>(ws + p.o_start);
+  a.bwd = ws + p.o_bwd;
 }
 
 // `aligned` for a list; NULL passes (presence is checked apart)
@@ -174,21 +192,8 @@ m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   DeltaArgs a = delta_args(dims, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state;
   a.o = o; a.s_out = state_out; a.ckpt = ckpt;
-  cudaError_t e;
-  if (act == M3_F32) {
-    e = launch_delta_rec<float>(a, s, sms);
-  } else if (ckpt) {
-    e = launch_delta_rec<__nv_bfloat16>(a, s, sms);
-  } else {
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    a.nc = (p.T + 63) / 64;
-    a.segs = p.segs; a.seg_chunks = p.seg_chunks;
-    a.status = static_cast<unsigned*>(workspace);
-    a.seg_end = reinterpret_cast<float*>(ws + p.o_end);
-    a.seg_phi = reinterpret_cast<float*>(ws + p.o_phi);
-    a.seg_start = reinterpret_cast<float*>(ws + p.o_start);
-    e = launch_delta_tc_fwd(a, s);
-  }
+  delta_ws(a, p, workspace);
+  const cudaError_t e = act == M3_BF16 ? launch_delta_tc_fwd(a, s) : launch_delta_rec<float>(a, s, sms);
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
@@ -230,11 +235,14 @@ m3_status m3scan_delta_bwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   DeltaArgs a = delta_args(dims, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.ckpt_in = ckpt; a.d_o = d_o; a.ds_out = d_state_out;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.ds_in = d_state;
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
-  a.status = static_cast<unsigned*>(workspace);
-  a.pdq = reinterpret_cast<float*>(ws + p.o_pdq);
-  a.pdk = reinterpret_cast<float*>(ws + p.o_pdk);
-  cudaError_t e = act == M3_BF16 ? launch_delta_bwd<__nv_bfloat16>(a, s) : launch_delta_bwd<float>(a, s);
+  delta_ws(a, p, workspace);
+  cudaError_t e;
+  if (act == M3_BF16) {
+    e = launch_delta_tc_rev(a, s);
+    if (e == cudaSuccess) e = launch_delta_tc_grad(a, s);
+  } else {
+    e = launch_delta_bwd(a, s);
+  }
   if (e == cudaSuccess && a.share > 1)
     e = act == M3_BF16 ? launch_delta_share<__nv_bfloat16>(a, s, true) : launch_delta_share<float>(a, s, true);
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;

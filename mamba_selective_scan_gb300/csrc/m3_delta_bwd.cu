@@ -399,21 +399,18 @@ __global__ void __launch_bounds__(256) m3_delta_share_kernel(const __grid_consta
   Act<T>::st(o, s.x); Act<T>::st(o + 1, s.y); Act<T>::st(o + 2, s.z); Act<T>::st(o + 3, s.w);
 }
 
-template <typename T>
 cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st) {
   // per call: the attribute belongs to the current context, and setting it costs under a microsecond
-  cudaError_t e = cudaFuncSetAttribute(m3_delta_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(m3_delta_bwd_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)sizeof(DeltaBwdSmem));
   if (e != cudaSuccess) return e;
-  return launch_k(m3_delta_bwd_kernel<T>, dim3((unsigned)(a.B * a.Hv)), 256, sizeof(DeltaBwdSmem), st, false, a);
+  return launch_k(m3_delta_bwd_kernel<float>, dim3((unsigned)(a.B * a.Hv)), 256, sizeof(DeltaBwdSmem), st, false, a);
 }
 template <typename T>
 cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl) {
   const int64_t n = (int64_t)a.B * a.T * (a.Hk * a.DK / 4);
   return launch_k(m3_delta_share_kernel<T>, dim3((unsigned)((n + 255) / 256), 2), 256, 0, st, pdl, a);
 }
-template cudaError_t launch_delta_bwd<float>(const DeltaArgs&, cudaStream_t);
-template cudaError_t launch_delta_bwd<__nv_bfloat16>(const DeltaArgs&, cudaStream_t);
 template cudaError_t launch_delta_share<float>(const DeltaArgs&, cudaStream_t, bool);
 template cudaError_t launch_delta_share<__nv_bfloat16>(const DeltaArgs&, cudaStream_t, bool);
 

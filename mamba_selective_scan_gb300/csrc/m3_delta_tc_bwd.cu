@@ -1,0 +1,879 @@
+// m3_delta_tc_bwd.cu -- the gated delta rule's backward on the tensor cores:
+// the reverse pass over the chunks (the state's adjoint), and the gradients
+// of every chunk from it.
+#include <initializer_list>
+
+#include "m3_delta_tc.cuh"
+
+namespace m3 {
+
+// nonzero once a kernel here gave up waiting
+__device__ unsigned int g_delta_bwd_status;
+
+cudaError_t take_delta_bwd_status(unsigned* out) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_delta_bwd_status, sizeof(v));
+  if (e == cudaSuccess && v) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(g_delta_bwd_status, &zero, sizeof(zero));
+  }
+  *out = v;
+  return e;
+}
+
+// ---------------------------------------------------------------------------
+// reverse pass
+// ---------------------------------------------------------------------------
+namespace rev {
+
+constexpr int CHAIN = 512;
+constexpr int THREADS = CHAIN + TP_THREADS + 32;
+constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), dO (2 tiles)
+
+struct Smem {  // after two stages
+  TcTP tp[2];
+  TcVec vec[2];
+  TcWork work;
+  uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbz, mbu, mbd;
+  uint64_t rdy_s, rdy_r, rdy_u;  // one arrival per chain warp
+  uint32_t tmem;
+};
+constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
+
+// tensor-memory columns
+constexpr uint32_t T_S = 0;    // dS: per 16 columns k, 8 of hi and 8 of lo; also the 128 columns of its update
+constexpr uint32_t T_X = 128;  // dS^T K^T, then dR
+constexpr uint32_t T_Z = 192;  // dO^T P
+constexpr uint32_t T_R = 256;  // dU as hi, lo (32 + 32), then -bfx dR
+constexpr uint32_t T_Y = 320;  // fq dO as hi, lo
+constexpr uint32_t T_K = 384;  // K over Q times K^T
+
+}  // namespace rev
+
+// The forward's chain backwards, with dS^T [head_v][head_k] in its place (see
+// m3_delta_tc_fwd_kernel for the layout, the two-term operands and the roles):
+//
+//   dU = fu (dS^T K^T) + dO^T P       dR = dU T          (N = 64 tokens)
+//   dV = beta dR
+//   dS^T = e^{gam_C} dS^T - (bfx dR) K + (fq dO^T) Q     (N = head_k)
+//
+// It leaves dS (at each chunk's end) and dR for the gradients' kernel, which
+// has no order among chunks.  AGG: a segment's effect on the adjoint, from
+// zero (blockIdx.z 0) and from the identity with dO = 0 (blockIdx.z 1).
+template <bool AGG, bool L2>
+__global__ void __launch_bounds__(rev::THREADS, 1)
+m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap md) {
+  using namespace rev;
+  extern __shared__ unsigned char raw[];
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
+  const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
+  const int seg = AGG ? blockIdx.y + 1 : blockIdx.y;
+  const int c_begin = seg * a.seg_chunks, c_end = min(a.nc, c_begin + a.seg_chunks);
+  const int N = c_end - c_begin;  // chunk n of the walk is c_end - 1 - n
+  const bool ident = AGG && blockIdx.z == 1;
+  const uint32_t st0 = smem_u32(base);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.tp_full[i], 1);
+      mbar_init(&s.tp_empty[i], 1);
+    }
+    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbz, &s.mbu, &s.mbd}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(&s.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
+  TcWait wait;
+
+  if (warp == (CHAIN + TP_THREADS) / 32) {
+    if (elect_one()) {
+      int issued = 0;
+      auto load = [&](int n) {
+        if (n >= N || !wait.ok) return;
+        const int g = issued++ & 1, c = c_end - 1 - n;
+        const uint32_t st = st0 + g * STAGE;
+        mbar_expect_tx(&s.kv_full[g], STAGE);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + 4 * TILE + blk * TILE, &md, blk * 64, h, c * TC, b, &s.kv_full[g]);
+        }
+      };
+      load(0);
+      load(1);
+      for (int n = 0; n < N; ++n) {
+        const int i = n & 1;
+        const uint32_t st = st0 + i * STAGE, par = n & 1;
+        const uint32_t th = smem_u32(s.tp[i].t_hi), tl = smem_u32(s.tp[i].t_lo);
+        const uint32_t ph = smem_u32(s.tp[i].p_hi), pl = smem_u32(s.tp[i].p_lo);
+        wait(&s.kv_full[i], (n >> 1) & 1);
+        wait(&s.rdy_s, par);  // dS is in tensor memory, the last chunk is done with
+        tmem_fence_after_sync();
+        if (wait.ok) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma_ts(tm + T_X, tm + T_S + ks * 16 + p * 8, tc_desc(st + (ks >> 2) * 2 * TILE + (ks & 3) * 32, 16, 1024),
+                        tc_idesc(128, 64, false, false), p + ks > 0);
+          tc_commit(&s.mbx);
+        }
+        if (n > 0) load(n + 1);
+        wait(&s.tp_full[i], (n >> 1) & 1);
+        if (wait.ok) {  // dO^T P: dO [64 tokens][head_v] as an M-major A, P [i][j] as an N-major B
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ss(tm + T_Z, tc_desc(st + 4 * TILE + ks * 2048, TILE, 1024), tc_desc((p ? pl : ph) + ks * 2048, 16, 1024),
+                        tc_idesc(128, 64, true, true), p + ks > 0);
+          tc_commit(&s.mbz);
+        }
+        wait(&s.rdy_r, par);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + T_X, tm + T_R + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? tl : th) + ks * 2048, 16, 1024),
+                        tc_idesc(128, 64, false, true), p + ks > 0);
+          tc_commit(&s.mbu);
+        }
+        wait(&s.rdy_u, par);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + T_S, tm + (p < 2 ? T_R : T_Y) + (p & 1) * 32 + ks * 8,
+                        tc_desc(st + (p < 2 ? 0 : TILE) + ks * 2048, 2 * TILE, 1024), tc_idesc(128, 128, false, true), p + ks > 0);
+          tc_commit(&s.mbd);
+          tc_commit(&s.tp_empty[i]);
+        }
+      }
+      // after a wait ran out, copies still in flight land before the block's
+      // shared memory is given up (bounded)
+      if (!wait.ok)
+        for (int i = 0; i < 2; ++i)
+          if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp >= CHAIN / 32) {
+    const int pt = tid - CHAIN;
+    const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.g) + (int64_t)b * a.T * a.Hv + h;
+    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + (int64_t)b * a.T * a.Hv + h;
+    auto gate = [&](const __nv_bfloat16* p, int n) {
+      const int t = (c_end - 1 - n) * TC + pt;
+      return n < N && pt < TC && t < a.T ? __bfloat162float(p[(int64_t)t * a.Hv]) : 0.0f;
+    };
+    float g = gate(gp, 0), beta = gate(bp, 0);
+    for (int n = 0; n < N; ++n) {
+      const int i = n & 1;
+      const float gn = gate(gp, n + 1), bn = gate(bp, n + 1);
+      wait(&s.kv_full[i], (n >> 1) & 1);
+      tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
+                     &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
+      if (pt == 0) mbar_arrive(&s.tp_full[i]);
+      g = gn;
+      beta = bn;
+    }
+  } else {
+    const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool live = row < a.DV;
+    float S[32];  // dS^T[row][32 qt + k]
+    if (AGG) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) S[k] = ident && qt * 32 + k == row ? 1.0f : 0.0f;
+    } else {
+      const bool last = seg == a.segs - 1;
+      const float* src = last ? a.ds_out ? a.ds_out + (size_t)bh * a.DK * a.DV : nullptr
+                              : a.seg_start + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+      const int ld = last ? a.DV : DMAX;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
+        S[k] = src && (!last || (live && kk < a.DK)) ? src[(size_t)kk * ld + row] : 0.0f;
+      }
+    }
+    __nv_bfloat16* const vb = static_cast<__nv_bfloat16*>(a.dv) + (int64_t)b * a.T * a.dvs + (int64_t)h * a.DV + row;
+
+    auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
+      tmem_wait_st();
+      tmem_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto put_state = [&](int n) {  // dS as hi, lo into tensor memory, and kept for chunk n's gradients
+      unsigned char* ck = nullptr;
+      if (!AGG && n < N) ck = a.bwd + ((size_t)bh * a.nc + c_end - 1 - n) * TC_BWD + (qt >> 1) * 16384;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split2(S[16 * p + 2 * k], S[16 * p + 2 * k + 1], hi[k], lo[k]);
+        tc_st8(tl + T_S + qt * 32 + p * 16, hi);
+        tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
+        if (ck) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t at = sw(row, (qt & 1) * 4 + p * 2 + u);
+            *reinterpret_cast<uint4*>(ck + at) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + 32768 + at) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          }
+        }
+      }
+      ready(&s.rdy_s);
+    };
+    // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns)
+    auto put_tokens = [&](uint32_t ta, const float (&x)[16], unsigned char* ck) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      if (ta != ~0u) {
+        tc_st8(tl + ta + qt * 8, hi);
+        tc_st8(tl + ta + 32 + qt * 8, lo);
+      }
+      if (ck) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          *reinterpret_cast<uint4*>(ck + sw(row, qt * 2 + u)) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 16384 + sw(row, qt * 2 + u)) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
+      }
+    };
+
+    put_state(0);
+    for (int n = 0; n < N; ++n) {
+      const int c = c_end - 1 - n, i = n & 1;
+      const uint32_t st = st0 + i * STAGE;
+      const uint32_t par = n & 1;
+      float x[16];
+      wait(&s.kv_full[i], (n >> 1) & 1);
+      wait(&s.tp_full[i], (n >> 1) & 1);
+      {  // fq dO
+        const uint32_t vt = st + (4 + (row >> 6)) * TILE + (row & 7) * 2;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          uint16_t vr;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(qt * 16 + j, (row & 63) >> 3)));
+          x[j] = ident ? 0.0f : __uint_as_float((uint32_t)vr << 16);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].fq[qt * 16 + j]);
+          x[j] *= f.x; x[j + 1] *= f.y; x[j + 2] *= f.z; x[j + 3] *= f.w;
+        }
+        put_tokens(T_Y, x, nullptr);
+      }
+      wait(&s.mbx, par);
+      tmem_fence_after_sync();
+      tc_ld16(tl + T_X + qt * 16, x);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].fu[qt * 16 + j]);
+        x[j] *= f.x; x[j + 1] *= f.y; x[j + 2] *= f.z; x[j + 3] *= f.w;
+      }
+      wait(&s.mbz, par);
+      tmem_fence_after_sync();
+      if (!ident) {
+        float z[16];
+        tc_ld16(tl + T_Z + qt * 16, z);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] += z[j];
+      }
+      put_tokens(T_R, x, nullptr);
+      ready(&s.rdy_r);
+      wait(&s.mbu, par);
+      tmem_fence_after_sync();
+      tc_ld16(tl + T_X + qt * 16, x);
+      {
+        float y[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].bfx[qt * 16 + j]);
+          y[j] = -f.x * x[j]; y[j + 1] = -f.y * x[j + 1]; y[j + 2] = -f.z * x[j + 2]; y[j + 3] = -f.w * x[j + 3];
+        }
+        put_tokens(T_R, y, nullptr);
+      }
+      const float ec = s.vec[i].ec;
+      float be[16];
+      if (!AGG) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].beta[qt * 16 + j]);
+          be[j] = f.x; be[j + 1] = f.y; be[j + 2] = f.z; be[j + 3] = f.w;
+        }
+      }
+      ready(&s.rdy_u);
+      if (!AGG) {  // while the update of dS runs
+        put_tokens(~0u, x, a.bwd + ((size_t)bh * a.nc + c) * TC_BWD + 65536);
+        const int t0 = c * TC + qt * 16;
+        if (live) {
+          __nv_bfloat16* vp = vb + (int64_t)t0 * a.dvs;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, vp += a.dvs)
+            if (t0 + j < a.T) *vp = __float2bfloat16_rn(be[j] * x[j]);
+        }
+      }
+      wait(&s.mbd, par);
+      tmem_fence_after_sync();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        tc_ld16(tl + T_S + qt * 32 + q * 16, x);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[q * 16 + k] = fmaf(ec, S[q * 16 + k], x[k]);
+      }
+      put_state(n + 1);
+    }
+    float* dst = nullptr;
+    int ld = a.DV;
+    if (AGG) {
+      dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+      ld = DMAX;
+    } else if (a.ds_in && seg == 0) {
+      dst = a.ds_in + (size_t)bh * a.DK * a.DV;
+    }
+    if (dst) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
+        if (AGG || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = S[k];
+      }
+    }
+  }
+  if (!wait.ok) report_timeout(&g_delta_bwd_status, a.status);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, md;
+  if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
+      !delta_tile_map(&md, a.d_o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
+    return cudaErrorInvalidValue;
+  auto go = [&](auto agg, auto fin) {
+    cudaError_t e = cudaSuccess;
+    const unsigned heads = (unsigned)(a.B * a.Hv);
+    if (a.segs > 1) {
+      e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
+      if (e == cudaSuccess)
+        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md);
+      if (e == cudaSuccess) e = launch_delta_seg(a, a.ds_out, true, st);
+    }
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = launch_k(fin, dim3(heads, (unsigned)a.segs), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md);
+    return e;
+  };
+  return a.l2 ? go(m3_delta_tc_rev_kernel<true, true>, m3_delta_tc_rev_kernel<false, true>)
+              : go(m3_delta_tc_rev_kernel<true, false>, m3_delta_tc_rev_kernel<false, false>);
+}
+
+// ---------------------------------------------------------------------------
+// gradients of a chunk
+// ---------------------------------------------------------------------------
+namespace grad {
+
+constexpr int EPI = 512;
+constexpr int THREADS = EPI + 32;
+// shared-memory offsets
+constexpr int KQ = 0;            // K, Q, K, Q tiles as in a stage
+constexpr int DO = 4 * TILE;     // dO, two tiles; the tile before each is read (and ignored) with it
+constexpr int S0 = 6 * TILE;     // S^T, two tiles of 128 rows; later P2 hi, lo and A2 hi, lo
+constexpr int U = S0 + 32768;    // U^T hi, lo
+constexpr int DS = U + 32768;    // dS^T hi (two tiles), lo (two tiles)
+constexpr int DR = DS + 65536;   // dR^T hi, lo
+constexpr int SMALL = DR + 32768;
+constexpr int BIG_BYTES = 32768 + (int)TC_BWD + 2 * TILE;
+
+struct Smem {  // at SMALL
+  float gam[TC], beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC];
+  float ss[4][2 * TC];
+  float row_p[4][TC], col_p[2][TC];  // sums of dP o P: per column quarter, per warp
+  float col_a[4][TC], row_a[2][TC];  // sums of dA o A (row_a without beta)
+  float dot[3][4][TC];               // Q.(dO S0^T), K.(dR S0^T), K.(U dS^T): per warp of 32 head_k
+  float red[16];
+  float ec, tot;
+  uint64_t big, s, kq, mb1, mb2, mb3, rdy1, rdy2;
+  uint32_t tmem;
+};
+constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
+
+// tensor-memory columns
+constexpr uint32_t T_YO = 0, T_Y = 64, T_Z = 128, T_DQ = 192, T_DK = 256, T_G = 320, T_DP = 384, T_KQ = 448;
+
+}  // namespace grad
+
+// The 16 values of every lane summed over the warp: lane l returns the sum of
+// value l / 2.
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int w = 8, o = 16; w >= 1; w >>= 1, o >>= 1)
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const bool up = (lane & o) != 0;
+      const float send = up ? v[j] : v[j + w], keep = up ? v[j + w] : v[j];
+      v[j] = keep + __shfl_xor_sync(~0u, send, o);
+    }
+  return v[0] + __shfl_xor_sync(~0u, v[0], 1);
+}
+
+// Persistent blocks, one (chunk, head) at a time, in any order.  With the
+// chunk's start state S0, U, dR and the adjoint dS at its end (q and k
+// normalised, D as in m3_delta.cuh):
+//
+//   G = dR U^T          dA = -G below the diagonal     dbeta_i = G_ii / beta_i
+//   dP = dO U^T         P2 = scale dP o D on and below it
+//   A2 = dA o beta D
+//   dQ = scale e^gam (dO S0^T) + P2 K
+//   dK = e^{gam_C - gam} (U dS^T) - beta e^gam (dR S0^T) + P2^T Q + (A2 + A2^T) K
+//
+// and the exponents' shares, whose suffix sums are dg.  The products with
+// S0 and dS stand transposed (head_k in the lanes, tokens in the columns), so
+// the tiles the other kernels wrote serve as M-major operands as they are and
+// no half of an MMA is idle; only G^T and dP share their lanes' two halves.
+// S0 enters with one bf16 term (it only meets gradients that are rounded to
+// bf16), everything else that is not an input with two.
+//
+// 240 KB come in and 32 to 64 KB go out per item: HBM bound, so the next
+// item's tiles are fetched as soon as the first products have read this one's.
+template <bool L2>
+__global__ void __launch_bounds__(grad::THREADS, 1)
+m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
+                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap md) {
+  using namespace grad;
+  extern __shared__ unsigned char raw[];
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  Smem& s = *reinterpret_cast<Smem*>(base + SMALL);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
+  const int64_t items = (int64_t)a.B * a.Hv * a.nc;
+  const uint32_t sb = smem_u32(base);
+
+  if (tid == 0) {
+    for (uint64_t* r : {&s.big, &s.s, &s.kq, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
+    mbar_init(&s.rdy1, EPI / 32);
+    mbar_init(&s.rdy2, EPI / 32);
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(&s.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
+  TcWait wait;
+
+  if (warp == EPI / 32) {
+    if (elect_one()) {
+      auto bulk = [&](int dst, const void* src, uint32_t bytes, uint64_t* bar) {
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                     ::"r"(sb + dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+      };
+      uint32_t n_big = 0, n_s = 0, n_kq = 0;  // loads issued
+      auto load_big = [&](int64_t it) {
+        ++n_big;
+        const int bh = (int)(it / a.nc), c = (int)(it % a.nc);
+        const unsigned char* ck = reinterpret_cast<const unsigned char*>(a.ckpt_in) + (size_t)it * TC_CKPT;
+        mbar_expect_tx(&s.big, BIG_BYTES);
+        bulk(U, ck + 32768, 32768, &s.big);
+        bulk(DS, a.bwd + (size_t)it * TC_BWD, (uint32_t)TC_BWD, &s.big);
+        for (int blk = 0; blk < 2; ++blk) tma_tile(sb + DO + blk * TILE, &md, blk * 64, bh % a.Hv, c * TC, bh / a.Hv, &s.big);
+      };
+      auto load_s = [&](int64_t it) {
+        ++n_s;
+        mbar_expect_tx(&s.s, 32768);
+        bulk(S0, reinterpret_cast<const unsigned char*>(a.ckpt_in) + (size_t)it * TC_CKPT, 32768, &s.s);
+      };
+      auto load_kq = [&](int64_t it) {
+        ++n_kq;
+        const int bh = (int)(it / a.nc), c = (int)(it % a.nc), hk = bh % a.Hv / a.share, b = bh / a.Hv;
+        mbar_expect_tx(&s.kq, 4 * TILE);
+        for (int blk = 0; blk < 2; ++blk) {
+          tma_tile(sb + KQ + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kq);
+          tma_tile(sb + KQ + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kq);
+        }
+      };
+      // a product of `steps` steps of 16 in K; operand descriptors by step
+      auto mma = [&](uint32_t d, int steps, uint32_t idesc, bool first, auto da, auto db) {
+#pragma unroll
+        for (int ks = 0; ks < steps; ++ks) tc_mma_ss(tm + d, da(ks), db(ks), idesc, !(first && ks == 0));
+      };
+      auto mn = [&](int at, int lbo) { return [=](int ks) { return tc_desc(sb + at + ks * 2048, lbo, 1024); }; };
+      auto kmaj = [&](int at, int blk) { return [=](int ks) { return tc_desc(sb + at + (ks >> 2) * blk + (ks & 3) * 32, 16, 1024); }; };
+      constexpr uint32_t NN = tc_idesc(128, 64, false, false), NM = tc_idesc(128, 64, false, true),
+                         MN = tc_idesc(128, 64, true, false), MM = tc_idesc(128, 64, true, true);
+      int64_t it = blockIdx.x;
+      if (it < items) {
+        load_kq(it);
+        load_big(it);
+        load_s(it);
+      }
+      for (uint32_t par = 0; it < items; it += gridDim.x, par ^= 1) {
+        const int64_t next = it + gridDim.x;
+        wait(&s.kq, par);
+        wait(&s.big, par);
+        wait(&s.s, par);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          mma(T_KQ, 8, NN, true, kmaj(KQ, 2 * TILE), kmaj(KQ, 2 * TILE));
+          mma(T_G, 8, MM, true, mn(U, 16384), mn(DR, 16));
+          mma(T_G, 8, MM, false, mn(U + 16384, 16384), mn(DR, 16));
+          mma(T_G, 8, MM, false, mn(U, 16384), mn(DR + 16384, 16));
+          mma(T_DP, 8, NM, true, kmaj(DO - TILE, TILE), mn(U, 16));
+          mma(T_DP, 8, NM, false, kmaj(DO - TILE, TILE), mn(U + 16384, 16));
+          mma(T_YO, 8, MN, true, mn(S0, 16384), kmaj(DO, TILE));
+          mma(T_Y, 8, MM, true, mn(S0, 16384), mn(DR, 16));
+          mma(T_Y, 8, MM, false, mn(S0, 16384), mn(DR + 16384, 16));
+          tc_commit(&s.mb1);
+          mma(T_Z, 8, MM, true, mn(DS, 16384), mn(U, 16));
+          mma(T_Z, 8, MM, false, mn(DS + 32768, 16384), mn(U, 16));
+          mma(T_Z, 8, MM, false, mn(DS, 16384), mn(U + 16384, 16));
+          tc_commit(&s.mb2);
+        }
+        wait(&s.rdy1, par);  // P2 and A2 are in place of S0; the inner product has read S0 and dS
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          constexpr int P2 = S0, A2 = S0 + 2 * TILE;
+          for (int p = 0; p < 2; ++p) {
+            mma(T_DQ, 4, MN, p == 0, mn(KQ, 2 * TILE), kmaj(P2 + p * TILE, 0));
+            mma(T_DK, 4, MM, p == 0, mn(KQ + TILE, 2 * TILE), mn(P2 + p * TILE, 16));
+            mma(T_DK, 4, MN, false, mn(KQ, 2 * TILE), kmaj(A2 + p * TILE, 0));
+            mma(T_DK, 4, MM, false, mn(KQ, 2 * TILE), mn(A2 + p * TILE, 16));
+          }
+          tc_commit(&s.mb3);
+        }
+        wait(&s.mb2, par);
+        if (next < items && wait.ok) load_big(next);
+        wait(&s.mb3, par);
+        if (next < items && wait.ok) load_s(next);
+        wait(&s.rdy2, par);  // K, Q and the accumulators are read
+        if (next < items && wait.ok) load_kq(next);
+      }
+      if (!wait.ok && n_kq) {  // as in the other kernels: copies in flight land first
+        mbar_wait(&s.kq, (n_kq - 1) & 1);
+        mbar_wait(&s.big, (n_big - 1) & 1);
+        mbar_wait(&s.s, (n_s - 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int qt = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t tl = tm + ((uint32_t)(wq * 32) << 16) + qt * 16;
+    auto ready = [&](uint64_t* bar) {
+      tmem_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    // element `row` (a head_k index) of token j of this quarter, K or Q
+    const uint32_t el = sb + KQ + (row >> 6) * 2 * TILE + (row & 7) * 2;
+    auto tok = [&](int q, int j) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(el + q * TILE + sw(qt * 16 + j, (row & 63) >> 3)));
+      return __uint_as_float((uint32_t)v << 16);
+    };
+    uint32_t par = 0;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x, par ^= 1) {
+      const int bh = (int)(it / a.nc), c = (int)(it % a.nc), b = bh / a.Hv, h = bh % a.Hv;
+      const int64_t tok0 = (int64_t)b * a.T + c * TC;  // the chunk's first token
+      const int n = min(TC, a.T - c * TC);
+      float g = 0.0f, beta = 0.0f;
+      if (tid < n) {
+        g = clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
+        beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[(tok0 + tid) * a.Hv + h]);
+      }
+      wait(&s.kq, par);
+      if (L2) {
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint4 x;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                       : "r"(sb + KQ + (qt >> 1) * (2 * TILE) + sw(row, (qt & 1) * 4 + u)));
+          const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = __uint_as_float(q[j] << 16), hi = __uint_as_float(q[j] & 0xFFFF0000u);
+            s0 = fmaf(lo, lo, s0);
+            s1 = fmaf(hi, hi, s1);
+          }
+        }
+        s.ss[qt][row] = s0 + s1;
+      }
+      if (warp < 2) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float up = __shfl_up_sync(~0u, g, o);
+          if (lane >= o) g += up;
+        }
+        if (tid == 31) s.tot = g;
+      }
+      // <dS, S0>
+      wait(&s.s, par);
+      wait(&s.big, par);
+      {
+        float acc = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = (tid + u * EPI) * 16;
+          const uint4 x = *reinterpret_cast<const uint4*>(base + S0 + at), y = *reinterpret_cast<const uint4*>(base + DS + at),
+                      z = *reinterpret_cast<const uint4*>(base + DS + 32768 + at);
+          const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc = fmaf(__uint_as_float(xv[j] << 16), __uint_as_float(yv[j] << 16) + __uint_as_float(zv[j] << 16), acc);
+            acc = fmaf(__uint_as_float(xv[j] & 0xFFFF0000u),
+                       __uint_as_float(yv[j] & 0xFFFF0000u) + __uint_as_float(zv[j] & 0xFFFF0000u), acc);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
+        if (lane == 0) s.red[warp] = acc;
+      }
+      bar_sync(1, EPI);
+      if (warp < 2) {
+        if (warp == 1) g += s.tot;
+        s.gam[tid] = g;
+        s.beta[tid] = beta;
+        const float nk = L2 ? rsqrtf((s.ss[0][tid] + s.ss[1][tid]) + (s.ss[2][tid] + s.ss[3][tid]) + DELTA_L2_EPS) : 1.0f;
+        const float nq = L2 ? rsqrtf((s.ss[0][TC + tid] + s.ss[1][TC + tid]) + (s.ss[2][TC + tid] + s.ss[3][TC + tid]) + DELTA_L2_EPS) : 1.0f;
+        const float eg = exp_neg(g);
+        s.eg[tid] = eg;
+        s.nk[tid] = nk;
+        s.nq[tid] = nq;
+        s.bfx[tid] = beta * eg * nk;
+        s.fq[tid] = a.scale * eg * nq;
+      }
+      bar_sync(1, EPI);
+      if (warp < 2) {
+        s.fu[tid] = exp_neg(s.gam[TC - 1] - g) * s.nk[tid];
+        if (tid == 0) s.ec = exp_neg(s.gam[TC - 1]);
+      }
+      wait(&s.mb1, par);
+      tmem_fence_after_sync();
+      {
+        const int r = row & (TC - 1), c0 = qt * 16;
+        const float gr = s.gam[r];
+        float v[16], k[16];
+        unsigned char* tile = base + S0;
+        if (wq < 2) {  // G^T: row j = r, columns i
+          tc_ld16(tl + T_G, v);
+          tc_ld16(tl + T_KQ, k);
+          const float nj = s.nk[r];
+          float col = 0.0f;
+#pragma unroll
+          for (int m = 0; m < 16; ++m) {
+            const int i = c0 + m;
+            if (i == r) s.gd[r] = v[m];
+            const float x = i > r ? -v[m] * exp_neg(s.gam[i] - gr) * nj * s.nk[i] : 0.0f;  // dA o D
+            const float be = s.beta[i];
+            v[m] = x * be;
+            k[m] *= x;
+            col = fmaf(k[m], be, col);
+          }
+          s.col_a[qt][r] = col;
+          const float t = reduce16(k, lane);
+          if (!(lane & 1)) s.row_a[wq][c0 + (lane >> 1)] = t;
+          tile += 2 * TILE;
+        } else {  // dP: row i = r, columns j
+          tc_ld16(tl + T_DP, v);
+          tc_ld16(tl + T_KQ, k);
+          const float f = a.scale * s.nq[r];
+          float rs = 0.0f;
+#pragma unroll
+          for (int m = 0; m < 16; ++m) {
+            const int j = c0 + m;
+            v[m] = j <= r ? v[m] * f * exp_neg(gr - s.gam[j]) * s.nk[j] : 0.0f;
+            k[m] *= v[m];
+            rs += k[m];
+          }
+          s.row_p[qt][r] = rs;
+          const float t = reduce16(k, lane);
+          if (!(lane & 1)) s.col_p[wq - 2][c0 + (lane >> 1)] = t;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint4 hi, lo;
+          split2(v[8 * u], v[8 * u + 1], hi.x, lo.x);
+          split2(v[8 * u + 2], v[8 * u + 3], hi.y, lo.y);
+          split2(v[8 * u + 4], v[8 * u + 5], hi.z, lo.z);
+          split2(v[8 * u + 6], v[8 * u + 7], hi.w, lo.w);
+          const uint32_t at = sw(r, qt * 2 + u);
+          *reinterpret_cast<uint4*>(tile + at) = hi;
+          *reinterpret_cast<uint4*>(tile + TILE + at) = lo;
+        }
+      }
+      fence_proxy_async();
+      ready(&s.rdy1);
+      // the products with the states, and their rows' dots with Q and K
+      wait(&s.mb2, par);
+      tmem_fence_after_sync();
+      float dq[16], dk[16];
+      {
+        float y[16];
+        tc_ld16(tl + T_YO, dq);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = dq[j] * tok(1, j);
+        float t = reduce16(y, lane);
+        if (!(lane & 1)) s.dot[0][wq][qt * 16 + (lane >> 1)] = t;
+        float x[16];
+        tc_ld16(tl + T_Y, dk);
+        tc_ld16(tl + T_Z, x);
+        float kv[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) kv[j] = tok(0, j);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = dk[j] * kv[j];
+        t = reduce16(y, lane);
+        if (!(lane & 1)) s.dot[1][wq][qt * 16 + (lane >> 1)] = t;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) y[j] = x[j] * kv[j];
+        t = reduce16(y, lane);
+        if (!(lane & 1)) s.dot[2][wq][qt * 16 + (lane >> 1)] = t;
+        bar_sync(1, EPI);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int i = qt * 16 + j;
+          dq[j] *= s.fq[i];
+          dk[j] = fmaf(s.fu[i], x[j], -s.bfx[i] * dk[j]);
+        }
+      }
+      if (warp == 0) {  // per-token sums: dg, dbeta and the normalisations' parts
+        float d[2], w = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = lane + 32 * e;
+          float dot[3];
+#pragma unroll
+          for (int m = 0; m < 3; ++m) dot[m] = (s.dot[m][0][i] + s.dot[m][1][i]) + (s.dot[m][2][i] + s.dot[m][3][i]);
+          const float rp = (s.row_p[0][i] + s.row_p[1][i]) + (s.row_p[2][i] + s.row_p[3][i]), cp = s.col_p[0][i] + s.col_p[1][i];
+          const float ca = (s.col_a[0][i] + s.col_a[1][i]) + (s.col_a[2][i] + s.col_a[3][i]), rah = s.row_a[0][i] + s.row_a[1][i];
+          const float be = s.beta[i], ra = be * rah;
+          const float yo = s.fq[i] * dot[0], y = s.bfx[i] * dot[1], z = s.fu[i] * dot[2];
+          s.cq[i] = L2 ? s.nq[i] * s.nq[i] * (yo + rp) : 0.0f;
+          s.ck[i] = L2 ? s.nk[i] * s.nk[i] * (z - y + cp + ra + ca) : 0.0f;
+          d[e] = (rp - cp) + (ra - ca) + yo - y - z;
+          w += z;
+          if (i < n) {
+            float db = s.gd[i] / be;
+            if (!(fabsf(be) > 1e-20f)) {
+              // U holds nothing of a token that writes nothing: from
+              // dR.(v - e^gam S0^T k) - (below the diagonal of D K K^T) G
+              const unsigned char* dr = a.bwd + (size_t)it * TC_BWD + 65536;
+              const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (tok0 + i) * a.vs + (int64_t)h * a.DV;
+              float rv = 0.0f;
+              for (int m = 0; m < a.DV; ++m) {
+                const uint32_t at = sw(m, i >> 3) + (i & 7) * 2;
+                const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + at)) +
+                                __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + 16384 + at));
+                rv = fmaf(x, __bfloat162float(vp[m]), rv);
+              }
+              db = rv - s.eg[i] * s.nk[i] * dot[1] + rah;
+            }
+            static_cast<__nv_bfloat16*>(a.dbeta)[(tok0 + i) * a.Hv + h] = __float2bfloat16_rn(db);
+          }
+        }
+        float in = lane < 16 ? s.red[lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          w += __shfl_xor_sync(~0u, w, o);
+          in += __shfl_xor_sync(~0u, in, o);
+        }
+        if (lane == 31) d[1] += fmaf(s.ec, in, w);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float x = __shfl_down_sync(~0u, d[0], o), y = __shfl_down_sync(~0u, d[1], o);
+          if (lane + o < 32) {
+            d[0] += x;
+            d[1] += y;
+          }
+        }
+        d[0] += __shfl_sync(~0u, d[1], 0);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (lane + 32 * e < n)
+            static_cast<__nv_bfloat16*>(a.dg)[(tok0 + lane + 32 * e) * a.Hv + h] = __float2bfloat16_rn(d[e]);
+      }
+      bar_sync(1, EPI);
+      wait(&s.mb3, par);
+      tmem_fence_after_sync();
+      {
+        float x[16];
+        tc_ld16(tl + T_DQ, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dq[j] += x[j];
+        tc_ld16(tl + T_DK, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) dk[j] += x[j];
+        if (L2) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            dq[j] = fmaf(-s.cq[qt * 16 + j], tok(1, j), dq[j]);
+            dk[j] = fmaf(-s.ck[qt * 16 + j], tok(0, j), dk[j]);
+          }
+        }
+      }
+      ready(&s.rdy2);
+      if (row < a.DK) {
+        const int64_t t0 = tok0 + qt * 16;
+        const int left = n - qt * 16;
+        if (a.share == 1) {
+          __nv_bfloat16* qp = static_cast<__nv_bfloat16*>(a.dq) + t0 * a.dqs + (int64_t)h * a.DK + row;
+          __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.dk) + t0 * a.dks + (int64_t)h * a.DK + row;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, qp += a.dqs, kp += a.dks)
+            if (j < left) {
+              *qp = __float2bfloat16_rn(dq[j]);
+              *kp = __float2bfloat16_rn(dk[j]);
+            }
+        } else {
+          const int64_t step = (int64_t)a.Hv * a.DK, at = (t0 * a.Hv + h) * a.DK + row;
+          float *qp = a.pdq + at, *kp = a.pdk + at;
+#pragma unroll
+          for (int j = 0; j < 16; ++j, qp += step, kp += step)
+            if (j < left) {
+              *qp = dq[j];
+              *kp = dk[j];
+            }
+        }
+      }
+    }
+  }
+  if (!wait.ok) report_timeout(&g_delta_bwd_status, a.status);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+cudaError_t launch_delta_tc_grad(const DeltaArgs& a, cudaStream_t st) {
+  CUtensorMap mq, mk, md;
+  if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
+      !delta_tile_map(&md, a.d_o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
+    return cudaErrorInvalidValue;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  auto kern = a.l2 ? m3_delta_tc_grad_kernel<true> : m3_delta_tc_grad_kernel<false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)a.B * a.Hv * a.nc;
+  return launch_k(kern, dim3((unsigned)(items < sms ? items : sms)), grad::THREADS, grad::SMEM_BYTES, st, false, a, mq, mk, md);
+}
+
+}  // namespace m3

@@ -245,7 +245,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     auto put_state = [&](int c) {  // S as hi, lo into tensor memory (and the chunk's checkpoint)
       unsigned char* ck = nullptr;
       if (!AGG && a.ckpt && c < c_end)
-        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + row * 256 + qt * 64;
+        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + (qt >> 1) * 16384;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t hi[8], lo[8];
@@ -255,10 +255,9 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
         if (ck) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            *reinterpret_cast<uint4*>(ck + p * 32 + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-            *reinterpret_cast<uint4*>(ck + 32768 + p * 32 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-          }
+          for (int u = 0; u < 2; ++u)
+            *reinterpret_cast<uint4*>(ck + sw(row, (qt & 1) * 4 + p * 2 + u)) =
+                make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
         }
       }
       ready(&s.rdy_s);
@@ -273,8 +272,8 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (ck) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          *reinterpret_cast<uint4*>(ck + u * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(ck + 16384 + u * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + sw(row, qt * 2 + u)) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 16384 + sw(row, qt * 2 + u)) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
         }
       }
     };
@@ -371,8 +370,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       if (!AGG)
-        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 65536 +
-                                        row * 128 + qt * 32
+        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 32768
                                   : nullptr);
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
@@ -443,18 +441,19 @@ bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, 
 }
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
-// start[s], 32 columns of the state per block, f32.
-__global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a) {
+// start[s], 32 columns of the state per block, f32.  rev: the adjoint's, from
+// the last segment to the first.
+__global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
   __shared__ __align__(16) float S[DMAX][32];
   __shared__ __align__(16) float P[32][DMAX + 4];
-  grid_dep_wait();
   const int tid = threadIdx.x, bh = blockIdx.x, v0 = blockIdx.y * 32;
   const int kq = (tid >> 3) * 4, vq = (tid & 7) * 4;  // 4 rows k x 4 columns per thread
   for (int i = tid; i < DMAX * 32; i += 256) {
     const int k = i >> 5, v = v0 + (i & 31);
-    S[k][i & 31] = a.s_in && k < a.DK && v < a.DV ? a.s_in[((size_t)bh * a.DK + k) * a.DV + v] : 0.0f;
+    S[k][i & 31] = first && k < a.DK && v < a.DV ? first[((size_t)bh * a.DK + k) * a.DV + v] : 0.0f;
   }
-  for (int sg = 0; sg + 1 < a.segs; ++sg) {
+  for (int n = 0; n + 1 < a.segs; ++n) {
+    const int sg = rev ? a.segs - 1 - n : n, to = rev ? sg - 1 : sg + 1;
     const size_t at = ((size_t)bh * a.segs + sg) * DMAX * DMAX;
     float acc[4][4];
 #pragma unroll
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant
       }
     }
     __syncthreads();
-    float* dst = a.seg_start + ((size_t)bh * a.segs + sg + 1) * DMAX * DMAX;
+    float* dst = a.seg_start + ((size_t)bh * a.segs + to) * DMAX * DMAX;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 r = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
@@ -487,6 +486,10 @@ __global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant
     }
     __syncthreads();
   }
+}
+
+cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st) {
+  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), 4), 256, 0, st, false, a, first, rev);
 }
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
@@ -501,7 +504,7 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
       e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
       if (e == cudaSuccess)
         e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv);
-      if (e == cudaSuccess) e = launch_k(m3_delta_seg_kernel, dim3(heads, 4), 256, 0, st, false, a);
+      if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e == cudaSuccess)
