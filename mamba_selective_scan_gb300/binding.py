@@ -9,6 +9,7 @@ library cannot be loaded the calls raise -- there is no other path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -344,16 +345,22 @@ def raw_bwd_noalloc(dims, act, x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias,
 # torch-tensor wrappers (allocation and pointer marshalling only)
 # ---------------------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _act_code(t) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return M3_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return M3_F32
     raise TypeError(f"activation dtype must be bfloat16 or float32, got {t.dtype}")
 
@@ -649,6 +656,10 @@ def m3scan_bwd_two_phase(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log
 # ---------------------------------------------------------------------------
 # block operators: layer norm and the gated delta rule
 # ---------------------------------------------------------------------------
+# Single tokens and small rows take a few microseconds on the GPU, so these
+# wrappers keep the host's share small: one pass of cheap checks per tensor
+# (the slow ones only name what is wrong), and the plan of a set of sizes is
+# made once.
 
 def m3scan_norm_plan(dims: M3NormDims, act: int) -> M3NormPlan:
     out = M3NormPlan()
@@ -671,6 +682,38 @@ def _shape(t, name, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need(t, name, dtype, index, shape):
+    """``t`` (or None), which must be a dense tensor of that dtype and shape
+    on CUDA device ``index``."""
+    if t is None or (t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous()):
+        return t
+    _shape(t, name, shape)
+    _check(t, name, dtype, _torch().device("cuda", index))
+    return t
+
+
+def _call(name, args):
+    st = getattr(_LIB, name)(*args)
+    if st != 0:
+        raise M3Error(st, name)
+
+
+def _scratch(workspace, nbytes, torch, dev):
+    """(address, bytes) of the caller's workspace or of a new one (whose
+    status block nobody can query, so it need not start at zero), and what
+    must stay alive until the call is enqueued."""
+    if workspace is not None:
+        return workspace.ptr, workspace.nbytes, workspace
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return buf.data_ptr(), nbytes, buf
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_sizes(rows, dim, eps, accumulate, code):
+    dims = M3NormDims(rows, dim, eps, accumulate)
+    return ctypes.byref(dims), m3scan_norm_plan(dims, code).workspace_bytes
+
+
 def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residual_out=None,
                     mean=None, rstd=None, want_stats=True, stream=None):
     """Layer norm over the last dimension of ``x`` [..., dim], of x + residual
@@ -679,31 +722,30 @@ def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, re
     residual unless a tensor for it is passed; ``mean`` and ``rstd`` (f32
     [...]) are None when ``want_stats`` is False."""
     torch = _torch()
-    dev, shape = x.device, tuple(x.shape)
-    dim = shape[-1]
     code = _act_code(x)
-    if y is None:
-        y = torch.empty_like(x)
-    if residual is not None and residual_out is None:
+    dev, shape, f32, index = x.device, x.shape, torch.float32, x.get_device()
+    if index < 0 or not x.is_contiguous():
+        _check(x, "x")
+    dim, rshape = shape[-1], shape[:-1]
+    _need(weight, "weight", f32, index, (dim,))
+    _need(bias, "bias", f32, index, (dim,))
+    _need(residual, "residual", f32, index, shape)
+    y = torch.empty_like(x) if y is None else _need(y, "y", x.dtype, index, shape)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", f32, index, shape)
+    elif residual is not None:
         residual_out = torch.empty_like(residual)
-    if want_stats and mean is None:
-        mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    if want_stats and rstd is None:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    _check(x, "x", None, dev)
-    _check(y, "y", x.dtype, dev)
-    _shape(y, "y", shape)
-    for n, t, s in (("weight", weight, (dim,)), ("bias", bias, (dim,)), ("residual", residual, shape),
-                    ("residual_out", residual_out, shape), ("mean", mean, shape[:-1]),
-                    ("rstd", rstd, shape[:-1])):
-        _check(t, n, torch.float32, dev)
-        _shape(t, n, s)
-    dims = M3NormDims(x.numel() // dim if dim else 0, dim, float(eps), 0)
-    st = _lib_handle().m3scan_norm_fwd(ctypes.byref(dims), code, _ptr(x), _ptr(residual), _ptr(weight),
-                                       _ptr(bias), _ptr(y), _ptr(residual_out), _ptr(mean), _ptr(rstd),
-                                       _stream_handle(stream))
-    if st != 0:
-        raise M3Error(st, "m3scan_norm_fwd")
+    if mean is not None:
+        _need(mean, "mean", f32, index, rshape)
+    elif want_stats:
+        mean = torch.empty(rshape, dtype=f32, device=dev)
+    if rstd is not None:
+        _need(rstd, "rstd", f32, index, rshape)
+    elif want_stats:
+        rstd = torch.empty(rshape, dtype=f32, device=dev)
+    dims, _ = _norm_sizes(x.numel() // dim if dim else 0, dim, float(eps), 0, code)
+    _call("m3scan_norm_fwd", (dims, code, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(),
+                              _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_of(stream, torch, dev)))
     return y, residual_out, mean, rstd
 
 
@@ -715,52 +757,59 @@ def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want
     ``dx`` (dtype of dy), ``d_residual`` (f32; None without
     ``d_residual_out`` unless passed in ``out``), ``d_weight``, ``d_bias``."""
     torch = _torch()
-    dev, shape = dy.device, tuple(dy.shape)
-    dim = shape[-1]
     code, ncode = _act_code(dy), _act_code(normed)
-    o = dict(out or {})
-    if o.get("dx") is None:
-        o["dx"] = torch.empty_like(dy)
-    if o.get("d_residual") is None:
-        o["d_residual"] = torch.empty_like(d_residual_out) if d_residual_out is not None else None
+    dev, shape, f32, index = dy.device, dy.shape, torch.float32, dy.get_device()
+    if index < 0 or not dy.is_contiguous():
+        _check(dy, "dy")
+    dim, rshape = shape[-1], shape[:-1]
+    o = dict(out) if out else {}
+    dx, d_res, d_w, d_b = o.get("dx"), o.get("d_residual"), o.get("d_weight"), o.get("d_bias")
     new = torch.zeros if accumulate_param_grads else torch.empty
-    if o.get("d_weight") is None:
-        o["d_weight"] = new((dim,), dtype=torch.float32, device=dev)
-    if o.get("d_bias") is None:
-        o["d_bias"] = new((dim,), dtype=torch.float32, device=dev) if want_bias else None
-    _check(dy, "dy", None, dev)
-    _check(normed, "normed", None, dev)
-    _shape(normed, "normed", shape)
-    _check(o["dx"], "dx", dy.dtype, dev)
-    _shape(o["dx"], "dx", shape)
-    for n, t, s in (("weight", weight, (dim,)), ("mean", mean, shape[:-1]), ("rstd", rstd, shape[:-1]),
-                    ("d_residual_out", d_residual_out, shape), ("d_residual", o["d_residual"], shape),
-                    ("d_weight", o["d_weight"], (dim,)), ("d_bias", o["d_bias"], (dim,))):
-        _check(t, n, torch.float32, dev)
-        _shape(t, n, s)
-    dims = M3NormDims(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)))
-    if workspace is None:
-        workspace = Workspace(m3scan_norm_plan(dims, code).workspace_bytes, dev)
-    st = _lib_handle().m3scan_norm_bwd(ctypes.byref(dims), code, _ptr(dy), _ptr(normed), ncode, _ptr(weight),
-                                       _ptr(mean), _ptr(rstd), _ptr(d_residual_out), _ptr(o["dx"]),
-                                       _ptr(o["d_residual"]), _ptr(o["d_weight"]), _ptr(o["d_bias"]),
-                                       workspace.ptr, workspace.nbytes, _stream_handle(stream))
-    if st != 0:
-        raise M3Error(st, "m3scan_norm_bwd")
+    _need(normed, "normed", normed.dtype, index, shape)
+    _need(weight, "weight", f32, index, (dim,))
+    _need(mean, "mean", f32, index, rshape)
+    _need(rstd, "rstd", f32, index, rshape)
+    _need(d_residual_out, "d_residual_out", f32, index, shape)
+    dx = torch.empty_like(dy) if dx is None else _need(dx, "dx", dy.dtype, index, shape)
+    if d_res is not None:
+        _need(d_res, "d_residual", f32, index, shape)
+    elif d_residual_out is not None:
+        d_res = torch.empty_like(d_residual_out)
+    d_w = new(dim, dtype=f32, device=dev) if d_w is None else _need(d_w, "d_weight", f32, index, (dim,))
+    if d_b is not None:
+        _need(d_b, "d_bias", f32, index, (dim,))
+    elif want_bias:
+        d_b = new(dim, dtype=f32, device=dev)
+    dims, nbytes = _norm_sizes(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)), code)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    _call("m3scan_norm_bwd", (dims, code, dy.data_ptr(), normed.data_ptr(), ncode, weight.data_ptr(), mean.data_ptr(),
+                              rstd.data_ptr(), _ptr(d_residual_out), dx.data_ptr(), _ptr(d_res), d_w.data_ptr(),
+                              _ptr(d_b), ws, nbytes, _stream_of(stream, torch, dev)))
+    o.update(dx=dx, d_residual=d_res, d_weight=d_w, d_bias=d_b)
     return o
 
 
-def _token_stride(t, name, dtype, dev):
+def _stream_of(stream, torch, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev.index)  # 20 times cheaper than the Stream object
+    except AttributeError:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _token_stride(t, name, dtype, index, shape):
     """Elements between tokens of a [B, T, H, D] tensor whose heads are dense
     and whose batch rows follow each other at that stride (a column view of a
-    projection's output)."""
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    projection's output); 0 = dense."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        _shape(t, name, shape)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.is_contiguous():
         return 0
-    B, T, H, D = t.shape
+    B, T, H, D = shape
     sb, stk, sh, sd = t.stride()
     if T <= 1:
         stk = sb if B > 1 else H * D
@@ -769,26 +818,28 @@ def _token_stride(t, name, dtype, dev):
     return stk
 
 
-def _delta_dims(q, k, v, g, beta, scale, qk_l2norm):
-    torch = _torch()
-    for n, t, nd in (("q", q, 4), ("k", k, 4), ("v", v, 4), ("g", g, 3), ("beta", beta, 3)):
-        if t.dim() != nd:
-            raise ValueError(f"{n} must have {nd} dimensions, got {tuple(t.shape)}")
-    dev, dt = v.device, v.dtype
-    B, T, Hv, dv = v.shape
+@functools.lru_cache(maxsize=1024)
+def _delta_sizes(code, *fields):
+    dims = M3DeltaDims(*fields)
+    pl = m3scan_delta_plan(dims, code)
+    B, _, _, Hv, dk, dv = fields[:6]
+    return ctypes.byref(dims), (B, Hv, dk, dv), pl.ckpt_bytes // 4, pl.workspace_bytes
+
+
+def _delta_fields(q, k, v, g, beta):
+    """Sizes and strides of the inputs as m3_delta_dims has them, checked."""
+    if v.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(k.shape)}, {tuple(v.shape)}")
+    dt, index = v.dtype, v.get_device()
+    if index < 0:
+        _check(v, "v")
+    B, T, Hv, dv = vshape = v.shape
     Hk, dk = k.shape[2:]
-    _shape(k, "k", (B, T, Hk, dk))
-    _shape(q, "q", (B, T, Hk, dk))
-    for n, t in (("g", g), ("beta", beta)):
-        _check(t, n, dt, dev)
-        _shape(t, n, (B, T, Hv))
-    return M3DeltaDims(B, T, Hk, Hv, dk, dv, _token_stride(q, "q", dt, dev), _token_stride(k, "k", dt, dev),
-                       _token_stride(v, "v", dt, dev), 0, 0, 0, float(scale), int(bool(qk_l2norm)))
-
-
-def _state_check(t, name, dims, dev):
-    _check(t, name, _torch().float32, dev)
-    _shape(t, name, (dims.batch, dims.v_heads, dims.head_k, dims.head_v))
+    kshape, gshape = (B, T, Hk, dk), (B, T, Hv)
+    _need(g, "g", dt, index, gshape)
+    _need(beta, "beta", dt, index, gshape)
+    return (B, T, Hk, Hv, dk, dv, _token_stride(q, "q", dt, index, kshape), _token_stride(k, "k", dt, index, kshape),
+            _token_stride(v, "v", dt, index, vshape)), index
 
 
 def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False, want_state=True,
@@ -799,29 +850,23 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     (zero).  Returns (o, state_out or None, ckpt or None); the backward needs
     ``want_ckpt=True``."""
     torch = _torch()
-    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
-    dev, code = v.device, _act_code(v)
-    pl = m3scan_delta_plan(dims, code)
-    if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    sshape = (dims.batch, dims.v_heads, dims.head_k, dims.head_v)
-    if want_state and state_out is None:
-        state_out = torch.empty(sshape, dtype=torch.float32, device=dev)
-    if want_ckpt and ckpt is None:
-        ckpt = torch.empty(pl.ckpt_bytes // 4, dtype=torch.float32, device=dev)
-    _check(o, "o", v.dtype, dev)
-    _shape(o, "o", v.shape)
-    _state_check(state, "state", dims, dev)
-    _state_check(state_out, "state_out", dims, dev)
-    _check(ckpt, "ckpt", torch.float32, dev)
-    _shape(ckpt, "ckpt", (pl.ckpt_bytes // 4,))
-    if workspace is None:
-        workspace = Workspace(pl.workspace_bytes, dev)
-    st = _lib_handle().m3scan_delta_fwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                        _ptr(beta), _ptr(state), _ptr(o), _ptr(state_out), _ptr(ckpt),
-                                        workspace.ptr, workspace.nbytes, _stream_handle(stream))
-    if st != 0:
-        raise M3Error(st, "m3scan_delta_fwd")
+    code, dev, f32 = _act_code(v), v.device, torch.float32
+    fields, index = _delta_fields(q, k, v, g, beta)
+    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, *fields, 0, 0, 0, float(scale), int(bool(qk_l2norm)))
+    _need(state, "state", f32, index, sshape)
+    o = torch.empty(v.shape, dtype=v.dtype, device=dev) if o is None else _need(o, "o", v.dtype, index, v.shape)
+    if state_out is not None:
+        _need(state_out, "state_out", f32, index, sshape)
+    elif want_state:
+        state_out = torch.empty(sshape, dtype=f32, device=dev)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", f32, index, (n_ckpt,))
+    elif want_ckpt:
+        ckpt = torch.empty(n_ckpt, dtype=f32, device=dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    _call("m3scan_delta_fwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                               _ptr(state), o.data_ptr(), _ptr(state_out), _ptr(ckpt), ws, nbytes,
+                               _stream_of(stream, torch, dev)))
     return o, state_out, ckpt
 
 
@@ -832,36 +877,27 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     (activation dtype) and d_state (f32, None unless wanted).  dq, dk and dv
     in ``out`` may be column views of a projection's gradient."""
     torch = _torch()
-    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
-    dev, dt, code = v.device, v.dtype, _act_code(v)
-    r = dict(out or {})
+    code, dev, dt, f32 = _act_code(v), v.device, v.dtype, torch.float32
+    fields, index = _delta_fields(q, k, v, g, beta)
+    r = dict(out) if out else {}
     for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
         if r.get(n) is None:
             r[n] = torch.empty(t.shape, dtype=dt, device=dev)
-        _shape(r[n], n, t.shape)
-    for n in ("dg", "dbeta"):
-        _check(r[n], n, dt, dev)
-    for n in ("dq", "dk", "dv"):
-        setattr(dims, n + "_stride", _token_stride(r[n], n, dt, dev))
-    pl = m3scan_delta_plan(dims, code)
+    _need(r["dg"], "dg", dt, index, g.shape)
+    _need(r["dbeta"], "dbeta", dt, index, g.shape)
+    strides = [_token_stride(r[n], n, dt, index, t.shape) for n, t in (("dq", q), ("dk", k), ("dv", v))]
+    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, *fields, *strides, float(scale), int(bool(qk_l2norm)))
     if r.get("d_state") is None:
-        r["d_state"] = torch.empty((dims.batch, dims.v_heads, dims.head_k, dims.head_v), dtype=torch.float32,
-                                   device=dev) if want_d_state else None
-    _state_check(d_state_out, "d_state_out", dims, dev)
-    _state_check(r["d_state"], "d_state", dims, dev)
-    _check(d_o, "d_o", dt, dev)
-    _shape(d_o, "d_o", v.shape)
-    _check(ckpt, "ckpt", torch.float32, dev)
-    _shape(ckpt, "ckpt", (pl.ckpt_bytes // 4,))
-    if workspace is None:
-        workspace = Workspace(pl.workspace_bytes, dev)
-    st = _lib_handle().m3scan_delta_bwd(ctypes.byref(dims), code, _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                        _ptr(beta), _ptr(ckpt), _ptr(d_o), _ptr(d_state_out), _ptr(r["dq"]),
-                                        _ptr(r["dk"]), _ptr(r["dv"]), _ptr(r["dg"]), _ptr(r["dbeta"]),
-                                        _ptr(r["d_state"]), workspace.ptr, workspace.nbytes,
-                                        _stream_handle(stream))
-    if st != 0:
-        raise M3Error(st, "m3scan_delta_bwd")
+        r["d_state"] = torch.empty(sshape, dtype=f32, device=dev) if want_d_state else None
+    _need(d_state_out, "d_state_out", f32, index, sshape)
+    _need(r["d_state"], "d_state", f32, index, sshape)
+    _need(d_o, "d_o", dt, index, v.shape)
+    _need(ckpt, "ckpt", f32, index, (n_ckpt,))
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    _call("m3scan_delta_bwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                               ckpt.data_ptr(), d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(),
+                               r["dk"].data_ptr(), r["dv"].data_ptr(), r["dg"].data_ptr(), r["dbeta"].data_ptr(),
+                               _ptr(r["d_state"]), ws, nbytes, _stream_of(stream, torch, dev)))
     return r
 
 
@@ -869,16 +905,14 @@ def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, 
     """A short window (typically one token: T = 1) from the carried ``state``
     [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""
     torch = _torch()
-    dims = _delta_dims(q, k, v, g, beta, scale, qk_l2norm)
-    dev = v.device
+    code, dev = _act_code(v), v.device
+    fields, index = _delta_fields(q, k, v, g, beta)
+    dims, sshape, _, _ = _delta_sizes(code, *fields, 0, 0, 0, float(scale), int(bool(qk_l2norm)))
     if o is None:
         o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _check(o, "o", v.dtype, dev)
-    _shape(o, "o", v.shape)
-    _state_check(state, "state", dims, dev)
-    st = _lib_handle().m3scan_delta_decode(ctypes.byref(dims), _act_code(v), _ptr(q), _ptr(k), _ptr(v),
-                                           _ptr(g), _ptr(beta), _ptr(state), _ptr(o),
-                                           _stream_handle(stream))
-    if st != 0:
-        raise M3Error(st, "m3scan_delta_decode")
+    else:
+        _need(o, "o", v.dtype, index, v.shape)
+    _need(state, "state", torch.float32, index, sshape)
+    _call("m3scan_delta_decode", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                  state.data_ptr(), o.data_ptr(), _stream_of(stream, torch, dev)))
     return o

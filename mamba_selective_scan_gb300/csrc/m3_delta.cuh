@@ -51,6 +51,9 @@ struct DeltaPlan {
   int fwd_launches, bwd_launches;
 };
 
+// SM count of the current device (a property that never changes: kept)
+cudaError_t sm_count(int* sms);
+
 __device__ __forceinline__ float clamp_g(float g) { return fmaxf(g, G_MIN); }
 
 // Forward by the recurrence itself, token after token (any length and type;

@@ -2,11 +2,24 @@
 // the launch plan and the launch sequences.
 #include <math.h>
 
+#include <atomic>
 #include <initializer_list>
 
 #include "m3_delta.cuh"
 
 namespace m3 {
+
+cudaError_t sm_count(int* sms) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+  return e;
+}
+
 namespace {
 
 m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
@@ -130,14 +143,6 @@ bool all_aligned(std::initializer_list<const void*> ptrs, size_t n) {
   return true;
 }
 
-m3_status sm_count(int* sms) {
-  int dev = 0;
-  if (note(cudaGetDevice(&dev)) != cudaSuccess ||
-      note(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return M3_ERR_CUDA;
-  return M3_OK;
-}
-
 // No tokens: the state passes through (zero where there is none)
 m3_status pass_state(const float* in, float* out, size_t bytes, cudaStream_t s) {
   if (!out || bytes == 0 || in == out) return M3_OK;
@@ -188,7 +193,7 @@ m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   st = check_workspace(workspace, workspace_bytes, p.ws_bytes);
   if (st != M3_OK) return st;
   int sms = 0;
-  if ((st = sm_count(&sms)) != M3_OK) return st;
+  if (note(sm_count(&sms)) != cudaSuccess) return M3_ERR_CUDA;
   DeltaArgs a = delta_args(dims, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state;
   a.o = o; a.s_out = state_out; a.ckpt = ckpt;
@@ -207,7 +212,7 @@ m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const voi
   if (p.B == 0 || p.T == 0) return M3_OK;
   if (!q || !k || !v || !g || !beta || !o || !state) return M3_ERR_NULL;
   int sms = 0;
-  if ((st = sm_count(&sms)) != M3_OK) return st;
+  if (note(sm_count(&sms)) != cudaSuccess) return M3_ERR_CUDA;
   DeltaArgs a = delta_args(dims, p);
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state; a.s_out = state; a.o = o;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -866,9 +866,8 @@ cudaError_t launch_delta_tc_grad(const DeltaArgs& a, cudaStream_t st) {
   if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
       !delta_tile_map(&md, a.d_o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
   auto kern = a.l2 ? m3_delta_tc_grad_kernel<true> : m3_delta_tc_grad_kernel<false>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad::SMEM_BYTES);
   if (e != cudaSuccess) return e;

@@ -18,7 +18,7 @@
 
 #include <initializer_list>
 
-#include "m3_common.cuh"
+#include "m3_delta.cuh"
 
 namespace m3 {
 
@@ -378,7 +378,7 @@ void (*bwd_kernel_nv(int nv))(const NormArgs) {
 
 template <typename T, typename X>
 cudaError_t launch_norm_bwd(NormArgs a, bool vec, cudaStream_t s) {
-  int nv = 0, sms = 0, dev = 0, occ = 0;
+  int nv = 0, sms = 0, occ = 0;
   const bool ok = vec ? norm_shape(a.dim, 4, 4, &a.wpr, &nv) || norm_shape(a.dim, 4, 8, &a.wpr, &nv)
                       : norm_shape(a.dim, 1, 4, &a.wpr, &nv) || norm_shape(a.dim, 1, 8, &a.wpr, &nv) ||
                             norm_shape(a.dim, 1, 16, &a.wpr, &nv);
@@ -389,8 +389,7 @@ cudaError_t launch_norm_bwd(NormArgs a, bool vec, cudaStream_t s) {
   const size_t smem = R > 1 ? (size_t)R * 2 * a.dim * 4 : 0;
   auto kern = vec ? bwd_kernel_nv<T, X, 4>(nv) : bwd_kernel_nv<T, X, 1>(nv);
   if (!kern) return cudaErrorInvalidValue;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = sm_count(&sms);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, (int)block, smem);
   if (e != cudaSuccess) return e;
   int64_t grid = (int64_t)sms * (occ < 1 ? 1 : occ);
