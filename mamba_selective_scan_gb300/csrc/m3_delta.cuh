@@ -37,7 +37,9 @@ struct DeltaArgs {
   int chunk, nc;
   float scale;
   int l2;
-  int segs, seg_chunks;  // time segments of the tensor-core kernels, chunks per segment
+  bool stream;           // tensor-core kernels: equal shares of all heads' chunks, one block per SM
+  unsigned* flags;       // stream: [B Hv], set once a head's state was handed over (in seg_start)
+  int segs, seg_chunks;  // else: time segments, chunks per segment
   float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
   unsigned char* bwd;  // [B Hv][nc][TC_BWD]
   unsigned* status;
@@ -46,8 +48,9 @@ struct DeltaArgs {
 struct DeltaPlan {
   int B, T, Hk, Hv, DK, DV, chunk, nc;
   size_t ckpt_bytes, ws_bytes;
-  size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd;  // workspace offsets
-  int segs, seg_chunks;  // forward time segments
+  size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd, o_flags;  // workspace offsets
+  bool stream;           // more heads than SMs: equal shares instead of segments
+  int segs, seg_chunks;  // time segments
   int fwd_launches, bwd_launches;
 };
 

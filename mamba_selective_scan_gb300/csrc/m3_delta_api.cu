@@ -93,15 +93,19 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->o_pdk = take(share_bytes);
   p->segs = 1;
   p->seg_chunks = p->nc;
-  if (tc) delta_segments((int64_t)p->B * p->Hv, p->nc, &p->segs, &p->seg_chunks);
+  // more heads than SMs: equal shares of all chunks, a block per SM
+  const int64_t heads = (int64_t)p->B * p->Hv;
+  p->stream = tc && heads > 152 && p->nc > 0;
+  if (tc && !p->stream) delta_segments(heads, p->nc, &p->segs, &p->seg_chunks);
   const size_t seg_bytes = p->segs > 1 ? (size_t)p->B * p->Hv * p->segs * DMAX * DMAX * 4 : 0;
   p->o_end = take(seg_bytes);
   p->o_phi = take(seg_bytes);
-  p->o_start = take(seg_bytes);
+  p->o_start = take(p->stream ? (size_t)heads * DMAX * DMAX * 4 : seg_bytes);
+  p->o_flags = take(p->stream ? (size_t)heads * 4 : 0);
   p->o_bwd = take(tc ? chunks * TC_BWD : 0);
   p->ws_bytes = off;
   const bool empty = p->B == 0 || p->T == 0;
-  p->fwd_launches = empty ? 0 : p->segs > 1 ? 3 : 1;
+  p->fwd_launches = empty ? 0 : p->segs > 1 ? 3 : 1;  // (shares: and a memset of their flags)
   p->bwd_launches = empty ? 0 : p->fwd_launches + (tc ? 1 : 0) + (shared ? 1 : 0);
   return M3_OK;
 }
@@ -129,6 +133,8 @@ void delta_ws(DeltaArgs& a, const DeltaPlan& p, void* workspace) {
   a.status = static_cast<unsigned*>(workspace);
   a.pdq = reinterpret_cast<float*>(ws + p.o_pdq);
   a.pdk = reinterpret_cast<float*>(ws + p.o_pdk);
+  a.stream = p.stream;
+  a.flags = reinterpret_cast<unsigned*>(ws + p.o_flags);
   a.segs = p.segs; a.seg_chunks = p.seg_chunks;
   a.seg_end = reinterpret_cast<float*>(ws + p.o_end);
   a.seg_phi = reinterpret_cast<float*>(ws + p.o_phi);

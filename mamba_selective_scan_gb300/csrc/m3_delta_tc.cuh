@@ -56,13 +56,23 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // 16 columns of the calling thread's tensor-memory lane
-__device__ __forceinline__ void tc_ld16(uint32_t t, float (&v)[16]) {
+__device__ __forceinline__ void tc_ld16(uint32_t t, float2 (&v)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y), "=f"(v[3].x),
+        "=f"(v[3].y), "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y), "=f"(v[6].x), "=f"(v[6].y),
+        "=f"(v[7].x), "=f"(v[7].y)
       : "r"(t) : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t t, float (&v)[16]) {
+  float2 x[8];
+  tc_ld16(t, x);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[2 * j] = x[j].x;
+    v[2 * j + 1] = x[j].y;
+  }
 }
 __device__ __forceinline__ void tc_st8(uint32_t t, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -70,15 +80,21 @@ __device__ __forceinline__ void tc_st8(uint32_t t, const uint32_t (&v)[8]) {
 }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// x = hi + lo + at most 2^-18 |x|: two bf16 terms, packed for neighbours a, b
-// (a in the low half)
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  const float2 f = __bfloat1622float2(h);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(a - f.x, b - f.y);
+// x = hi + lo + at most 2^-18 |x|: two bf16 terms of a pair (x in the low
+// half)
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
+  const float2 r = __ffma2_rn(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), f2b(-1.0f), x);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(r.x, r.y);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) { split2(make_float2(a, b), hi, lo); }
+// values 2 j and 2 j + 1 of 16 consecutive shared-memory floats, as pairs
+struct Vec16 {
+  const float* p;
+  __device__ __forceinline__ float2 operator[](int j) const { return *reinterpret_cast<const float2*>(p + 2 * j); }
+};
 // byte offset of the 16-byte unit u of row r in a swizzled tile
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
@@ -106,14 +122,14 @@ struct TcWork {  // scratch of the warps that make T and P
 constexpr int TP_THREADS = 256;
 
 // mbar_wait of m3_common.cuh for the short waits of these kernels' chains:
-// the clock is looked at every 64th try only.
+// a try may sleep up to 20 us, and the clock is looked at every 64th only.
 __device__ __forceinline__ bool mbar_wait_fast(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     uint32_t done;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done) : "r"(a), "r"(parity) : "memory");
     if (done) return true;
@@ -172,6 +188,88 @@ __device__ __forceinline__ void warp_mma_store(const float (&d)[4], float* o, in
   *reinterpret_cast<float2*>(o + (g + 8) * ld + t) = make_float2(sign * d[2], sign * d[3]);
 }
 
+// Which (head, chunk) a block works on at each step.  Either one run of
+// chunks of one head (a time segment), or, when there are more heads than
+// SMs, an equal share of all chunks of all heads: block s of G has the range
+// [s, s + 1) / G of the heads' chunks laid end to end.  It starts with the
+// first chunks of the head that the next block ends, hands that head's state
+// on, goes through its whole heads, and ends with the last chunks of the
+// head that the block before began.  A share is at least a head long, so the
+// part handed on is never longer than what its receiver does before it.
+struct TcStep {
+  int bh, c;          // head (batch row x value head), chunk
+  bool first, last;   // of a run
+  bool take, give;    // the run starts from, or ends in, a state handed over
+};
+struct TcWalk {
+  int nc, n, len_a, whole, h0, c0, ha, ca;
+  bool stream;
+  __device__ __forceinline__ TcWalk(const DeltaArgs& a, int seg) {
+    nc = a.nc;
+    stream = a.stream;
+    if (stream) {
+      const int64_t total = (int64_t)a.B * a.Hv * nc;
+      const int64_t r0 = total * blockIdx.x / gridDim.x, r1 = total * (blockIdx.x + 1) / gridDim.x;
+      const int hs = (int)(r0 / nc);
+      c0 = (int)(r0 % nc);
+      ha = (int)(r1 / nc);
+      len_a = (int)(r1 % nc);
+      ca = 0;
+      h0 = c0 ? hs : hs - 1;  // whole heads are h0 + 1 ...
+      whole = ha - h0 - 1;
+      n = (int)(r1 - r0);
+    } else {
+      ha = blockIdx.x;
+      ca = seg * a.seg_chunks;
+      len_a = n = min(nc, ca + a.seg_chunks) - ca;
+      h0 = c0 = whole = 0;
+    }
+  }
+  __device__ __forceinline__ TcStep at(int i) const {
+    TcStep r;
+    if (i < len_a) {
+      r.bh = ha;
+      r.c = ca + i;
+      r.first = i == 0;
+      r.last = i == len_a - 1;
+      r.take = false;
+      r.give = stream;
+    } else if (i < len_a + whole * nc) {
+      const int m = i - len_a, w = m / nc;
+      r.bh = h0 + 1 + w;
+      r.c = m - w * nc;
+      r.first = r.c == 0;
+      r.last = r.c == nc - 1;
+      r.take = r.give = false;
+    } else {
+      r.bh = h0;
+      r.c = c0 + i - len_a - whole * nc;
+      r.first = r.c == c0;
+      r.last = r.c == nc - 1;
+      r.take = true;
+      r.give = false;
+    }
+    return r;
+  }
+};
+// The flag of a state handed over: set behind its writes, waited for (at
+// most ten seconds; see TcWalk for why it is hardly ever waited for at all).
+__device__ __forceinline__ void flag_set(unsigned* f) {
+  asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(f) : "memory");
+}
+__device__ __forceinline__ bool flag_wait(const unsigned* f) {
+  uint64_t t0 = 0;
+  for (;;) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(f) : "memory");
+    if (v) return true;
+    const uint64_t now = global_ns();
+    if (t0 == 0) t0 = now;
+    else if (now - t0 > 10000000000ull) return false;
+    __nanosleep(200);
+  }
+}
+
 // A chunk's T = (I + A)^-1 and P = scale D o (Q K^T), by 256 threads.
 //
 // K over Q times K^T is one 128 x 64 MMA; a thread then has half a row of
@@ -202,7 +300,7 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
   }
   __syncwarp();
   if (L2) {  // sums of squares, half a row per thread
-    float s0 = 0.0f, s1 = 0.0f;
+    float2 s0 = f2b(0.0f), s1 = f2b(0.0f);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       uint4 x;
@@ -211,14 +309,13 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
       const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float lo = __uint_as_float(q[j] << 16), hi = __uint_as_float(q[j] & 0xFFFF0000u);
-        s0 = fmaf(lo, lo, s0);
-        s1 = fmaf(hi, hi, s1);
+        const float2 e = make_float2(__uint_as_float(q[j] << 16), __uint_as_float(q[j] & 0xFFFF0000u));
+        (j & 1 ? s1 : s0) = __ffma2_rn(e, e, j & 1 ? s1 : s0);
       }
     }
-    w.ss[ch][row] = s0 + s1;
+    w.ss[ch][row] = (s0.x + s0.y) + (s1.x + s1.y);
   }
-  float gam = clamp_g(g);
+  float gam = clamp_g(g) * LOG2E;  // exponents in powers of two
   if (wp < 2) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -238,12 +335,12 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
   bar_sync(BAR, TP_THREADS);
   if (wait_empty) wait(empty, epar);
   if (wp < 2) {
-    const float gc = w.gam[TC - 1], eg = exp_neg(gam);
+    const float gc = w.gam[TC - 1], eg = ex2(gam);
     vec.beta[pt] = beta;
     vec.bfx[pt] = beta * eg * w.nk[pt];
-    vec.fu[pt] = exp_neg(gc - gam) * w.nk[pt];
+    vec.fu[pt] = ex2(gc - gam) * w.nk[pt];
     vec.fq[pt] = scale * eg * w.nq[pt];
-    if (pt == 0) vec.ec = exp_neg(gc);
+    if (pt == 0) vec.ec = ex2(gc);
   }
   wait(mbk, kpar);
   tmem_fence_after_sync();
@@ -253,35 +350,43 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
     const float gi = w.gam[i];
     const float f = isA ? w.beta[i] * w.nk[i] : scale * w.nq[i];
     const int last = isA ? i - 1 : i;  // last column that counts
-    const bool any = ch == 0 || (wp & 1);  // rows 0-31 have nothing in the second half
+    const bool any = ch == 0 || (wp & 1);   // rows 0-31 have nothing in the second half,
+    const bool all = ch == 0 && (wp & 1);   // rows 32-63 everything in the first
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const int c0 = ch * 32 + q * 16;
-      float v[16];
-      if (any) tc_ld16(acc + ((uint32_t)((wp & 3) * 32) << 16) + c0, v);
+      float2 v[8];
+      if (any) {
+        tc_ld16(acc + ((uint32_t)((wp & 3) * 32) << 16) + c0, v);
+        const Vec16 gj{&w.gam[c0]}, nj{&w.nk[c0]};
 #pragma unroll
-      for (int c = 0; c < 16; c += 4) {
-        const float4 gj = *reinterpret_cast<const float4*>(&w.gam[c0 + c]);
-        const float4 nj = *reinterpret_cast<const float4*>(&w.nk[c0 + c]);
-        const float gv[4] = {gj.x, gj.y, gj.z, gj.w}, nv[4] = {nj.x, nj.y, nj.z, nj.w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float r = f * nv[m] * exp_neg(gi - gv[m]) * v[c + m];
-          v[c + m] = any && c0 + c + m <= last ? r : 0.0f;
+        for (int m = 0; m < 8; ++m) {
+          const float2 d = __ffma2_rn(gj[m], f2b(-1.0f), f2b(gi));
+          v[m] = __fmul2_rn(__fmul2_rn(__fmul2_rn(nj[m], f2b(f)), ex2x2(d)), v[m]);
         }
+        if (!all) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            if (c0 + 2 * m > last) v[m].x = 0.0f;
+            if (c0 + 2 * m + 1 > last) v[m].y = 0.0f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) v[m] = f2b(0.0f);
       }
       if (isA) {
 #pragma unroll
-        for (int c = 0; c < 16; c += 4)
-          *reinterpret_cast<float4*>(&w.A[i][c0 + c]) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        for (int m = 0; m < 8; m += 2)
+          *reinterpret_cast<float4*>(&w.A[i][c0 + 2 * m]) = make_float4(v[m].x, v[m].y, v[m + 1].x, v[m + 1].y);
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint4 h, l;
-          split2(v[8 * u], v[8 * u + 1], h.x, l.x);
-          split2(v[8 * u + 2], v[8 * u + 3], h.y, l.y);
-          split2(v[8 * u + 4], v[8 * u + 5], h.z, l.z);
-          split2(v[8 * u + 6], v[8 * u + 7], h.w, l.w);
+          split2(v[4 * u], h.x, l.x);
+          split2(v[4 * u + 1], h.y, l.y);
+          split2(v[4 * u + 2], h.z, l.z);
+          split2(v[4 * u + 3], h.w, l.w);
           const uint32_t at = sw(i, (c0 >> 3) + u);
           *reinterpret_cast<uint4*>(tp.p_hi + at) = h;
           *reinterpret_cast<uint4*>(tp.p_lo + at) = l;
@@ -372,6 +477,33 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, i
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(head), "r"(tok), "r"(b), "r"(smem_u32(bar)) : "memory");
+}
+
+// The same tile back (only columns below D and tokens below T are written)
+__device__ __forceinline__ void tma_tile_store(const CUtensorMap* map, uint32_t src, int col, int head, int tok, int b) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];"
+               ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(col), "r"(head), "r"(tok), "r"(b) : "memory");
+}
+
+// The chain kernels' grid: a block per (head, segment), or one per SM in
+// equal shares.  Those wait for a state that the block before hands over, so
+// they are launched cooperatively (all of them resident at once).
+template <typename... Args, typename... Vals>
+cudaError_t launch_delta_blocks(void (*kern)(Args...), const DeltaArgs& a, int threads, size_t smem, cudaStream_t st, Vals... maps) {
+  cudaLaunchConfig_t cfg{};
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = a.stream ? dim3((unsigned)sms) : dim3((unsigned)(a.B * a.Hv), (unsigned)a.segs);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.stream ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a, maps...);
 }
 
 }  // namespace m3

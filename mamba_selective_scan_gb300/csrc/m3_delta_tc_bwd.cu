@@ -32,6 +32,7 @@ constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), dO (2 tiles)
 
 struct Smem {  // after two stages
   TcTP tp[2];
+  unsigned char v[2 * TILE];  // a chunk's dV, for the tile store
   TcVec vec[2];
   TcWork work;
   uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbz, mbu, mbd;
@@ -63,17 +64,21 @@ constexpr uint32_t T_K = 384;  // K over Q times K^T
 template <bool AGG, bool L2>
 __global__ void __launch_bounds__(rev::THREADS, 1)
 m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
-                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap md) {
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap md,
+                       const __grid_constant__ CUtensorMap mv) {
   using namespace rev;
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
-  const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
-  const int seg = AGG ? blockIdx.y + 1 : blockIdx.y;
-  const int c_begin = seg * a.seg_chunks, c_end = min(a.nc, c_begin + a.seg_chunks);
-  const int N = c_end - c_begin;  // chunk n of the walk is c_end - 1 - n
+  // the walk's steps count chunks from the end: of the head, or of a segment
+  // (segments from the last one)
+  const int seg = a.stream ? 0 : a.segs - 1 - (int)blockIdx.y;
+  const int c_seg = seg * a.seg_chunks, n_seg = min(a.nc, c_seg + a.seg_chunks) - c_seg;
+  TcWalk walk(a, 0);
+  if (!a.stream) walk.n = walk.len_a = n_seg;
+  auto chunk = [&](const TcStep& t) { return a.stream ? a.nc - 1 - t.c : c_seg + n_seg - 1 - t.c; };
   const bool ident = AGG && blockIdx.z == 1;
   const uint32_t st0 = smem_u32(base);
 
@@ -98,8 +103,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     if (elect_one()) {
       int issued = 0;
       auto load = [&](int n) {
-        if (n >= N || !wait.ok) return;
-        const int g = issued++ & 1, c = c_end - 1 - n;
+        if (n >= walk.n || !wait.ok) return;
+        const int g = issued++ & 1;
+        const TcStep t = walk.at(n);
+        const int c = chunk(t), b = t.bh / a.Hv, h = t.bh % a.Hv, hk = h / a.share;
         const uint32_t st = st0 + g * STAGE;
         mbar_expect_tx(&s.kv_full[g], STAGE);
 #pragma unroll
@@ -109,9 +116,17 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           tma_tile(st + 4 * TILE + blk * TILE, &md, blk * 64, h, c * TC, b, &s.kv_full[g]);
         }
       };
+      auto store = [&](int n) {  // a step's dV, which the chain warps left in s.v
+        if (AGG || !wait.ok) return;
+        const TcStep t = walk.at(n);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+          if (blk * 64 < a.DV) tma_tile_store(&mv, smem_u32(s.v) + blk * TILE, blk * 64, t.bh % a.Hv, chunk(t) * TC, t.bh / a.Hv);
+        bulk_commit();
+      };
       load(0);
       load(1);
-      for (int n = 0; n < N; ++n) {
+      for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
         const uint32_t st = st0 + i * STAGE, par = n & 1;
         const uint32_t th = smem_u32(s.tp[i].t_hi), tl = smem_u32(s.tp[i].t_lo);
@@ -128,7 +143,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_idesc(128, 64, false, false), p + ks > 0);
           tc_commit(&s.mbx);
         }
-        if (n > 0) load(n + 1);
+        if (n > 0) {
+          store(n - 1);
+          load(n + 1);
+        }
         wait(&s.tp_full[i], (n >> 1) & 1);
         if (wait.ok) {  // dO^T P: dO [64 tokens][head_v] as an M-major A, P [i][j] as an N-major B
 #pragma unroll
@@ -148,6 +166,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
             for (int ks = 0; ks < 4; ++ks)
               tc_mma_ts(tm + T_X, tm + T_R + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? tl : th) + ks * 2048, 16, 1024),
                         tc_idesc(128, 64, false, true), p + ks > 0);
+          if (!AGG) bulk_wait_read();  // whoever sees this commit may write s.v again
           tc_commit(&s.mbu);
         }
         wait(&s.rdy_u, par);
@@ -163,6 +182,11 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           tc_commit(&s.tp_empty[i]);
         }
       }
+      if (!AGG) {
+        wait(&s.rdy_s, walk.n & 1);
+        store(walk.n - 1);
+        bulk_wait_all();
+      }
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
       if (!wait.ok)
@@ -172,16 +196,21 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     __syncwarp();
   } else if (warp >= CHAIN / 32) {
     const int pt = tid - CHAIN;
-    const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.g) + (int64_t)b * a.T * a.Hv + h;
-    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + (int64_t)b * a.T * a.Hv + h;
-    auto gate = [&](const __nv_bfloat16* p, int n) {
-      const int t = (c_end - 1 - n) * TC + pt;
-      return n < N && pt < TC && t < a.T ? __bfloat162float(p[(int64_t)t * a.Hv]) : 0.0f;
+    auto gates = [&](int n, float& g, float& beta) {
+      g = beta = 0.0f;
+      if (n >= walk.n || pt >= TC) return;
+      const TcStep st = walk.at(n);
+      const int t = chunk(st) * TC + pt;
+      if (t >= a.T) return;
+      const int64_t at = ((int64_t)(st.bh / a.Hv) * a.T + t) * a.Hv + st.bh % a.Hv;
+      g = __bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[at]);
+      beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[at]);
     };
-    float g = gate(gp, 0), beta = gate(bp, 0);
-    for (int n = 0; n < N; ++n) {
+    float g, beta, gn, bn;
+    gates(0, g, beta);
+    for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
-      const float gn = gate(gp, n + 1), bn = gate(bp, n + 1);
+      gates(n + 1, gn, bn);
       wait(&s.kv_full[i], (n >> 1) & 1);
       tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
                      &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
@@ -193,22 +222,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const bool live = row < a.DV;
-    float S[32];  // dS^T[row][32 qt + k]
-    if (AGG) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) S[k] = ident && qt * 32 + k == row ? 1.0f : 0.0f;
-    } else {
-      const bool last = seg == a.segs - 1;
-      const float* src = last ? a.ds_out ? a.ds_out + (size_t)bh * a.DK * a.DV : nullptr
-                              : a.seg_start + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
-      const int ld = last ? a.DV : DMAX;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int kk = qt * 32 + k;
-        S[k] = src && (!last || (live && kk < a.DK)) ? src[(size_t)kk * ld + row] : 0.0f;
-      }
-    }
-    __nv_bfloat16* const vb = static_cast<__nv_bfloat16*>(a.dv) + (int64_t)b * a.T * a.dvs + (int64_t)h * a.DV + row;
+    // this row's element of token 16 qt + j in a [64 tokens][head_v] tile pair
+    const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
+    auto at = [&](int j) { return el + j * 128 + ((eu ^ (j & 7)) << 4); };
+    float2 S[16];  // dS^T[row][32 qt + k]
 
     auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
       tmem_wait_st();
@@ -216,32 +233,76 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto put_state = [&](int n) {  // dS as hi, lo into tensor memory, and kept for chunk n's gradients
-      unsigned char* ck = nullptr;
-      if (!AGG && n < N) ck = a.bwd + ((size_t)bh * a.nc + c_end - 1 - n) * TC_BWD + (qt >> 1) * 16384;
+    auto get_state = [&](const TcStep& t) {  // the adjoint a run starts from
+      if (AGG) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          S[k] = make_float2(ident && qt * 32 + 2 * k == row ? 1.0f : 0.0f, ident && qt * 32 + 2 * k + 1 == row ? 1.0f : 0.0f);
+        return;
+      }
+      if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
+      const bool own = chunk(t) < a.nc - 1;
+      const float* src = own ? a.seg_start + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX
+                             : a.ds_out ? a.ds_out + (size_t)t.bh * a.DK * a.DV : nullptr;
+      const int ld = own ? DMAX : a.DV;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
+        const float v = src && (own || (live && kk < a.DK)) ? __ldcg(src + (size_t)kk * ld + row) : 0.0f;
+        (k & 1 ? S[k >> 1].y : S[k >> 1].x) = v;
+      }
+    };
+    auto end_state = [&](const TcStep& t) {  // where a run leaves it
+      float* dst = nullptr;
+      bool own = true;
+      if (AGG) {
+        dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+      } else if (t.give) {
+        dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
+      } else if (a.ds_in && chunk(t) == 0) {
+        dst = a.ds_in + (size_t)t.bh * a.DK * a.DV;
+        own = false;
+      }
+      if (dst) {
+        const int ld = own ? DMAX : a.DV;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int kk = qt * 32 + k;
+          if (own || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
+        }
+      }
+      if (t.give) {
+        __threadfence();
+        bar_sync(1, CHAIN);
+        if (tid == 0) flag_set(a.flags + t.bh);
+      }
+    };
+    auto put_state = [&](const TcStep& t) {  // dS as hi, lo into tensor memory, and kept for the step's gradients
+      unsigned char* ck = AGG ? nullptr : a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + (qt >> 1) * 16384;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split2(S[16 * p + 2 * k], S[16 * p + 2 * k + 1], hi[k], lo[k]);
+        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[k], lo[k]);
         tc_st8(tl + T_S + qt * 32 + p * 16, hi);
         tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
         if (ck) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t at = sw(row, (qt & 1) * 4 + p * 2 + u);
-            *reinterpret_cast<uint4*>(ck + at) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-            *reinterpret_cast<uint4*>(ck + 32768 + at) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+            const uint32_t o = sw(row, (qt & 1) * 4 + p * 2 + u);
+            *reinterpret_cast<uint4*>(ck + o) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + 32768 + o) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
           }
         }
       }
       ready(&s.rdy_s);
     };
-    // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns)
-    auto put_tokens = [&](uint32_t ta, const float (&x)[16], unsigned char* ck) {
+    // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns; or
+    // only into ck)
+    auto put_tokens = [&](uint32_t ta, const float2 (&x)[8], unsigned char* ck) {
       uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      for (int k = 0; k < 8; ++k) split2(x[k], hi[k], lo[k]);
       if (ta != ~0u) {
         tc_st8(tl + ta + qt * 8, hi);
         tc_st8(tl + ta + 32 + qt * 8, lo);
@@ -255,44 +316,42 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
     };
 
-    put_state(0);
-    for (int n = 0; n < N; ++n) {
-      const int c = c_end - 1 - n, i = n & 1;
+    TcStep t = walk.at(0);
+    get_state(t);
+    put_state(t);
+    for (int n = 0; n < walk.n; ++n) {
+      const int i = n & 1;
       const uint32_t st = st0 + i * STAGE;
       const uint32_t par = n & 1;
-      float x[16];
+      float2 x[8];
       wait(&s.kv_full[i], (n >> 1) & 1);
       wait(&s.tp_full[i], (n >> 1) & 1);
       {  // fq dO
-        const uint32_t vt = st + (4 + (row >> 6)) * TILE + (row & 7) * 2;
+        const uint32_t vt = st + 4 * TILE;
+        const Vec16 fq{&s.vec[i].fq[qt * 16]};
+        uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           uint16_t vr;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(qt * 16 + j, (row & 63) >> 3)));
-          x[j] = ident ? 0.0f : __uint_as_float((uint32_t)vr << 16);
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + at(j)));
+          v[j] = vr;
         }
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].fq[qt * 16 + j]);
-          x[j] *= f.x; x[j + 1] *= f.y; x[j + 2] *= f.z; x[j + 3] *= f.w;
-        }
+        for (int j = 0; j < 8; ++j)
+          x[j] = ident ? f2b(0.0f)
+                       : __fmul2_rn(make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16)), fq[j]);
         put_tokens(T_Y, x, nullptr);
       }
       wait(&s.mbx, par);
-      tmem_fence_after_sync();
-      tc_ld16(tl + T_X + qt * 16, x);
-#pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].fu[qt * 16 + j]);
-        x[j] *= f.x; x[j + 1] *= f.y; x[j + 2] *= f.z; x[j + 3] *= f.w;
-      }
       wait(&s.mbz, par);
       tmem_fence_after_sync();
-      if (!ident) {
-        float z[16];
+      tc_ld16(tl + T_X + qt * 16, x);
+      {
+        const Vec16 fu{&s.vec[i].fu[qt * 16]};
+        float2 z[8];
         tc_ld16(tl + T_Z + qt * 16, z);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] += z[j];
+        for (int j = 0; j < 8; ++j) x[j] = __ffma2_rn(x[j], fu[j], ident ? f2b(0.0f) : z[j]);
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
@@ -300,57 +359,43 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        float y[16];
+        const Vec16 bx{&s.vec[i].bfx[qt * 16]};
+        float2 y[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].bfx[qt * 16 + j]);
-          y[j] = -f.x * x[j]; y[j + 1] = -f.y * x[j + 1]; y[j + 2] = -f.z * x[j + 2]; y[j + 3] = -f.w * x[j + 3];
-        }
+        for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(__fmul2_rn(x[j], f2b(-1.0f)), bx[j]);
         put_tokens(T_R, y, nullptr);
       }
-      const float ec = s.vec[i].ec;
-      float be[16];
-      if (!AGG) {
+      const float2 ec = f2b(s.vec[i].ec);
+      if (!AGG) {  // dV
+        const Vec16 be{&s.vec[i].beta[qt * 16]};
+        const uint32_t vb = smem_u32(s.v);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&s.vec[i].beta[qt * 16 + j]);
-          be[j] = f.x; be[j + 1] = f.y; be[j + 2] = f.z; be[j + 3] = f.w;
+        for (int j = 0; j < 8; ++j) {
+          const float2 o = __fmul2_rn(be[j], x[j]);
+          const __nv_bfloat162 v = __floats2bfloat162_rn(o.x, o.y);
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vb + at(2 * j)), "h"(__bfloat16_as_ushort(v.x)) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vb + at(2 * j + 1)), "h"(__bfloat16_as_ushort(v.y)) : "memory");
         }
+        fence_proxy_async();
       }
       ready(&s.rdy_u);
-      if (!AGG) {  // while the update of dS runs
-        put_tokens(~0u, x, a.bwd + ((size_t)bh * a.nc + c) * TC_BWD + 65536);
-        const int t0 = c * TC + qt * 16;
-        if (live) {
-          __nv_bfloat16* vp = vb + (int64_t)t0 * a.dvs;
-#pragma unroll
-          for (int j = 0; j < 16; ++j, vp += a.dvs)
-            if (t0 + j < a.T) *vp = __float2bfloat16_rn(be[j] * x[j]);
-        }
-      }
+      if (!AGG)  // while the update of dS runs
+        put_tokens(~0u, x, a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + 65536);
       wait(&s.mbd, par);
       tmem_fence_after_sync();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         tc_ld16(tl + T_S + qt * 32 + q * 16, x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) S[q * 16 + k] = fmaf(ec, S[q * 16 + k], x[k]);
+        for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(ec, S[q * 8 + k], x[k]);
       }
-      put_state(n + 1);
-    }
-    float* dst = nullptr;
-    int ld = a.DV;
-    if (AGG) {
-      dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
-      ld = DMAX;
-    } else if (a.ds_in && seg == 0) {
-      dst = a.ds_in + (size_t)bh * a.DK * a.DV;
-    }
-    if (dst) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int kk = qt * 32 + k;
-        if (AGG || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = S[k];
+      if (t.last) end_state(t);
+      if (n + 1 < walk.n) {
+        t = walk.at(n + 1);
+        if (t.first) get_state(t);
+        put_state(t);
+      } else {
+        ready(&s.rdy_s);  // the last dV is in place
       }
     }
   }
@@ -362,9 +407,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
 }
 
 cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
-  CUtensorMap mq, mk, md;
+  CUtensorMap mq, mk, md, mv;
   if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
-      !delta_tile_map(&md, a.d_o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
+      !delta_tile_map(&md, a.d_o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV) ||
+      !delta_tile_map(&mv, a.dv, a.DV, a.Hv, a.T, a.B, a.dvs))
     return cudaErrorInvalidValue;
   auto go = [&](auto agg, auto fin) {
     cudaError_t e = cudaSuccess;
@@ -372,12 +418,12 @@ cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
     if (a.segs > 1) {
       e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
       if (e == cudaSuccess)
-        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md);
+        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md, mv);
       if (e == cudaSuccess) e = launch_delta_seg(a, a.ds_out, true, st);
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
-    if (e == cudaSuccess)
-      e = launch_k(fin, dim3(heads, (unsigned)a.segs), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md);
+    if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
+    if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, mq, mk, md, mv);
     return e;
   };
   return a.l2 ? go(m3_delta_tc_rev_kernel<true, true>, m3_delta_tc_rev_kernel<false, true>)

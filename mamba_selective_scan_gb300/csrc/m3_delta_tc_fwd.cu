@@ -28,6 +28,7 @@ constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), V (2 tiles)
 
 struct Smem {  // after two stages
   TcTP tp[2];
+  unsigned char o[2 * TILE];  // a chunk's outputs, for the tile store
   TcVec vec[2];
   TcWork work;
   int bad[128];
@@ -36,6 +37,7 @@ struct Smem {  // after two stages
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
+static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 
 // tensor-memory columns
 constexpr uint32_t T_S = 0;     // S: per 16 columns k, 8 of hi and 8 of lo; also the 128 columns of U'^T K
@@ -48,8 +50,7 @@ constexpr uint32_t T_K = 448;   // K over Q times K^T
 
 }  // namespace
 
-// One block per (batch row, value head, time segment) walks its chunks.  The
-// state is held transposed, S^T [head_v][head_k], one row per tensor-memory
+// A block walks the chunks of TcWalk.  The state is held transposed, S^T [head_v][head_k], one row per tensor-memory
 // lane, so that every product of the chain has the state's rows (M = 128) as
 // its A operand in tensor memory and token tiles as B in shared memory, and
 // every per-token factor is a column factor:
@@ -77,15 +78,15 @@ constexpr uint32_t T_K = 448;   // K over Q times K^T
 template <bool AGG, bool L2>
 __global__ void __launch_bounds__(THREADS, 1)
 m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
-                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ CUtensorMap mo) {
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
-  const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
   const int seg = blockIdx.y;
-  const int c_begin = seg * a.seg_chunks, c_end = min(a.nc, c_begin + a.seg_chunks);
+  const TcWalk walk(a, seg);
   const bool ident = AGG && blockIdx.z == 1;
   const uint32_t st0 = smem_u32(base);
 
@@ -110,17 +111,27 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   if (warp == (CHAIN + TP_THREADS) / 32) {
     if (elect_one()) {
       int issued = 0;
-      auto load = [&](int c) {  // one chunk's copies, once the stage is free
-        if (c >= c_end || !wait.ok) return;
+      auto load = [&](int n) {  // a step's copies, once the stage is free
+        if (n >= walk.n || !wait.ok) return;
         const int g = issued++ & 1;
+        const TcStep t = walk.at(n);
+        const int b = t.bh / a.Hv, h = t.bh % a.Hv, hk = h / a.share;
         const uint32_t st = st0 + g * STAGE;
         mbar_expect_tx(&s.kv_full[g], STAGE);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
-          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-          tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, t.c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, t.c * TC, b, &s.kv_full[g]);
+          tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, t.c * TC, b, &s.kv_full[g]);
         }
+      };
+      auto store = [&](int n) {  // a step's outputs, which the chain warps left in s.o
+        if (!wait.ok) return;
+        const TcStep t = walk.at(n);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+          if (blk * 64 < a.DV) tma_tile_store(&mo, smem_u32(s.o) + blk * TILE, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv);
+        bulk_commit();
       };
       auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
 #pragma unroll
@@ -138,10 +149,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
             tc_mma_ts(tm + d, tm + ta + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? blo : bhi) + ks * 32, 16, 1024),
                       tc_idesc(128, 64, false, false), p + ks > 0);
       };
-      load(c_begin);
-      load(c_begin + 1);
-      for (int c = c_begin; c < c_end; ++c) {
-        const int n = c - c_begin, i = n & 1;
+      load(0);
+      load(1);
+      for (int n = 0; n < walk.n; ++n) {
+        const int i = n & 1;
         const uint32_t st = st0 + i * STAGE, par = n & 1;
         wait(&s.kv_full[i], (n >> 1) & 1);
         wait(&s.rdy_s, par);  // S is in tensor memory
@@ -152,9 +163,12 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
         if (!AGG) {
           wait(&s.rdy_o, par);  // the last chunk's outputs, V and factors are read
-          if (n > 0) mbar_arrive(&s.tp_empty[i ^ 1]);
+          if (n > 0) {
+            mbar_arrive(&s.tp_empty[i ^ 1]);
+            store(n - 1);
+          }
         }
-        if (n > 0) load(c + 1);
+        if (n > 0) load(n + 1);
         if (!AGG && wait.ok) {
           tmem_fence_after_sync();
           mma_state(T_Q, st + TILE);
@@ -182,9 +196,15 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
             tc_commit(&s.tp_empty[i]);
           } else {
             mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
+            bulk_wait_read();  // whoever sees this commit may write s.o again
             tc_commit(&s.mbo);
           }
         }
+      }
+      if (!AGG) {
+        wait(&s.rdy_o, walk.n & 1);
+        store(walk.n - 1);
+        bulk_wait_all();
       }
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
@@ -195,16 +215,21 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     __syncwarp();
   } else if (warp >= CHAIN / 32) {
     const int pt = tid - CHAIN;
-    const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.g) + (int64_t)b * a.T * a.Hv + h;
-    const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.beta) + (int64_t)b * a.T * a.Hv + h;
-    auto gate = [&](const __nv_bfloat16* p, int c) {
-      const int t = c * TC + pt;
-      return pt < TC && t < a.T ? __bfloat162float(p[(int64_t)t * a.Hv]) : 0.0f;
+    auto gates = [&](int n, float& g, float& beta) {
+      g = beta = 0.0f;
+      if (n >= walk.n || pt >= TC) return;
+      const TcStep st = walk.at(n);
+      const int t = st.c * TC + pt;
+      if (t >= a.T) return;
+      const int64_t at = ((int64_t)(st.bh / a.Hv) * a.T + t) * a.Hv + st.bh % a.Hv;
+      g = __bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[at]);
+      beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[at]);
     };
-    float g = gate(gp, c_begin), beta = gate(bp, c_begin);
-    for (int c = c_begin; c < c_end; ++c) {
-      const int n = c - c_begin, i = n & 1;
-      const float gn = c + 1 < c_end ? gate(gp, c + 1) : 0.0f, bn = c + 1 < c_end ? gate(bp, c + 1) : 0.0f;
+    float g, beta, gn, bn;
+    gates(0, g, beta);
+    for (int n = 0; n < walk.n; ++n) {
+      const int i = n & 1;
+      gates(n + 1, gn, bn);
       wait(&s.kv_full[i], (n >> 1) & 1);
       tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
                      &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
@@ -216,25 +241,12 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
     const bool live = row < a.DV;
-    float S[32];  // S^T[row][32 qt + k]
-    if (AGG) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) S[k] = ident && qt * 32 + k == row ? 1.0f : 0.0f;
-    } else {
-      // the segment's start: the carried state, or what the segments before left
-      const float* src = seg == 0 ? a.s_in ? a.s_in + (size_t)bh * a.DK * a.DV : nullptr
-                                  : a.seg_start + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
-      const int ld = seg == 0 ? a.DV : DMAX;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int kk = qt * 32 + k;
-        S[k] = src && (seg > 0 || (live && kk < a.DK)) ? src[(size_t)kk * ld + row] : 0.0f;
-      }
-    }
-    const int64_t ostep = (int64_t)a.Hv * a.DV;
-    __nv_bfloat16* const ob = static_cast<__nv_bfloat16*>(a.o) + ((int64_t)b * a.T * a.Hv + h) * a.DV + row;
-    bool nan_row = false;
+    // this row's element of token 16 qt + j in a [64 tokens][head_v] tile pair
+    const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
+    auto at = [&](int j) { return el + j * 128 + ((eu ^ (j & 7)) << 4); };
+    float2 S[16];  // S^T[row][32 qt + k]
     if (qt == 0) s.bad[row] = TC;
+    bar_sync(1, CHAIN);
 
     auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
       tmem_wait_st();
@@ -242,15 +254,60 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    auto put_state = [&](int c) {  // S as hi, lo into tensor memory (and the chunk's checkpoint)
+    auto get_state = [&](const TcStep& t) {  // the state a run starts from
+      if (AGG) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          S[k] = make_float2(ident && qt * 32 + 2 * k == row ? 1.0f : 0.0f, ident && qt * 32 + 2 * k + 1 == row ? 1.0f : 0.0f);
+        return;
+      }
+      // the carried state, what the segments before left, or a state handed over
+      if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
+      const bool own = t.c > 0;
+      const float* src = own ? a.seg_start + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX
+                             : a.s_in ? a.s_in + (size_t)t.bh * a.DK * a.DV : nullptr;
+      const int ld = own ? DMAX : a.DV;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int kk = qt * 32 + k;
+        const float v = src && (own || (live && kk < a.DK)) ? __ldcg(src + (size_t)kk * ld + row) : 0.0f;
+        (k & 1 ? S[k >> 1].y : S[k >> 1].x) = v;
+      }
+    };
+    auto end_state = [&](const TcStep& t) {  // where a run leaves it
+      float* dst = nullptr;
+      bool own = true;
+      if (AGG) {
+        dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+      } else if (t.give) {
+        dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
+      } else if (a.s_out && t.c == a.nc - 1) {
+        dst = a.s_out + (size_t)t.bh * a.DK * a.DV;
+        own = false;
+      }
+      if (dst) {
+        const int ld = own ? DMAX : a.DV;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int kk = qt * 32 + k;
+          if (own || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
+        }
+      }
+      if (t.give) {
+        __threadfence();
+        bar_sync(1, CHAIN);
+        if (tid == 0) flag_set(a.flags + t.bh);
+      }
+    };
+    auto put_state = [&](const TcStep* t) {  // S as hi, lo into tensor memory (and the step's checkpoint)
       unsigned char* ck = nullptr;
-      if (!AGG && a.ckpt && c < c_end)
-        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + (qt >> 1) * 16384;
+      if (!AGG && a.ckpt && t)
+        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t->bh * a.nc + t->c) * TC_CKPT + (qt >> 1) * 16384;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split2(S[16 * p + 2 * k], S[16 * p + 2 * k + 1], hi[k], lo[k]);
+        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[k], lo[k]);
         tc_st8(tl + T_S + qt * 32 + p * 16, hi);
         tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
         if (ck) {
@@ -263,10 +320,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       ready(&s.rdy_s);
     };
     // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns)
-    auto put_tokens = [&](uint32_t ta, const float (&x)[16], unsigned char* ck) {
+    auto put_tokens = [&](uint32_t ta, const float2 (&x)[8], unsigned char* ck) {
       uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) split2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+      for (int k = 0; k < 8; ++k) split2(x[k], hi[k], lo[k]);
       tc_st8(tl + ta + qt * 8, hi);
       tc_st8(tl + ta + 32 + qt * 8, lo);
       if (ck) {
@@ -277,108 +334,103 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
       }
     };
-    auto outputs = [&](int c) {  // O of chunk c from T_Q and T_O
-      const int n = c - c_begin, i = n & 1;
-      float q[16], o[16];
+    auto outputs = [&](int n) {  // O of step n from T_Q and T_O into s.o
+      float2 q[8], o[8];
       wait(&s.mbq, n & 1);
       wait(&s.mbo, n & 1);
       tmem_fence_after_sync();
       tc_ld16(tl + T_Q + qt * 16, q);
       tc_ld16(tl + T_O + qt * 16, o);
-      tmem_fence_before_sync();
-      const int t0 = c * TC + qt * 16;
       const int bad = s.bad[row] - qt * 16;
+      const Vec16 fq{&s.vec[n & 1].fq[qt * 16]};
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 fq = *reinterpret_cast<const float4*>(&s.vec[i].fq[qt * 16 + j]);
-        o[j] = fmaf(fq.x, q[j], o[j]); o[j + 1] = fmaf(fq.y, q[j + 1], o[j + 1]);
-        o[j + 2] = fmaf(fq.z, q[j + 2], o[j + 2]); o[j + 3] = fmaf(fq.w, q[j + 3], o[j + 3]);
-      }
+      for (int j = 0; j < 8; ++j) o[j] = __ffma2_rn(fq[j], q[j], o[j]);
       if (bad < 16) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j >= bad) o[j] = __int_as_float(0x7FFFFFFF);
-      }
-      if (live) {
-        __nv_bfloat16* op = ob + t0 * ostep;
-        if (t0 + 16 <= a.T) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j, op += ostep) *op = __float2bfloat16_rn(o[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j, op += ostep)
-            if (t0 + j < a.T) *op = __float2bfloat16_rn(o[j]);
+        for (int j = 0; j < 8; ++j) {
+          if (2 * j >= bad) o[j].x = __int_as_float(0x7FFFFFFF);
+          if (2 * j + 1 >= bad) o[j].y = __int_as_float(0x7FFFFFFF);
         }
       }
+      const uint32_t ob = smem_u32(s.o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(o[j].x, o[j].y);
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j)), "h"(__bfloat16_as_ushort(v.x)) : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j + 1)), "h"(__bfloat16_as_ushort(v.y)) : "memory");
+      }
+      fence_proxy_async();
     };
 
-    bar_sync(1, CHAIN);  // s.bad is set
-    put_state(c_begin);
-    for (int c = c_begin; c < c_end; ++c) {
-      const int n = c - c_begin, i = n & 1;
+    TcStep t = walk.at(0);
+    get_state(t);
+    put_state(&t);
+    for (int n = 0; n < walk.n; ++n) {
+      const int i = n & 1;
       const uint32_t st = st0 + i * STAGE;
       const uint32_t par = n & 1;
       if (!AGG) {
-        if (n > 0) outputs(c - 1);
+        if (n > 0) outputs(n - 1);
+        if (t.first && n > 0) {  // another head: its row starts clean
+          __syncwarp();
+          bar_sync(1, CHAIN);
+          if (qt == 0) s.bad[row] = TC;
+          bar_sync(1, CHAIN);
+        }
         ready(&s.rdy_o);
       }
       // R = beta V - bfx X
       wait(&s.tp_full[i], (n >> 1) & 1);
       wait(&s.kv_full[i], (n >> 1) & 1);
-      float x[16];
+      float2 x[8];
       {
-        const uint32_t vt = st + (4 + (row >> 6)) * TILE + (row & 7) * 2;
+        const uint32_t vt = st + 4 * TILE;
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           uint16_t vr;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + sw(qt * 16 + j, (row & 63) >> 3)));
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + at(j)));
           v[j] = vr;
         }
         wait(&s.mbx, par);
         tmem_fence_after_sync();
         tc_ld16(tl + T_X + qt * 16, x);
-        float chk = 0.0f;
+        float2 chk = f2b(0.0f);
+        const Vec16 be{&s.vec[i].beta[qt * 16]}, bx{&s.vec[i].bfx[qt * 16]};
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 be = *reinterpret_cast<const float4*>(&s.vec[i].beta[qt * 16 + j]);
-          const float4 bx = *reinterpret_cast<const float4*>(&s.vec[i].bfx[qt * 16 + j]);
-          const float bv[4] = {be.x, be.y, be.z, be.w}, xv[4] = {bx.x, bx.y, bx.z, bx.w};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            const float vv = ident ? 0.0f : __uint_as_float(v[j + m] << 16);
-            x[j + m] = fmaf(-xv[m], x[j + m], bv[m] * vv);
-            chk = fmaf(x[j + m], 0.0f, chk);  // 0 unless a value is not finite
-          }
+        for (int j = 0; j < 8; ++j) {
+          const float2 vv = ident ? f2b(0.0f) : make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16));
+          const float2 m = __fmul2_rn(x[j], f2b(-1.0f));
+          x[j] = __ffma2_rn(bx[j], m, __fmul2_rn(be[j], vv));
+          chk = __ffma2_rn(x[j], f2b(0.0f), chk);  // 0 unless a value is not finite
         }
         // a value that is not finite must not reach earlier tokens through
         // the zeros of T: it is taken out, and every output from its token
         // on becomes NaN
-        if (!(chk == 0.0f)) {
+        if (!(chk.x + chk.y == 0.0f)) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (!(fabsf(x[j]) <= FINITE_MAX)) {
-              x[j] = 0.0f;
+          for (int j = 0; j < 16; ++j) {
+            float& e = j & 1 ? x[j >> 1].y : x[j >> 1].x;
+            if (!(fabsf(e) <= FINITE_MAX)) {
+              e = 0.0f;
               atomicMin(&s.bad[row], qt * 16 + j);
             }
+          }
         }
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
       wait(&s.mbu, par);
-      nan_row = s.bad[row] < TC;
+      const bool nan_row = s.bad[row] < TC;
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       if (!AGG)
-        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)bh * a.nc + c) * TC_CKPT + 32768
-                                  : nullptr);
+        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
+      const Vec16 fu{&s.vec[i].fu[qt * 16]};
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 fu = *reinterpret_cast<const float4*>(&s.vec[i].fu[qt * 16 + j]);
-        x[j] *= fu.x; x[j + 1] *= fu.y; x[j + 2] *= fu.z; x[j + 3] *= fu.w;
-      }
+      for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], fu[j]);
       put_tokens(T_R, x, nullptr);
-      const float ec = s.vec[i].ec;
+      const float2 ec = f2b(s.vec[i].ec);
       ready(&s.rdy_u);
       wait(&s.mbd, par);
       tmem_fence_after_sync();
@@ -386,30 +438,22 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       for (int q = 0; q < 2; ++q) {
         tc_ld16(tl + T_S + qt * 32 + q * 16, x);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) S[q * 16 + k] = fmaf(ec, S[q * 16 + k], x[k]);
+        for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(ec, S[q * 8 + k], x[k]);
       }
       if (nan_row) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) S[k] = __int_as_float(0x7FFFFFFF);
+        for (int k = 0; k < 16; ++k) S[k] = f2b(__int_as_float(0x7FFFFFFF));
       }
-      put_state(c + 1);
-    }
-    if (!AGG) outputs(c_end - 1);
-    // the state's way out
-    float* dst = nullptr;
-    int ld = a.DV;
-    if (AGG) {
-      dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
-      ld = DMAX;
-    } else if (a.s_out && c_end == a.nc) {
-      dst = a.s_out + (size_t)bh * a.DK * a.DV;
-    }
-    if (dst) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const int kk = qt * 32 + k;
-        if (AGG || (live && kk < a.DK)) dst[(size_t)kk * ld + row] = S[k];
+      if (t.last) end_state(t);
+      if (n + 1 < walk.n) {
+        t = walk.at(n + 1);
+        if (t.first) get_state(t);
+        put_state(&t);
       }
+    }
+    if (!AGG) {
+      outputs(walk.n - 1);
+      ready(&s.rdy_o);
     }
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
@@ -493,9 +537,10 @@ cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, c
 }
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!delta_tile_map(&mq, a.q, a.DK, a.Hk, a.T, a.B, a.qs) || !delta_tile_map(&mk, a.k, a.DK, a.Hk, a.T, a.B, a.ks) ||
-      !delta_tile_map(&mv, a.v, a.DV, a.Hv, a.T, a.B, a.vs))
+      !delta_tile_map(&mv, a.v, a.DV, a.Hv, a.T, a.B, a.vs) ||
+      !delta_tile_map(&mo, a.o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
     return cudaErrorInvalidValue;
   auto go = [&](auto agg, auto fin) {
     cudaError_t e = cudaSuccess;
@@ -503,12 +548,13 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
     if (a.segs > 1) {
       e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
       if (e == cudaSuccess)
-        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv);
+        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv, mo);
       if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
     if (e == cudaSuccess)
-      e = launch_k(fin, dim3(heads, (unsigned)a.segs), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv);
+      e = launch_delta_blocks(fin, a, THREADS, SMEM_BYTES, st, mq, mk, mv, mo);
     return e;
   };
   return a.l2 ? go(m3_delta_tc_fwd_kernel<true, true>, m3_delta_tc_fwd_kernel<false, true>)

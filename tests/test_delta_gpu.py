@@ -79,6 +79,26 @@ def test_forward_and_gradients(case, l2norm):
     _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta"] + (["d_state"] if state else []))
 
 
+@pytest.mark.parametrize("B,T,Hk,Hv,state", [(8, 200, 10, 20, True), (40, 64, 4, 4, False), (31, 129, 5, 10, True), (51, 1, 3, 3, True)])
+def test_more_heads_than_sms(B, T, Hk, Hv, state):
+    """Heads in equal shares: some are begun by one block and ended by the
+    next, which takes the state (or its adjoint) over."""
+    x = delta_inputs(B, T, Hk, Hv, 64, 72, torch.bfloat16, seed=B, device="cuda", state=state)
+    got = _run(x, True)
+    ref = delta_ref_grads(x, 64 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta"] + (["d_state"] if state else []))
+
+
+@pytest.mark.parametrize("B,T,H", [(1, 1100, 1), (2, 2000, 2)])
+def test_few_heads_in_segments(B, T, H):
+    """Few heads over a long sequence: time segments, whose start states come
+    from the segments' transitions."""
+    x = delta_inputs(B, T, H, H, 128, 128, torch.bfloat16, seed=T, device="cuda")
+    got = _run(x, True)
+    ref = delta_ref_grads(x, 128 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_extreme_gates(dt):
     """-inf and very negative log decays forget the state; beta 0 writes
