@@ -151,6 +151,15 @@ struct TcWait {
   }
 };
 
+// K over Q times K^T into 64 columns (one thread)
+__device__ __forceinline__ void tc_mma_kq(uint32_t kq, uint32_t acc, uint64_t* mbk) {
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    const uint64_t d = tc_desc(kq + (ks >> 2) * (2 * TILE) + (ks & 3) * 32, 16, 1024);
+    tc_mma_ss(acc, d, d, tc_idesc(128, 64, false, false), ks > 0);
+  }
+  tc_commit(mbk);
+}
 __device__ __forceinline__ float exp_neg(float d) { return ex2(d * LOG2E); }
 // D (16 x 8) += A (16 x K) B (K x 8) by one warp, f32 in shared memory, each
 // operand as two bf16 terms (three products; these blocks are far too small
@@ -279,26 +288,16 @@ __device__ __forceinline__ bool flag_wait(const unsigned* f) {
 // warp products of two bf16 terms.  T and P are stored as two bf16 terms, 17
 // bits of mantissa, so that what they multiply keeps f32-grade sums.
 //   kq: the stage's K/Q tiles;  acc: 64 tensor-memory columns (all lanes)
+//   mbk: tc_mma_kq's commit (parity kpar)
 //   g, beta: this thread's token's (threads 0-63; 0 past the sequence)
 //   empty: completes (parity epar) when tp and vec may be overwritten
 template <bool L2>
 __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, TcVec& vec, TcWork& w, float g,
                                            float beta, float scale, int pt, uint64_t* mbk, uint32_t kpar,
-                                           uint64_t* empty, uint32_t epar, bool wait_empty, TcWait& wait) {
+                                           uint64_t* k_free, uint64_t* empty, uint32_t epar, bool wait_empty, TcWait& wait) {
   constexpr int BAR = 2;
   const int lane = pt & 31, wp = __shfl_sync(~0u, pt >> 5, 0);
   const int row = (wp & 3) * 32 + lane, ch = wp >> 2;  // row of K over Q, half of its columns
-  if (wp == 0 && elect_one() && wait.ok) {
-    tmem_fence_after_sync();
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t at = kq + (ks >> 2) * (2 * TILE) + (ks & 3) * 32;
-      const uint64_t d = tc_desc(at, 16, 1024);
-      tc_mma_ss(acc, d, d, tc_idesc(128, 64, false, false), ks > 0);
-    }
-    tc_commit(mbk);
-  }
-  __syncwarp();
   if (L2) {  // sums of squares, half a row per thread
     float2 s0 = f2b(0.0f), s1 = f2b(0.0f);
 #pragma unroll
@@ -394,8 +393,9 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
       }
     }
   }
-  tmem_fence_before_sync();  // the accumulator is read: the next chunk's MMA may overwrite it
+  tmem_fence_before_sync();
   bar_sync(BAR, TP_THREADS);
+  if (pt == 0) mbar_arrive(k_free);  // the accumulator is read: the next chunk's MMA may overwrite it
   if (pt < TC) {  // 8 x 8 diagonal blocks, a column per thread
     const int d = pt & ~7, c = pt & 7;
     float x[8];

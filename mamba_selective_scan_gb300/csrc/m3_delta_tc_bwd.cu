@@ -27,19 +27,20 @@ cudaError_t take_delta_bwd_status(unsigned* out) {
 namespace rev {
 
 constexpr int CHAIN = 512;
-constexpr int THREADS = CHAIN + TP_THREADS + 32;
-constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), dO (2 tiles)
+constexpr int THREADS = CHAIN + TP_THREADS + 64;
+constexpr int KQ = 4 * TILE;            // one chunk's K/Q tiles; three stages
+constexpr int VO = 3 * KQ;              // dO, two stages of two tiles; a chunk's dV takes its dO's place
+constexpr int SMALL = VO + 4 * TILE;
 
-struct Smem {  // after two stages
+struct Smem {  // at SMALL
   TcTP tp[2];
-  unsigned char v[2 * TILE];  // a chunk's dV, for the tile store
   TcVec vec[2];
   TcWork work;
-  uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbz, mbu, mbd;
+  uint64_t kq_full[3], kq_empty[3], v_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbz, mbu, mbd, k_free;
   uint64_t rdy_s, rdy_r, rdy_u;  // one arrival per chain warp
   uint32_t tmem;
 };
-constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
+constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
 
 // tensor-memory columns
 constexpr uint32_t T_S = 0;    // dS: per 16 columns k, 8 of hi and 8 of lo; also the 128 columns of its update
@@ -69,7 +70,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   using namespace rev;
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
+  Smem& s = *reinterpret_cast<Smem*>(base + SMALL);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
   // the walk's steps count chunks from the end: of the head, or of a segment
@@ -83,12 +84,16 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&s.kq_full[i], 1);
+      mbar_init(&s.kq_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.v_full[i], 1);
       mbar_init(&s.tp_full[i], 1);
       mbar_init(&s.tp_empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbz, &s.mbu, &s.mbd}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbz, &s.mbu, &s.mbd, &s.k_free}) mbar_init(r, 1);
     for (uint64_t* r : {&s.rdy_s, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
@@ -99,39 +104,80 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   TcWait wait;
 
-  if (warp == (CHAIN + TP_THREADS) / 32) {
+  if (warp == (CHAIN + TP_THREADS) / 32 + 1) {
     if (elect_one()) {
-      int issued = 0;
-      auto load = [&](int n) {
+      int n_kq = 0, n_v = 0;  // loads issued
+      auto load_kq = [&](int n) {  // a step's copies, once the stage is free
         if (n >= walk.n || !wait.ok) return;
-        const int g = issued++ & 1;
+        ++n_kq;
         const TcStep t = walk.at(n);
-        const int c = chunk(t), b = t.bh / a.Hv, h = t.bh % a.Hv, hk = h / a.share;
-        const uint32_t st = st0 + g * STAGE;
-        mbar_expect_tx(&s.kv_full[g], STAGE);
+        const int c = chunk(t), b = t.bh / a.Hv, hk = t.bh % a.Hv / a.share;
+        const uint32_t st = st0 + n % 3 * KQ;
+        uint64_t* bar = &s.kq_full[n % 3];
+        mbar_expect_tx(bar, KQ);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
-          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kv_full[g]);
-          tma_tile(st + 4 * TILE + blk * TILE, &md, blk * 64, h, c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, bar);
+          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, bar);
         }
       };
-      auto store = [&](int n) {  // a step's dV, which the chain warps left in s.v
+      auto load_v = [&](int n) {
+        if (n >= walk.n || !wait.ok) return;
+        ++n_v;
+        const TcStep t = walk.at(n);
+        mbar_expect_tx(&s.v_full[n & 1], 2 * TILE);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+          tma_tile(st0 + VO + ((n & 1) * 2 + blk) * TILE, &md, blk * 64, t.bh % a.Hv, chunk(t) * TC, t.bh / a.Hv, &s.v_full[n & 1]);
+      };
+      auto store = [&](int n) {  // a step's dV, which the chain warps left in place of its inputs
         if (AGG || !wait.ok) return;
         const TcStep t = walk.at(n);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
-          if (blk * 64 < a.DV) tma_tile_store(&mv, smem_u32(s.v) + blk * TILE, blk * 64, t.bh % a.Hv, chunk(t) * TC, t.bh / a.Hv);
+          if (blk * 64 < a.DV)
+            tma_tile_store(&mv, st0 + VO + ((n & 1) * 2 + blk) * TILE, blk * 64, t.bh % a.Hv, chunk(t) * TC, t.bh / a.Hv);
         bulk_commit();
+        bulk_wait_read();
       };
-      load(0);
-      load(1);
+      auto products = [&](int n) {  // K over Q times K^T, for the warps that make T and P
+        if (n >= walk.n) return;
+        wait(&s.kq_full[n % 3], n / 3 & 1);
+        if (n > 0) wait(&s.k_free, (n - 1) & 1);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          tc_mma_kq(st0 + n % 3 * KQ, tm + T_K, &s.mbk);
+        }
+      };
+      for (int n = 0; n < 3; ++n) load_kq(n);
+      for (int n = 0; n < 2; ++n) load_v(n);
+      products(0);
+      for (int n = 0; n <= walk.n; ++n) {
+        products(n + 1);
+        if (n == 0) continue;
+        wait(&s.kq_empty[(n - 1) % 3], (n - 1) / 3 & 1);  // step n - 1's products are done
+        load_kq(n + 2);
+        wait(&s.rdy_s, n & 1);  // its dV is in place
+        store(n - 1);
+        load_v(n + 1);
+      }
+      if (!AGG) bulk_wait_all();
+      // after a wait ran out, copies still in flight land before the block's
+      // shared memory is given up (bounded)
+      if (!wait.ok) {
+        for (int i = 1; i <= 3 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) % 3], (n_kq - i) / 3 & 1);
+        for (int i = 1; i <= 2 && i <= n_v; ++i) mbar_wait(&s.v_full[(n_v - i) & 1], (n_v - i) >> 1 & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == (CHAIN + TP_THREADS) / 32) {
+    if (elect_one()) {
       for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
-        const uint32_t st = st0 + i * STAGE, par = n & 1;
+        const uint32_t st = st0 + n % 3 * KQ, par = n & 1;
         const uint32_t th = smem_u32(s.tp[i].t_hi), tl = smem_u32(s.tp[i].t_lo);
         const uint32_t ph = smem_u32(s.tp[i].p_hi), pl = smem_u32(s.tp[i].p_lo);
-        wait(&s.kv_full[i], (n >> 1) & 1);
+        wait(&s.kq_full[n % 3], n / 3 & 1);
         wait(&s.rdy_s, par);  // dS is in tensor memory, the last chunk is done with
         tmem_fence_after_sync();
         if (wait.ok) {
@@ -143,17 +189,14 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_idesc(128, 64, false, false), p + ks > 0);
           tc_commit(&s.mbx);
         }
-        if (n > 0) {
-          store(n - 1);
-          load(n + 1);
-        }
         wait(&s.tp_full[i], (n >> 1) & 1);
+        wait(&s.v_full[i], (n >> 1) & 1);
         if (wait.ok) {  // dO^T P: dO [64 tokens][head_v] as an M-major A, P [i][j] as an N-major B
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ss(tm + T_Z, tc_desc(st + 4 * TILE + ks * 2048, TILE, 1024), tc_desc((p ? pl : ph) + ks * 2048, 16, 1024),
+              tc_mma_ss(tm + T_Z, tc_desc(st0 + VO + i * 2 * TILE + ks * 2048, TILE, 1024), tc_desc((p ? pl : ph) + ks * 2048, 16, 1024),
                         tc_idesc(128, 64, true, true), p + ks > 0);
           tc_commit(&s.mbz);
         }
@@ -166,7 +209,6 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
             for (int ks = 0; ks < 4; ++ks)
               tc_mma_ts(tm + T_X, tm + T_R + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? tl : th) + ks * 2048, 16, 1024),
                         tc_idesc(128, 64, false, true), p + ks > 0);
-          if (!AGG) bulk_wait_read();  // whoever sees this commit may write s.v again
           tc_commit(&s.mbu);
         }
         wait(&s.rdy_u, par);
@@ -180,18 +222,9 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_desc(st + (p < 2 ? 0 : TILE) + ks * 2048, 2 * TILE, 1024), tc_idesc(128, 128, false, true), p + ks > 0);
           tc_commit(&s.mbd);
           tc_commit(&s.tp_empty[i]);
+          tc_commit(&s.kq_empty[n % 3]);
         }
       }
-      if (!AGG) {
-        wait(&s.rdy_s, walk.n & 1);
-        store(walk.n - 1);
-        bulk_wait_all();
-      }
-      // after a wait ran out, copies still in flight land before the block's
-      // shared memory is given up (bounded)
-      if (!wait.ok)
-        for (int i = 0; i < 2; ++i)
-          if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
     }
     __syncwarp();
   } else if (warp >= CHAIN / 32) {
@@ -211,9 +244,9 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
       gates(n + 1, gn, bn);
-      wait(&s.kv_full[i], (n >> 1) & 1);
-      tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
-                     &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
+      wait(&s.kq_full[n % 3], n / 3 & 1);
+      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
+                     &s.k_free, &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
       if (pt == 0) mbar_arrive(&s.tp_full[i]);
       g = gn;
       beta = bn;
@@ -321,13 +354,12 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     put_state(t);
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
-      const uint32_t st = st0 + i * STAGE;
+      const uint32_t vt = st0 + VO + i * 2 * TILE;
       const uint32_t par = n & 1;
       float2 x[8];
-      wait(&s.kv_full[i], (n >> 1) & 1);
+      wait(&s.v_full[i], (n >> 1) & 1);
       wait(&s.tp_full[i], (n >> 1) & 1);
       {  // fq dO
-        const uint32_t vt = st + 4 * TILE;
         const Vec16 fq{&s.vec[i].fq[qt * 16]};
         uint32_t v[16];
 #pragma unroll
@@ -366,21 +398,24 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         put_tokens(T_R, y, nullptr);
       }
       const float2 ec = f2b(s.vec[i].ec);
-      if (!AGG) {  // dV
-        const Vec16 be{&s.vec[i].beta[qt * 16]};
-        const uint32_t vb = smem_u32(s.v);
+      float2 be[8];
+      {
+        const Vec16 v{&s.vec[i].beta[qt * 16]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) be[j] = v[j];  // (the factors are free after this arrival)
+      }
+      ready(&s.rdy_u);
+      if (!AGG) {  // dV in place of dO, and dR for the gradients, while the update of dS runs
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 o = __fmul2_rn(be[j], x[j]);
           const __nv_bfloat162 v = __floats2bfloat162_rn(o.x, o.y);
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vb + at(2 * j)), "h"(__bfloat16_as_ushort(v.x)) : "memory");
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vb + at(2 * j + 1)), "h"(__bfloat16_as_ushort(v.y)) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vt + at(2 * j)), "h"(__bfloat16_as_ushort(v.x)) : "memory");
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(vt + at(2 * j + 1)), "h"(__bfloat16_as_ushort(v.y)) : "memory");
         }
         fence_proxy_async();
-      }
-      ready(&s.rdy_u);
-      if (!AGG)  // while the update of dS runs
         put_tokens(~0u, x, a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + 65536);
+      }
       wait(&s.mbd, par);
       tmem_fence_after_sync();
 #pragma unroll

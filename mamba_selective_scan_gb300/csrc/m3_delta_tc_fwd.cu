@@ -23,20 +23,21 @@ cudaError_t take_delta_fwd_status(unsigned* out) {
 namespace {
 
 constexpr int CHAIN = 512;                   // threads on the state: a row's columns in quarters
-constexpr int THREADS = CHAIN + TP_THREADS + 32;  // those on T and P, and the warp that issues
-constexpr int STAGE = 6 * TILE;  // K/Q (4 tiles), V (2 tiles)
+constexpr int THREADS = CHAIN + TP_THREADS + 64;  // those on T and P, a warp for the MMAs, one for the copies
+constexpr int KQ = 4 * TILE;            // one chunk's K/Q tiles; three stages
+constexpr int VO = 3 * KQ;              // V, two stages of two tiles; a chunk's outputs take its V's place
+constexpr int SMALL = VO + 4 * TILE;
 
-struct Smem {  // after two stages
+struct Smem {  // at SMALL
   TcTP tp[2];
-  unsigned char o[2 * TILE];  // a chunk's outputs, for the tile store
   TcVec vec[2];
   TcWork work;
   int bad[128];
-  uint64_t kv_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbq, mbu, mbd, mbo;
-  uint64_t rdy_s, rdy_o, rdy_r, rdy_u;  // one arrival per chain warp
+  uint64_t kq_full[3], kq_empty[3], v_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbq, mbu, mbd, mbo, k_free;
+  uint64_t rdy_s, rdy_o, rdy_r, rdy_u, rdy_v;  // one arrival per chain warp
   uint32_t tmem;
 };
-constexpr size_t SMEM_BYTES = 2 * STAGE + sizeof(Smem) + 1024;
+constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
 
 // tensor-memory columns
@@ -66,8 +67,9 @@ constexpr uint32_t T_K = 448;   // K over Q times K^T
 // registers, a quarter row per thread.
 //
 // Roles: warps 0-15 the chain above (a row's columns in quarters), warps
-// 16-23 T and P of the chunk ahead (tc_make_tp), warp 24 issues the MMAs and
-// the copies (two stages), so that a full MMA queue stops nobody else.  The
+// 16-23 T and P of the chunk ahead (tc_make_tp), warp 24 issues the chain's
+// MMAs, warp 25 the copies and the MMA that T and P start from,
+// so that a full queue stops nobody else.  The
 // columns of U'^T K that a thread reads are those its part of S goes back
 // to, so the chain needs no barrier among its warps.  A chunk is a chain of four dependent products, bound by their
 // latency and the register work between them, not by HBM.
@@ -82,7 +84,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                        const __grid_constant__ CUtensorMap mo) {
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  Smem& s = *reinterpret_cast<Smem*>(base + 2 * STAGE);
+  Smem& s = *reinterpret_cast<Smem*>(base + SMALL);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
   const int seg = blockIdx.y;
@@ -91,14 +93,17 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&s.kq_full[i], 1);
+      mbar_init(&s.kq_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.kv_full[i], 1);
+      mbar_init(&s.v_full[i], 1);
       mbar_init(&s.tp_full[i], 1);
       mbar_init(&s.tp_empty[i], 1);
     }
-    mbar_init(&s.mbk, 1); mbar_init(&s.mbx, 1); mbar_init(&s.mbq, 1);
-    mbar_init(&s.mbu, 1); mbar_init(&s.mbd, 1); mbar_init(&s.mbo, 1);
-    for (uint64_t* r : {&s.rdy_s, &s.rdy_o, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
+    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbq, &s.mbu, &s.mbd, &s.mbo, &s.k_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_o, &s.rdy_r, &s.rdy_u, &s.rdy_v}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -108,31 +113,74 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   TcWait wait;
 
-  if (warp == (CHAIN + TP_THREADS) / 32) {
+  if (warp == (CHAIN + TP_THREADS) / 32 + 1) {
     if (elect_one()) {
-      int issued = 0;
-      auto load = [&](int n) {  // a step's copies, once the stage is free
+      int n_kq = 0, n_v = 0;  // loads issued
+      auto load_kq = [&](int n) {  // a step's copies, once the stage is free
         if (n >= walk.n || !wait.ok) return;
-        const int g = issued++ & 1;
+        ++n_kq;
         const TcStep t = walk.at(n);
-        const int b = t.bh / a.Hv, h = t.bh % a.Hv, hk = h / a.share;
-        const uint32_t st = st0 + g * STAGE;
-        mbar_expect_tx(&s.kv_full[g], STAGE);
+        const int c = t.c, b = t.bh / a.Hv, hk = t.bh % a.Hv / a.share;
+        const uint32_t st = st0 + n % 3 * KQ;
+        uint64_t* bar = &s.kq_full[n % 3];
+        mbar_expect_tx(bar, KQ);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
-          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, t.c * TC, b, &s.kv_full[g]);
-          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, t.c * TC, b, &s.kv_full[g]);
-          tma_tile(st + 4 * TILE + blk * TILE, &mv, blk * 64, h, t.c * TC, b, &s.kv_full[g]);
+          tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, bar);
+          tma_tile(st + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, bar);
         }
       };
-      auto store = [&](int n) {  // a step's outputs, which the chain warps left in s.o
-        if (!wait.ok) return;
+      auto load_v = [&](int n) {
+        if (n >= walk.n || !wait.ok) return;
+        ++n_v;
+        const TcStep t = walk.at(n);
+        mbar_expect_tx(&s.v_full[n & 1], 2 * TILE);
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk)
+          tma_tile(st0 + VO + ((n & 1) * 2 + blk) * TILE, &mv, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv, &s.v_full[n & 1]);
+      };
+      auto store = [&](int n) {  // a step's outputs, which the chain warps left in place of its inputs
+        if (AGG || !wait.ok) return;
         const TcStep t = walk.at(n);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
-          if (blk * 64 < a.DV) tma_tile_store(&mo, smem_u32(s.o) + blk * TILE, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv);
+          if (blk * 64 < a.DV)
+            tma_tile_store(&mo, st0 + VO + ((n & 1) * 2 + blk) * TILE, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv);
         bulk_commit();
+        bulk_wait_read();
       };
+      auto products = [&](int n) {  // K over Q times K^T, for the warps that make T and P
+        if (n >= walk.n) return;
+        wait(&s.kq_full[n % 3], n / 3 & 1);
+        if (n > 0) wait(&s.k_free, (n - 1) & 1);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          tc_mma_kq(st0 + n % 3 * KQ, tm + T_K, &s.mbk);
+        }
+      };
+      for (int n = 0; n < 3; ++n) load_kq(n);
+      for (int n = 0; n < 2; ++n) load_v(n);
+      products(0);
+      for (int n = 0; n <= walk.n; ++n) {
+        products(n + 1);
+        if (n == 0) continue;
+        wait(&s.kq_empty[(n - 1) % 3], (n - 1) / 3 & 1);  // step n - 1's products are done
+        load_kq(n + 2);
+        wait(&s.rdy_o, n & 1);  // its outputs are in place
+        store(n - 1);
+        load_v(n + 1);
+      }
+      if (!AGG) bulk_wait_all();
+      // after a wait ran out, copies still in flight land before the block's
+      // shared memory is given up (bounded)
+      if (!wait.ok) {
+        for (int i = 1; i <= 3 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) % 3], (n_kq - i) / 3 & 1);
+        for (int i = 1; i <= 2 && i <= n_v; ++i) mbar_wait(&s.v_full[(n_v - i) & 1], (n_v - i) >> 1 & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == (CHAIN + TP_THREADS) / 32) {
+    if (elect_one()) {
       auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -149,12 +197,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
             tc_mma_ts(tm + d, tm + ta + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? blo : bhi) + ks * 32, 16, 1024),
                       tc_idesc(128, 64, false, false), p + ks > 0);
       };
-      load(0);
-      load(1);
       for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
-        const uint32_t st = st0 + i * STAGE, par = n & 1;
-        wait(&s.kv_full[i], (n >> 1) & 1);
+        const uint32_t st = st0 + n % 3 * KQ, par = n & 1;
+        wait(&s.kq_full[n % 3], n / 3 & 1);
         wait(&s.rdy_s, par);  // S is in tensor memory
         tmem_fence_after_sync();
         if (wait.ok) {
@@ -162,17 +208,13 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           tc_commit(&s.mbx);
         }
         if (!AGG) {
-          wait(&s.rdy_o, par);  // the last chunk's outputs, V and factors are read
-          if (n > 0) {
-            mbar_arrive(&s.tp_empty[i ^ 1]);
-            store(n - 1);
+          wait(&s.rdy_o, par);  // the last chunk's outputs and factors are read
+          if (n > 0) mbar_arrive(&s.tp_empty[i ^ 1]);
+          if (wait.ok) {
+            tmem_fence_after_sync();
+            mma_state(T_Q, st + TILE);
+            tc_commit(&s.mbq);
           }
-        }
-        if (n > 0) load(n + 1);
-        if (!AGG && wait.ok) {
-          tmem_fence_after_sync();
-          mma_state(T_Q, st + TILE);
-          tc_commit(&s.mbq);
         }
         wait(&s.tp_full[i], (n >> 1) & 1);
         wait(&s.rdy_r, par);
@@ -192,25 +234,18 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
               tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
                         tc_idesc(128, 128, false, true), p + ks > 0);
           tc_commit(&s.mbd);
-          if (AGG) {
-            tc_commit(&s.tp_empty[i]);
-          } else {
+          if (AGG) tc_commit(&s.tp_empty[i]);
+          tc_commit(&s.kq_empty[n % 3]);  // (U P^T reads no stage)
+        }
+        if (!AGG) {
+          wait(&s.rdy_v, par);
+          if (wait.ok) {
+            tmem_fence_after_sync();
             mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
-            bulk_wait_read();  // whoever sees this commit may write s.o again
             tc_commit(&s.mbo);
           }
         }
       }
-      if (!AGG) {
-        wait(&s.rdy_o, walk.n & 1);
-        store(walk.n - 1);
-        bulk_wait_all();
-      }
-      // after a wait ran out, copies still in flight land before the block's
-      // shared memory is given up (bounded)
-      if (!wait.ok)
-        for (int i = 0; i < 2; ++i)
-          if (issued > i) mbar_wait(&s.kv_full[(issued - 1 - i) & 1], ((issued - 1 - i) >> 1) & 1);
     }
     __syncwarp();
   } else if (warp >= CHAIN / 32) {
@@ -230,9 +265,9 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
       gates(n + 1, gn, bn);
-      wait(&s.kv_full[i], (n >> 1) & 1);
-      tc_make_tp<L2>(st0 + i * STAGE, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
-                     &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
+      wait(&s.kq_full[n % 3], n / 3 & 1);
+      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
+                     &s.k_free, &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
       if (pt == 0) mbar_arrive(&s.tp_full[i]);
       g = gn;
       beta = bn;
@@ -334,7 +369,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
       }
     };
-    auto outputs = [&](int n) {  // O of step n from T_Q and T_O into s.o
+    auto outputs = [&](int n) {  // O of step n from T_Q and T_O, in place of its V
       float2 q[8], o[8];
       wait(&s.mbq, n & 1);
       wait(&s.mbo, n & 1);
@@ -352,7 +387,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           if (2 * j + 1 >= bad) o[j].y = __int_as_float(0x7FFFFFFF);
         }
       }
-      const uint32_t ob = smem_u32(s.o);
+      const uint32_t ob = st0 + VO + (n & 1) * 2 * TILE;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(o[j].x, o[j].y);
@@ -367,7 +402,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     put_state(&t);
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
-      const uint32_t st = st0 + i * STAGE;
+      const uint32_t vt = st0 + VO + i * 2 * TILE;
       const uint32_t par = n & 1;
       if (!AGG) {
         if (n > 0) outputs(n - 1);
@@ -377,14 +412,13 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           if (qt == 0) s.bad[row] = TC;
           bar_sync(1, CHAIN);
         }
-        ready(&s.rdy_o);
       }
+      ready(&s.rdy_o);
       // R = beta V - bfx X
       wait(&s.tp_full[i], (n >> 1) & 1);
-      wait(&s.kv_full[i], (n >> 1) & 1);
+      wait(&s.v_full[i], (n >> 1) & 1);
       float2 x[8];
       {
-        const uint32_t vt = st + 4 * TILE;
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -424,14 +458,19 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       const bool nan_row = s.bad[row] < TC;
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
-      if (!AGG)
-        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
-      const Vec16 fu{&s.vec[i].fu[qt * 16]};
+      {
+        const Vec16 fu{&s.vec[i].fu[qt * 16]};
+        float2 y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], fu[j]);
-      put_tokens(T_R, x, nullptr);
+        for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(x[j], fu[j]);
+        put_tokens(T_R, y, nullptr);
+      }
       const float2 ec = f2b(s.vec[i].ec);
       ready(&s.rdy_u);
+      if (!AGG) {  // while the update of S runs
+        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
+        ready(&s.rdy_v);
+      }
       wait(&s.mbd, par);
       tmem_fence_after_sync();
 #pragma unroll
@@ -451,10 +490,8 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         put_state(&t);
       }
     }
-    if (!AGG) {
-      outputs(walk.n - 1);
-      ready(&s.rdy_o);
-    }
+    if (!AGG) outputs(walk.n - 1);
+    ready(&s.rdy_o);
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
   tmem_fence_before_sync();
