@@ -396,48 +396,50 @@ __device__ __forceinline__ void tc_make_tp(uint32_t kq, uint32_t acc, TcTP& tp, 
   tmem_fence_before_sync();
   bar_sync(BAR, TP_THREADS);
   if (pt == 0) mbar_arrive(k_free);  // the accumulator is read: the next chunk's MMA may overwrite it
-  if (pt < TC) {  // 8 x 8 diagonal blocks, a column per thread
-    const int d = pt & ~7, c = pt & 7;
-    float x[8];
+  if (wp < 4) {  // a 16 x 16 diagonal block per warp
+    const int d = wp * 16;
+    if (lane < 16) {  // its two 8 x 8 blocks, a column per thread
+      const int e = d + (lane & 8), c = lane & 7;
+      float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s0 = i == c ? 1.0f : 0.0f, s1 = 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        float s0 = i == c ? 1.0f : 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int l = 0; l < i; ++l) (l & 1 ? s1 : s0) = fmaf(-w.A[d + i][d + l], x[l], l & 1 ? s1 : s0);
-      x[i] = s0 + s1;
+        for (int l = 0; l < i; ++l) (l & 1 ? s1 : s0) = fmaf(-w.A[e + i][e + l], x[l], l & 1 ? s1 : s0);
+        x[i] = s0 + s1;
+      }
+      __syncwarp(0xFFFF);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w.A[e + i][e + c] = x[i];
     }
     __syncwarp();
+    {  // 8 -> 16: two columns of a row per thread
+      const int r = lane >> 2, c = (lane & 3) * 2;
+      float2 m = f2b(0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w.A[d + i][d + c] = x[i];
-  }
-  bar_sync(BAR, TP_THREADS);
-  {  // 8 -> 16: four blocks of 64 threads, an element each
-    const int d = (pt >> 6) * 16, r = (pt >> 3) & 7, c = pt & 7;
-    float m = 0.0f;
+      for (int l = 0; l < 8; ++l)
+        m = __ffma2_rn(f2b(w.A[d + 8 + r][d + l]), *reinterpret_cast<const float2*>(&w.A[d + l][d + c]), m);
+      float* M = &w.M[wp * 8][0];
+      *reinterpret_cast<float2*>(M + r * 36 + c) = m;
+      __syncwarp();
+      m = f2b(0.0f);
 #pragma unroll
-    for (int l = 0; l < 8; ++l) m = fmaf(w.A[d + 8 + r][d + l], w.A[d + l][d + c], m);
-    float* M = &w.M[(pt >> 6) * 8][0];
-    M[r * 36 + c] = m;
-    bar_sync(BAR, TP_THREADS);
-    m = 0.0f;
-#pragma unroll
-    for (int l = 0; l < 8; ++l) m = fmaf(-w.A[d + 8 + r][d + 8 + l], M[l * 36 + c], m);
-    w.A[d + 8 + r][d + c] = m;
-  }
-  bar_sync(BAR, TP_THREADS);
-  // 16 -> 32: four tiles of 16 x 8, a warp each
-  {
-    const int d = (wp >> 1 & 1) * 32, c = (wp & 1) * 8;
-    float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (wp < 4) {
-      warp_mma_split<16>(m, &w.A[d + 16][d], TC + 4, &w.A[d][d + c], TC + 4, lane);
-      warp_mma_store(m, &w.M[d >> 1][c], 36, lane, 1.0f);
+      for (int l = 0; l < 8; ++l)
+        m = __ffma2_rn(f2b(-w.A[d + 8 + r][d + 8 + l]), *reinterpret_cast<const float2*>(M + l * 36 + c), m);
+      *reinterpret_cast<float2*>(&w.A[d + 8 + r][d + c]) = m;
     }
-    bar_sync(BAR, TP_THREADS);
-    if (wp < 4) {
+    // 16 -> 32: a pair of warps, a 16 x 8 tile each
+    bar_sync(4 + (wp >> 1), 64);
+    {
+      const int e = (wp >> 1) * 32, c = (wp & 1) * 8;
+      float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      warp_mma_split<16>(m, &w.A[e + 16][e], TC + 4, &w.A[e][e + c], TC + 4, lane);
+      float* M = &w.M[e >> 1][c];  // (a tile's columns are its own warp's)
+      warp_mma_store(m, M, 36, lane, 1.0f);
+      bar_sync(4 + (wp >> 1), 64);  // both warps have read C
       m[0] = m[1] = m[2] = m[3] = 0.0f;
-      warp_mma_split<16>(m, &w.A[d + 16][d + 16], TC + 4, &w.M[d >> 1][c], 36, lane);
-      warp_mma_store(m, &w.A[d + 16][d + c], TC + 4, lane, -1.0f);
+      warp_mma_split<16>(m, &w.A[e + 16][e + 16], TC + 4, M, 36, lane);
+      warp_mma_store(m, &w.A[e + 16][e + c], TC + 4, lane, -1.0f);
     }
   }
   bar_sync(BAR, TP_THREADS);

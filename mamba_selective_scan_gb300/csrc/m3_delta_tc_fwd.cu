@@ -250,23 +250,25 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     __syncwarp();
   } else if (warp >= CHAIN / 32) {
     const int pt = tid - CHAIN;
-    auto gates = [&](int n, float& g, float& beta) {
-      g = beta = 0.0f;
+    // the bf16 bits of this thread's token's gates (widened when they are
+    // needed, a step later, so that nothing waits for the loads)
+    auto gates = [&](int n, uint32_t& g, uint32_t& beta) {
+      g = beta = 0;
       if (n >= walk.n || pt >= TC) return;
       const TcStep st = walk.at(n);
       const int t = st.c * TC + pt;
       if (t >= a.T) return;
       const int64_t at = ((int64_t)(st.bh / a.Hv) * a.T + t) * a.Hv + st.bh % a.Hv;
-      g = __bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[at]);
-      beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[at]);
+      g = static_cast<const unsigned short*>(a.g)[at];
+      beta = static_cast<const unsigned short*>(a.beta)[at];
     };
-    float g, beta, gn, bn;
+    uint32_t g, beta, gn, bn;
     gates(0, g, beta);
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
       gates(n + 1, gn, bn);
       wait(&s.kq_full[n % 3], n / 3 & 1);
-      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, g, beta, a.scale, pt, &s.mbk, n & 1,
+      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, __uint_as_float(g << 16), __uint_as_float(beta << 16), a.scale, pt, &s.mbk, n & 1,
                      &s.k_free, &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
       if (pt == 0) mbar_arrive(&s.tp_full[i]);
       g = gn;
@@ -454,6 +456,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
+      const TcStep tn = walk.at(n + 1);  // (past the last step: not used)
       wait(&s.mbu, par);
       const bool nan_row = s.bad[row] < TC;
       tmem_fence_after_sync();
@@ -485,7 +488,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       if (t.last) end_state(t);
       if (n + 1 < walk.n) {
-        t = walk.at(n + 1);
+        t = tn;
         if (t.first) get_state(t);
         put_state(&t);
       }
