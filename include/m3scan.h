@@ -490,7 +490,9 @@ typedef struct {
 
 typedef struct {
     int64_t chunk, n_chunks;
-    int64_t ckpt_bytes, workspace_bytes;
+    int64_t ckpt_bytes;
+    int64_t workspace_bytes;     /* enough for both directions */
+    int64_t fwd_workspace_bytes; /* enough for m3scan_delta_fwd */
     int32_t fwd_launches, bwd_launches;
 } m3_delta_plan;
 

@@ -108,6 +108,7 @@ class M3DeltaDims(ctypes.Structure):
 class M3DeltaPlan(ctypes.Structure):
     _fields_ = [("chunk", ctypes.c_int64), ("n_chunks", ctypes.c_int64),
                 ("ckpt_bytes", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
+                ("fwd_workspace_bytes", ctypes.c_int64),
                 ("fwd_launches", ctypes.c_int32), ("bwd_launches", ctypes.c_int32)]
 
 
@@ -823,7 +824,7 @@ def _delta_sizes(code, *fields):
     dims = M3DeltaDims(*fields)
     pl = m3scan_delta_plan(dims, code)
     B, _, _, Hv, dk, dv = fields[:6]
-    return ctypes.byref(dims), (B, Hv, dk, dv), pl.ckpt_bytes // 4, pl.workspace_bytes
+    return ctypes.byref(dims), (B, Hv, dk, dv), pl.ckpt_bytes // 4, (pl.fwd_workspace_bytes, pl.workspace_bytes)
 
 
 def _delta_fields(q, k, v, g, beta):
@@ -863,7 +864,7 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
         _need(ckpt, "ckpt", f32, index, (n_ckpt,))
     elif want_ckpt:
         ckpt = torch.empty(n_ckpt, dtype=f32, device=dev)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev)
     _call("m3scan_delta_fwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                _ptr(state), o.data_ptr(), _ptr(state_out), _ptr(ckpt), ws, nbytes,
                                _stream_of(stream, torch, dev)))
@@ -893,7 +894,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _need(r["d_state"], "d_state", f32, index, sshape)
     _need(d_o, "d_o", dt, index, v.shape)
     _need(ckpt, "ckpt", f32, index, (n_ckpt,))
-    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev)
     _call("m3scan_delta_bwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                ckpt.data_ptr(), d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(),
                                r["dk"].data_ptr(), r["dv"].data_ptr(), r["dg"].data_ptr(), r["dbeta"].data_ptr(),

@@ -15,10 +15,11 @@ cudaError_t take_aux_status(unsigned* out) {
     e = cudaMemcpyToSymbol(g_aux_status, &zero, sizeof(zero));
   }
   // the gated delta rule's units report through this one
-  unsigned f = 0, b = 0;
+  unsigned f = 0, b = 0, q = 0;
   if (e == cudaSuccess) e = take_delta_fwd_status(&f);
   if (e == cudaSuccess) e = take_delta_bwd_status(&b);
-  *out = v | f | b;
+  if (e == cudaSuccess) e = take_delta_prep_status(&q);
+  *out = v | f | b | q;
   return e;
 }
 

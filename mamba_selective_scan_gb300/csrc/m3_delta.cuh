@@ -20,8 +20,11 @@ namespace m3 {
 
 // Per chunk and head, bf16 tiles of 128 rows (head_v) x 64 in the swizzle of
 // shared-memory operands, so that one bulk copy brings them in ready to use:
-constexpr size_t TC_CKPT = 65536;  // the forward's: S^T (head_k in two tiles), U^T hi, U^T lo
+constexpr size_t TC_PREP = 33920;  // T, P and the per-token factors (TcPrep)
+constexpr size_t TC_CKPT = 65536 + TC_PREP;  // the forward's: S^T (head_k in two tiles), U^T hi, U^T lo, TcPrep
 constexpr size_t TC_BWD = 98304;   // the reverse pass's: dS^T hi, lo (two tiles each), dR^T hi, dR^T lo
+constexpr int TC = 64;             // tokens per chunk of the tensor-core kernels
+constexpr int TC_BLOCKS = 152;     // persistent blocks of the gradients' kernel, at most (the SMs of a GB300)
 constexpr int DMAX = 128;          // head_k and head_v, at most
 constexpr float DELTA_L2_EPS = 1e-6f;  // added to the sum of squares of q and of k
 constexpr float G_MIN = -110.0f;       // exp(-110) is 0 in f32: lower log decays (and -inf) count as this
@@ -31,7 +34,7 @@ struct DeltaArgs {
   const float *s_in, *ckpt_in, *ds_out;  // state in, checkpoints and d(state out) of the backward
   void *o, *dq, *dk, *dv, *dg, *dbeta;
   float *s_out, *ckpt, *ds_in;
-  float *pdq, *pdk;  // shared heads: per-value-head shares of dq, dk [B, T, Hv, dk]
+  float *pdq, *pdk;  // shared heads: f32 per-value-head shares of dq, dk [B, T, Hv, dk]; bf16 (pdq) running sums per block
   int64_t qs, ks, vs, dqs, dks, dvs;  // elements between tokens
   int B, T, Hk, Hv, DK, DV, share;
   int chunk, nc;
@@ -42,13 +45,15 @@ struct DeltaArgs {
   int segs, seg_chunks;  // else: time segments, chunks per segment
   float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
   unsigned char* bwd;  // [B Hv][nc][TC_BWD]
+  unsigned char* tp;   // TcPrep of every chunk, tp_stride bytes apart (in the checkpoints, or the workspace)
+  size_t tp_stride;
   unsigned* status;
 };
 
 struct DeltaPlan {
   int B, T, Hk, Hv, DK, DV, chunk, nc;
-  size_t ckpt_bytes, ws_bytes;
-  size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd, o_flags;  // workspace offsets
+  size_t ckpt_bytes, fwd_ws_bytes, ws_bytes;  // (the forward's part comes first)
+  size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd, o_flags, o_tp;  // workspace offsets
   bool stream;           // more heads than SMs: equal shares instead of segments
   int segs, seg_chunks;  // time segments
   int fwd_launches, bwd_launches;
@@ -64,10 +69,13 @@ __device__ __forceinline__ float clamp_g(float g) { return fmaxf(g, G_MIN); }
 template <typename T> cudaError_t launch_delta_rec(const DeltaArgs& a, cudaStream_t st, int sms);
 // Backward of f32 activations from the checkpoints: m3_delta_bwd.cu
 cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st);
-// Sum of the per-value-head shares of dq and dk
-template <typename T> cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl);
+// and the sum of its per-value-head shares of dq and dk
+cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st);
 
-// Forward of bf16 activations by chunks of 64 on the tensor cores
+// bf16 activations, chunks of 64 on the tensor cores: T, P and factors of
+// every chunk, then the forward
+cudaError_t launch_delta_tc_prep(const DeltaArgs& a, cudaStream_t st);
+cudaError_t take_delta_prep_status(unsigned* out);
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st);
 // Tensor map of a [B, T, H, D] bf16 tensor (`stride` elements between
 // tokens) read in tiles of 64 tokens x 64 columns, 128-byte swizzle

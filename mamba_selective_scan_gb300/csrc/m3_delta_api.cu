@@ -80,6 +80,7 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->chunk = tc ? 64 : 32;
   p->nc = (p->T + p->chunk - 1) / p->chunk;
   const size_t chunks = (size_t)p->B * p->Hv * p->nc;
+  if (chunks > 0x7FFFFFFF) return M3_ERR_DIMS;  // one block each
   p->ckpt_bytes = chunks * (tc ? TC_CKPT : (size_t)p->DK * p->DV * 4);
   size_t off = STATUS_BYTES;
   auto take = [&](size_t bytes) {
@@ -87,10 +88,6 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  const bool shared = p->Hv != p->Hk;
-  const size_t share_bytes = shared ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
-  p->o_pdq = take(share_bytes);
-  p->o_pdk = take(share_bytes);
   p->segs = 1;
   p->seg_chunks = p->nc;
   // more heads than SMs: equal shares of all chunks, a block per SM
@@ -102,11 +99,22 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->o_phi = take(seg_bytes);
   p->o_start = take(p->stream ? (size_t)heads * DMAX * DMAX * 4 : seg_bytes);
   p->o_flags = take(p->stream ? (size_t)heads * 4 : 0);
+  // T, P and factors of a forward without checkpoints; what the backward
+  // keeps takes their place
+  const size_t mark = off;
+  p->o_tp = take(tc ? chunks * TC_PREP : 0);
+  p->fwd_ws_bytes = off;
+  off = mark;
   p->o_bwd = take(tc ? chunks * TC_BWD : 0);
-  p->ws_bytes = off;
+  const bool shared = p->Hv != p->Hk;
+  const size_t share_bytes = (size_t)p->B * p->T * p->Hv * p->DK * 4;
+  p->o_pdq = take(!shared ? 0 : tc ? (size_t)TC_BLOCKS * TC * DMAX * 2 * 4 : share_bytes);
+  p->o_pdk = take(shared && !tc ? share_bytes : 0);
+  p->ws_bytes = off > p->fwd_ws_bytes ? off : p->fwd_ws_bytes;
   const bool empty = p->B == 0 || p->T == 0;
-  p->fwd_launches = empty ? 0 : p->segs > 1 ? 3 : 1;  // (shares: and a memset of their flags)
-  p->bwd_launches = empty ? 0 : p->fwd_launches + (tc ? 1 : 0) + (shared ? 1 : 0);
+  const int walk = p->segs > 1 ? 3 : 1;  // (shares: and a memset of their flags)
+  p->fwd_launches = empty ? 0 : walk + (tc ? 1 : 0);
+  p->bwd_launches = empty ? 0 : walk + (tc ? 1 : shared ? 1 : 0);
   return M3_OK;
 }
 
@@ -140,6 +148,10 @@ void delta_ws(DeltaArgs& a, const DeltaPlan& p, void* workspace) {
   a.seg_phi = reinterpret_cast<float*>(ws + p.o_phi);
   a.seg_start = reinterpret_cast<float*>(ws + p.o_start);
   a.bwd = ws + p.o_bwd;
+  // in the checkpoints, where there are some
+  const void* ck = a.ckpt ? a.ckpt : a.ckpt_in;
+  a.tp = ck ? static_cast<unsigned char*>(const_cast<void*>(ck)) + 65536 : ws + p.o_tp;
+  a.tp_stride = ck ? TC_CKPT : TC_PREP;
 }
 
 // `aligned` for a list; NULL passes (presence is checked apart)
@@ -178,6 +190,7 @@ m3_status m3scan_delta_plan(const m3_delta_dims* dims, m3_dtype act, m3_delta_pl
   out->n_chunks = p.nc;
   out->ckpt_bytes = (int64_t)p.ckpt_bytes;
   out->workspace_bytes = (int64_t)p.ws_bytes;
+  out->fwd_workspace_bytes = (int64_t)p.fwd_ws_bytes;
   out->fwd_launches = p.fwd_launches;
   out->bwd_launches = p.bwd_launches;
   return M3_OK;
@@ -196,7 +209,7 @@ m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   if (p.B == 0 || p.T == 0)
     return pass_state(state, state_out, (size_t)p.B * p.Hv * p.DK * p.DV * 4, s);
   if (!q || !k || !v || !g || !beta || !o) return M3_ERR_NULL;
-  st = check_workspace(workspace, workspace_bytes, p.ws_bytes);
+  st = check_workspace(workspace, workspace_bytes, p.fwd_ws_bytes);
   if (st != M3_OK) return st;
   int sms = 0;
   if (note(sm_count(&sms)) != cudaSuccess) return M3_ERR_CUDA;
@@ -204,7 +217,13 @@ m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* 
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.s_in = state;
   a.o = o; a.s_out = state_out; a.ckpt = ckpt;
   delta_ws(a, p, workspace);
-  const cudaError_t e = act == M3_BF16 ? launch_delta_tc_fwd(a, s) : launch_delta_rec<float>(a, s, sms);
+  cudaError_t e;
+  if (act == M3_BF16) {
+    e = launch_delta_tc_prep(a, s);
+    if (e == cudaSuccess) e = launch_delta_tc_fwd(a, s);
+  } else {
+    e = launch_delta_rec<float>(a, s, sms);
+  }
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
@@ -253,9 +272,8 @@ m3_status m3scan_delta_bwd(const m3_delta_dims* dims, m3_dtype act, const void* 
     if (e == cudaSuccess) e = launch_delta_tc_grad(a, s);
   } else {
     e = launch_delta_bwd(a, s);
+    if (e == cudaSuccess && a.share > 1) e = launch_delta_share(a, s);
   }
-  if (e == cudaSuccess && a.share > 1)
-    e = act == M3_BF16 ? launch_delta_share<__nv_bfloat16>(a, s, true) : launch_delta_share<float>(a, s, true);
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 

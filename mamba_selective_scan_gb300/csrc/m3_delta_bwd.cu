@@ -381,7 +381,6 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_kernel(const __grid_constant
 }
 
 // dq and dk of a key head: the shares of its value heads added in order.
-template <typename T>
 __global__ void __launch_bounds__(256) m3_delta_share_kernel(const __grid_constant__ DeltaArgs a) {
   grid_dep_wait();
   const int per = a.Hk * a.DK / 4;
@@ -395,8 +394,8 @@ __global__ void __launch_bounds__(256) m3_delta_share_kernel(const __grid_consta
     const float4 x = *reinterpret_cast<const float4*>(src + ((size_t)tok * a.Hv + hk * a.share + m) * a.DK + k);
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
-  T* o = static_cast<T*>(blockIdx.y ? a.dk : a.dq) + tok * (blockIdx.y ? a.dks : a.dqs) + c;
-  Act<T>::st(o, s.x); Act<T>::st(o + 1, s.y); Act<T>::st(o + 2, s.z); Act<T>::st(o + 3, s.w);
+  float* o = static_cast<float*>(blockIdx.y ? a.dk : a.dq) + tok * (blockIdx.y ? a.dks : a.dqs) + c;
+  *reinterpret_cast<float4*>(o) = s;
 }
 
 cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st) {
@@ -406,12 +405,9 @@ cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return launch_k(m3_delta_bwd_kernel<float>, dim3((unsigned)(a.B * a.Hv)), 256, sizeof(DeltaBwdSmem), st, false, a);
 }
-template <typename T>
-cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st, bool pdl) {
+cudaError_t launch_delta_share(const DeltaArgs& a, cudaStream_t st) {
   const int64_t n = (int64_t)a.B * a.T * (a.Hk * a.DK / 4);
-  return launch_k(m3_delta_share_kernel<T>, dim3((unsigned)((n + 255) / 256), 2), 256, 0, st, pdl, a);
+  return launch_k(m3_delta_share_kernel, dim3((unsigned)((n + 255) / 256), 2), 256, 0, st, true, a);
 }
-template cudaError_t launch_delta_share<float>(const DeltaArgs&, cudaStream_t, bool);
-template cudaError_t launch_delta_share<__nv_bfloat16>(const DeltaArgs&, cudaStream_t, bool);
 
 }  // namespace m3

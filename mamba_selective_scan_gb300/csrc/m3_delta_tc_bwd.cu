@@ -27,16 +27,15 @@ cudaError_t take_delta_bwd_status(unsigned* out) {
 namespace rev {
 
 constexpr int CHAIN = 512;
-constexpr int THREADS = CHAIN + TP_THREADS + 64;
-constexpr int KQ = 4 * TILE;            // one chunk's K/Q tiles; three stages
-constexpr int VO = 3 * KQ;              // dO, two stages of two tiles; a chunk's dV takes its dO's place
+constexpr int THREADS = CHAIN + 64;
+constexpr int KQ = 4 * TILE;      // one chunk's K/Q tiles; two stages
+constexpr int PREP = 2 * KQ;      // TcPrep, two stages
+constexpr int PREP_STAGE = 34 * 1024;
+constexpr int VO = PREP + 2 * PREP_STAGE;  // dO, two stages of two tiles; a chunk's dV takes its dO's place
 constexpr int SMALL = VO + 4 * TILE;
 
 struct Smem {  // at SMALL
-  TcTP tp[2];
-  TcVec vec[2];
-  TcWork work;
-  uint64_t kq_full[3], kq_empty[3], v_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbz, mbu, mbd, k_free;
+  uint64_t kq_full[2], v_full[2], mbx, mbz, mbu, mbd;
   uint64_t rdy_s, rdy_r, rdy_u;  // one arrival per chain warp
   uint32_t tmem;
 };
@@ -48,7 +47,6 @@ constexpr uint32_t T_X = 128;  // dS^T K^T, then dR
 constexpr uint32_t T_Z = 192;  // dO^T P
 constexpr uint32_t T_R = 256;  // dU as hi, lo (32 + 32), then -bfx dR
 constexpr uint32_t T_Y = 320;  // fq dO as hi, lo
-constexpr uint32_t T_K = 384;  // K over Q times K^T
 
 }  // namespace rev
 
@@ -84,16 +82,11 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&s.kq_full[i], 1);
-      mbar_init(&s.kq_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.kq_full[i], 1);
       mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.tp_full[i], 1);
-      mbar_init(&s.tp_empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbz, &s.mbu, &s.mbd, &s.k_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.mbx, &s.mbz, &s.mbu, &s.mbd}) mbar_init(r, 1);
     for (uint64_t* r : {&s.rdy_s, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
@@ -104,7 +97,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   TcWait wait;
 
-  if (warp == (CHAIN + TP_THREADS) / 32 + 1) {
+  if (warp == CHAIN / 32 + 1) {
     if (elect_one()) {
       int n_kq = 0, n_v = 0;  // loads issued
       auto load_kq = [&](int n) {  // a step's copies, once the stage is free
@@ -112,9 +105,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         ++n_kq;
         const TcStep t = walk.at(n);
         const int c = chunk(t), b = t.bh / a.Hv, hk = t.bh % a.Hv / a.share;
-        const uint32_t st = st0 + n % 3 * KQ;
-        uint64_t* bar = &s.kq_full[n % 3];
-        mbar_expect_tx(bar, KQ);
+        const uint32_t st = st0 + (n & 1) * KQ;
+        uint64_t* bar = &s.kq_full[n & 1];
+        mbar_expect_tx(bar, KQ + (uint32_t)sizeof(TcPrep));
+        bulk_load(st0 + PREP + (n & 1) * PREP_STAGE, a.tp + ((size_t)t.bh * a.nc + c) * a.tp_stride, (uint32_t)sizeof(TcPrep), bar);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, bar);
@@ -140,24 +134,15 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         bulk_commit();
         bulk_wait_read();
       };
-      auto products = [&](int n) {  // K over Q times K^T, for the warps that make T and P
-        if (n >= walk.n) return;
-        wait(&s.kq_full[n % 3], n / 3 & 1);
-        if (n > 0) wait(&s.k_free, (n - 1) & 1);
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          tc_mma_kq(st0 + n % 3 * KQ, tm + T_K, &s.mbk);
-        }
-      };
-      for (int n = 0; n < 3; ++n) load_kq(n);
-      for (int n = 0; n < 2; ++n) load_v(n);
-      products(0);
+      for (int n = 0; n < 2; ++n) {
+        load_kq(n);
+        load_v(n);
+      }
       for (int n = 0; n <= walk.n; ++n) {
-        products(n + 1);
+        // step n - 1 is done with its tiles, its results are in place
+        wait(&s.rdy_s, n & 1);
         if (n == 0) continue;
-        wait(&s.kq_empty[(n - 1) % 3], (n - 1) / 3 & 1);  // step n - 1's products are done
-        load_kq(n + 2);
-        wait(&s.rdy_s, n & 1);  // its dV is in place
+        load_kq(n + 1);
         store(n - 1);
         load_v(n + 1);
       }
@@ -165,19 +150,18 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
       if (!wait.ok) {
-        for (int i = 1; i <= 3 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) % 3], (n_kq - i) / 3 & 1);
+        for (int i = 1; i <= 2 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) & 1], (n_kq - i) >> 1 & 1);
         for (int i = 1; i <= 2 && i <= n_v; ++i) mbar_wait(&s.v_full[(n_v - i) & 1], (n_v - i) >> 1 & 1);
       }
     }
     __syncwarp();
-  } else if (warp == (CHAIN + TP_THREADS) / 32) {
+  } else if (warp == CHAIN / 32) {
     if (elect_one()) {
       for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
-        const uint32_t st = st0 + n % 3 * KQ, par = n & 1;
-        const uint32_t th = smem_u32(s.tp[i].t_hi), tl = smem_u32(s.tp[i].t_lo);
-        const uint32_t ph = smem_u32(s.tp[i].p_hi), pl = smem_u32(s.tp[i].p_lo);
-        wait(&s.kq_full[n % 3], n / 3 & 1);
+        const uint32_t st = st0 + i * KQ, par = n & 1;
+        const uint32_t tp = st0 + PREP + i * PREP_STAGE;  // T hi, T lo, P hi, P lo
+        wait(&s.kq_full[i], (n >> 1) & 1);
         wait(&s.rdy_s, par);  // dS is in tensor memory, the last chunk is done with
         tmem_fence_after_sync();
         if (wait.ok) {
@@ -189,14 +173,13 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_idesc(128, 64, false, false), p + ks > 0);
           tc_commit(&s.mbx);
         }
-        wait(&s.tp_full[i], (n >> 1) & 1);
         wait(&s.v_full[i], (n >> 1) & 1);
         if (wait.ok) {  // dO^T P: dO [64 tokens][head_v] as an M-major A, P [i][j] as an N-major B
 #pragma unroll
           for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ss(tm + T_Z, tc_desc(st0 + VO + i * 2 * TILE + ks * 2048, TILE, 1024), tc_desc((p ? pl : ph) + ks * 2048, 16, 1024),
+              tc_mma_ss(tm + T_Z, tc_desc(st0 + VO + i * 2 * TILE + ks * 2048, TILE, 1024), tc_desc(tp + (2 + p) * TILE + ks * 2048, 16, 1024),
                         tc_idesc(128, 64, true, true), p + ks > 0);
           tc_commit(&s.mbz);
         }
@@ -207,7 +190,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           for (int p = 0; p < 3; ++p)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ts(tm + T_X, tm + T_R + (p == 1 ? 32 : 0) + ks * 8, tc_desc((p == 2 ? tl : th) + ks * 2048, 16, 1024),
+              tc_mma_ts(tm + T_X, tm + T_R + (p == 1 ? 32 : 0) + ks * 8, tc_desc(tp + (p == 2 ? TILE : 0) + ks * 2048, 16, 1024),
                         tc_idesc(128, 64, false, true), p + ks > 0);
           tc_commit(&s.mbu);
         }
@@ -221,38 +204,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
               tc_mma_ts(tm + T_S, tm + (p < 2 ? T_R : T_Y) + (p & 1) * 32 + ks * 8,
                         tc_desc(st + (p < 2 ? 0 : TILE) + ks * 2048, 2 * TILE, 1024), tc_idesc(128, 128, false, true), p + ks > 0);
           tc_commit(&s.mbd);
-          tc_commit(&s.tp_empty[i]);
-          tc_commit(&s.kq_empty[n % 3]);
         }
       }
     }
     __syncwarp();
-  } else if (warp >= CHAIN / 32) {
-    const int pt = tid - CHAIN;
-    // the bf16 bits of this thread's token's gates (widened when they are
-    // needed, a step later, so that nothing waits for the loads)
-    auto gates = [&](int n, uint32_t& g, uint32_t& beta) {
-      g = beta = 0;
-      if (n >= walk.n || pt >= TC) return;
-      const TcStep st = walk.at(n);
-      const int t = chunk(st) * TC + pt;
-      if (t >= a.T) return;
-      const int64_t at = ((int64_t)(st.bh / a.Hv) * a.T + t) * a.Hv + st.bh % a.Hv;
-      g = static_cast<const unsigned short*>(a.g)[at];
-      beta = static_cast<const unsigned short*>(a.beta)[at];
-    };
-    uint32_t g, beta, gn, bn;
-    gates(0, g, beta);
-    for (int n = 0; n < walk.n; ++n) {
-      const int i = n & 1;
-      gates(n + 1, gn, bn);
-      wait(&s.kq_full[n % 3], n / 3 & 1);
-      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, __uint_as_float(g << 16), __uint_as_float(beta << 16), a.scale, pt, &s.mbk, n & 1,
-                     &s.k_free, &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
-      if (pt == 0) mbar_arrive(&s.tp_full[i]);
-      g = gn;
-      beta = bn;
-    }
   } else {
     const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -260,6 +215,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     // this row's element of token 16 qt + j in a [64 tokens][head_v] tile pair
     const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
     auto at = [&](int j) { return el + j * 128 + ((eu ^ (j & 7)) << 4); };
+    auto vec = [&](int n) -> const TcVec& { return reinterpret_cast<const TcPrep*>(base + PREP + (n & 1) * PREP_STAGE)->vec; };
     float2 S[16];  // dS^T[row][32 qt + k]
 
     auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
@@ -359,10 +315,10 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       const uint32_t vt = st0 + VO + i * 2 * TILE;
       const uint32_t par = n & 1;
       float2 x[8];
+      wait(&s.kq_full[i], (n >> 1) & 1);
       wait(&s.v_full[i], (n >> 1) & 1);
-      wait(&s.tp_full[i], (n >> 1) & 1);
       {  // fq dO
-        const Vec16 fq{&s.vec[i].fq[qt * 16]};
+        const Vec16 fq{&vec(n).fq[qt * 16]};
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -381,7 +337,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        const Vec16 fu{&s.vec[i].fu[qt * 16]};
+        const Vec16 fu{&vec(n).fu[qt * 16]};
         float2 z[8];
         tc_ld16(tl + T_Z + qt * 16, z);
 #pragma unroll
@@ -394,16 +350,16 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        const Vec16 bx{&s.vec[i].bfx[qt * 16]};
+        const Vec16 bx{&vec(n).bfx[qt * 16]};
         float2 y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(__fmul2_rn(x[j], f2b(-1.0f)), bx[j]);
         put_tokens(T_R, y, nullptr);
       }
-      const float2 ec = f2b(s.vec[i].ec);
+      const float2 ec = f2b(vec(n).ec);
       float2 be[8];
       {
-        const Vec16 v{&s.vec[i].beta[qt * 16]};
+        const Vec16 v{&vec(n).beta[qt * 16]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) be[j] = v[j];  // (the factors are free after this arrival)
       }
@@ -504,6 +460,33 @@ constexpr uint32_t T_YO = 0, T_Y = 64, T_Z = 128, T_DQ = 192, T_DK = 256, T_G = 
 
 }  // namespace grad
 
+// One head's chunk; a block takes the value heads of a key head's chunk one
+// after the other.
+struct GradItem {
+  int64_t group;
+  int b, hk, m, c, h;
+  size_t at;  // batch row x value head x chunk
+  __device__ __forceinline__ GradItem(const DeltaArgs& a, int64_t g) { set(a, g); }
+  __device__ __forceinline__ void set(const DeltaArgs& a, int64_t g) {
+    group = g;
+    const int bk = (int)(g / a.nc);
+    c = (int)(g % a.nc);
+    b = bk / a.Hk;
+    hk = bk % a.Hk;
+    m = 0;
+    h = hk * a.share;
+    at = ((size_t)b * a.Hv + h) * a.nc + c;
+  }
+  __device__ __forceinline__ void next(const DeltaArgs& a) {
+    if (++m < a.share) {
+      ++h;
+      at += a.nc;
+    } else {
+      set(a, group + gridDim.x);
+    }
+  }
+};
+
 // The 16 values of every lane summed over the warp: lane l returns the sum of
 // value l / 2.
 __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
@@ -535,7 +518,7 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
 // S0 enters with one bf16 term (it only meets gradients that are rounded to
 // bf16), everything else that is not an input with two.
 //
-// 240 KB come in and 32 to 64 KB go out per item: HBM bound, so the next
+// 210 KB come in and 32 KB go out per item: HBM bound, so the next
 // item's tiles are fetched as soon as the first products have read this one's.
 template <bool L2>
 __global__ void __launch_bounds__(grad::THREADS, 1)
@@ -547,7 +530,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   Smem& s = *reinterpret_cast<Smem*>(base + SMALL);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
-  const int64_t items = (int64_t)a.B * a.Hv * a.nc;
+  const int64_t groups = (int64_t)a.B * a.Hk * a.nc;  // (batch row, key head, chunk), `share` items each
   const uint32_t sb = smem_u32(base);
 
   if (tid == 0) {
@@ -565,32 +548,26 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 
   if (warp == EPI / 32) {
     if (elect_one()) {
-      auto bulk = [&](int dst, const void* src, uint32_t bytes, uint64_t* bar) {
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                     ::"r"(sb + dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-      };
       uint32_t n_big = 0, n_s = 0, n_kq = 0;  // loads issued
-      auto load_big = [&](int64_t it) {
+      auto load_big = [&](const GradItem& it) {
         ++n_big;
-        const int bh = (int)(it / a.nc), c = (int)(it % a.nc);
-        const unsigned char* ck = reinterpret_cast<const unsigned char*>(a.ckpt_in) + (size_t)it * TC_CKPT;
+        const unsigned char* ck = reinterpret_cast<const unsigned char*>(a.ckpt_in) + it.at * TC_CKPT;
         mbar_expect_tx(&s.big, BIG_BYTES);
-        bulk(U, ck + 32768, 32768, &s.big);
-        bulk(DS, a.bwd + (size_t)it * TC_BWD, (uint32_t)TC_BWD, &s.big);
-        for (int blk = 0; blk < 2; ++blk) tma_tile(sb + DO + blk * TILE, &md, blk * 64, bh % a.Hv, c * TC, bh / a.Hv, &s.big);
+        bulk_load(sb + U, ck + 32768, 32768, &s.big);
+        bulk_load(sb + DS, a.bwd + it.at * TC_BWD, (uint32_t)TC_BWD, &s.big);
+        for (int blk = 0; blk < 2; ++blk) tma_tile(sb + DO + blk * TILE, &md, blk * 64, it.h, it.c * TC, it.b, &s.big);
       };
-      auto load_s = [&](int64_t it) {
+      auto load_s = [&](const GradItem& it) {
         ++n_s;
         mbar_expect_tx(&s.s, 32768);
-        bulk(S0, reinterpret_cast<const unsigned char*>(a.ckpt_in) + (size_t)it * TC_CKPT, 32768, &s.s);
+        bulk_load(sb + S0, reinterpret_cast<const unsigned char*>(a.ckpt_in) + it.at * TC_CKPT, 32768, &s.s);
       };
-      auto load_kq = [&](int64_t it) {
+      auto load_kq = [&](const GradItem& it) {
         ++n_kq;
-        const int bh = (int)(it / a.nc), c = (int)(it % a.nc), hk = bh % a.Hv / a.share, b = bh / a.Hv;
         mbar_expect_tx(&s.kq, 4 * TILE);
         for (int blk = 0; blk < 2; ++blk) {
-          tma_tile(sb + KQ + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, &s.kq);
-          tma_tile(sb + KQ + blk * 2 * TILE + TILE, &mq, blk * 64, hk, c * TC, b, &s.kq);
+          tma_tile(sb + KQ + blk * 2 * TILE, &mk, blk * 64, it.hk, it.c * TC, it.b, &s.kq);
+          tma_tile(sb + KQ + blk * 2 * TILE + TILE, &mq, blk * 64, it.hk, it.c * TC, it.b, &s.kq);
         }
       };
       // a product of `steps` steps of 16 in K; operand descriptors by step
@@ -602,14 +579,13 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       auto kmaj = [&](int at, int blk) { return [=](int ks) { return tc_desc(sb + at + (ks >> 2) * blk + (ks & 3) * 32, 16, 1024); }; };
       constexpr uint32_t NN = tc_idesc(128, 64, false, false), NM = tc_idesc(128, 64, false, true),
                          MN = tc_idesc(128, 64, true, false), MM = tc_idesc(128, 64, true, true);
-      int64_t it = blockIdx.x;
-      if (it < items) {
-        load_kq(it);
-        load_big(it);
-        load_s(it);
-      }
-      for (uint32_t par = 0; it < items; it += gridDim.x, par ^= 1) {
-        const int64_t next = it + gridDim.x;
+      GradItem it(a, blockIdx.x);
+      load_kq(it);
+      load_big(it);
+      load_s(it);
+      for (uint32_t par = 0; it.group < groups; par ^= 1) {
+        it.next(a);
+        const bool more = it.group < groups;
         wait(&s.kq, par);
         wait(&s.big, par);
         wait(&s.s, par);
@@ -643,11 +619,11 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           tc_commit(&s.mb3);
         }
         wait(&s.mb2, par);
-        if (next < items && wait.ok) load_big(next);
+        if (more && wait.ok) load_big(it);
         wait(&s.mb3, par);
-        if (next < items && wait.ok) load_s(next);
+        if (more && wait.ok) load_s(it);
         wait(&s.rdy2, par);  // K, Q and the accumulators are read
-        if (next < items && wait.ok) load_kq(next);
+        if (more && wait.ok) load_kq(it);
       }
       if (!wait.ok && n_kq) {  // as in the other kernels: copies in flight land first
         mbar_wait(&s.kq, (n_kq - 1) & 1);
@@ -672,8 +648,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       return __uint_as_float((uint32_t)v << 16);
     };
     uint32_t par = 0;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x, par ^= 1) {
-      const int bh = (int)(it / a.nc), c = (int)(it % a.nc), b = bh / a.Hv, h = bh % a.Hv;
+    for (GradItem it(a, blockIdx.x); it.group < groups; it.next(a), par ^= 1) {
+      const int c = it.c, b = it.b, h = it.h;
       const int64_t tok0 = (int64_t)b * a.T + c * TC;  // the chunk's first token
       const int n = min(TC, a.T - c * TC);
       float g = 0.0f, beta = 0.0f;
@@ -858,7 +834,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
             if (!(fabsf(be) > 1e-20f)) {
               // U holds nothing of a token that writes nothing: from
               // dR.(v - e^gam S0^T k) - (below the diagonal of D K K^T) G
-              const unsigned char* dr = a.bwd + (size_t)it * TC_BWD + 65536;
+              const unsigned char* dr = a.bwd + it.at * TC_BWD + 65536;
               const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (tok0 + i) * a.vs + (int64_t)h * a.DV;
               float rv = 0.0f;
               for (int m = 0; m < a.DV; ++m) {
@@ -913,28 +889,38 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         }
       }
       ready(&s.rdy2);
+      // value heads that share a key head: their sum so far, in a place of
+      // this thread's own that stays in L2
+      if (a.share > 1) {
+        float4* acc = reinterpret_cast<float4*>(a.pdq) + (size_t)blockIdx.x * 8 * EPI + tid;
+        if (it.m > 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 x = acc[j * EPI], y = acc[(4 + j) * EPI];
+            dq[4 * j] += x.x; dq[4 * j + 1] += x.y; dq[4 * j + 2] += x.z; dq[4 * j + 3] += x.w;
+            dk[4 * j] += y.x; dk[4 * j + 1] += y.y; dk[4 * j + 2] += y.z; dk[4 * j + 3] += y.w;
+          }
+        }
+        if (it.m + 1 < a.share) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[j * EPI] = make_float4(dq[4 * j], dq[4 * j + 1], dq[4 * j + 2], dq[4 * j + 3]);
+            acc[(4 + j) * EPI] = make_float4(dk[4 * j], dk[4 * j + 1], dk[4 * j + 2], dk[4 * j + 3]);
+          }
+          continue;
+        }
+      }
       if (row < a.DK) {
         const int64_t t0 = tok0 + qt * 16;
         const int left = n - qt * 16;
-        if (a.share == 1) {
-          __nv_bfloat16* qp = static_cast<__nv_bfloat16*>(a.dq) + t0 * a.dqs + (int64_t)h * a.DK + row;
-          __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.dk) + t0 * a.dks + (int64_t)h * a.DK + row;
+        __nv_bfloat16* qp = static_cast<__nv_bfloat16*>(a.dq) + t0 * a.dqs + (int64_t)it.hk * a.DK + row;
+        __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.dk) + t0 * a.dks + (int64_t)it.hk * a.DK + row;
 #pragma unroll
-          for (int j = 0; j < 16; ++j, qp += a.dqs, kp += a.dks)
-            if (j < left) {
-              *qp = __float2bfloat16_rn(dq[j]);
-              *kp = __float2bfloat16_rn(dk[j]);
-            }
-        } else {
-          const int64_t step = (int64_t)a.Hv * a.DK, at = (t0 * a.Hv + h) * a.DK + row;
-          float *qp = a.pdq + at, *kp = a.pdk + at;
-#pragma unroll
-          for (int j = 0; j < 16; ++j, qp += step, kp += step)
-            if (j < left) {
-              *qp = dq[j];
-              *kp = dk[j];
-            }
-        }
+        for (int j = 0; j < 16; ++j, qp += a.dqs, kp += a.dks)
+          if (j < left) {
+            *qp = __float2bfloat16_rn(dq[j]);
+            *kp = __float2bfloat16_rn(dk[j]);
+          }
       }
     }
   }
@@ -955,8 +941,9 @@ cudaError_t launch_delta_tc_grad(const DeltaArgs& a, cudaStream_t st) {
   auto kern = a.l2 ? m3_delta_tc_grad_kernel<true> : m3_delta_tc_grad_kernel<false>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)grad::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.B * a.Hv * a.nc;
-  return launch_k(kern, dim3((unsigned)(items < sms ? items : sms)), grad::THREADS, grad::SMEM_BYTES, st, false, a, mq, mk, md);
+  const int64_t groups = (int64_t)a.B * a.Hk * a.nc;
+  if (sms > TC_BLOCKS) sms = TC_BLOCKS;
+  return launch_k(kern, dim3((unsigned)(groups < sms ? groups : sms)), grad::THREADS, grad::SMEM_BYTES, st, false, a, mq, mk, md);
 }
 
 }  // namespace m3

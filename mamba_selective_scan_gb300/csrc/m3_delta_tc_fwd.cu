@@ -23,17 +23,16 @@ cudaError_t take_delta_fwd_status(unsigned* out) {
 namespace {
 
 constexpr int CHAIN = 512;                   // threads on the state: a row's columns in quarters
-constexpr int THREADS = CHAIN + TP_THREADS + 64;  // those on T and P, a warp for the MMAs, one for the copies
-constexpr int KQ = 4 * TILE;            // one chunk's K/Q tiles; three stages
-constexpr int VO = 3 * KQ;              // V, two stages of two tiles; a chunk's outputs take its V's place
+constexpr int THREADS = CHAIN + 64;  // and a warp for the MMAs, one for the copies
+constexpr int KQ = 4 * TILE;      // one chunk's K/Q tiles; two stages
+constexpr int PREP = 2 * KQ;      // TcPrep, two stages
+constexpr int PREP_STAGE = 34 * 1024;
+constexpr int VO = PREP + 2 * PREP_STAGE;  // V, two stages of two tiles; a chunk's outputs take its V's place
 constexpr int SMALL = VO + 4 * TILE;
 
 struct Smem {  // at SMALL
-  TcTP tp[2];
-  TcVec vec[2];
-  TcWork work;
   int bad[128];
-  uint64_t kq_full[3], kq_empty[3], v_full[2], tp_full[2], tp_empty[2], mbk, mbx, mbq, mbu, mbd, mbo, k_free;
+  uint64_t kq_full[2], v_full[2], mbx, mbq, mbu, mbd, mbo;
   uint64_t rdy_s, rdy_o, rdy_r, rdy_u, rdy_v;  // one arrival per chain warp
   uint32_t tmem;
 };
@@ -47,7 +46,6 @@ constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_R = 256;   // R as hi, lo (32 + 32), then U' = U e^{gam_C - gam}
 constexpr uint32_t T_U = 320;   // U as hi, lo
 constexpr uint32_t T_O = 384;   // U P^T
-constexpr uint32_t T_K = 448;   // K over Q times K^T
 
 }  // namespace
 
@@ -66,13 +64,13 @@ constexpr uint32_t T_K = 448;   // K over Q times K^T
 // below f32's own rounding of these sums).  The state itself stays f32 in
 // registers, a quarter row per thread.
 //
-// Roles: warps 0-15 the chain above (a row's columns in quarters), warps
-// 16-23 T and P of the chunk ahead (tc_make_tp), warp 24 issues the chain's
-// MMAs, warp 25 the copies and the MMA that T and P start from,
-// so that a full queue stops nobody else.  The
-// columns of U'^T K that a thread reads are those its part of S goes back
-// to, so the chain needs no barrier among its warps.  A chunk is a chain of four dependent products, bound by their
-// latency and the register work between them, not by HBM.
+// Roles: warps 0-15 the chain above (a row's columns in quarters), warp 16
+// issues its MMAs, warp 17 the copies (T, P and the factors come ready from
+// m3_delta_tc_prep_kernel; two stages), so that a full queue stops nobody
+// else.  The columns of U'^T K that a thread reads are those its part of S
+// goes back to, so the chain needs no barrier among its warps.  A chunk is a
+// chain of four dependent products, bound by their latency and the register
+// work between them, not by HBM.
 //
 // AGG: the segment's effect on the state instead of outputs: blockIdx.z 0
 // from a zero state, blockIdx.z 1 from the identity with V = 0 (the rows of
@@ -93,16 +91,11 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&s.kq_full[i], 1);
-      mbar_init(&s.kq_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.kq_full[i], 1);
       mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.tp_full[i], 1);
-      mbar_init(&s.tp_empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbk, &s.mbx, &s.mbq, &s.mbu, &s.mbd, &s.mbo, &s.k_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.mbx, &s.mbq, &s.mbu, &s.mbd, &s.mbo}) mbar_init(r, 1);
     for (uint64_t* r : {&s.rdy_s, &s.rdy_o, &s.rdy_r, &s.rdy_u, &s.rdy_v}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
@@ -113,7 +106,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   TcWait wait;
 
-  if (warp == (CHAIN + TP_THREADS) / 32 + 1) {
+  if (warp == CHAIN / 32 + 1) {
     if (elect_one()) {
       int n_kq = 0, n_v = 0;  // loads issued
       auto load_kq = [&](int n) {  // a step's copies, once the stage is free
@@ -121,9 +114,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         ++n_kq;
         const TcStep t = walk.at(n);
         const int c = t.c, b = t.bh / a.Hv, hk = t.bh % a.Hv / a.share;
-        const uint32_t st = st0 + n % 3 * KQ;
-        uint64_t* bar = &s.kq_full[n % 3];
-        mbar_expect_tx(bar, KQ);
+        const uint32_t st = st0 + (n & 1) * KQ;
+        uint64_t* bar = &s.kq_full[n & 1];
+        mbar_expect_tx(bar, KQ + (uint32_t)sizeof(TcPrep));
+        bulk_load(st0 + PREP + (n & 1) * PREP_STAGE, a.tp + ((size_t)t.bh * a.nc + c) * a.tp_stride, (uint32_t)sizeof(TcPrep), bar);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, bar);
@@ -149,24 +143,15 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         bulk_commit();
         bulk_wait_read();
       };
-      auto products = [&](int n) {  // K over Q times K^T, for the warps that make T and P
-        if (n >= walk.n) return;
-        wait(&s.kq_full[n % 3], n / 3 & 1);
-        if (n > 0) wait(&s.k_free, (n - 1) & 1);
-        if (wait.ok) {
-          tmem_fence_after_sync();
-          tc_mma_kq(st0 + n % 3 * KQ, tm + T_K, &s.mbk);
-        }
-      };
-      for (int n = 0; n < 3; ++n) load_kq(n);
-      for (int n = 0; n < 2; ++n) load_v(n);
-      products(0);
+      for (int n = 0; n < 2; ++n) {
+        load_kq(n);
+        load_v(n);
+      }
       for (int n = 0; n <= walk.n; ++n) {
-        products(n + 1);
+        // step n - 1 is done with its tiles, its results are in place
+        wait(&s.rdy_o, n & 1);
         if (n == 0) continue;
-        wait(&s.kq_empty[(n - 1) % 3], (n - 1) / 3 & 1);  // step n - 1's products are done
-        load_kq(n + 2);
-        wait(&s.rdy_o, n & 1);  // its outputs are in place
+        load_kq(n + 1);
         store(n - 1);
         load_v(n + 1);
       }
@@ -174,12 +159,12 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
       if (!wait.ok) {
-        for (int i = 1; i <= 3 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) % 3], (n_kq - i) / 3 & 1);
+        for (int i = 1; i <= 2 && i <= n_kq; ++i) mbar_wait(&s.kq_full[(n_kq - i) & 1], (n_kq - i) >> 1 & 1);
         for (int i = 1; i <= 2 && i <= n_v; ++i) mbar_wait(&s.v_full[(n_v - i) & 1], (n_v - i) >> 1 & 1);
       }
     }
     __syncwarp();
-  } else if (warp == (CHAIN + TP_THREADS) / 32) {
+  } else if (warp == CHAIN / 32) {
     if (elect_one()) {
       auto mma_state = [&](uint32_t d, uint32_t bt) {  // S (hi, lo) x [64 tokens][128]
 #pragma unroll
@@ -199,8 +184,9 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       };
       for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
-        const uint32_t st = st0 + n % 3 * KQ, par = n & 1;
-        wait(&s.kq_full[n % 3], n / 3 & 1);
+        const uint32_t st = st0 + i * KQ, par = n & 1;
+        const uint32_t tp = st0 + PREP + i * PREP_STAGE;  // T hi, T lo, P hi, P lo
+        wait(&s.kq_full[i], (n >> 1) & 1);
         wait(&s.rdy_s, par);  // S is in tensor memory
         tmem_fence_after_sync();
         if (wait.ok) {
@@ -209,18 +195,16 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
         if (!AGG) {
           wait(&s.rdy_o, par);  // the last chunk's outputs and factors are read
-          if (n > 0) mbar_arrive(&s.tp_empty[i ^ 1]);
           if (wait.ok) {
             tmem_fence_after_sync();
             mma_state(T_Q, st + TILE);
             tc_commit(&s.mbq);
           }
         }
-        wait(&s.tp_full[i], (n >> 1) & 1);
         wait(&s.rdy_r, par);
         if (wait.ok) {
           tmem_fence_after_sync();
-          mma_tokens(T_X, T_R, smem_u32(s.tp[i].t_hi), smem_u32(s.tp[i].t_lo));
+          mma_tokens(T_X, T_R, tp, tp + TILE);
           tc_commit(&s.mbu);
         }
         wait(&s.rdy_u, par);
@@ -234,46 +218,18 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
               tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
                         tc_idesc(128, 128, false, true), p + ks > 0);
           tc_commit(&s.mbd);
-          if (AGG) tc_commit(&s.tp_empty[i]);
-          tc_commit(&s.kq_empty[n % 3]);  // (U P^T reads no stage)
         }
         if (!AGG) {
           wait(&s.rdy_v, par);
           if (wait.ok) {
             tmem_fence_after_sync();
-            mma_tokens(T_O, T_U, smem_u32(s.tp[i].p_hi), smem_u32(s.tp[i].p_lo));
+            mma_tokens(T_O, T_U, tp + 2 * TILE, tp + 3 * TILE);
             tc_commit(&s.mbo);
           }
         }
       }
     }
     __syncwarp();
-  } else if (warp >= CHAIN / 32) {
-    const int pt = tid - CHAIN;
-    // the bf16 bits of this thread's token's gates (widened when they are
-    // needed, a step later, so that nothing waits for the loads)
-    auto gates = [&](int n, uint32_t& g, uint32_t& beta) {
-      g = beta = 0;
-      if (n >= walk.n || pt >= TC) return;
-      const TcStep st = walk.at(n);
-      const int t = st.c * TC + pt;
-      if (t >= a.T) return;
-      const int64_t at = ((int64_t)(st.bh / a.Hv) * a.T + t) * a.Hv + st.bh % a.Hv;
-      g = static_cast<const unsigned short*>(a.g)[at];
-      beta = static_cast<const unsigned short*>(a.beta)[at];
-    };
-    uint32_t g, beta, gn, bn;
-    gates(0, g, beta);
-    for (int n = 0; n < walk.n; ++n) {
-      const int i = n & 1;
-      gates(n + 1, gn, bn);
-      wait(&s.kq_full[n % 3], n / 3 & 1);
-      tc_make_tp<L2>(st0 + n % 3 * KQ, tm + T_K, s.tp[i], s.vec[i], s.work, __uint_as_float(g << 16), __uint_as_float(beta << 16), a.scale, pt, &s.mbk, n & 1,
-                     &s.k_free, &s.tp_empty[i], ((n >> 1) - 1) & 1, n >= 2, wait);
-      if (pt == 0) mbar_arrive(&s.tp_full[i]);
-      g = gn;
-      beta = bn;
-    }
   } else {
     const int qt = warp >> 2, row = (warp & 3) * 32 + lane;  // quarter; row: the state's head_v index
     const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -281,6 +237,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     // this row's element of token 16 qt + j in a [64 tokens][head_v] tile pair
     const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
     auto at = [&](int j) { return el + j * 128 + ((eu ^ (j & 7)) << 4); };
+    auto vec = [&](int n) -> const TcVec& { return reinterpret_cast<const TcPrep*>(base + PREP + (n & 1) * PREP_STAGE)->vec; };
     float2 S[16];  // S^T[row][32 qt + k]
     if (qt == 0) s.bad[row] = TC;
     bar_sync(1, CHAIN);
@@ -379,7 +336,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tc_ld16(tl + T_Q + qt * 16, q);
       tc_ld16(tl + T_O + qt * 16, o);
       const int bad = s.bad[row] - qt * 16;
-      const Vec16 fq{&s.vec[n & 1].fq[qt * 16]};
+      const Vec16 fq{&vec(n).fq[qt * 16]};
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = __ffma2_rn(fq[j], q[j], o[j]);
       if (bad < 16) {
@@ -417,7 +374,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       ready(&s.rdy_o);
       // R = beta V - bfx X
-      wait(&s.tp_full[i], (n >> 1) & 1);
+      wait(&s.kq_full[i], (n >> 1) & 1);
       wait(&s.v_full[i], (n >> 1) & 1);
       float2 x[8];
       {
@@ -432,7 +389,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         tmem_fence_after_sync();
         tc_ld16(tl + T_X + qt * 16, x);
         float2 chk = f2b(0.0f);
-        const Vec16 be{&s.vec[i].beta[qt * 16]}, bx{&s.vec[i].bfx[qt * 16]};
+        const Vec16 be{&vec(n).beta[qt * 16]}, bx{&vec(n).bfx[qt * 16]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 vv = ident ? f2b(0.0f) : make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16));
@@ -462,13 +419,13 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        const Vec16 fu{&s.vec[i].fu[qt * 16]};
+        const Vec16 fu{&vec(n).fu[qt * 16]};
         float2 y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(x[j], fu[j]);
         put_tokens(T_R, y, nullptr);
       }
-      const float2 ec = f2b(s.vec[i].ec);
+      const float2 ec = f2b(vec(n).ec);
       ready(&s.rdy_u);
       if (!AGG) {  // while the update of S runs
         put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);

@@ -32,13 +32,13 @@ def _delta_plan(dims, act=BF16):
 def test_delta_plan_sizes(lib):
     st, p = _delta_plan(_delta())
     assert st == 0 and p.n_chunks == -(-100 // p.chunk)
-    assert p.ckpt_bytes == 2 * 4 * p.n_chunks * 65536  # bf16: state and update tiles, padded to 128
-    assert p.workspace_bytes >= binding.STATUS_BYTES and p.fwd_launches >= 1 and p.bwd_launches >= 1
+    assert p.ckpt_bytes == 2 * 4 * p.n_chunks * 99456  # bf16: state and update tiles padded to 128, T, P, factors
+    assert p.workspace_bytes >= p.fwd_workspace_bytes >= binding.STATUS_BYTES and p.fwd_launches >= 1 and p.bwd_launches >= 1
     st, p = _delta_plan(_delta(seq_len=0))
     assert st == 0 and p.n_chunks == 0 and p.ckpt_bytes == 0 and p.fwd_launches == 0 and p.bwd_launches == 0
     # sizes past 32 bits
     st, p = _delta_plan(_delta(batch=8, seq_len=1 << 20, v_heads=64, k_heads=64, head_k=128))
-    assert st == 0 and p.ckpt_bytes == 8 * 64 * p.n_chunks * 65536
+    assert st == 0 and p.ckpt_bytes == 8 * 64 * p.n_chunks * 99456
     st, p = _delta_plan(_delta(), act=F32)
     assert st == 0 and p.ckpt_bytes == 2 * 4 * p.n_chunks * 64 * 128 * 4
 
