@@ -18,11 +18,11 @@
 
 namespace m3 {
 
-// Per chunk and head, bf16 tiles of 128 rows (head_v) x 64 in the swizzle of
+// Per chunk and head, bf16 [16-byte unit][128 rows (head_v)][8], a layout of
 // shared-memory operands, so that one bulk copy brings them in ready to use:
 constexpr size_t TC_PREP = 33920;  // T, P and the per-token factors (TcPrep)
-constexpr size_t TC_CKPT = 65536 + TC_PREP;  // the forward's: S^T (head_k in two tiles), U^T hi, U^T lo, TcPrep
-constexpr size_t TC_BWD = 98304;   // the reverse pass's: dS^T hi, lo (two tiles each), dR^T hi, dR^T lo
+constexpr size_t TC_CKPT = 65536 + TC_PREP;  // the forward's: S^T, U^T hi, U^T lo, TcPrep
+constexpr size_t TC_BWD = 98304;   // the reverse pass's: dS^T hi, lo, dR^T hi, lo
 constexpr int TC = 64;             // tokens per chunk of the tensor-core kernels
 constexpr int TC_BLOCKS = 152;     // persistent blocks of the gradients' kernel, at most (the SMs of a GB300)
 constexpr int DMAX = 128;          // head_k and head_v, at most

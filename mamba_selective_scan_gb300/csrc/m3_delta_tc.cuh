@@ -23,6 +23,13 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
   return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
          (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | 1ull << 46 | 2ull << 61;
 }
+// What the chain kernels keep for the gradients is [16-byte unit][128 rows
+// (head_v)][8 elements] without a swizzle (a warp whose lanes are rows writes
+// whole lines): an M- or N-major operand whose rows are K, units 2048 bytes
+// apart, 8 rows 128 bytes apart; a step of 16 in K is 256 bytes.
+__device__ __forceinline__ uint64_t tc_desc_plain(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(2048 >> 4) << 32 | 1ull << 46;
+}
 // bf16 x bf16 -> f32, M x N, operands K-major unless set
 __host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool a_mn, bool b_mn) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |

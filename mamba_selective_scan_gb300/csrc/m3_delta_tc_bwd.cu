@@ -269,7 +269,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
     };
     auto put_state = [&](const TcStep& t) {  // dS as hi, lo into tensor memory, and kept for the step's gradients
-      unsigned char* ck = AGG ? nullptr : a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + (qt >> 1) * 16384;
+      unsigned char* ck = AGG ? nullptr : a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + row * 16;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t hi[8], lo[8];
@@ -280,7 +280,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         if (ck) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t o = sw(row, (qt & 1) * 4 + p * 2 + u);
+            const int o = (qt * 4 + p * 2 + u) * 2048;
             *reinterpret_cast<uint4*>(ck + o) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
             *reinterpret_cast<uint4*>(ck + 32768 + o) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
           }
@@ -301,8 +301,8 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (ck) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          *reinterpret_cast<uint4*>(ck + sw(row, qt * 2 + u)) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(ck + 16384 + sw(row, qt * 2 + u)) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + (qt * 2 + u) * 2048 + row * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 16384 + (qt * 2 + u) * 2048 + row * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
         }
       }
     };
@@ -434,9 +434,9 @@ constexpr int THREADS = EPI + 32;
 // shared-memory offsets
 constexpr int KQ = 0;            // K, Q, K, Q tiles as in a stage
 constexpr int DO = 4 * TILE;     // dO, two tiles; the tile before each is read (and ignored) with it
-constexpr int S0 = 6 * TILE;     // S^T, two tiles of 128 rows; later P2 hi, lo and A2 hi, lo
+constexpr int S0 = 6 * TILE;     // S^T; later P2 hi, lo and A2 hi, lo
 constexpr int U = S0 + 32768;    // U^T hi, lo
-constexpr int DS = U + 32768;    // dS^T hi (two tiles), lo (two tiles)
+constexpr int DS = U + 32768;    // dS^T hi, lo
 constexpr int DR = DS + 65536;   // dR^T hi, lo
 constexpr int SMALL = DR + 32768;
 constexpr int BIG_BYTES = 32768 + (int)TC_BWD + 2 * TILE;
@@ -575,6 +575,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 #pragma unroll
         for (int ks = 0; ks < steps; ++ks) tc_mma_ss(tm + d, da(ks), db(ks), idesc, !(first && ks == 0));
       };
+      auto kept = [&](int at) { return [=](int ks) { return tc_desc_plain(sb + at + ks * 256); }; };
       auto mn = [&](int at, int lbo) { return [=](int ks) { return tc_desc(sb + at + ks * 2048, lbo, 1024); }; };
       auto kmaj = [&](int at, int blk) { return [=](int ks) { return tc_desc(sb + at + (ks >> 2) * blk + (ks & 3) * 32, 16, 1024); }; };
       constexpr uint32_t NN = tc_idesc(128, 64, false, false), NM = tc_idesc(128, 64, false, true),
@@ -592,18 +593,18 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         if (wait.ok) {
           tmem_fence_after_sync();
           mma(T_KQ, 8, NN, true, kmaj(KQ, 2 * TILE), kmaj(KQ, 2 * TILE));
-          mma(T_G, 8, MM, true, mn(U, 16384), mn(DR, 16));
-          mma(T_G, 8, MM, false, mn(U + 16384, 16384), mn(DR, 16));
-          mma(T_G, 8, MM, false, mn(U, 16384), mn(DR + 16384, 16));
-          mma(T_DP, 8, NM, true, kmaj(DO - TILE, TILE), mn(U, 16));
-          mma(T_DP, 8, NM, false, kmaj(DO - TILE, TILE), mn(U + 16384, 16));
-          mma(T_YO, 8, MN, true, mn(S0, 16384), kmaj(DO, TILE));
-          mma(T_Y, 8, MM, true, mn(S0, 16384), mn(DR, 16));
-          mma(T_Y, 8, MM, false, mn(S0, 16384), mn(DR + 16384, 16));
+          mma(T_G, 8, MM, true, kept(U), kept(DR));
+          mma(T_G, 8, MM, false, kept(U + 16384), kept(DR));
+          mma(T_G, 8, MM, false, kept(U), kept(DR + 16384));
+          mma(T_DP, 8, NM, true, kmaj(DO - TILE, TILE), kept(U));
+          mma(T_DP, 8, NM, false, kmaj(DO - TILE, TILE), kept(U + 16384));
+          mma(T_YO, 8, MN, true, kept(S0), kmaj(DO, TILE));
+          mma(T_Y, 8, MM, true, kept(S0), kept(DR));
+          mma(T_Y, 8, MM, false, kept(S0), kept(DR + 16384));
           tc_commit(&s.mb1);
-          mma(T_Z, 8, MM, true, mn(DS, 16384), mn(U, 16));
-          mma(T_Z, 8, MM, false, mn(DS + 32768, 16384), mn(U, 16));
-          mma(T_Z, 8, MM, false, mn(DS, 16384), mn(U + 16384, 16));
+          mma(T_Z, 8, MM, true, kept(DS), kept(U));
+          mma(T_Z, 8, MM, false, kept(DS + 32768), kept(U));
+          mma(T_Z, 8, MM, false, kept(DS), kept(U + 16384));
           tc_commit(&s.mb2);
         }
         wait(&s.rdy1, par);  // P2 and A2 are in place of S0; the inner product has read S0 and dS
@@ -838,7 +839,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
               const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (tok0 + i) * a.vs + (int64_t)h * a.DV;
               float rv = 0.0f;
               for (int m = 0; m < a.DV; ++m) {
-                const uint32_t at = sw(m, i >> 3) + (i & 7) * 2;
+                const uint32_t at = (i >> 3) * 2048 + m * 16 + (i & 7) * 2;
                 const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + at)) +
                                 __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + 16384 + at));
                 rv = fmaf(x, __bfloat162float(vp[m]), rv);

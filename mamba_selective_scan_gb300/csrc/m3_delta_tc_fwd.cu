@@ -296,7 +296,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     auto put_state = [&](const TcStep* t) {  // S as hi, lo into tensor memory (and the step's checkpoint)
       unsigned char* ck = nullptr;
       if (!AGG && a.ckpt && t)
-        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t->bh * a.nc + t->c) * TC_CKPT + (qt >> 1) * 16384;
+        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t->bh * a.nc + t->c) * TC_CKPT + row * 16;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         uint32_t hi[8], lo[8];
@@ -307,7 +307,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         if (ck) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            *reinterpret_cast<uint4*>(ck + sw(row, (qt & 1) * 4 + p * 2 + u)) =
+            *reinterpret_cast<uint4*>(ck + (qt * 4 + p * 2 + u) * 2048) =
                 make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
         }
       }
@@ -323,8 +323,8 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (ck) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          *reinterpret_cast<uint4*>(ck + sw(row, qt * 2 + u)) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(ck + 16384 + sw(row, qt * 2 + u)) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + (qt * 2 + u) * 2048 + row * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(ck + 16384 + (qt * 2 + u) * 2048 + row * 16) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
         }
       }
     };
@@ -486,7 +486,7 @@ bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, 
 // the last segment to the first.
 __global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
   __shared__ __align__(16) float S[DMAX][32];
-  __shared__ __align__(16) float P[32][DMAX + 4];
+  __shared__ __align__(16) float P[32][DMAX + 4];  // (rows 4 banks apart)
   const int tid = threadIdx.x, bh = blockIdx.x, v0 = blockIdx.y * 32;
   const int kq = (tid >> 3) * 4, vq = (tid & 7) * 4;  // 4 rows k x 4 columns per thread
   for (int i = tid; i < DMAX * 32; i += 256) {
@@ -504,7 +504,11 @@ __global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant
     }
     for (int r0 = 0; r0 < DMAX; r0 += 32) {  // Phi[r][k] is stored [k][r]
       __syncthreads();
-      for (int i = tid; i < 32 * DMAX; i += 256) P[i & 31][i >> 5] = a.seg_phi[at + (size_t)(i >> 5) * DMAX + r0 + (i & 31)];
+      float f[16];  // all loads before the first store, so that they overlap
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] = a.seg_phi[at + (size_t)(i * 8 + (tid >> 5)) * DMAX + r0 + (tid & 31)];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) P[tid & 31][i * 8 + (tid >> 5)] = f[i];
       __syncthreads();
 #pragma unroll 8
       for (int r = 0; r < 32; ++r) {
