@@ -247,7 +247,14 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       float* dst = nullptr;
       bool own = true;
       if (AGG) {
-        dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+        dst = a.seg_end + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+        if (ident) {  // by rows of the transition
+          float* o = a.seg_phi + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
+#pragma unroll
+          for (int k = 0; k < 16; k += 2)
+            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
+          return;
+        }
       } else if (t.give) {
         dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
       } else if (a.ds_in && chunk(t) == 0) {
@@ -434,12 +441,12 @@ constexpr int THREADS = EPI + 32;
 // shared-memory offsets
 constexpr int KQ = 0;            // K, Q, K, Q tiles as in a stage
 constexpr int DO = 4 * TILE;     // dO, two tiles; the tile before each is read (and ignored) with it
-constexpr int S0 = 6 * TILE;     // S^T; later P2 hi, lo and A2 hi, lo
+constexpr int S0 = 6 * TILE;     // S^T
 constexpr int U = S0 + 32768;    // U^T hi, lo
-constexpr int DS = U + 32768;    // dS^T hi, lo
+constexpr int DS = U + 32768;    // dS^T hi, lo; in the place of lo later P2 hi, lo and A2 hi, lo
 constexpr int DR = DS + 65536;   // dR^T hi, lo
 constexpr int SMALL = DR + 32768;
-constexpr int BIG_BYTES = 32768 + (int)TC_BWD + 2 * TILE;
+constexpr int P2 = DS + 32768, A2 = P2 + 2 * TILE;
 
 struct Smem {  // at SMALL
   float gam[TC], beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC];
@@ -449,7 +456,9 @@ struct Smem {  // at SMALL
   float dot[3][4][TC];               // Q.(dO S0^T), K.(dR S0^T), K.(U dS^T): per warp of 32 head_k
   float red[16];
   float ec, tot;
-  uint64_t big, s, kq, mb1, mb2, mb3, rdy1, rdy2;
+  uint64_t ds, dl, us, kq;           // arrived: dS hi; dS lo; U, dR, dO, S0; K, Q
+  uint64_t mb0, mb1, mb2, mb3;       // done: Z; G, dP, K Q^T; Yo, Y; the products with P2 and A2
+  uint64_t rdy0, rdy1, rdy2;
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -534,9 +543,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   const uint32_t sb = smem_u32(base);
 
   if (tid == 0) {
-    for (uint64_t* r : {&s.big, &s.s, &s.kq, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
-    mbar_init(&s.rdy1, EPI / 32);
-    mbar_init(&s.rdy2, EPI / 32);
+    for (uint64_t* r : {&s.ds, &s.dl, &s.us, &s.kq, &s.mb0, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy0, &s.rdy1, &s.rdy2}) mbar_init(r, EPI / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -548,19 +556,23 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 
   if (warp == EPI / 32) {
     if (elect_one()) {
-      uint32_t n_big = 0, n_s = 0, n_kq = 0;  // loads issued
-      auto load_big = [&](const GradItem& it) {
-        ++n_big;
-        const unsigned char* ck = reinterpret_cast<const unsigned char*>(a.ckpt_in) + it.at * TC_CKPT;
-        mbar_expect_tx(&s.big, BIG_BYTES);
-        bulk_load(sb + U, ck + 32768, 32768, &s.big);
-        bulk_load(sb + DS, a.bwd + it.at * TC_BWD, (uint32_t)TC_BWD, &s.big);
-        for (int blk = 0; blk < 2; ++blk) tma_tile(sb + DO + blk * TILE, &md, blk * 64, it.h, it.c * TC, it.b, &s.big);
+      uint32_t n_ds = 0, n_dl = 0, n_us = 0, n_kq = 0;  // loads issued
+      auto load_ds = [&](const GradItem& it) {
+        ++n_ds;
+        mbar_expect_tx(&s.ds, 32768);
+        bulk_load(sb + DS, a.bwd + it.at * TC_BWD, 32768, &s.ds);
       };
-      auto load_s = [&](const GradItem& it) {
-        ++n_s;
-        mbar_expect_tx(&s.s, 32768);
-        bulk_load(sb + S0, reinterpret_cast<const unsigned char*>(a.ckpt_in) + it.at * TC_CKPT, 32768, &s.s);
+      auto load_dl = [&](const GradItem& it) {
+        ++n_dl;
+        mbar_expect_tx(&s.dl, 32768);
+        bulk_load(sb + DS + 32768, a.bwd + it.at * TC_BWD + 32768, 32768, &s.dl);
+      };
+      auto load_us = [&](const GradItem& it) {
+        ++n_us;
+        mbar_expect_tx(&s.us, 3 * 32768 + 2 * TILE);
+        bulk_load(sb + S0, reinterpret_cast<const unsigned char*>(a.ckpt_in) + it.at * TC_CKPT, 65536, &s.us);  // and U
+        bulk_load(sb + DR, a.bwd + it.at * TC_BWD + 65536, 32768, &s.us);
+        for (int blk = 0; blk < 2; ++blk) tma_tile(sb + DO + blk * TILE, &md, blk * 64, it.h, it.c * TC, it.b, &s.us);
       };
       auto load_kq = [&](const GradItem& it) {
         ++n_kq;
@@ -581,36 +593,46 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       constexpr uint32_t NN = tc_idesc(128, 64, false, false), NM = tc_idesc(128, 64, false, true),
                          MN = tc_idesc(128, 64, true, false), MM = tc_idesc(128, 64, true, true);
       GradItem it(a, blockIdx.x);
+      load_us(it);
+      load_ds(it);
+      load_dl(it);
       load_kq(it);
-      load_big(it);
-      load_s(it);
       for (uint32_t par = 0; it.group < groups; par ^= 1) {
         it.next(a);
         const bool more = it.group < groups;
-        wait(&s.kq, par);
-        wait(&s.big, par);
-        wait(&s.s, par);
+        wait(&s.us, par);
+        wait(&s.ds, par);
+        wait(&s.dl, par);
         if (wait.ok) {
           tmem_fence_after_sync();
+          mma(T_Z, 8, MM, true, kept(DS), kept(U));
+          mma(T_Z, 8, MM, false, kept(DS), kept(U + 16384));
+          mma(T_Z, 8, MM, false, kept(DS + 32768), kept(U));
+          tc_commit(&s.mb0);
+        }
+        wait(&s.kq, par);
+        if (wait.ok) {
           mma(T_KQ, 8, NN, true, kmaj(KQ, 2 * TILE), kmaj(KQ, 2 * TILE));
           mma(T_G, 8, MM, true, kept(U), kept(DR));
           mma(T_G, 8, MM, false, kept(U + 16384), kept(DR));
           mma(T_G, 8, MM, false, kept(U), kept(DR + 16384));
           mma(T_DP, 8, NM, true, kmaj(DO - TILE, TILE), kept(U));
           mma(T_DP, 8, NM, false, kmaj(DO - TILE, TILE), kept(U + 16384));
+          tc_commit(&s.mb1);
           mma(T_YO, 8, MN, true, kept(S0), kmaj(DO, TILE));
           mma(T_Y, 8, MM, true, kept(S0), kept(DR));
           mma(T_Y, 8, MM, false, kept(S0), kept(DR + 16384));
-          tc_commit(&s.mb1);
-          mma(T_Z, 8, MM, true, kept(DS), kept(U));
-          mma(T_Z, 8, MM, false, kept(DS + 32768), kept(U));
-          mma(T_Z, 8, MM, false, kept(DS), kept(U + 16384));
           tc_commit(&s.mb2);
         }
-        wait(&s.rdy1, par);  // P2 and A2 are in place of S0; the inner product has read S0 and dS
+        // the next item's tiles as soon as this one's have been read
+        wait(&s.mb0, par);
+        wait(&s.rdy0, par);  // the inner product has read S0 and dS
+        if (more && wait.ok) load_ds(it);
+        wait(&s.mb2, par);
+        if (more && wait.ok) load_us(it);
+        wait(&s.rdy1, par);  // P2 and A2 are in place
         if (wait.ok) {
           tmem_fence_after_sync();
-          constexpr int P2 = S0, A2 = S0 + 2 * TILE;
           for (int p = 0; p < 2; ++p) {
             mma(T_DQ, 4, MN, p == 0, mn(KQ, 2 * TILE), kmaj(P2 + p * TILE, 0));
             mma(T_DK, 4, MM, p == 0, mn(KQ + TILE, 2 * TILE), mn(P2 + p * TILE, 16));
@@ -619,17 +641,16 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           }
           tc_commit(&s.mb3);
         }
-        wait(&s.mb2, par);
-        if (more && wait.ok) load_big(it);
         wait(&s.mb3, par);
-        if (more && wait.ok) load_s(it);
+        if (more && wait.ok) load_dl(it);
         wait(&s.rdy2, par);  // K, Q and the accumulators are read
         if (more && wait.ok) load_kq(it);
       }
-      if (!wait.ok && n_kq) {  // as in the other kernels: copies in flight land first
-        mbar_wait(&s.kq, (n_kq - 1) & 1);
-        mbar_wait(&s.big, (n_big - 1) & 1);
-        mbar_wait(&s.s, (n_s - 1) & 1);
+      if (!wait.ok) {  // as in the other kernels: copies in flight land first
+        if (n_ds) mbar_wait(&s.ds, (n_ds - 1) & 1);
+        if (n_dl) mbar_wait(&s.dl, (n_dl - 1) & 1);
+        if (n_us) mbar_wait(&s.us, (n_us - 1) & 1);
+        if (n_kq) mbar_wait(&s.kq, (n_kq - 1) & 1);
       }
     }
     __syncwarp();
@@ -658,6 +679,30 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         g = clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
         beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[(tok0 + tid) * a.Hv + h]);
       }
+      // <dS, S0>
+      wait(&s.us, par);
+      wait(&s.ds, par);
+      wait(&s.dl, par);
+      {
+        float acc = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = (tid + u * EPI) * 16;
+          const uint4 x = *reinterpret_cast<const uint4*>(base + S0 + at), y = *reinterpret_cast<const uint4*>(base + DS + at),
+                      z = *reinterpret_cast<const uint4*>(base + DS + 32768 + at);
+          const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc = fmaf(__uint_as_float(xv[j] << 16), __uint_as_float(yv[j] << 16) + __uint_as_float(zv[j] << 16), acc);
+            acc = fmaf(__uint_as_float(xv[j] & 0xFFFF0000u),
+                       __uint_as_float(yv[j] & 0xFFFF0000u) + __uint_as_float(zv[j] & 0xFFFF0000u), acc);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
+        if (lane == 0) s.red[warp] = acc;
+      }
+      ready(&s.rdy0);
       wait(&s.kq, par);
       if (L2) {
         float s0 = 0.0f, s1 = 0.0f;
@@ -684,28 +729,6 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         }
         if (tid == 31) s.tot = g;
       }
-      // <dS, S0>
-      wait(&s.s, par);
-      wait(&s.big, par);
-      {
-        float acc = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int at = (tid + u * EPI) * 16;
-          const uint4 x = *reinterpret_cast<const uint4*>(base + S0 + at), y = *reinterpret_cast<const uint4*>(base + DS + at),
-                      z = *reinterpret_cast<const uint4*>(base + DS + 32768 + at);
-          const uint32_t xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc = fmaf(__uint_as_float(xv[j] << 16), __uint_as_float(yv[j] << 16) + __uint_as_float(zv[j] << 16), acc);
-            acc = fmaf(__uint_as_float(xv[j] & 0xFFFF0000u),
-                       __uint_as_float(yv[j] & 0xFFFF0000u) + __uint_as_float(zv[j] & 0xFFFF0000u), acc);
-          }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
-        if (lane == 0) s.red[warp] = acc;
-      }
       bar_sync(1, EPI);
       if (warp < 2) {
         if (warp == 1) g += s.tot;
@@ -731,7 +754,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         const int r = row & (TC - 1), c0 = qt * 16;
         const float gr = s.gam[r];
         float v[16], k[16];
-        unsigned char* tile = base + S0;
+        unsigned char* tile = base + grad::P2;
         if (wq < 2) {  // G^T: row j = r, columns i
           tc_ld16(tl + T_G, v);
           tc_ld16(tl + T_KQ, k);
@@ -767,6 +790,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           const float t = reduce16(k, lane);
           if (!(lane & 1)) s.col_p[wq - 2][c0 + (lane >> 1)] = t;
         }
+        wait(&s.mb0, par);  // dS is read (so has the inner product, two barriers ago)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint4 hi, lo;

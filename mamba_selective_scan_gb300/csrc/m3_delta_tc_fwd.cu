@@ -272,7 +272,14 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       float* dst = nullptr;
       bool own = true;
       if (AGG) {
-        dst = (ident ? a.seg_phi : a.seg_end) + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+        dst = a.seg_end + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
+        if (ident) {  // by rows of the transition
+          float* o = a.seg_phi + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
+#pragma unroll
+          for (int k = 0; k < 16; k += 2)
+            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
+          return;
+        }
       } else if (t.give) {
         dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
       } else if (a.s_out && t.c == a.nc - 1) {
@@ -482,59 +489,44 @@ bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, 
 }
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
-// start[s], 32 columns of the state per block, f32.  rev: the adjoint's, from
-// the last segment to the first.
-__global__ void __launch_bounds__(256) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
-  __shared__ __align__(16) float S[DMAX][32];
-  __shared__ __align__(16) float P[32][DMAX + 4];  // (rows 4 banks apart)
-  const int tid = threadIdx.x, bh = blockIdx.x, v0 = blockIdx.y * 32;
-  const int kq = (tid >> 3) * 4, vq = (tid & 7) * 4;  // 4 rows k x 4 columns per thread
-  for (int i = tid; i < DMAX * 32; i += 256) {
-    const int k = i >> 5, v = v0 + (i & 31);
-    S[k][i & 31] = first && k < a.DK && v < a.DV ? first[((size_t)bh * a.DK + k) * a.DV + v] : 0.0f;
-  }
+// start[s], 16 columns of the state per block, a row and four columns per
+// thread, f32.  rev: the adjoint's, from the last segment to the first.  A
+// segment is one pass over its Phi (64 KB, from L2) and bound by the latency
+// of those loads, 32 at a time; few heads are what makes segments, so blocks
+// are kept small.
+__global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
+  __shared__ __align__(16) float S[DMAX][16];
+  const int tid = threadIdx.x, bh = blockIdx.x, k = tid & (DMAX - 1), vq = (tid >> 7) * 4, v = blockIdx.y * 16 + vq;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (first && k < a.DK && v < a.DV) x = *reinterpret_cast<const float4*>(first + ((size_t)bh * a.DK + k) * a.DV + v);
+  *reinterpret_cast<float4*>(&S[k][vq]) = x;
   for (int n = 0; n + 1 < a.segs; ++n) {
     const int sg = rev ? a.segs - 1 - n : n, to = rev ? sg - 1 : sg + 1;
     const size_t at = ((size_t)bh * a.segs + sg) * DMAX * DMAX;
-    float acc[4][4];
+    x = *reinterpret_cast<const float4*>(a.seg_end + at + (size_t)k * DMAX + v);
+    const float* phi = a.seg_phi + at + k;  // Phi[r][k]
+    __syncthreads();
+#pragma unroll 1
+    for (int r0 = 0; r0 < DMAX; r0 += 32) {
+      float p[32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 n = *reinterpret_cast<const float4*>(a.seg_end + at + (size_t)(kq + i) * DMAX + v0 + vq);
-      acc[i][0] = n.x; acc[i][1] = n.y; acc[i][2] = n.z; acc[i][3] = n.w;
-    }
-    for (int r0 = 0; r0 < DMAX; r0 += 32) {  // Phi[r][k] is stored [k][r]
-      __syncthreads();
-      float f[16];  // all loads before the first store, so that they overlap
+      for (int r = 0; r < 32; ++r)  // (volatile: all of them before the first use)
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(p[r]) : "l"(phi + (size_t)(r0 + r) * DMAX) : "memory");
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = a.seg_phi[at + (size_t)(i * 8 + (tid >> 5)) * DMAX + r0 + (tid & 31)];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) P[tid & 31][i * 8 + (tid >> 5)] = f[i];
-      __syncthreads();
-#pragma unroll 8
       for (int r = 0; r < 32; ++r) {
-        const float4 p = *reinterpret_cast<const float4*>(&P[r][kq]);
-        const float4 x = *reinterpret_cast<const float4*>(&S[r0 + r][vq]);
-        const float pv[4] = {p.x, p.y, p.z, p.w}, xv[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(pv[i], xv[j], acc[i][j]);
+        const float4 y = *reinterpret_cast<const float4*>(&S[r0 + r][vq]);
+        x.x = fmaf(p[r], y.x, x.x); x.y = fmaf(p[r], y.y, x.y);
+        x.z = fmaf(p[r], y.z, x.z); x.w = fmaf(p[r], y.w, x.w);
       }
     }
     __syncthreads();
-    float* dst = a.seg_start + ((size_t)bh * a.segs + to) * DMAX * DMAX;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 r = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *reinterpret_cast<float4*>(&S[kq + i][vq]) = r;
-      *reinterpret_cast<float4*>(dst + (size_t)(kq + i) * DMAX + v0 + vq) = r;
-    }
-    __syncthreads();
+    *reinterpret_cast<float4*>(&S[k][vq]) = x;
+    *reinterpret_cast<float4*>(a.seg_start + ((size_t)bh * a.segs + to) * DMAX * DMAX + (size_t)k * DMAX + v) = x;
   }
 }
 
 cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st) {
-  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), 4), 256, 0, st, false, a, first, rev);
+  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), DMAX / 16), 512, 0, st, false, a, first, rev);
 }
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {

@@ -20,17 +20,23 @@ cudaError_t take_delta_prep_status(unsigned* out) {
 
 namespace {
 
+constexpr int TP_THREADS = 256;
 struct TcWork {  // scratch
-  float A[TC][TC + 4];
   float M[32][36];
   float gam[TC], ss[2][2 * TC], beta[TC], nk[TC], nq[TC];
   float tot;
 };
-constexpr int TP_THREADS = 256;
 
 
-constexpr int OUT = (int)((sizeof(TcPrep) + 1023) / 1024 * 1024);  // the K/Q tiles', then the results'
-constexpr size_t SMEM_BYTES = OUT + sizeof(TcWork) + 1024;
+// shared memory: the K/Q tiles; once their product is there, A and P with the
+// factors take their place, and T at last A's (four blocks per SM)
+constexpr int A_BYTES = TC * (TC + 4) * 4;
+static_assert(A_BYTES % 1024 == 0 && A_BYTES >= 2 * TILE, "P's tiles follow A");
+constexpr int PV = A_BYTES;
+constexpr int PV_BYTES = (int)sizeof(TcPrep) - 2 * TILE;
+constexpr int WORK = (PV + PV_BYTES + 1023) / 1024 * 1024;
+static_assert(WORK >= 4 * TILE, "the K/Q tiles");
+constexpr size_t SMEM_BYTES = WORK + sizeof(TcWork) + 1024;
 
 // D (16 x 8) += A (16 x K) B (K x 8) by one warp, f32 in shared memory, each
 // operand as two bf16 terms (three products; these blocks are far too small
@@ -71,7 +77,7 @@ __device__ __forceinline__ void warp_mma_store(const float (&d)[4], float* o, in
 }  // namespace
 
 // A chunk's T = (I + A)^-1 and P = scale D o (Q K^T), by 256 threads, one
-// block per (chunk, head), three blocks per SM.
+// block per (chunk, head), four blocks per SM.
 //
 // K over Q times K^T is one 128 x 64 MMA; a thread then has half a row of
 // K K^T (rows 0-63) or of Q K^T (64-127).  I + A is inverted by blocks: the
@@ -85,17 +91,17 @@ __device__ __forceinline__ void warp_mma_store(const float (&d)[4], float* o, in
 // other and are bound by that chain; this work has no order, so it is done
 // here once, with full SMs, and read back (34 KB per chunk and head).
 template <bool L2>
-__global__ void __launch_bounds__(TP_THREADS, 3)
+__global__ void __launch_bounds__(TP_THREADS, 4)
 m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
                         const __grid_constant__ CUtensorMap mk) {
   extern __shared__ unsigned char raw[];
   unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   __shared__ __align__(8) uint64_t full, mbk;
   __shared__ uint32_t slot;
-  TcPrep& out = *reinterpret_cast<TcPrep*>(base);
-  TcTP& tp = out.tp;
-  TcVec& vec = out.vec;
-  TcWork& w = *reinterpret_cast<TcWork*>(base + OUT);
+  float (&A)[TC][TC + 4] = *reinterpret_cast<float (*)[TC][TC + 4]>(base);
+  unsigned char *t_hi = base, *t_lo = base + TILE, *p_hi = base + PV, *p_lo = base + PV + TILE;
+  TcVec& vec = *reinterpret_cast<TcVec*>(base + PV + 2 * TILE);
+  TcWork& w = *reinterpret_cast<TcWork*>(base + WORK);
   const int pt = threadIdx.x, lane = pt & 31, wp = __shfl_sync(~0u, pt >> 5, 0);
   const int bh = blockIdx.x / a.nc, c = blockIdx.x % a.nc, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share;
   const uint32_t kq = smem_u32(base);
@@ -165,6 +171,8 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     w.nq[pt] = L2 ? rsqrtf(w.ss[0][TC + pt] + w.ss[1][TC + pt] + DELTA_L2_EPS) : 1.0f;
   }
   __syncthreads();
+  wait(&mbk, 0);  // (and every thread has read its rows of K and Q)
+  tmem_fence_after_sync();
   if (wp < 2) {
     const float gc = w.gam[TC - 1], eg = ex2(gam);
     vec.beta[pt] = beta;
@@ -173,8 +181,6 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     vec.fq[pt] = scale * eg * w.nq[pt];
     if (pt == 0) vec.ec = ex2(gc);
   }
-  wait(&mbk, 0);
-  tmem_fence_after_sync();
   {
     const int i = row & (TC - 1);
     const bool isA = (wp & 3) < 2;
@@ -209,7 +215,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       if (isA) {
 #pragma unroll
         for (int m = 0; m < 8; m += 2)
-          *reinterpret_cast<float4*>(&w.A[i][c0 + 2 * m]) = make_float4(v[m].x, v[m].y, v[m + 1].x, v[m + 1].y);
+          *reinterpret_cast<float4*>(&A[i][c0 + 2 * m]) = make_float4(v[m].x, v[m].y, v[m + 1].x, v[m + 1].y);
       } else {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -219,8 +225,8 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           split2(v[4 * u + 2], h.z, l.z);
           split2(v[4 * u + 3], h.w, l.w);
           const uint32_t at = sw(i, (c0 >> 3) + u);
-          *reinterpret_cast<uint4*>(tp.p_hi + at) = h;
-          *reinterpret_cast<uint4*>(tp.p_lo + at) = l;
+          *reinterpret_cast<uint4*>(p_hi + at) = h;
+          *reinterpret_cast<uint4*>(p_lo + at) = l;
         }
       }
     }
@@ -235,12 +241,12 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       for (int i = 0; i < 8; ++i) {
         float s0 = i == c ? 1.0f : 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int l = 0; l < i; ++l) (l & 1 ? s1 : s0) = fmaf(-w.A[e + i][e + l], x[l], l & 1 ? s1 : s0);
+        for (int l = 0; l < i; ++l) (l & 1 ? s1 : s0) = fmaf(-A[e + i][e + l], x[l], l & 1 ? s1 : s0);
         x[i] = s0 + s1;
       }
       __syncwarp(0xFFFF);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w.A[e + i][e + c] = x[i];
+      for (int i = 0; i < 8; ++i) A[e + i][e + c] = x[i];
     }
     __syncwarp();
     {  // 8 -> 16: two columns of a row per thread
@@ -248,63 +254,69 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       float2 m = f2b(0.0f);
 #pragma unroll
       for (int l = 0; l < 8; ++l)
-        m = __ffma2_rn(f2b(w.A[d + 8 + r][d + l]), *reinterpret_cast<const float2*>(&w.A[d + l][d + c]), m);
+        m = __ffma2_rn(f2b(A[d + 8 + r][d + l]), *reinterpret_cast<const float2*>(&A[d + l][d + c]), m);
       float* M = &w.M[wp * 8][0];
       *reinterpret_cast<float2*>(M + r * 36 + c) = m;
       __syncwarp();
       m = f2b(0.0f);
 #pragma unroll
       for (int l = 0; l < 8; ++l)
-        m = __ffma2_rn(f2b(-w.A[d + 8 + r][d + 8 + l]), *reinterpret_cast<const float2*>(M + l * 36 + c), m);
-      *reinterpret_cast<float2*>(&w.A[d + 8 + r][d + c]) = m;
+        m = __ffma2_rn(f2b(-A[d + 8 + r][d + 8 + l]), *reinterpret_cast<const float2*>(M + l * 36 + c), m);
+      *reinterpret_cast<float2*>(&A[d + 8 + r][d + c]) = m;
     }
     // 16 -> 32: a pair of warps, a 16 x 8 tile each
     bar_sync(1 + (wp >> 1), 64);
     {
       const int e = (wp >> 1) * 32, c = (wp & 1) * 8;
       float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      warp_mma_split<16>(m, &w.A[e + 16][e], TC + 4, &w.A[e][e + c], TC + 4, lane);
+      warp_mma_split<16>(m, &A[e + 16][e], TC + 4, &A[e][e + c], TC + 4, lane);
       float* M = &w.M[e >> 1][c];  // (a tile's columns are its own warp's)
       warp_mma_store(m, M, 36, lane, 1.0f);
       bar_sync(1 + (wp >> 1), 64);  // both warps have read C
       m[0] = m[1] = m[2] = m[3] = 0.0f;
-      warp_mma_split<16>(m, &w.A[e + 16][e + 16], TC + 4, M, 36, lane);
-      warp_mma_store(m, &w.A[e + 16][e + c], TC + 4, lane, -1.0f);
+      warp_mma_split<16>(m, &A[e + 16][e + 16], TC + 4, M, 36, lane);
+      warp_mma_store(m, &A[e + 16][e + c], TC + 4, lane, -1.0f);
     }
   }
   __syncthreads();
   {  // 32 -> 64: eight tiles of 16 x 8
     const int r = (wp & 1) * 16, c = (wp >> 1) * 8;
     float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    warp_mma_split<32>(m, &w.A[32 + r][0], TC + 4, &w.A[0][c], TC + 4, lane);
+    warp_mma_split<32>(m, &A[32 + r][0], TC + 4, &A[0][c], TC + 4, lane);
     warp_mma_store(m, &w.M[r][c], 36, lane, 1.0f);
     __syncthreads();
     m[0] = m[1] = m[2] = m[3] = 0.0f;
-    warp_mma_split<32>(m, &w.A[32 + r][32], TC + 4, &w.M[0][c], 36, lane);
-    warp_mma_store(m, &w.A[32 + r][c], TC + 4, lane, -1.0f);
+    warp_mma_split<32>(m, &A[32 + r][32], TC + 4, &w.M[0][c], 36, lane);
+    warp_mma_store(m, &A[32 + r][c], TC + 4, lane, -1.0f);
   }
   __syncthreads();
-  {  // T as hi and lo: a quarter row per thread
+  {  // T as hi and lo in place of A: a quarter row per thread
     const int r = pt >> 2, u0 = (pt & 3) * 2;
+    float4 x[4];
 #pragma unroll
-    for (int u = u0; u < u0 + 2; ++u) {
-      const float4 a = *reinterpret_cast<const float4*>(&w.A[r][u * 8]), b = *reinterpret_cast<const float4*>(&w.A[r][u * 8 + 4]);
+    for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4*>(&A[r][u0 * 8 + u * 4]);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
       uint4 h, l;
-      split2(a.x, a.y, h.x, l.x);
-      split2(a.z, a.w, h.y, l.y);
-      split2(b.x, b.y, h.z, l.z);
-      split2(b.z, b.w, h.w, l.w);
-      const uint32_t at = sw(r, u);
-      *reinterpret_cast<uint4*>(tp.t_hi + at) = h;
-      *reinterpret_cast<uint4*>(tp.t_lo + at) = l;
+      split2(x[2 * u].x, x[2 * u].y, h.x, l.x);
+      split2(x[2 * u].z, x[2 * u].w, h.y, l.y);
+      split2(x[2 * u + 1].x, x[2 * u + 1].y, h.z, l.z);
+      split2(x[2 * u + 1].z, x[2 * u + 1].w, h.w, l.w);
+      const uint32_t at = sw(r, u0 + u);
+      *reinterpret_cast<uint4*>(t_hi + at) = h;
+      *reinterpret_cast<uint4*>(t_lo + at) = l;
     }
   }
   fence_proxy_async();
   __syncthreads();
   if (pt == 0) {
     if (wait.ok) {
+      unsigned char* dst = a.tp + (size_t)blockIdx.x * a.tp_stride;
       asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
-                   ::"l"(a.tp + (size_t)blockIdx.x * a.tp_stride), "r"(kq), "r"((uint32_t)sizeof(TcPrep)) : "memory");
+                   ::"l"(dst), "r"(kq), "r"(2 * TILE) : "memory");
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                   ::"l"(dst + 2 * TILE), "r"(kq + PV), "r"(PV_BYTES) : "memory");
       bulk_commit();
       bulk_wait_read();
     }
