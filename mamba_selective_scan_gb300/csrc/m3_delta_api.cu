@@ -45,12 +45,12 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
   return M3_OK;
 }
 
-// Time segments of the tensor-core forward.  A block per (head, segment) runs
-// one chunk in a unit of time (about 2 us); with S segments, first the S - 1
-// earlier ones run twice without outputs (from zero and from the identity,
-// about 3/4 of a unit per chunk), then a kernel chains them (about half a
-// unit per segment and three for its launch), then all S run.  The count
-// with the least total is taken, with at least four chunks per segment.
+// Time segments of the tensor-core chains.  A block per (head, segment) runs
+// one chunk in a unit of time (3.2 us in the forward); with S segments, first
+// the S - 1 earlier ones run twice without outputs (from zero and from the
+// identity, 3/4 of a unit per chunk), then a kernel chains them (2/3 of a
+// unit per segment and two for its launch), then all S run.  The count with
+// the least total is taken, with at least four chunks per segment.
 void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
   constexpr int64_t SMS = 152;
   double best = 0.0;
@@ -61,7 +61,7 @@ void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
     const double fin = (double)((heads * S + SMS - 1) / SMS) * m;
-    const double agg = S > 1 ? (double)((heads * (S - 1) * 2 + SMS - 1) / SMS) * m * 0.75 + 0.5 * S + 3.0 : 0.0;
+    const double agg = S > 1 ? (double)((heads * (S - 1) * 2 + SMS - 1) / SMS) * m * 0.75 + 0.67 * S + 2.0 : 0.0;
     if (want == 1 || fin + agg < best - 1e-9) {
       best = fin + agg;
       *segs = S;

@@ -165,7 +165,6 @@ __device__ __forceinline__ void tc_mma_kq(uint32_t kq, uint32_t acc, uint64_t* m
   }
   tc_commit(mbk);
 }
-__device__ __forceinline__ float exp_neg(float d) { return ex2(d * LOG2E); }
 // Which (head, chunk) a block works on at each step.  Either one run of
 // chunks of one head (a time segment), or, when there are more heads than
 // SMs, an equal share of all chunks of all heads: block s of G has the range

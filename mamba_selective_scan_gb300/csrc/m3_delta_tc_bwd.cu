@@ -449,16 +449,16 @@ constexpr int SMALL = DR + 32768;
 constexpr int P2 = DS + 32768, A2 = P2 + 2 * TILE;
 
 struct Smem {  // at SMALL
-  float gam[TC], beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC];
+  float gam[TC], beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC], d[TC], z[TC];
   float ss[4][2 * TC];
   float row_p[4][TC], col_p[2][TC];  // sums of dP o P: per column quarter, per warp
   float col_a[4][TC], row_a[2][TC];  // sums of dA o A (row_a without beta)
   float dot[3][4][TC];               // Q.(dO S0^T), K.(dR S0^T), K.(U dS^T): per warp of 32 head_k
-  float red[16];
+  float red[2][16];  // (by turns: the next item's may be written before this one's are summed)
   float ec, tot;
   uint64_t ds, dl, us, kq;           // arrived: dS hi; dS lo; U, dR, dO, S0; K, Q
-  uint64_t mb0, mb1, mb2, mb3;       // done: Z; G, dP, K Q^T; Yo, Y; the products with P2 and A2
-  uint64_t rdy0, rdy1, rdy2;
+  uint64_t mb1, mb2, mb3;            // done: K Q^T (and all before it); G, dP, Yo, Y, Z; the products with P2 and A2
+  uint64_t rdy0, rdy1, rdya, rdy2;   // see the issuing warp
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -543,8 +543,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   const uint32_t sb = smem_u32(base);
 
   if (tid == 0) {
-    for (uint64_t* r : {&s.ds, &s.dl, &s.us, &s.kq, &s.mb0, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy0, &s.rdy1, &s.rdy2}) mbar_init(r, EPI / 32);
+    for (uint64_t* r : {&s.ds, &s.dl, &s.us, &s.kq, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy0, &s.rdy1, &s.rdya, &s.rdy2}) mbar_init(r, EPI / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -597,39 +597,54 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       load_ds(it);
       load_dl(it);
       load_kq(it);
-      for (uint32_t par = 0; it.group < groups; par ^= 1) {
-        it.next(a);
-        const bool more = it.group < groups;
+      uint32_t pkq = 0;
+      for (uint32_t n = 0; it.group < groups; ++n) {
+        const uint32_t par = n & 1;
+        const int m = it.m;
+        // while the last item's outputs are still being written
         wait(&s.us, par);
         wait(&s.ds, par);
-        wait(&s.dl, par);
+        if (n > 0) wait(&s.rdya, par ^ 1);  // its G, dP, Yo, Y and Z are read
         if (wait.ok) {
           tmem_fence_after_sync();
-          mma(T_Z, 8, MM, true, kept(DS), kept(U));
-          mma(T_Z, 8, MM, false, kept(DS), kept(U + 16384));
-          mma(T_Z, 8, MM, false, kept(DS + 32768), kept(U));
-          tc_commit(&s.mb0);
-        }
-        wait(&s.kq, par);
-        if (wait.ok) {
-          mma(T_KQ, 8, NN, true, kmaj(KQ, 2 * TILE), kmaj(KQ, 2 * TILE));
           mma(T_G, 8, MM, true, kept(U), kept(DR));
           mma(T_G, 8, MM, false, kept(U + 16384), kept(DR));
           mma(T_G, 8, MM, false, kept(U), kept(DR + 16384));
           mma(T_DP, 8, NM, true, kmaj(DO - TILE, TILE), kept(U));
           mma(T_DP, 8, NM, false, kmaj(DO - TILE, TILE), kept(U + 16384));
-          tc_commit(&s.mb1);
+          mma(T_Z, 8, MM, true, kept(DS), kept(U));
+          mma(T_Z, 8, MM, false, kept(DS), kept(U + 16384));
           mma(T_YO, 8, MN, true, kept(S0), kmaj(DO, TILE));
           mma(T_Y, 8, MM, true, kept(S0), kept(DR));
           mma(T_Y, 8, MM, false, kept(S0), kept(DR + 16384));
+        }
+        if (n > 0) {
+          wait(&s.rdy2, par ^ 1);  // its K and Q are read
+          if (m == 0 && wait.ok) load_kq(it);  // (else they are this item's too)
+        }
+        wait(&s.dl, par);
+        if (wait.ok) {
+          mma(T_Z, 8, MM, false, kept(DS + 32768), kept(U));
           tc_commit(&s.mb2);
         }
+        if (m == 0) {
+          wait(&s.kq, pkq);
+          pkq ^= 1;
+          if (wait.ok) {
+            tmem_fence_after_sync();
+            mma(T_KQ, 8, NN, true, kmaj(KQ, 2 * TILE), kmaj(KQ, 2 * TILE));
+          }
+        }
+        if (wait.ok) tc_commit(&s.mb1);
+        it.next(a);
+        const bool more = it.group < groups;
         // the next item's tiles as soon as this one's have been read
-        wait(&s.mb0, par);
-        wait(&s.rdy0, par);  // the inner product has read S0 and dS
-        if (more && wait.ok) load_ds(it);
         wait(&s.mb2, par);
-        if (more && wait.ok) load_us(it);
+        wait(&s.rdy0, par);  // the inner product has read S0 and dS
+        if (more && wait.ok) {
+          load_us(it);
+          load_ds(it);
+        }
         wait(&s.rdy1, par);  // P2 and A2 are in place
         if (wait.ok) {
           tmem_fence_after_sync();
@@ -643,8 +658,6 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         }
         wait(&s.mb3, par);
         if (more && wait.ok) load_dl(it);
-        wait(&s.rdy2, par);  // K, Q and the accumulators are read
-        if (more && wait.ok) load_kq(it);
       }
       if (!wait.ok) {  // as in the other kernels: copies in flight land first
         if (n_ds) mbar_wait(&s.ds, (n_ds - 1) & 1);
@@ -669,14 +682,14 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(el + q * TILE + sw(qt * 16 + j, (row & 63) >> 3)));
       return __uint_as_float((uint32_t)v << 16);
     };
-    uint32_t par = 0;
+    uint32_t par = 0, pkq = 0;
     for (GradItem it(a, blockIdx.x); it.group < groups; it.next(a), par ^= 1) {
       const int c = it.c, b = it.b, h = it.h;
       const int64_t tok0 = (int64_t)b * a.T + c * TC;  // the chunk's first token
       const int n = min(TC, a.T - c * TC);
-      float g = 0.0f, beta = 0.0f;
+      float g = 0.0f, beta = 0.0f;  // (g in powers of two)
       if (tid < n) {
-        g = clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
+        g = LOG2E * clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
         beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[(tok0 + tid) * a.Hv + h]);
       }
       // <dS, S0>
@@ -700,10 +713,13 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
-        if (lane == 0) s.red[warp] = acc;
+        if (lane == 0) s.red[par][warp] = acc;
       }
       ready(&s.rdy0);
-      wait(&s.kq, par);
+      if (it.m == 0) {
+        wait(&s.kq, pkq);
+        pkq ^= 1;
+      }
       if (L2) {
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
@@ -736,7 +752,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         s.beta[tid] = beta;
         const float nk = L2 ? rsqrtf((s.ss[0][tid] + s.ss[1][tid]) + (s.ss[2][tid] + s.ss[3][tid]) + DELTA_L2_EPS) : 1.0f;
         const float nq = L2 ? rsqrtf((s.ss[0][TC + tid] + s.ss[1][TC + tid]) + (s.ss[2][TC + tid] + s.ss[3][TC + tid]) + DELTA_L2_EPS) : 1.0f;
-        const float eg = exp_neg(g);
+        const float eg = ex2(g);
         s.eg[tid] = eg;
         s.nk[tid] = nk;
         s.nq[tid] = nq;
@@ -745,59 +761,73 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       }
       bar_sync(1, EPI);
       if (warp < 2) {
-        s.fu[tid] = exp_neg(s.gam[TC - 1] - g) * s.nk[tid];
-        if (tid == 0) s.ec = exp_neg(s.gam[TC - 1]);
+        s.fu[tid] = ex2(s.gam[TC - 1] - g) * s.nk[tid];
+        if (tid == 0) s.ec = ex2(s.gam[TC - 1]);
       }
       wait(&s.mb1, par);
       tmem_fence_after_sync();
       {
         const int r = row & (TC - 1), c0 = qt * 16;
-        const float gr = s.gam[r];
-        float v[16], k[16];
+        const float2 gr = f2b(s.gam[r]);
+        const Vec16 gc{&s.gam[c0]}, nc{&s.nk[c0]}, bc{&s.beta[c0]};
+        float2 v[8], k[8];
+        float sum[16];
         unsigned char* tile = base + grad::P2;
         if (wq < 2) {  // G^T: row j = r, columns i
           tc_ld16(tl + T_G, v);
           tc_ld16(tl + T_KQ, k);
-          const float nj = s.nk[r];
-          float col = 0.0f;
+          if (r >> 4 == qt) {
 #pragma unroll
-          for (int m = 0; m < 16; ++m) {
-            const int i = c0 + m;
-            if (i == r) s.gd[r] = v[m];
-            const float x = i > r ? -v[m] * exp_neg(s.gam[i] - gr) * nj * s.nk[i] : 0.0f;  // dA o D
-            const float be = s.beta[i];
-            v[m] = x * be;
-            k[m] *= x;
-            col = fmaf(k[m], be, col);
+            for (int m = 0; m < 16; ++m)
+              if (c0 + m == r) s.gd[r] = m & 1 ? v[m >> 1].y : v[m >> 1].x;
           }
-          s.col_a[qt][r] = col;
-          const float t = reduce16(k, lane);
+          const float2 f = f2b(-s.nk[r]);
+          float2 col = f2b(0.0f);
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {
+            const float2 e = ex2x2(__ffma2_rn(gr, f2b(-1.0f), gc[m]));
+            float2 x = __fmul2_rn(__fmul2_rn(__fmul2_rn(nc[m], f), e), v[m]);  // dA o D
+            x.x = c0 + 2 * m > r ? x.x : 0.0f;
+            x.y = c0 + 2 * m + 1 > r ? x.y : 0.0f;
+            v[m] = __fmul2_rn(x, bc[m]);
+            k[m] = __fmul2_rn(k[m], x);
+            col = __ffma2_rn(k[m], bc[m], col);
+            sum[2 * m] = k[m].x;
+            sum[2 * m + 1] = k[m].y;
+          }
+          s.col_a[qt][r] = col.x + col.y;
+          const float t = reduce16(sum, lane);
           if (!(lane & 1)) s.row_a[wq][c0 + (lane >> 1)] = t;
           tile += 2 * TILE;
         } else {  // dP: row i = r, columns j
           tc_ld16(tl + T_DP, v);
           tc_ld16(tl + T_KQ, k);
-          const float f = a.scale * s.nq[r];
-          float rs = 0.0f;
+          const float2 f = f2b(a.scale * s.nq[r]);
+          float2 rs = f2b(0.0f);
 #pragma unroll
-          for (int m = 0; m < 16; ++m) {
-            const int j = c0 + m;
-            v[m] = j <= r ? v[m] * f * exp_neg(gr - s.gam[j]) * s.nk[j] : 0.0f;
-            k[m] *= v[m];
-            rs += k[m];
+          for (int m = 0; m < 8; ++m) {
+            const float2 e = ex2x2(__ffma2_rn(gc[m], f2b(-1.0f), gr));
+            float2 x = __fmul2_rn(__fmul2_rn(__fmul2_rn(nc[m], f), e), v[m]);
+            x.x = c0 + 2 * m <= r ? x.x : 0.0f;
+            x.y = c0 + 2 * m + 1 <= r ? x.y : 0.0f;
+            v[m] = x;
+            k[m] = __fmul2_rn(k[m], x);
+            rs = __fadd2_rn(rs, k[m]);
+            sum[2 * m] = k[m].x;
+            sum[2 * m + 1] = k[m].y;
           }
-          s.row_p[qt][r] = rs;
-          const float t = reduce16(k, lane);
+          s.row_p[qt][r] = rs.x + rs.y;
+          const float t = reduce16(sum, lane);
           if (!(lane & 1)) s.col_p[wq - 2][c0 + (lane >> 1)] = t;
         }
-        wait(&s.mb0, par);  // dS is read (so has the inner product, two barriers ago)
+        wait(&s.mb2, par);  // dS is read (so has the inner product, two barriers ago)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint4 hi, lo;
-          split2(v[8 * u], v[8 * u + 1], hi.x, lo.x);
-          split2(v[8 * u + 2], v[8 * u + 3], hi.y, lo.y);
-          split2(v[8 * u + 4], v[8 * u + 5], hi.z, lo.z);
-          split2(v[8 * u + 6], v[8 * u + 7], hi.w, lo.w);
+          split2(v[4 * u], hi.x, lo.x);
+          split2(v[4 * u + 1], hi.y, lo.y);
+          split2(v[4 * u + 2], hi.z, lo.z);
+          split2(v[4 * u + 3], hi.w, lo.w);
           const uint32_t at = sw(r, qt * 2 + u);
           *reinterpret_cast<uint4*>(tile + at) = hi;
           *reinterpret_cast<uint4*>(tile + TILE + at) = lo;
@@ -808,72 +838,82 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       // the products with the states, and their rows' dots with Q and K
       wait(&s.mb2, par);
       tmem_fence_after_sync();
-      float dq[16], dk[16];
+      float2 dq[8], dk[8];
       {
         float y[16];
+        float2 x[8], kv[8];
         tc_ld16(tl + T_YO, dq);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = dq[j] * tok(1, j);
+        for (int j = 0; j < 8; ++j) {
+          const float2 p = __fmul2_rn(dq[j], make_float2(tok(1, 2 * j), tok(1, 2 * j + 1)));
+          y[2 * j] = p.x;
+          y[2 * j + 1] = p.y;
+        }
         float t = reduce16(y, lane);
         if (!(lane & 1)) s.dot[0][wq][qt * 16 + (lane >> 1)] = t;
-        float x[16];
         tc_ld16(tl + T_Y, dk);
         tc_ld16(tl + T_Z, x);
-        float kv[16];
+        ready(&s.rdya);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) kv[j] = tok(0, j);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = dk[j] * kv[j];
+        for (int j = 0; j < 8; ++j) {
+          kv[j] = make_float2(tok(0, 2 * j), tok(0, 2 * j + 1));
+          const float2 p = __fmul2_rn(dk[j], kv[j]);
+          y[2 * j] = p.x;
+          y[2 * j + 1] = p.y;
+        }
         t = reduce16(y, lane);
         if (!(lane & 1)) s.dot[1][wq][qt * 16 + (lane >> 1)] = t;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) y[j] = x[j] * kv[j];
+        for (int j = 0; j < 8; ++j) {
+          const float2 p = __fmul2_rn(x[j], kv[j]);
+          y[2 * j] = p.x;
+          y[2 * j + 1] = p.y;
+        }
         t = reduce16(y, lane);
         if (!(lane & 1)) s.dot[2][wq][qt * 16 + (lane >> 1)] = t;
         bar_sync(1, EPI);
+        const Vec16 fq{&s.fq[qt * 16]}, fu{&s.fu[qt * 16]}, bx{&s.bfx[qt * 16]};
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int i = qt * 16 + j;
-          dq[j] *= s.fq[i];
-          dk[j] = fmaf(s.fu[i], x[j], -s.bfx[i] * dk[j]);
+        for (int j = 0; j < 8; ++j) {
+          dq[j] = __fmul2_rn(dq[j], fq[j]);
+          dk[j] = __ffma2_rn(fu[j], x[j], __fmul2_rn(__fmul2_rn(dk[j], f2b(-1.0f)), bx[j]));
         }
       }
-      if (warp == 0) {  // per-token sums: dg, dbeta and the normalisations' parts
-        float d[2], w = 0.0f;
+      if (warp < 2) {  // per-token sums: dbeta, the normalisations' parts, the exponent's share
+        const int i = tid;
+        float dot[3];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = lane + 32 * e;
-          float dot[3];
-#pragma unroll
-          for (int m = 0; m < 3; ++m) dot[m] = (s.dot[m][0][i] + s.dot[m][1][i]) + (s.dot[m][2][i] + s.dot[m][3][i]);
-          const float rp = (s.row_p[0][i] + s.row_p[1][i]) + (s.row_p[2][i] + s.row_p[3][i]), cp = s.col_p[0][i] + s.col_p[1][i];
-          const float ca = (s.col_a[0][i] + s.col_a[1][i]) + (s.col_a[2][i] + s.col_a[3][i]), rah = s.row_a[0][i] + s.row_a[1][i];
-          const float be = s.beta[i], ra = be * rah;
-          const float yo = s.fq[i] * dot[0], y = s.bfx[i] * dot[1], z = s.fu[i] * dot[2];
-          s.cq[i] = L2 ? s.nq[i] * s.nq[i] * (yo + rp) : 0.0f;
-          s.ck[i] = L2 ? s.nk[i] * s.nk[i] * (z - y + cp + ra + ca) : 0.0f;
-          d[e] = (rp - cp) + (ra - ca) + yo - y - z;
-          w += z;
-          if (i < n) {
-            float db = s.gd[i] / be;
-            if (!(fabsf(be) > 1e-20f)) {
-              // U holds nothing of a token that writes nothing: from
-              // dR.(v - e^gam S0^T k) - (below the diagonal of D K K^T) G
-              const unsigned char* dr = a.bwd + it.at * TC_BWD + 65536;
-              const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (tok0 + i) * a.vs + (int64_t)h * a.DV;
-              float rv = 0.0f;
-              for (int m = 0; m < a.DV; ++m) {
-                const uint32_t at = (i >> 3) * 2048 + m * 16 + (i & 7) * 2;
-                const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + at)) +
-                                __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + 16384 + at));
-                rv = fmaf(x, __bfloat162float(vp[m]), rv);
-              }
-              db = rv - s.eg[i] * s.nk[i] * dot[1] + rah;
+        for (int m = 0; m < 3; ++m) dot[m] = (s.dot[m][0][i] + s.dot[m][1][i]) + (s.dot[m][2][i] + s.dot[m][3][i]);
+        const float rp = (s.row_p[0][i] + s.row_p[1][i]) + (s.row_p[2][i] + s.row_p[3][i]), cp = s.col_p[0][i] + s.col_p[1][i];
+        const float ca = (s.col_a[0][i] + s.col_a[1][i]) + (s.col_a[2][i] + s.col_a[3][i]), rah = s.row_a[0][i] + s.row_a[1][i];
+        const float be = s.beta[i], ra = be * rah;
+        const float yo = s.fq[i] * dot[0], y = s.bfx[i] * dot[1], z = s.fu[i] * dot[2];
+        s.cq[i] = L2 ? s.nq[i] * s.nq[i] * (yo + rp) : 0.0f;
+        s.ck[i] = L2 ? s.nk[i] * s.nk[i] * (z - y + cp + ra + ca) : 0.0f;
+        s.d[i] = (rp - cp) + (ra - ca) + yo - y - z;
+        s.z[i] = z;
+        if (i < n) {
+          float db = s.gd[i] / be;
+          if (!(fabsf(be) > 1e-20f)) {
+            // U holds nothing of a token that writes nothing: from
+            // dR.(v - e^gam S0^T k) - (below the diagonal of D K K^T) G
+            const unsigned char* dr = a.bwd + it.at * TC_BWD + 65536;
+            const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (tok0 + i) * a.vs + (int64_t)h * a.DV;
+            float rv = 0.0f;
+            for (int m = 0; m < a.DV; ++m) {
+              const uint32_t at = (i >> 3) * 2048 + m * 16 + (i & 7) * 2;
+              const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + at)) +
+                              __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(dr + 16384 + at));
+              rv = fmaf(x, __bfloat162float(vp[m]), rv);
             }
-            static_cast<__nv_bfloat16*>(a.dbeta)[(tok0 + i) * a.Hv + h] = __float2bfloat16_rn(db);
+            db = rv - s.eg[i] * s.nk[i] * dot[1] + rah;
           }
+          static_cast<__nv_bfloat16*>(a.dbeta)[(tok0 + i) * a.Hv + h] = __float2bfloat16_rn(db);
         }
-        float in = lane < 16 ? s.red[lane] : 0.0f;
+      }
+      bar_sync(1, EPI);
+      if (warp == EPI / 32 - 1) {  // dg: suffix sums, tokens lane and lane + 32
+        float d[2] = {s.d[lane], s.d[lane + 32]}, w = s.z[lane] + s.z[lane + 32], in = lane < 16 ? s.red[par][lane] : 0.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           w += __shfl_xor_sync(~0u, w, o);
@@ -894,22 +934,23 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           if (lane + 32 * e < n)
             static_cast<__nv_bfloat16*>(a.dg)[(tok0 + lane + 32 * e) * a.Hv + h] = __float2bfloat16_rn(d[e]);
       }
-      bar_sync(1, EPI);
       wait(&s.mb3, par);
       tmem_fence_after_sync();
       {
-        float x[16];
+        float2 x[8];
         tc_ld16(tl + T_DQ, x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) dq[j] += x[j];
+        for (int j = 0; j < 8; ++j) dq[j] = __fadd2_rn(dq[j], x[j]);
         tc_ld16(tl + T_DK, x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) dk[j] += x[j];
+        for (int j = 0; j < 8; ++j) dk[j] = __fadd2_rn(dk[j], x[j]);
         if (L2) {
+          const Vec16 cq{&s.cq[qt * 16]}, ck{&s.ck[qt * 16]};
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            dq[j] = fmaf(-s.cq[qt * 16 + j], tok(1, j), dq[j]);
-            dk[j] = fmaf(-s.ck[qt * 16 + j], tok(0, j), dk[j]);
+          for (int j = 0; j < 8; ++j) {
+            const float2 q = make_float2(-tok(1, 2 * j), -tok(1, 2 * j + 1)), k = make_float2(-tok(0, 2 * j), -tok(0, 2 * j + 1));
+            dq[j] = __ffma2_rn(cq[j], q, dq[j]);
+            dk[j] = __ffma2_rn(ck[j], k, dk[j]);
           }
         }
       }
@@ -922,15 +963,17 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 x = acc[j * EPI], y = acc[(4 + j) * EPI];
-            dq[4 * j] += x.x; dq[4 * j + 1] += x.y; dq[4 * j + 2] += x.z; dq[4 * j + 3] += x.w;
-            dk[4 * j] += y.x; dk[4 * j + 1] += y.y; dk[4 * j + 2] += y.z; dk[4 * j + 3] += y.w;
+            dq[2 * j] = __fadd2_rn(dq[2 * j], make_float2(x.x, x.y));
+            dq[2 * j + 1] = __fadd2_rn(dq[2 * j + 1], make_float2(x.z, x.w));
+            dk[2 * j] = __fadd2_rn(dk[2 * j], make_float2(y.x, y.y));
+            dk[2 * j + 1] = __fadd2_rn(dk[2 * j + 1], make_float2(y.z, y.w));
           }
         }
         if (it.m + 1 < a.share) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[j * EPI] = make_float4(dq[4 * j], dq[4 * j + 1], dq[4 * j + 2], dq[4 * j + 3]);
-            acc[(4 + j) * EPI] = make_float4(dk[4 * j], dk[4 * j + 1], dk[4 * j + 2], dk[4 * j + 3]);
+            acc[j * EPI] = make_float4(dq[2 * j].x, dq[2 * j].y, dq[2 * j + 1].x, dq[2 * j + 1].y);
+            acc[(4 + j) * EPI] = make_float4(dk[2 * j].x, dk[2 * j].y, dk[2 * j + 1].x, dk[2 * j + 1].y);
           }
           continue;
         }
@@ -943,8 +986,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 #pragma unroll
         for (int j = 0; j < 16; ++j, qp += a.dqs, kp += a.dks)
           if (j < left) {
-            *qp = __float2bfloat16_rn(dq[j]);
-            *kp = __float2bfloat16_rn(dk[j]);
+            *qp = __float2bfloat16_rn(j & 1 ? dq[j >> 1].y : dq[j >> 1].x);
+            *kp = __float2bfloat16_rn(j & 1 ? dk[j >> 1].y : dk[j >> 1].x);
           }
       }
     }

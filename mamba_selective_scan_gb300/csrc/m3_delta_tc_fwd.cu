@@ -490,43 +490,57 @@ bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, 
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
 // start[s], 16 columns of the state per block, a row and four columns per
-// thread, f32.  rev: the adjoint's, from the last segment to the first.  A
-// segment is one pass over its Phi (64 KB, from L2) and bound by the latency
-// of those loads, 32 at a time; few heads are what makes segments, so blocks
-// are kept small.
+// thread, f32.  rev: the adjoint's, from the last segment to the first.  The
+// segments' Phi (64 KB each) do not depend on the states, so each arrives by
+// one bulk copy while the one before is used.
+constexpr int SEG_PHI = DMAX * DMAX * 4;
+constexpr size_t SEG_SMEM = 2 * SEG_PHI + 128;
 __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
+  extern __shared__ __align__(128) unsigned char raw[];
   __shared__ __align__(16) float S[DMAX][16];
+  __shared__ __align__(8) uint64_t full[2];
   const int tid = threadIdx.x, bh = blockIdx.x, k = tid & (DMAX - 1), vq = (tid >> 7) * 4, v = blockIdx.y * 16 + vq;
+  auto where = [&](int n) { return ((size_t)bh * a.segs + (rev ? a.segs - 1 - n : n)) * DMAX * DMAX; };
+  auto load = [&](int n) {
+    if (n + 1 >= a.segs) return;
+    mbar_expect_tx(&full[n & 1], SEG_PHI);
+    bulk_load(smem_u32(raw) + (n & 1) * SEG_PHI, a.seg_phi + where(n), SEG_PHI, &full[n & 1]);
+  };
+  if (tid == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    mbar_init_fence();
+    load(0);
+    load(1);
+  }
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (first && k < a.DK && v < a.DV) x = *reinterpret_cast<const float4*>(first + ((size_t)bh * a.DK + k) * a.DV + v);
   *reinterpret_cast<float4*>(&S[k][vq]) = x;
+  TcWait wait;
   for (int n = 0; n + 1 < a.segs; ++n) {
-    const int sg = rev ? a.segs - 1 - n : n, to = rev ? sg - 1 : sg + 1;
-    const size_t at = ((size_t)bh * a.segs + sg) * DMAX * DMAX;
-    x = *reinterpret_cast<const float4*>(a.seg_end + at + (size_t)k * DMAX + v);
-    const float* phi = a.seg_phi + at + k;  // Phi[r][k]
+    x = *reinterpret_cast<const float4*>(a.seg_end + where(n) + (size_t)k * DMAX + v);
     __syncthreads();
-#pragma unroll 1
-    for (int r0 = 0; r0 < DMAX; r0 += 32) {
-      float p[32];
-#pragma unroll
-      for (int r = 0; r < 32; ++r)  // (volatile: all of them before the first use)
-        asm volatile("ld.global.f32 %0, [%1];" : "=f"(p[r]) : "l"(phi + (size_t)(r0 + r) * DMAX) : "memory");
-#pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        const float4 y = *reinterpret_cast<const float4*>(&S[r0 + r][vq]);
-        x.x = fmaf(p[r], y.x, x.x); x.y = fmaf(p[r], y.y, x.y);
-        x.z = fmaf(p[r], y.z, x.z); x.w = fmaf(p[r], y.w, x.w);
-      }
+    wait(&full[n & 1], (n >> 1) & 1);
+    const float* phi = reinterpret_cast<const float*>(raw + (n & 1) * SEG_PHI) + k;  // Phi[r][k]
+#pragma unroll 16
+    for (int r = 0; r < DMAX; ++r) {
+      const float4 y = *reinterpret_cast<const float4*>(&S[r][vq]);
+      const float p = phi[r * DMAX];
+      x.x = fmaf(p, y.x, x.x); x.y = fmaf(p, y.y, x.y);
+      x.z = fmaf(p, y.z, x.z); x.w = fmaf(p, y.w, x.w);
     }
     __syncthreads();
+    if (tid == 0 && wait.ok) load(n + 2);
     *reinterpret_cast<float4*>(&S[k][vq]) = x;
-    *reinterpret_cast<float4*>(a.seg_start + ((size_t)bh * a.segs + to) * DMAX * DMAX + (size_t)k * DMAX + v) = x;
+    *reinterpret_cast<float4*>(a.seg_start + where(n + 1) + (size_t)k * DMAX + v) = x;
   }
+  if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
 }
 
 cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st) {
-  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), DMAX / 16), 512, 0, st, false, a, first, rev);
+  const cudaError_t e = cudaFuncSetAttribute(m3_delta_seg_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SEG_SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), DMAX / 16), 512, SEG_SMEM, st, false, a, first, rev);
 }
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
