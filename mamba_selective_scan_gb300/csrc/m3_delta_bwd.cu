@@ -10,7 +10,9 @@ constexpr int LD = DMAX + 4;  // row length of the [C][128] arrays: float4 colum
 constexpr int LS = C + 1;     // row length of the [C][C] arrays
 
 struct DeltaBwdSmem {
-  float K[C][LD], Q[C][LD], E[C][LD], dO[C][LD], U[C][LD], dU[C][LD], dR[C][LD];
+  float K[C][LD], Q[C][LD], dO[C][LD];
+  float U[C][LD], dR[C][LD];  // side by side: half of S0's rows fit in their place before they are made,
+  float E[C][LD], dU[C][LD];  // and in that of these two when they are used up
   float dS[DMAX][LD];
   float A[C][LS], P[C][LS], Ti[C][LS], X[C][LS];
   float gam[C], beta[C], nq[C], nk[C], dgam[C], dbeta[C], eg[C], el[C];
@@ -109,9 +111,17 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_kernel(const __grid_constant
       }
     }
     __syncthreads();
+    auto half_of_S0 = [&](float (*to)[LD], int half) {  // 64 rows
+      for (int i = tid; i < 64 * (DMAX / 4); i += 256) {
+        const int k = i >> 5, v = (i & 31) * 4, kk = half * 64 + k;
+        *reinterpret_cast<float4*>(&to[k][v]) =
+            kk < a.DK && v < a.DV ? __ldg(reinterpret_cast<const float4*>(S0 + (size_t)kk * a.DV + v)) : make_float4(0, 0, 0, 0);
+      }
+    };
     // A, P (row i of a warp, column j = lane), and E -= e^gam (K S0)
+    float kk[4] = {0, 0, 0, 0};  // k_i.k_j
     {
-      float kk[4] = {0, 0, 0, 0}, qk[4] = {0, 0, 0, 0};
+      float qk[4] = {0, 0, 0, 0};
       for (int c = 0; c < DMAX; c += 4) {
         const float4 kj = f4(&s.K[lane][c]);
 #pragma unroll
@@ -128,22 +138,33 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_kernel(const __grid_constant
         s.A[r][lane] = lane < r ? s.beta[r] * D * kk[i] : 0.0f;
       }
       float4 acc[4] = {};
-      if (c0 < a.DV)
-        for (int k = 0; k < a.DK; ++k) {
-          const float4 sv = __ldg(reinterpret_cast<const float4*>(S0 + (size_t)k * a.DV + c0));
+      float (*S0h)[LD] = s.U;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        half_of_S0(S0h, half);
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < 64; ++k) {
+          const float4 sv = f4(&S0h[k][c0]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) axpy4(acc[i], s.K[r0 + i][k], sv);
+          for (int i = 0; i < 4; ++i) axpy4(acc[i], s.K[r0 + i][half * 64 + k], sv);
         }
+        __syncthreads();
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) axpy4(*reinterpret_cast<float4*>(&s.E[r0 + i][c0]), -s.eg[r0 + i], acc[i]);
     }
     __syncthreads();
     // T = (I + A)^-1 by forward substitution, a column per lane
     if (warp == 0) {
+      float x[C];
+#pragma unroll
       for (int i = 0; i < C; ++i) {
-        float t = i == lane ? 1.0f : 0.0f;
-        for (int l = 0; l < i; ++l) t = fmaf(-s.A[i][l], l >= lane ? s.Ti[l][lane] : 0.0f, t);
-        s.Ti[i][lane] = t;
+        float t0 = i == lane ? 1.0f : 0.0f, t1 = 0.0f;
+#pragma unroll
+        for (int l = 0; l < i; ++l) (l & 1 ? t1 : t0) = fmaf(-s.A[i][l], x[l], l & 1 ? t1 : t0);
+        x[i] = t0 + t1;
+        s.Ti[i][lane] = x[i];
       }
     }
     __syncthreads();
@@ -215,9 +236,7 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_kernel(const __grid_constant
         const float xa = lane < r ? -da[i] : 0.0f, xp = lane <= r ? dp[i] : 0.0f;
         const float ma = xa * s.A[r][lane], mp = xp * s.P[r][lane];
         // A carries beta_r: its derivative is taken with A / beta_r = D k_r.k_j
-        float kk = 0.0f;
-        for (int c = 0; c < DMAX; c += 4) kk = dot4(f4(&s.K[r][c]), f4(&s.K[lane][c]), kk);
-        const float db = wsum(xa * D * kk);
+        const float db = wsum(xa * D * kk[i]);
         const float row = wsum(ma + mp);
         if (lane == 0) {
           s.dbeta[r] += db;
@@ -240,24 +259,30 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_kernel(const __grid_constant
     float wtot = 0.0f;
     {
       float os[4][4] = {}, us[4][4] = {}, rs[4][4] = {};
-      for (int v = 0; v < a.DV; v += 4) {
-        float4 sv[4], dv[4];
+      float (*S0h)[LD] = s.E;  // 64 rows of S0 at a time
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int k = lane + 32 * m;
-          sv[m] = k < a.DK ? __ldg(reinterpret_cast<const float4*>(S0 + (size_t)k * a.DV + v)) : make_float4(0, 0, 0, 0);
-          dv[m] = f4(&s.dS[k][v]);
-        }
+      for (int half = 0; half < 2; ++half) {
+        half_of_S0(S0h, half);
+        __syncthreads();
+        for (int v = 0; v < a.DV; v += 4) {
+          float4 sv[2], dv[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 o = f4(&s.dO[r0 + i][v]), u = f4(&s.U[r0 + i][v]), r = f4(&s.dR[r0 + i][v]);
+          for (int m = 0; m < 2; ++m) {
+            sv[m] = f4(&S0h[lane + 32 * m][v]);
+            dv[m] = f4(&s.dS[half * 64 + lane + 32 * m][v]);
+          }
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            os[i][m] = dot4(o, sv[m], os[i][m]);
-            us[i][m] = dot4(u, dv[m], us[i][m]);
-            rs[i][m] = dot4(r, sv[m], rs[i][m]);
+          for (int i = 0; i < 4; ++i) {
+            const float4 o = f4(&s.dO[r0 + i][v]), u = f4(&s.U[r0 + i][v]), r = f4(&s.dR[r0 + i][v]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              os[i][half * 2 + m] = dot4(o, sv[m], os[i][half * 2 + m]);
+              us[i][half * 2 + m] = dot4(u, dv[m], us[i][half * 2 + m]);
+              rs[i][half * 2 + m] = dot4(r, sv[m], rs[i][half * 2 + m]);
+            }
           }
         }
+        __syncthreads();
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
