@@ -25,7 +25,7 @@ namespace m3 {
 constexpr int NORM_W_MAX = 16;        // warps that share a row, at most
 constexpr int NORM_DIM_MAX = 16384;   // dim % 8 == 0 and 16-byte aligned rows
 constexpr int NORM_DIM_MAX1 = 8192;   // any other dim
-constexpr int NORM_BWD_BLOCKS = 1216; // share rows of the backward's workspace, at most
+constexpr int NORM_BWD_BLOCKS = 912;  // share rows of the backward's workspace (and its blocks), at most
 
 struct NormArgs {
   const void *x, *dy;
@@ -365,30 +365,37 @@ cudaError_t launch_norm_fwd(NormArgs a, bool vec, cudaStream_t s) {
 
 template <typename T, typename X, int VEC>
 void (*bwd_kernel_nv(int nv))(const NormArgs) {
-  switch (nv) {
-    case 1: return m3_norm_bwd_kernel<T, X, VEC, 1>;
-    case 2: return m3_norm_bwd_kernel<T, X, VEC, 2>;
-    case 3: return m3_norm_bwd_kernel<T, X, VEC, 3>;
-    case 4: return m3_norm_bwd_kernel<T, X, VEC, 4>;
+  if constexpr (VEC == 1) {
+    if (nv == 4) return m3_norm_bwd_kernel<T, X, 1, 4>;
+    if (nv == 8) return m3_norm_bwd_kernel<T, X, 1, 8>;
+    return m3_norm_bwd_kernel<T, X, 1, 16>;
+  } else {
+    if (nv == 1) return m3_norm_bwd_kernel<T, X, VEC, 1>;
+    if (nv == 2) return m3_norm_bwd_kernel<T, X, VEC, 2>;
+    if (nv == 4) return m3_norm_bwd_kernel<T, X, VEC, 4>;
+    return m3_norm_bwd_kernel<T, X, VEC, 8>;
   }
-  if (nv <= 8) return m3_norm_bwd_kernel<T, X, VEC, 8>;
-  if (VEC == 1 && nv <= 16) return m3_norm_bwd_kernel<T, X, 1, 16>;
-  return nullptr;
 }
 
 template <typename T, typename X>
 cudaError_t launch_norm_bwd(NormArgs a, bool vec, cudaStream_t s) {
+  // 16-byte rows: the fewest vectors per thread, in as many warps as that
+  // takes (a thread keeps five values for each column: 16384 x 768 bf16 with
+  // its residual stream runs in 39 us with 6 warps x 1 vector, 47 us with 2 x
+  // 3).  Others: four columns per thread (4099 x 1003 f32: 16 us with 8 warps
+  // x 4, 25 us with 16 x 2, whose rows have too few loads in flight)
   int nv = 0, sms = 0, occ = 0;
-  const bool ok = vec ? norm_shape(a.dim, 4, 4, &a.wpr, &nv) || norm_shape(a.dim, 4, 8, &a.wpr, &nv)
-                      : norm_shape(a.dim, 1, 4, &a.wpr, &nv) || norm_shape(a.dim, 1, 8, &a.wpr, &nv) ||
-                            norm_shape(a.dim, 1, 16, &a.wpr, &nv);
-  if (!ok) return cudaErrorInvalidValue;
+  const int nvec = a.dim / (vec ? 4 : 1);
+  for (int n : {vec ? 1 : 4, vec ? 2 : 8, vec ? 4 : 16, 8})
+    if (!nv && nvec <= NORM_W_MAX * 32 * n) nv = n;
+  if (!nv) return cudaErrorInvalidValue;
+  a.wpr = (nvec + 32 * nv - 1) / (32 * nv);
+  if (a.wpr < 1) a.wpr = 1;
   const int R = a.wpr >= 8 ? 1 : 8 / a.wpr;
   const unsigned block = 32 * a.wpr * R;
-  // R > 1: at most 8 / W rows of W * 32 * 16 columns, 32 KB of shares
+  // R > 1: at most 8 / W rows of W * 32 * 4 columns (one vector per thread), 8 KB of shares
   const size_t smem = R > 1 ? (size_t)R * 2 * a.dim * 4 : 0;
   auto kern = vec ? bwd_kernel_nv<T, X, 4>(nv) : bwd_kernel_nv<T, X, 1>(nv);
-  if (!kern) return cudaErrorInvalidValue;
   cudaError_t e = sm_count(&sms);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, (int)block, smem);
   if (e != cudaSuccess) return e;
