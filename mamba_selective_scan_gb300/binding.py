@@ -699,13 +699,15 @@ def _call(name, args):
         raise M3Error(st, name)
 
 
-def _scratch(workspace, nbytes, torch, dev):
+def _scratch(workspace, nbytes, torch, dev, stream):
     """(address, bytes) of the caller's workspace or of a new one (whose
     status block nobody can query, so it need not start at zero), and what
     must stay alive until the call is enqueued."""
     if workspace is not None:
         return workspace.ptr, workspace.nbytes, workspace
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None:  # its memory is given up here, while that stream may still be using it
+        buf.record_stream(stream)
     return buf.data_ptr(), nbytes, buf
 
 
@@ -782,7 +784,7 @@ def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want
     elif want_bias:
         d_b = new(dim, dtype=f32, device=dev)
     dims, nbytes = _norm_sizes(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)), code)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev, stream)
     _call("m3scan_norm_bwd", (dims, code, dy.data_ptr(), normed.data_ptr(), ncode, weight.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), _ptr(d_residual_out), dx.data_ptr(), _ptr(d_res), d_w.data_ptr(),
                               _ptr(d_b), ws, nbytes, _stream_of(stream, torch, dev)))
@@ -864,7 +866,7 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
         _need(ckpt, "ckpt", f32, index, (n_ckpt,))
     elif want_ckpt:
         ckpt = torch.empty(n_ckpt, dtype=f32, device=dev)
-    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev, stream)
     _call("m3scan_delta_fwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                _ptr(state), o.data_ptr(), _ptr(state_out), _ptr(ckpt), ws, nbytes,
                                _stream_of(stream, torch, dev)))
@@ -894,7 +896,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _need(r["d_state"], "d_state", f32, index, sshape)
     _need(d_o, "d_o", dt, index, v.shape)
     _need(ckpt, "ckpt", f32, index, (n_ckpt,))
-    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev, stream)
     _call("m3scan_delta_bwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                ckpt.data_ptr(), d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(),
                                r["dk"].data_ptr(), r["dv"].data_ptr(), r["dg"].data_ptr(), r["dbeta"].data_ptr(),
