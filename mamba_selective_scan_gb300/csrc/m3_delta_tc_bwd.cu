@@ -36,7 +36,7 @@ constexpr int SMALL = VO + 4 * TILE;
 
 struct Smem {  // at SMALL
   uint64_t kq_full[2], v_full[2], mbx, mbz, mbu, mbd;
-  uint64_t rdy_s, rdy_r, rdy_u;  // one arrival per chain warp
+  uint64_t rdy_s, rdy_y, rdy_r, rdy_u;  // one arrival per chain warp
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -87,7 +87,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       mbar_init(&s.v_full[i], 1);
     }
     for (uint64_t* r : {&s.mbx, &s.mbz, &s.mbu, &s.mbd}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy_s, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_y, &s.rdy_r, &s.rdy_u}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -183,6 +183,17 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_idesc(128, 64, true, true), p + ks > 0);
           tc_commit(&s.mbz);
         }
+        wait(&s.rdy_y, par);
+        wait(&s.mbx, par);  // dS is read: its columns may be overwritten
+        if (wait.ok) {  // the update's first half, which needs no dR
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + T_S, tm + T_Y + p * 32 + ks * 8, tc_desc(st + TILE + ks * 2048, 2 * TILE, 1024),
+                        tc_idesc(128, 128, false, true), p + ks > 0);
+        }
         wait(&s.rdy_r, par);
         if (wait.ok) {
           tmem_fence_after_sync();
@@ -198,11 +209,11 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         if (wait.ok) {
           tmem_fence_after_sync();
 #pragma unroll
-          for (int p = 0; p < 4; ++p)
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              tc_mma_ts(tm + T_S, tm + (p < 2 ? T_R : T_Y) + (p & 1) * 32 + ks * 8,
-                        tc_desc(st + (p < 2 ? 0 : TILE) + ks * 2048, 2 * TILE, 1024), tc_idesc(128, 128, false, true), p + ks > 0);
+              tc_mma_ts(tm + T_S, tm + T_R + p * 32 + ks * 8, tc_desc(st + ks * 2048, 2 * TILE, 1024),
+                        tc_idesc(128, 128, false, true), true);
           tc_commit(&s.mbd);
         }
       }
@@ -276,24 +287,26 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
     };
     auto put_state = [&](const TcStep& t) {  // dS as hi, lo into tensor memory, and kept for the step's gradients
-      unsigned char* ck = AGG ? nullptr : a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + row * 16;
+      uint32_t hi[2][8], lo[2][8];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[k], lo[k]);
-        tc_st8(tl + T_S + qt * 32 + p * 16, hi);
-        tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
-        if (ck) {
+        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[p][k], lo[p][k]);
+        tc_st8(tl + T_S + qt * 32 + p * 16, hi[p]);
+        tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo[p]);
+      }
+      ready(&s.rdy_s);
+      if (!AGG) {
+        unsigned char* ck = a.bwd + ((size_t)t.bh * a.nc + chunk(t)) * TC_BWD + row * 16;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int o = (qt * 4 + p * 2 + u) * 2048;
-            *reinterpret_cast<uint4*>(ck + o) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-            *reinterpret_cast<uint4*>(ck + 32768 + o) = make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + o) = make_uint4(hi[p][4 * u], hi[p][4 * u + 1], hi[p][4 * u + 2], hi[p][4 * u + 3]);
+            *reinterpret_cast<uint4*>(ck + 32768 + o) = make_uint4(lo[p][4 * u], lo[p][4 * u + 1], lo[p][4 * u + 2], lo[p][4 * u + 3]);
           }
-        }
       }
-      ready(&s.rdy_s);
     };
     // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns; or
     // only into ck)
@@ -338,6 +351,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           x[j] = ident ? f2b(0.0f)
                        : __fmul2_rn(make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16)), fq[j]);
         put_tokens(T_Y, x, nullptr);
+        ready(&s.rdy_y);
       }
       wait(&s.mbx, par);
       wait(&s.mbz, par);

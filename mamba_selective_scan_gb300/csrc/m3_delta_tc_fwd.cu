@@ -25,15 +25,17 @@ namespace {
 constexpr int CHAIN = 512;                   // threads on the state: a row's columns in quarters
 constexpr int THREADS = CHAIN + 64;  // and a warp for the MMAs, one for the copies
 constexpr int KQ = 4 * TILE;      // one chunk's K/Q tiles; two stages
-constexpr int PREP = 2 * KQ;      // TcPrep, two stages
-constexpr int PREP_STAGE = 34 * 1024;
-constexpr int VO = PREP + 2 * PREP_STAGE;  // V, two stages of two tiles; a chunk's outputs take its V's place
-constexpr int SMALL = VO + 4 * TILE;
+constexpr int TP = 2 * KQ;        // T and P, two stages
+constexpr int TP_BYTES = (int)sizeof(TcTP);
+constexpr int VO = TP + 2 * TP_BYTES;  // V, two stages of two tiles
+constexpr int OUT = VO + 4 * TILE;     // a chunk's outputs, for the tile store
+constexpr int SMALL = OUT + 2 * TILE;
 
 struct Smem {  // at SMALL
+  TcVec vec[3];  // (a chunk's last use is in the next one's step)
   int bad[128];
-  uint64_t kq_full[2], v_full[2], mbx, mbq, mbu, mbd, mbo;
-  uint64_t rdy_s, rdy_o, rdy_r, rdy_u, rdy_v;  // one arrival per chain warp
+  uint64_t kq_full[2], v_full[2], mbx, mbq, mbu, mbd, mbo, o_free;
+  uint64_t rdy_s, rdy_q, rdy_o, rdy_r, rdy_u, rdy_v;  // one arrival per chain warp
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -95,8 +97,8 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       mbar_init(&s.kq_full[i], 1);
       mbar_init(&s.v_full[i], 1);
     }
-    for (uint64_t* r : {&s.mbx, &s.mbq, &s.mbu, &s.mbd, &s.mbo}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy_s, &s.rdy_o, &s.rdy_r, &s.rdy_u, &s.rdy_v}) mbar_init(r, CHAIN / 32);
+    for (uint64_t* r : {&s.mbx, &s.mbq, &s.mbu, &s.mbd, &s.mbo, &s.o_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_q, &s.rdy_o, &s.rdy_r, &s.rdy_u, &s.rdy_v}) mbar_init(r, CHAIN / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -116,8 +118,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         const int c = t.c, b = t.bh / a.Hv, hk = t.bh % a.Hv / a.share;
         const uint32_t st = st0 + (n & 1) * KQ;
         uint64_t* bar = &s.kq_full[n & 1];
+        const unsigned char* prep = a.tp + ((size_t)t.bh * a.nc + c) * a.tp_stride;
         mbar_expect_tx(bar, KQ + (uint32_t)sizeof(TcPrep));
-        bulk_load(st0 + PREP + (n & 1) * PREP_STAGE, a.tp + ((size_t)t.bh * a.nc + c) * a.tp_stride, (uint32_t)sizeof(TcPrep), bar);
+        bulk_load(st0 + TP + (n & 1) * TP_BYTES, prep, TP_BYTES, bar);
+        bulk_load(smem_u32(&s.vec[n % 3]), prep + TP_BYTES, (uint32_t)sizeof(TcVec), bar);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk) {
           tma_tile(st + blk * 2 * TILE, &mk, blk * 64, hk, c * TC, b, bar);
@@ -133,13 +137,13 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         for (int blk = 0; blk < 2; ++blk)
           tma_tile(st0 + VO + ((n & 1) * 2 + blk) * TILE, &mv, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv, &s.v_full[n & 1]);
       };
-      auto store = [&](int n) {  // a step's outputs, which the chain warps left in place of its inputs
-        if (AGG || !wait.ok) return;
+      auto store = [&](int n) {  // a step's outputs, which the chain warps left in OUT
+        if (!wait.ok) return;
         const TcStep t = walk.at(n);
 #pragma unroll
         for (int blk = 0; blk < 2; ++blk)
           if (blk * 64 < a.DV)
-            tma_tile_store(&mo, st0 + VO + ((n & 1) * 2 + blk) * TILE, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv);
+            tma_tile_store(&mo, st0 + OUT + blk * TILE, blk * 64, t.bh % a.Hv, t.c * TC, t.bh / a.Hv);
         bulk_commit();
         bulk_wait_read();
       };
@@ -147,13 +151,16 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         load_kq(n);
         load_v(n);
       }
-      for (int n = 0; n <= walk.n; ++n) {
-        // step n - 1 is done with its tiles, its results are in place
-        wait(&s.rdy_o, n & 1);
-        if (n == 0) continue;
-        load_kq(n + 1);
-        store(n - 1);
-        load_v(n + 1);
+      for (int n = 0; n < walk.n; ++n) {
+        // step n's last products are done: so is everything with its tiles
+        wait(AGG ? &s.mbd : &s.mbo, n & 1);
+        load_kq(n + 2);
+        load_v(n + 2);
+        if (!AGG) {
+          wait(&s.rdy_o, n & 1);  // its outputs are in place
+          store(n);
+          mbar_arrive(&s.o_free);
+        }
       }
       if (!AGG) bulk_wait_all();
       // after a wait ran out, copies still in flight land before the block's
@@ -185,7 +192,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       for (int n = 0; n < walk.n; ++n) {
         const int i = n & 1;
         const uint32_t st = st0 + i * KQ, par = n & 1;
-        const uint32_t tp = st0 + PREP + i * PREP_STAGE;  // T hi, T lo, P hi, P lo
+        const uint32_t tp = st0 + TP + i * TP_BYTES;  // T hi, T lo, P hi, P lo
         wait(&s.kq_full[i], (n >> 1) & 1);
         wait(&s.rdy_s, par);  // S is in tensor memory
         tmem_fence_after_sync();
@@ -193,19 +200,19 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           mma_state(T_X, st);
           tc_commit(&s.mbx);
         }
-        if (!AGG) {
-          wait(&s.rdy_o, par);  // the last chunk's outputs and factors are read
-          if (wait.ok) {
-            tmem_fence_after_sync();
-            mma_state(T_Q, st + TILE);
-            tc_commit(&s.mbq);
-          }
-        }
         wait(&s.rdy_r, par);
         if (wait.ok) {
           tmem_fence_after_sync();
           mma_tokens(T_X, T_R, tp, tp + TILE);
           tc_commit(&s.mbu);
+        }
+        if (!AGG) {  // behind U: nothing waits for it before the outputs
+          wait(&s.rdy_q, par);  // the last chunk's S^T Q^T is read
+          if (wait.ok) {
+            tmem_fence_after_sync();
+            mma_state(T_Q, st + TILE);
+            tc_commit(&s.mbq);
+          }
         }
         wait(&s.rdy_u, par);
         if (!AGG) wait(&s.mbq, par);  // S is read: its columns may be overwritten
@@ -237,10 +244,11 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     // this row's element of token 16 qt + j in a [64 tokens][head_v] tile pair
     const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
     auto at = [&](int j) { return el + j * 128 + ((eu ^ (j & 7)) << 4); };
-    auto vec = [&](int n) -> const TcVec& { return reinterpret_cast<const TcPrep*>(base + PREP + (n & 1) * PREP_STAGE)->vec; };
+    auto vec = [&](int n) -> const TcVec& { return s.vec[n % 3]; };
     float2 S[16];  // S^T[row][32 qt + k]
     if (qt == 0) s.bad[row] = TC;
     bar_sync(1, CHAIN);
+    int bad = TC;  // this step's first token (in this quarter) from which the row's outputs are NaN
 
     auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
       tmem_wait_st();
@@ -300,25 +308,25 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         if (tid == 0) flag_set(a.flags + t.bh);
       }
     };
-    auto put_state = [&](const TcStep* t) {  // S as hi, lo into tensor memory (and the step's checkpoint)
-      unsigned char* ck = nullptr;
-      if (!AGG && a.ckpt && t)
-        ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t->bh * a.nc + t->c) * TC_CKPT + row * 16;
+    auto put_state = [&](const TcStep& t) {  // S as hi, lo into tensor memory (and the step's checkpoint)
+      uint32_t hi[2][8], lo[8];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[k], lo[k]);
-        tc_st8(tl + T_S + qt * 32 + p * 16, hi);
+        for (int k = 0; k < 8; ++k) split2(S[8 * p + k], hi[p][k], lo[k]);
+        tc_st8(tl + T_S + qt * 32 + p * 16, hi[p]);
         tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
-        if (ck) {
+      }
+      ready(&s.rdy_s);
+      if (!AGG && a.ckpt) {
+        unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + row * 16;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             *reinterpret_cast<uint4*>(ck + (qt * 4 + p * 2 + u) * 2048) =
-                make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-        }
+                make_uint4(hi[p][4 * u], hi[p][4 * u + 1], hi[p][4 * u + 2], hi[p][4 * u + 3]);
       }
-      ready(&s.rdy_s);
     };
     // x (16 tokens of this row) as hi, lo at column ta (32 + 32 columns)
     auto put_tokens = [&](uint32_t ta, const float2 (&x)[8], unsigned char* ck) {
@@ -335,14 +343,16 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
       }
     };
-    auto outputs = [&](int n) {  // O of step n from T_Q and T_O, in place of its V
+    // O of step n: read from T_Q and T_O and rounded, and (later) written to
+    // OUT
+    __nv_bfloat162 ov[8];
+    auto read_outputs = [&](int n) {
       float2 q[8], o[8];
       wait(&s.mbq, n & 1);
       wait(&s.mbo, n & 1);
       tmem_fence_after_sync();
       tc_ld16(tl + T_Q + qt * 16, q);
       tc_ld16(tl + T_O + qt * 16, o);
-      const int bad = s.bad[row] - qt * 16;
       const Vec16 fq{&vec(n).fq[qt * 16]};
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = __ffma2_rn(fq[j], q[j], o[j]);
@@ -353,33 +363,27 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           if (2 * j + 1 >= bad) o[j].y = __int_as_float(0x7FFFFFFF);
         }
       }
-      const uint32_t ob = st0 + VO + (n & 1) * 2 * TILE;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ov[j] = __floats2bfloat162_rn(o[j].x, o[j].y);
+    };
+    auto write_outputs = [&](int n) {
+      if (n > 0) wait(&s.o_free, (n - 1) & 1);
+      const uint32_t ob = st0 + OUT;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(o[j].x, o[j].y);
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j)), "h"(__bfloat16_as_ushort(v.x)) : "memory");
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j + 1)), "h"(__bfloat16_as_ushort(v.y)) : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j)), "h"(__bfloat16_as_ushort(ov[j].x)) : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(ob + at(2 * j + 1)), "h"(__bfloat16_as_ushort(ov[j].y)) : "memory");
       }
       fence_proxy_async();
     };
 
     TcStep t = walk.at(0);
     get_state(t);
-    put_state(&t);
+    put_state(t);
     for (int n = 0; n < walk.n; ++n) {
       const int i = n & 1;
       const uint32_t vt = st0 + VO + i * 2 * TILE;
       const uint32_t par = n & 1;
-      if (!AGG) {
-        if (n > 0) outputs(n - 1);
-        if (t.first && n > 0) {  // another head: its row starts clean
-          __syncwarp();
-          bar_sync(1, CHAIN);
-          if (qt == 0) s.bad[row] = TC;
-          bar_sync(1, CHAIN);
-        }
-      }
-      ready(&s.rdy_o);
       // R = beta V - bfx X
       wait(&s.kq_full[i], (n >> 1) & 1);
       wait(&s.v_full[i], (n >> 1) & 1);
@@ -420,9 +424,15 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
+      if (!AGG) {
+        if (n > 0) read_outputs(n - 1);  // while U is made
+        ready(&s.rdy_q);
+      }
       const TcStep tn = walk.at(n + 1);  // (past the last step: not used)
       wait(&s.mbu, par);
-      const bool nan_row = s.bad[row] < TC;
+      const int bad_t = s.bad[row];
+      bad = bad_t - qt * 16;
+      const bool nan_row = bad_t < TC;
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
@@ -437,6 +447,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (!AGG) {  // while the update of S runs
         put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
         ready(&s.rdy_v);
+        if (n > 0) {
+          write_outputs(n - 1);
+          ready(&s.rdy_o);
+        }
       }
       wait(&s.mbd, par);
       tmem_fence_after_sync();
@@ -453,12 +467,20 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (t.last) end_state(t);
       if (n + 1 < walk.n) {
         t = tn;
-        if (t.first) get_state(t);
-        put_state(&t);
+        if (t.first) {
+          bar_sync(1, CHAIN);
+          if (qt == 0) s.bad[row] = TC;
+          bar_sync(1, CHAIN);
+          get_state(t);
+        }
+        put_state(t);
       }
     }
-    if (!AGG) outputs(walk.n - 1);
-    ready(&s.rdy_o);
+    if (!AGG) {
+      read_outputs(walk.n - 1);
+      write_outputs(walk.n - 1);
+      ready(&s.rdy_o);
+    }
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
   tmem_fence_before_sync();
