@@ -693,12 +693,6 @@ def _need(t, name, dtype, index, shape):
     return t
 
 
-def _call(name, args):
-    st = getattr(_LIB, name)(*args)
-    if st != 0:
-        raise M3Error(st, name)
-
-
 def _scratch(workspace, nbytes, torch, dev, stream):
     """(address, bytes) of the caller's workspace or of a new one (whose
     status block nobody can query, so it need not start at zero), and what
@@ -724,7 +718,7 @@ def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, re
     mean, rstd): ``residual_out`` (f32) is x + residual, None without a
     residual unless a tensor for it is passed; ``mean`` and ``rstd`` (f32
     [...]) are None when ``want_stats`` is False."""
-    torch = _torch()
+    torch = _TORCH or _torch()
     code = _act_code(x)
     dev, shape, f32, index = x.device, x.shape, torch.float32, x.get_device()
     if index < 0 or not x.is_contiguous():
@@ -747,8 +741,10 @@ def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, re
     elif want_stats:
         rstd = torch.empty(rshape, dtype=f32, device=dev)
     dims, _ = _norm_sizes(x.numel() // dim if dim else 0, dim, float(eps), 0, code)
-    _call("m3scan_norm_fwd", (dims, code, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(),
-                              _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_of(stream, torch, dev)))
+    st = _LIB.m3scan_norm_fwd(dims, code, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(),
+                              _ptr(residual_out), _ptr(mean), _ptr(rstd), _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_norm_fwd")
     return y, residual_out, mean, rstd
 
 
@@ -785,20 +781,22 @@ def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want
         d_b = new(dim, dtype=f32, device=dev)
     dims, nbytes = _norm_sizes(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)), code)
     ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev, stream)
-    _call("m3scan_norm_bwd", (dims, code, dy.data_ptr(), normed.data_ptr(), ncode, weight.data_ptr(), mean.data_ptr(),
+    st = _LIB.m3scan_norm_bwd(dims, code, dy.data_ptr(), normed.data_ptr(), ncode, weight.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), _ptr(d_residual_out), dx.data_ptr(), _ptr(d_res), d_w.data_ptr(),
-                              _ptr(d_b), ws, nbytes, _stream_of(stream, torch, dev)))
+                              _ptr(d_b), ws, nbytes, _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_norm_bwd")
     o.update(dx=dx, d_residual=d_res, d_weight=d_w, d_bias=d_b)
     return o
 
 
-def _stream_of(stream, torch, dev):
+def _stream_of(stream, index):
     if stream is not None:
         return stream.cuda_stream
     try:
-        return torch._C._cuda_getCurrentRawStream(dev.index)  # 20 times cheaper than the Stream object
+        return _TORCH._C._cuda_getCurrentRawStream(index)  # 20 times cheaper than the Stream object
     except AttributeError:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _TORCH.cuda.current_stream(index).cuda_stream
 
 
 def _token_stride(t, name, dtype, index, shape):
@@ -822,27 +820,37 @@ def _token_stride(t, name, dtype, index, shape):
 
 
 @functools.lru_cache(maxsize=1024)
-def _delta_sizes(code, *fields):
-    dims = M3DeltaDims(*fields)
+def _delta_sizes(code, kshape, vshape, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, scale, qk_l2norm):
+    """(dims, state shape, checkpoint floats, (forward, any) workspace bytes)
+    for those shapes."""
+    if len(kshape) != 4 or len(vshape) != 4 or tuple(kshape[:2]) != tuple(vshape[:2]):
+        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(kshape)}, {tuple(vshape)}")
+    B, T, Hv, dv = vshape
+    Hk, dk = kshape[2:]
+    dims = M3DeltaDims(B, T, Hk, Hv, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, float(scale),
+                       int(bool(qk_l2norm)))
     pl = m3scan_delta_plan(dims, code)
-    B, _, _, Hv, dk, dv = fields[:6]
     return ctypes.byref(dims), (B, Hv, dk, dv), pl.ckpt_bytes // 4, (pl.fwd_workspace_bytes, pl.workspace_bytes)
 
 
-def _delta_fields(q, k, v, g, beta):
-    """Sizes and strides of the inputs as m3_delta_dims has them, checked."""
-    if v.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(k.shape)}, {tuple(v.shape)}")
+def _delta_inputs(q, k, v, g, beta):
+    """Checks the inputs; returns (dtype code, device index, k's and v's
+    shapes, token strides of q, k, v)."""
     dt, index = v.dtype, v.get_device()
+    code = _act_code(v)
+    kshape, vshape, gshape = k.shape, v.shape, v.shape[:3]
     if index < 0:
         _check(v, "v")
-    B, T, Hv, dv = vshape = v.shape
-    Hk, dk = k.shape[2:]
-    kshape, gshape = (B, T, Hk, dk), (B, T, Hv)
     _need(g, "g", dt, index, gshape)
     _need(beta, "beta", dt, index, gshape)
-    return (B, T, Hk, Hv, dk, dv, _token_stride(q, "q", dt, index, kshape), _token_stride(k, "k", dt, index, kshape),
-            _token_stride(v, "v", dt, index, vshape)), index
+    if (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and q.dtype is dt and k.dtype is dt
+            and q.shape == kshape and q.get_device() == index and k.get_device() == index):
+        return code, index, kshape, vshape, 0, 0, 0
+    if len(kshape) != 4 or len(vshape) != 4:
+        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(kshape)}, {tuple(vshape)}")
+    kwant = (*vshape[:2], *kshape[2:])
+    return (code, index, kshape, vshape, _token_stride(q, "q", dt, index, kwant), _token_stride(k, "k", dt, index, kwant),
+            _token_stride(v, "v", dt, index, vshape))
 
 
 def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False, want_state=True,
@@ -853,11 +861,11 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     (zero).  Returns (o, state_out or None, ckpt or None); the backward needs
     ``want_ckpt=True``."""
     torch = _torch()
-    code, dev, f32 = _act_code(v), v.device, torch.float32
-    fields, index = _delta_fields(q, k, v, g, beta)
-    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, *fields, 0, 0, 0, float(scale), int(bool(qk_l2norm)))
+    dev, f32 = v.device, torch.float32
+    code, index, kshape, vshape, sq, sk, sv = _delta_inputs(q, k, v, g, beta)
+    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, kshape, vshape, sq, sk, sv, 0, 0, 0, scale, qk_l2norm)
     _need(state, "state", f32, index, sshape)
-    o = torch.empty(v.shape, dtype=v.dtype, device=dev) if o is None else _need(o, "o", v.dtype, index, v.shape)
+    o = torch.empty(vshape, dtype=v.dtype, device=dev) if o is None else _need(o, "o", v.dtype, index, vshape)
     if state_out is not None:
         _need(state_out, "state_out", f32, index, sshape)
     elif want_state:
@@ -867,9 +875,11 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     elif want_ckpt:
         ckpt = torch.empty(n_ckpt, dtype=f32, device=dev)
     ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev, stream)
-    _call("m3scan_delta_fwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+    st = _LIB.m3scan_delta_fwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                _ptr(state), o.data_ptr(), _ptr(state_out), _ptr(ckpt), ws, nbytes,
-                               _stream_of(stream, torch, dev)))
+                               _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_delta_fwd")
     return o, state_out, ckpt
 
 
@@ -880,8 +890,8 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     (activation dtype) and d_state (f32, None unless wanted).  dq, dk and dv
     in ``out`` may be column views of a projection's gradient."""
     torch = _torch()
-    code, dev, dt, f32 = _act_code(v), v.device, v.dtype, torch.float32
-    fields, index = _delta_fields(q, k, v, g, beta)
+    dev, dt, f32 = v.device, v.dtype, torch.float32
+    code, index, kshape, vshape, sq, sk, sv = _delta_inputs(q, k, v, g, beta)
     r = dict(out) if out else {}
     for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
         if r.get(n) is None:
@@ -889,7 +899,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _need(r["dg"], "dg", dt, index, g.shape)
     _need(r["dbeta"], "dbeta", dt, index, g.shape)
     strides = [_token_stride(r[n], n, dt, index, t.shape) for n, t in (("dq", q), ("dk", k), ("dv", v))]
-    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, *fields, *strides, float(scale), int(bool(qk_l2norm)))
+    dims, sshape, n_ckpt, nbytes = _delta_sizes(code, kshape, vshape, sq, sk, sv, *strides, scale, qk_l2norm)
     if r.get("d_state") is None:
         r["d_state"] = torch.empty(sshape, dtype=f32, device=dev) if want_d_state else None
     _need(d_state_out, "d_state_out", f32, index, sshape)
@@ -897,10 +907,12 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _need(d_o, "d_o", dt, index, v.shape)
     _need(ckpt, "ckpt", f32, index, (n_ckpt,))
     ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev, stream)
-    _call("m3scan_delta_bwd", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+    st = _LIB.m3scan_delta_bwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                ckpt.data_ptr(), d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(),
                                r["dk"].data_ptr(), r["dv"].data_ptr(), r["dg"].data_ptr(), r["dbeta"].data_ptr(),
-                               _ptr(r["d_state"]), ws, nbytes, _stream_of(stream, torch, dev)))
+                               _ptr(r["d_state"]), ws, nbytes, _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_delta_bwd")
     return r
 
 
@@ -908,14 +920,12 @@ def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, 
     """A short window (typically one token: T = 1) from the carried ``state``
     [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""
     torch = _torch()
-    code, dev = _act_code(v), v.device
-    fields, index = _delta_fields(q, k, v, g, beta)
-    dims, sshape, _, _ = _delta_sizes(code, *fields, 0, 0, 0, float(scale), int(bool(qk_l2norm)))
-    if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    else:
-        _need(o, "o", v.dtype, index, v.shape)
+    code, index, kshape, vshape, sq, sk, sv = _delta_inputs(q, k, v, g, beta)
+    dims, sshape, _, _ = _delta_sizes(code, kshape, vshape, sq, sk, sv, 0, 0, 0, scale, qk_l2norm)
+    o = torch.empty(vshape, dtype=v.dtype, device=v.device) if o is None else _need(o, "o", v.dtype, index, vshape)
     _need(state, "state", torch.float32, index, sshape)
-    _call("m3scan_delta_decode", (dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                  state.data_ptr(), o.data_ptr(), _stream_of(stream, torch, dev)))
+    st = _LIB.m3scan_delta_decode(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                  state.data_ptr(), o.data_ptr(), _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_delta_decode")
     return o
