@@ -46,11 +46,13 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
 }
 
 // Time segments of the tensor-core chains.  A block per (head, segment) runs
-// one chunk in a unit of time (3.2 us in the forward); with S segments, first
-// the S - 1 earlier ones run twice without outputs (from zero and from the
-// identity, 3/4 of a unit per chunk), then a kernel chains them (2/3 of a
-// unit per segment and two for its launch), then all S run.  The count with
-// the least total is taken, with at least four chunks per segment.
+// one chunk in a unit of time (2.8 us in the forward); with S segments, first
+// the effect of the S - 1 earlier ones is found (1.1 units per chunk), then a
+// kernel chains them (eight blocks per head, 1.6 units per segment), then all
+// S run; the two extra launches and their first loads are four units.  The
+// count with the least total is taken, with at least four chunks per segment.
+// 1 x 65536 x 16 heads: nine segments, 0.96 ms against 3.0 ms for one; 36
+// heads of 24 chunks: about the same in one and in three (measured for both).
 void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
   constexpr int64_t SMS = 152;
   double best = 0.0;
@@ -61,7 +63,8 @@ void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
     const double fin = (double)((heads * S + SMS - 1) / SMS) * m;
-    const double agg = S > 1 ? (double)((heads * (S - 1) * 2 + SMS - 1) / SMS) * m * 0.75 + 0.67 * S + 2.0 : 0.0;
+    const double agg = S > 1 ? (double)((heads * (S - 1) + SMS - 1) / SMS) * m * 1.1 +
+                                     (double)((heads * 8 + SMS - 1) / SMS) * (S - 1) * 1.6 + 4.0 : 0.0;
     if (want == 1 || fin + agg < best - 1e-9) {
       best = fin + agg;
       *segs = S;

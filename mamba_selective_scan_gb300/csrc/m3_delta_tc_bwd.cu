@@ -60,7 +60,7 @@ constexpr uint32_t T_Y = 320;  // fq dO as hi, lo
 // It leaves dS (at each chunk's end) and dR for the gradients' kernel, which
 // has no order among chunks.  AGG: a segment's effect on the adjoint, from
 // zero (blockIdx.z 0) and from the identity with dO = 0 (blockIdx.z 1).
-template <bool AGG, bool L2>
+template <bool AGG>
 __global__ void __launch_bounds__(rev::THREADS, 1)
 m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap md,
@@ -441,8 +441,7 @@ cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
     if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, mq, mk, md, mv);
     return e;
   };
-  return a.l2 ? go(m3_delta_tc_rev_kernel<true, true>, m3_delta_tc_rev_kernel<false, true>)
-              : go(m3_delta_tc_rev_kernel<true, false>, m3_delta_tc_rev_kernel<false, false>);
+  return go(m3_delta_tc_rev_kernel<true>, m3_delta_tc_rev_kernel<false>);
 }
 
 // ---------------------------------------------------------------------------

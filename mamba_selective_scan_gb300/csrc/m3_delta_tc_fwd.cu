@@ -73,11 +73,6 @@ constexpr uint32_t T_O = 384;   // U P^T
 // goes back to, so the chain needs no barrier among its warps.  A chunk is a
 // chain of four dependent products, bound by their latency and the register
 // work between them, not by HBM.
-//
-// AGG: the segment's effect on the state instead of outputs: blockIdx.z 0
-// from a zero state, blockIdx.z 1 from the identity with V = 0 (the rows of
-// the state's transition), both written to seg.
-template <bool AGG, bool L2>
 __global__ void __launch_bounds__(THREADS, 1)
 m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -89,7 +84,6 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
   const int seg = blockIdx.y;
   const TcWalk walk(a, seg);
-  const bool ident = AGG && blockIdx.z == 1;
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
@@ -153,16 +147,14 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       for (int n = 0; n < walk.n; ++n) {
         // step n's last products are done: so is everything with its tiles
-        wait(AGG ? &s.mbd : &s.mbo, n & 1);
+        wait(&s.mbo, n & 1);
         load_kq(n + 2);
         load_v(n + 2);
-        if (!AGG) {
-          wait(&s.rdy_o, n & 1);  // its outputs are in place
-          store(n);
-          mbar_arrive(&s.o_free);
-        }
+        wait(&s.rdy_o, n & 1);  // its outputs are in place
+        store(n);
+        mbar_arrive(&s.o_free);
       }
-      if (!AGG) bulk_wait_all();
+      bulk_wait_all();
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
       if (!wait.ok) {
@@ -206,16 +198,14 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
           mma_tokens(T_X, T_R, tp, tp + TILE);
           tc_commit(&s.mbu);
         }
-        if (!AGG) {  // behind U: nothing waits for it before the outputs
-          wait(&s.rdy_q, par);  // the last chunk's S^T Q^T is read
-          if (wait.ok) {
-            tmem_fence_after_sync();
-            mma_state(T_Q, st + TILE);
-            tc_commit(&s.mbq);
-          }
+        wait(&s.rdy_q, par);  // the last chunk's S^T Q^T is read
+        if (wait.ok) {  // behind U: nothing waits for it before the outputs
+          tmem_fence_after_sync();
+          mma_state(T_Q, st + TILE);
+          tc_commit(&s.mbq);
         }
         wait(&s.rdy_u, par);
-        if (!AGG) wait(&s.mbq, par);  // S is read: its columns may be overwritten
+        wait(&s.mbq, par);  // S is read: its columns may be overwritten
         if (wait.ok) {
           tmem_fence_after_sync();
 #pragma unroll
@@ -226,13 +216,11 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
                         tc_idesc(128, 128, false, true), p + ks > 0);
           tc_commit(&s.mbd);
         }
-        if (!AGG) {
-          wait(&s.rdy_v, par);
-          if (wait.ok) {
-            tmem_fence_after_sync();
-            mma_tokens(T_O, T_U, tp + 2 * TILE, tp + 3 * TILE);
-            tc_commit(&s.mbo);
-          }
+        wait(&s.rdy_v, par);
+        if (wait.ok) {
+          tmem_fence_after_sync();
+          mma_tokens(T_O, T_U, tp + 2 * TILE, tp + 3 * TILE);
+          tc_commit(&s.mbo);
         }
       }
     }
@@ -257,12 +245,6 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (lane == 0) mbar_arrive(bar);
     };
     auto get_state = [&](const TcStep& t) {  // the state a run starts from
-      if (AGG) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          S[k] = make_float2(ident && qt * 32 + 2 * k == row ? 1.0f : 0.0f, ident && qt * 32 + 2 * k + 1 == row ? 1.0f : 0.0f);
-        return;
-      }
       // the carried state, what the segments before left, or a state handed over
       if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
       const bool own = t.c > 0;
@@ -279,16 +261,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     auto end_state = [&](const TcStep& t) {  // where a run leaves it
       float* dst = nullptr;
       bool own = true;
-      if (AGG) {
-        dst = a.seg_end + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
-        if (ident) {  // by rows of the transition
-          float* o = a.seg_phi + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2)
-            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
-          return;
-        }
-      } else if (t.give) {
+      if (t.give) {
         dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
       } else if (a.s_out && t.c == a.nc - 1) {
         dst = a.s_out + (size_t)t.bh * a.DK * a.DV;
@@ -318,7 +291,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         tc_st8(tl + T_S + qt * 32 + p * 16 + 8, lo);
       }
       ready(&s.rdy_s);
-      if (!AGG && a.ckpt) {
+      if (a.ckpt) {
         unsigned char* ck = reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + row * 16;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -403,7 +376,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         const Vec16 be{&vec(n).beta[qt * 16]}, bx{&vec(n).bfx[qt * 16]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 vv = ident ? f2b(0.0f) : make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16));
+          const float2 vv = make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16));
           const float2 m = __fmul2_rn(x[j], f2b(-1.0f));
           x[j] = __ffma2_rn(bx[j], m, __fmul2_rn(be[j], vv));
           chk = __ffma2_rn(x[j], f2b(0.0f), chk);  // 0 unless a value is not finite
@@ -424,10 +397,8 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
-      if (!AGG) {
-        if (n > 0) read_outputs(n - 1);  // while U is made
-        ready(&s.rdy_q);
-      }
+      if (n > 0) read_outputs(n - 1);  // while U is made
+      ready(&s.rdy_q);
       const TcStep tn = walk.at(n + 1);  // (past the last step: not used)
       wait(&s.mbu, par);
       const int bad_t = s.bad[row];
@@ -444,13 +415,12 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       }
       const float2 ec = f2b(vec(n).ec);
       ready(&s.rdy_u);
-      if (!AGG) {  // while the update of S runs
-        put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
-        ready(&s.rdy_v);
-        if (n > 0) {
-          write_outputs(n - 1);
-          ready(&s.rdy_o);
-        }
+      // while the update of S runs
+      put_tokens(T_U, x, a.ckpt ? reinterpret_cast<unsigned char*>(a.ckpt) + ((size_t)t.bh * a.nc + t.c) * TC_CKPT + 32768 : nullptr);
+      ready(&s.rdy_v);
+      if (n > 0) {
+        write_outputs(n - 1);
+        ready(&s.rdy_o);
       }
       wait(&s.mbd, par);
       tmem_fence_after_sync();
@@ -476,11 +446,9 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         put_state(t);
       }
     }
-    if (!AGG) {
-      read_outputs(walk.n - 1);
-      write_outputs(walk.n - 1);
-      ready(&s.rdy_o);
-    }
+    read_outputs(walk.n - 1);
+    write_outputs(walk.n - 1);
+    ready(&s.rdy_o);
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
   tmem_fence_before_sync();
@@ -508,6 +476,263 @@ bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, 
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// ---------------------------------------------------------------------------
+// time segments
+// ---------------------------------------------------------------------------
+namespace agg {
+
+constexpr int THREADS = CHAIN + 64;
+constexpr int KT_ = 2 * TILE;           // one chunk's K tiles; two stages
+constexpr int TT_ = 2 * KT_;            // T hi, lo, two stages
+constexpr int VT = TT_ + 4 * TILE;      // V, two stages
+constexpr int SMALL = VT + 4 * TILE;
+struct Smem {  // at SMALL
+  TcVec vec[2];
+  int bad[2][128];
+  uint64_t full[2];
+  uint64_t mbx[2], mbu[2], mbd[2], rdy_s[2], rdy_r[2], rdy_u[2];  // by chain; rdy: one arrival per chain warp
+  uint32_t tmem;
+};
+constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
+// tensor-memory columns of a chain (256 each)
+constexpr uint32_t A_S = 0, A_X = 128, A_R = 192;
+
+}  // namespace agg
+
+// A segment's effect on the state, S_end = N + Phi^T S_start: the chain of
+// m3_delta_tc_fwd_kernel without outputs, twice in one block, from a zero
+// state (N) and from the identity with V = 0 (the rows of Phi).  The two use
+// the same tiles and take turns: one's products run under the other's
+// register work.
+__global__ void __launch_bounds__(agg::THREADS, 1)
+m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv) {
+  using namespace agg;
+  extern __shared__ unsigned char raw[];
+  unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  agg::Smem& s = *reinterpret_cast<agg::Smem*>(base + agg::SMALL);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
+  const int bh = blockIdx.x, b = bh / a.Hv, h = bh % a.Hv, hk = h / a.share, seg = blockIdx.y;
+  const int c_begin = seg * a.seg_chunks, N = min(a.nc, c_begin + a.seg_chunks) - c_begin;
+  const uint32_t st0 = smem_u32(base);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      for (uint64_t* r : {&s.full[i], &s.mbx[i], &s.mbu[i], &s.mbd[i]}) mbar_init(r, 1);
+      for (uint64_t* r : {&s.rdy_s[i], &s.rdy_r[i], &s.rdy_u[i]}) mbar_init(r, CHAIN / 32);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 0) tmem_alloc(&s.tmem, 512);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
+  TcWait wait;
+
+  if (warp == CHAIN / 32 + 1) {
+    if (elect_one()) {
+      int issued = 0;
+      auto load = [&](int n) {
+        if (n >= N || !wait.ok) return;
+        ++issued;
+        const int i = n & 1, c = c_begin + n;
+        const unsigned char* prep = a.tp + ((size_t)bh * a.nc + c) * a.tp_stride;
+        mbar_expect_tx(&s.full[i], 6 * TILE + (uint32_t)sizeof(TcVec));
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          tma_tile(st0 + i * KT_ + blk * TILE, &mk, blk * 64, hk, c * TC, b, &s.full[i]);
+          tma_tile(st0 + VT + (i * 2 + blk) * TILE, &mv, blk * 64, h, c * TC, b, &s.full[i]);
+        }
+        bulk_load(st0 + TT_ + i * 2 * TILE, prep, 2 * TILE, &s.full[i]);
+        bulk_load(smem_u32(&s.vec[i]), prep + sizeof(TcTP), (uint32_t)sizeof(TcVec), &s.full[i]);
+      };
+      load(0);
+      load(1);
+      for (int n = 0; n < N; ++n) {  // step n's last products are done: so is everything with its tiles
+        wait(&s.mbd[0], n & 1);
+        wait(&s.mbd[1], n & 1);
+        load(n + 2);
+      }
+      if (!wait.ok)  // as in the other kernels: copies in flight land first
+        for (int i = 1; i <= 2 && i <= issued; ++i) mbar_wait(&s.full[(issued - i) & 1], (issued - i) >> 1 & 1);
+    }
+    __syncwarp();
+  } else if (warp == CHAIN / 32) {
+    if (elect_one()) {
+      for (int n = 0; n < N; ++n) {
+        const int i = n & 1;
+        const uint32_t par = n & 1, kt = st0 + i * KT_, tt = st0 + TT_ + i * 2 * TILE;
+        wait(&s.full[i], (n >> 1) & 1);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          wait(&s.rdy_s[m], par);
+          if (!wait.ok) continue;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma_ts(tm + m * 256 + A_X, tm + m * 256 + A_S + ks * 16 + p * 8,
+                        tc_desc(kt + (ks >> 2) * TILE + (ks & 3) * 32, 16, 1024), tc_idesc(128, 64, false, false), p + ks > 0);
+          tc_commit(&s.mbx[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          wait(&s.rdy_r[m], par);
+          if (!wait.ok) continue;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + m * 256 + A_X, tm + m * 256 + A_R + (p == 1 ? 32 : 0) + ks * 8,
+                        tc_desc(tt + (p == 2 ? TILE : 0) + ks * 32, 16, 1024), tc_idesc(128, 64, false, false), p + ks > 0);
+          tc_commit(&s.mbu[m]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          wait(&s.rdy_u[m], par);
+          if (!wait.ok) continue;
+          tmem_fence_after_sync();
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc_mma_ts(tm + m * 256 + A_S, tm + m * 256 + A_R + p * 32 + ks * 8, tc_desc(kt + ks * 2048, TILE, 1024),
+                        tc_idesc(128, 128, false, true), p + ks > 0);
+          tc_commit(&s.mbd[m]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int qt = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t el = (row >> 6) * TILE + qt * 16 * 128 + (row & 7) * 2, eu = (row & 63) >> 3;
+    float2 S[2][16];
+    if (qt == 0) s.bad[0][row] = s.bad[1][row] = TC;
+    bar_sync(1, CHAIN);
+    auto ready = [&](uint64_t* bar) {
+      tmem_wait_st();
+      tmem_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto put_state = [&](int m) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split2(S[m][8 * p + k], hi[k], lo[k]);
+        tc_st8(tl + m * 256 + A_S + qt * 32 + p * 16, hi);
+        tc_st8(tl + m * 256 + A_S + qt * 32 + p * 16 + 8, lo);
+      }
+      ready(&s.rdy_s[m]);
+    };
+    auto put_tokens = [&](int m, const float2 (&x)[8]) {
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) split2(x[k], hi[k], lo[k]);
+      tc_st8(tl + m * 256 + A_R + qt * 8, hi);
+      tc_st8(tl + m * 256 + A_R + 32 + qt * 8, lo);
+    };
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        S[m][k] = make_float2(m && qt * 32 + 2 * k == row ? 1.0f : 0.0f, m && qt * 32 + 2 * k + 1 == row ? 1.0f : 0.0f);
+      put_state(m);
+    }
+    for (int n = 0; n < N; ++n) {
+      const int i = n & 1;
+      const uint32_t par = n & 1, vt = st0 + VT + i * 2 * TILE;
+      const TcVec& vec = s.vec[i];
+      wait(&s.full[i], (n >> 1) & 1);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {  // R = beta V - bfx X (as in the forward kernel)
+        float2 x[8];
+        uint32_t v[16];
+        if (m == 0) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            uint16_t vr;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(vr) : "r"(vt + el + j * 128 + ((eu ^ (j & 7)) << 4)));
+            v[j] = vr;
+          }
+        }
+        wait(&s.mbx[m], par);
+        tmem_fence_after_sync();
+        tc_ld16(tl + m * 256 + A_X + qt * 16, x);
+        float2 chk = f2b(0.0f);
+        const Vec16 be{&vec.beta[qt * 16]}, bx{&vec.bfx[qt * 16]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 y = __fmul2_rn(__fmul2_rn(x[j], f2b(-1.0f)), bx[j]);
+          x[j] = m ? y : __ffma2_rn(be[j], make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16)), y);
+          chk = __ffma2_rn(x[j], f2b(0.0f), chk);
+        }
+        if (!(chk.x + chk.y == 0.0f)) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float& e = j & 1 ? x[j >> 1].y : x[j >> 1].x;
+            if (!(fabsf(e) <= FINITE_MAX)) {
+              e = 0.0f;
+              atomicMin(&s.bad[m][row], qt * 16 + j);
+            }
+          }
+        }
+        put_tokens(m, x);
+        ready(&s.rdy_r[m]);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        float2 x[8];
+        wait(&s.mbu[m], par);
+        tmem_fence_after_sync();
+        tc_ld16(tl + m * 256 + A_X + qt * 16, x);
+        const Vec16 fu{&vec.fu[qt * 16]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(x[j], fu[j]);
+        put_tokens(m, x);
+        ready(&s.rdy_u[m]);
+      }
+      const float2 ec = f2b(vec.ec);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const bool nan_row = s.bad[m][row] < TC;
+        wait(&s.mbd[m], par);
+        tmem_fence_after_sync();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float2 x[8];
+          tc_ld16(tl + m * 256 + A_S + qt * 32 + q * 16, x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) S[m][q * 8 + k] = __ffma2_rn(ec, S[m][q * 8 + k], x[k]);
+        }
+        if (nan_row) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) S[m][k] = f2b(__int_as_float(0x7FFFFFFF));
+        }
+        if (n + 1 < N) put_state(m);
+      }
+    }
+    // N as [head_k][row], Phi by its rows
+    float* end = a.seg_end + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+    float* phi = a.seg_phi + ((size_t)bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) end[(size_t)(qt * 32 + k) * DMAX + row] = k & 1 ? S[0][k >> 1].y : S[0][k >> 1].x;
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) *reinterpret_cast<float4*>(phi + 2 * k) = make_float4(S[1][k].x, S[1][k].y, S[1][k + 1].x, S[1][k + 1].y);
+  }
+  if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
+  tmem_fence_before_sync();
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 0) tmem_dealloc(tm, 512);
 }
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
@@ -571,23 +796,18 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
       !delta_tile_map(&mv, a.v, a.DV, a.Hv, a.T, a.B, a.vs) ||
       !delta_tile_map(&mo, a.o, a.DV, a.Hv, a.T, a.B, (int64_t)a.Hv * a.DV))
     return cudaErrorInvalidValue;
-  auto go = [&](auto agg, auto fin) {
-    cudaError_t e = cudaSuccess;
-    const unsigned heads = (unsigned)(a.B * a.Hv);
-    if (a.segs > 1) {
-      e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-      if (e == cudaSuccess)
-        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), THREADS, SMEM_BYTES, st, false, a, mq, mk, mv, mo);
-      if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
-    }
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
+  cudaError_t e = cudaSuccess;
+  const unsigned heads = (unsigned)(a.B * a.Hv);
+  if (a.segs > 1) {
+    e = cudaFuncSetAttribute(m3_delta_tc_agg_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)agg::SMEM_BYTES);
     if (e == cudaSuccess)
-      e = launch_delta_blocks(fin, a, THREADS, SMEM_BYTES, st, mq, mk, mv, mo);
-    return e;
-  };
-  return a.l2 ? go(m3_delta_tc_fwd_kernel<true, true>, m3_delta_tc_fwd_kernel<false, true>)
-              : go(m3_delta_tc_fwd_kernel<true, false>, m3_delta_tc_fwd_kernel<false, false>);
+      e = launch_k(m3_delta_tc_agg_kernel, dim3(heads, (unsigned)(a.segs - 1)), agg::THREADS, agg::SMEM_BYTES, st, false, a, mk, mv);
+    if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
+  }
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_delta_tc_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
+  if (e == cudaSuccess) e = launch_delta_blocks(m3_delta_tc_fwd_kernel, a, THREADS, SMEM_BYTES, st, mq, mk, mv, mo);
+  return e;
 }
 
 }  // namespace m3
