@@ -23,6 +23,7 @@ namespace m3 {
 constexpr size_t TC_PREP = 33920;  // T, P and the per-token factors (TcPrep)
 constexpr size_t TC_CKPT = 65536 + TC_PREP;  // the forward's: S^T, U^T hi, U^T lo, TcPrep
 constexpr size_t TC_BWD = 98304;   // the reverse pass's: dS^T hi, lo, dR^T hi, lo
+constexpr size_t F32_KEPT = 155904;  // per chunk of 32 and head, between the kernels of the f32 backward
 constexpr int TC = 64;             // tokens per chunk of the tensor-core kernels
 constexpr int TC_BLOCKS = 152;     // persistent blocks of the gradients' kernel, at most (the SMs of a GB300)
 constexpr int DMAX = 128;          // head_k and head_v, at most
@@ -44,7 +45,7 @@ struct DeltaArgs {
   unsigned* flags;       // stream: [B Hv], set once a head's state was handed over (in seg_start)
   int segs, seg_chunks;  // else: time segments, chunks per segment
   float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
-  unsigned char* bwd;  // [B Hv][nc][TC_BWD]
+  unsigned char* bwd;  // [B Hv][nc] of TC_BWD (f32: F32_KEPT) bytes
   unsigned char* tp;   // TcPrep of every chunk, tp_stride bytes apart (in the checkpoints, or the workspace)
   size_t tp_stride;
   unsigned* status;

@@ -108,7 +108,7 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->o_tp = take(tc ? chunks * TC_PREP : 0);
   p->fwd_ws_bytes = off;
   off = mark;
-  p->o_bwd = take(tc ? chunks * TC_BWD : 0);
+  p->o_bwd = take(chunks * (tc ? TC_BWD : F32_KEPT));
   const bool shared = p->Hv != p->Hk;
   const size_t share_bytes = (size_t)p->B * p->T * p->Hv * p->DK * 4;
   p->o_pdq = take(!shared ? 0 : tc ? (size_t)TC_BLOCKS * TC * DMAX * 2 * 4 : share_bytes);
@@ -117,7 +117,7 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   const bool empty = p->B == 0 || p->T == 0;
   const int walk = p->segs > 1 ? 3 : 1;  // (shares: and a memset of their flags)
   p->fwd_launches = empty ? 0 : walk + (tc ? 1 : 0);
-  p->bwd_launches = empty ? 0 : walk + (tc ? 1 : shared ? 1 : 0);
+  p->bwd_launches = empty ? 0 : tc ? walk + 1 : shared ? 4 : 3;
   return M3_OK;
 }
 
