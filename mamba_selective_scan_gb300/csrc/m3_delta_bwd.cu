@@ -44,9 +44,10 @@ struct PrepSmem {
   float A[C][LS], P[C][LS], Ti[C][LS];
   Gates g;
 };
+constexpr int RV = 32, LR = RV + 4;  // columns of dS per block of the reverse pass
 struct RevSmem {
-  float K[C][LD], Q[C][LD], dO[C][LD], dU[C][LD], dR[C][LD];
-  float dS[DMAX][LD];
+  float K[C][LD], Q[C][LD];
+  float dO[C][LR], dU[C][LR], dR[C][LR], dS[DMAX][LR];
   float P[C][LS], Ti[C][LS];
   Gates g;
 };
@@ -130,9 +131,9 @@ __device__ __forceinline__ const float* start_state(const DeltaArgs& a, const Pl
 }
 }  // namespace
 
-// Blocks of 8 warps.  Every warp owns four rows of a chunk (and 16 rows of
-// dS); a lane four columns, side by side where a product's sum runs over
-// rows, 32 apart where it runs along a row.
+// Blocks of 8 warps.  Every warp owns four rows of a chunk; a lane four
+// columns, side by side where a product's sum runs over rows, 32 apart where
+// it runs along a row.
 __global__ void __launch_bounds__(256) m3_delta_bwd_prep_kernel(const __grid_constant__ DeltaArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   PrepSmem& s = *reinterpret_cast<PrepSmem*>(smem_raw);
@@ -239,100 +240,87 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_prep_kernel(const __grid_con
   }
 }
 
-// One block per (batch row, value head), chunks last to first, dS in shared
-// memory.
+// Chunks last to first, 32 of dS's columns per block in shared memory (the
+// columns never meet).  A thread has a row of the chunk, and four rows of dS,
+// in four columns.
 __global__ void __launch_bounds__(256) m3_delta_bwd_rev_kernel(const __grid_constant__ DeltaArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   RevSmem& s = *reinterpret_cast<RevSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = warp * 4, c0 = lane * 4;
-  for (int half = 0; half < 2; ++half) {
-    if (a.ds_out) load_half(s.dS + half * 64, a.ds_out + (size_t)blockIdx.x * a.DK * a.DV, half, a, tid);
-    else
-      for (int e = tid; e < 64 * DMAX / 4; e += 256) f4(&s.dS[half * 64 + (e >> 5)][(e & 31) * 4]) = make_float4(0, 0, 0, 0);
+  const int bh = blockIdx.x, v0 = blockIdx.y * RV;
+  const int r = tid >> 3, c0 = (tid & 7) * 4, k0 = r * 4;
+  const bool vok = v0 + c0 < a.DV;
+  float4 d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    d[i] = a.ds_out && vok && k0 + i < a.DK ? f4(a.ds_out + ((size_t)bh * a.DK + k0 + i) * a.DV + v0 + c0)
+                                            : make_float4(0, 0, 0, 0);
+    f4(&s.dS[k0 + i][c0]) = d[i];
   }
   for (int ch = a.nc - 1; ch >= 0; --ch) {
-    const Place p(a, blockIdx.x, ch);
+    const Place p(a, bh, ch);
     Kept& kp = kept(a, p);
     __syncthreads();
     load_kept(s.K, kp.K, C, tid);
     load_kept(s.Q, kp.Q, C, tid);
-    load_rows(s.dO, static_cast<const float*>(a.d_o) + (p.tok0 * a.Hv + p.h) * a.DV, (int64_t)a.Hv * a.DV, a.DV, p.n, tid);
+    f4(&s.dO[r][c0]) = r < p.n && vok ? f4(static_cast<const float*>(a.d_o) + ((p.tok0 + r) * a.Hv + p.h) * a.DV + v0 + c0)
+                                      : make_float4(0, 0, 0, 0);
     for (int e = tid; e < C * C; e += 256) {
       s.P[e >> 5][e & 31] = kp.P[e >> 5][e & 31];
       s.Ti[e >> 5][e & 31] = kp.T[e >> 5][e & 31];
     }
     if (warp == 0) load_gates(s.g, a, p, lane);
-    for (int e = tid; e < DMAX * DMAX / 4; e += 256) f4(&kp.dS[e >> 5][(e & 31) * 4]) = f4(&s.dS[e >> 5][(e & 31) * 4]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f4(&kp.dS[k0 + i][v0 + c0]) = d[i];
     __syncthreads();
     {  // dU = P^T dO + (e^{gam_C - gam} K) dS
-      float4 d[4] = {}, w[4] = {};
-#pragma unroll 4
-      for (int j = 0; j < C; ++j) {
-        const float4 o = f4(&s.dO[j][c0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) axpy4(d[i], s.P[j][r0 + i], o);
-      }
+      float4 u = make_float4(0, 0, 0, 0), w = u;
 #pragma unroll 8
-      for (int k = 0; k < DMAX; ++k) {
-        const float4 x = f4(&s.dS[k][c0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) axpy4(w[i], s.K[r0 + i][k], x);
+      for (int j = 0; j < C; ++j) axpy4(u, s.P[j][r], f4(&s.dO[j][c0]));
+#pragma unroll 4
+      for (int k = 0; k < DMAX; k += 4) {
+        const float4 kr = f4(&s.K[r][k]);
+        axpy4(w, kr.x, f4(&s.dS[k][c0]));
+        axpy4(w, kr.y, f4(&s.dS[k + 1][c0]));
+        axpy4(w, kr.z, f4(&s.dS[k + 2][c0]));
+        axpy4(w, kr.w, f4(&s.dS[k + 3][c0]));
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        axpy4(d[i], s.g.el[r0 + i], w[i]);
-        f4(&s.dU[r0 + i][c0]) = d[i];
-      }
+      axpy4(u, s.g.el[r], w);
+      f4(&s.dU[r][c0]) = u;
     }
     __syncthreads();
     {  // dR = T^T dU;  dV = beta dR
-      float4 d[4] = {};
+      float4 x = make_float4(0, 0, 0, 0);
 #pragma unroll 8
-      for (int j = 0; j < C; ++j) {
-        const float4 x = f4(&s.dU[j][c0]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) axpy4(d[i], s.Ti[j][r0 + i], x);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + i;
-        f4(&kp.dR[r][c0]) = d[i];
-        const float bt = s.g.beta[r];
-        d[i] = make_float4(bt * d[i].x, bt * d[i].y, bt * d[i].z, bt * d[i].w);
-        f4(&s.dR[r][c0]) = d[i];  // beta dR
-        if (r < p.n && c0 < a.DV) f4(static_cast<float*>(a.dv) + (p.tok0 + r) * a.dvs + (int64_t)p.h * a.DV + c0) = d[i];
-      }
+      for (int j = 0; j < C; ++j) axpy4(x, s.Ti[j][r], f4(&s.dU[j][c0]));
+      f4(&kp.dR[r][v0 + c0]) = x;
+      const float bt = s.g.beta[r];
+      x = make_float4(bt * x.x, bt * x.y, bt * x.z, bt * x.w);
+      f4(&s.dR[r][c0]) = x;  // beta dR
+      if (r < p.n && vok) f4(static_cast<float*>(a.dv) + (p.tok0 + r) * a.dvs + (int64_t)p.h * a.DV + v0 + c0) = x;
     }
     __syncthreads();
     {  // dS0
       const float ec = s.g.eg[C - 1];
-      const int k0 = warp * 16;
-      float4 d[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 x = f4(&s.dS[k0 + i][c0]);
-        d[i] = make_float4(ec * x.x, ec * x.y, ec * x.z, ec * x.w);
-      }
-#pragma unroll 1
+      for (int i = 0; i < 4; ++i) d[i] = make_float4(ec * d[i].x, ec * d[i].y, ec * d[i].z, ec * d[i].w);
+#pragma unroll 4
       for (int j = 0; j < C; ++j) {
-        const float4 o = f4(&s.dO[j][c0]), r = f4(&s.dR[j][c0]);
+        const float4 o = f4(&s.dO[j][c0]), x = f4(&s.dR[j][c0]);
+        const float4 q = f4(&s.Q[j][k0]), k = f4(&s.K[j][k0]);
         const float fq = a.scale * s.g.eg[j], fk = -s.g.eg[j];
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 q = f4(&s.Q[j][k0 + i]), k = f4(&s.K[j][k0 + i]);
-          axpy4(d[i], fq * q.x, o); axpy4(d[i + 1], fq * q.y, o); axpy4(d[i + 2], fq * q.z, o); axpy4(d[i + 3], fq * q.w, o);
-          axpy4(d[i], fk * k.x, r); axpy4(d[i + 1], fk * k.y, r); axpy4(d[i + 2], fk * k.z, r); axpy4(d[i + 3], fk * k.w, r);
-        }
+        axpy4(d[0], fq * q.x, o); axpy4(d[1], fq * q.y, o); axpy4(d[2], fq * q.z, o); axpy4(d[3], fq * q.w, o);
+        axpy4(d[0], fk * k.x, x); axpy4(d[1], fk * k.y, x); axpy4(d[2], fk * k.z, x); axpy4(d[3], fk * k.w, x);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f4(&s.dS[k0 + i][c0]) = d[i];  // (a thread's own)
+      for (int i = 0; i < 4; ++i) f4(&s.dS[k0 + i][c0]) = d[i];
     }
   }
-  __syncthreads();
-  if (a.ds_in)
-    for (int i = tid; i < a.DK * a.DV; i += 256)
-      a.ds_in[(size_t)blockIdx.x * a.DK * a.DV + i] = s.dS[i / a.DV][i % a.DV];
+  if (a.ds_in && vok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (k0 + i < a.DK) f4(a.ds_in + ((size_t)bh * a.DK + k0 + i) * a.DV + v0 + c0) = d[i];
+  }
 }
 
 __global__ void __launch_bounds__(256) m3_delta_bwd_grad_kernel(const __grid_constant__ DeltaArgs a) {
@@ -539,14 +527,14 @@ __global__ void __launch_bounds__(256) m3_delta_share_kernel(const __grid_consta
 }
 
 cudaError_t launch_delta_bwd(const DeltaArgs& a, cudaStream_t st) {
-  const struct { void (*kern)(DeltaArgs); size_t smem; unsigned blocks; } steps[] = {
-      {m3_delta_bwd_prep_kernel, sizeof(PrepSmem), (unsigned)(a.B * a.Hv * a.nc)},
-      {m3_delta_bwd_rev_kernel, sizeof(RevSmem), (unsigned)(a.B * a.Hv)},
-      {m3_delta_bwd_grad_kernel, sizeof(GradSmem), (unsigned)(a.B * a.Hv * a.nc)}};
+  const struct { void (*kern)(DeltaArgs); size_t smem; unsigned x, y; } steps[] = {
+      {m3_delta_bwd_prep_kernel, sizeof(PrepSmem), (unsigned)(a.B * a.Hv * a.nc), 1},
+      {m3_delta_bwd_rev_kernel, sizeof(RevSmem), (unsigned)(a.B * a.Hv), DMAX / RV},
+      {m3_delta_bwd_grad_kernel, sizeof(GradSmem), (unsigned)(a.B * a.Hv * a.nc), 1}};
   for (const auto& s : steps) {
     // (the attribute belongs to the current context, and setting it costs under a microsecond)
     cudaError_t e = cudaFuncSetAttribute(s.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
-    if (e == cudaSuccess) e = launch_k(s.kern, dim3(s.blocks), 256, s.smem, st, false, a);
+    if (e == cudaSuccess) e = launch_k(s.kern, dim3(s.x, s.y), 256, s.smem, st, false, a);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
