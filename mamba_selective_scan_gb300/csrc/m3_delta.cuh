@@ -35,7 +35,7 @@ struct DeltaArgs {
   const float *s_in, *ckpt_in, *ds_out;  // state in, checkpoints and d(state out) of the backward
   void *o, *dq, *dk, *dv, *dg, *dbeta;
   float *s_out, *ckpt, *ds_in;
-  float *pdq, *pdk;  // shared heads: f32 per-value-head shares of dq, dk [B, T, Hv, dk]; bf16 (pdq) running sums per block
+  float *pdq, *pdk;  // f32, shared heads: per-value-head shares of dq, dk [B, T, Hv, dk]
   int64_t qs, ks, vs, dqs, dks, dvs;  // elements between tokens
   int B, T, Hk, Hv, DK, DV, share;
   int chunk, nc;

@@ -110,9 +110,9 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   off = mark;
   p->o_bwd = take(chunks * (tc ? TC_BWD : F32_KEPT));
   const bool shared = p->Hv != p->Hk;
-  const size_t share_bytes = (size_t)p->B * p->T * p->Hv * p->DK * 4;
-  p->o_pdq = take(!shared ? 0 : tc ? (size_t)TC_BLOCKS * TC * DMAX * 2 * 4 : share_bytes);
-  p->o_pdk = take(shared && !tc ? share_bytes : 0);
+  const size_t share_bytes = shared && !tc ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
+  p->o_pdq = take(share_bytes);
+  p->o_pdk = take(share_bytes);
   p->ws_bytes = off > p->fwd_ws_bytes ? off : p->fwd_ws_bytes;
   const bool empty = p->B == 0 || p->T == 0;
   const int walk = p->segs > 1 ? 3 : 1;  // (shares: and a memset of their flags)

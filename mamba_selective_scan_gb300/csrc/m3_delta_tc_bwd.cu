@@ -471,7 +471,7 @@ struct Smem {  // at SMALL
   float ec, tot;
   uint64_t ds, dl, us, kq;           // arrived: dS hi; dS lo; U, dR, dO, S0; K, Q
   uint64_t mb1, mb2, mb3;            // done: K Q^T (and all before it); G, dP, Yo, Y, Z; the products with P2 and A2
-  uint64_t rdy0, rdy1, rdya, rdy2;   // see the issuing warp
+  uint64_t rdy0, rdy1, rdya;   // see the issuing warp
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -557,7 +557,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 
   if (tid == 0) {
     for (uint64_t* r : {&s.ds, &s.dl, &s.us, &s.kq, &s.mb1, &s.mb2, &s.mb3}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy0, &s.rdy1, &s.rdya, &s.rdy2}) mbar_init(r, EPI / 32);
+    for (uint64_t* r : {&s.rdy0, &s.rdy1, &s.rdya}) mbar_init(r, EPI / 32);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc(&s.tmem, 512);
@@ -617,7 +617,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         // while the last item's outputs are still being written
         wait(&s.us, par);
         wait(&s.ds, par);
-        if (n > 0) wait(&s.rdya, par ^ 1);  // its G, dP, Yo, Y and Z are read
+        if (n > 0) wait(&s.rdya, par ^ 1);  // its G, dP, Yo, Y, Z, K and Q are read
         if (wait.ok) {
           tmem_fence_after_sync();
           mma(T_G, 8, MM, true, kept(U), kept(DR));
@@ -630,10 +630,6 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           mma(T_YO, 8, MN, true, kept(S0), kmaj(DO, TILE));
           mma(T_Y, 8, MM, true, kept(S0), kept(DR));
           mma(T_Y, 8, MM, false, kept(S0), kept(DR + 16384));
-        }
-        if (n > 0) {
-          wait(&s.rdy2, par ^ 1);  // its K and Q are read
-          if (m == 0 && wait.ok) load_kq(it);  // (else they are this item's too)
         }
         wait(&s.dl, par);
         if (wait.ok) {
@@ -662,8 +658,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         if (wait.ok) {
           tmem_fence_after_sync();
           for (int p = 0; p < 2; ++p) {
-            mma(T_DQ, 4, MN, p == 0, mn(KQ, 2 * TILE), kmaj(P2 + p * TILE, 0));
-            mma(T_DK, 4, MM, p == 0, mn(KQ + TILE, 2 * TILE), mn(P2 + p * TILE, 16));
+            mma(T_DQ, 4, MN, p + m == 0, mn(KQ, 2 * TILE), kmaj(P2 + p * TILE, 0));
+            mma(T_DK, 4, MM, p + m == 0, mn(KQ + TILE, 2 * TILE), mn(P2 + p * TILE, 16));
             mma(T_DK, 4, MN, false, mn(KQ, 2 * TILE), kmaj(A2 + p * TILE, 0));
             mma(T_DK, 4, MM, false, mn(KQ, 2 * TILE), mn(A2 + p * TILE, 16));
           }
@@ -671,6 +667,10 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         }
         wait(&s.mb3, par);
         if (more && wait.ok) load_dl(it);
+        if (more && it.m == 0) {  // (else K and Q are the next item's too)
+          wait(&s.rdya, par);     // and read
+          if (wait.ok) load_kq(it);
+        }
       }
       if (!wait.ok) {  // as in the other kernels: copies in flight land first
         if (n_ds) mbar_wait(&s.ds, (n_ds - 1) & 1);
@@ -688,13 +688,17 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // element `row` (a head_k index) of token j of this quarter, K or Q
+    // elements `row` (a head_k index) of tokens 2 j and 2 j + 1 of this
+    // quarter, K (0) or Q (1), as their bf16 pair
     const uint32_t el = sb + KQ + (row >> 6) * 2 * TILE + (row & 7) * 2;
     auto tok = [&](int q, int j) {
-      uint16_t v;
-      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(el + q * TILE + sw(qt * 16 + j, (row & 63) >> 3)));
-      return __uint_as_float((uint32_t)v << 16);
+      uint16_t v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v[e]) : "r"(el + q * TILE + sw(qt * 16 + 2 * j + e, (row & 63) >> 3)));
+      return (uint32_t)v[0] | (uint32_t)v[1] << 16;
     };
+    auto wide = [](uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)); };
     uint32_t par = 0, pkq = 0;
     for (GradItem it(a, blockIdx.x); it.group < groups; it.next(a), par ^= 1) {
       const int c = it.c, b = it.b, h = it.h;
@@ -852,13 +856,15 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       wait(&s.mb2, par);
       tmem_fence_after_sync();
       float2 dq[8], dk[8];
+      uint32_t qv[8], kv[8];  // (kept: shared memory is busy with the next item's products when they are wanted again)
       {
         float y[16];
-        float2 x[8], kv[8];
+        float2 x[8];
         tc_ld16(tl + T_YO, dq);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 p = __fmul2_rn(dq[j], make_float2(tok(1, 2 * j), tok(1, 2 * j + 1)));
+          qv[j] = tok(1, j);
+          const float2 p = __fmul2_rn(dq[j], wide(qv[j]));
           y[2 * j] = p.x;
           y[2 * j + 1] = p.y;
         }
@@ -866,11 +872,12 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         if (!(lane & 1)) s.dot[0][wq][qt * 16 + (lane >> 1)] = t;
         tc_ld16(tl + T_Y, dk);
         tc_ld16(tl + T_Z, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) kv[j] = tok(0, j);
         ready(&s.rdya);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          kv[j] = make_float2(tok(0, 2 * j), tok(0, 2 * j + 1));
-          const float2 p = __fmul2_rn(dk[j], kv[j]);
+          const float2 p = __fmul2_rn(dk[j], wide(kv[j]));
           y[2 * j] = p.x;
           y[2 * j + 1] = p.y;
         }
@@ -878,7 +885,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         if (!(lane & 1)) s.dot[1][wq][qt * 16 + (lane >> 1)] = t;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float2 p = __fmul2_rn(x[j], kv[j]);
+          const float2 p = __fmul2_rn(x[j], wide(kv[j]));
           y[2 * j] = p.x;
           y[2 * j + 1] = p.y;
         }
@@ -901,8 +908,8 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         const float ca = (s.col_a[0][i] + s.col_a[1][i]) + (s.col_a[2][i] + s.col_a[3][i]), rah = s.row_a[0][i] + s.row_a[1][i];
         const float be = s.beta[i], ra = be * rah;
         const float yo = s.fq[i] * dot[0], y = s.bfx[i] * dot[1], z = s.fu[i] * dot[2];
-        s.cq[i] = L2 ? s.nq[i] * s.nq[i] * (yo + rp) : 0.0f;
-        s.ck[i] = L2 ? s.nk[i] * s.nk[i] * (z - y + cp + ra + ca) : 0.0f;
+        s.cq[i] = L2 ? -s.nq[i] * s.nq[i] * (yo + rp) : 0.0f;
+        s.ck[i] = L2 ? -s.nk[i] * s.nk[i] * (z - y + cp + ra + ca) : 0.0f;
         s.d[i] = (rp - cp) + (ra - ca) + yo - y - z;
         s.z[i] = z;
         if (i < n) {
@@ -961,47 +968,48 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           const Vec16 cq{&s.cq[qt * 16]}, ck{&s.ck[qt * 16]};
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 q = make_float2(-tok(1, 2 * j), -tok(1, 2 * j + 1)), k = make_float2(-tok(0, 2 * j), -tok(0, 2 * j + 1));
-            dq[j] = __ffma2_rn(cq[j], q, dq[j]);
-            dk[j] = __ffma2_rn(ck[j], k, dk[j]);
+            dq[j] = __ffma2_rn(cq[j], wide(qv[j]), dq[j]);  // (cq, ck are negative)
+            dk[j] = __ffma2_rn(ck[j], wide(kv[j]), dk[j]);
           }
         }
       }
-      ready(&s.rdy2);
-      // value heads that share a key head: their sum so far, in a place of
-      // this thread's own that stays in L2
-      if (a.share > 1) {
-        float4* acc = reinterpret_cast<float4*>(a.pdq) + (size_t)blockIdx.x * 8 * EPI + tid;
-        if (it.m > 0) {
+      // value heads that share a key head: their sum so far goes back to where
+      // the next one's products with P2 and A2 are added to it
+      if (it.m + 1 < a.share) {
+        auto put = [&](uint32_t at, const float2 (&v)[8]) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 x = acc[j * EPI], y = acc[(4 + j) * EPI];
-            dq[2 * j] = __fadd2_rn(dq[2 * j], make_float2(x.x, x.y));
-            dq[2 * j + 1] = __fadd2_rn(dq[2 * j + 1], make_float2(x.z, x.w));
-            dk[2 * j] = __fadd2_rn(dk[2 * j], make_float2(y.x, y.y));
-            dk[2 * j + 1] = __fadd2_rn(dk[2 * j + 1], make_float2(y.z, y.w));
-          }
-        }
-        if (it.m + 1 < a.share) {
+          for (int p = 0; p < 2; ++p) {
+            uint32_t x[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[j * EPI] = make_float4(dq[2 * j].x, dq[2 * j].y, dq[2 * j + 1].x, dq[2 * j + 1].y);
-            acc[(4 + j) * EPI] = make_float4(dk[2 * j].x, dk[2 * j].y, dk[2 * j + 1].x, dk[2 * j + 1].y);
+            for (int j = 0; j < 4; ++j) {
+              x[2 * j] = __float_as_uint(v[4 * p + j].x);
+              x[2 * j + 1] = __float_as_uint(v[4 * p + j].y);
+            }
+            tc_st8(tl + at + p * 8, x);
           }
-          continue;
-        }
+        };
+        put(T_DQ, dq);
+        put(T_DK, dk);
+        tmem_wait_st();  // (behind this thread's next arrival at rdy1)
+        continue;
       }
-      if (row < a.DK) {
-        const int64_t t0 = tok0 + qt * 16;
-        const int left = n - qt * 16;
-        __nv_bfloat16* qp = static_cast<__nv_bfloat16*>(a.dq) + t0 * a.dqs + (int64_t)it.hk * a.DK + row;
-        __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.dk) + t0 * a.dks + (int64_t)it.hk * a.DK + row;
+      tmem_fence_before_sync();
+      // out, two neighbours of a token at a time: an even lane takes the even
+      // tokens of its pair of rows, the odd lane the odd ones
+      const int row2 = row & ~1, odd = row & 1;
+      const bool in = row2 < a.DK;  // (head_k is even)
+      __nv_bfloat16* qp = static_cast<__nv_bfloat16*>(a.dq) + (tok0 + qt * 16 + odd) * a.dqs + (int64_t)it.hk * a.DK + row2;
+      __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(a.dk) + (tok0 + qt * 16 + odd) * a.dks + (int64_t)it.hk * a.DK + row2;
+      const int left = n - qt * 16 - odd;
 #pragma unroll
-        for (int j = 0; j < 16; ++j, qp += a.dqs, kp += a.dks)
-          if (j < left) {
-            *qp = __float2bfloat16_rn(j & 1 ? dq[j >> 1].y : dq[j >> 1].x);
-            *kp = __float2bfloat16_rn(j & 1 ? dk[j >> 1].y : dk[j >> 1].x);
-          }
+      for (int j = 0; j < 8; ++j, qp += 2 * a.dqs, kp += 2 * a.dks) {
+        const float oq = __shfl_xor_sync(~0u, odd ? dq[j].x : dq[j].y, 1), ok = __shfl_xor_sync(~0u, odd ? dk[j].x : dk[j].y, 1);
+        const __nv_bfloat162 q2 = odd ? __floats2bfloat162_rn(oq, dq[j].y) : __floats2bfloat162_rn(dq[j].x, oq);
+        const __nv_bfloat162 k2 = odd ? __floats2bfloat162_rn(ok, dk[j].y) : __floats2bfloat162_rn(dk[j].x, ok);
+        if (in && 2 * j < left) {
+          *reinterpret_cast<__nv_bfloat162*>(qp) = q2;
+          *reinterpret_cast<__nv_bfloat162*>(kp) = k2;
+        }
       }
     }
   }
