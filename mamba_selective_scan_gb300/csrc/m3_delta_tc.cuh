@@ -268,9 +268,11 @@ __device__ __forceinline__ void tma_tile_store(const CUtensorMap* map, uint32_t 
 
 // The chain kernels' grid: a block per (head, segment), or one per SM in
 // equal shares.  Those wait for a state that the block before hands over, so
-// they are launched cooperatively (all of them resident at once).
+// they are launched cooperatively (all of them resident at once).  Otherwise,
+// with `pdl`, the blocks may come up while the kernel before them ends.
 template <typename... Args, typename... Vals>
-cudaError_t launch_delta_blocks(void (*kern)(Args...), const DeltaArgs& a, int threads, size_t smem, cudaStream_t st, Vals... maps) {
+cudaError_t launch_delta_blocks(void (*kern)(Args...), const DeltaArgs& a, int threads, size_t smem, cudaStream_t st, bool pdl,
+                                Vals... maps) {
   cudaLaunchConfig_t cfg{};
   int sms = 0;
   cudaError_t e = sm_count(&sms);
@@ -280,10 +282,15 @@ cudaError_t launch_delta_blocks(void (*kern)(Args...), const DeltaArgs& a, int t
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
+  if (a.stream) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = a.stream ? 1 : 0;
+  cfg.numAttrs = a.stream || pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, a, maps...);
 }
 

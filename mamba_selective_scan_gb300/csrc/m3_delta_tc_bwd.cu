@@ -438,7 +438,7 @@ cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
     if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
-    if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, mq, mk, md, mv);
+    if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, false, mq, mk, md, mv);
     return e;
   };
   return go(m3_delta_tc_rev_kernel<true>, m3_delta_tc_rev_kernel<false>);
@@ -606,6 +606,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       constexpr uint32_t NN = tc_idesc(128, 64, false, false), NM = tc_idesc(128, 64, false, true),
                          MN = tc_idesc(128, 64, true, false), MM = tc_idesc(128, 64, true, true);
       GradItem it(a, blockIdx.x);
+      grid_dep_wait();  // the reverse pass is done
       load_us(it);
       load_ds(it);
       load_dl(it);
@@ -1032,7 +1033,7 @@ cudaError_t launch_delta_tc_grad(const DeltaArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t groups = (int64_t)a.B * a.Hk * a.nc;
   if (sms > TC_BLOCKS) sms = TC_BLOCKS;
-  return launch_k(kern, dim3((unsigned)(groups < sms ? groups : sms)), grad::THREADS, grad::SMEM_BYTES, st, false, a, mq, mk, md);
+  return launch_k(kern, dim3((unsigned)(groups < sms ? groups : sms)), grad::THREADS, grad::SMEM_BYTES, st, true, a, mq, mk, md);
 }
 
 }  // namespace m3

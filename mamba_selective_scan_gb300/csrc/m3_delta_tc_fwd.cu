@@ -141,6 +141,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         bulk_commit();
         bulk_wait_read();
       };
+      grid_dep_wait();  // T, P and the factors are there
       for (int n = 0; n < 2; ++n) {
         load_kq(n);
         load_v(n);
@@ -806,7 +807,7 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
   }
   if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_delta_tc_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
-  if (e == cudaSuccess) e = launch_delta_blocks(m3_delta_tc_fwd_kernel, a, THREADS, SMEM_BYTES, st, mq, mk, mv, mo);
+  if (e == cudaSuccess) e = launch_delta_blocks(m3_delta_tc_fwd_kernel, a, THREADS, SMEM_BYTES, st, a.segs == 1, mq, mk, mv, mo);
   return e;
 }
 

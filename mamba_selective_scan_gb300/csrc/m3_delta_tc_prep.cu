@@ -124,6 +124,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t acc = __shfl_sync(~0u, slot, 0);
+  grid_dep_trigger();  // the chain's blocks may come up (they need this block's tensor memory only once it is given back)
   if (wp == 0 && elect_one()) {
     mbar_expect_tx(&full, 4 * TILE);
 #pragma unroll
