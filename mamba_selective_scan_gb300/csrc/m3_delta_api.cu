@@ -51,8 +51,9 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
 // kernel chains them (eight blocks per head, 1.6 units per segment), then all
 // S run; the two extra launches and their first loads are four units.  The
 // count with the least total is taken, with at least four chunks per segment.
-// 1 x 65536 x 16 heads: nine segments, 0.96 ms against 3.0 ms for one; 36
-// heads of 24 chunks: about the same in one and in three (measured for both).
+// 1 x 65536 x 16 heads: nine segments, 0.89 ms, where one would take 1024
+// chunks one after the other, some 3 ms; 36 heads of 24 chunks: about the same
+// in one and in three (measured for both).
 void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
   constexpr int64_t SMS = 152;
   double best = 0.0;

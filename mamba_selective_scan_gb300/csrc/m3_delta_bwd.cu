@@ -16,7 +16,10 @@
 // and each exponent gam_i that a term carries takes that term's share; dg is
 // their sum from the end of the chunk.  Only rev goes from chunk to chunk:
 // prep and grad run over all chunks at once, what they share with rev is in
-// the workspace (8 x 128 x 4 heads: see the kernels' times below).
+// the workspace.  8 x 128 x 4 heads of 128 x 128: 17, 50 and 43 us, bound by
+// latency (128 blocks, four chunks one after the other in rev).  With 128
+// columns per block in rev (32 blocks) the training pass took 174 us instead of
+// 141.
 #include "m3_delta.cuh"
 
 namespace m3 {

