@@ -45,6 +45,7 @@ struct DeltaArgs {
   unsigned* flags;       // stream: [B Hv], set once a head's state was handed over (in seg_start)
   int segs, seg_chunks;  // else: time segments, chunks per segment
   float *seg_end, *seg_phi, *seg_start;  // [B Hv][segs][128][128]: zero-start ends, transitions, start states
+  float* seg_keep;     // with checkpoints: the transitions' transposes, which are the adjoint's transitions
   unsigned char* bwd;  // [B Hv][nc] of TC_BWD (f32: F32_KEPT) bytes
   unsigned char* tp;   // TcPrep of every chunk, tp_stride bytes apart (in the checkpoints, or the workspace)
   size_t tp_stride;
@@ -55,6 +56,7 @@ struct DeltaPlan {
   int B, T, Hk, Hv, DK, DV, chunk, nc;
   size_t ckpt_bytes, fwd_ws_bytes, ws_bytes;  // (the forward's part comes first)
   size_t o_pdq, o_pdk, o_end, o_phi, o_start, o_bwd, o_flags, o_tp;  // workspace offsets
+  size_t o_keep;  // in the checkpoints
   bool stream;           // more heads than SMs: equal shares instead of segments
   int segs, seg_chunks;  // time segments
   int fwd_launches, bwd_launches;

@@ -99,6 +99,8 @@ m3_status delta_plan(const m3_delta_dims* d, m3_dtype act, DeltaPlan* p) {
   p->stream = tc && heads > 152 && p->nc > 0;
   if (tc && !p->stream) delta_segments(heads, p->nc, &p->segs, &p->seg_chunks);
   const size_t seg_bytes = p->segs > 1 ? (size_t)p->B * p->Hv * p->segs * DMAX * DMAX * 4 : 0;
+  p->o_keep = p->ckpt_bytes;  // the segments' transitions, behind the chunks' checkpoints
+  p->ckpt_bytes += seg_bytes;
   p->o_end = take(seg_bytes);
   p->o_phi = take(seg_bytes);
   p->o_start = take(p->stream ? (size_t)heads * DMAX * DMAX * 4 : seg_bytes);
@@ -156,6 +158,7 @@ void delta_ws(DeltaArgs& a, const DeltaPlan& p, void* workspace) {
   const void* ck = a.ckpt ? a.ckpt : a.ckpt_in;
   a.tp = ck ? static_cast<unsigned char*>(const_cast<void*>(ck)) + 65536 : ws + p.o_tp;
   a.tp_stride = ck ? TC_CKPT : TC_PREP;
+  a.seg_keep = ck ? reinterpret_cast<float*>(static_cast<unsigned char*>(const_cast<void*>(ck)) + p.o_keep) : nullptr;
 }
 
 // `aligned` for a list; NULL passes (presence is checked apart)

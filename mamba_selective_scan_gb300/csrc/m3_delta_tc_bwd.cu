@@ -59,7 +59,7 @@ constexpr uint32_t T_Y = 320;  // fq dO as hi, lo
 //
 // It leaves dS (at each chunk's end) and dR for the gradients' kernel, which
 // has no order among chunks.  AGG: a segment's effect on the adjoint, from
-// zero (blockIdx.z 0) and from the identity with dO = 0 (blockIdx.z 1).
+// zero (the transition is the forward's, transposed).
 //
 // Bound like the forward by a chunk's dependent products, 4.3 us (24 chunks of
 // 36 heads: 104 us), and with every SM at work by what it reads and writes
@@ -82,7 +82,6 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   TcWalk walk(a, 0);
   if (!a.stream) walk.n = walk.len_a = n_seg;
   auto chunk = [&](const TcStep& t) { return a.stream ? a.nc - 1 - t.c : c_seg + n_seg - 1 - t.c; };
-  const bool ident = AGG && blockIdx.z == 1;
   const uint32_t st0 = smem_u32(base);
 
   if (tid == 0) {
@@ -243,7 +242,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (AGG) {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          S[k] = make_float2(ident && qt * 32 + 2 * k == row ? 1.0f : 0.0f, ident && qt * 32 + 2 * k + 1 == row ? 1.0f : 0.0f);
+          S[k] = f2b(0.0f);
         return;
       }
       if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
@@ -263,13 +262,6 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       bool own = true;
       if (AGG) {
         dst = a.seg_end + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX;
-        if (ident) {  // by rows of the transition
-          float* o = a.seg_phi + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2)
-            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
-          return;
-        }
       } else if (t.give) {
         dst = a.seg_start + (size_t)t.bh * DMAX * DMAX;
       } else if (a.ds_in && chunk(t) == 0) {
@@ -352,8 +344,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          x[j] = ident ? f2b(0.0f)
-                       : __fmul2_rn(make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16)), fq[j]);
+          x[j] = __fmul2_rn(make_float2(__uint_as_float(v[2 * j] << 16), __uint_as_float(v[2 * j + 1] << 16)), fq[j]);
         put_tokens(T_Y, x, nullptr);
         ready(&s.rdy_y);
       }
@@ -366,7 +357,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         float2 z[8];
         tc_ld16(tl + T_Z + qt * 16, z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __ffma2_rn(x[j], fu[j], ident ? f2b(0.0f) : z[j]);
+        for (int j = 0; j < 8; ++j) x[j] = __ffma2_rn(x[j], fu[j], z[j]);
       }
       put_tokens(T_R, x, nullptr);
       ready(&s.rdy_r);
@@ -437,7 +428,7 @@ cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
     if (a.segs > 1) {
       e = cudaFuncSetAttribute(agg, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
       if (e == cudaSuccess)
-        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1), 2), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md, mv);
+        e = launch_k(agg, dim3(heads, (unsigned)(a.segs - 1)), rev::THREADS, rev::SMEM_BYTES, st, false, a, mq, mk, md, mv);
       if (e == cudaSuccess) e = launch_delta_seg(a, a.ds_out, true, st);
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);

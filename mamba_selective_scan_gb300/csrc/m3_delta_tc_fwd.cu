@@ -508,7 +508,9 @@ constexpr uint32_t A_S = 0, A_X = 128, A_R = 192;
 // m3_delta_tc_fwd_kernel without outputs, twice in one block, from a zero
 // state (N) and from the identity with V = 0 (the rows of Phi).  The two use
 // the same tiles and take turns: one's products run under the other's
-// register work.  3.1 us per chunk for both (128 segments of 114 chunks: 350
+// register work.  With checkpoints Phi is kept for the backward, transposed:
+// it takes the adjoint of a segment's end to the adjoint of its start.  3.1 us
+// per chunk for both (128 segments of 114 chunks: 350
 // us); with a block for each, 1 x 65536 x 16 heads took 1.20 ms instead of
 // 0.96.
 __global__ void __launch_bounds__(agg::THREADS, 1)
@@ -725,13 +727,18 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         if (n + 1 < N) put_state(m);
       }
     }
-    // N as [head_k][row], Phi by its rows
+    // N as [head_k][row], Phi by its rows (and by its columns for the backward)
     float* end = a.seg_end + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
     float* phi = a.seg_phi + ((size_t)bh * a.segs + seg) * DMAX * DMAX + (size_t)row * DMAX + qt * 32;
 #pragma unroll
     for (int k = 0; k < 32; ++k) end[(size_t)(qt * 32 + k) * DMAX + row] = k & 1 ? S[0][k >> 1].y : S[0][k >> 1].x;
 #pragma unroll
     for (int k = 0; k < 16; k += 2) *reinterpret_cast<float4*>(phi + 2 * k) = make_float4(S[1][k].x, S[1][k].y, S[1][k + 1].x, S[1][k + 1].y);
+    if (a.seg_keep) {
+      float* keep = a.seg_keep + ((size_t)bh * a.segs + seg) * DMAX * DMAX;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) keep[(size_t)(qt * 32 + k) * DMAX + row] = k & 1 ? S[1][k >> 1].y : S[1][k >> 1].x;
+    }
   }
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
   tmem_fence_before_sync();
@@ -754,10 +761,11 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
   __shared__ __align__(8) uint64_t full[2];
   const int tid = threadIdx.x, bh = blockIdx.x, k = tid & (DMAX - 1), vq = (tid >> 7) * 4, v = blockIdx.y * 16 + vq;
   auto where = [&](int n) { return ((size_t)bh * a.segs + (rev ? a.segs - 1 - n : n)) * DMAX * DMAX; };
+  const float* phis = rev ? a.seg_keep : a.seg_phi;
   auto load = [&](int n) {
     if (n + 1 >= a.segs) return;
     mbar_expect_tx(&full[n & 1], SEG_PHI);
-    bulk_load(smem_u32(raw) + (n & 1) * SEG_PHI, a.seg_phi + where(n), SEG_PHI, &full[n & 1]);
+    bulk_load(smem_u32(raw) + (n & 1) * SEG_PHI, phis + where(n), SEG_PHI, &full[n & 1]);
   };
   if (tid == 0) {
     mbar_init(&full[0], 1);
@@ -807,7 +815,8 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
   if (a.segs > 1) {
     e = cudaFuncSetAttribute(m3_delta_tc_agg_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)agg::SMEM_BYTES);
     if (e == cudaSuccess)
-      e = launch_k(m3_delta_tc_agg_kernel, dim3(heads, (unsigned)(a.segs - 1)), agg::THREADS, agg::SMEM_BYTES, st, false, a, mk, mv);
+      // (the last segment's effect is wanted by the backward only)
+      e = launch_k(m3_delta_tc_agg_kernel, dim3(heads, (unsigned)(a.segs - (a.seg_keep ? 0 : 1))), agg::THREADS, agg::SMEM_BYTES, st, false, a, mk, mv);
     if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
   }
   if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_delta_tc_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
