@@ -754,12 +754,14 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
 // one bulk copy while the one before is used (16 heads of nine segments: 38
 // us, latency; 2 x 8 values per thread in half the blocks was slower).
 constexpr int SEG_PHI = DMAX * DMAX * 4;
-constexpr size_t SEG_SMEM = 2 * SEG_PHI + 128;
+constexpr size_t SEG_SMEM = 2 * SEG_PHI + 4 * 16 * DMAX * 4;  // and the quarters' sums [4][16][128]
 __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
   extern __shared__ __align__(128) unsigned char raw[];
   __shared__ __align__(16) float S[DMAX][16];
   __shared__ __align__(8) uint64_t full[2];
   const int tid = threadIdx.x, bh = blockIdx.x, k = tid & (DMAX - 1), vq = (tid >> 7) * 4, v = blockIdx.y * 16 + vq;
+  const int lane = tid & 31, vg = (tid >> 5 & 3) * 4;
+  float* part = reinterpret_cast<float*>(raw + 2 * SEG_PHI);
   auto where = [&](int n) { return ((size_t)bh * a.segs + (rev ? a.segs - 1 - n : n)) * DMAX * DMAX; };
   const float* phis = rev ? a.seg_keep : a.seg_phi;
   auto load = [&](int n) {
@@ -780,18 +782,33 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
   TcWait wait;
   for (int n = 0; n + 1 < a.segs; ++n) {
     x = *reinterpret_cast<const float4*>(a.seg_end + where(n) + (size_t)k * DMAX + v);
-    __syncthreads();
+    __syncthreads();  // S
     wait(&full[n & 1], (n >> 1) & 1);
-    const float* phi = reinterpret_cast<const float*>(raw + (n & 1) * SEG_PHI) + k;  // Phi[r][k]
-#pragma unroll 16
-    for (int r = 0; r < DMAX; ++r) {
-      const float4 y = *reinterpret_cast<const float4*>(&S[r][vq]);
-      const float p = phi[r * DMAX];
-      x.x = fmaf(p, y.x, x.x); x.y = fmaf(p, y.y, x.y);
-      x.z = fmaf(p, y.z, x.z); x.w = fmaf(p, y.w, x.w);
+    // a quarter of the rows per 128 threads, four by four values per thread
+    const float* phi = reinterpret_cast<const float*>(raw + (n & 1) * SEG_PHI) + (tid >> 7) * 32 * DMAX + lane * 4;  // Phi[r][..]
+    const float* sr = &S[(tid >> 7) * 32][vg];
+    float2 acc[4][2] = {};
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const float4 y = *reinterpret_cast<const float4*>(sr + r * 16), f = *reinterpret_cast<const float4*>(phi + r * DMAX);
+      const float yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i][0] = __ffma2_rn(make_float2(f.x, f.y), f2b(yv[i]), acc[i][0]);
+        acc[i][1] = __ffma2_rn(make_float2(f.z, f.w), f2b(yv[i]), acc[i][1]);
+      }
     }
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4*>(part + ((tid >> 7) * 16 + vg + i) * DMAX + lane * 4) =
+          make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+    __syncthreads();  // the quarters; S and Phi are read
     if (tid == 0 && wait.ok) load(n + 2);
+    auto sum = [&](int i) {
+      const float* q = part + (vq + i) * DMAX + k;
+      return (q[0] + q[16 * DMAX]) + (q[32 * DMAX] + q[48 * DMAX]);
+    };
+    x.x += sum(0); x.y += sum(1); x.z += sum(2); x.w += sum(3);
     *reinterpret_cast<float4*>(&S[k][vq]) = x;
     *reinterpret_cast<float4*>(a.seg_start + where(n + 1) + (size_t)k * DMAX + v) = x;
   }
