@@ -98,6 +98,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
+  grid_dep_trigger();
   TcWait wait;
 
   if (warp == CHAIN / 32 + 1) {
@@ -324,6 +325,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     };
 
     TcStep t = walk.at(0);
+    if (!AGG) grid_dep_wait();  // the segments' adjoints are there (the rest is the forward's, or the caller's)
     get_state(t);
     put_state(t);
     for (int n = 0; n < walk.n; ++n) {
@@ -433,7 +435,7 @@ cudaError_t launch_delta_tc_rev(const DeltaArgs& a, cudaStream_t st) {
     }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fin, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rev::SMEM_BYTES);
     if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
-    if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, false, mq, mk, md, mv);
+    if (e == cudaSuccess) e = launch_delta_blocks(fin, a, rev::THREADS, rev::SMEM_BYTES, st, a.segs > 1, mq, mk, md, mv);
     return e;
   };
   return go(m3_delta_tc_rev_kernel<true>, m3_delta_tc_rev_kernel<false>);

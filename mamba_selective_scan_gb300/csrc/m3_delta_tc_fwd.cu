@@ -143,7 +143,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         bulk_commit();
         bulk_wait_read();
       };
-      grid_dep_wait();  // T, P and the factors are there
+      grid_dep_wait();  // what the kernels before this one leave is there
       for (int n = 0; n < 2; ++n) {
         load_kq(n);
         load_v(n);
@@ -354,6 +354,7 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
     };
 
     TcStep t = walk.at(0);
+    grid_dep_wait();  // the segments' states, too
     get_state(t);
     put_state(t);
     for (int n = 0; n < walk.n; ++n) {
@@ -538,6 +539,7 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
+  grid_dep_trigger();
   TcWait wait;
 
   if (warp == CHAIN / 32 + 1) {
@@ -769,6 +771,8 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
     mbar_expect_tx(&full[n & 1], SEG_PHI);
     bulk_load(smem_u32(raw) + (n & 1) * SEG_PHI, phis + where(n), SEG_PHI, &full[n & 1]);
   };
+  grid_dep_trigger();
+  grid_dep_wait();
   if (tid == 0) {
     mbar_init(&full[0], 1);
     mbar_init(&full[1], 1);
@@ -818,7 +822,7 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
 cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(m3_delta_seg_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SEG_SMEM);
   if (e != cudaSuccess) return e;
-  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), DMAX / 16), 512, SEG_SMEM, st, false, a, first, rev);
+  return launch_k(m3_delta_seg_kernel, dim3((unsigned)(a.B * a.Hv), DMAX / 16), 512, SEG_SMEM, st, true, a, first, rev);
 }
 
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
@@ -833,12 +837,13 @@ cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st) {
     e = cudaFuncSetAttribute(m3_delta_tc_agg_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)agg::SMEM_BYTES);
     if (e == cudaSuccess)
       // (the last segment's effect is wanted by the backward only)
+      // (not launched ahead of the end of the kernel before: blocks that come up one by one as SMs get free run 4 % slower)
       e = launch_k(m3_delta_tc_agg_kernel, dim3(heads, (unsigned)(a.segs - (a.seg_keep ? 0 : 1))), agg::THREADS, agg::SMEM_BYTES, st, false, a, mk, mv);
     if (e == cudaSuccess) e = launch_delta_seg(a, a.s_in, false, st);
   }
   if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_delta_tc_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)heads * 4, st);
-  if (e == cudaSuccess) e = launch_delta_blocks(m3_delta_tc_fwd_kernel, a, THREADS, SMEM_BYTES, st, a.segs == 1, mq, mk, mv, mo);
+  if (e == cudaSuccess) e = launch_delta_blocks(m3_delta_tc_fwd_kernel, a, THREADS, SMEM_BYTES, st, true, mq, mk, mv, mo);
   return e;
 }
 
