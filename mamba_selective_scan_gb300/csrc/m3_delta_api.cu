@@ -48,12 +48,12 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
 // Time segments of the tensor-core chains.  A block per (head, segment) runs
 // one chunk in a unit of time (2.8 us in the forward); with S segments, first
 // the effect of the S - 1 earlier ones is found (1.1 units per chunk), then a
-// kernel chains them (eight blocks per head, 1.6 units per segment), then all
-// S run; the two extra launches and their first loads are four units.  The
+// kernel chains them (eight blocks per head, 1.1 units per segment), then all
+// S run; the two extra launches and their first loads are three units.  The
 // count with the least total is taken, with at least four chunks per segment.
 // 1 x 65536 x 16 heads: nine segments, 0.89 ms, where one would take 1024
-// chunks one after the other, some 3 ms; 36 heads of 24 chunks: about the same
-// in one and in three (measured for both).
+// chunks one after the other, some 3 ms; 36 heads of 24 chunks: four segments,
+// forward and backward 94 and 129 us against 107 and 155 in one.
 void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
   constexpr int64_t SMS = 152;
   double best = 0.0;
@@ -65,7 +65,7 @@ void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {
     const int S = (nc + m - 1) / m;
     const double fin = (double)((heads * S + SMS - 1) / SMS) * m;
     const double agg = S > 1 ? (double)((heads * (S - 1) + SMS - 1) / SMS) * m * 1.1 +
-                                     (double)((heads * 8 + SMS - 1) / SMS) * (S - 1) * 1.6 + 4.0 : 0.0;
+                                     (double)((heads * 8 + SMS - 1) / SMS) * (S - 1) * 1.1 + 3.0 : 0.0;
     if (want == 1 || fin + agg < best - 1e-9) {
       best = fin + agg;
       *segs = S;

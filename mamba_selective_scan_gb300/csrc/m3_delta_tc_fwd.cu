@@ -750,11 +750,12 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
 }
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
-// start[s], 16 columns of the state per block, a row and four columns per
-// thread, f32.  rev: the adjoint's, from the last segment to the first.  The
+// start[s], 16 columns of the state per block, f32.  rev: the adjoint's, from the last segment to the first.  The
 // segments' Phi (64 KB each) do not depend on the states, so each arrives by
-// one bulk copy while the one before is used (16 heads of nine segments: 38
-// us, latency; 2 x 8 values per thread in half the blocks was slower).
+// one bulk copy while the one before is used.  A thread has four by four values
+// over a quarter of the rows, so that shared memory is read twice per sixteen
+// products: 16 heads of nine segments 25 us (38 with four values over all
+// rows), latency and that way through shared memory.
 constexpr int SEG_PHI = DMAX * DMAX * 4;
 constexpr size_t SEG_SMEM = 2 * SEG_PHI + 4 * 16 * DMAX * 4;  // and the quarters' sums [4][16][128]
 __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
