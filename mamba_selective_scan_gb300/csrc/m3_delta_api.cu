@@ -51,7 +51,7 @@ m3_status delta_validate(const m3_delta_dims* d, m3_dtype act) {
 // kernel chains them (eight blocks per head, 1.1 units per segment), then all
 // S run; the two extra launches and their first loads are three units.  The
 // count with the least total is taken, with at least four chunks per segment.
-// 1 x 65536 x 16 heads: nine segments, 0.89 ms, where one would take 1024
+// 1 x 65536 x 16 heads: 19 segments, 0.88 ms, where one would take 1024
 // chunks one after the other, some 3 ms; 36 heads of 24 chunks: four segments,
 // forward and backward 94 and 129 us against 107 and 155 in one.
 void delta_segments(int64_t heads, int nc, int* segs, int* seg_chunks) {

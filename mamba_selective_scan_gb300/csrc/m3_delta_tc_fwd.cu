@@ -511,8 +511,7 @@ constexpr uint32_t A_S = 0, A_X = 128, A_R = 192;
 // the same tiles and take turns: one's products run under the other's
 // register work.  With checkpoints Phi is kept for the backward, transposed:
 // it takes the adjoint of a segment's end to the adjoint of its start.  3.1 us
-// per chunk for both (128 segments of 114 chunks: 350
-// us); with a block for each, 1 x 65536 x 16 heads took 1.20 ms instead of
+// per chunk for both (128 segments of 114 chunks: 350 us); with a block for each, 1 x 65536 x 16 heads took 1.20 ms instead of
 // 0.96.
 __global__ void __launch_bounds__(agg::THREADS, 1)
 m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mk,
@@ -750,12 +749,13 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
 }
 
 // A segment's start state from the ones before: start[s+1] = N_s + Phi_s^T
-// start[s], 16 columns of the state per block, f32.  rev: the adjoint's, from the last segment to the first.  The
-// segments' Phi (64 KB each) do not depend on the states, so each arrives by
-// one bulk copy while the one before is used.  A thread has four by four values
-// over a quarter of the rows, so that shared memory is read twice per sixteen
-// products: 16 heads of nine segments 25 us (38 with four values over all
-// rows), latency and that way through shared memory.
+// start[s], 16 columns of the state per block, f32.  rev: the adjoint's, from
+// the last segment to the first.  The segments' Phi (64 KB each) do not depend
+// on the states, so each arrives by one bulk copy while the one before is
+// used.  A thread has four by four values over a quarter of the rows, so that
+// shared memory is read twice per sixteen products: 16 heads of nine segments
+// 25 us (38 with four values over all rows), latency and that way through
+// shared memory; two blocks per SM, Phi by halves, were no faster.
 constexpr int SEG_PHI = DMAX * DMAX * 4;
 constexpr size_t SEG_SMEM = 2 * SEG_PHI + 4 * 16 * DMAX * 4;  // and the quarters' sums [4][16][128]
 __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant__ DeltaArgs a, const float* first, bool rev) {
