@@ -97,10 +97,24 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) { split2(make_float2(a, b), hi, lo); }
-// values 2 j and 2 j + 1 of 16 consecutive shared-memory floats, as pairs
+// values 2 j and 2 j + 1 of 16 consecutive shared-memory floats, as pairs: read
+// where they are used, or (16-byte aligned) at once by half as many loads,
+// where the registers allow it
 struct Vec16 {
   const float* p;
   __device__ __forceinline__ float2 operator[](int j) const { return *reinterpret_cast<const float2*>(p + 2 * j); }
+};
+struct Reg16 {
+  float2 x[8];
+  __device__ __forceinline__ explicit Reg16(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = reinterpret_cast<const float4*>(p)[i];
+      x[2 * i] = make_float2(t.x, t.y);
+      x[2 * i + 1] = make_float2(t.z, t.w);
+    }
+  }
+  __device__ __forceinline__ float2 operator[](int j) const { return x[j]; }
 };
 // byte offset of the 16-byte unit u of row r in a swizzled tile
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t u) { return r * 128 + ((u ^ (r & 7)) << 4); }

@@ -336,7 +336,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       wait(&s.kq_full[i], (n >> 1) & 1);
       wait(&s.v_full[i], (n >> 1) & 1);
       {  // fq dO
-        const Vec16 fq{&vec(n).fq[qt * 16]};
+        const Reg16 fq{&vec(n).fq[qt * 16]};
         uint32_t v[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -355,7 +355,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        const Vec16 fu{&vec(n).fu[qt * 16]};
+        const Reg16 fu{&vec(n).fu[qt * 16]};
         float2 z[8];
         tc_ld16(tl + T_Z + qt * 16, z);
 #pragma unroll
@@ -368,7 +368,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tmem_fence_after_sync();
       tc_ld16(tl + T_X + qt * 16, x);
       {
-        const Vec16 bx{&vec(n).bfx[qt * 16]};
+        const Reg16 bx{&vec(n).bfx[qt * 16]};
         float2 y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = __fmul2_rn(__fmul2_rn(x[j], f2b(-1.0f)), bx[j]);
@@ -377,7 +377,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       const float2 ec = f2b(vec(n).ec);
       float2 be[8];
       {
-        const Vec16 v{&vec(n).beta[qt * 16]};
+        const Reg16 v{&vec(n).beta[qt * 16]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) be[j] = v[j];  // (the factors are free after this arrival)
       }
@@ -482,14 +482,14 @@ constexpr uint32_t T_YO = 0, T_Y = 64, T_Z = 128, T_DQ = 192, T_DK = 256, T_G = 
 // One head's chunk; a block takes the value heads of a key head's chunk one
 // after the other.
 struct GradItem {
-  int64_t group;
+  uint32_t group;  // (there are fewer than 2^31)
   int b, hk, m, c, h;
   size_t at;  // batch row x value head x chunk
-  __device__ __forceinline__ GradItem(const DeltaArgs& a, int64_t g) { set(a, g); }
-  __device__ __forceinline__ void set(const DeltaArgs& a, int64_t g) {
+  __device__ __forceinline__ GradItem(const DeltaArgs& a, uint32_t g) { set(a, g); }
+  __device__ __forceinline__ void set(const DeltaArgs& a, uint32_t g) {
     group = g;
-    const int bk = (int)(g / a.nc);
-    c = (int)(g % a.nc);
+    const int bk = (int)(g / (uint32_t)a.nc);
+    c = (int)(g - (uint32_t)bk * a.nc);
     b = bk / a.Hk;
     hk = bk % a.Hk;
     m = 0;
@@ -552,7 +552,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   Smem& s = *reinterpret_cast<Smem*>(base + SMALL);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
-  const int64_t groups = (int64_t)a.B * a.Hk * a.nc;  // (batch row, key head, chunk), `share` items each
+  const uint32_t groups = (uint32_t)a.B * a.Hk * a.nc;  // (batch row, key head, chunk), `share` items each
   const uint32_t sb = smem_u32(base);
 
   if (tid == 0) {
@@ -787,7 +787,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       {
         const int r = row & (TC - 1), c0 = qt * 16;
         const float2 gr = f2b(s.gam[r]);
-        const Vec16 gc{&s.gam[c0]}, nc{&s.nk[c0]}, bc{&s.beta[c0]};
+        const Reg16 gc{&s.gam[c0]}, nc{&s.nk[c0]}, bc{&s.beta[c0]};
         float2 v[8], k[8];
         float sum[16];
         unsigned char* tile = base + grad::P2;
@@ -893,7 +893,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         t = reduce16(y, lane);
         if (!(lane & 1)) s.dot[2][wq][qt * 16 + (lane >> 1)] = t;
         bar_sync(1, EPI);
-        const Vec16 fq{&s.fq[qt * 16]}, fu{&s.fu[qt * 16]}, bx{&s.bfx[qt * 16]};
+        const Reg16 fq{&s.fq[qt * 16]}, fu{&s.fu[qt * 16]}, bx{&s.bfx[qt * 16]};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           dq[j] = __fmul2_rn(dq[j], fq[j]);
@@ -966,7 +966,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) dk[j] = __fadd2_rn(dk[j], x[j]);
         if (L2) {
-          const Vec16 cq{&s.cq[qt * 16]}, ck{&s.ck[qt * 16]};
+          const Reg16 cq{&s.cq[qt * 16]}, ck{&s.ck[qt * 16]};
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             dq[j] = __ffma2_rn(cq[j], wide(qv[j]), dq[j]);  // (cq, ck are negative)

@@ -250,7 +250,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         float2 v[8];
         if (any) {
           tc_ld16(acc + ((uint32_t)((wp & 3) * 32) << 16) + c0, v);
-          const Vec16 gj{&w.gam[c0]}, nj{&w.nk[c0]};
+          const Reg16 gj{&w.gam[c0]}, nj{&w.nk[c0]};
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const float2 d = __ffma2_rn(gj[m], f2b(-1.0f), f2b(gi));
