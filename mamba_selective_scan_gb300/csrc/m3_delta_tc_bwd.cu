@@ -62,8 +62,9 @@ constexpr uint32_t T_Y = 320;  // fq dO as hi, lo
 // zero (the transition is the forward's, transposed).
 //
 // Bound like the forward by a chunk's dependent products, 4.3 us (24 chunks of
-// 36 heads: 104 us), and with every SM at work by what it reads and writes
-// (194 KB per chunk and head; 4 x 4096 x 40 heads: 360 us, 5.5 TB/s).
+// 36 heads one after the other: 104 us), and with every SM at work by what it
+// reads and writes (194 KB per chunk and head; 4 x 4096 x 40 heads: 336 us,
+// 5.9 TB/s).
 template <bool AGG>
 __global__ void __launch_bounds__(rev::THREADS, 1)
 m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
@@ -539,9 +540,10 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
 //
 // 210 KB come in and 32 KB go out per item, so the next item's tiles are
 // fetched as soon as the first products have read this one's.  The sums over
-// the heads of a key head stay in tensor memory.  4 x 4096 x 40 heads: 475 us,
-// 13200 cycles an item, 4.8 TB/s: the way of an item through its products and
-// epilogues is the bound, with shared memory busy for most of it.
+// the heads of a key head stay in tensor memory.  4 x 4096 x 40 heads: 425 us,
+// 12600 cycles an item, 5.4 TB/s.  Shared memory is the bound: the products'
+// operands keep its data path busy 6000 cycles an item, the epilogues' reads,
+// writes and shuffles 6700, besides what the copies write.
 template <bool L2>
 __global__ void __launch_bounds__(grad::THREADS, 1)
 m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
@@ -738,7 +740,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         wait(&s.kq, pkq);
         pkq ^= 1;
       }
-      if (L2) {
+      if (L2 && it.m == 0) {  // (the heads of a key head share its norms)
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -768,8 +770,12 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         if (warp == 1) g += s.tot;
         s.gam[tid] = g;
         s.beta[tid] = beta;
-        const float nk = L2 ? rsqrtf((s.ss[0][tid] + s.ss[1][tid]) + (s.ss[2][tid] + s.ss[3][tid]) + DELTA_L2_EPS) : 1.0f;
-        const float nq = L2 ? rsqrtf((s.ss[0][TC + tid] + s.ss[1][TC + tid]) + (s.ss[2][TC + tid] + s.ss[3][TC + tid]) + DELTA_L2_EPS) : 1.0f;
+        float nk = 1.0f, nq = 1.0f;
+        if (L2) {
+          nk = it.m ? s.nk[tid] : rsqrtf((s.ss[0][tid] + s.ss[1][tid]) + (s.ss[2][tid] + s.ss[3][tid]) + DELTA_L2_EPS);
+          nq = it.m ? s.nq[tid]
+                    : rsqrtf((s.ss[0][TC + tid] + s.ss[1][TC + tid]) + (s.ss[2][TC + tid] + s.ss[3][TC + tid]) + DELTA_L2_EPS);
+        }
         const float eg = ex2(g);
         s.eg[tid] = eg;
         s.nk[tid] = nk;
