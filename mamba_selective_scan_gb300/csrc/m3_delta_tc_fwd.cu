@@ -767,8 +767,10 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
   float* part = reinterpret_cast<float*>(raw + 2 * SEG_PHI);
   auto where = [&](int n) { return ((size_t)bh * a.segs + (rev ? a.segs - 1 - n : n)) * DMAX * DMAX; };
   const float* phis = rev ? a.seg_keep : a.seg_phi;
+  int n_phi = 0;  // loads issued
   auto load = [&](int n) {
     if (n + 1 >= a.segs) return;
+    ++n_phi;
     mbar_expect_tx(&full[n & 1], SEG_PHI);
     bulk_load(smem_u32(raw) + (n & 1) * SEG_PHI, phis + where(n), SEG_PHI, &full[n & 1]);
   };
@@ -817,6 +819,8 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
     *reinterpret_cast<float4*>(&S[k][vq]) = x;
     *reinterpret_cast<float4*>(a.seg_start + where(n + 1) + (size_t)k * DMAX + v) = x;
   }
+  if (!wait.ok)  // as in the other kernels: copies in flight land first
+    for (int i = 1; i <= 2 && i <= n_phi; ++i) mbar_wait(&full[(n_phi - i) & 1], (n_phi - i) >> 1 & 1);
   if (!wait.ok) report_timeout(&g_delta_fwd_status, a.status);
 }
 

@@ -137,7 +137,9 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     mbar_init_fence();
   }
   // a chunk's K and Q (one thread)
+  int n_kq = 0;  // loads issued
   auto load_kq = [&](uint32_t it) {
+    ++n_kq;
     const uint32_t bh = it / nc, bb = bh / hv;
     const int c = (int)(it - bh * nc), b = (int)bb, hk = (int)((bh - bb * hv) / (uint32_t)a.share);
     mbar_expect_tx(&full, 4 * TILE);
@@ -390,7 +392,11 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     for (int at = pt * 16; at < 2 * TILE; at += TP_THREADS * 16)
       *reinterpret_cast<uint4*>(dst + at) = *reinterpret_cast<const uint4*>(base + at);
   }
-  if (io) bulk_wait_read();
+  if (io) {
+    bulk_wait_read();
+    // after a wait ran out, copies still in flight land first (bounded)
+    if (!wait.ok) mbar_wait(&full, (n_kq - 1) & 1);
+  }
   if (!wait.ok) report_timeout(&g_delta_prep_status, a.status);
   if (wp == 0) {
     __syncwarp();

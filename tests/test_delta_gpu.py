@@ -99,6 +99,56 @@ def test_few_heads_in_segments(B, T, H):
     _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
 
 
+@pytest.mark.parametrize("B,T,Hk,Hv,dk,dv,state", [(1, 1301, 1, 3, 64, 96, True), (2, 1537, 2, 4, 72, 40, False), (5, 1030, 2, 4, 128, 64, True)])
+def test_segments_of_shared_and_narrow_heads(B, T, Hk, Hv, dk, dv, state):
+    """Time segments with heads narrower than their tiles, key heads shared by
+    value heads, and a last segment that is shorter than the others."""
+    x = delta_inputs(B, T, Hk, Hv, dk, dv, torch.bfloat16, seed=T, device="cuda", state=state)
+    got = _run(x, True)
+    ref = delta_ref_grads(x, dk ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta"] + (["d_state"] if state else []))
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv", [(9, 470, 8, 16), (3, 700, 50, 50)])
+def test_more_chunks_than_blocks(B, T, Hk, Hv):
+    """More (chunk, head) pairs than the preparing kernel has blocks: each goes
+    through several."""
+    x = delta_inputs(B, T, Hk, Hv, 32, 24, torch.bfloat16, seed=B, device="cuda")
+    got = _run(x, True)
+    ref = delta_ref_grads(x, 32 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
+
+
+@pytest.mark.parametrize("B,T,H", [(1, 1100, 2), (8, 130, 20), (2, 90, 3)])
+def test_in_a_graph(B, T, H):
+    """Forward and backward captured and replayed on new values: the bits of
+    calls outside it (time segments, shares of heads, plain heads)."""
+    names = ("q", "k", "v", "g", "beta")
+    x = delta_inputs(B, T, H, H, 64, 64, torch.bfloat16, seed=3, device="cuda")
+    y = delta_inputs(B, T, H, H, 64, 64, torch.bfloat16, seed=4, device="cuda")
+
+    def both(x):
+        o, st, ck = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=True, want_ckpt=True)
+        return o, st, binding.m3scan_delta_bwd(*[x[n] for n in names], ck, x["d_o"], d_state_out=x["d_state_out"], qk_l2norm=True)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both(x)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(x)
+    want = both(y)
+    for n in x:
+        x[n].copy_(y[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for n, w in want[2].items():
+        assert (w is None and got[2][n] is None) or torch.equal(got[2][n], w), n
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_extreme_gates(dt):
     """-inf and very negative log decays forget the state; beta 0 writes
