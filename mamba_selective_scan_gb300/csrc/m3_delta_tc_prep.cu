@@ -105,15 +105,16 @@ __device__ __forceinline__ void block_store(unsigned char* t, const float (&d)[4
 // T and P are stored as two bf16 terms, 17 bits of mantissa, so that what
 // they multiply keeps f32-grade sums.
 //
-// The chain kernels that follow (the forward's and the reverse pass's, each
-// twice more over time segments) go through a head's chunks one after the
-// other and are bound by that chain; this work has no order, so it is done
-// here once, with full SMs, and read back (34 KB per chunk and head).
+// The chain kernels that follow (the forward's and the reverse pass's, with
+// time segments each twice) go through a head's chunks one after the other and
+// are bound by that chain; this work has no order, so it is done here once,
+// with full SMs, and read back (34 KB per chunk and head).
 //
 // Bound by HBM for many chunks (32 KB in, 34 KB out per item): 16384 items
 // take 178 us, 6.1 TB/s; 4 x 4096 x 40 heads (K and Q of 20 heads) 114 us;
-// 3072 items 39 us.  Before that by shared memory: with the blocks in f32,
-// split at every use, in blocks of their own per item, 246, 147 and 51 us.
+// 8 x 2048 x 12 heads 39 us.  With I + A's blocks in f32, split at every use,
+// and a block per item it was bound by shared memory and barriers: 246, 147
+// and 51 us.
 template <bool L2>
 __global__ void __launch_bounds__(TP_THREADS, PREP_PER_SM)
 m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
