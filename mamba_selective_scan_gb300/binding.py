@@ -814,6 +814,8 @@ def _token_stride(t, name, dtype, index, shape):
     sb, stk, sh, sd = t.stride()
     if T <= 1:
         stk = sb if B > 1 else H * D
+    if stk < H * D:  # a broadcast view (0 would be taken as dense), or tokens that overlap
+        raise ValueError(f"{name}: tokens must be at least {H * D} elements apart, got strides {t.stride()}")
     if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 0 and sb != T * stk):
         raise ValueError(f"{name}: heads must be dense and batch rows T token strides apart, got strides {t.stride()}")
     return stk

@@ -119,3 +119,28 @@ def test_reference_gradients_against_differences():
         num = (loss({**x, n: x[n] + eps * d}) - loss({**x, n: x[n] - eps * d})) / (2 * eps)
         ana = (ref["d_state" if n == "state" else "d" + n] * d).sum().item()
         assert abs(num - ana) <= 1e-6 * max(1.0, abs(ana)), n
+
+
+@pytest.mark.parametrize("shape,view", [
+    ((1, 1, 2, 64), lambda t: t.expand(1, 100, 2, 64)),   # one key for all tokens
+    ((1, 1, 2, 64), lambda t: t.expand(2, 100, 2, 64)),   # and for all sequences
+    ((1, 1, 2, 64), lambda t: t.expand(3, 1, 2, 64)),     # a single token shared by a batch
+    ((1, 710), lambda t: t.as_strided((1, 10, 2, 64), (0, 64, 64, 1))),  # tokens that overlap
+    ((1, 710), lambda t: t.as_strided((4, 1, 2, 64), (120, 64, 64, 1))),
+])
+def test_token_stride_refuses_overlapping_tokens(shape, view):
+    """A token stride below a token's width (0 in a broadcast view) is not
+    passed on: 0 is the C ABI's word for dense."""
+    t = view(torch.zeros(shape))
+    with pytest.raises(ValueError):
+        binding._token_stride(t, "k", t.dtype, -1, t.shape)
+
+
+@pytest.mark.parametrize("B,T", [(1, 1), (1, 5), (3, 1), (2, 5), (0, 4), (2, 0)])
+def test_token_stride_of_views_and_dense_tensors(B, T):
+    assert binding._token_stride(torch.zeros(B, T, 2, 64), "k", torch.float32, -1, (B, T, 2, 64)) == 0
+    row = torch.zeros(B, T, 400)
+    for t in (row[..., :128], row[..., 128:256], row[..., 272:]):
+        t = t.unflatten(2, (2, 64))
+        want = 0 if t.is_contiguous() else 400 if B * T > 1 else 128
+        assert binding._token_stride(t, "k", torch.float32, -1, (B, T, 2, 64)) == want
