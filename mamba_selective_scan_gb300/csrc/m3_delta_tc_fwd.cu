@@ -696,6 +696,7 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         put_tokens(m, x);
         ready(&s.rdy_r[m]);
       }
+      const float2 ec = f2b(vec.ec);  // (the factors are free after the arrivals below)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         float2 x[8];
@@ -708,7 +709,6 @@ m3_delta_tc_agg_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         put_tokens(m, x);
         ready(&s.rdy_u[m]);
       }
-      const float2 ec = f2b(vec.ec);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const bool nan_row = s.bad[m][row] < TC;

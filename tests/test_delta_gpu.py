@@ -282,3 +282,19 @@ def test_nan_stays_in_its_row():
     assert torch.equal(got["o"][:, :40], clean["o"][:, :40])
     assert torch.isnan(got["o"][0, 40, 1, 3])
     assert torch.equal(got["dv"][:, :, 0], clean["dv"][:, :, 0])
+
+
+def test_segments_of_changing_decays():
+    """Long time segments whose chunks decay differently from the ones two
+    before and two behind them (the stage their factors share): the chunks'
+    own decays count in every call."""
+    x = delta_inputs(1, 6000, 2, 2, 128, 64, torch.bfloat16, seed=12, device="cuda")
+    chunk = torch.arange(6000, device="cuda") // 64
+    x["g"] *= 0.02
+    x["g"][:, chunk % 4 >= 2] = -0.25
+    names = ("q", "k", "v", "g", "beta")
+    got = _run(x, True)
+    _check_all(got, delta_ref_grads(x, 128 ** -0.5, True), ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
+    for _ in range(30):
+        o, st, _ = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=True)
+        assert torch.equal(o, got["o"]) and torch.equal(st, got["state_out"])
