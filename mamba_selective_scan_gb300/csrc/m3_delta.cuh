@@ -65,7 +65,8 @@ struct DeltaPlan {
 // SM count of the current device (a property that never changes: kept)
 cudaError_t sm_count(int* sms);
 
-__device__ __forceinline__ float clamp_g(float g) { return fmaxf(g, G_MIN); }
+// (a comparison, not fmaxf: a gate that is NaN stays one)
+__device__ __forceinline__ float clamp_g(float g) { return g < G_MIN ? G_MIN : g; }
 
 // Forward by the recurrence itself, token after token (any length and type;
 // decoding): provided by m3_delta_rec.cu

@@ -10,7 +10,7 @@ over up to a few hundred terms: 2e-5."""
 import pytest
 import torch
 
-from delta_util import delta_inputs, delta_ref_grads, rel
+from delta_util import delta_inputs, delta_ref, delta_ref_grads, rel
 from mamba_selective_scan_gb300 import binding
 
 pytestmark = pytest.mark.gpu
@@ -298,3 +298,45 @@ def test_segments_of_changing_decays():
     for _ in range(30):
         o, st, _ = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=True)
         assert torch.equal(o, got["o"]) and torch.equal(st, got["state_out"])
+
+
+NOT_FINITE = [(n, v) for n in ("g", "beta", "k", "q", "v") for v in ("nan", "inf")]
+
+
+def _spoil(x, name, value, at):
+    """x with one value of key head 0 or value head 1 of the last sequence not finite from token `at`."""
+    y = dict(x)
+    y[name] = x[name].clone()
+    i = {"g": (-1, at, 1), "beta": (-1, at, 1), "v": (-1, at, 1, 5)}.get(name, (-1, at, 0, 3))
+    y[name][i] = float(value)
+    return y
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 100, 1, 2, 40), (1, 1100, 1, 2, 601), (8, 130, 10, 20, 70)])
+def test_nan_gate_is_not_a_reset(B, T, Hk, Hv, at, dt):
+    """exp(NaN) is NaN: the outputs from that token on and the state (in f32
+    also the gradients that depend on it), none of which may come out finite."""
+    if dt == "f32" and T > 1000:
+        pytest.skip("no segments in f32")
+    x = delta_inputs(B, T, Hk, Hv, 64, 64, DT[dt], seed=at, device="cuda")
+    y = _spoil(x, "g", "nan", at)
+    got = _run(y, True)
+    ref = delta_ref_grads(y, 64 ** -0.5, True)
+    for n in ("o", "state_out") + (("dq", "dk", "dv", "dg", "dbeta", "d_state") if dt == "f32" else ()):
+        assert not (torch.isfinite(got[n]).cpu() & ~torch.isfinite(ref[n])).any(), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name,value", NOT_FINITE)
+def test_not_finite_in_decode(name, value, dt):
+    x = delta_inputs(3, 4, 2, 4, 64, 72, DT[dt], seed=2, device="cuda")
+    y = _spoil(x, name, value, 1)
+    names = ("q", "k", "v", "g", "beta")
+    ref, rst = delta_ref(*[y[n].double().cpu() for n in names], y["state"].double().cpu(), 64 ** -0.5, True)
+    for step in (1, 4):
+        S = y["state"].clone()
+        o = torch.cat([binding.m3scan_delta_decode(*[y[n][:, t:t + step].contiguous() for n in names], S, qk_l2norm=True)
+                       for t in range(0, 4, step)], 1)
+        assert torch.equal(torch.isfinite(o), torch.isfinite(ref).cuda())
+        assert torch.equal(torch.isfinite(S), torch.isfinite(rst).cuda())
