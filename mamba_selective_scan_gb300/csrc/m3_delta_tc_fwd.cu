@@ -312,6 +312,10 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       tc_st8(tl + ta + qt * 8, hi);
       tc_st8(tl + ta + 32 + qt * 8, lo);
       if (ck) {
+        if (bad < 16) {  // to the gradients such a row's U is NaN from that token on
+#pragma unroll
+          for (int k = 0; k < 8; ++k) hi[k] |= (2 * k >= bad ? 0x7FFFu : 0u) | (2 * k + 1 >= bad ? 0x7FFF0000u : 0u);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           *reinterpret_cast<uint4*>(ck + (qt * 2 + u) * 2048 + row * 16) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);

@@ -340,3 +340,25 @@ def test_not_finite_in_decode(name, value, dt):
                        for t in range(0, 4, step)], 1)
         assert torch.equal(torch.isfinite(o), torch.isfinite(ref).cuda())
         assert torch.equal(torch.isfinite(S), torch.isfinite(rst).cuda())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["g", "q", "v"])
+@pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 150, 2, 4, 40), (1, 1100, 2, 4, 601), (8, 130, 10, 20, 70)])
+def test_not_finite_in_gradients(B, T, Hk, Hv, at, name, dt):
+    """No gradient is finite that the definition's is not, those that are
+    finite are right, and other key heads' are the same bits."""
+    if dt == "f32" and B * T > 500:
+        pytest.skip("no segments or shares in f32")
+    x = delta_inputs(B, T, Hk, Hv, 64, 64, DT[dt], seed=at, device="cuda")
+    y = _spoil(x, name, "nan", at)
+    clean, got, ref = _run(x, True), _run(y, True), delta_ref_grads(y, 64 ** -0.5, True)
+    for n in ("dq", "dk", "dv", "dg", "dbeta", "d_state"):
+        g, r = got[n].double().cpu(), ref[n]
+        ok = torch.isfinite(g)
+        assert not (ok & ~torch.isfinite(r)).any(), n
+        d = (g[ok] - r[ok]).norm()
+        assert d <= TOL[got[n].dtype] * r[ok].norm(), n
+        h = g.shape[1 if n == "d_state" else 2] // Hk  # (key head 0's own)
+        rest = (slice(None), slice(h, None)) if n == "d_state" else (slice(None), slice(None), slice(h, None))
+        assert torch.equal(got[n][rest], clean[n][rest]), n
