@@ -25,6 +25,7 @@ struct TcWork {  // scratch
   float D[4][16][20];  // the diagonal blocks of I + A, then of T
   float M[4][8][12];
   float gam[TC], beta[TC], nk[TC], nq[TC];
+  uint4 lost;  // bits: tokens with a k (x: 0-31, y: 32-63) or a gate (z: even, w: odd) that is not finite
 };
 
 // shared memory: T (A at first), P, the factors; the K/Q tiles
@@ -105,6 +106,11 @@ __device__ __forceinline__ void block_store(unsigned char* t, const float (&d)[4
 // T and P are stored as two bf16 terms, 17 bits of mantissa, so that what
 // they multiply keeps f32-grade sums.
 //
+// From the first token on whose k, g or beta is not finite, T's rows are the
+// identity's (so that nothing of them meets the zeros in the rows above), P's
+// rows and beta are NaN: the forward's outputs and the state are NaN from that
+// token on and untouched before it, the adjoint is NaN.
+//
 // The chain kernels that follow (the forward's and the reverse pass's, with
 // time segments each twice) go through a head's chunks one after the other and
 // are bound by that chain; this work has no order, so it is done here once,
@@ -177,7 +183,11 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     }
     if (wp == 4) {
       const float g0 = clamp_g(__bfloat162float(g_in[0])) * LOG2E;  // exponents in powers of two
-      float sum = g0 + clamp_g(__bfloat162float(g_in[1])) * LOG2E;
+      const float g1 = clamp_g(__bfloat162float(g_in[1])) * LOG2E;
+      const float b0 = __bfloat162float(beta_in[0]), b1 = __bfloat162float(beta_in[1]);
+      w.lost.z = __ballot_sync(~0u, !(fmaf(g0, 0.0f, b0 * 0.0f) == 0.0f));
+      w.lost.w = __ballot_sync(~0u, !(fmaf(g1, 0.0f, b1 * 0.0f) == 0.0f));
+      float sum = g0 + g1;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float up = __shfl_up_sync(~0u, sum, o);
@@ -185,18 +195,22 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       }
       const float before = __shfl_up_sync(~0u, sum, 1);
       *reinterpret_cast<float2*>(&w.gam[lane * 2]) = make_float2(lane ? before + g0 : g0, sum);
-      *reinterpret_cast<float2*>(&w.beta[lane * 2]) = make_float2(__bfloat162float(beta_in[0]), __bfloat162float(beta_in[1]));
+      *reinterpret_cast<float2*>(&w.beta[lane * 2]) = make_float2(b0, b1);
       if (it + gridDim.x < items) load_gates(it + gridDim.x);
     }
     const int r = pt - 128;  // row of K over Q
     float nrm = 1.0f;
-    if (L2) {
-      float2 s0 = f2b(0.0f), s1 = f2b(0.0f);
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
+    if (L2 || wp < 6) {
+      auto row16 = [&](int u) {
         uint4 x;
         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                      : "r"(kq + (u >> 3) * (2 * TILE) + sw(r, u & 7)));
+        return x;
+      };
+      float2 s0 = f2b(0.0f), s1 = f2b(0.0f);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const uint4 x = row16(u);
         const uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -204,7 +218,19 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           (j & 1 ? s1 : s0) = __ffma2_rn(e, e, j & 1 ? s1 : s0);
         }
       }
-      nrm = rsqrtf((s0.x + s0.y) + (s1.x + s1.y) + DELTA_L2_EPS);
+      const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+      if (L2) nrm = rsqrtf(sum + DELTA_L2_EPS);
+      if (wp < 6) {
+        bool lost = false;
+        if (!(sum <= FINITE_MAX)) {  // (finite values whose squares overflow are none of these)
+          for (int u = 0; u < 16; ++u) {
+            const uint4 x = row16(u);
+            const uint32_t q[4] = {x.x, x.y, x.z, x.w};
+            for (int j = 0; j < 4; ++j) lost |= (q[j] & 0x7F80u) == 0x7F80u || (q[j] & 0x7F800000u) == 0x7F800000u;
+          }
+        }
+        (wp == 4 ? w.lost.x : w.lost.y) = __ballot_sync(~0u, lost);
+      }
     }
     (r < TC ? w.nk : w.nq)[r & (TC - 1)] = nrm;
     bar_sync(3, 128);  // K and Q are read
@@ -230,9 +256,15 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     wait(&mbk, par);
     tmem_fence_after_sync();
     const int row = (wp & 3) * 32 + lane, ch = wp >> 2;  // row of K over Q, half of its columns
+    int lost = TC;  // first token whose k, g or beta is not finite
+    if (const uint4 at = w.lost; at.x | at.y | at.z | at.w) {
+      if (at.x | at.y) lost = at.x ? __ffs(at.x) - 1 : __ffs(at.y) + 31;
+      if (at.z) lost = min(lost, 2 * __ffs(at.z) - 2);
+      if (at.w) lost = min(lost, 2 * __ffs(at.w) - 1);
+    }
     if (wp == 4 || wp == 6) {  // (without work in the next step)
       const int t = (wp - 4) * 16 + lane;
-      const float gc = w.gam[TC - 1], gam = w.gam[t], eg = ex2(gam), beta = w.beta[t];
+      const float gc = w.gam[TC - 1], gam = w.gam[t], eg = ex2(gam), beta = t < lost ? w.beta[t] : NAN;
       vec.beta[t] = beta;
       vec.bfx[t] = beta * eg * w.nk[t];
       vec.fu[t] = ex2(gc - gam) * w.nk[t];
@@ -269,6 +301,10 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         } else {
 #pragma unroll
           for (int m = 0; m < 8; ++m) v[m] = f2b(0.0f);
+        }
+        if (i >= lost) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) v[m] = f2b(isA ? 0.0f : NAN);
         }
         unsigned char* t = base + (isA ? 0 : 2 * TILE);
 #pragma unroll

@@ -362,3 +362,46 @@ def test_not_finite_in_gradients(B, T, Hk, Hv, at, name, dt):
         h = g.shape[1 if n == "d_state" else 2] // Hk  # (key head 0's own)
         rest = (slice(None), slice(h, None)) if n == "d_state" else (slice(None), slice(None), slice(h, None))
         assert torch.equal(got[n][rest], clean[n][rest]), n
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 150, 2, 4, 40), (2, 130, 1, 3, 64), (1, 70, 1, 2, 0), (1, 90, 1, 2, 89)])
+@pytest.mark.parametrize("name,value", NOT_FINITE)
+@pytest.mark.parametrize("dt,l2norm", [("bf16", True), ("bf16", False), ("f32", True)])
+def test_not_finite_from_its_token_on(dt, l2norm, name, value, B, T, Hk, Hv, at):
+    """A value that is not finite reaches what the recurrence lets it reach:
+    nothing of earlier tokens or other heads, and all that depends on it."""
+    x = delta_inputs(B, T, Hk, Hv, 64, 72, DT[dt], seed=at, device="cuda")
+    if not l2norm:
+        for n in ("q", "k"):
+            x[n] = (x[n].float() * 0.1).to(DT[dt])
+    y = _spoil(x, name, value, at)
+    names = ("q", "k", "v", "g", "beta")
+    clean = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=l2norm)
+    got = binding.m3scan_delta_fwd(*[y[n] for n in names], state=y["state"], qk_l2norm=l2norm)
+    ref = delta_ref(*[y[n].double().cpu() for n in names], y["state"].double().cpu(), 64 ** -0.5, l2norm)
+    for g, c, r in zip(got, clean, ref):
+        ok = torch.isfinite(r).cuda()
+        assert torch.equal(torch.isfinite(g), ok)
+        if name == "q" or g is got[0]:
+            assert torch.equal(g[ok], c[ok])
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 1100, 1, 2, 601), (8, 130, 10, 20, 70)])
+@pytest.mark.parametrize("name", ["g", "beta", "k", "v"])
+def test_not_finite_in_segments_and_shares(name, B, T, Hk, Hv, at):
+    x = delta_inputs(B, T, Hk, Hv, 64, 64, torch.bfloat16, seed=at, device="cuda")
+    y = _spoil(x, name, "nan", at)
+    names = ("q", "k", "v", "g", "beta")
+    clean, _, _ = binding.m3scan_delta_fwd(*[x[n] for n in names], state=x["state"], qk_l2norm=True)
+    got, st, _ = binding.m3scan_delta_fwd(*[y[n] for n in names], state=y["state"], qk_l2norm=True)
+    ref, rst = delta_ref(*[y[n].double().cpu() for n in names], y["state"].double().cpu(), 64 ** -0.5, True)
+    ok = torch.isfinite(ref).cuda()
+    assert torch.equal(torch.isfinite(got), ok) and torch.equal(got[ok], clean[ok])
+    assert torch.equal(torch.isfinite(st), torch.isfinite(rst).cuda())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["beta", "k"])
+@pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 150, 2, 4, 40), (1, 1100, 2, 4, 601), (8, 130, 10, 20, 70)])
+def test_gradients_of_keys_and_beta_not_finite(B, T, Hk, Hv, at, name, dt):
+    test_not_finite_in_gradients(B, T, Hk, Hv, at, name, dt)
