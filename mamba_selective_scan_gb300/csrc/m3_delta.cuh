@@ -68,6 +68,29 @@ cudaError_t sm_count(int* sms);
 // (a comparison, not fmaxf: a gate that is NaN stays one)
 __device__ __forceinline__ float clamp_g(float g) { return g < G_MIN ? G_MIN : g; }
 
+// A chunk's gates are summed in two f32 terms: each forgetting token brings up
+// to 110, so that in one term the small decays between such tokens would be
+// differences of numbers in the thousands (errors to 2e-4).  A decay is then
+// e^{h_i - h_j} (1 + l_i) (1 - l_j): h_i - h_j is exact where it is small, and
+// |l| stays below 2^-10, so the linear factor is good to f32's rounding (l in
+// powers of e) and goes into the tokens' own factors.
+struct GateSum {
+  float h, l;
+};
+__device__ __forceinline__ GateSum gate_add(GateSum a, GateSum b) {
+  const float s = a.h + b.h, t = s - a.h, e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l), h = s + e;
+  return {h, e - (h - s)};
+}
+// lane i's sum over the lanes up to i
+__device__ __forceinline__ GateSum gate_scan(GateSum v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const GateSum up = {__shfl_up_sync(~0u, v.h, o), __shfl_up_sync(~0u, v.l, o)};
+    if (lane >= o) v = gate_add(up, v);
+  }
+  return v;
+}
+
 // Forward by the recurrence itself, token after token (any length and type;
 // decoding): provided by m3_delta_rec.cu
 template <typename T> cudaError_t launch_delta_rec(const DeltaArgs& a, cudaStream_t st, int sms);

@@ -39,7 +39,8 @@ struct Kept {
 static_assert(sizeof(Kept) == F32_KEPT, "the workspace's share");
 
 struct Gates {
-  float gam[C], beta[C], eg[C], el[C];  // el = e^{gam_C - gam}
+  float gam[C], lo[C], beta[C], eg[C], el[C];  // gam + lo: the gates' sum; el = e^{gam_C - gam}
+  __device__ __forceinline__ float decay(int i, int j) const { return expf(gam[i] - gam[j]) * (1.0f + (lo[i] - lo[j])); }
 };
 struct PrepSmem {
   float K[C][LD], Q[C][LD], E[C][LD];
@@ -118,16 +119,12 @@ __device__ __forceinline__ void load_half(float (*to)[LD], const float* S, int h
 __device__ __forceinline__ void load_gates(Gates& s, const DeltaArgs& a, const Place& p, int lane) {  // one warp
   const bool ok = lane < p.n;
   const int64_t at = (p.tok0 + lane) * a.Hv + p.h;
-  float g = ok ? clamp_g(static_cast<const float*>(a.g)[at]) : 0.0f;
+  const GateSum g = gate_scan({ok ? clamp_g(static_cast<const float*>(a.g)[at]) : 0.0f, 0.0f}, lane);
   s.beta[lane] = ok ? static_cast<const float*>(a.beta)[at] : 0.0f;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float up = __shfl_up_sync(~0u, g, o);
-    if (lane >= o) g += up;
-  }
-  s.gam[lane] = g;
-  s.eg[lane] = expf(g);
-  s.el[lane] = expf(__shfl_sync(~0u, g, 31) - g);
+  s.gam[lane] = g.h;
+  s.lo[lane] = g.l;
+  s.eg[lane] = expf(g.h) * (1.0f + g.l);
+  s.el[lane] = expf(__shfl_sync(~0u, g.h, 31) - g.h) * (1.0f + (__shfl_sync(~0u, g.l, 31) - g.l));
 }
 __device__ __forceinline__ const float* start_state(const DeltaArgs& a, const Place& p) {
   return a.ckpt_in + ((size_t)p.bh * a.nc + p.ch) * a.DK * a.DV;
@@ -184,7 +181,7 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_prep_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + i;
-      const float D = lane <= r ? expf(s.g.gam[r] - s.g.gam[lane]) : 0.0f;
+      const float D = lane <= r ? s.g.decay(r, lane) : 0.0f;
       const float P = a.scale * D * qk[i];
       s.P[r][lane] = P;
       out.P[r][lane] = P;
@@ -364,7 +361,7 @@ __global__ void __launch_bounds__(256) m3_delta_bwd_grad_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + i;
-      const float D = lane <= r ? expf(s.g.gam[r] - s.g.gam[lane]) : 0.0f, be = s.g.beta[r];
+      const float D = lane <= r ? s.g.decay(r, lane) : 0.0f, be = s.g.beta[r];
       const float xa = lane < r ? -da[i] : 0.0f, xp = lane <= r ? dp[i] : 0.0f;
       const float dk = xa * D * kk[i], m = dk * be + xp * s.P[r][lane];
       // A carries beta_r: its derivative is taken with A / beta_r = D k_r.k_j

@@ -460,13 +460,15 @@ constexpr int SMALL = DR + 32768;
 constexpr int P2 = DS + 32768, A2 = P2 + 2 * TILE;
 
 struct Smem {  // at SMALL
-  float gam[TC], beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC], d[TC], z[TC];
+  float gam[TC], lo[TC], nkp[TC], nkm[TC];  // gam + lo: the gates' sum; nk (1 + lo), nk (1 - lo)
+  float beta[TC], eg[TC], nk[TC], nq[TC], bfx[TC], fu[TC], fq[TC], cq[TC], ck[TC], gd[TC], d[TC], z[TC];
   float ss[4][2 * TC];
   float row_p[4][TC], col_p[2][TC];  // sums of dP o P: per column quarter, per warp
   float col_a[4][TC], row_a[2][TC];  // sums of dA o A (row_a without beta)
   float dot[3][4][TC];               // Q.(dO S0^T), K.(dR S0^T), K.(U dS^T): per warp of 32 head_k
   float red[2][16];  // (by turns: the next item's may be written before this one's are summed)
-  float ec, tot;
+  float ec;
+  GateSum tot;
   uint64_t ds, dl, us, kq;           // arrived: dS hi; dS lo; U, dR, dO, S0; K, Q
   uint64_t mb1, mb2, mb3;            // done: K Q^T (and all before it); G, dP, Yo, Y, Z; the products with P2 and A2
   uint64_t rdy0, rdy1, rdya;   // see the issuing warp
@@ -707,9 +709,10 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       const int c = it.c, b = it.b, h = it.h;
       const int64_t tok0 = (int64_t)b * a.T + c * TC;  // the chunk's first token
       const int n = min(TC, a.T - c * TC);
-      float g = 0.0f, beta = 0.0f;  // (g in powers of two)
+      GateSum g = {0.0f, 0.0f};  // (in powers of two)
+      float beta = 0.0f;
       if (tid < n) {
-        g = LOG2E * clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
+        g.h = LOG2E * clamp_g(__bfloat162float(static_cast<const __nv_bfloat16*>(a.g)[(tok0 + tid) * a.Hv + h]));
         beta = __bfloat162float(static_cast<const __nv_bfloat16*>(a.beta)[(tok0 + tid) * a.Hv + h]);
       }
       // <dS, S0>
@@ -758,17 +761,15 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         s.ss[qt][row] = s0 + s1;
       }
       if (warp < 2) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float up = __shfl_up_sync(~0u, g, o);
-          if (lane >= o) g += up;
-        }
+        g = gate_scan(g, lane);
         if (tid == 31) s.tot = g;
       }
       bar_sync(1, EPI);
       if (warp < 2) {
-        if (warp == 1) g += s.tot;
-        s.gam[tid] = g;
+        if (warp == 1) g = gate_add(s.tot, g);
+        g.l *= LN2;  // (in powers of e from here on)
+        s.gam[tid] = g.h;
+        s.lo[tid] = g.l;
         s.beta[tid] = beta;
         float nk = 1.0f, nq = 1.0f;
         if (L2) {
@@ -776,24 +777,26 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
           nq = it.m ? s.nq[tid]
                     : rsqrtf((s.ss[0][TC + tid] + s.ss[1][TC + tid]) + (s.ss[2][TC + tid] + s.ss[3][TC + tid]) + DELTA_L2_EPS);
         }
-        const float eg = ex2(g);
+        const float eg = ex2(g.h) * (1.0f + g.l);
         s.eg[tid] = eg;
         s.nk[tid] = nk;
+        s.nkp[tid] = nk * (1.0f + g.l);
+        s.nkm[tid] = nk * (1.0f - g.l);
         s.nq[tid] = nq;
         s.bfx[tid] = beta * eg * nk;
         s.fq[tid] = a.scale * eg * nq;
       }
       bar_sync(1, EPI);
       if (warp < 2) {
-        s.fu[tid] = ex2(s.gam[TC - 1] - g) * s.nk[tid];
-        if (tid == 0) s.ec = ex2(s.gam[TC - 1]);
+        s.fu[tid] = ex2(s.gam[TC - 1] - g.h) * (1.0f + (s.lo[TC - 1] - g.l)) * s.nk[tid];
+        if (tid == 0) s.ec = ex2(s.gam[TC - 1]) * (1.0f + s.lo[TC - 1]);
       }
       wait(&s.mb1, par);
       tmem_fence_after_sync();
       {
         const int r = row & (TC - 1), c0 = qt * 16;
         const float2 gr = f2b(s.gam[r]);
-        const Reg16 gc{&s.gam[c0]}, nc{&s.nk[c0]}, bc{&s.beta[c0]};
+        const Reg16 gc{&s.gam[c0]}, nc{wq < 2 ? &s.nkp[c0] : &s.nkm[c0]}, bc{&s.beta[c0]};
         float2 v[8], k[8];
         float sum[16];
         unsigned char* tile = base + grad::P2;
@@ -805,7 +808,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
             for (int m = 0; m < 16; ++m)
               if (c0 + m == r) s.gd[r] = m & 1 ? v[m >> 1].y : v[m >> 1].x;
           }
-          const float2 f = f2b(-s.nk[r]);
+          const float2 f = f2b(-s.nkm[r]);
           float2 col = f2b(0.0f);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
@@ -826,7 +829,7 @@ m3_delta_tc_grad_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         } else {  // dP: row i = r, columns j
           tc_ld16(tl + T_DP, v);
           tc_ld16(tl + T_KQ, k);
-          const float2 f = f2b(a.scale * s.nq[r]);
+          const float2 f = f2b(a.scale * s.nq[r] * (1.0f + s.lo[r]));
           float2 rs = f2b(0.0f);
 #pragma unroll
           for (int m = 0; m < 8; ++m) {

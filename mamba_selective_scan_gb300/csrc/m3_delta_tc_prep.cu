@@ -24,12 +24,18 @@ constexpr int TP_THREADS = 256;
 struct TcWork {  // scratch
   float D[4][16][20];  // the diagonal blocks of I + A, then of T
   float M[4][8][12];
-  float gam[TC], beta[TC], nk[TC], nq[TC];
+  float beta[TC], nk[TC], nq[TC];
   uint4 lost;  // bits: tokens with a k (x: 0-31, y: 32-63) or a gate (z: even, w: odd) that is not finite
 };
 
-// shared memory: T (A at first), P, the factors; the K/Q tiles
+struct TcGates {  // behind the factors, where the tiles' alignment leaves room
+  float gam[TC], lo[TC];  // the gates' sum (lo in powers of e)
+  float nj[TC];           // nk (1 - lo)
+};
+
+// shared memory: T (A at first), P, the factors, the gates; the K/Q tiles
 constexpr int KQ = ((int)sizeof(TcPrep) + 1023) / 1024 * 1024;
+static_assert(sizeof(TcPrep) + sizeof(TcGates) <= KQ && sizeof(TcPrep) % 16 == 0, "the gates' place");
 constexpr int WORK = KQ + 4 * TILE;
 constexpr size_t SMEM_BYTES = WORK + sizeof(TcWork) + 1024;
 constexpr int PREP_PER_SM = 3;
@@ -131,6 +137,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
   __shared__ uint32_t slot;
   TcVec& vec = *reinterpret_cast<TcVec*>(base + 4 * TILE);
   TcWork& w = *reinterpret_cast<TcWork*>(base + WORK);
+  TcGates& gt = *reinterpret_cast<TcGates*>(base + sizeof(TcPrep));
   const int pt = threadIdx.x, lane = pt & 31, wp = __shfl_sync(~0u, pt >> 5, 0);
   const uint32_t sb = smem_u32(base), kq = sb + KQ;
   const uint32_t items = (uint32_t)(a.B * a.Hv * a.nc), nc = (uint32_t)a.nc, hv = (uint32_t)a.Hv;  // (below 2^31)
@@ -187,14 +194,12 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
       const float b0 = __bfloat162float(beta_in[0]), b1 = __bfloat162float(beta_in[1]);
       w.lost.z = __ballot_sync(~0u, !(fmaf(g0, 0.0f, b0 * 0.0f) == 0.0f));
       w.lost.w = __ballot_sync(~0u, !(fmaf(g1, 0.0f, b1 * 0.0f) == 0.0f));
-      float sum = g0 + g1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float up = __shfl_up_sync(~0u, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const float before = __shfl_up_sync(~0u, sum, 1);
-      *reinterpret_cast<float2*>(&w.gam[lane * 2]) = make_float2(lane ? before + g0 : g0, sum);
+      const GateSum sum = gate_scan(gate_add({g0, 0.0f}, {g1, 0.0f}), lane);
+      GateSum even = {__shfl_up_sync(~0u, sum.h, 1), __shfl_up_sync(~0u, sum.l, 1)};
+      if (lane == 0) even = {0.0f, 0.0f};
+      even = gate_add(even, {g0, 0.0f});
+      *reinterpret_cast<float2*>(&gt.gam[lane * 2]) = make_float2(even.h, sum.h);
+      *reinterpret_cast<float2*>(&gt.lo[lane * 2]) = make_float2(even.l * LN2, sum.l * LN2);
       *reinterpret_cast<float2*>(&w.beta[lane * 2]) = make_float2(b0, b1);
       if (it + gridDim.x < items) load_gates(it + gridDim.x);
     }
@@ -234,6 +239,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     }
     (r < TC ? w.nk : w.nq)[r & (TC - 1)] = nrm;
     bar_sync(3, 128);  // K and Q are read
+    if (wp < 6) gt.nj[r] = nrm * (1.0f - gt.lo[r]);
     if (io && it + gridDim.x < items) {
       wait(&mbk, par);
       if (wait.ok) load_kq(it + gridDim.x);
@@ -264,18 +270,19 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
     }
     if (wp == 4 || wp == 6) {  // (without work in the next step)
       const int t = (wp - 4) * 16 + lane;
-      const float gc = w.gam[TC - 1], gam = w.gam[t], eg = ex2(gam), beta = t < lost ? w.beta[t] : NAN;
+      const float gc = gt.gam[TC - 1], gam = gt.gam[t], lc = gt.lo[TC - 1], lo = gt.lo[t];
+      const float eg = ex2(gam) * (1.0f + lo), beta = t < lost ? w.beta[t] : NAN;
       vec.beta[t] = beta;
       vec.bfx[t] = beta * eg * w.nk[t];
-      vec.fu[t] = ex2(gc - gam) * w.nk[t];
+      vec.fu[t] = ex2(gc - gam) * (1.0f + (lc - lo)) * w.nk[t];
       vec.fq[t] = scale * eg * w.nq[t];
-      if (t == 0) vec.ec = ex2(gc);
+      if (t == 0) vec.ec = ex2(gc) * (1.0f + lc);
     }
     {
       const int i = row & (TC - 1);
       const bool isA = (wp & 3) < 2;
-      const float gi = w.gam[i];
-      const float f = isA ? w.beta[i] * w.nk[i] : scale * w.nq[i];
+      const float gi = gt.gam[i];
+      const float f = (isA ? w.beta[i] * w.nk[i] : scale * w.nq[i]) * (1.0f + gt.lo[i]);
       const int last = isA ? i - 1 : i;  // last column that counts
       const bool any = ch == 0 || (wp & 1);   // rows 0-31 have nothing in the second half,
       const bool all = ch == 0 && (wp & 1);   // rows 32-63 everything in the first
@@ -285,7 +292,7 @@ m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_consta
         float2 v[8];
         if (any) {
           tc_ld16(acc + ((uint32_t)((wp & 3) * 32) << 16) + c0, v);
-          const Reg16 gj{&w.gam[c0]}, nj{&w.nk[c0]};
+          const Reg16 gj{&gt.gam[c0]}, nj{&gt.nj[c0]};
 #pragma unroll
           for (int m = 0; m < 8; ++m) {
             const float2 d = __ffma2_rn(gj[m], f2b(-1.0f), f2b(gi));

@@ -405,3 +405,19 @@ def test_not_finite_in_segments_and_shares(name, B, T, Hk, Hv, at):
 @pytest.mark.parametrize("B,T,Hk,Hv,at", [(1, 150, 2, 4, 40), (1, 1100, 2, 4, 601), (8, 130, 10, 20, 70)])
 def test_gradients_of_keys_and_beta_not_finite(B, T, Hk, Hv, at, name, dt):
     test_not_finite_in_gradients(B, T, Hk, Hv, at, name, dt)
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("low", [float("-inf"), -60.0])
+@pytest.mark.parametrize("every", [2, 3, 5, 8])
+def test_decays_between_resets(every, low, dt):
+    """Many forgetting tokens in a chunk (short sequences packed into one): the
+    small decays between them keep their precision, which shows in the f32
+    results (the state; every gradient of f32 activations)."""
+    x = delta_inputs(1, 192, 1, 2, 64, 64, DT[dt], seed=every, device="cuda")
+    x["g"] = -0.5 * torch.rand(1, 192, 2, generator=torch.Generator().manual_seed(every)).to(DT[dt]).cuda()
+    x["g"][:, ::every] = low
+    got = _run(x, True)
+    y = dict(x)
+    y["g"] = x["g"].clamp(min=-800.0)  # exp(-800) is 0 in float64
+    ref = delta_ref_grads(y, 64 ** -0.5, True)
+    _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
