@@ -389,6 +389,20 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _on_stream(call):
+    """A call with ``stream=``: that stream is made the current one while it
+    runs, so that what it allocates (results, scratch) is that stream's
+    memory.  Memory of the stream that was current may still be in use by what
+    was enqueued there before."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return on
+
+
 class Workspace:
     """A device workspace sized for a plan (reusable across calls).  Its
     status block (the first STATUS_BYTES) starts at zero, as the library
@@ -693,15 +707,13 @@ def _need(t, name, dtype, index, shape):
     return t
 
 
-def _scratch(workspace, nbytes, torch, dev, stream):
-    """(address, bytes) of the caller's workspace or of a new one (whose
-    status block nobody can query, so it need not start at zero), and what
-    must stay alive until the call is enqueued."""
+def _scratch(workspace, nbytes, torch, dev):
+    """(address, bytes) of the caller's workspace or of a new one, the current
+    stream's (whose status block nobody can query, so it need not start at
+    zero), and what must stay alive until the call is enqueued."""
     if workspace is not None:
         return workspace.ptr, workspace.nbytes, workspace
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None:  # its memory is given up here, while that stream may still be using it
-        buf.record_stream(stream)
     return buf.data_ptr(), nbytes, buf
 
 
@@ -711,6 +723,7 @@ def _norm_sizes(rows, dim, eps, accumulate, code):
     return ctypes.byref(dims), m3scan_norm_plan(dims, code).workspace_bytes
 
 
+@_on_stream
 def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residual_out=None,
                     mean=None, rstd=None, want_stats=True, stream=None):
     """Layer norm over the last dimension of ``x`` [..., dim], of x + residual
@@ -748,6 +761,7 @@ def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, re
     return y, residual_out, mean, rstd
 
 
+@_on_stream
 def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want_bias=True,
                     accumulate_param_grads=False, out=None, workspace=None, stream=None):
     """Backward of ``m3scan_norm_fwd``.  ``normed`` is its ``residual_out``
@@ -780,7 +794,7 @@ def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want
     elif want_bias:
         d_b = new(dim, dtype=f32, device=dev)
     dims, nbytes = _norm_sizes(dy.numel() // dim if dim else 0, dim, 0.0, int(bool(accumulate_param_grads)), code)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev, stream)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
     st = _LIB.m3scan_norm_bwd(dims, code, dy.data_ptr(), normed.data_ptr(), ncode, weight.data_ptr(), mean.data_ptr(),
                               rstd.data_ptr(), _ptr(d_residual_out), dx.data_ptr(), _ptr(d_res), d_w.data_ptr(),
                               _ptr(d_b), ws, nbytes, _stream_of(stream, index))
@@ -855,6 +869,7 @@ def _delta_inputs(q, k, v, g, beta):
             _token_stride(v, "v", dt, index, vshape))
 
 
+@_on_stream
 def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False, want_state=True,
                      want_ckpt=False, o=None, state_out=None, ckpt=None, workspace=None, stream=None):
     """Gated delta rule over a sequence.  q, k [B, T, Hk, dk], v [B, T, Hv,
@@ -876,7 +891,7 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
         _need(ckpt, "ckpt", f32, index, (n_ckpt,))
     elif want_ckpt:
         ckpt = torch.empty(n_ckpt, dtype=f32, device=dev)
-    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev, stream)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev)
     st = _LIB.m3scan_delta_fwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                _ptr(state), o.data_ptr(), _ptr(state_out), _ptr(ckpt), ws, nbytes,
                                _stream_of(stream, index))
@@ -885,6 +900,7 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     return o, state_out, ckpt
 
 
+@_on_stream
 def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_state=False, scale=0.0,
                      qk_l2norm=False, out=None, workspace=None, stream=None):
     """Backward of ``m3scan_delta_fwd`` (same q, k, v, g, beta, scale and
@@ -908,7 +924,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     _need(r["d_state"], "d_state", f32, index, sshape)
     _need(d_o, "d_o", dt, index, v.shape)
     _need(ckpt, "ckpt", f32, index, (n_ckpt,))
-    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev, stream)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev)
     st = _LIB.m3scan_delta_bwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                ckpt.data_ptr(), d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(),
                                r["dk"].data_ptr(), r["dv"].data_ptr(), r["dg"].data_ptr(), r["dbeta"].data_ptr(),
@@ -918,6 +934,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     return r
 
 
+@_on_stream
 def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, o=None, stream=None):
     """A short window (typically one token: T = 1) from the carried ``state``
     [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""
