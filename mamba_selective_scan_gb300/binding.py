@@ -425,6 +425,7 @@ def plan_for(x, chunk=0, segments=0):
     return dims, m3scan_plan(dims, _act_code(x))
 
 
+@_on_stream
 def m3scan_fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *, chunk=0,
                segments=0, gated=None, y_dbg=None, want_y=False, ckpt=None, workspace=None,
                stream=None, threads_per_channel=0):
@@ -433,6 +434,7 @@ def m3scan_fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *, ch
                 gated, y_dbg, want_y, ckpt, workspace, stream, None, threads_per_channel)[:3]
 
 
+@_on_stream
 def m3scan_fwd_state(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *,
                      ssm_state=None, conv_state=None, chunk=0, segments=0, gated=None,
                      y_dbg=None, want_y=False, ckpt=None, ssm_state_out=None,
@@ -495,6 +497,7 @@ def _fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, chunk, segm
     return gated, ckpt, y_dbg
 
 
+@_on_stream
 def m3scan_bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gated, *,
                chunk=0, segments=0, want_du=False, accumulate_param_grads=False, out=None,
                workspace=None, stream=None, threads_per_channel=0, deterministic=False):
@@ -507,6 +510,7 @@ def m3scan_bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt,
                 threads_per_channel, deterministic)
 
 
+@_on_stream
 def m3scan_bwd_state(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gated,
                      *, conv_state=None, d_ssm_state_out=None, d_conv_state_out=None, chunk=0,
                      segments=0, want_du=False, accumulate_param_grads=False, out=None,
@@ -585,6 +589,7 @@ def _bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gat
     return o
 
 
+@_on_stream
 def m3scan_decode(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ssm_state,
                   conv_state, *, gated=None, y_dbg=None, want_y=False, stream=None):
     """Forward of a short window (x [B, T, D], typically T = 1) from the
@@ -614,6 +619,7 @@ def m3scan_decode(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ss
     return gated, y_dbg
 
 
+@_on_stream
 def m3scan_bwd_two_phase(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt,
                          d_gated, du_extra_fn=None, *, conv_state=None, d_ssm_state_out=None,
                          d_conv_state_out=None, chunk=0, segments=0, bc_stride=0, dbc_stride=0,

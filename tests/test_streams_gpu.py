@@ -5,6 +5,8 @@ import torch
 
 from delta_util import delta_inputs
 from mamba_selective_scan_gb300 import binding
+from mamba_selective_scan_gb300.inputs import make_inputs
+from parity_util import to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,35 @@ def test_two_streams_in_turn():
             for g, w in zip(rows, want):
                 for n in w:
                     assert torch.equal(g[n], w[n]), n
+
+
+def _scan(act, call):
+    inp = make_inputs(2, 40, 64, act=act, seed=3)
+    d = to_device(inp)
+    a = [d[n] for n in ("x", "delta_raw", "z", "B", "C", "conv_w", "conv_b", "dt_bias", "a_log", "D")]
+    h = torch.zeros(2, 16, 64, device="cuda")
+    c = torch.zeros(2, 3, 64, dtype=d["x"].dtype, device="cuda")
+
+    def run(**kw):
+        if call == "decode":
+            S, C = h.clone(), c.clone()
+            torch.cuda.synchronize()
+            gated, _ = binding.m3scan_decode(*a, S, C, **kw)
+            return {"gated": gated, "S": S, "C": C}
+        if call == "state":
+            gated, ck, _, h1, c1 = binding.m3scan_fwd_state(*a, ssm_state=h, conv_state=c, **kw)
+            return {"gated": gated, "h": h1, "c": c1,
+                    **binding.m3scan_bwd_state(*a, ck, d["d_gated"], conv_state=c, deterministic=True, **kw)}
+        gated, ck, _ = binding.m3scan_fwd(*a, **kw)
+        bwd = binding.m3scan_bwd_two_phase if call == "two_phase" else binding.m3scan_bwd
+        return {"gated": gated, **bwd(*a, ck, d["d_gated"], deterministic=True, **kw)}
+    return run
+
+
+SCANS = {f"scan-{act}-{call}": (act, call) for act in ("f32", "bf16") for call in ("plain", "state", "two_phase", "decode")}
+
+
+@pytest.mark.parametrize("name", list(SCANS))
+def test_scan_takes_memory_of_its_stream(name, monkeypatch):
+    monkeypatch.setitem(CALLS, name, lambda: _scan(*SCANS[name]))
+    test_takes_memory_of_its_stream(name, monkeypatch)
