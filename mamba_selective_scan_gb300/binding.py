@@ -389,18 +389,29 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
-def _on_stream(call):
-    """A call with ``stream=``: that stream is made the current one while it
-    runs, so that what it allocates (results, scratch) is that stream's
-    memory.  Memory of the stream that was current may still be in use by what
-    was enqueued there before."""
+def _placed(call):
+    """A call runs with its first tensor's device current, and with ``stream=``
+    with that stream current.  The library launches on the current device;
+    and what a call allocates (results, scratch) is the memory of the stream it
+    runs on: that of another stream may still be in use by what was enqueued
+    there before."""
+    first = call.__code__.co_varnames[0]
+
     @functools.wraps(call)
-    def on(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with _torch().cuda.stream(stream):
-            return call(*args, stream=stream, **kw)
-    return on
+    def placed(*args, stream=None, **kw):
+        t = args[0] if args else kw.get(first)
+        index = -1 if t is None else t.get_device()
+        cuda = (_TORCH or _torch()).cuda
+        if stream is not None:
+            if index >= 0 and stream.device.index != index:
+                raise ValueError(f"{first} is on cuda:{index}, stream on {stream.device}")
+            with cuda.stream(stream):
+                return call(*args, stream=stream, **kw)
+        if index >= 0 and index != cuda.current_device():
+            with cuda.device(index):
+                return call(*args, **kw)
+        return call(*args, **kw)
+    return placed
 
 
 class Workspace:
@@ -425,7 +436,7 @@ def plan_for(x, chunk=0, segments=0):
     return dims, m3scan_plan(dims, _act_code(x))
 
 
-@_on_stream
+@_placed
 def m3scan_fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *, chunk=0,
                segments=0, gated=None, y_dbg=None, want_y=False, ckpt=None, workspace=None,
                stream=None, threads_per_channel=0):
@@ -434,7 +445,7 @@ def m3scan_fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *, ch
                 gated, y_dbg, want_y, ckpt, workspace, stream, None, threads_per_channel)[:3]
 
 
-@_on_stream
+@_placed
 def m3scan_fwd_state(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, *,
                      ssm_state=None, conv_state=None, chunk=0, segments=0, gated=None,
                      y_dbg=None, want_y=False, ckpt=None, ssm_state_out=None,
@@ -497,7 +508,7 @@ def _fwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, chunk, segm
     return gated, ckpt, y_dbg
 
 
-@_on_stream
+@_placed
 def m3scan_bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gated, *,
                chunk=0, segments=0, want_du=False, accumulate_param_grads=False, out=None,
                workspace=None, stream=None, threads_per_channel=0, deterministic=False):
@@ -510,7 +521,7 @@ def m3scan_bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt,
                 threads_per_channel, deterministic)
 
 
-@_on_stream
+@_placed
 def m3scan_bwd_state(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gated,
                      *, conv_state=None, d_ssm_state_out=None, d_conv_state_out=None, chunk=0,
                      segments=0, want_du=False, accumulate_param_grads=False, out=None,
@@ -589,7 +600,7 @@ def _bwd(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt, d_gat
     return o
 
 
-@_on_stream
+@_placed
 def m3scan_decode(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ssm_state,
                   conv_state, *, gated=None, y_dbg=None, want_y=False, stream=None):
     """Forward of a short window (x [B, T, D], typically T = 1) from the
@@ -619,7 +630,7 @@ def m3scan_decode(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ss
     return gated, y_dbg
 
 
-@_on_stream
+@_placed
 def m3scan_bwd_two_phase(x, delta_raw, z, Bm, Cm, conv_w, conv_b, dt_bias, a_log, D, ckpt,
                          d_gated, du_extra_fn=None, *, conv_state=None, d_ssm_state_out=None,
                          d_conv_state_out=None, chunk=0, segments=0, bc_stride=0, dbc_stride=0,
@@ -729,7 +740,7 @@ def _norm_sizes(rows, dim, eps, accumulate, code):
     return ctypes.byref(dims), m3scan_norm_plan(dims, code).workspace_bytes
 
 
-@_on_stream
+@_placed
 def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, residual_out=None,
                     mean=None, rstd=None, want_stats=True, stream=None):
     """Layer norm over the last dimension of ``x`` [..., dim], of x + residual
@@ -767,7 +778,7 @@ def m3scan_norm_fwd(x, weight, bias=None, *, residual=None, eps=1e-5, y=None, re
     return y, residual_out, mean, rstd
 
 
-@_on_stream
+@_placed
 def m3scan_norm_bwd(dy, normed, weight, mean, rstd, *, d_residual_out=None, want_bias=True,
                     accumulate_param_grads=False, out=None, workspace=None, stream=None):
     """Backward of ``m3scan_norm_fwd``.  ``normed`` is its ``residual_out``
@@ -875,7 +886,7 @@ def _delta_inputs(q, k, v, g, beta):
             _token_stride(v, "v", dt, index, vshape))
 
 
-@_on_stream
+@_placed
 def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False, want_state=True,
                      want_ckpt=False, o=None, state_out=None, ckpt=None, workspace=None, stream=None):
     """Gated delta rule over a sequence.  q, k [B, T, Hk, dk], v [B, T, Hv,
@@ -906,7 +917,7 @@ def m3scan_delta_fwd(q, k, v, g, beta, *, state=None, scale=0.0, qk_l2norm=False
     return o, state_out, ckpt
 
 
-@_on_stream
+@_placed
 def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_state=False, scale=0.0,
                      qk_l2norm=False, out=None, workspace=None, stream=None):
     """Backward of ``m3scan_delta_fwd`` (same q, k, v, g, beta, scale and
@@ -940,7 +951,7 @@ def m3scan_delta_bwd(q, k, v, g, beta, ckpt, d_o, *, d_state_out=None, want_d_st
     return r
 
 
-@_on_stream
+@_placed
 def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, o=None, stream=None):
     """A short window (typically one token: T = 1) from the carried ``state``
     [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""

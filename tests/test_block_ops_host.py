@@ -144,3 +144,59 @@ def test_token_stride_of_views_and_dense_tensors(B, T):
         t = t.unflatten(2, (2, 64))
         want = 0 if t.is_contiguous() else 400 if B * T > 1 else 128
         assert binding._token_stride(t, "k", torch.float32, -1, (B, T, 2, 64)) == want
+
+
+class _Cuda:
+    """Stands in for torch.cuda on a machine with several devices."""
+
+    def __init__(self):
+        self.now = (0, None)
+
+    def _on(self, place):
+        import contextlib
+
+        @contextlib.contextmanager
+        def on():
+            was, self.now = self.now, place
+            yield
+            self.now = was
+        return on()
+
+    def current_device(self):
+        return self.now[0]
+
+    def device(self, index):
+        return self._on((index, None))
+
+    def stream(self, s):
+        return self._on((s.device.index, s))
+
+
+WRAPPERS = ("m3scan_fwd", "m3scan_fwd_state", "m3scan_bwd", "m3scan_bwd_state", "m3scan_decode", "m3scan_bwd_two_phase",
+            "m3scan_norm_fwd", "m3scan_norm_bwd", "m3scan_delta_fwd", "m3scan_delta_bwd", "m3scan_delta_decode")
+
+
+@pytest.mark.parametrize("name", WRAPPERS)
+def test_calls_run_on_their_tensors_device(name, monkeypatch):
+    """The library launches on the current device, so a wrapper makes its
+    tensors' device current (and its stream); a stream of another device is
+    refused."""
+    from types import SimpleNamespace as NS
+
+    cuda, seen = _Cuda(), []
+    monkeypatch.setattr(binding, "_TORCH", NS(cuda=cuda))
+    tensor = lambda index: NS(get_device=lambda: index)
+
+    def probe(x, stream=None):
+        seen.append((cuda.now, stream))
+        return "done"
+
+    placed = binding._placed(probe)
+    assert placed(tensor(0)) == "done" and placed(tensor(1)) == "done" and placed(x=tensor(2)) == "done"
+    assert [s[0][0] for s in seen] == [0, 1, 2] and cuda.now == (0, None)
+    s1 = NS(device=NS(index=1))
+    assert placed(tensor(1), stream=s1) == "done" and seen[-1] == ((1, s1), s1)
+    with pytest.raises(ValueError):
+        placed(tensor(0), stream=s1)
+    assert placed(tensor(-1)) == "done"  # (a host tensor: the call itself says what is wrong)
+    assert getattr(binding, name).__code__ is placed.__code__  # this wrapper is placed like the probe
