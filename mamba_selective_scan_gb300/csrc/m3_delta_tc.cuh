@@ -185,22 +185,27 @@ __device__ __forceinline__ void tc_mma_kq(uint32_t kq, uint32_t acc, uint64_t* m
 // [s, s + 1) / G of the heads' chunks laid end to end.  It starts with the
 // first chunks of the head that the next block ends, hands that head's state
 // on, goes through its whole heads, and ends with the last chunks of the
-// head that the block before began.  A share is at least a head long, so the
-// part handed on is never longer than what its receiver does before it.
+// head that the block before began.  There are no more blocks than heads, so a
+// share is at least a head long: a head has two blocks at most, and the part
+// handed on is never longer than what its receiver does before it.
 struct TcStep {
   int bh, c;          // head (batch row x value head), chunk
   bool first, last;   // of a run
   bool take, give;    // the run starts from, or ends in, a state handed over
 };
+inline unsigned delta_share_blocks(int64_t heads, int sms) { return (unsigned)(heads < sms ? heads : sms); }
 struct TcWalk {
   int nc, n, len_a, whole, h0, c0, ha, ca;
   bool stream;
-  __device__ __forceinline__ TcWalk(const DeltaArgs& a, int seg) {
-    nc = a.nc;
-    stream = a.stream;
+  __device__ __forceinline__ TcWalk(const DeltaArgs& a, int seg)
+      : TcWalk(a.stream, (int64_t)a.B * a.Hv, a.nc, blockIdx.x, gridDim.x, seg, a.seg_chunks) {}
+  __host__ __device__ __forceinline__ TcWalk(bool shares, int64_t heads, int chunks, unsigned block, unsigned blocks, int seg,
+                                             int seg_chunks) {
+    nc = chunks;
+    stream = shares;
     if (stream) {
-      const int64_t total = (int64_t)a.B * a.Hv * nc;
-      const int64_t r0 = total * blockIdx.x / gridDim.x, r1 = total * (blockIdx.x + 1) / gridDim.x;
+      const int64_t total = heads * nc;
+      const int64_t r0 = total * block / blocks, r1 = total * (block + 1) / blocks;
       const int hs = (int)(r0 / nc);
       c0 = (int)(r0 % nc);
       ha = (int)(r1 / nc);
@@ -210,13 +215,13 @@ struct TcWalk {
       whole = ha - h0 - 1;
       n = (int)(r1 - r0);
     } else {
-      ha = blockIdx.x;
-      ca = seg * a.seg_chunks;
-      len_a = n = min(nc, ca + a.seg_chunks) - ca;
+      ha = (int)block;
+      ca = seg * seg_chunks;
+      len_a = n = (nc < ca + seg_chunks ? nc : ca + seg_chunks) - ca;
       h0 = c0 = whole = 0;
     }
   }
-  __device__ __forceinline__ TcStep at(int i) const {
+  __host__ __device__ __forceinline__ TcStep at(int i) const {
     TcStep r;
     if (i < len_a) {
       r.bh = ha;
@@ -280,8 +285,8 @@ __device__ __forceinline__ void tma_tile_store(const CUtensorMap* map, uint32_t 
                ::"l"(reinterpret_cast<uint64_t>(map)), "r"(src), "r"(col), "r"(head), "r"(tok), "r"(b) : "memory");
 }
 
-// The chain kernels' grid: a block per (head, segment), or one per SM in
-// equal shares.  Those wait for a state that the block before hands over, so
+// The chain kernels' grid: a block per (head, segment), or one per SM (and not
+// more than heads) in equal shares.  Those wait for a state that the block before hands over, so
 // they are launched cooperatively (all of them resident at once).  Otherwise,
 // with `pdl`, the blocks may come up while the kernel before them ends.
 template <typename... Args, typename... Vals>
@@ -291,7 +296,7 @@ cudaError_t launch_delta_blocks(void (*kern)(Args...), const DeltaArgs& a, int t
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = a.stream ? dim3((unsigned)sms) : dim3((unsigned)(a.B * a.Hv), (unsigned)a.segs);
+  cfg.gridDim = a.stream ? dim3(delta_share_blocks((int64_t)a.B * a.Hv, sms)) : dim3((unsigned)(a.B * a.Hv), (unsigned)a.segs);
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
