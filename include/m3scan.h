@@ -499,14 +499,16 @@ typedef struct {
 m3_status m3scan_delta_plan(const m3_delta_dims* dims, m3_dtype act, m3_delta_plan* out);
 
 /* state NULL = zero.  state_out and ckpt are written where they are not
- * NULL; m3scan_delta_bwd needs ckpt. */
+ * NULL; m3scan_delta_bwd needs ckpt.  state_out may be state (carried in
+ * place); no other output may overlap an input. */
 m3_status m3scan_delta_fwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
                            const void* v, const void* g, const void* beta, const float* state,
                            void* o, float* state_out, float* ckpt, void* workspace,
                            size_t workspace_bytes, m3_stream_t stream);
 
 /* The derivative of sum(d_o * o) + sum(d_state_out * state_out).
- * d_state_out NULL = zero; d_state is written where it is not NULL. */
+ * d_state_out NULL = zero; d_state is written where it is not NULL,
+ * and may be d_state_out; no other output may overlap an input. */
 m3_status m3scan_delta_bwd(const m3_delta_dims* dims, m3_dtype act, const void* q, const void* k,
                            const void* v, const void* g, const void* beta, const float* ckpt,
                            const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,

@@ -248,7 +248,7 @@ m3_delta_tc_rev_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
         return;
       }
       if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
-      const bool own = chunk(t) < a.nc - 1;
+      const bool own = chunk(t) < a.nc - 1 || a.segs > 1;  // (of the last segment too: see the forward)
       const float* src = own ? a.seg_start + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX
                              : a.ds_out ? a.ds_out + (size_t)t.bh * a.DK * a.DV : nullptr;
       const int ld = own ? DMAX : a.DV;

@@ -248,9 +248,11 @@ m3_delta_tc_fwd_kernel(const __grid_constant__ DeltaArgs a, const __grid_constan
       if (lane == 0) mbar_arrive(bar);
     };
     auto get_state = [&](const TcStep& t) {  // the state a run starts from
-      // the carried state, what the segments before left, or a state handed over
+      // the carried state, what the chaining of segments left (the first one's
+      // too: the last one's may be written where the carried state is), or a
+      // state handed over
       if (t.take && wait.ok) wait.ok = flag_wait(a.flags + t.bh);
-      const bool own = t.c > 0;
+      const bool own = t.c > 0 || a.segs > 1;
       const float* src = own ? a.seg_start + ((size_t)t.bh * a.segs + seg) * DMAX * DMAX
                              : a.s_in ? a.s_in + (size_t)t.bh * a.DK * a.DV : nullptr;
       const int ld = own ? DMAX : a.DV;
@@ -790,6 +792,7 @@ __global__ void __launch_bounds__(512) m3_delta_seg_kernel(const __grid_constant
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (first && k < a.DK && v < a.DV) x = *reinterpret_cast<const float4*>(first + ((size_t)bh * a.DK + k) * a.DV + v);
   *reinterpret_cast<float4*>(&S[k][vq]) = x;
+  *reinterpret_cast<float4*>(a.seg_start + where(0) + (size_t)k * DMAX + v) = x;
   TcWait wait;
   for (int n = 0; n + 1 < a.segs; ++n) {
     x = *reinterpret_cast<const float4*>(a.seg_end + where(n) + (size_t)k * DMAX + v);

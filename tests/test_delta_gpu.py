@@ -421,3 +421,22 @@ def test_decays_between_resets(every, low, dt):
     y["g"] = x["g"].clamp(min=-800.0)  # exp(-800) is 0 in float64
     ref = delta_ref_grads(y, 64 ** -0.5, True)
     _check_all(got, ref, ["o", "state_out", "dq", "dk", "dv", "dg", "dbeta", "d_state"])
+
+
+@pytest.mark.parametrize("B,T,Hk,Hv,dt", [(1, 1100, 1, 2, "bf16"), (2, 2000, 2, 2, "bf16"), (8, 130, 10, 20, "bf16"),
+                                          (2, 100, 1, 2, "bf16"), (2, 70, 1, 2, "f32"), (2, 0, 1, 2, "bf16")])
+def test_state_in_place(B, T, Hk, Hv, dt):
+    """The state carried in place, and its gradient: the bits of calls with
+    separate ones (with time segments, whose last may end before the first
+    one's block starts, too)."""
+    x = delta_inputs(B, T, Hk, Hv, 128, 64, DT[dt], seed=T, device="cuda")
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    want = _run(x, True)
+    for _ in range(5):
+        S, dS = x["state"].clone(), x["d_state_out"].clone()
+        o, st, ck = binding.m3scan_delta_fwd(*args, state=S, state_out=S, qk_l2norm=True, want_ckpt=True)
+        r = binding.m3scan_delta_bwd(*args, ck, x["d_o"], d_state_out=dS, out={"d_state": dS}, qk_l2norm=True)
+        assert st is S and r["d_state"] is dS
+        assert torch.equal(o, want["o"]) and torch.equal(S, want["state_out"]) and torch.equal(dS, want["d_state"])
+        for n in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(r[n], want[n]), n
