@@ -476,6 +476,14 @@ m3_status m3scan_norm_bwd(const m3_norm_dims* dims, m3_dtype act, const void* dy
  * g is a log decay: normally <= 0; -inf forgets everything.  head_k and
  * head_v are multiples of 8 up to 128.  Activation and state pointers are
  * 16-byte aligned.  All results are the same bits on every call.
+ *
+ * States are f32.  With bf16 activations what is not an input enters the
+ * products with 17 bits (states come out at about 5e-6), and the gradients
+ * are those of a start state that is rounded to bf16 every 64 tokens.
+ *
+ * Outputs and states are not finite exactly where the recurrence's are not.
+ * Gradients are NaN wherever the derivative is, and may be NaN elsewhere in
+ * the same 64 tokens of that key head.
  */
 typedef struct {
     int64_t batch, seq_len, k_heads, v_heads, head_k, head_v;

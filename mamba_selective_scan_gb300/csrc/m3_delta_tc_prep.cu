@@ -122,11 +122,12 @@ __device__ __forceinline__ void block_store(unsigned char* t, const float (&d)[4
 // are bound by that chain; this work has no order, so it is done here once,
 // with full SMs, and read back (34 KB per chunk and head).
 //
-// Bound by HBM for many chunks (32 KB in, 34 KB out per item): 16384 items
-// take 178 us, 6.1 TB/s; 4 x 4096 x 40 heads (K and Q of 20 heads) 114 us;
-// 8 x 2048 x 12 heads 39 us.  With I + A's blocks in f32, split at every use,
-// and a block per item it was bound by shared memory and barriers: 246, 147
-// and 51 us.
+// Bound by HBM for many chunks (32 KB in, 34 KB out per item), between events
+// with L2 flushed before: 16384 items take 192 us, 5.7 TB/s; 4 x 4096 x 40 heads
+// (K and Q of 20 heads) 123 us; 8 x 2048 x 12 heads 45 us.  10, 6 and 2 us of
+// it are the gates' second term and the search for values that are not finite.
+// With I + A's blocks in f32, split at every use, and a block per item it was
+// bound by shared memory and barriers, and took a third longer.
 template <bool L2>
 __global__ void __launch_bounds__(TP_THREADS, PREP_PER_SM)
 m3_delta_tc_prep_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ CUtensorMap mq,
