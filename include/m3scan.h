@@ -529,6 +529,129 @@ m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const voi
                               const void* v, const void* g, const void* beta, float* state,
                               void* o, m3_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Queries and keys on their way into attention: the norm of each head and the
+ * rotation by position, in one pass.
+ *
+ *   n = x / sqrt(sum x^2 / head_dim + eps) * weight           per token and head
+ *   pair (a, b) of n -> (a cos f - b sin f, a sin f + b cos f)
+ *   f = position * inv_freq[i],  i < rot_dim / 2
+ *
+ * Pair i is (i, i + rot_dim / 2), or with interleaved (2 i, 2 i + 1); values
+ * past rot_dim are normalised only.
+ *
+ *   q, q_out, dq_out, dq : [batch, seq_len, q_heads, head_dim]  activation dtype
+ *   k, k_out, dk_out, dk : [batch, seq_len, k_heads, head_dim]  activation dtype
+ *   q_weight, k_weight and their gradients : [head_dim]  float32
+ *   positions : [batch, seq_len] int64, batch rows position_stride apart
+ *               (0: [seq_len], the same for every batch row)
+ *   inv_freq  : [rot_dim / 2] float32, radians per position
+ *
+ * Angles are exact for every position up to the rounding of inv_freq / (2 pi)
+ * to 2^-64 turns: far positions lose nothing.  Sums are f32.  head_dim 2 to
+ * 256; tensors whose heads and tokens start on 16 bytes (and, not
+ * interleaved, rot_dim / 2 a multiple of 8 for bf16, 4 for f32) run the vector
+ * kernels.  The weights' gradients are fixed-order sums: identical bits on
+ * every call.
+ */
+typedef struct {
+    int64_t batch, seq_len, q_heads, k_heads, head_dim, rot_dim;
+    /* Elements between consecutive tokens (batch rows follow each other at
+       the same stride); 0 = dense.  A larger stride lets a tensor be columns
+       of one projection's output or of its gradient. */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int64_t dq_stride, dk_stride, dq_out_stride, dk_out_stride;
+    int64_t position_stride;
+    float eps;                      /* >= 0 */
+    int32_t interleaved;
+    int32_t accumulate_param_grads; /* 1: d_q_weight, d_k_weight are added to; 0: overwritten */
+    int32_t reserved;               /* 0 */
+} m3_qkrot_dims;
+
+typedef struct {
+    int64_t workspace_bytes;        /* of m3scan_qkrot_bwd */
+} m3_qkrot_plan;
+
+m3_status m3scan_qkrot_plan(const m3_qkrot_dims* dims, m3_dtype act, m3_qkrot_plan* out);
+
+/* q_weight, k_weight NULL: ones.  positions and inv_freq may be NULL when
+ * rot_dim is 0.  q_out may be q and k_out may be k (at the same stride); no
+ * other output may overlap an input. */
+m3_status m3scan_qkrot_fwd(const m3_qkrot_dims* dims, m3_dtype act, const void* q, const void* k,
+                           const float* q_weight, const float* k_weight, const int64_t* positions,
+                           const float* inv_freq, void* q_out, void* k_out, m3_stream_t stream);
+
+/* q and k: what the forward was given.  dq may be dq_out and dk may be dk_out
+ * (at the same stride).  d_q_weight and d_k_weight may be NULL. */
+m3_status m3scan_qkrot_bwd(const m3_qkrot_dims* dims, m3_dtype act, const void* dq_out,
+                           const void* dk_out, const void* q, const void* k,
+                           const float* q_weight, const float* k_weight, const int64_t* positions,
+                           const float* inv_freq, void* dq, void* dk, float* d_q_weight,
+                           float* d_k_weight, void* workspace, size_t workspace_bytes,
+                           m3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: a state S [head_k, head_v] per
+ * (batch row, value head) that fades at the head's own constant rate,
+ *
+ *   S_t = exp(log_decay) S_{t-1} + k_t v_t^T
+ *   o_t = scale S_t^T q_t
+ *
+ * Value head h uses key head h / (v_heads / k_heads).
+ *
+ *   q, k, dq, dk  : [batch, seq_len, k_heads, head_k]  activation dtype
+ *   v, dv         : [batch, seq_len, v_heads, head_v]  activation dtype
+ *   o, d_o        : the same, dense
+ *   log_decay     : [v_heads] float32, normally <= 0 (-inf keeps nothing); a
+ *                   constant of the layer, not differentiated
+ *   state, state_out, d_state, d_state_out : [batch, v_heads, head_k, head_v] float32
+ *
+ * head_k and head_v are multiples of 8 up to 128.  Activation and state
+ * pointers are 16-byte aligned.  All results are the same bits on every call.
+ * States are f32.
+ */
+typedef struct {
+    int64_t batch, seq_len, k_heads, v_heads, head_k, head_v;
+    /* Elements between consecutive tokens of q, k, v and of dq, dk, dv (the
+       rows of a batch row follow each other at the same stride); 0 = dense.
+       stride x element size must be a multiple of 16. */
+    int64_t q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
+    float scale;       /* 0 = 1 / sqrt(head_k) */
+    int32_t reserved;  /* 0 */
+} m3_linattn_dims;
+
+typedef struct {
+    int64_t workspace_bytes;     /* enough for both directions */
+    int64_t fwd_workspace_bytes; /* enough for m3scan_linattn_fwd */
+    int32_t fwd_launches, bwd_launches;
+} m3_linattn_plan;
+
+m3_status m3scan_linattn_plan(const m3_linattn_dims* dims, m3_dtype act, m3_linattn_plan* out);
+
+/* state NULL = zero.  state_out is written where it is not NULL and may be
+ * state (carried in place; a backward needs the state that came in).  No
+ * other output may overlap an input. */
+m3_status m3scan_linattn_fwd(const m3_linattn_dims* dims, m3_dtype act, const void* q,
+                             const void* k, const void* v, const float* log_decay,
+                             const float* state, void* o, float* state_out, void* workspace,
+                             size_t workspace_bytes, m3_stream_t stream);
+
+/* The derivative of sum(d_o * o) + sum(d_state_out * state_out); needs no
+ * checkpoints, only what the forward was given.  state and d_state_out NULL =
+ * zero; d_state is written where it is not NULL, and may be d_state_out; no
+ * other output may overlap an input. */
+m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const void* q,
+                             const void* k, const void* v, const float* log_decay,
+                             const float* state, const void* d_o, const float* d_state_out,
+                             void* dq, void* dk, void* dv, float* d_state, void* workspace,
+                             size_t workspace_bytes, m3_stream_t stream);
+
+/* A short window (typically one token) from the carried state, which is
+ * updated in place; no workspace. */
+m3_status m3scan_linattn_decode(const m3_linattn_dims* dims, m3_dtype act, const void* q,
+                                const void* k, const void* v, const float* log_decay,
+                                float* state, void* o, m3_stream_t stream);
+
 /* A static, human-readable name for a status code. */
 const char* m3scan_status_string(m3_status status);
 

@@ -37,7 +37,9 @@ EXPORTS = ("m3scan_plan", "m3scan_fwd", "m3scan_bwd", "m3scan_fwd_state", "m3sca
            "m3scan_bwd_scan", "m3scan_conv_bwd", "m3scan_decode", "m3scan_bwd_noalloc", "m3scan_status_string", "m3scan_last_cuda_error",
            "m3scan_version", "m3scan_get_status", "m3scan_device_status",
            "m3scan_selftest_wait_timeout", "m3scan_norm_plan", "m3scan_norm_fwd", "m3scan_norm_bwd",
-           "m3scan_delta_plan", "m3scan_delta_fwd", "m3scan_delta_bwd", "m3scan_delta_decode")
+           "m3scan_delta_plan", "m3scan_delta_fwd", "m3scan_delta_bwd", "m3scan_delta_decode",
+           "m3scan_qkrot_plan", "m3scan_qkrot_fwd", "m3scan_qkrot_bwd",
+           "m3scan_linattn_plan", "m3scan_linattn_fwd", "m3scan_linattn_bwd", "m3scan_linattn_decode")
 
 # size of the library's own scratch array used by m3scan_bwd_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -112,6 +114,30 @@ class M3DeltaPlan(ctypes.Structure):
                 ("fwd_launches", ctypes.c_int32), ("bwd_launches", ctypes.c_int32)]
 
 
+class M3QkrotDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "seq_len", "q_heads", "k_heads", "head_dim", "rot_dim", "q_stride", "k_stride",
+        "q_out_stride", "k_out_stride", "dq_stride", "dk_stride", "dq_out_stride", "dk_out_stride",
+        "position_stride")] + [("eps", ctypes.c_float), ("interleaved", ctypes.c_int32),
+                               ("accumulate_param_grads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class M3QkrotPlan(ctypes.Structure):
+    _fields_ = [("workspace_bytes", ctypes.c_int64)]
+
+
+class M3LinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "seq_len", "k_heads", "v_heads", "head_k", "head_v", "q_stride", "k_stride",
+        "v_stride", "dq_stride", "dk_stride", "dv_stride")] + [
+            ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class M3LinattnPlan(ctypes.Structure):
+    _fields_ = [("workspace_bytes", ctypes.c_int64), ("fwd_workspace_bytes", ctypes.c_int64),
+                ("fwd_launches", ctypes.c_int32), ("bwd_launches", ctypes.c_int32)]
+
+
 _LIB = None
 _LOCK = threading.Lock()
 _vp = ctypes.c_void_p
@@ -182,6 +208,7 @@ def _lib_handle(build_if_missing: bool = True):
             lib.m3scan_selftest_wait_timeout.restype = ctypes.c_int
             lib.m3scan_selftest_wait_timeout.argtypes = [_vp, _vp]
             pn, pd = ctypes.POINTER(M3NormDims), ctypes.POINTER(M3DeltaDims)
+            pr, pl = ctypes.POINTER(M3QkrotDims), ctypes.POINTER(M3LinattnDims)
             ci, sz = ctypes.c_int, ctypes.c_size_t
             for name, args in (
                     ("m3scan_norm_plan", [pn, ci, ctypes.POINTER(M3NormPlan)]),
@@ -190,7 +217,14 @@ def _lib_handle(build_if_missing: bool = True):
                     ("m3scan_delta_plan", [pd, ci, ctypes.POINTER(M3DeltaPlan)]),
                     ("m3scan_delta_fwd", [pd, ci] + [_vp] * 10 + [sz, _vp]),
                     ("m3scan_delta_bwd", [pd, ci] + [_vp] * 15 + [sz, _vp]),
-                    ("m3scan_delta_decode", [pd, ci] + [_vp] * 8)):
+                    ("m3scan_delta_decode", [pd, ci] + [_vp] * 8),
+                    ("m3scan_qkrot_plan", [pr, ci, ctypes.POINTER(M3QkrotPlan)]),
+                    ("m3scan_qkrot_fwd", [pr, ci] + [_vp] * 9),
+                    ("m3scan_qkrot_bwd", [pr, ci] + [_vp] * 13 + [sz, _vp]),
+                    ("m3scan_linattn_plan", [pl, ci, ctypes.POINTER(M3LinattnPlan)]),
+                    ("m3scan_linattn_fwd", [pl, ci] + [_vp] * 8 + [sz, _vp]),
+                    ("m3scan_linattn_bwd", [pl, ci] + [_vp] * 12 + [sz, _vp]),
+                    ("m3scan_linattn_decode", [pl, ci] + [_vp] * 7)):
                 getattr(lib, name).restype = ctypes.c_int
                 getattr(lib, name).argtypes = args
             _LIB = lib
@@ -964,4 +998,253 @@ def m3scan_delta_decode(q, k, v, g, beta, state, *, scale=0.0, qk_l2norm=False, 
                                   state.data_ptr(), o.data_ptr(), _stream_of(stream, index))
     if st:
         raise M3Error(st, "m3scan_delta_decode")
+    return o
+
+
+# ---------------------------------------------------------------------------
+# norm and rotation of queries and keys
+# ---------------------------------------------------------------------------
+
+def m3scan_qkrot_plan(dims: M3QkrotDims, act: int) -> M3QkrotPlan:
+    out = M3QkrotPlan()
+    st = _lib_handle().m3scan_qkrot_plan(ctypes.byref(dims), int(act), ctypes.byref(out))
+    if st != 0:
+        raise M3Error(st, "m3scan_qkrot_plan")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _qkrot_sizes(code, qshape, kshape, rot, strides, position_stride, eps, interleaved, accumulate):
+    if len(qshape) != 4 or len(kshape) != 4 or qshape[:2] != kshape[:2] or qshape[3] != kshape[3]:
+        raise ValueError(f"q and k must be [batch, seq_len, heads, head size], got {tuple(qshape)}, {tuple(kshape)}")
+    B, T, Hq, D = qshape
+    dims = M3QkrotDims(B, T, Hq, kshape[2], D, rot, *strides, position_stride, eps, interleaved, accumulate, 0)
+    return ctypes.byref(dims), m3scan_qkrot_plan(dims, code).workspace_bytes
+
+
+def _qkrot_positions(positions, B, T, index, torch):
+    """(address, elements between batch rows) of int64 positions [B, T] or [T]."""
+    if positions is None:
+        return None, 0
+    if positions.dtype is not torch.int64:
+        raise TypeError(f"positions must be {torch.int64}, got {positions.dtype}")
+    if positions.get_device() != index:
+        raise ValueError(f"positions is on {positions.device}, expected cuda:{index}")
+    shape = positions.shape
+    if shape == (T,):
+        batch = 0
+    elif shape == (B, T):
+        batch = positions.stride(0) if B > 1 else 0
+        if B > 1 and 0 < batch < T or batch < 0:
+            raise ValueError(f"positions: batch rows overlap, strides {positions.stride()}")
+    else:
+        raise ValueError(f"positions must have shape {(B, T)} or {(T,)}, got {tuple(shape)}")
+    if T > 1 and positions.stride(-1) != 1:
+        raise ValueError(f"positions must be dense in time, got strides {positions.stride()}")
+    return positions.data_ptr(), batch
+
+
+def _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch):
+    """Checks the inputs; returns (dtype code, device index, token strides of q
+    and k, address and batch stride of the positions, rotated size)."""
+    dt, index, qshape, kshape = q.dtype, q.get_device(), q.shape, k.shape
+    code = _act_code(q)
+    if index < 0:
+        _check(q, "q")
+    if len(qshape) != 4 or len(kshape) != 4:
+        raise ValueError(f"q and k must be [batch, seq_len, heads, head size], got {tuple(qshape)}, {tuple(kshape)}")
+    B, T, _, D = qshape
+    sq = _token_stride(q, "q", dt, index, qshape)
+    sk = _token_stride(k, "k", dt, index, (B, T, kshape[2], D))
+    f32 = torch.float32
+    _need(q_weight, "q_weight", f32, index, (D,))
+    _need(k_weight, "k_weight", f32, index, (D,))
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", f32, index, (inv_freq.numel(),))
+        rot = 2 * inv_freq.numel()
+        if rot and positions is None:
+            raise ValueError("positions are needed where inv_freq is given")
+    pos, pos_stride = _qkrot_positions(positions, B, T, index, torch)
+    return code, index, sq, sk, pos, pos_stride, rot
+
+
+@_placed
+def m3scan_qkrot_fwd(q, k, q_weight, k_weight, positions, inv_freq, *, eps=1e-6, interleaved=False,
+                     q_out=None, k_out=None, stream=None):
+    """Root-mean-square norm of every head of q [B, T, Hq, D] and k [B, T, Hk,
+    D] (column views of a projection's output are fine) with weights [D] (f32;
+    None = ones), and their rotation by ``positions`` (int64 [B, T] or [T]) and
+    ``inv_freq`` (f32 [R], 2 R <= D; None = no rotation).  Pairs are (i, i + R),
+    or neighbours with ``interleaved``.  Returns (q_out, k_out), which may be q
+    and k themselves."""
+    torch = _TORCH or _torch()
+    code, index, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
+    dt, qshape, kshape = q.dtype, q.shape, k.shape
+    if q_out is None:
+        q_out, sqo = torch.empty(qshape, dtype=dt, device=q.device), 0
+    else:
+        sqo = _token_stride(q_out, "q_out", dt, index, qshape)
+    if k_out is None:
+        k_out, sko = torch.empty(kshape, dtype=dt, device=q.device), 0
+    else:
+        sko = _token_stride(k_out, "k_out", dt, index, kshape)
+    dims, _ = _qkrot_sizes(code, qshape, kshape, rot, (sq, sk, sqo, sko, 0, 0, 0, 0), pos_stride, float(eps),
+                           int(bool(interleaved)), 0)
+    st = _LIB.m3scan_qkrot_fwd(dims, code, q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos,
+                               _ptr(inv_freq), q_out.data_ptr(), k_out.data_ptr(), _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_qkrot_fwd")
+    return q_out, k_out
+
+
+@_placed
+def m3scan_qkrot_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, *, eps=1e-6,
+                     interleaved=False, accumulate_param_grads=False, out=None, workspace=None, stream=None):
+    """Backward of ``m3scan_qkrot_fwd`` (the same q, k, weights, positions,
+    inv_freq, eps and interleaved).  Returns a dict: dq, dk (activation dtype;
+    in ``out`` they may be column views of a projection's gradient, or dq_out
+    and dk_out themselves) and d_q_weight, d_k_weight (f32 [D]; None for a
+    weight that is None)."""
+    torch = _TORCH or _torch()
+    code, index, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
+    dt, dev, f32, D = q.dtype, q.device, torch.float32, q.shape[3]
+    o = dict(out) if out else {}
+    strides = []
+    for n, t in (("dq", q), ("dk", k)):
+        if o.get(n) is None:
+            o[n] = torch.empty(t.shape, dtype=dt, device=dev)
+        strides.append(_token_stride(o[n], n, dt, index, t.shape))
+    strides += [_token_stride(dq_out, "dq_out", dt, index, q.shape), _token_stride(dk_out, "dk_out", dt, index, k.shape)]
+    new = torch.zeros if accumulate_param_grads else torch.empty
+    for n, w in (("d_q_weight", q_weight), ("d_k_weight", k_weight)):
+        if o.get(n) is None:
+            o[n] = None if w is None else new(D, dtype=f32, device=dev)
+        else:
+            _need(o[n], n, f32, index, (D,))
+    dims, nbytes = _qkrot_sizes(code, q.shape, k.shape, rot, (sq, sk, 0, 0, *strides), pos_stride, float(eps),
+                                int(bool(interleaved)), int(bool(accumulate_param_grads)))
+    ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
+    st = _LIB.m3scan_qkrot_bwd(dims, code, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                               _ptr(q_weight), _ptr(k_weight), pos, _ptr(inv_freq), o["dq"].data_ptr(),
+                               o["dk"].data_ptr(), _ptr(o["d_q_weight"]), _ptr(o["d_k_weight"]), ws, nbytes,
+                               _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_qkrot_bwd")
+    return o
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head
+# ---------------------------------------------------------------------------
+
+def m3scan_linattn_plan(dims: M3LinattnDims, act: int) -> M3LinattnPlan:
+    out = M3LinattnPlan()
+    st = _lib_handle().m3scan_linattn_plan(ctypes.byref(dims), int(act), ctypes.byref(out))
+    if st != 0:
+        raise M3Error(st, "m3scan_linattn_plan")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _linattn_sizes(code, kshape, vshape, strides, scale):
+    """(dims, state shape, (forward, any) workspace bytes) for those shapes."""
+    if len(kshape) != 4 or len(vshape) != 4 or tuple(kshape[:2]) != tuple(vshape[:2]):
+        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(kshape)}, {tuple(vshape)}")
+    B, T, Hv, dv = vshape
+    Hk, dk = kshape[2:]
+    dims = M3LinattnDims(B, T, Hk, Hv, dk, dv, *strides, float(scale), 0)
+    pl = m3scan_linattn_plan(dims, code)
+    return ctypes.byref(dims), (B, Hv, dk, dv), (pl.fwd_workspace_bytes, pl.workspace_bytes)
+
+
+def _linattn_inputs(q, k, v, log_decay, torch):
+    """Checks the inputs; returns (dtype code, device index, k's and v's
+    shapes, token strides of q, k, v)."""
+    dt, index = v.dtype, v.get_device()
+    code = _act_code(v)
+    kshape, vshape = k.shape, v.shape
+    if index < 0:
+        _check(v, "v")
+    if len(kshape) != 4 or len(vshape) != 4:
+        raise ValueError(f"k and v must be [batch, seq_len, heads, head size], got {tuple(kshape)}, {tuple(vshape)}")
+    _need(log_decay, "log_decay", torch.float32, index, vshape[2:3])
+    if (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and q.dtype is dt and k.dtype is dt
+            and q.shape == kshape and q.get_device() == index and k.get_device() == index):
+        return code, index, kshape, vshape, 0, 0, 0
+    kwant = (*vshape[:2], *kshape[2:])
+    return (code, index, kshape, vshape, _token_stride(q, "q", dt, index, kwant), _token_stride(k, "k", dt, index, kwant),
+            _token_stride(v, "v", dt, index, vshape))
+
+
+@_placed
+def m3scan_linattn_fwd(q, k, v, log_decay, *, state=None, scale=0.0, want_state=True, o=None, state_out=None,
+                       workspace=None, stream=None):
+    """Linear attention with a decay per head over a sequence.  q, k [B, T, Hk,
+    dk], v [B, T, Hv, dv] (column views of a projection's output are fine), bf16
+    or f32; ``log_decay`` [Hv] f32; ``state`` [B, Hv, dk, dv] f32 or None
+    (zero).  Returns (o, state_out or None)."""
+    torch = _TORCH or _torch()
+    dev, f32 = v.device, torch.float32
+    code, index, kshape, vshape, sq, sk, sv = _linattn_inputs(q, k, v, log_decay, torch)
+    dims, sshape, nbytes = _linattn_sizes(code, kshape, vshape, (sq, sk, sv, 0, 0, 0), scale)
+    _need(state, "state", f32, index, sshape)
+    o = torch.empty(vshape, dtype=v.dtype, device=dev) if o is None else _need(o, "o", v.dtype, index, vshape)
+    if state_out is not None:
+        _need(state_out, "state_out", f32, index, sshape)
+    elif want_state:
+        state_out = torch.empty(sshape, dtype=f32, device=dev)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[0], torch, dev)
+    st = _LIB.m3scan_linattn_fwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state),
+                                 o.data_ptr(), _ptr(state_out), ws, nbytes, _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_linattn_fwd")
+    return o, state_out
+
+
+@_placed
+def m3scan_linattn_bwd(q, k, v, log_decay, d_o, *, state=None, d_state_out=None, want_d_state=False, scale=0.0,
+                       out=None, workspace=None, stream=None):
+    """Backward of ``m3scan_linattn_fwd`` (same q, k, v, log_decay, ``state``
+    and scale; no checkpoints).  Returns a dict: dq, dk, dv (activation dtype)
+    and d_state (f32, None unless wanted).  dq, dk and dv in ``out`` may be
+    column views of a projection's gradient."""
+    torch = _TORCH or _torch()
+    dev, dt, f32 = v.device, v.dtype, torch.float32
+    code, index, kshape, vshape, sq, sk, sv = _linattn_inputs(q, k, v, log_decay, torch)
+    r = dict(out) if out else {}
+    strides = []
+    for n, t in (("dq", q), ("dk", k), ("dv", v)):
+        if r.get(n) is None:
+            r[n] = torch.empty(t.shape, dtype=dt, device=dev)
+        strides.append(_token_stride(r[n], n, dt, index, t.shape))
+    dims, sshape, nbytes = _linattn_sizes(code, kshape, vshape, (sq, sk, sv, *strides), scale)
+    if r.get("d_state") is None:
+        r["d_state"] = torch.empty(sshape, dtype=f32, device=dev) if want_d_state else None
+    _need(state, "state", f32, index, sshape)
+    _need(d_state_out, "d_state_out", f32, index, sshape)
+    _need(r["d_state"], "d_state", f32, index, sshape)
+    _need(d_o, "d_o", dt, index, vshape)
+    ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev)
+    st = _LIB.m3scan_linattn_bwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state),
+                                 d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(), r["dk"].data_ptr(),
+                                 r["dv"].data_ptr(), _ptr(r["d_state"]), ws, nbytes, _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_linattn_bwd")
+    return r
+
+
+@_placed
+def m3scan_linattn_decode(q, k, v, log_decay, state, *, scale=0.0, o=None, stream=None):
+    """A short window (typically one token: T = 1) from the carried ``state``
+    [B, Hv, dk, dv] (f32), which is updated in place.  Returns o."""
+    torch = _TORCH or _torch()
+    code, index, kshape, vshape, sq, sk, sv = _linattn_inputs(q, k, v, log_decay, torch)
+    dims, sshape, _ = _linattn_sizes(code, kshape, vshape, (sq, sk, sv, 0, 0, 0), scale)
+    o = torch.empty(vshape, dtype=v.dtype, device=v.device) if o is None else _need(o, "o", v.dtype, index, vshape)
+    _need(state, "state", torch.float32, index, sshape)
+    st = _LIB.m3scan_linattn_decode(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                    state.data_ptr(), o.data_ptr(), _stream_of(stream, index))
+    if st:
+        raise M3Error(st, "m3scan_linattn_decode")
     return o
