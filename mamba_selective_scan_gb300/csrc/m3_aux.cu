@@ -1,6 +1,7 @@
 // m3_aux.cu -- the conv backward of the two-phase backward and the decode
 // kernels, and their launch.
 #include "m3_delta.cuh"
+#include "m3_lin.cuh"
 
 namespace m3 {
 
@@ -14,12 +15,13 @@ cudaError_t take_aux_status(unsigned* out) {
     const unsigned zero = 0;
     e = cudaMemcpyToSymbol(g_aux_status, &zero, sizeof(zero));
   }
-  // the gated delta rule's units report through this one
-  unsigned f = 0, b = 0, q = 0;
+  // the gated delta rule's and linear attention's units report through this one
+  unsigned f = 0, b = 0, q = 0, l = 0;
   if (e == cudaSuccess) e = take_delta_fwd_status(&f);
   if (e == cudaSuccess) e = take_delta_bwd_status(&b);
   if (e == cudaSuccess) e = take_delta_prep_status(&q);
-  *out = v | f | b | q;
+  if (e == cudaSuccess) e = take_lin_status(&l);
+  *out = v | f | b | q | l;
   return e;
 }
 

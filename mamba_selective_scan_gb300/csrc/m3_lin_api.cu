@@ -14,6 +14,13 @@ struct LinPlan {
   int B, T, Hk, Hv, DK, DV, share;
   size_t fwd_ws_bytes, ws_bytes;
   size_t o_pdq, o_pdk, o_dstate;  // workspace offsets
+  bool tc;                        // the tensor-core kernels
+  int nc;
+  struct Walk {                   // of the forward (one pass), of the backward (three)
+    bool stream;
+    int segs, seg_chunks;
+    size_t o_start, o_end, o_flags;
+  } walk[2];
   int fwd_launches, bwd_launches;
 };
 
@@ -53,7 +60,20 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  p->fwd_ws_bytes = off;
+  // (a few tokens by the recurrence, without the chunks' latency)
+  p->tc = act == M3_BF16 && p->T > 1;
+  p->nc = (p->T + LIN_C - 1) / LIN_C;
+  for (int i = 0; i < 2; ++i) {
+    LinPlan::Walk& w = p->walk[i];
+    const int64_t items = (int64_t)(i ? 3 : 1) * p->B * p->Hv;
+    w.segs = 1;
+    w.seg_chunks = p->nc;
+    w.stream = p->tc && items > 152;
+    w.o_start = take(p->tc && w.stream ? (size_t)items * LIN_DMAX * LIN_DMAX * 4 : 0);
+    w.o_end = off;
+    w.o_flags = take(w.stream ? (size_t)items * 4 : 0);
+    if (i == 0) p->fwd_ws_bytes = off;
+  }
   // the backward's: shares of dq and dk where key heads are shared, and a
   // copy of a state gradient that is to be overwritten
   const size_t part = p->share > 1 ? (size_t)p->B * p->T * p->Hv * p->DK * 4 : 0;
@@ -89,10 +109,21 @@ LinPass lin_fwd_pass(const m3_linattn_dims* d, const LinPlan& p, const void* q, 
   return r;
 }
 
-cudaError_t lin_launch(const LinArgs& a, m3_dtype act, cudaStream_t s) {
+cudaError_t lin_launch(LinArgs a, const LinPlan& p, m3_dtype act, void* workspace, cudaStream_t s) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
+  if (p.tc) {
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    const LinPlan::Walk& w = p.walk[a.np > 1];
+    a.status = static_cast<unsigned*>(workspace);
+    a.nc = p.nc;
+    a.stream = w.stream; a.segs = w.segs; a.seg_chunks = w.seg_chunks;
+    a.seg_start = reinterpret_cast<float*>(ws + w.o_start);
+    a.seg_end = reinterpret_cast<float*>(ws + w.o_end);
+    a.flags = reinterpret_cast<unsigned*>(ws + w.o_flags);
+    return launch_lin_tc(a, s, sms);
+  }
   return act == M3_BF16 ? launch_lin_rec<__nv_bfloat16>(a, s, sms) : launch_lin_rec<float>(a, s, sms);
 }
 
@@ -148,11 +179,10 @@ m3_status m3scan_linattn_fwd(const m3_linattn_dims* dims, m3_dtype act, const vo
   st = check_workspace(workspace, workspace_bytes, p.fwd_ws_bytes);
   if (st != M3_OK) return st;
   LinArgs a = lin_args(dims, p, log_decay);
-  a.status = static_cast<unsigned*>(workspace);
   a.np = 1;
   a.p[0] = lin_fwd_pass(dims, p, q, k, v);
   a.p[0].out = o; a.p[0].s_in = state; a.p[0].s_out = state_out;
-  return note(lin_launch(a, act, s)) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+  return note(lin_launch(a, p, act, workspace, s)) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
 m3_status m3scan_linattn_decode(const m3_linattn_dims* dims, m3_dtype act, const void* q, const void* k, const void* v,
@@ -196,7 +226,6 @@ m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const vo
     d_state_out = copy;
   }
   LinArgs a = lin_args(dims, p, log_decay);
-  a.status = static_cast<unsigned*>(workspace);
   a.np = 3;
   const LinPass f = lin_fwd_pass(dims, p, q, k, v);
   const int64_t kw = (int64_t)p.Hk * p.DK, vw = (int64_t)p.Hv * p.DV, pw = (int64_t)p.Hv * p.DK;
@@ -231,7 +260,7 @@ m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const vo
   pq.out = shared ? part[0] : dq;
   pq.os = shared ? pw : or_dense(dims->dq_stride, kw);
   pq.oh = 1; pq.out_f32 = pk.out_f32;
-  cudaError_t e = lin_launch(a, act, s);
+  cudaError_t e = lin_launch(a, p, act, workspace, s);
   if (e == cudaSuccess && shared) {
     LinShare sh{};
     sh.part[0] = part[0]; sh.part[1] = part[1];
