@@ -41,16 +41,18 @@ enum { F_REV = 1, F_TAKE = 2, F_GIVE = 4, F_FIRST = 8, F_LAST = 16 };
 
 // A step's factors (lam the head's decay, n the chunk's tokens)
 struct LinVec {
-  float fk[TC];      // of a token's share in the next state
-  float fo[TC];      // of the start state in a token's output
-  float pz[2 * TC];  // at 64 + i - j: of token j's share in token i's output
-  float near, off;   // lam^n
-  float pad[2];
+  uint32_t fk[3][TC / 2];  // of a token's share in the next state, as three bf16 terms (pairs of tokens)
+  float fo[TC];            // of the start state in a token's output
+  // of token j's share in token i's output: pz[0][64 + j - i], and one place
+  // earlier in pz[1], so that the two of a pair of j lie on 8 bytes for every i
+  float pz[2][2 * TC + 4];
+  float dec;         // lam^n
+  float pad[3];
 };
 
-constexpr int GROUP = 256;             // threads on the state, and as many on the outputs
+constexpr int GROUP = 256;             // threads on the state, on V', on the outputs
 constexpr int GW = GROUP / 32;
-constexpr int THREADS = 2 * GROUP + 128;  // and a warp each for the MMAs, the loads, the stores
+constexpr int THREADS = 3 * GROUP + 128;  // and a warp each for the MMAs, the loads, the stores
 constexpr int STAGES = 3;
 constexpr int STAGE = 6 * TILE;        // K, Q (columns 0-63), K, Q (64-127), V, V
 constexpr int PT = STAGES * STAGE;     // P
@@ -75,29 +77,39 @@ constexpr uint32_t T_S = 0;     // S, bf16
 constexpr uint32_t T_X = 64;    // V'^T K
 constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_O = 256;   // V^T P^T
-constexpr uint32_t T_V = 320;   // V' in three terms of 32 columns
-constexpr uint32_t T_P = 416;   // Q K^T: row i in lane 32 (i / 16) + i % 16
+constexpr uint32_t T_V = 320;   // V' in four terms of 32 columns
+constexpr uint32_t T_P = 448;   // Q K^T: row i in lane 32 (i / 16) + i % 16
 
-// Waits of a kernel's roles, few instructions each (their loops have to stay
-// in the instruction cache): a try may sleep up to a microsecond, and 2^22
-// tries end the wait.  A role that ran out of patience goes on without waiting
-// (and without issuing copies or MMAs), passing every barrier, so that no
-// other role is left behind.
+// Waits of a kernel's roles, few instructions each: a try may sleep up to a
+// microsecond, and 2^22 tries end the wait.  A role that ran out of patience
+// goes on without waiting (and without issuing copies or MMAs), passing every
+// barrier, so that no other role is left behind.
 struct LinWait {
-  bool ok = true;
-  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
-    const uint32_t a = smem_u32(bar);
-    uint32_t done = ok ? 0u : 1u;
-#pragma unroll 1
-    for (uint32_t i = 0; !done; ++i) {
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(done) : "r"(a), "r"(parity) : "memory");
-      if (!done && i == 1u << 22) {
-        ok = false;
-        done = 1;
-      }
+  uint32_t tries = 1u << 22;  // 0 once a wait ran out
+  __device__ __forceinline__ bool ok() const { return tries != 0; }
+  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 i;\n\t"
+        "mov.b32 i, 0;\n"
+        "LIN_WAIT_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "@p bra LIN_DONE_%=;\n\t"
+        "add.u32 i, i, 1;\n\t"
+        "setp.lt.u32 q, i, %0;\n\t"
+        "@q bra LIN_WAIT_%=;\n\t"
+        "mov.b32 %0, 0;\n"
+        "LIN_DONE_%=:\n\t}"
+        : "+r"(tries) : "r"(bar), "r"(parity) : "memory");
+  }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) { (*this)(smem_u32(bar), parity); }
+};
+// The stage that a step's tiles are in, and its turn's parity
+struct LinStage {
+  uint32_t i = 0, par = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == 3) {
+      i = 0;
+      par ^= 1;
     }
   }
 };
@@ -127,25 +139,46 @@ struct LinCursor : LinInfo {
   }
 };
 
-// One warp: a step's factors
+// One warp: a step's factors.  Those of tokens stay in their slot while the
+// head and the chunk's length do; the state's decay is made anew.
 __device__ __forceinline__ void lin_factors(const LinArgs& a, const LinInfo& t, LinVec& v, int lane) {
   const bool rev = t.flags & F_REV;
-  const float raw = a.ld[t.h], ld = lin_ld(raw);
-#pragma unroll 1
-  for (int j = lane; j < TC; j += 32) {
+  const float ld = lin_ld(a.ld[t.h]);
+  float fk[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = 2 * lane + i;
     // in time: lam^{n-1-j} and scale lam^{j+1}; backwards: scale lam^{j+1} and lam^{n-1-j}
     const float w = a.scale * expf(ld * (float)j);
     const float up = a.scale * expf(ld * (float)(j + 1)), down = j < t.n ? expf(ld * (float)(t.n - 1 - j)) : 0.0f;
-    v.fk[j] = rev ? up : down;
+    fk[i] = rev ? up : down;
     v.fo[j] = rev ? down : up;
-    v.pz[TC + j] = rev && j ? 0.0f : w;
-    if (j) v.pz[TC - j] = rev ? w : 0.0f;
+    const float before = rev && j ? 0.0f : w, after = rev || !j ? w : 0.0f;
+    v.pz[0][TC - j] = before;
+    v.pz[1][TC - 1 - j] = before;
+    v.pz[0][TC + j] = after;
+    v.pz[1][TC - 1 + j] = after;
   }
-  if (lane == 0) {
-    const LinDecay d = lin_decay(raw, t.n);
-    v.near = d.near;
-    v.off = d.off;
+  // f = f1 + f2 + f3 to f32's last bit
+#pragma unroll
+  for (int m = 0; m < 3; ++m) {
+    const __nv_bfloat162 f = __floats2bfloat162_rn(fk[0], fk[1]);
+    v.fk[m][lane] = *reinterpret_cast<const uint32_t*>(&f);
+    fk[0] -= __low2float(f);
+    fk[1] -= __high2float(f);
   }
+}
+// The decay of a chunk of n tokens, rounded to f32 now up and now down so that
+// the product over a run's chunks stays within a rounding of the true one (`acc`
+// carries what is owed, in last places)
+__device__ __forceinline__ float lin_chunk_decay(float ld, int n, float& acc) {
+  const LinDecay d = lin_decay(ld, n);
+  if (d.near != 1.0f) return d.near;  // above a half: 1 + off
+  const float near = 1.0f + d.off, ulp = near < 1.0f ? 0x1p-24f : 0x1p-23f;
+  acc += (d.off - (near - 1.0f)) / ulp;
+  const float up = acc > 0.5f ? 1.0f : acc < -0.5f ? -1.0f : 0.0f;
+  acc -= up;
+  return near + up * ulp;
 }
 
 // Tensor memory in the layout of matrix fragments: 16 lanes x 8 columns per
@@ -183,16 +216,8 @@ __device__ __forceinline__ uint32_t pack2(float2 x) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// x = hi + mid + lo, each a pair of bf16: f32's 24 bits cut into three
-__device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-  const uint32_t a0 = __float_as_uint(x.x), a1 = __float_as_uint(x.y);
-  hi = __byte_perm(a0, a1, 0x7632);
-  const float2 r = __ffma2_rn(make_float2(__uint_as_float(a0 & 0xFFFF0000u), __uint_as_float(a1 & 0xFFFF0000u)), f2b(-1.0f), x);
-  const uint32_t b0 = __float_as_uint(r.x), b1 = __float_as_uint(r.y);
-  mid = __byte_perm(b0, b1, 0x7632);
-  const float2 q = __ffma2_rn(make_float2(__uint_as_float(b0 & 0xFFFF0000u), __uint_as_float(b1 & 0xFFFF0000u)), f2b(-1.0f), r);
-  lo = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
-}
+__device__ __forceinline__ __nv_bfloat162 as_bf2(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
 }  // namespace
 
@@ -209,8 +234,8 @@ __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, ui
 // registers: X needs no state, so the products of a chunk run under the
 // register work of the ones around it.
 //
-// V' enters as three bf16 terms, its 24 bits cut in three, so states are f32
-// sums of exact products.  S and P enter the outputs' products as one: each
+// V' enters as four bf16 terms that hold the product with f32's factor, so states are f32
+// sums of f32-grade products.  S and P enter the outputs' products as one: each
 // rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; both come
 // to 2.3e-3 at most, their shares of the output being 1 together).
 //
@@ -220,9 +245,8 @@ __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, ui
 // is not finite (in K, Q, V', S) reaches exactly the rows and columns that it
 // reaches in the recurrence.
 //
-// Roles: warps 0-7 the state (V', S^T), warps 8-15 the outputs (P, O^T), warp
-// 16 issues the MMAs, warp 17 the loads (and makes the factors), warp 18 the
-// stores.
+// Roles: warps 0-7 the state, 8-15 V', 16-23 the outputs (P, O^T), warp 24
+// issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
 __global__ void __launch_bounds__(THREADS, 1)
 m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps) {
   extern __shared__ unsigned char raw[];
@@ -259,18 +283,20 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   };
   const uint32_t quad = (uint32_t)(warp & 3), tq = tm + (quad << 21);  // this warp's 32 lanes
 
-  // registers go to the warps that hold the state: 144 x 256 + 72 x 256 + 48 x
-  // 128 is what the block was launched with, 96 x 640
-  if (warp >= 2 * GW) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (warp == 2 * GW + 2) {  // stores
+  // registers go to the warps that hold the state: (RA + RB + RC) x 256 + RM x
+  // 128 is what the block was launched with
+  constexpr int LAUNCHED = 65536 / THREADS / 8 * 8, RA = 88, RB = 72, RC = 72, RM = 40;
+  static_assert((RA + RB + RC) * GROUP + RM * 128 <= LAUNCHED * THREADS, "registers of the block");
+  if (warp >= 3 * GW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RM));
+    if (warp == 3 * GW + 2) {  // stores
       if (elect_one()) {
 #pragma unroll 1
         for (int n = 0; n < walk.n; ++n) {
           wait(&s.rdy_o, n & 1);  // the outputs are in place
           const LinInfo& t = s.info[n & 7];
           const LinPass& p = a.p[t.pass];
-          if (wait.ok && !p.out_f32) {
+          if (wait.ok() && !p.out_f32) {
             const int h = p.oh == 1 ? t.h : t.h / p.oh;
             tma_tile_store(&maps.m[t.pass][3], st0 + OUT, 0, h, t.tok, t.b);
             if (p.DV > 64) tma_tile_store(&maps.m[t.pass][3], st0 + OUT + TILE, 64, h, t.tok, t.b);
@@ -282,17 +308,19 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         bulk_wait_all();
       }
       __syncwarp();
-    } else if (warp == 2 * GW + 1) {  // loads and factors
+    } else if (warp == 3 * GW + 1) {  // loads and factors
       grid_dep_wait();  // what the kernels before this one leave is there
-      int issued = 0;
+      int issued = 0, run = 0;  // run: steps since the factors changed
+      float acc = 0.0f;
       LinCursor t;
+      LinStage g;
 #pragma unroll 1
-      for (int n = 0; n < walk.n; ++n) {
-        const int i = n % STAGES;
+      for (int n = 0; n < walk.n; ++n, g.next()) {
+        const uint32_t i = g.i;
         t.next(a, walk);
-        if (n >= STAGES) wait(&s.empty[i], (n / STAGES - 1) & 1);
+        if (n >= STAGES) wait(&s.empty[i], g.par ^ 1);
         if (lane == 0) {
-          if (wait.ok) {
+          if (wait.ok()) {
             const LinPass& p = a.p[t.pass];
             const CUtensorMap* m = maps.m[t.pass];
             const uint32_t st = st0 + i * STAGE;
@@ -308,28 +336,39 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           }
           s.info[n & 7] = t;
         }
-        if (wait.ok) issued = n + 1;
-        lin_factors(a, t, s.vec[n & 3], lane);
+        if (wait.ok()) issued = n + 1;
+        LinVec& v = s.vec[n & 3];
+        if (t.flags & F_FIRST) {
+          run = 0;
+          acc = 0.0f;
+        }
+        if (run < 4 || t.n < TC) {
+          lin_factors(a, t, v, lane);
+          run = t.n < TC ? -4 : run;  // (a short chunk's are made anew in every slot)
+        }
+        ++run;
+        if (lane == 0) v.dec = lin_chunk_decay(a.ld[t.h], t.n, acc);
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i]);
       }
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
-      if (!wait.ok)
+      if (!wait.ok())
 #pragma unroll 1
         for (int m = issued > STAGES ? issued - STAGES : 0; m < issued; ++m) mbar_wait(&s.full[m % STAGES], (m / STAGES) & 1);
-    } else if (warp == 2 * GW) {  // MMAs
+    } else if (warp == 3 * GW) {  // MMAs
       if (elect_one()) {
         const uint64_t pd = tc_desc(st0 + PT, 16, 1024);
+        LinStage g;
 #pragma unroll 1
-        for (int n = 0; n < walk.n; ++n) {
-          const uint32_t st = st0 + (n % STAGES) * STAGE, par = n & 1;
+        for (int n = 0; n < walk.n; ++n, g.next()) {
+          const uint32_t st = st0 + g.i * STAGE, par = n & 1;
           // (an address in a descriptor counts 16 bytes)
           const uint64_t kd = tc_desc(st, 16, 1024), qd = tc_desc(st + TILE, 16, 1024);  // K, Q by rows
           const uint64_t kn = tc_desc(st, 2 * TILE, 1024), vn = tc_desc(st + 4 * TILE, TILE, 1024);  // K, V by columns
-          wait(&s.full[n % STAGES], (n / STAGES) & 1);
+          wait(&s.full[g.i], g.par);
           if (n > 0) wait(&s.rdy_p, par ^ 1);      // the last chunk's P is read
-          if (wait.ok) {                           // Q K^T
+          if (wait.ok()) {                           // Q K^T
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -340,10 +379,10 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           }
           wait(&s.rdy_v, par);                     // V' is in tensor memory
           if (n > 0) wait(&s.rdy_x, par ^ 1);      // the last X is read
-          if (wait.ok) {
+          if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc_mma_ts(tm + T_X, tm + T_V + p * 32 + ks * 8, kn + (ks * 2048 >> 4), tc_idesc(128, 128, false, true), p + ks > 0);
@@ -351,7 +390,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           }
           wait(&s.rdy_s, par);                     // S is in tensor memory
           if (n > 0) wait(&s.rdy_q, par ^ 1);      // the last outputs are read
-          if (wait.ok) {
+          if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
@@ -359,93 +398,42 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             tc_commit(&s.mbq);
           }
           wait(&s.rdy_p, par);                     // P is in shared memory
-          if (wait.ok) {
+          if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               tc_mma_ss(tm + T_O, vn + (ks * 2048 >> 4), pd + (ks * 32 >> 4), tc_idesc(128, 64, true, false), ks > 0);
             tc_commit(&s.mbo);
-            tc_commit(&s.empty[n % STAGES]);
+            tc_commit(&s.empty[g.i]);
           }
         }
       }
       __syncwarp();
     }
   } else if (warp < GW) {  // the state
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
-    const int hf = warp >> 2, row = quad * 32 + lane;  // half of the keys, and of the tokens; the row: a value
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RA));
+    const int hf = warp >> 2, row = quad * 32 + lane;  // half of the keys; the row: a value
     float2 S[32];  // S^T[row][64 hf + k]
-    uint32_t hi[2][8], mid[2][8], lo[2][8];  // V': [half of the lanes][fragment]
-    const uint32_t vl = st0 + 4 * TILE + (quad >> 1) * TILE;
 
     grid_dep_wait();  // the segments' states, too
+    int flags = 0;
+    LinStage g;
 #pragma unroll 1
-    for (int n = 0; n <= walk.n; ++n) {
-      if (n < walk.n) {
-        // V' of this step: 32 values (this warp's lanes) of 32 tokens,
-        // transposed on their way out of shared memory.  Made while the X
-        // before it runs, written as soon as that is done with the columns.
-        wait(&s.full[n % STAGES], (n / STAGES) & 1);
-        const uint32_t vt = vl + (n % STAGES) * STAGE;
-        const float* fk = &s.vec[n & 3].fk[hf * 32 + 2 * (lane & 3)];
-        float2 chk = f2b(0.0f);
-#pragma unroll
-        for (int tp = 0; tp < 2; ++tp) {  // tokens 32 hf + 16 tp ..
-          const float2 f0 = *reinterpret_cast<const float2*>(fk + tp * 16), f1 = *reinterpret_cast<const float2*>(fk + tp * 16 + 8);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // lanes 16 h ..
-            uint32_t x[4];  // (values 0-7, tokens 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-            ldmatrix4t(x, vt + sw(hf * 32 + tp * 16 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + h * 2 + ((lane >> 3) & 1)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 v = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
-              chk = __ffma2_rn(v, f2b(0.0f), chk);  // 0 unless a value is not finite
-              split3(__fmul2_rn(v, i < 2 ? f0 : f1), hi[h][tp * 4 + i], mid[h][tp * 4 + i], lo[h][tp * 4 + i]);
-            }
-          }
-        }
-        if (__any_sync(~0u, !(chk.x + chk.y == 0.0f))) {
-          const bool rev = s.info[n & 7].flags & F_REV;
-#pragma unroll 1
-          for (int tok = hf * 32; tok < hf * 32 + 32; ++tok) {
-            const uint32_t el = vt + sw(tok, (row & 63) >> 3) + (row & 7) * 2;
-            uint16_t v;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(el) : "memory");
-            if ((v & 0x7F80) == 0x7F80) {
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(el), "h"((uint16_t)0) : "memory");
-              atomicMax(&s.bad[n & 3][row], ((unsigned)(n + 1) & 0xFFFFFF) << 7 | (unsigned)(127 - (rev ? TC - 1 - tok : tok)));
-              s.any_bad[n & 3] = (unsigned)(n + 1);
-            }
-          }
-          fence_proxy_async();
-        }
-      }
-      if (n > 0) {
+    for (int n = 0; n <= walk.n; ++n, g.next()) {
+      if (n > 0) {  // S = lam^n S + X of the step before
+        const float2 dec = f2b(s.vec[(n - 1) & 3].dec);
         wait(&s.mbx, (n - 1) & 1);
         tmem_fence_after_sync();
-      }
-      if (n < walk.n) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = tq + (h << 20) + T_V + hf * 16;
-          tc_st_frag(at, hi[h]);
-          tc_st_frag(at + 32, mid[h]);
-          tc_st_frag(at + 64, lo[h]);
-        }
-        ready(&s.rdy_v);
-      }
-      if (n > 0) {  // S = lam^n S + X of the step before
-        const float2 near = f2b(s.vec[(n - 1) & 3].near), off = f2b(s.vec[(n - 1) & 3].off);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float2 x[8];
           tc_ld16(tq + T_X + hf * 64 + q * 16, x);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(near, S[q * 8 + k], __ffma2_rn(off, S[q * 8 + k], x[k]));
+          for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
         }
         ready(&s.rdy_x);
-        const LinInfo t = s.info[(n - 1) & 7];
-        if (t.flags & F_LAST) {  // where the run leaves its state
+        if (flags & F_LAST) {  // where the run leaves its state
+          const LinInfo t = s.info[(n - 1) & 7];
           const LinPass& p = a.p[t.pass];
           if (t.flags & F_GIVE) {
             float* dst = a.seg_start + ((size_t)t.item * LIN_DMAX + hf * 64) * LIN_DMAX + row;
@@ -468,32 +456,32 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
               }
           }
         }
+        if (n == walk.n) break;
       }
-      if (n == walk.n) break;
-      {
+      wait(&s.full[g.i], g.par);
+      flags = s.info[n & 7].flags;
+      if (flags & F_FIRST) {  // the state a run starts from
         const LinInfo t = s.info[n & 7];
-        if (t.flags & F_FIRST) {  // the state a run starts from
-          const LinPass& p = a.p[t.pass];
-          if (t.flags & F_TAKE && wait.ok) wait.ok = flag_wait(a.flags + t.item);
-          if (t.w > 0 || a.segs > 1) {
-            const float* src = a.seg_start + (((size_t)t.item * a.segs + seg) * LIN_DMAX + hf * 64) * LIN_DMAX + row;
+        const LinPass& p = a.p[t.pass];
+        if (flags & F_TAKE && wait.ok()) wait.tries = flag_wait(a.flags + t.item) ? wait.tries : 0;
+        if (t.w > 0 || a.segs > 1) {
+          const float* src = a.seg_start + (((size_t)t.item * a.segs + seg) * LIN_DMAX + hf * 64) * LIN_DMAX + row;
 #pragma unroll
-            for (int k = 0; k < 64; ++k) (k & 1 ? S[k >> 1].y : S[k >> 1].x) = __ldcg(src + k * LIN_DMAX);
-          } else {
-            const int live = p.s_in && row < p.DV ? p.DK - hf * 64 : 0;
-            const size_t head = ((size_t)t.b * a.Hv + t.h) * p.DK * p.DV;
-            const float* src = p.s_in + head + (p.st ? (size_t)row * p.DK + hf * 64 : (size_t)hf * 64 * p.DV + row);
-            const int step = p.st ? 1 : p.DV;
+          for (int k = 0; k < 64; ++k) (k & 1 ? S[k >> 1].y : S[k >> 1].x) = __ldcg(src + k * LIN_DMAX);
+        } else {
+          const int live = p.s_in && row < p.DV ? p.DK - hf * 64 : 0;
+          const size_t head = ((size_t)t.b * a.Hv + t.h) * p.DK * p.DV;
+          const float* src = p.s_in + head + (p.st ? (size_t)row * p.DK + hf * 64 : (size_t)hf * 64 * p.DV + row);
+          const int step = p.st ? 1 : p.DV;
 #pragma unroll
-            for (int k = 0; k < 64; k += 8) {
+          for (int k = 0; k < 64; k += 8) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) (j & 1 ? S[(k + j) >> 1].y : S[(k + j) >> 1].x) = 0.0f;
-              if (k < live) {
+            for (int j = 0; j < 8; ++j) (j & 1 ? S[(k + j) >> 1].y : S[(k + j) >> 1].x) = 0.0f;
+            if (k < live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  (j & 1 ? S[(k + j) >> 1].y : S[(k + j) >> 1].x) = __ldcg(src);
-                  src += step;
-                }
+              for (int j = 0; j < 8; ++j) {
+                (j & 1 ? S[(k + j) >> 1].y : S[(k + j) >> 1].x) = __ldcg(src);
+                src += step;
               }
             }
           }
@@ -512,10 +500,82 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       }
       ready(&s.rdy_s);
     }
+  } else if (warp < 2 * GW) {  // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RC));
+    const int hf = (warp >> 2) & 1, row = quad * 32 + lane;  // half of the tokens
+    const uint32_t vl = st0 + 4 * TILE + (quad >> 1) * TILE;
+    const uint32_t el = sw(hf * 32 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
+    LinStage g;
+#pragma unroll 1
+    for (int n = 0; n < walk.n; ++n, g.next()) {
+      // v f exactly, as terms: hi = v f1 rounded, its rest v f1 - hi (eight bits
+      // at most), v f2 rounded, and its rest with v f3.  Five packed bf16
+      // instructions for two values.  Made while the X before runs; written as
+      // soon as that is done with the columns.
+      uint32_t x[2][8], y[4][8];  // [half of the lanes][fragment], [term][fragment]
+      wait(&s.full[g.i], g.par);
+      const uint32_t vt = vl + g.i * STAGE;
+      const LinVec& vec = s.vec[n & 3];
+      __nv_bfloat162 chk = as_bf2(0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int tp = 0; tp < 2; ++tp) {  // tokens 32 hf + 16 tp ..
+          // (values 0-7, tokens 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+          uint32_t (&z)[4] = reinterpret_cast<uint32_t(&)[4]>(x[h][tp * 4]);
+          ldmatrix4t(z, vt + (el ^ (h * 32)) + tp * 2048);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) chk = __hfma2(as_bf2(z[i]), as_bf2(0), chk);  // 0 unless a value is not finite
+        }
+      auto terms = [&](int h) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const int at = hf * 16 + tb * 4 + (lane & 3);
+          const __nv_bfloat162 f1 = as_bf2(vec.fk[0][at]), f2 = as_bf2(vec.fk[1][at]), f3 = as_bf2(vec.fk[2][at]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1), t = __hmul2_rn(v, f2);
+            y[0][tb * 2 + i] = as_u32(hi);
+            y[1][tb * 2 + i] = as_u32(__hfma2(v, f1, __hneg2(hi)));
+            y[2][tb * 2 + i] = as_u32(t);
+            y[3][tb * 2 + i] = as_u32(__hfma2(v, f3, __hfma2(v, f2, __hneg2(t))));
+          }
+        }
+      };
+      terms(0);
+      if (__any_sync(~0u, (as_u32(chk) & 0x7FFF7FFFu) != 0)) {
+        const bool rev = s.info[n & 7].flags & F_REV;
+#pragma unroll 1
+        for (int tok = hf * 32; tok < hf * 32 + 32; ++tok) {
+          const uint32_t at = vt + sw(tok, (row & 63) >> 3) + (row & 7) * 2;
+          uint16_t v;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+          if ((v & 0x7F80) == 0x7F80) {
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)0) : "memory");
+            atomicMax(&s.bad[n & 3][row], ((unsigned)(n + 1) & 0xFFFFFF) << 7 | (unsigned)(127 - (rev ? TC - 1 - tok : tok)));
+            s.any_bad[n & 3] = (unsigned)(n + 1);
+          }
+        }
+        fence_proxy_async();
+      }
+      if (n > 0) {
+        wait(&s.mbx, (n - 1) & 1);
+        tmem_fence_after_sync();
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h) terms(1);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + T_V + m * 32 + hf * 16, y[m]);
+      }
+      ready(&s.rdy_v);
+    }
   } else {  // the outputs
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RB));
     const int hf = (warp >> 2) & 1;  // half of the tokens (of P: of its columns)
     const int i0 = quad * 16, j0 = hf * 32;
+    const int pz_at = TC + j0 + 2 * (lane & 3) - i0 - (lane >> 2) - ((lane >> 2) & 1);  // (even)
+    const uint32_t op = st0 + OUT + (quad >> 1) * TILE + sw(j0 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
 #pragma unroll 1
     for (int n = 0; n <= walk.n; ++n) {
       // O of the step before: values 32 quad .. of tokens 32 hf ..
@@ -526,8 +586,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         const float* fo = &s.vec[m & 3].fo[j0 + 2 * (lane & 3)];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) f[tb] = *reinterpret_cast<const float2*>(fo + tb * 8);
-        wait(&s.mbq, m & 1);
-        wait(&s.mbo, m & 1);
+        wait(&s.mbo, m & 1);  // (and S Q^T, which was issued before)
         tmem_fence_after_sync();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -558,23 +617,29 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         ready(&s.rdy_q);
       }
       if (n < walk.n) {  // P: rows 16 quad .., columns 32 hf ..
-        wait(&s.full[n % STAGES], (n / STAGES) & 1);
-        const bool rev = s.info[n & 7].flags & F_REV;
         float2 x[8];  // [column block of 8][row + 8]
-        wait(&s.mbp, n & 1);
+        wait(&s.mbp, n & 1);  // (and with it the factors, which the products were issued behind)
+        const bool rev = s.info[n & 7].flags & F_REV;
         tmem_fence_after_sync();
         if (rev ? j0 + 31 >= i0 : j0 <= i0 + 15) {
           tc_ld_frag(tq + T_P + j0, x);
+          const float* pz = s.vec[n & 3].pz[(lane >> 2) & 1] + pz_at;
           tc_wait_frag(x);
-          const int d = i0 + (lane >> 2) - j0 - 2 * (lane & 3);  // i - j of the first value
-          const float* pz = &s.vec[n & 3].pz[TC + d];
-          const int ds = rev ? -d : d, s1 = rev ? -1 : 1;        // tokens that j lies before i, in the pass's order
+          float2 chk = f2b(0.0f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const int e = 8 * (c & 1) - 8 * (c >> 1);
-            const float f0 = pz[e], f1 = pz[e - 1];
-            x[c] = make_float2(ds >= -s1 * e ? x[c].x * f0 : 0.0f, ds >= s1 * (1 - e) ? x[c].y * f1 : 0.0f);
+            chk = __ffma2_rn(x[c], f2b(0.0f), chk);
+            x[c] = __fmul2_rn(x[c], *reinterpret_cast<const float2*>(pz + 8 * (c >> 1) - 8 * (c & 1)));
           }
+          if (!(chk.x + chk.y == 0.0f)) {  // what is not finite among pairs that do not count
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int d = i0 + (lane >> 2) + 8 * (c & 1) - j0 - 2 * (lane & 3) - 8 * (c >> 1);  // i - j
+              if (rev ? d > 0 : d < 0) x[c].x = 0.0f;
+              if (rev ? d > 1 : d < 1) x[c].y = 0.0f;
+            }
+          }
+          __syncwarp();
         } else {
 #pragma unroll
           for (int c = 0; c < 8; ++c) x[c] = f2b(0.0f);
@@ -605,8 +670,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int tp = 0; tp < 2; ++tp)
-              stmatrix4<true>(st0 + OUT + (quad >> 1) * TILE + sw(j0 + tp * 16 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + h * 2 + ((lane >> 3) & 1)),
-                              pack2(o[h][tp * 4]), pack2(o[h][tp * 4 + 1]), pack2(o[h][tp * 4 + 2]), pack2(o[h][tp * 4 + 3]));
+              stmatrix4<true>((op ^ (h * 32)) + tp * 2048, pack2(o[h][tp * 4]), pack2(o[h][tp * 4 + 1]), pack2(o[h][tp * 4 + 2]), pack2(o[h][tp * 4 + 3]));
           fence_proxy_async();
         }
         __syncwarp();
@@ -614,7 +678,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       }
     }
   }
-  if (!wait.ok) report_timeout(&g_lin_status, a.status);
+  if (!wait.ok()) report_timeout(&g_lin_status, a.status);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
