@@ -47,6 +47,27 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
   return M3_OK;
 }
 
+// Time segments of the tensor-core kernels for few items.  With S segments the
+// ends of the first S - 1 are found first, chained, and then all run.
+void lin_segments(int64_t items, int nc, int* segs, int* seg_chunks) {
+  constexpr int64_t SMS = 152;
+  double best = 0.0;
+  *segs = 1;
+  *seg_chunks = nc < 1 ? 1 : nc;
+  for (int want = 1; want <= 152 && want * 4 <= (nc > 4 ? nc : 4); ++want) {
+    const int m = (nc + want - 1) / want;
+    if (m < 1) break;
+    const int S = (nc + m - 1) / m;
+    const double fin = (double)((items * S + SMS - 1) / SMS) * (m + 3.0);
+    const double agg = S > 1 ? (double)((items * (S - 1) + SMS - 1) / SMS) * (m + 3.0) * 0.7 + 4.0 + 0.1 * S : 0.0;
+    if (want == 1 || fin + agg < best - 1e-9) {
+      best = fin + agg;
+      *segs = S;
+      *seg_chunks = m;
+    }
+  }
+}
+
 m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
   const m3_status st = lin_validate(d, act);
   if (st != M3_OK) return st;
@@ -69,8 +90,12 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     w.segs = 1;
     w.seg_chunks = p->nc;
     w.stream = p->tc && items > 152;
-    w.o_start = take(p->tc && w.stream ? (size_t)items * LIN_DMAX * LIN_DMAX * 4 : 0);
-    w.o_end = off;
+    if (p->tc && !w.stream) {
+      lin_segments(items, p->nc, &w.segs, &w.seg_chunks);
+    }
+    const size_t slots = (size_t)items * w.segs * LIN_DMAX * LIN_DMAX * 4;
+    w.o_start = take(w.stream || w.segs > 1 ? slots : 0);
+    w.o_end = take(w.segs > 1 ? slots : 0);
     w.o_flags = take(w.stream ? (size_t)items * 4 : 0);
     if (i == 0) p->fwd_ws_bytes = off;
   }
@@ -82,8 +107,8 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
   p->o_dstate = take((size_t)p->B * p->Hv * p->DK * p->DV * 4);
   p->ws_bytes = off;
   const bool empty = p->B == 0 || p->T == 0;
-  p->fwd_launches = empty ? 0 : 1;
-  p->bwd_launches = empty ? 0 : p->share > 1 ? 2 : 1;
+  p->fwd_launches = empty ? 0 : p->walk[0].segs > 1 ? 3 : 1;
+  p->bwd_launches = empty ? 0 : (p->walk[1].segs > 1 ? 3 : 1) + (p->share > 1 ? 1 : 0);
   return M3_OK;
 }
 

@@ -55,22 +55,26 @@ constexpr int GW = GROUP / 32;
 constexpr int THREADS = 3 * GROUP + 128;  // and a warp each for the MMAs, the loads, the stores
 constexpr int STAGES = 3;
 constexpr int STAGE = 6 * TILE;        // K, Q (columns 0-63), K, Q (64-127), V, V
+constexpr int AGG_STAGES = 5;
+constexpr int AGG_STAGE = 4 * TILE;    // K, K, V, V
 constexpr int PT = STAGES * STAGE;     // P
 constexpr int OUT = PT + TILE;         // a chunk's outputs, for the tile store
 constexpr int SMALL = OUT + 2 * TILE;
 
 struct Smem {  // at SMALL
-  LinVec vec[4];
+  LinVec vec[8];
   unsigned bad[4][128];  // per row: (step + 1) << 7 | 127 - (first token whose value is not finite)
   unsigned any_bad[4];   // step + 1
   LinInfo info[8];       // (a step's stores come up to two steps later)
-  uint64_t full[STAGES], empty[STAGES];
-  uint64_t mbp, mbx, mbq, mbo, o_free;
-  uint64_t rdy_v, rdy_x, rdy_s, rdy_q, rdy_p, rdy_o;  // one arrival per warp of a group
+  uint64_t full[AGG_STAGES], empty[AGG_STAGES];
+  uint64_t mbx[2];           // (AGG: by step, for two X in flight)
+  uint64_t mbp, mbq, mbo, o_free;
+  uint64_t rdy_v[2], rdy_x[2];
+  uint64_t rdy_s, rdy_q, rdy_p, rdy_o;  // one arrival per warp of a group
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory of one block");
+static_assert(SMEM_BYTES <= 232448 && AGG_STAGES * AGG_STAGE <= SMALL, "shared memory of one block");
 
 // tensor-memory columns
 constexpr uint32_t T_S = 0;     // S, bf16
@@ -79,6 +83,8 @@ constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_O = 256;   // V^T P^T
 constexpr uint32_t T_V = 320;   // V' in four terms of 32 columns
 constexpr uint32_t T_P = 448;   // Q K^T: row i in lane 32 (i / 16) + i % 16
+// and where only the states are wanted: two of each, by step
+constexpr uint32_t A_X = 0, A_V = 256;
 
 // Waits of a kernel's roles, few instructions each: a try may sleep up to a
 // microsecond, and 2^22 tries end the wait.  A role that ran out of patience
@@ -104,10 +110,10 @@ struct LinWait {
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) { (*this)(smem_u32(bar), parity); }
 };
 // The stage that a step's tiles are in, and its turn's parity
-struct LinStage {
+template <uint32_t N> struct LinStage {
   uint32_t i = 0, par = 0;
   __device__ __forceinline__ void next() {
-    if (++i == 3) {
+    if (++i == N) {
       i = 0;
       par ^= 1;
     }
@@ -124,11 +130,10 @@ struct LinCursor : LinInfo {
       flags &= ~F_FIRST;
     } else {
       const TcStep t = walk.at(step);
-      item = t.bh;
-      const int bh = item / a.np;
-      pass = item - bh * a.np;
-      b = bh / a.Hv;
-      h = bh - b * a.Hv;
+      pass = (int)(blockIdx.x % (unsigned)a.np);
+      item = t.bh * a.np + pass;
+      b = t.bh / a.Hv;
+      h = t.bh - b * a.Hv;
       w = t.c;
       left = step < walk.len_a ? walk.len_a : walk.nc - t.c;
       flags = (a.p[pass].rev ? F_REV : 0) | (t.take ? F_TAKE : 0) | (t.give ? F_GIVE : 0) | F_FIRST;
@@ -247,6 +252,10 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 //
 // Roles: warps 0-7 the state, 8-15 V', 16-23 the outputs (P, O^T), warp 24
 // issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
+//
+// AGG: only the states, each time segment's end from a zero start (into
+// seg_end); no queries, no outputs.
+template <bool AGG>
 __global__ void __launch_bounds__(THREADS, 1)
 m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps) {
   extern __shared__ unsigned char raw[];
@@ -255,16 +264,26 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // uniform for the compiler too
   const int seg = blockIdx.y;
-  const TcWalk walk(a.stream, (int64_t)a.np * a.B * a.Hv, a.nc, blockIdx.x, gridDim.x, seg, a.seg_chunks);
+  // neighbouring blocks take the passes of one head: those of dk and dv go
+  // through the same chunks at the same time, and share them in L2
+  const unsigned np = (unsigned)a.np;
+  const TcWalk walk(a.stream, (int64_t)a.B * a.Hv, a.nc, blockIdx.x / np, gridDim.x / np, seg, a.seg_chunks);
   const uint32_t st0 = smem_u32(base);
+  constexpr int NST = AGG ? AGG_STAGES : STAGES, STB = AGG ? AGG_STAGE : STAGE;
+  // X, V' and their barriers: one of each, or two in turns
+  auto two = [](int n) { return AGG ? n & 1 : 0; };
+  auto two_par = [](int n) { return (uint32_t)(AGG ? n >> 1 : n) & 1u; };
+  auto at_x = [&](int n) { return AGG ? A_X + (n & 1) * 128 : T_X; };
+  auto at_v = [&](int n) { return AGG ? A_V + (n & 1) * 128 : T_V; };
+  constexpr int BACK = AGG ? 2 : 1;  // steps after which X and V' are used again
 
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < NST; ++i) {
       mbar_init(&s.full[i], 2);  // the copies, the factors
       mbar_init(&s.empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbp, &s.mbx, &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy_v, &s.rdy_x, &s.rdy_s, &s.rdy_q, &s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
+    for (uint64_t* r : {&s.mbp, &s.mbx[0], &s.mbx[1], &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_v[0], &s.rdy_v[1], &s.rdy_x[0], &s.rdy_x[1], &s.rdy_s, &s.rdy_q, &s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
     mbar_init_fence();
   }
   if (tid < 512) reinterpret_cast<unsigned*>(s.bad)[tid] = 0;
@@ -281,6 +300,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  if (AGG) grid_dep_trigger();
   const uint32_t quad = (uint32_t)(warp & 3), tq = tm + (quad << 21);  // this warp's 32 lanes
 
   // registers go to the warps that hold the state: (RA + RB + RC) x 256 + RM x
@@ -290,7 +310,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   if (warp >= 3 * GW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RM));
     if (warp == 3 * GW + 2) {  // stores
-      if (elect_one()) {
+      if (!AGG && elect_one()) {
 #pragma unroll 1
         for (int n = 0; n < walk.n; ++n) {
           wait(&s.rdy_o, n & 1);  // the outputs are in place
@@ -313,38 +333,38 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       int issued = 0, run = 0;  // run: steps since the factors changed
       float acc = 0.0f;
       LinCursor t;
-      LinStage g;
+      LinStage<NST> g;
 #pragma unroll 1
       for (int n = 0; n < walk.n; ++n, g.next()) {
         const uint32_t i = g.i;
         t.next(a, walk);
-        if (n >= STAGES) wait(&s.empty[i], g.par ^ 1);
+        if (n >= NST) wait(&s.empty[i], g.par ^ 1);
         if (lane == 0) {
           if (wait.ok()) {
             const LinPass& p = a.p[t.pass];
             const CUtensorMap* m = maps.m[t.pass];
-            const uint32_t st = st0 + i * STAGE;
+            const uint32_t st = st0 + i * STB;
             const int hk = p.kh == 1 ? t.h : t.h / p.kh, hv = p.vh == 1 ? t.h : t.h / p.vh, hq = p.qh == 1 ? t.h : t.h / p.qh;
             uint64_t* bar = &s.full[i];
-            mbar_expect_tx(bar, STAGE);
+            mbar_expect_tx(bar, AGG ? 4 * TILE : STAGE);
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
-              tma_tile(st + blk * 2 * TILE, &m[1], blk * 64, hk, t.tok, t.b, bar);
-              tma_tile(st + (4 + blk) * TILE, &m[2], blk * 64, hv, t.tok, t.b, bar);
-              tma_tile(st + blk * 2 * TILE + TILE, &m[0], blk * 64, hq, t.tok, t.b, bar);
+              tma_tile(st + blk * (AGG ? 1 : 2) * TILE, &m[1], blk * 64, hk, t.tok, t.b, bar);
+              tma_tile(st + ((AGG ? 2 : 4) + blk) * TILE, &m[2], blk * 64, hv, t.tok, t.b, bar);
+              if (!AGG) tma_tile(st + blk * 2 * TILE + TILE, &m[0], blk * 64, hq, t.tok, t.b, bar);
             }
           }
           s.info[n & 7] = t;
         }
         if (wait.ok()) issued = n + 1;
-        LinVec& v = s.vec[n & 3];
+        LinVec& v = s.vec[n & 7];
         if (t.flags & F_FIRST) {
           run = 0;
           acc = 0.0f;
         }
-        if (run < 4 || t.n < TC) {
+        if (run < 8 || t.n < TC) {
           lin_factors(a, t, v, lane);
-          run = t.n < TC ? -4 : run;  // (a short chunk's are made anew in every slot)
+          run = t.n < TC ? -8 : run;  // (a short chunk's are made anew in every slot)
         }
         ++run;
         if (lane == 0) v.dec = lin_chunk_decay(a.ld[t.h], t.n, acc);
@@ -355,20 +375,20 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       // shared memory is given up (bounded)
       if (!wait.ok())
 #pragma unroll 1
-        for (int m = issued > STAGES ? issued - STAGES : 0; m < issued; ++m) mbar_wait(&s.full[m % STAGES], (m / STAGES) & 1);
+        for (int m = issued > NST ? issued - NST : 0; m < issued; ++m) mbar_wait(&s.full[m % NST], (m / NST) & 1);
     } else if (warp == 3 * GW) {  // MMAs
       if (elect_one()) {
         const uint64_t pd = tc_desc(st0 + PT, 16, 1024);
-        LinStage g;
+        LinStage<NST> g;
 #pragma unroll 1
         for (int n = 0; n < walk.n; ++n, g.next()) {
-          const uint32_t st = st0 + g.i * STAGE, par = n & 1;
+          const uint32_t st = st0 + g.i * STB, par = n & 1;
           // (an address in a descriptor counts 16 bytes)
           const uint64_t kd = tc_desc(st, 16, 1024), qd = tc_desc(st + TILE, 16, 1024);  // K, Q by rows
-          const uint64_t kn = tc_desc(st, 2 * TILE, 1024), vn = tc_desc(st + 4 * TILE, TILE, 1024);  // K, V by columns
+          const uint64_t kn = tc_desc(st, (AGG ? 1 : 2) * TILE, 1024), vn = tc_desc(st + 4 * TILE, TILE, 1024);  // K, V by columns
           wait(&s.full[g.i], g.par);
-          if (n > 0) wait(&s.rdy_p, par ^ 1);      // the last chunk's P is read
-          if (wait.ok()) {                           // Q K^T
+          if (!AGG && n > 0) wait(&s.rdy_p, par ^ 1);  // the last chunk's P is read
+          if (!AGG && wait.ok()) {                     // Q K^T
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -377,17 +397,19 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             }
             tc_commit(&s.mbp);
           }
-          wait(&s.rdy_v, par);                     // V' is in tensor memory
-          if (n > 0) wait(&s.rdy_x, par ^ 1);      // the last X is read
+          wait(&s.rdy_v[two(n)], two_par(n));      // V' is in tensor memory
+          if (n >= BACK) wait(&s.rdy_x[two(n)], two_par(n) ^ 1);  // the last X is read
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                tc_mma_ts(tm + T_X, tm + T_V + p * 32 + ks * 8, kn + (ks * 2048 >> 4), tc_idesc(128, 128, false, true), p + ks > 0);
-            tc_commit(&s.mbx);
+                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4), tc_idesc(128, 128, false, true), p + ks > 0);
+            tc_commit(&s.mbx[two(n)]);
+            if (AGG) tc_commit(&s.empty[g.i]);
           }
+          if (AGG) continue;
           wait(&s.rdy_s, par);                     // S is in tensor memory
           if (n > 0) wait(&s.rdy_q, par ^ 1);      // the last outputs are read
           if (wait.ok()) {
@@ -417,25 +439,29 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 
     grid_dep_wait();  // the segments' states, too
     int flags = 0;
-    LinStage g;
+    LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n <= walk.n; ++n, g.next()) {
       if (n > 0) {  // S = lam^n S + X of the step before
-        const float2 dec = f2b(s.vec[(n - 1) & 3].dec);
-        wait(&s.mbx, (n - 1) & 1);
+        const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
+        wait(&s.mbx[two(n - 1)], two_par(n - 1));
         tmem_fence_after_sync();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float2 x[8];
-          tc_ld16(tq + T_X + hf * 64 + q * 16, x);
+          tc_ld16(tq + at_x(n - 1) + hf * 64 + q * 16, x);
 #pragma unroll
           for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
         }
-        ready(&s.rdy_x);
+        ready(&s.rdy_x[two(n - 1)]);
         if (flags & F_LAST) {  // where the run leaves its state
           const LinInfo t = s.info[(n - 1) & 7];
           const LinPass& p = a.p[t.pass];
-          if (t.flags & F_GIVE) {
+          if (AGG) {
+            float* dst = a.seg_end + (((size_t)t.item * a.segs + seg) * LIN_DMAX + hf * 64) * LIN_DMAX + row;
+#pragma unroll
+            for (int k = 0; k < 64; ++k) dst[k * LIN_DMAX] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
+          } else if (t.flags & F_GIVE) {
             float* dst = a.seg_start + ((size_t)t.item * LIN_DMAX + hf * 64) * LIN_DMAX + row;
 #pragma unroll
             for (int k = 0; k < 64; ++k) dst[k * LIN_DMAX] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
@@ -460,6 +486,13 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       }
       wait(&s.full[g.i], g.par);
       flags = s.info[n & 7].flags;
+      if (AGG) {
+        if (n == 0) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) S[k] = f2b(0.0f);
+        }
+        continue;
+      }
       if (flags & F_FIRST) {  // the state a run starts from
         const LinInfo t = s.info[n & 7];
         const LinPass& p = a.p[t.pass];
@@ -503,9 +536,9 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   } else if (warp < 2 * GW) {  // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RC));
     const int hf = (warp >> 2) & 1, row = quad * 32 + lane;  // half of the tokens
-    const uint32_t vl = st0 + 4 * TILE + (quad >> 1) * TILE;
+    const uint32_t vl = st0 + (AGG ? 2 : 4) * TILE + (quad >> 1) * TILE;
     const uint32_t el = sw(hf * 32 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
-    LinStage g;
+    LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n < walk.n; ++n, g.next()) {
       // v f exactly, as terms: hi = v f1 rounded, its rest v f1 - hi (eight bits
@@ -514,8 +547,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       // soon as that is done with the columns.
       uint32_t x[2][8], y[4][8];  // [half of the lanes][fragment], [term][fragment]
       wait(&s.full[g.i], g.par);
-      const uint32_t vt = vl + g.i * STAGE;
-      const LinVec& vec = s.vec[n & 3];
+      const uint32_t vt = vl + g.i * STB;
+      const LinVec& vec = s.vec[n & 7];
       __nv_bfloat162 chk = as_bf2(0);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -558,20 +591,21 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         }
         fence_proxy_async();
       }
-      if (n > 0) {
-        wait(&s.mbx, (n - 1) & 1);
+      if (n >= BACK) {
+        wait(&s.mbx[two(n)], two_par(n) ^ 1);
         tmem_fence_after_sync();
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h) terms(1);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + T_V + m * 32 + hf * 16, y[m]);
+        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
       }
-      ready(&s.rdy_v);
+      ready(&s.rdy_v[two(n)]);
     }
   } else {  // the outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RB));
+    if constexpr (!AGG) {
     const int hf = (warp >> 2) & 1;  // half of the tokens (of P: of its columns)
     const int i0 = quad * 16, j0 = hf * 32;
     const int pz_at = TC + j0 + 2 * (lane & 3) - i0 - (lane >> 2) - ((lane >> 2) & 1);  // (even)
@@ -583,7 +617,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       if (n > 0) {
         const int m = n - 1;
         float2 f[4];
-        const float* fo = &s.vec[m & 3].fo[j0 + 2 * (lane & 3)];
+        const float* fo = &s.vec[m & 7].fo[j0 + 2 * (lane & 3)];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) f[tb] = *reinterpret_cast<const float2*>(fo + tb * 8);
         wait(&s.mbo, m & 1);  // (and S Q^T, which was issued before)
@@ -623,7 +657,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         tmem_fence_after_sync();
         if (rev ? j0 + 31 >= i0 : j0 <= i0 + 15) {
           tc_ld_frag(tq + T_P + j0, x);
-          const float* pz = s.vec[n & 3].pz[(lane >> 2) & 1] + pz_at;
+          const float* pz = s.vec[n & 7].pz[(lane >> 2) & 1] + pz_at;
           tc_wait_frag(x);
           float2 chk = f2b(0.0f);
 #pragma unroll
@@ -677,12 +711,47 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         if (lane == 0) mbar_arrive(&s.rdy_o);
       }
     }
+    }
   }
   if (!wait.ok()) report_timeout(&g_lin_status, a.status);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
   if (warp == 0) tmem_dealloc(tm, 512);
+}
+
+// The segments' start states: each is the one before, decayed over its
+// segment's tokens, and that segment's end from zero.  A float4 per thread.
+__global__ void __launch_bounds__(256) m3_lin_seg_kernel(const __grid_constant__ LinArgs a) {
+  grid_dep_trigger();
+  const int item = blockIdx.x, pass = item % a.np, bh = item / a.np;
+  const LinPass& p = a.p[pass];
+  const int at = (blockIdx.y * 256 + threadIdx.x) * 4, k = at / LIN_DMAX, v = at % LIN_DMAX;
+  const size_t slot = LIN_DMAX * LIN_DMAX;
+  const float* end = a.seg_end + (size_t)item * a.segs * slot + at;
+  float* start = a.seg_start + (size_t)item * a.segs * slot + at;
+  const float ld = a.ld[bh % a.Hv];
+  const int whole = a.seg_chunks * TC, odd = a.nc * TC - a.T;  // (backwards, the short chunk comes first)
+  const LinDecay d0 = lin_decay(ld, p.rev ? whole - odd : whole), d1 = lin_decay(ld, whole);
+  grid_dep_wait();
+  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (p.s_in && k < p.DK) {
+    const float* src = p.s_in + (size_t)bh * p.DK * p.DV;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v + i < p.DV) x[i] = src[p.st ? (size_t)(v + i) * p.DK + k : (size_t)k * p.DV + v + i];
+  }
+  *reinterpret_cast<float4*>(start) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll 4
+  for (int s = 0; s + 1 < a.segs; ++s) {
+    const float4 e = *reinterpret_cast<const float4*>(end + s * slot);
+    const LinDecay d = s ? d1 : d0;
+    x[0] = fmaf(d.near, x[0], fmaf(d.off, x[0], e.x));
+    x[1] = fmaf(d.near, x[1], fmaf(d.off, x[1], e.y));
+    x[2] = fmaf(d.near, x[2], fmaf(d.off, x[2], e.z));
+    x[3] = fmaf(d.near, x[3], fmaf(d.off, x[3], e.w));
+    *reinterpret_cast<float4*>(start + (s + 1) * slot) = make_float4(x[0], x[1], x[2], x[3]);
+  }
 }
 
 cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
@@ -696,20 +765,32 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
     if (!p.out_f32 && !delta_tile_map(&maps.m[i][3], p.out, p.DV, a.Hv / p.oh, a.T, a.B, p.os)) return cudaErrorInvalidValue;
   }
   const int64_t items = (int64_t)a.np * a.B * a.Hv;
-  cudaError_t e = cudaFuncSetAttribute(m3_lin_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  cudaError_t e = cudaSuccess;
+  if (a.segs > 1) {  // (the last segment's end is nobody's start)
+    e = cudaFuncSetAttribute(m3_lin_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess)
+      e = launch_k(m3_lin_tc_kernel<true>, dim3((unsigned)items, (unsigned)(a.segs - 1)), THREADS, SMEM_BYTES, st, false, a, maps);
+    if (e == cudaSuccess) e = launch_k(m3_lin_seg_kernel, dim3((unsigned)items, LIN_DMAX / 8), 256, 0, st, true, a);
+  }
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)items * 4, st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = a.stream ? dim3(delta_share_blocks(items, sms)) : dim3((unsigned)items, (unsigned)a.segs);
+  cfg.gridDim = a.stream ? dim3(delta_share_blocks((int64_t)a.B * a.Hv, sms / a.np) * a.np) : dim3((unsigned)items, (unsigned)a.segs);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;  // shares: a block may wait for the state of the one before
-  attr[0].val.cooperative = 1;
+  if (a.stream) {  // a block may wait for the state of the one before
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = a.stream ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, m3_lin_tc_kernel, a, maps);
+  cfg.numAttrs = a.stream || a.segs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, m3_lin_tc_kernel<false>, a, maps);
 }
 
 }  // namespace m3
