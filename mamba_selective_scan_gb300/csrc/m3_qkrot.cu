@@ -28,81 +28,112 @@ namespace {
 constexpr int ROT_DMAX = 256;       // head size, at most
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_WARPS = ROT_THREADS / 32;
-constexpr int ROT_BLOCKS = 608;     // share rows of the backward's workspace (and its blocks), at most
-constexpr int ROT_TABLE = 1024;     // pairs of (cos, sin) that a block keeps
+constexpr int ROT_BLOCKS = 456;     // share rows of the backward's workspace (and its blocks), at most
 
+struct RotSide {      // queries, or keys
+  const void *x, *dy; // [tokens][heads][D], heads dense; dy: the gradient of the output
+  void* y;            // output, or the gradient of x
+  int64_t xs, dys, ys;  // elements between tokens
+  const float* w;
+  float* dw;
+  int heads, groups, its, units;  // groups of heads a warp takes at once; units of `its` groups per token
+  int blocks;
+};
 struct RotArgs {
-  const void *q, *k, *dqo, *dko;  // [tokens][heads][D], heads dense
-  void *qo, *ko;                  // outputs: q_out and k_out, or dq and dk
-  int64_t qs, ks, dqos, dkos, qos, kos;  // elements between tokens
-  const float *wq, *wk, *freq;
+  RotSide side[2];
+  const float* freq;
   const int64_t* pos;
-  int64_t pos_bs;                 // between batch rows (0: the same for all)
-  float *part, *dwq, *dwk;        // [blocks][2][D]
+  int64_t pos_bs;     // between batch rows (0: the same for all)
+  float* part;        // [blocks][D]
   int64_t tokens;
-  int T, Hq, Hk, D, R;            // R pairs turn
-  int np, per, group;             // slots per head, slots per thread, lanes per head
-  int tb;                         // tokens per table
-  int nparts, accumulate;
+  int T, D, R;        // R pairs turn
+  int np, group;      // slots per head, lanes per head
+  int accumulate;
   float eps;
 };
 
-// cos and sin of position * freq
-__device__ __forceinline__ float2 turn_of(int64_t pos, float freq) {
-  if (!(fabsf(freq) <= 3.4028235e38f)) return f2b(__int_as_float(0x7FFFFFFF));
-  double t = (double)freq * 0.15915494309189533577;  // turns per position
+// turns per position as a 64-bit fraction
+__device__ __forceinline__ uint64_t turn_step(float freq) {
+  double t = (double)freq * 0.15915494309189533577;
   t -= rint(t);
-  const int64_t step = __double2ll_rn(t * 18446744073709551616.0);
-  const uint64_t ph = (uint64_t)pos * (uint64_t)step;       // of a turn, in 2^-64
-  const uint64_t near = ph + (1ull << 61);
-  const int quad = (int)(near >> 62);                       // the nearest quarter turn
-  const int64_t rest = (int64_t)(ph - ((uint64_t)quad << 62));  // within an eighth
-  float s, c;
-  sincospif((float)rest * 0x1p-63f, &s, &c);
-  if (quad & 1) {
-    const float x = c;
-    c = -s;
-    s = x;
-  }
-  if (quad & 2) {
-    c = -c;
-    s = -s;
-  }
-  return make_float2(c, s);
+  return (uint64_t)__double2ll_rn(t * 18446744073709551616.0);
+}
+// cos and sin of that many positions' turn: the angle within an eighth of the
+// nearest quarter turn, and Taylor's series there (to x^9 and x^10: the next
+// terms are below 2e-9)
+__device__ __forceinline__ float2 turn_of(int64_t pos, uint64_t step) {
+  const uint64_t ph = (uint64_t)pos * step;                     // of a turn, in 2^-64
+  const int quad = (int)((ph + (1ull << 61)) >> 62);
+  const int rest = (int)((int64_t)(ph - ((uint64_t)quad << 62)) >> 30);  // in 2^-34
+  const float x = (float)rest * (6.2831853071795864769f * 0x1p-34f), z = x * x;
+  const float s = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), 1.0f);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f), -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
+  const float a = quad & 1 ? -s : c, b = quad & 1 ? c : s;
+  return quad & 2 ? make_float2(-a, -b) : make_float2(a, b);
 }
 
-template <int VEC> __device__ __forceinline__ void ldr(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) v[0] = *p;
-  else {
-    const float4 t = *reinterpret_cast<const float4*>(p);
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+// VEC consecutive values as they are in memory
+template <typename T, int VEC> struct Raw;
+template <> struct Raw<float, 4> { float4 v; };
+template <> struct Raw<float, 1> { float v; };
+template <> struct Raw<__nv_bfloat16, 8> { uint4 v; };
+template <> struct Raw<__nv_bfloat16, 1> { __nv_bfloat16 v; };
+// and as f32
+__device__ __forceinline__ void open(const Raw<float, 4>& r, float (&v)[4]) { v[0] = r.v.x; v[1] = r.v.y; v[2] = r.v.z; v[3] = r.v.w; }
+__device__ __forceinline__ void open(const Raw<float, 1>& r, float (&v)[1]) { v[0] = r.v; }
+__device__ __forceinline__ void open(const Raw<__nv_bfloat16, 1>& r, float (&v)[1]) { v[0] = __bfloat162float(r.v); }
+__device__ __forceinline__ void open(const Raw<__nv_bfloat16, 8>& r, float (&v)[8]) {
+  const uint32_t x[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(x[i] << 16);
+    v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
   }
 }
-template <int VEC> __device__ __forceinline__ void ldr(const __nv_bfloat16* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) v[0] = __bfloat162float(*p);
-  else {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    const uint32_t x[4] = {t.x, t.y, t.z, t.w};
+__device__ __forceinline__ void put(float* p, const float (&v)[1]) { *p = v[0]; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
+__device__ __forceinline__ void put(float* p, const float (&v)[4]) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[8]) {
+  __nv_bfloat162 t[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(x[i] << 16);
-      v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+}
+// The pairs of a slot's two vectors: first values p, second values q, two
+// pairs to a float2 (of a vector of one value the second half stays 0)
+template <int VEC> struct Pairs {
+  static constexpr int N = VEC > 1 ? VEC / 2 : 1;
+  float2 p[N], q[N];
+  __device__ __forceinline__ float& first(int j) { return j & 1 ? p[j >> 1].y : p[j >> 1].x; }
+  __device__ __forceinline__ float& second(int j) { return j & 1 ? q[j >> 1].y : q[j >> 1].x; }
+  // value i of vector h: halves of a head, or neighbours
+  template <bool IL> __device__ __forceinline__ float& at(int h, int i) {
+    if (!IL || VEC == 1) return h ? second(i) : first(i);
+    const int e = h * VEC + i;
+    return e & 1 ? second(e >> 1) : first(e >> 1);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = q[j] = f2b(0.0f);
+  }
+  template <bool IL, typename T> __device__ __forceinline__ void take(const Raw<T, VEC> (&r)[2]) {
+    if (VEC == 1) zero();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[VEC];
+      open(r[h], v);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) at<IL>(h, i) = v[i];
     }
   }
-}
-template <int VEC> __device__ __forceinline__ void str(float* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) *p = v[0];
-  else *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <int VEC> __device__ __forceinline__ void str(__nv_bfloat16* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) *p = __float2bfloat16_rn(v[0]);
-  else {
-    __nv_bfloat162 t[4];
+  template <bool IL, typename T> __device__ __forceinline__ void give(T* dst, int h) {
+    float v[VEC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(t);
+    for (int i = 0; i < VEC; ++i) v[i] = at<IL>(h, i);
+    put(dst, v);
   }
-}
+};
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 
 // Slot u of a head: the elements e0 .. e0 + VEC and e1 .. e1 + VEC, and the
 // pairs u VEC .. of the table.  Half-split: the slots below R / VEC hold the
@@ -119,17 +150,28 @@ template <int VEC, bool IL> __device__ __forceinline__ void slot_at(const RotArg
   }
 }
 
-// Work is (token, group of heads): a warp takes 32 / group heads at a time.
-// A block goes through tables of tb tokens with a grid stride.
+// A unit of work is a token and `its` groups of its heads: a warp takes 32 /
+// group heads at a time, with the token's cosines and sines (and the weights)
+// in registers and the next groups' values on their way, across units.  A
+// warp makes its token's cosines and sines itself, so no barrier stands
+// between units.  Blocks take the queries or the keys.
 template <typename T, int VEC, int NS, bool IL, bool BWD>
-__global__ void __launch_bounds__(ROT_THREADS) m3_qkrot_kernel(const __grid_constant__ RotArgs a) {
-  __shared__ __align__(16) float2 cs[ROT_TABLE];
-  extern __shared__ float comb[];  // backward: [warps][2][D]
+__global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int ROW = VEC > 1 ? ROT_DMAX / 2 : 32 * NS;  // pairs of a head, at most
+  __shared__ __align__(16) float2 cs_all[ROT_WARPS][ROW];
+  __shared__ uint64_t steps[ROT_DMAX / 2];
+  __shared__ float lost[ROT_DMAX / 2];  // NaN where a frequency is not finite, else 0
+  extern __shared__ float comb[];       // backward: [warps][D]
+  const bool keys = blockIdx.x >= (unsigned)a.side[0].blocks;
+  const RotSide& sd = a.side[keys];
+  const int block = keys ? blockIdx.x - a.side[0].blocks : blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = a.group, heads_at_once = 32 / group, u0 = lane % group, sub = lane / group;
-  const int qg = (a.Hq + heads_at_once - 1) / heads_at_once, kg = (a.Hk + heads_at_once - 1) / heads_at_once;
-  const int per_tok = qg + kg, row = a.np * VEC;  // table entries per token
+  const int group = a.group, at_once = 32 / group, u0 = lane % group, sub = lane / group;
+  const int row = a.np * VEC;  // pairs of a head
   const float inv = 1.0f / (float)a.D;
+  float2* cs = cs_all[warp];
+  using P = Pairs<VEC>;
+  constexpr int N = P::N;
   int e0[NS], e1[NS];
   bool l0[NS], l1[NS];
 #pragma unroll
@@ -141,198 +183,260 @@ __global__ void __launch_bounds__(ROT_THREADS) m3_qkrot_kernel(const __grid_cons
     if (!l0[i]) e0[i] = 0;
     if (!l1[i]) e1[i] = 0;
   }
-  float dw[BWD ? 2 : 1][NS][2][VEC];
-  if constexpr (BWD) {
+  P w[NS];
+  auto weights = [&]() {
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int i = 0; i < NS; ++i) {
+      w[i].zero();
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dw[w][i][0][j] = dw[w][i][1][j] = 0.0f;
-  }
-  for (int64_t tok0 = (int64_t)blockIdx.x * a.tb; tok0 < a.tokens; tok0 += (int64_t)gridDim.x * a.tb) {
-    const int nt = (int)min((int64_t)a.tb, a.tokens - tok0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * row; i += ROT_THREADS) {
-      const int m = i % row;
-      const int64_t tok = tok0 + i / row;
-      cs[i] = m < a.R ? turn_of(a.pos[tok / a.T * a.pos_bs + tok % a.T], a.freq[m]) : make_float2(1.0f, 0.0f);
+      for (int j = 0; j < VEC; ++j) {
+        w[i].template at<IL>(0, j) = sd.w ? sd.w[e0[i] + j] : 1.0f;
+        w[i].template at<IL>(1, j) = sd.w ? sd.w[e1[i] + j] : 1.0f;
+      }
     }
-    __syncthreads();
-    for (int w = warp; w < nt * per_tok; w += ROT_WARPS) {
-      const int t = w / per_tok, g = w % per_tok;
-      const bool isk = g >= qg;
-      const int h = (isk ? g - qg : g) * heads_at_once + sub;
-      const bool live = h < (isk ? a.Hk : a.Hq);
-      const int64_t tok = tok0 + t;
-      const T* src = static_cast<const T*>(isk ? a.k : a.q) + tok * (isk ? a.ks : a.qs) + (int64_t)(live ? h : 0) * a.D;
-      T* dst = static_cast<T*>(isk ? a.ko : a.qo) + tok * (isk ? a.kos : a.qos) + (int64_t)(live ? h : 0) * a.D;
-      const float* wt = isk ? a.wk : a.wq;
-      float x[NS][2][VEC], y[NS][2][VEC];
-      float ss = 0.0f;
+  };
+  if (BWD) weights();
+  P dw[BWD ? NS : 1];
+#pragma unroll
+  for (int i = 0; i < (BWD ? NS : 1); ++i) dw[i].zero();
+  for (int m = threadIdx.x; m < a.R; m += ROT_THREADS) {
+    const float f = a.freq[m];
+    steps[m] = turn_step(f);
+    lost[m] = f * 0.0f;
+  }
+  __syncthreads();
+
+  // the values of a group of a token's heads (what no fetch fills stays zero)
+  struct Values {
+    Raw<T, VEC> x[NS][2], y[BWD ? NS : 1][2];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[i][0][j] = x[i][1][j] = 0.0f;
-        if (live && l0[i]) ldr<VEC>(src + e0[i], x[i][0]);
-        if (live && l1[i]) ldr<VEC>(src + e1[i], x[i][1]);
+        x[i][0] = x[i][1] = Raw<T, VEC>{};
+        if constexpr (BWD) y[i][0] = y[i][1] = Raw<T, VEC>{};
       }
-      if constexpr (BWD) {
-        const T* up = static_cast<const T*>(isk ? a.dko : a.dqo) + tok * (isk ? a.dkos : a.dqos) + (int64_t)(live ? h : 0) * a.D;
+    }
+  };
+  constexpr int AHEAD = BWD ? 1 : 2;  // groups on their way (backward, two would not fit the registers)
+  Values val[AHEAD];
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
+  for (int k = 0; k < AHEAD; ++k) val[k].zero();
+  auto fetch = [&](Values& r, int64_t tok, int g) {
+    const int h = g * at_once + sub;
+    const int at = h * a.D;
+    const T* xp = static_cast<const T*>(sd.x) + tok * sd.xs + at;
+    const T* yp = static_cast<const T*>(sd.dy) + tok * sd.dys + at;
+    if (h < sd.heads) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) y[i][0][j] = y[i][1][j] = 0.0f;
-          if (live && l0[i]) ldr<VEC>(up + e0[i], y[i][0]);
-          if (live && l1[i]) ldr<VEC>(up + e1[i], y[i][1]);
+      for (int i = 0; i < NS; ++i) {
+        if (l0[i]) r.x[i][0] = *reinterpret_cast<const Raw<T, VEC>*>(xp + e0[i]);
+        if (l1[i]) r.x[i][1] = *reinterpret_cast<const Raw<T, VEC>*>(xp + e1[i]);
+        if constexpr (BWD) {
+          if (l0[i]) r.y[i][0] = *reinterpret_cast<const Raw<T, VEC>*>(yp + e0[i]);
+          if (l1[i]) r.y[i][1] = *reinterpret_cast<const Raw<T, VEC>*>(yp + e1[i]);
         }
       }
+    } else {
+      r.zero();
+    }
+  };
+  // this warp's units: `step` apart, counted as token (batch row b, time t) and
+  // part of its groups
+  struct Unit {
+    int64_t tok, pos;
+    int b, t, part, g0, g1;
+  };
+  const int64_t step = (int64_t)sd.blocks * ROT_WARPS;
+  const int64_t step_tok = step / sd.units;
+  const int step_part = (int)(step % sd.units), step_b = (int)(step_tok / a.T), step_t = (int)(step_tok % a.T);
+  auto place = [&](Unit& r) {
+    if (r.tok >= a.tokens) {
+      r.g0 = r.g1 = 0;
+      return;
+    }
+    r.g0 = r.part * sd.its;
+    r.g1 = min(r.g0 + sd.its, sd.groups);
+    if (a.R > 0) r.pos = a.pos[r.b * a.pos_bs + r.t];
+  };
+  Unit now;
+  {
+    const int64_t first = (int64_t)block * ROT_WARPS + warp;
+    now.tok = first / sd.units;
+    now.part = (int)(first % sd.units);
+    now.b = (int)(now.tok / a.T);
+    now.t = (int)(now.tok % a.T);
+    now.pos = 0;
+    place(now);
 #pragma unroll
-      for (int i = 0; i < NS; ++i)
+    for (int k = 0; k < AHEAD; ++k)
+      if (now.g0 + k < now.g1) fetch(val[k], now.tok, now.g0 + k);
+  }
+  while (now.tok < a.tokens) {
+    Unit then = now;
+    then.tok += step_tok;
+    then.b += step_b;
+    then.t += step_t;
+    then.part += step_part;
+    if (then.part >= sd.units) {
+      then.part -= sd.units;
+      ++then.tok;
+      ++then.t;
+    }
+    if (then.t >= a.T) {
+      then.t -= a.T;
+      ++then.b;
+    }
+    place(then);
+    __syncwarp();
+    for (int m = lane; m < row; m += 32) {
+      float2 c = make_float2(1.0f, 0.0f);
+      if (m < a.R) {
+        c = turn_of(now.pos, steps[m]);
+        c.x += lost[m];
+        c.y += lost[m];
+      }
+      cs[m] = c;
+    }
+    __syncwarp();
+    // cosines and sines; forward, times the weights: of the first value and
+    // of the second in either output
+    if (!BWD) weights();  // (there again for each unit: no registers in between)
+    float2 co[NS][N], si[NS][N], wc[BWD ? 1 : NS][N], ws[BWD ? 1 : NS][N];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) ss = fmaf(x[i][0][j], x[i][0][j], fmaf(x[i][1][j], x[i][1][j], ss));
-      for (int o = 1; o < group; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      const float r = live ? rsqrtf(ss * inv + a.eps) : 0.0f;  // (no head: 1 / sqrt(0) with eps 0)
-      if constexpr (!BWD) {
+    for (int i = 0; i < NS; ++i) {
+      const float2* tb = cs + (l0[i] ? u0 + i * group : 0) * VEC;
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          float w0[VEC], w1[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) w0[j] = w1[j] = 1.0f;
-          if (wt) {
-            ldr<VEC == 1 ? 1 : 4>(wt + e0[i], reinterpret_cast<float(&)[VEC == 1 ? 1 : 4]>(w0));
-            ldr<VEC == 1 ? 1 : 4>(wt + e1[i], reinterpret_cast<float(&)[VEC == 1 ? 1 : 4]>(w1));
-            if constexpr (VEC == 8) {
-              ldr<4>(wt + e0[i] + 4, reinterpret_cast<float(&)[4]>(w0[4]));
-              ldr<4>(wt + e1[i] + 4, reinterpret_cast<float(&)[4]>(w1[4]));
-            }
-          }
-          const int u = l0[i] ? u0 + i * group : 0;
-          const float2* tb = cs + t * row + u * VEC;
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            x[i][0][j] = x[i][0][j] * r * w0[j];
-            x[i][1][j] = x[i][1][j] * r * w1[j];
-          }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float2 c = tb[j];
-            float &p = IL && VEC > 1 ? x[i][2 * j / VEC][2 * j % VEC] : x[i][0][j];
-            float &q = IL && VEC > 1 ? x[i][2 * j / VEC][2 * j % VEC + 1] : x[i][1][j];
-            const float aa = p * c.x - q * c.y, bb = p * c.y + q * c.x;
-            p = aa;
-            q = bb;
-          }
-          if (live && l0[i]) str<VEC>(dst + e0[i], x[i][0]);
-          if (live && l1[i]) str<VEC>(dst + e1[i], x[i][1]);
-        }
-      } else {
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-          float w0[VEC], w1[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) w0[j] = w1[j] = 1.0f;
-          if (wt) {
-            ldr<VEC == 1 ? 1 : 4>(wt + e0[i], reinterpret_cast<float(&)[VEC == 1 ? 1 : 4]>(w0));
-            ldr<VEC == 1 ? 1 : 4>(wt + e1[i], reinterpret_cast<float(&)[VEC == 1 ? 1 : 4]>(w1));
-            if constexpr (VEC == 8) {
-              ldr<4>(wt + e0[i] + 4, reinterpret_cast<float(&)[4]>(w0[4]));
-              ldr<4>(wt + e1[i] + 4, reinterpret_cast<float(&)[4]>(w1[4]));
-            }
-          }
-          const int u = l0[i] ? u0 + i * group : 0;
-          const float2* tb = cs + t * row + u * VEC;
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float2 c = tb[j];
-            float &p = IL && VEC > 1 ? y[i][2 * j / VEC][2 * j % VEC] : y[i][0][j];
-            float &q = IL && VEC > 1 ? y[i][2 * j / VEC][2 * j % VEC + 1] : y[i][1][j];
-            const float aa = p * c.x + q * c.y, bb = q * c.x - p * c.y;
-            p = aa;
-            q = bb;
-          }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float a0 = y[i][0][j] * x[i][0][j] * r, a1 = y[i][1][j] * x[i][1][j] * r;
-            if (isk) {
-              dw[1][i][0][j] += a0;
-              dw[1][i][1][j] += a1;
-            } else {
-              dw[0][i][0][j] += a0;
-              dw[0][i][1][j] += a1;
-            }
-            dot = fmaf(a0, w0[j], fmaf(a1, w1[j], dot));
-            y[i][0][j] *= w0[j];
-            y[i][1][j] *= w1[j];
-          }
-        }
-        for (int o = 1; o < group; o <<= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        const float m = dot * inv * r;
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            y[i][0][j] = r * (y[i][0][j] - x[i][0][j] * m);
-            y[i][1][j] = r * (y[i][1][j] - x[i][1][j] * m);
-          }
-          if (live && l0[i]) str<VEC>(dst + e0[i], y[i][0]);
-          if (live && l1[i]) str<VEC>(dst + e1[i], y[i][1]);
+      for (int j = 0; j < N; ++j) {
+        const float2 c0 = tb[2 * j], c1 = VEC > 1 ? tb[2 * j + 1] : f2b(0.0f);
+        co[i][j] = make_float2(c0.x, c1.x);
+        si[i][j] = make_float2(c0.y, c1.y);
+        if constexpr (!BWD) {
+          wc[i][j] = __fmul2_rn(w[i].q[j], co[i][j]);
+          ws[i][j] = neg2(__fmul2_rn(w[i].q[j], si[i][j]));
+          co[i][j] = __fmul2_rn(w[i].p[j], co[i][j]);
+          si[i][j] = __fmul2_rn(w[i].p[j], si[i][j]);
         }
       }
     }
-  }
-  if constexpr (BWD) {
-    // this block's share of the weights' gradients: lanes that hold the same
-    // slots, then the warps, in a fixed order
-    grid_dep_trigger();
-    __syncthreads();
+    T* op = static_cast<T*>(sd.y) + now.tok * sd.ys;
+    auto work = [&](int g, int k) {  // group g, and its values' place for the one that comes AHEAD of it
+      Values& r = val[k];
+      const int h = g * at_once + sub;
+      const bool live = h < sd.heads;
+      P v[NS], u[BWD ? NS : 1];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+      for (int i = 0; i < NS; ++i) {
+        v[i].template take<IL, T>(r.x[i]);
+        if constexpr (BWD) u[i].template take<IL, T>(r.y[i]);
+      }
+      if (g + AHEAD < now.g1) fetch(r, now.tok, g + AHEAD);
+      else if (then.g0 + k < then.g1) fetch(r, then.tok, then.g0 + k);
+      float2 s2 = f2b(0.0f);
 #pragma unroll
       for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float s0 = dw[w][i][0][j], s1 = dw[w][i][1][j];
-          for (int o = group; o < 32; o <<= 1) {
-            s0 += __shfl_xor_sync(~0u, s0, o);
-            s1 += __shfl_xor_sync(~0u, s1, o);
+        for (int j = 0; j < N; ++j) s2 = __ffma2_rn(v[i].p[j], v[i].p[j], __ffma2_rn(v[i].q[j], v[i].q[j], s2));
+      float ss = s2.x + s2.y;
+      for (int o = 1; o < group; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+      const float rn = live ? rsqrtf(ss * inv + a.eps) : 0.0f;  // (no head: 1 / sqrt(0) with eps 0)
+      const float2 r2 = f2b(rn);
+      if constexpr (!BWD) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float2 p = __fmul2_rn(v[i].p[j], r2), q = __fmul2_rn(v[i].q[j], r2);
+            v[i].p[j] = __ffma2_rn(p, co[i][j], __fmul2_rn(q, ws[i][j]));
+            v[i].q[j] = __ffma2_rn(p, si[i][j], __fmul2_rn(q, wc[i][j]));
           }
-          if (sub == 0 && l0[i]) comb[(warp * 2 + w) * a.D + e0[i] + j] = s0;
-          if (sub == 0 && l1[i]) comb[(warp * 2 + w) * a.D + e1[i] + j] = s1;
-        }
+      } else {
+        // u = r dn w,  dx = u - x r^2 mean(u x)
+        float2 d2 = f2b(0.0f);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            const float2 p = __fmul2_rn(u[i].p[j], r2), q = __fmul2_rn(u[i].q[j], r2);
+            const float2 np = __ffma2_rn(p, co[i][j], __fmul2_rn(q, si[i][j])), nq = __ffma2_rn(q, co[i][j], __fmul2_rn(p, neg2(si[i][j])));
+            dw[i].p[j] = __ffma2_rn(np, v[i].p[j], dw[i].p[j]);
+            dw[i].q[j] = __ffma2_rn(nq, v[i].q[j], dw[i].q[j]);
+            u[i].p[j] = __fmul2_rn(np, w[i].p[j]);
+            u[i].q[j] = __fmul2_rn(nq, w[i].q[j]);
+            d2 = __ffma2_rn(u[i].p[j], v[i].p[j], __ffma2_rn(u[i].q[j], v[i].q[j], d2));
+          }
+        float dot = d2.x + d2.y;
+        for (int o = 1; o < group; o <<= 1) dot += __shfl_xor_sync(~0u, dot, o);
+        const float2 m = f2b(-dot * inv * rn * rn);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            v[i].p[j] = __ffma2_rn(v[i].p[j], m, u[i].p[j]);
+            v[i].q[j] = __ffma2_rn(v[i].q[j], m, u[i].q[j]);
+          }
+      }
+      T* dst = op + h * a.D;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        if (live && l0[i]) v[i].template give<IL>(dst + e0[i], 0);
+        if (live && l1[i]) v[i].template give<IL>(dst + e1[i], 1);
+      }
+    };
+#pragma unroll 1
+    for (int g = now.g0; g < now.g1; g += AHEAD) {
+      work(g, 0);
+      if constexpr (AHEAD > 1) {
+        if (g + 1 < now.g1) work(g + 1, 1);
+        else if (then.g0 + 1 < then.g1) fetch(val[1], then.tok, then.g0 + 1);
+      }
+    }
+    now = then;
+  }
+  if constexpr (BWD) {
+    // this block's share of the weight's gradient: lanes that hold the same
+    // slots, then the warps, in a fixed order
+    grid_dep_trigger();
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int j = 0; j < 2 * VEC; ++j) {
+        float d = dw[i].template at<IL>(j / VEC, j % VEC);
+        for (int o = group; o < 32; o <<= 1) d += __shfl_xor_sync(~0u, d, o);
+        if (sub == 0 && (j < VEC ? l0[i] : l1[i])) comb[warp * a.D + (j < VEC ? e0[i] + j : e1[i] + j - VEC)] = d;
+      }
     __syncthreads();
-    for (int c = threadIdx.x; c < 2 * a.D; c += ROT_THREADS) {
-      float s = 0.0f;
-      for (int w = 0; w < ROT_WARPS; ++w) s += comb[w * 2 * a.D + c];
-      a.part[(size_t)blockIdx.x * 2 * a.D + c] = s;
+    for (int k = threadIdx.x; k < a.D; k += ROT_THREADS) {
+      float d = 0.0f;
+      for (int m = 0; m < ROT_WARPS; ++m) d += comb[m * a.D + k];
+      a.part[(size_t)blockIdx.x * a.D + k] = d;
     }
   }
 }
 
-// The weights' gradients: the blocks' shares [nparts][2][D] added over the
+// The weights' gradients: the blocks' shares [blocks][D] added over the
 // blocks, 32 columns per block, the rows over 32 warps and a fixed tree.
 __global__ void __launch_bounds__(1024) m3_qkrot_wgrad_kernel(const __grid_constant__ RotArgs a) {
   __shared__ float sh[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + lane, n2 = 2 * a.D;
+  const int c = blockIdx.x * 32 + lane;
+  const RotSide& sd = a.side[blockIdx.y];
+  const float* part = a.part + (blockIdx.y ? (size_t)a.side[0].blocks * a.D : 0) + c;
   grid_dep_wait();
-  float s = 0.0f;
-  if (c < n2)
-    for (int r = warp; r < a.nparts; r += 32) s += a.part[(size_t)r * n2 + c];
-  sh[warp][lane] = s;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < a.D) {
+    int r = warp;
+    for (; r + 96 < sd.blocks; r += 128)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += part[(size_t)(r + 32 * i) * a.D];
+    for (; r < sd.blocks; r += 32) s[0] += part[(size_t)r * a.D];
+  }
+  sh[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
   float t = sh[lane][warp];  // column blockIdx.x * 32 + warp
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
   const int cc = blockIdx.x * 32 + warp;
-  if (lane == 0 && cc < n2) {
-    float* o = cc < a.D ? a.dwq : a.dwk;
-    if (o) {
-      o += cc < a.D ? cc : cc - a.D;
-      *o = a.accumulate ? *o + t : t;
-    }
-  }
+  if (lane == 0 && cc < a.D && sd.dw) sd.dw[cc] = a.accumulate ? sd.dw[cc] + t : t;
 }
 
 m3_status rot_validate(const m3_qkrot_dims* d, m3_dtype act) {
@@ -357,19 +461,22 @@ m3_status rot_validate(const m3_qkrot_dims* d, m3_dtype act) {
 }
 
 int64_t rot_parts(const m3_qkrot_dims* d) {
-  const int64_t n = d->batch * d->seq_len;
-  return n < ROT_BLOCKS ? n : ROT_BLOCKS;
+  return d->batch && d->seq_len ? ROT_BLOCKS : 0;
 }
 
-RotArgs rot_args(const m3_qkrot_dims* d, const float* wq, const float* wk, const int64_t* pos, const float* freq) {
+RotArgs rot_args(const m3_qkrot_dims* d, const void* q, const void* k, const float* wq, const float* wk, const int64_t* pos,
+                 const float* freq) {
   RotArgs a{};
   const int64_t qw = d->q_heads * d->head_dim, kw = d->k_heads * d->head_dim;
-  a.qs = d->q_stride ? d->q_stride : qw;
-  a.ks = d->k_stride ? d->k_stride : kw;
-  a.wq = wq; a.wk = wk; a.pos = pos; a.freq = freq;
+  a.side[0].x = q; a.side[1].x = k;
+  a.side[0].xs = d->q_stride ? d->q_stride : qw;
+  a.side[1].xs = d->k_stride ? d->k_stride : kw;
+  a.side[0].w = wq; a.side[1].w = wk;
+  a.side[0].heads = (int)d->q_heads; a.side[1].heads = (int)d->k_heads;
+  a.pos = pos; a.freq = freq;
   a.pos_bs = d->position_stride;
   a.tokens = d->batch * d->seq_len;
-  a.T = (int)d->seq_len; a.Hq = (int)d->q_heads; a.Hk = (int)d->k_heads;
+  a.T = (int)d->seq_len;
   a.D = (int)d->head_dim; a.R = (int)d->rot_dim / 2;
   a.eps = d->eps;
   a.accumulate = d->accumulate_param_grads;
@@ -380,24 +487,33 @@ template <typename T, int VEC, int NS, bool IL, bool BWD>
 cudaError_t rot_go(RotArgs& a, cudaStream_t s) {
   auto kern = m3_qkrot_kernel<T, VEC, NS, IL, BWD>;
   int sms = 0, occ = 0;
-  const size_t smem = BWD ? (size_t)ROT_WARPS * 2 * a.D * 4 : 0;
+  const size_t smem = BWD ? (size_t)ROT_WARPS * a.D * 4 : 0;
   cudaError_t e = sm_count(&sms);
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, ROT_THREADS, smem);
   if (e != cudaSuccess) return e;
-  // tokens per table: as many as it holds, but no fewer blocks than fit the GPU at once
   int64_t blocks = (int64_t)sms * (occ < 1 ? 1 : occ);
   if (BWD && blocks > ROT_BLOCKS) blocks = ROT_BLOCKS;
-  const int64_t row = (int64_t)a.np * VEC;
-  int64_t tb = ROT_TABLE / row, fill = (a.tokens + blocks - 1) / blocks;
-  if (tb > fill) tb = fill;
-  if (tb < 1) tb = 1;
-  a.tb = (int)tb;
-  const int64_t need = (a.tokens + tb - 1) / tb;
-  if (blocks > need) blocks = need;
-  a.nparts = (int)blocks;
-  e = launch_k(kern, dim3((unsigned)blocks), ROT_THREADS, smem, s, false, a);
+  if (blocks < 2) blocks = 2;
+  // blocks by the sides' work; groups per unit: a token's, but no fewer units
+  // than a side's warps
+  const int at_once = 32 / a.group;
+  int64_t all = 0, left = blocks;
+  for (RotSide& sd : a.side) all += sd.groups = (sd.heads + at_once - 1) / at_once;
+  for (int i = 0; i < 2; ++i) {
+    RotSide& sd = a.side[i];
+    int64_t n = i ? left : (blocks * sd.groups + all / 2) / all;
+    if (i == 0 && n > blocks - 1) n = blocks - 1;
+    if (n < 1) n = 1;
+    left -= n;
+    const int64_t its = sd.groups * a.tokens / (n * ROT_WARPS);
+    sd.its = its < 1 ? 1 : its > sd.groups ? sd.groups : (int)its;
+    sd.units = (sd.groups + sd.its - 1) / sd.its;
+    const int64_t need = (a.tokens * sd.units + ROT_WARPS - 1) / ROT_WARPS;
+    sd.blocks = (int)(n < need ? n : need);
+  }
+  e = launch_k(kern, dim3((unsigned)(a.side[0].blocks + a.side[1].blocks)), ROT_THREADS, smem, s, false, a);
   if (BWD && e == cudaSuccess)
-    e = launch_k(m3_qkrot_wgrad_kernel, dim3((unsigned)((2 * a.D + 31) / 32)), 1024, 0, s, true, a);
+    e = launch_k(m3_qkrot_wgrad_kernel, dim3((unsigned)((a.D + 31) / 32), 2), 1024, 0, s, true, a);
   return e;
 }
 
@@ -408,10 +524,10 @@ cudaError_t rot_launch(RotArgs a, bool vec, bool il, cudaStream_t s) {
   a.np = (a.D + 2 * v - 1) / (2 * v);
   a.group = 1;
   while (a.group < a.np && a.group < 32) a.group *= 2;
-  a.per = (a.np + a.group - 1) / a.group;
+  const int per = (a.np + a.group - 1) / a.group;
   if (vec) return il ? rot_go<T, V, 1, true, BWD>(a, s) : rot_go<T, V, 1, false, BWD>(a, s);
-  if (a.per == 1) return il ? rot_go<T, 1, 1, true, BWD>(a, s) : rot_go<T, 1, 1, false, BWD>(a, s);
-  if (a.per == 2) return il ? rot_go<T, 1, 2, true, BWD>(a, s) : rot_go<T, 1, 2, false, BWD>(a, s);
+  if (per == 1) return il ? rot_go<T, 1, 1, true, BWD>(a, s) : rot_go<T, 1, 1, false, BWD>(a, s);
+  if (per == 2) return il ? rot_go<T, 1, 2, true, BWD>(a, s) : rot_go<T, 1, 2, false, BWD>(a, s);
   return il ? rot_go<T, 1, 4, true, BWD>(a, s) : rot_go<T, 1, 4, false, BWD>(a, s);
 }
 
@@ -439,7 +555,7 @@ m3_status m3scan_qkrot_plan(const m3_qkrot_dims* dims, m3_dtype act, m3_qkrot_pl
   const m3_status st = rot_validate(dims, act);
   if (st != M3_OK) return st;
   if (!out) return M3_ERR_NULL;
-  out->workspace_bytes = STATUS_BYTES + rot_parts(dims) * 2 * dims->head_dim * 4;
+  out->workspace_bytes = STATUS_BYTES + rot_parts(dims) * dims->head_dim * 4;
   return M3_OK;
 }
 
@@ -457,11 +573,11 @@ m3_status m3scan_qkrot_fwd(const m3_qkrot_dims* dims, m3_dtype act, const void* 
   if (dims->batch == 0 || dims->seq_len == 0) return M3_OK;
   if (!q || !k || !q_out || !k_out) return M3_ERR_NULL;
   if (dims->rot_dim > 0 && (!positions || !inv_freq)) return M3_ERR_NULL;
-  RotArgs a = rot_args(dims, q_weight, k_weight, positions, inv_freq);
-  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
-  a.qos = dims->q_out_stride ? dims->q_out_stride : dims->q_heads * dims->head_dim;
-  a.kos = dims->k_out_stride ? dims->k_out_stride : dims->k_heads * dims->head_dim;
-  const bool vec = rot_vec(dims, es, {q, k, q_out, k_out, q_weight, k_weight}, {a.qs, a.ks, a.qos, a.kos});
+  RotArgs a = rot_args(dims, q, k, q_weight, k_weight, positions, inv_freq);
+  a.side[0].y = q_out; a.side[1].y = k_out;
+  a.side[0].ys = dims->q_out_stride ? dims->q_out_stride : dims->q_heads * dims->head_dim;
+  a.side[1].ys = dims->k_out_stride ? dims->k_out_stride : dims->k_heads * dims->head_dim;
+  const bool vec = rot_vec(dims, es, {q, k, q_out, k_out}, {a.side[0].xs, a.side[1].xs, a.side[0].ys, a.side[1].ys});
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = act == M3_BF16 ? rot_launch<__nv_bfloat16, false>(a, vec, dims->interleaved, s)
                                        : rot_launch<float, false>(a, vec, dims->interleaved, s);
@@ -493,16 +609,18 @@ m3_status m3scan_qkrot_bwd(const m3_qkrot_dims* dims, m3_dtype act, const void* 
   m3scan_qkrot_plan(dims, act, &pl);
   if (!workspace || (int64_t)workspace_bytes < pl.workspace_bytes) return M3_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return M3_ERR_ALIGN;
-  RotArgs a = rot_args(dims, q_weight, k_weight, positions, inv_freq);
+  RotArgs a = rot_args(dims, q, k, q_weight, k_weight, positions, inv_freq);
   const int64_t qw = dims->q_heads * dims->head_dim, kw = dims->k_heads * dims->head_dim;
-  a.q = q; a.k = k; a.dqo = dq_out; a.dko = dk_out; a.qo = dq; a.ko = dk;
-  a.dqos = dims->dq_out_stride ? dims->dq_out_stride : qw;
-  a.dkos = dims->dk_out_stride ? dims->dk_out_stride : kw;
-  a.qos = dims->dq_stride ? dims->dq_stride : qw;
-  a.kos = dims->dk_stride ? dims->dk_stride : kw;
-  a.dwq = d_q_weight; a.dwk = d_k_weight;
+  a.side[0].dy = dq_out; a.side[1].dy = dk_out;
+  a.side[0].y = dq; a.side[1].y = dk;
+  a.side[0].dys = dims->dq_out_stride ? dims->dq_out_stride : qw;
+  a.side[1].dys = dims->dk_out_stride ? dims->dk_out_stride : kw;
+  a.side[0].ys = dims->dq_stride ? dims->dq_stride : qw;
+  a.side[1].ys = dims->dk_stride ? dims->dk_stride : kw;
+  a.side[0].dw = d_q_weight; a.side[1].dw = d_k_weight;
   a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + STATUS_BYTES);
-  const bool vec = rot_vec(dims, es, {dq_out, dk_out, q, k, dq, dk, q_weight, k_weight}, {a.qs, a.ks, a.dqos, a.dkos, a.qos, a.kos});
+  const bool vec = rot_vec(dims, es, {dq_out, dk_out, q, k, dq, dk},
+                           {a.side[0].xs, a.side[1].xs, a.side[0].dys, a.side[1].dys, a.side[0].ys, a.side[1].ys});
   const cudaError_t e = act == M3_BF16 ? rot_launch<__nv_bfloat16, true>(a, vec, dims->interleaved, s)
                                        : rot_launch<float, true>(a, vec, dims->interleaved, s);
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
