@@ -106,7 +106,8 @@ cudaError_t take_delta_prep_status(unsigned* out);
 cudaError_t launch_delta_tc_fwd(const DeltaArgs& a, cudaStream_t st);
 // Tensor map of a [B, T, H, D] bf16 tensor (`stride` elements between
 // tokens) read in tiles of 64 tokens x 64 columns, 128-byte swizzle
-bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, int64_t B, int64_t stride);
+// (of an f32 tensor: 64 tokens x 32 columns)
+bool delta_tile_map(CUtensorMap* map, const void* ptr, int D, int H, int64_t T, int64_t B, int64_t stride, bool f32 = false);
 cudaError_t launch_delta_seg(const DeltaArgs& a, const float* first, bool rev, cudaStream_t st);
 cudaError_t take_delta_fwd_status(unsigned* out);
 // Its backward: the reverse pass over the chunks, then every chunk's gradients

@@ -235,8 +235,13 @@ __global__ void __launch_bounds__(256) m3_lin_share_kernel(const __grid_constant
     const float4 x = *reinterpret_cast<const float4*>(src + (size_t)m * a.D);
     s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
   }
-  T* o = static_cast<T*>(a.out[which]) + tok * a.os[which] + c;
-  Act<T>::st(o, s.x); Act<T>::st(o + 1, s.y); Act<T>::st(o + 2, s.z); Act<T>::st(o + 3, s.w);
+  T* o = static_cast<T*>(a.out[which]) + tok * a.os[which] + c;  // (16-byte tokens and heads of 8)
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(o) = s;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 }
 template <typename T> cudaError_t launch_lin_share(const LinShare& a, cudaStream_t st) {
   const int64_t n = a.tokens * (a.Hk * a.D / 4);

@@ -59,7 +59,7 @@ constexpr int AGG_STAGES = 5;
 constexpr int AGG_STAGE = 4 * TILE;    // K, K, V, V
 constexpr int PT = STAGES * STAGE;     // P
 constexpr int OUT = PT + TILE;         // a chunk's outputs, for the tile store
-constexpr int SMALL = OUT + 2 * TILE;
+constexpr int SMALL = OUT + 4 * TILE;  // (f32: four tiles of 32 values)
 
 struct Smem {  // at SMALL
   LinVec vec[8];
@@ -316,10 +316,10 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           wait(&s.rdy_o, n & 1);  // the outputs are in place
           const LinInfo& t = s.info[n & 7];
           const LinPass& p = a.p[t.pass];
-          if (wait.ok() && !p.out_f32) {
-            const int h = p.oh == 1 ? t.h : t.h / p.oh;
-            tma_tile_store(&maps.m[t.pass][3], st0 + OUT, 0, h, t.tok, t.b);
-            if (p.DV > 64) tma_tile_store(&maps.m[t.pass][3], st0 + OUT + TILE, 64, h, t.tok, t.b);
+          if (wait.ok()) {
+            const int h = p.oh == 1 ? t.h : t.h / p.oh, cols = p.out_f32 ? 32 : 64;
+            for (int col = 0, at = OUT; col < p.DV; col += cols, at += TILE)
+              tma_tile_store(&maps.m[t.pass][3], st0 + at, col, h, t.tok, t.b);
             bulk_commit();
             bulk_wait_read();
           }
@@ -609,6 +609,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     const int hf = (warp >> 2) & 1;  // half of the tokens (of P: of its columns)
     const int i0 = quad * 16, j0 = hf * 32;
     const int pz_at = TC + j0 + 2 * (lane & 3) - i0 - (lane >> 2) - ((lane >> 2) & 1);  // (even)
+    // where this thread's first value goes: bf16 (rows of 64 values), f32 (of 32)
+    const uint32_t op32 = st0 + OUT + quad * TILE + sw(j0 + 2 * (lane & 3), lane >> 4) + ((lane >> 2) & 3) * 4;
     const uint32_t op = st0 + OUT + (quad >> 1) * TILE + sw(j0 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
 #pragma unroll 1
     for (int n = 0; n <= walk.n; ++n) {
@@ -689,15 +691,14 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         if (n > 1) wait(&s.o_free, n & 1);
         const LinInfo& t = s.info[(n - 1) & 7];
         const LinPass& p = a.p[t.pass];
-        if (p.out_f32) {  // straight to memory
-          float* dst = static_cast<float*>(p.out) + ((int64_t)t.b * a.T + t.tok) * p.os + (int64_t)(t.h / p.oh) * p.DV;
+        if (p.out_f32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int r = quad * 32 + h * 16 + (c & 1) * 8 + (lane >> 2), tok = j0 + (c >> 1) * 8 + 2 * (lane & 3);
-              if (r < p.DV && tok < t.n) dst[tok * p.os + r] = o[h][c].x;
-              if (r < p.DV && tok + 1 < t.n) dst[(tok + 1) * p.os + r] = o[h][c].y;
+            for (int c = 0; c < 8; ++c) {  // value 16 h + 8 (c & 1) + lane / 4 of this warp's tile, tokens j0 + 8 (c >> 1) + 2 (lane & 3), + 1
+              const uint32_t at = (op32 ^ ((4 * h + 2 * (c & 1)) << 4)) + (c >> 1) * 1024;
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(o[h][c].x) : "memory");
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"((at ^ 16u) + 128u), "f"(o[h][c].y) : "memory");
             }
         } else {
 #pragma unroll
@@ -705,8 +706,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
             for (int tp = 0; tp < 2; ++tp)
               stmatrix4<true>((op ^ (h * 32)) + tp * 2048, pack2(o[h][tp * 4]), pack2(o[h][tp * 4 + 1]), pack2(o[h][tp * 4 + 2]), pack2(o[h][tp * 4 + 3]));
-          fence_proxy_async();
         }
+        fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.rdy_o);
       }
@@ -762,7 +763,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
         !delta_tile_map(&maps.m[i][1], p.k, p.DK, a.Hv / p.kh, a.T, a.B, p.ks) ||
         !delta_tile_map(&maps.m[i][2], p.v, p.DV, a.Hv / p.vh, a.T, a.B, p.vs))
       return cudaErrorInvalidValue;
-    if (!p.out_f32 && !delta_tile_map(&maps.m[i][3], p.out, p.DV, a.Hv / p.oh, a.T, a.B, p.os)) return cudaErrorInvalidValue;
+    if (!delta_tile_map(&maps.m[i][3], p.out, p.DV, a.Hv / p.oh, a.T, a.B, p.os, p.out_f32)) return cudaErrorInvalidValue;
   }
   const int64_t items = (int64_t)a.np * a.B * a.Hv;
   cudaError_t e = cudaSuccess;
