@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(256) m3_lin_share_kernel(const __grid_constant
   const int per = a.Hk * a.D / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.tokens * per) return;
-  const int64_t tok = i / per;
+  const int64_t tok = a.tokens * per < ((int64_t)1 << 32) ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
   const int c = (int)(i % per) * 4, hk = c / a.D, k = c % a.D;
   const int which = blockIdx.y;
   const float* src = a.part[which] + ((size_t)tok * a.Hk * a.share + (size_t)hk * a.share) * a.D + k;

@@ -41,7 +41,7 @@ enum { F_REV = 1, F_TAKE = 2, F_GIVE = 4, F_FIRST = 8, F_LAST = 16 };
 
 // A step's factors (lam the head's decay, n the chunk's tokens)
 struct LinVec {
-  uint32_t fk[3][TC / 2];  // of a token's share in the next state, as three bf16 terms (pairs of tokens)
+  uint4 fk[TC / 2];        // of two tokens' shares in the next state, as three bf16 terms
   float fo[TC];            // of the start state in a token's output
   // of token j's share in token i's output: pz[0][64 + j - i], and one place
   // earlier in pz[1], so that the two of a pair of j lie on 8 bytes for every i
@@ -50,6 +50,7 @@ struct LinVec {
   float pad[3];
 };
 
+constexpr uint32_t TC_NEGATE_A = 1u << 13;  // in an MMA's instruction descriptor
 constexpr int GROUP = 256;             // threads on the state, on V', on the outputs
 constexpr int GW = GROUP / 32;
 constexpr int THREADS = 3 * GROUP + 128;  // and a warp each for the MMAs, the loads, the stores
@@ -165,13 +166,15 @@ __device__ __forceinline__ void lin_factors(const LinArgs& a, const LinInfo& t, 
     v.pz[1][TC - 1 + j] = after;
   }
   // f = f1 + f2 + f3 to f32's last bit
+  uint32_t term[3];
 #pragma unroll
   for (int m = 0; m < 3; ++m) {
     const __nv_bfloat162 f = __floats2bfloat162_rn(fk[0], fk[1]);
-    v.fk[m][lane] = *reinterpret_cast<const uint32_t*>(&f);
+    term[m] = *reinterpret_cast<const uint32_t*>(&f);
     fk[0] -= __low2float(f);
     fk[1] -= __high2float(f);
   }
+  v.fk[lane] = make_uint4(term[0], term[1], term[2], 0);
 }
 // The decay of a chunk of n tokens, rounded to f32 now up and now down so that
 // the product over a run's chunks stays within a rounding of the true one (`acc`
@@ -405,7 +408,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             for (int p = 0; p < 4; ++p)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4), tc_idesc(128, 128, false, true), p + ks > 0);
+                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
+                          tc_idesc(128, 128, false, true) | (p & 1 ? TC_NEGATE_A : 0u), p + ks > 0);
             tc_commit(&s.mbx[two(n)]);
             if (AGG) tc_commit(&s.empty[g.i]);
           }
@@ -541,9 +545,10 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n < walk.n; ++n, g.next()) {
-      // v f exactly, as terms: hi = v f1 rounded, its rest v f1 - hi (eight bits
-      // at most), v f2 rounded, and its rest with v f3.  Five packed bf16
-      // instructions for two values.  Made while the X before runs; written as
+      // v f exactly, as terms: hi = v f1 rounded, its rest hi - v f1 (eight bits
+      // at most, negated), v f2 rounded, and its rest with v f3 (negated; the
+      // MMAs of these two negate their A).  Five packed bf16 instructions for
+      // two values.  Made while the X before runs; written as
       // soon as that is done with the columns.
       uint32_t x[2][8], y[4][8];  // [half of the lanes][fragment], [term][fragment]
       wait(&s.full[g.i], g.par);
@@ -563,15 +568,16 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       auto terms = [&](int h) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const int at = hf * 16 + tb * 4 + (lane & 3);
-          const __nv_bfloat162 f1 = as_bf2(vec.fk[0][at]), f2 = as_bf2(vec.fk[1][at]), f3 = as_bf2(vec.fk[2][at]);
+          const uint4 f = vec.fk[hf * 16 + tb * 4 + (lane & 3)];
+          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y);
+          const __nv_bfloat162 n1 = as_bf2(f.x ^ 0x80008000u), n2 = as_bf2(f.y ^ 0x80008000u), n3 = as_bf2(f.z ^ 0x80008000u);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1), t = __hmul2_rn(v, f2);
             y[0][tb * 2 + i] = as_u32(hi);
-            y[1][tb * 2 + i] = as_u32(__hfma2(v, f1, __hneg2(hi)));
+            y[1][tb * 2 + i] = as_u32(__hfma2(v, n1, hi));
             y[2][tb * 2 + i] = as_u32(t);
-            y[3][tb * 2 + i] = as_u32(__hfma2(v, f3, __hfma2(v, f2, __hneg2(t))));
+            y[3][tb * 2 + i] = as_u32(__hfma2(v, n3, __hfma2(v, n2, t)));
           }
         }
       };
