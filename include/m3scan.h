@@ -622,7 +622,8 @@ typedef struct {
 
 typedef struct {
     int64_t workspace_bytes;     /* enough for both directions */
-    int64_t fwd_workspace_bytes; /* enough for m3scan_linattn_fwd */
+    int64_t fwd_workspace_bytes; /* enough for m3scan_linattn_fwd; 0: it may be NULL (such
+                                    a call reports to m3scan_device_status only) */
     int32_t fwd_launches, bwd_launches;
 } m3_linattn_plan;
 

@@ -764,6 +764,8 @@ def _scratch(workspace, nbytes, torch, dev):
     zero), and what must stay alive until the call is enqueued."""
     if workspace is not None:
         return workspace.ptr, workspace.nbytes, workspace
+    if nbytes == 0:
+        return None, 0, None
     buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     return buf.data_ptr(), nbytes, buf
 

@@ -47,19 +47,25 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
   return M3_OK;
 }
 
-// Time segments of the tensor-core kernels for few items.  With S segments the
-// ends of the first S - 1 are found first, chained, and then all run.
+// Time segments of the tensor-core kernels for few items.  A block per (item,
+// segment) takes a unit of time per chunk (1.25 us) and seven to come up and to
+// end; with S segments, first the ends of the S - 1 earlier ones are found (0.7
+// units per chunk), then a kernel chains them, then all S run.  The count with
+// the least total is taken, with at least three chunks per segment.  16 heads of
+// 1024 chunks: nine segments, 269 us, where one takes 1225, four 522, 19 282;
+// 12 of 256 (2 x 8192): six, 71 us, where one takes 168 and nine 98; 48 heads of
+// 32: three, 46 us, where one takes 52.
 void lin_segments(int64_t items, int nc, int* segs, int* seg_chunks) {
   constexpr int64_t SMS = 152;
   double best = 0.0;
   *segs = 1;
   *seg_chunks = nc < 1 ? 1 : nc;
-  for (int want = 1; want <= 152 && want * 4 <= (nc > 4 ? nc : 4); ++want) {
+  for (int want = 1; want <= 152 && want * 3 <= (nc > 3 ? nc : 3); ++want) {
     const int m = (nc + want - 1) / want;
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
-    const double fin = (double)((items * S + SMS - 1) / SMS) * (m + 3.0);
-    const double agg = S > 1 ? (double)((items * (S - 1) + SMS - 1) / SMS) * (m + 3.0) * 0.7 + 4.0 + 0.1 * S : 0.0;
+    const double fin = (double)((items * S + SMS - 1) / SMS) * (m + 7.0);
+    const double agg = S > 1 ? (double)((items * (S - 1) + SMS - 1) / SMS) * (m + 7.0) * 0.7 + 4.0 + 0.25 * S : 0.0;
     if (want == 1 || fin + agg < best - 1e-9) {
       best = fin + agg;
       *segs = S;
@@ -97,7 +103,7 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     w.o_start = take(w.stream || w.segs > 1 ? slots : 0);
     w.o_end = take(w.segs > 1 ? slots : 0);
     w.o_flags = take(w.stream ? (size_t)items * 4 : 0);
-    if (i == 0) p->fwd_ws_bytes = off;
+    if (i == 0) p->fwd_ws_bytes = off > align_up(STATUS_BYTES, 256) ? off : 0;  // (no more than a status block: none at all)
   }
   // the backward's: shares of dq and dk where key heads are shared, and a
   // copy of a state gradient that is to be overwritten
@@ -167,8 +173,10 @@ m3_status pass_state(const float* in, float* out, size_t bytes, cudaStream_t s) 
   return note(e) == cudaSuccess ? M3_OK : M3_ERR_CUDA;
 }
 
+// (none needed: NULL will do, and one that is given has its status block)
 m3_status check_workspace(const void* ws, size_t bytes, size_t need) {
-  if (!ws || bytes < need) return M3_ERR_WORKSPACE;
+  if (need == 0 && !ws) return M3_OK;
+  if (!ws || bytes < need || bytes < STATUS_BYTES) return M3_ERR_WORKSPACE;
   return aligned(ws, 256) ? M3_OK : M3_ERR_ALIGN;
 }
 

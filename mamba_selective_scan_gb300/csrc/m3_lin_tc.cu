@@ -749,15 +749,21 @@ __global__ void __launch_bounds__(256) m3_lin_seg_kernel(const __grid_constant__
       if (v + i < p.DV) x[i] = src[p.st ? (size_t)(v + i) * p.DK + k : (size_t)k * p.DV + v + i];
   }
   *reinterpret_cast<float4*>(start) = make_float4(x[0], x[1], x[2], x[3]);
-#pragma unroll 4
-  for (int s = 0; s + 1 < a.segs; ++s) {
-    const float4 e = *reinterpret_cast<const float4*>(end + s * slot);
-    const LinDecay d = s ? d1 : d0;
-    x[0] = fmaf(d.near, x[0], fmaf(d.off, x[0], e.x));
-    x[1] = fmaf(d.near, x[1], fmaf(d.off, x[1], e.y));
-    x[2] = fmaf(d.near, x[2], fmaf(d.off, x[2], e.z));
-    x[3] = fmaf(d.near, x[3], fmaf(d.off, x[3], e.w));
-    *reinterpret_cast<float4*>(start + (s + 1) * slot) = make_float4(x[0], x[1], x[2], x[3]);
+  for (int s0 = 0; s0 + 1 < a.segs; s0 += 8) {  // eight ends on their way at once
+    float4 e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s0 + i + 1 < a.segs) e[i] = *reinterpret_cast<const float4*>(end + (s0 + i) * slot);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i + 1 >= a.segs) break;
+      const LinDecay d = s0 + i ? d1 : d0;
+      x[0] = fmaf(d.near, x[0], fmaf(d.off, x[0], e[i].x));
+      x[1] = fmaf(d.near, x[1], fmaf(d.off, x[1], e[i].y));
+      x[2] = fmaf(d.near, x[2], fmaf(d.off, x[2], e[i].z));
+      x[3] = fmaf(d.near, x[3], fmaf(d.off, x[3], e[i].w));
+      *reinterpret_cast<float4*>(start + (s0 + i + 1) * slot) = make_float4(x[0], x[1], x[2], x[3]);
+    }
   }
 }
 

@@ -44,8 +44,13 @@ def _rot_plan(dims, act=BF16):
 @pytest.mark.parametrize("act", [BF16, F32])
 def test_linattn_plan(lib, act):
     st, p = _lin_plan(_lin(), act)
-    assert st == 0 and p.workspace_bytes >= p.fwd_workspace_bytes >= binding.STATUS_BYTES
-    assert p.fwd_launches >= 1 and p.bwd_launches >= 1
+    assert st == 0 and p.workspace_bytes >= binding.STATUS_BYTES and p.fwd_workspace_bytes == 0
+    assert p.fwd_launches == 1 and p.bwd_launches >= 1
+    # segments of a long sequence, shares of many heads
+    for kw in (dict(batch=1, seq_len=20000), dict(batch=100)):
+        st, p = _lin_plan(_lin(**kw), act)
+        assert st == 0 and p.workspace_bytes >= p.fwd_workspace_bytes
+        assert p.fwd_workspace_bytes > binding.STATUS_BYTES if act == BF16 else p.fwd_workspace_bytes == 0
     st, p = _lin_plan(_lin(seq_len=0), act)
     assert st == 0 and p.fwd_launches == 0 and p.bwd_launches == 0
     # sizes past 32 bits: the shares of shared heads' dq and dk
@@ -67,7 +72,7 @@ def test_linattn_refuses(lib, kw, status):
 def test_linattn_refuses_pointers(lib):
     assert _lin_plan(_lin(), act=5)[0] == 3
     assert lib.m3scan_linattn_plan(None, BF16, ctypes.byref(binding.M3LinattnPlan())) == 1
-    d, a = _lin(), 1 << 20
+    d, a = _lin(batch=1, seq_len=20000), 1 << 20
     ref = ctypes.byref(d)
     assert lib.m3scan_linattn_plan(ref, BF16, None) == 1
     assert lib.m3scan_linattn_fwd(ref, BF16, *([None] * 8), 0, None) == 1
