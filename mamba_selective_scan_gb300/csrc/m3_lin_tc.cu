@@ -82,8 +82,8 @@ constexpr uint32_t T_S = 0;     // S, bf16
 constexpr uint32_t T_X = 64;    // V'^T K
 constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_O = 256;   // V^T P^T
-constexpr uint32_t T_V = 320;   // V' in four terms of 32 columns
-constexpr uint32_t T_P = 448;   // Q K^T: row i in lane 32 (i / 16) + i % 16
+constexpr uint32_t T_V = 320;   // V' in three terms of 32 columns
+constexpr uint32_t T_P = 416;   // Q K^T: row i in lane 32 (i / 16) + i % 16
 // and where only the states are wanted: two of each, by step
 constexpr uint32_t A_X = 0, A_V = 256;
 
@@ -242,8 +242,8 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // registers: X needs no state, so the products of a chunk run under the
 // register work of the ones around it.
 //
-// V' enters as four bf16 terms that hold the product with f32's factor, so states are f32
-// sums of f32-grade products.  S and P enter the outputs' products as one: each
+// V' enters as three bf16 terms, 20 bits of the product with an f32 factor:
+// states come out at 7e-7.  S and P enter the outputs' products as one: each
 // rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; both come
 // to 2.3e-3 at most, their shares of the output being 1 together).
 //
@@ -272,6 +272,12 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   const unsigned np = (unsigned)a.np;
   const TcWalk walk(a.stream, (int64_t)a.B * a.Hv, a.nc, blockIdx.x / np, gridDim.x / np, seg, a.seg_chunks);
   const uint32_t st0 = smem_u32(base);
+  // a block's pass, and how many tiles of 64 its keys and its values are: of
+  // narrow heads the second ones are neither copied nor multiplied, and the
+  // warps whose rows or columns lie there only keep step
+  const int pass = (int)(blockIdx.x % np);
+  const int DK = a.p[pass].DK, DV = a.p[pass].DV;
+  const int nk = DK > 64 ? 2 : 1, nv = DV > 64 ? 2 : 1;
   constexpr int NST = AGG ? AGG_STAGES : STAGES, STB = AGG ? AGG_STAGE : STAGE;
   // X, V' and their barriers: one of each, or two in turns
   auto two = [](int n) { return AGG ? n & 1 : 0; };
@@ -349,12 +355,12 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             const uint32_t st = st0 + i * STB;
             const int hk = p.kh == 1 ? t.h : t.h / p.kh, hv = p.vh == 1 ? t.h : t.h / p.vh, hq = p.qh == 1 ? t.h : t.h / p.qh;
             uint64_t* bar = &s.full[i];
-            mbar_expect_tx(bar, AGG ? 4 * TILE : STAGE);
+            mbar_expect_tx(bar, (uint32_t)((AGG ? nk : 2 * nk) + nv) * TILE);
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
-              tma_tile(st + blk * (AGG ? 1 : 2) * TILE, &m[1], blk * 64, hk, t.tok, t.b, bar);
-              tma_tile(st + ((AGG ? 2 : 4) + blk) * TILE, &m[2], blk * 64, hv, t.tok, t.b, bar);
-              if (!AGG) tma_tile(st + blk * 2 * TILE + TILE, &m[0], blk * 64, hq, t.tok, t.b, bar);
+              if (blk < nk) tma_tile(st + blk * (AGG ? 1 : 2) * TILE, &m[1], blk * 64, hk, t.tok, t.b, bar);
+              if (blk < nv) tma_tile(st + ((AGG ? 2 : 4) + blk) * TILE, &m[2], blk * 64, hv, t.tok, t.b, bar);
+              if (!AGG && blk < nk) tma_tile(st + blk * 2 * TILE + TILE, &m[0], blk * 64, hq, t.tok, t.b, bar);
             }
           }
           s.info[n & 7] = t;
@@ -396,7 +402,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
               const int off = ((ks >> 2) * 2 * TILE + (ks & 3) * 32) >> 4;
-              tc_mma_ss(tm + T_P, qd + off, kd + off, tc_idesc(64, 64, false, false), ks > 0);
+              if (ks < 4 * nk) tc_mma_ss(tm + T_P, qd + off, kd + off, tc_idesc(64, 64, false, false), ks > 0);
             }
             tc_commit(&s.mbp);
           }
@@ -405,11 +411,11 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 3; ++p)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
-                          tc_idesc(128, 128, false, true) | (p & 1 ? TC_NEGATE_A : 0u), p + ks > 0);
+                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? TC_NEGATE_A : 0u), p + ks > 0);
             tc_commit(&s.mbx[two(n)]);
             if (AGG) tc_commit(&s.empty[g.i]);
           }
@@ -420,7 +426,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              tc_mma_ts(tm + T_Q, tm + T_S + ks * 8, qd + (((ks >> 2) * 2 * TILE + (ks & 3) * 32) >> 4), tc_idesc(128, 64, false, false), ks > 0);
+              if (ks < 4 * nk) tc_mma_ts(tm + T_Q, tm + T_S + ks * 8, qd + (((ks >> 2) * 2 * TILE + (ks & 3) * 32) >> 4), tc_idesc(128, 64, false, false), ks > 0);
             tc_commit(&s.mbq);
           }
           wait(&s.rdy_p, par);                     // P is in shared memory
@@ -439,6 +445,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   } else if (warp < GW) {  // the state
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RA));
     const int hf = warp >> 2, row = quad * 32 + lane;  // half of the keys; the row: a value
+    const bool idle = hf >= nk || (int)quad * 32 >= DV;
     float2 S[32];  // S^T[row][64 hf + k]
 
     grid_dep_wait();  // the segments' states, too
@@ -450,6 +457,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
         wait(&s.mbx[two(n - 1)], two_par(n - 1));
         tmem_fence_after_sync();
+        if (!idle)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           float2 x[8];
@@ -528,6 +536,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         wait(&s.mbq, (n - 1) & 1);  // the last state is read
         tmem_fence_after_sync();
       }
+      if (!idle)
 #pragma unroll
       for (int p = 0; p < 4; ++p) {  // S into tensor memory
         uint32_t x[8];
@@ -540,21 +549,23 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   } else if (warp < 2 * GW) {  // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RC));
     const int hf = (warp >> 2) & 1, row = quad * 32 + lane;  // half of the tokens
+    const bool idle = (int)quad * 32 >= DV;
     const uint32_t vl = st0 + (AGG ? 2 : 4) * TILE + (quad >> 1) * TILE;
     const uint32_t el = sw(hf * 32 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
     LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n < walk.n; ++n, g.next()) {
-      // v f exactly, as terms: hi = v f1 rounded, its rest hi - v f1 (eight bits
-      // at most, negated), v f2 rounded, and its rest with v f3 (negated; the
-      // MMAs of these two negate their A).  Five packed bf16 instructions for
-      // two values.  Made while the X before runs; written as
-      // soon as that is done with the columns.
-      uint32_t x[2][8], y[4][8];  // [half of the lanes][fragment], [term][fragment]
+      // v f in three terms: hi = v f1 rounded, its rest hi - v f1 (exact, eight
+      // bits at most; negated, as is the A of its MMAs), and v f2 + v f3
+      // rounded, whose error is 2^-9 of 2^-9 at most: 7e-7 in the 2-norm.  Four
+      // packed bf16 instructions for two values.  Made while the X before runs;
+      // written as soon as that is done with the columns.
+      uint32_t x[2][8], y[3][8];  // [half of the lanes][fragment], [term][fragment]
       wait(&s.full[g.i], g.par);
       const uint32_t vt = vl + g.i * STB;
       const LinVec& vec = s.vec[n & 7];
       __nv_bfloat162 chk = as_bf2(0);
+      if (!idle)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -569,19 +580,17 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
           const uint4 f = vec.fk[hf * 16 + tb * 4 + (lane & 3)];
-          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y);
-          const __nv_bfloat162 n1 = as_bf2(f.x ^ 0x80008000u), n2 = as_bf2(f.y ^ 0x80008000u), n3 = as_bf2(f.z ^ 0x80008000u);
+          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y), f3 = as_bf2(f.z), n1 = as_bf2(f.x ^ 0x80008000u);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1), t = __hmul2_rn(v, f2);
+            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1);
             y[0][tb * 2 + i] = as_u32(hi);
             y[1][tb * 2 + i] = as_u32(__hfma2(v, n1, hi));
-            y[2][tb * 2 + i] = as_u32(t);
-            y[3][tb * 2 + i] = as_u32(__hfma2(v, n3, __hfma2(v, n2, t)));
+            y[2][tb * 2 + i] = as_u32(__hfma2(v, f2, __hmul2_rn(v, f3)));
           }
         }
       };
-      terms(0);
+      if (!idle) terms(0);
       if (__any_sync(~0u, (as_u32(chk) & 0x7FFF7FFFu) != 0)) {
         const bool rev = s.info[n & 7].flags & F_REV;
 #pragma unroll 1
@@ -601,11 +610,12 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         wait(&s.mbx[two(n)], two_par(n) ^ 1);
         tmem_fence_after_sync();
       }
+      if (!idle)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (h) terms(1);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
+        for (int m = 0; m < 3; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
       }
       ready(&s.rdy_v[two(n)]);
     }
@@ -614,6 +624,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     if constexpr (!AGG) {
     const int hf = (warp >> 2) & 1;  // half of the tokens (of P: of its columns)
     const int i0 = quad * 16, j0 = hf * 32;
+    const bool idle = (int)quad * 32 >= DV;  // (P's rows are tokens: no warp is idle there)
     const int pz_at = TC + j0 + 2 * (lane & 3) - i0 - (lane >> 2) - ((lane >> 2) & 1);  // (even)
     // where this thread's first value goes: bf16 (rows of 64 values), f32 (of 32)
     const uint32_t op32 = st0 + OUT + quad * TILE + sw(j0 + 2 * (lane & 3), lane >> 4) + ((lane >> 2) & 3) * 4;
@@ -630,6 +641,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         for (int tb = 0; tb < 4; ++tb) f[tb] = *reinterpret_cast<const float2*>(fo + tb * 8);
         wait(&s.mbo, m & 1);  // (and S Q^T, which was issued before)
         tmem_fence_after_sync();
+        if (!idle)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float2 q[8];
@@ -640,7 +652,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
           for (int c = 0; c < 8; ++c) o[h][c] = __ffma2_rn(f[c >> 1], q[c], o[h][c]);
         }
-        if (s.any_bad[m & 3] == (unsigned)n) {
+        if (!idle && s.any_bad[m & 3] == (unsigned)n) {
           const bool rev = s.info[m & 7].flags & F_REV;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -697,7 +709,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         if (n > 1) wait(&s.o_free, n & 1);
         const LinInfo& t = s.info[(n - 1) & 7];
         const LinPass& p = a.p[t.pass];
-        if (p.out_f32) {
+        if (idle) {
+        } else if (p.out_f32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
