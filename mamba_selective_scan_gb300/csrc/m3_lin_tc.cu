@@ -316,6 +316,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   // 128 is what the block was launched with
   constexpr int LAUNCHED = 65536 / THREADS / 8 * 8, RA = 88, RB = 72, RC = 72, RM = 40;
   static_assert((RA + RB + RC) * GROUP + RM * 128 <= LAUNCHED * THREADS, "registers of the block");
+  static_assert(RA >= LAUNCHED && RB <= LAUNCHED && RC <= LAUNCHED && RM <= LAUNCHED, "inc only raises, dec only lowers");
   if (warp >= 3 * GW) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RM));
     if (warp == 3 * GW + 2) {  // stores
