@@ -82,8 +82,8 @@ constexpr uint32_t T_S = 0;     // S, bf16
 constexpr uint32_t T_X = 64;    // V'^T K
 constexpr uint32_t T_Q = 192;   // S Q^T
 constexpr uint32_t T_O = 256;   // V^T P^T
-constexpr uint32_t T_V = 320;   // V' in three terms of 32 columns
-constexpr uint32_t T_P = 416;   // Q K^T: row i in lane 32 (i / 16) + i % 16
+constexpr uint32_t T_V = 320;   // V' in four terms of 32 columns
+constexpr uint32_t T_P = 448;   // Q K^T: row i in lane 32 (i / 16) + i % 16
 // and where only the states are wanted: two of each, by step
 constexpr uint32_t A_X = 0, A_V = 256;
 
@@ -242,8 +242,8 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // registers: X needs no state, so the products of a chunk run under the
 // register work of the ones around it.
 //
-// V' enters as three bf16 terms, 20 bits of the product with an f32 factor:
-// states come out at 7e-7.  S and P enter the outputs' products as one: each
+// V' enters as four bf16 terms that hold its product with an f32 factor, so
+// states are f32 sums of f32-grade products.  S and P enter the outputs' products as one: each
 // rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; both come
 // to 2.3e-3 at most, their shares of the output being 1 together).
 //
@@ -412,7 +412,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
@@ -556,12 +556,14 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n < walk.n; ++n, g.next()) {
-      // v f in three terms: hi = v f1 rounded, its rest hi - v f1 (exact, eight
-      // bits at most; negated, as is the A of its MMAs), and v f2 + v f3
-      // rounded, whose error is 2^-9 of 2^-9 at most: 7e-7 in the 2-norm.  Four
-      // packed bf16 instructions for two values.  Made while the X before runs;
-      // written as soon as that is done with the columns.
-      uint32_t x[2][8], y[3][8];  // [half of the lanes][fragment], [term][fragment]
+      // v f to f32's grade, as terms: hi = v f1 rounded, its rest hi - v f1
+      // (exact, eight bits at most; negated), v f2 rounded, and its rest with
+      // v f3 (negated: the MMAs of these two negate their A).  Five packed bf16
+      // instructions for two values, where three terms cut from the f32 product
+      // take twelve.  (Three terms of this kind are 4 % faster, and 2e-6 off.)
+      // Made while the X before runs; written as soon as that is done with the
+      // columns.
+      uint32_t x[2][8], y[4][8];  // [half of the lanes][fragment], [term][fragment]
       wait(&s.full[g.i], g.par);
       const uint32_t vt = vl + g.i * STB;
       const LinVec& vec = s.vec[n & 7];
@@ -581,13 +583,15 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
           const uint4 f = vec.fk[hf * 16 + tb * 4 + (lane & 3)];
-          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y), f3 = as_bf2(f.z), n1 = as_bf2(f.x ^ 0x80008000u);
+          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y), n1 = as_bf2(f.x ^ 0x80008000u);
+          const __nv_bfloat162 n2 = as_bf2(f.y ^ 0x80008000u), n3 = as_bf2(f.z ^ 0x80008000u);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1);
+            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1), t = __hmul2_rn(v, f2);
             y[0][tb * 2 + i] = as_u32(hi);
             y[1][tb * 2 + i] = as_u32(__hfma2(v, n1, hi));
-            y[2][tb * 2 + i] = as_u32(__hfma2(v, f2, __hmul2_rn(v, f3)));
+            y[2][tb * 2 + i] = as_u32(t);
+            y[3][tb * 2 + i] = as_u32(__hfma2(v, n3, __hfma2(v, n2, t)));
           }
         }
       };
@@ -616,7 +620,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       for (int h = 0; h < 2; ++h) {
         if (h) terms(1);
 #pragma unroll
-        for (int m = 0; m < 3; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
+        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
       }
       ready(&s.rdy_v[two(n)]);
     }
