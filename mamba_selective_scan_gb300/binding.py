@@ -1020,7 +1020,8 @@ def _qkrot_sizes(code, qshape, kshape, rot, strides, position_stride, eps, inter
     if len(qshape) != 4 or len(kshape) != 4 or qshape[:2] != kshape[:2] or qshape[3] != kshape[3]:
         raise ValueError(f"q and k must be [batch, seq_len, heads, head size], got {tuple(qshape)}, {tuple(kshape)}")
     B, T, Hq, D = qshape
-    dims = M3QkrotDims(B, T, Hq, kshape[2], D, rot, *strides, position_stride, eps, interleaved, accumulate, 0)
+    dims = M3QkrotDims(B, T, Hq, kshape[2], D, rot, *strides, position_stride, float(eps), int(bool(interleaved)),
+                       int(bool(accumulate)), 0)
     return ctypes.byref(dims), m3scan_qkrot_plan(dims, code).workspace_bytes
 
 
@@ -1033,6 +1034,8 @@ def _qkrot_positions(positions, B, T, index, torch):
     if positions.get_device() != index:
         raise ValueError(f"positions is on {positions.device}, expected cuda:{index}")
     shape = positions.shape
+    if shape == (B, T) and positions.is_contiguous():
+        return positions.data_ptr(), T if B > 1 else 0
     if shape == (T,):
         batch = 0
     elif shape == (B, T):
@@ -1046,9 +1049,17 @@ def _qkrot_positions(positions, B, T, index, torch):
     return positions.data_ptr(), batch
 
 
+def _tokens_of(t, name, dtype, index, shape):
+    """``_token_stride``, at once for the dense tensors that most are."""
+    if t.is_contiguous() and t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        return 0
+    return _token_stride(t, name, dtype, index, shape)
+
+
 def _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch):
-    """Checks the inputs; returns (dtype code, device index, token strides of q
-    and k, address and batch stride of the positions, rotated size)."""
+    """Checks the inputs; returns (dtype code, device index, q's and k's
+    shapes, token strides of q and k, address and batch stride of the
+    positions, rotated size)."""
     dt, index, qshape, kshape = q.dtype, q.get_device(), q.shape, k.shape
     code = _act_code(q)
     if index < 0:
@@ -1056,19 +1067,19 @@ def _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch):
     if len(qshape) != 4 or len(kshape) != 4:
         raise ValueError(f"q and k must be [batch, seq_len, heads, head size], got {tuple(qshape)}, {tuple(kshape)}")
     B, T, _, D = qshape
-    sq = _token_stride(q, "q", dt, index, qshape)
-    sk = _token_stride(k, "k", dt, index, (B, T, kshape[2], D))
+    sq = _tokens_of(q, "q", dt, index, qshape)
+    sk = _tokens_of(k, "k", dt, index, (B, T, kshape[2], D))
     f32 = torch.float32
     _need(q_weight, "q_weight", f32, index, (D,))
     _need(k_weight, "k_weight", f32, index, (D,))
     rot = 0
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", f32, index, (inv_freq.numel(),))
         rot = 2 * inv_freq.numel()
+        _need(inv_freq, "inv_freq", f32, index, (rot // 2,))
         if rot and positions is None:
             raise ValueError("positions are needed where inv_freq is given")
     pos, pos_stride = _qkrot_positions(positions, B, T, index, torch)
-    return code, index, sq, sk, pos, pos_stride, rot
+    return code, index, qshape, kshape, sq, sk, pos, pos_stride, rot
 
 
 @_placed
@@ -1081,18 +1092,17 @@ def m3scan_qkrot_fwd(q, k, q_weight, k_weight, positions, inv_freq, *, eps=1e-6,
     or neighbours with ``interleaved``.  Returns (q_out, k_out), which may be q
     and k themselves."""
     torch = _TORCH or _torch()
-    code, index, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
-    dt, qshape, kshape = q.dtype, q.shape, k.shape
+    code, index, qshape, kshape, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
+    dt, sqo, sko = q.dtype, 0, 0
     if q_out is None:
-        q_out, sqo = torch.empty(qshape, dtype=dt, device=q.device), 0
+        q_out = torch.empty(qshape, dtype=dt, device=q.device)
     else:
-        sqo = _token_stride(q_out, "q_out", dt, index, qshape)
+        sqo = _tokens_of(q_out, "q_out", dt, index, qshape)
     if k_out is None:
-        k_out, sko = torch.empty(kshape, dtype=dt, device=q.device), 0
+        k_out = torch.empty(kshape, dtype=dt, device=q.device)
     else:
-        sko = _token_stride(k_out, "k_out", dt, index, kshape)
-    dims, _ = _qkrot_sizes(code, qshape, kshape, rot, (sq, sk, sqo, sko, 0, 0, 0, 0), pos_stride, float(eps),
-                           int(bool(interleaved)), 0)
+        sko = _tokens_of(k_out, "k_out", dt, index, kshape)
+    dims, _ = _qkrot_sizes(code, qshape, kshape, rot, (sq, sk, sqo, sko, 0, 0, 0, 0), pos_stride, eps, interleaved, False)
     st = _LIB.m3scan_qkrot_fwd(dims, code, q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), pos,
                                _ptr(inv_freq), q_out.data_ptr(), k_out.data_ptr(), _stream_of(stream, index))
     if st:
@@ -1109,30 +1119,37 @@ def m3scan_qkrot_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
     and dk_out themselves) and d_q_weight, d_k_weight (f32 [D]; None for a
     weight that is None)."""
     torch = _TORCH or _torch()
-    code, index, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
-    dt, dev, f32, D = q.dtype, q.device, torch.float32, q.shape[3]
+    code, index, qshape, kshape, sq, sk, pos, pos_stride, rot = _qkrot_inputs(q, k, q_weight, k_weight, positions, inv_freq, torch)
+    dt, dev, f32, D = q.dtype, q.device, torch.float32, qshape[3]
     o = dict(out) if out else {}
-    strides = []
-    for n, t in (("dq", q), ("dk", k)):
-        if o.get(n) is None:
-            o[n] = torch.empty(t.shape, dtype=dt, device=dev)
-        strides.append(_token_stride(o[n], n, dt, index, t.shape))
-    strides += [_token_stride(dq_out, "dq_out", dt, index, q.shape), _token_stride(dk_out, "dk_out", dt, index, k.shape)]
+    dq, dk, dwq, dwk = o.get("dq"), o.get("dk"), o.get("d_q_weight"), o.get("d_k_weight")
+    sdq = sdk = 0
+    if dq is None:
+        dq = torch.empty(qshape, dtype=dt, device=dev)
+    else:
+        sdq = _tokens_of(dq, "dq", dt, index, qshape)
+    if dk is None:
+        dk = torch.empty(kshape, dtype=dt, device=dev)
+    else:
+        sdk = _tokens_of(dk, "dk", dt, index, kshape)
     new = torch.zeros if accumulate_param_grads else torch.empty
-    for n, w in (("d_q_weight", q_weight), ("d_k_weight", k_weight)):
-        if o.get(n) is None:
-            o[n] = None if w is None else new(D, dtype=f32, device=dev)
-        else:
-            _need(o[n], n, f32, index, (D,))
-    dims, nbytes = _qkrot_sizes(code, q.shape, k.shape, rot, (sq, sk, 0, 0, *strides), pos_stride, float(eps),
-                                int(bool(interleaved)), int(bool(accumulate_param_grads)))
+    if dwq is not None:
+        _need(dwq, "d_q_weight", f32, index, (D,))
+    elif q_weight is not None:
+        dwq = new(D, dtype=f32, device=dev)
+    if dwk is not None:
+        _need(dwk, "d_k_weight", f32, index, (D,))
+    elif k_weight is not None:
+        dwk = new(D, dtype=f32, device=dev)
+    strides = (sq, sk, 0, 0, sdq, sdk, _tokens_of(dq_out, "dq_out", dt, index, qshape), _tokens_of(dk_out, "dk_out", dt, index, kshape))
+    dims, nbytes = _qkrot_sizes(code, qshape, kshape, rot, strides, pos_stride, eps, interleaved, accumulate_param_grads)
     ws, nbytes, _keep = _scratch(workspace, nbytes, torch, dev)
     st = _LIB.m3scan_qkrot_bwd(dims, code, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), k.data_ptr(),
-                               _ptr(q_weight), _ptr(k_weight), pos, _ptr(inv_freq), o["dq"].data_ptr(),
-                               o["dk"].data_ptr(), _ptr(o["d_q_weight"]), _ptr(o["d_k_weight"]), ws, nbytes,
-                               _stream_of(stream, index))
+                               _ptr(q_weight), _ptr(k_weight), pos, _ptr(inv_freq), dq.data_ptr(), dk.data_ptr(),
+                               _ptr(dwq), _ptr(dwk), ws, nbytes, _stream_of(stream, index))
     if st:
         raise M3Error(st, "m3scan_qkrot_bwd")
+    o.update(dq=dq, dk=dk, d_q_weight=dwq, d_k_weight=dwk)
     return o
 
 
@@ -1175,8 +1192,8 @@ def _linattn_inputs(q, k, v, log_decay, torch):
             and q.shape == kshape and q.get_device() == index and k.get_device() == index):
         return code, index, kshape, vshape, 0, 0, 0
     kwant = (*vshape[:2], *kshape[2:])
-    return (code, index, kshape, vshape, _token_stride(q, "q", dt, index, kwant), _token_stride(k, "k", dt, index, kwant),
-            _token_stride(v, "v", dt, index, vshape))
+    return (code, index, kshape, vshape, _tokens_of(q, "q", dt, index, kwant), _tokens_of(k, "k", dt, index, kwant),
+            _tokens_of(v, "v", dt, index, vshape))
 
 
 @_placed
@@ -1215,24 +1232,35 @@ def m3scan_linattn_bwd(q, k, v, log_decay, d_o, *, state=None, d_state_out=None,
     dev, dt, f32 = v.device, v.dtype, torch.float32
     code, index, kshape, vshape, sq, sk, sv = _linattn_inputs(q, k, v, log_decay, torch)
     r = dict(out) if out else {}
-    strides = []
-    for n, t in (("dq", q), ("dk", k), ("dv", v)):
-        if r.get(n) is None:
-            r[n] = torch.empty(t.shape, dtype=dt, device=dev)
-        strides.append(_token_stride(r[n], n, dt, index, t.shape))
-    dims, sshape, nbytes = _linattn_sizes(code, kshape, vshape, (sq, sk, sv, *strides), scale)
-    if r.get("d_state") is None:
-        r["d_state"] = torch.empty(sshape, dtype=f32, device=dev) if want_d_state else None
+    dq, dk, d_v, d_state = r.get("dq"), r.get("dk"), r.get("dv"), r.get("d_state")
+    sdq = sdk = sdv = 0
+    if dq is None:
+        dq = torch.empty(kshape, dtype=dt, device=dev)
+    else:
+        sdq = _tokens_of(dq, "dq", dt, index, kshape)
+    if dk is None:
+        dk = torch.empty(kshape, dtype=dt, device=dev)
+    else:
+        sdk = _tokens_of(dk, "dk", dt, index, kshape)
+    if d_v is None:
+        d_v = torch.empty(vshape, dtype=dt, device=dev)
+    else:
+        sdv = _tokens_of(d_v, "dv", dt, index, vshape)
+    dims, sshape, nbytes = _linattn_sizes(code, kshape, vshape, (sq, sk, sv, sdq, sdk, sdv), scale)
+    if d_state is not None:
+        _need(d_state, "d_state", f32, index, sshape)
+    elif want_d_state:
+        d_state = torch.empty(sshape, dtype=f32, device=dev)
     _need(state, "state", f32, index, sshape)
     _need(d_state_out, "d_state_out", f32, index, sshape)
-    _need(r["d_state"], "d_state", f32, index, sshape)
     _need(d_o, "d_o", dt, index, vshape)
     ws, nbytes, _keep = _scratch(workspace, nbytes[1], torch, dev)
     st = _LIB.m3scan_linattn_bwd(dims, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(state),
-                                 d_o.data_ptr(), _ptr(d_state_out), r["dq"].data_ptr(), r["dk"].data_ptr(),
-                                 r["dv"].data_ptr(), _ptr(r["d_state"]), ws, nbytes, _stream_of(stream, index))
+                                 d_o.data_ptr(), _ptr(d_state_out), dq.data_ptr(), dk.data_ptr(), d_v.data_ptr(),
+                                 _ptr(d_state), ws, nbytes, _stream_of(stream, index))
     if st:
         raise M3Error(st, "m3scan_linattn_bwd")
+    r.update(dq=dq, dk=dk, dv=d_v, d_state=d_state)
     return r
 
 

@@ -44,14 +44,13 @@ struct LinArgs {
   int np, B, T, Hv;
   float scale;
   unsigned* status;
-  // the tensor-core kernels'
   int nc;                // chunks of a sequence
-  bool stream;           // equal shares of all items' chunks, one block per SM
+  bool stream;           // tensor-core kernels: equal shares of all items' chunks, one block per SM
   unsigned* flags;       // stream: per item, set once its state was handed over (in seg_start)
   int segs, seg_chunks;  // else: time segments, chunks per segment
   float *seg_end, *seg_start;  // [items][segs][128][128]: ends from a zero start, start states
 };
-constexpr int LIN_C = 64;  // tokens per chunk of the tensor-core kernels
+constexpr int LIN_C = 64;  // tokens per chunk
 
 // (a comparison, not fmaxf: a decay that is NaN stays one)
 __device__ __forceinline__ float lin_ld(float x) { return x < LIN_LD_MIN ? LIN_LD_MIN : x; }
@@ -69,7 +68,9 @@ __device__ __forceinline__ LinDecay lin_decay(float ld, int n) {
 }
 
 // Token after token, any type and length: m3_lin_rec.cu
-template <typename T> cudaError_t launch_lin_rec(const LinArgs& a, cudaStream_t st, int sms);
+template <typename T> cudaError_t launch_lin_rec(LinArgs a, cudaStream_t st, int sms);
+// The start states of time segments from the ends that the kernel before left: m3_lin_tc.cu
+cudaError_t launch_lin_seg(const LinArgs& a, cudaStream_t st);
 
 // bf16, chunks of 64 on the tensor cores: m3_lin_tc.cu
 cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms);

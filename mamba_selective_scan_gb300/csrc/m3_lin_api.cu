@@ -55,19 +55,23 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 // 1024 chunks: nine segments, 269 us, where one takes 1225, four 522, 19 282;
 // 12 of 256 (2 x 8192): six, 71 us, where one takes 168 and nine 98; 48 heads of
 // 32: three, 46 us, where one takes 52.
-void lin_segments(int64_t items, int nc, int* segs, int* seg_chunks) {
-  constexpr int64_t SMS = 152;
+// f32: a unit is 64 tokens of the sequential kernel (13 us), four blocks of 32
+// columns per item, two blocks per SM.
+void lin_segments(int64_t items, int nc, bool tc, int* segs, int* seg_chunks) {
+  const int64_t at_once = tc ? 152 : 76;
+  const double up = tc ? 7.0 : 0.3, agg = tc ? 0.7 : 0.6, chain = tc ? 4.0 : 0.6, link = tc ? 0.25 : 0.03;
+  const int least = tc ? 3 : 1;
   double best = 0.0;
   *segs = 1;
   *seg_chunks = nc < 1 ? 1 : nc;
-  for (int want = 1; want <= 152 && want * 3 <= (nc > 3 ? nc : 3); ++want) {
+  for (int want = 1; want <= 152 && want * least <= (nc > least ? nc : least); ++want) {
     const int m = (nc + want - 1) / want;
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
-    const double fin = (double)((items * S + SMS - 1) / SMS) * (m + 7.0);
-    const double agg = S > 1 ? (double)((items * (S - 1) + SMS - 1) / SMS) * (m + 7.0) * 0.7 + 4.0 + 0.25 * S : 0.0;
-    if (want == 1 || fin + agg < best - 1e-9) {
-      best = fin + agg;
+    const double all = (double)((items * S + at_once - 1) / at_once) * (m + up);
+    const double ends = S > 1 ? (double)((items * (S - 1) + at_once - 1) / at_once) * (m + up) * agg + chain + link * S : 0.0;
+    if (want == 1 || all + ends < best - 1e-9) {
+      best = all + ends;
       *segs = S;
       *seg_chunks = m;
     }
@@ -96,9 +100,7 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     w.segs = 1;
     w.seg_chunks = p->nc;
     w.stream = p->tc && items > 152;
-    if (p->tc && !w.stream) {
-      lin_segments(items, p->nc, &w.segs, &w.seg_chunks);
-    }
+    if (!w.stream && p->T > 1) lin_segments(items, p->nc, p->tc, &w.segs, &w.seg_chunks);
     const size_t slots = (size_t)items * w.segs * LIN_DMAX * LIN_DMAX * 4;
     w.o_start = take(w.stream || w.segs > 1 ? slots : 0);
     w.o_end = take(w.segs > 1 ? slots : 0);
@@ -144,17 +146,17 @@ cudaError_t lin_launch(LinArgs a, const LinPlan& p, m3_dtype act, void* workspac
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if (p.tc) {
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    const LinPlan::Walk& w = p.walk[a.np > 1];
-    a.status = static_cast<unsigned*>(workspace);
-    a.nc = p.nc;
-    a.stream = w.stream; a.segs = w.segs; a.seg_chunks = w.seg_chunks;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const LinPlan::Walk& w = p.walk[a.np > 1];
+  a.status = static_cast<unsigned*>(workspace);
+  a.nc = p.nc;
+  a.stream = w.stream; a.segs = w.segs; a.seg_chunks = w.seg_chunks;
+  if (ws) {
     a.seg_start = reinterpret_cast<float*>(ws + w.o_start);
     a.seg_end = reinterpret_cast<float*>(ws + w.o_end);
     a.flags = reinterpret_cast<unsigned*>(ws + w.o_flags);
-    return launch_lin_tc(a, s, sms);
   }
+  if (p.tc) return launch_lin_tc(a, s, sms);
   return act == M3_BF16 ? launch_lin_rec<__nv_bfloat16>(a, s, sms) : launch_lin_rec<float>(a, s, sms);
 }
 

@@ -71,11 +71,11 @@ __global__ void __launch_bounds__(256, 2) m3_lin_step_kernel(const __grid_consta
   }
 }
 
-// A sequence: 32 columns of one head's state per block, eight lanes to a
-// column (a lane has rows 4 s .. 4 s + 3 of every 32).  16 tokens at a time are
-// brought into shared memory, the next 16 in flight meanwhile.  Within those
-// 16 the state that they start from stays as it is and what they add grows
-// beside it from zero,
+// A sequence: 32 COLS columns of one head's state per block, eight lanes to
+// COLS neighbouring columns (a lane has rows 4 s .. 4 s + 3 of every 32).  16
+// tokens at a time are brought into shared memory, the next 16 in flight
+// meanwhile.  Within those 16 the state that they start from stays as it is and
+// what they add grows beside it from zero,
 //
 //   o_i = scale (lam^{i+1} S0^T q_i + L_i^T q_i),  L_i = lam L_{i-1} + k_i v_i^T
 //
@@ -83,9 +83,18 @@ __global__ void __launch_bounds__(256, 2) m3_lin_step_kernel(const __grid_consta
 // in 16 tokens: with a state that hardly fades, roundings that all fall the
 // same way added up to 3e-5 over 16384 tokens.  The outputs of eight tokens
 // are summed over the lanes at once (seven shuffles instead of 24).
-template <typename T>
-__global__ void __launch_bounds__(256) m3_lin_seq_kernel(const __grid_constant__ LinArgs a) {
-  constexpr int NT = 16, TV = 32;
+//
+// With every SM at work shared memory is the bound: a lane reads its 16 rows'
+// k and q of every token, 128 bytes, 32 wavefronts a warp whatever the lanes
+// share.  A second column per lane halves that (8 x 512 x 16 heads, training
+// pass: 1.05 instead of 1.34 ms); with few blocks the latency of a token counts,
+// 0.2 us with one column, 0.35 with two.
+//
+// blockIdx.z: time segments, from the chaining's start states.  AGG: only the
+// states, each segment's end from a zero start.
+template <typename T, int COLS, bool AGG>
+__global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constant__ LinArgs a) {
+  constexpr int NT = 16, TV = 32 * COLS;
   __shared__ __align__(16) float kq[2][NT][LIN_DMAX];  // k, q
   __shared__ float vs[NT][TV], os[NT][TV + 1];
   __shared__ float pw[NT];  // the start state's weight in each token's output
@@ -95,127 +104,183 @@ __global__ void __launch_bounds__(256) m3_lin_seq_kernel(const __grid_constant__
   const int bh = blockIdx.x / MAX_TILES, v0 = (blockIdx.x % MAX_TILES) * TV;
   if (v0 >= p.DV) return;
   const int b = bh / a.Hv, h = bh % a.Hv;
-  const int s = lane & 7, col = warp * 4 + (lane >> 3);
-  const bool vok = v0 + col < p.DV;
+  const int s = lane & 7, col = (warp * 4 + (lane >> 3)) * COLS;
+  // this segment's tokens, in the pass's order
+  const int seg = blockIdx.z, seg_tok = a.seg_chunks * LIN_C, odd = p.rev ? a.nc * LIN_C - a.T : 0;
+  const int first = seg ? seg * seg_tok - odd : 0, last = seg + 1 < a.segs ? (seg + 1) * seg_tok - odd : a.T;
+  const size_t slot = ((size_t)(bh * a.np + blockIdx.y) * a.segs + seg) * LIN_DMAX * LIN_DMAX + v0 + col;  // row k: + k LIN_DMAX
   const size_t sbase = (size_t)bh * p.DK * p.DV;
-  auto where = [&](int k) { return p.st ? sbase + (size_t)(v0 + col) * p.DK + k : sbase + (size_t)k * p.DV + v0 + col; };
+  auto where = [&](int k, int c) { return p.st ? sbase + (size_t)(v0 + col + c) * p.DK + k : sbase + (size_t)k * p.DV + v0 + col + c; };
   auto row = [&](int i) { return (i >> 2) * 32 + s * 4 + (i & 3); };
 
-  float2 S[8], L[8];  // rows row(2 i), row(2 i + 1)
+  float2 S[COLS][8], L[COLS][8];  // rows row(2 i), row(2 i + 1)
+  grid_dep_wait();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int k = row(i);
-    (i & 1 ? S[i >> 1].y : S[i >> 1].x) = p.s_in && vok && k < p.DK ? p.s_in[where(k)] : 0.0f;
-  }
+  for (int c = 0; c < COLS; ++c)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int k = row(i);
+      float x = 0.0f;
+      if (!AGG && v0 + col + c < p.DV && k < p.DK) {
+        if (a.segs > 1) x = a.seg_start[slot + (size_t)k * LIN_DMAX + c];
+        else if (p.s_in) x = p.s_in[where(k, c)];
+      }
+      (i & 1 ? S[c][i >> 1].y : S[c][i >> 1].x) = x;
+    }
   const float ld = lin_ld(a.ld[h]);
   const float fv = p.rev ? a.scale : 1.0f, fo = p.rev ? 1.0f : a.scale;
   if (tid < NT) pw[tid] = expf(ld * (float)(p.rev ? tid : tid + 1));
   const float2 lam = f2b(expf(ld));
   const int64_t tok0 = (int64_t)b * a.T;
-  const int c = tid & (LIN_DMAX - 1), which = tid >> 7;  // this thread brings column c of k (0) or q (1)
+  const int c0 = tid & (LIN_DMAX - 1), which = tid >> 7;  // this thread brings column c0 of k (0) or q (1)
   const int64_t xs = which ? p.qs : p.ks;
-  const T* xp = static_cast<const T*>(which ? p.q : p.k) + tok0 * xs + (int64_t)(h / (which ? p.qh : p.kh)) * p.DK + c;
+  const T* xp = static_cast<const T*>(which ? p.q : p.k) + tok0 * xs + (int64_t)(h / (which ? p.qh : p.kh)) * p.DK + c0;
   const T* vp = static_cast<const T*>(p.v) + tok0 * p.vs + (int64_t)(h / p.vh) * p.DV + v0;
   const size_t ob = (size_t)tok0 * p.os + (size_t)(h / p.oh) * p.DV + v0;
   auto time = [&](int i) { return (int64_t)(p.rev ? a.T - 1 - i : i); };  // of the pass's i-th token
 
-  float x[NT], v[2];
+  float x[NT], v[2][COLS];
   auto fetch = [&](int t0) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x[i] = t0 + i < a.T && c < p.DK ? Act<T>::ld(xp + time(t0 + i) * xs) : 0.0f;
+    for (int i = 0; i < NT; ++i) x[i] = t0 + i < last && c0 < p.DK && !(AGG && which) ? Act<T>::ld(xp + time(t0 + i) * xs) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + warp + i * 8;
-      v[i] = t < a.T && v0 + lane < p.DV ? Act<T>::ld(vp + time(t) * p.vs + lane) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c)
+        v[i][c] = t < last && v0 + lane + 32 * c < p.DV ? Act<T>::ld(vp + time(t) * p.vs + lane + 32 * c) : 0.0f;
     }
   };
-  fetch(0);
-  for (int t0 = 0; t0 < a.T; t0 += NT) {
+  fetch(first);
+  for (int t0 = first; t0 < last; t0 += NT) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) kq[which][i][c] = x[i];
+    for (int i = 0; i < NT; ++i) kq[which][i][c0] = x[i];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) vs[warp + i * 8][lane] = v[i] * fv;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) vs[warp + i * 8][lane + 32 * c] = v[i][c] * fv;
     __syncthreads();
-    if (t0 + NT < a.T) fetch(t0 + NT);
-    const int n = min(NT, a.T - t0);
+    if (t0 + NT < last) fetch(t0 + NT);
+    const int n = min(NT, last - t0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) L[i] = f2b(0.0f);
+    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) L[c][i] = f2b(0.0f);
 #pragma unroll
     for (int g = 0; g < NT; g += 8) {
-      float o[8];
+      float o[COLS][8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float2 old = f2b(0.0f), sum = f2b(0.0f);
+        float2 old[COLS], sum[COLS];
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) old[c] = sum[c] = f2b(0.0f);
         if (g + j < n) {
-          const float2 vv = f2b(vs[g + j][col]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 kk = *reinterpret_cast<const float4*>(&kq[0][g + j][i * 32 + s * 4]);
-            const float4 q = *reinterpret_cast<const float4*>(&kq[1][g + j][i * 32 + s * 4]);
+            float4 q;
+            if (!AGG) q = *reinterpret_cast<const float4*>(&kq[1][g + j][i * 32 + s * 4]);
             const float2 q0 = make_float2(q.x, q.y), q1 = make_float2(q.z, q.w);
-            L[2 * i] = __ffma2_rn(lam, L[2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv));
-            L[2 * i + 1] = __ffma2_rn(lam, L[2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv));
-            sum = __ffma2_rn(L[2 * i], q0, sum);
-            old = __ffma2_rn(S[2 * i], q0, old);
-            sum = __ffma2_rn(L[2 * i + 1], q1, sum);
-            old = __ffma2_rn(S[2 * i + 1], q1, old);
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+              const float2 vv = f2b(vs[g + j][col + c]);
+              L[c][2 * i] = __ffma2_rn(lam, L[c][2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv));
+              L[c][2 * i + 1] = __ffma2_rn(lam, L[c][2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv));
+              if (AGG) continue;
+              sum[c] = __ffma2_rn(L[c][2 * i], q0, sum[c]);
+              old[c] = __ffma2_rn(S[c][2 * i], q0, old[c]);
+              sum[c] = __ffma2_rn(L[c][2 * i + 1], q1, sum[c]);
+              old[c] = __ffma2_rn(S[c][2 * i + 1], q1, old[c]);
+            }
           }
-          sum = __ffma2_rn(f2b(pw[g + j]), old, sum);
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) sum[c] = __ffma2_rn(f2b(pw[g + j]), old[c], sum[c]);
         }
-        o[j] = sum.x + sum.y;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[c][j] = sum[c].x + sum[c].y;
       }
       // lane s ends with the sum of token g + s
 #pragma unroll
-      for (int m = 4; m > 0; m >>= 1) {
-        const bool up = s & m;
+      for (int c = 0; c < (AGG ? 0 : COLS); ++c) {
 #pragma unroll
-        for (int j = 0; j < m; ++j) {
-          const float give = up ? o[j] : o[j + m], keep = up ? o[j + m] : o[j];
-          o[j] = keep + __shfl_xor_sync(~0u, give, m);
+        for (int m = 4; m > 0; m >>= 1) {
+          const bool up = s & m;
+#pragma unroll
+          for (int j = 0; j < m; ++j) {
+            const float give = up ? o[c][j] : o[c][j + m], keep = up ? o[c][j + m] : o[c][j];
+            o[c][j] = keep + __shfl_xor_sync(~0u, give, m);
+          }
         }
+        os[g + s][col + c] = o[c][0] * fo;
       }
-      os[g + s][col] = o[0] * fo;
     }
     const LinDecay d = lin_decay(ld, n);
     const float2 fl = p.rev ? lam : f2b(1.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) S[i] = __ffma2_rn(f2b(d.near), S[i], __ffma2_rn(f2b(d.off), S[i], __fmul2_rn(fl, L[i])));
+    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        S[c][i] = __ffma2_rn(f2b(d.near), S[c][i], __ffma2_rn(f2b(d.off), S[c][i], __fmul2_rn(fl, L[c][i])));
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int j = warp + i * 8;
-      if (j < n && v0 + lane < p.DV) {
-        const size_t at = ob + (size_t)time(t0 + j) * p.os + lane;
-        if (p.out_f32) static_cast<float*>(p.out)[at] = os[j][lane];
-        else Act<T>::st(static_cast<T*>(p.out) + at, os[j][lane]);
-      }
+#pragma unroll
+      for (int c = 0; c < (AGG ? 0 : COLS); ++c)
+        if (j < n && v0 + lane + 32 * c < p.DV) {
+          const size_t at = ob + (size_t)time(t0 + j) * p.os + lane + 32 * c;
+          if (p.out_f32) static_cast<float*>(p.out)[at] = os[j][lane + 32 * c];
+          else Act<T>::st(static_cast<T*>(p.out) + at, os[j][lane + 32 * c]);
+        }
     }
   }
-  if (p.s_out) {
+  if (AGG) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (vok && row(2 * i) < p.DK) p.s_out[where(row(2 * i))] = S[i].x;
-      if (vok && row(2 * i + 1) < p.DK) p.s_out[where(row(2 * i + 1))] = S[i].y;
-    }
+    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a.seg_end[slot + (size_t)row(i) * LIN_DMAX + c] = i & 1 ? S[c][i >> 1].y : S[c][i >> 1].x;
+  } else if (p.s_out && last == a.T) {
+#pragma unroll
+    for (int c = 0; c < COLS; ++c)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (v0 + col + c < p.DV && row(i) < p.DK) p.s_out[where(row(i), c)] = i & 1 ? S[c][i >> 1].y : S[c][i >> 1].x;
   }
 }
 
+template <typename T, int COLS>
+cudaError_t launch_lin_seq(const LinArgs& a, cudaStream_t st) {
+  const unsigned x = (unsigned)((int64_t)a.B * a.Hv * (LIN_DMAX / (32 * COLS)));
+  cudaError_t e = cudaSuccess;
+  if (a.segs > 1) {  // (the last segment's end is nobody's start)
+    e = launch_k(m3_lin_seq_kernel<T, COLS, true>, dim3(x, a.np, a.segs - 1), 256, 0, st, false, a);
+    if (e == cudaSuccess) e = launch_lin_seg(a, st);
+  }
+  return e == cudaSuccess ? launch_k(m3_lin_seq_kernel<T, COLS, false>, dim3(x, a.np, a.segs), 256, 0, st, a.segs > 1, a) : e;
+}
+
 // One token of one pass (decoding): wide blocks once there are two per SM.
+// Sequences: two columns per lane once blocks of one fill the SMs (two each)
+// more than twice.
 template <typename T>
-cudaError_t launch_lin_rec(const LinArgs& a, cudaStream_t st, int sms) {
+cudaError_t launch_lin_rec(LinArgs a, cudaStream_t st, int sms) {
   const int64_t heads = (int64_t)a.B * a.Hv;
   if (a.T == 1 && a.np == 1 && !a.p[0].rev) {
     const int tv = heads >= 2 * (int64_t)sms ? 128 : 32;
     const dim3 grid((unsigned)(heads * ((a.p[0].DV + tv - 1) / tv)));
     if (tv == 128) m3_lin_step_kernel<T, 128><<<grid, 256, 0, st>>>(a);
     else m3_lin_step_kernel<T, 32><<<grid, 256, 0, st>>>(a);
-  } else {
-    m3_lin_seq_kernel<T><<<dim3((unsigned)(heads * (LIN_DMAX / 32)), a.np), 256, 0, st>>>(a);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+  if (a.segs < 1) {  // no plan of segments: one
+    a.segs = 1;
+    a.nc = a.seg_chunks = (a.T + LIN_C - 1) / LIN_C;
+  }
+  const int64_t blocks = heads * a.np * a.segs * ((a.p[0].DV + 31) / 32);
+  return blocks > 4 * (int64_t)sms ? launch_lin_seq<T, 2>(a, st) : launch_lin_seq<T, 1>(a, st);
 }
-template cudaError_t launch_lin_rec<float>(const LinArgs&, cudaStream_t, int);
-template cudaError_t launch_lin_rec<__nv_bfloat16>(const LinArgs&, cudaStream_t, int);
+template cudaError_t launch_lin_rec<float>(LinArgs, cudaStream_t, int);
+template cudaError_t launch_lin_rec<__nv_bfloat16>(LinArgs, cudaStream_t, int);
 
 // dq and dk of shared key heads: the value heads' shares added in their order
 // (f32, the same bits on every call), rounded once.  Four columns per thread.

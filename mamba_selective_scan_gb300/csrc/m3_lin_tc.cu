@@ -785,6 +785,10 @@ __global__ void __launch_bounds__(256) m3_lin_seg_kernel(const __grid_constant__
   }
 }
 
+cudaError_t launch_lin_seg(const LinArgs& a, cudaStream_t st) {
+  return launch_k(m3_lin_seg_kernel, dim3((unsigned)(a.np * a.B * a.Hv), LIN_DMAX / 8), 256, 0, st, true, a);
+}
+
 cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
   LinMaps maps{};
   for (int i = 0; i < a.np; ++i) {
@@ -801,7 +805,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
     e = cudaFuncSetAttribute(m3_lin_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e == cudaSuccess)
       e = launch_k(m3_lin_tc_kernel<true>, dim3((unsigned)items, (unsigned)(a.segs - 1)), THREADS, SMEM_BYTES, st, false, a, maps);
-    if (e == cudaSuccess) e = launch_k(m3_lin_seg_kernel, dim3((unsigned)items, LIN_DMAX / 8), 256, 0, st, true, a);
+    if (e == cudaSuccess) e = launch_lin_seg(a, st);
   }
   if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)items * 4, st);

@@ -94,23 +94,25 @@ def test_scale(dt, scale):
 
 
 @pytest.mark.parametrize("B,T,Hk,Hv,state", [(8, 200, 10, 20, True), (40, 64, 4, 4, False), (31, 129, 5, 10, True), (51, 2, 3, 3, True)])
-def test_more_heads_than_sms(B, T, Hk, Hv, state):
-    x = lin_inputs(B, T, Hk, Hv, 64, 72, torch.bfloat16, seed=B, device="cuda", state=state)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_more_heads_than_sms(dt, B, T, Hk, Hv, state):
+    x = lin_inputs(B, T, Hk, Hv, 64, 72, DT[dt], seed=B, device="cuda", state=state)
     _check_all(_run(x), lin_ref_grads(x, 64 ** -0.5), NAMES + (["d_state"] if state else []))
 
 
 @pytest.mark.parametrize("B,T,Hk,Hv,dk,dv,dt,state", [
     (1, 1100, 1, 1, 128, 128, "bf16", True), (2, 2000, 2, 2, 128, 128, "bf16", True), (1, 1301, 1, 3, 64, 96, "bf16", True),
-    (2, 1537, 2, 4, 72, 40, "bf16", False), (5, 1030, 2, 4, 128, 64, "bf16", True), (1, 1999, 1, 2, 128, 128, "f32", True)])
+    (2, 1537, 2, 4, 72, 40, "bf16", False), (5, 1030, 2, 4, 128, 64, "bf16", True), (1, 1999, 1, 2, 128, 128, "f32", True), (2, 1301, 1, 3, 40, 72, "f32", False)])
 def test_few_heads_over_long_sequences(B, T, Hk, Hv, dk, dv, dt, state):
     x = lin_inputs(B, T, Hk, Hv, dk, dv, DT[dt], seed=T, device="cuda", state=state)
     _check_all(_run(x), lin_ref_grads(x, dk ** -0.5), NAMES + (["d_state"] if state else []))
 
 
-def test_slow_decays_over_many_chunks():
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_slow_decays_over_many_chunks(dt):
     """A state that hardly fades over hundreds of chunks: the decay of a chunk
     must not be rounded in a way that adds up."""
-    x = lin_inputs(1, 16384, 2, 2, 64, 64, torch.bfloat16, seed=5, device="cuda", state=True, log_decay=[-3e-7, -2e-5])
+    x = lin_inputs(1, 16384, 2, 2, 64, 64, DT[dt], seed=5, device="cuda", state=True, log_decay=[-3e-7, -2e-5])
     o, st = binding.m3scan_linattn_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"])
     i = torch.arange(16384, device="cuda", dtype=torch.float64)
     w = torch.exp(x["log_decay"].double() * (16383 - i)[:, None])[None, :, :, None]
