@@ -58,8 +58,8 @@ constexpr int STAGES = 3;
 constexpr int STAGE = 6 * TILE;        // K, Q (columns 0-63), K, Q (64-127), V, V
 constexpr int AGG_STAGES = 5;
 constexpr int AGG_STAGE = 4 * TILE;    // K, K, V, V
-constexpr int PT = STAGES * STAGE;     // P
-constexpr int OUT = PT + TILE;         // a chunk's outputs, for the tile store
+constexpr int PT = STAGES * STAGE;     // P, and of short sequences its second term
+constexpr int OUT = PT + 2 * TILE;     // a chunk's outputs, for the tile store
 constexpr int SMALL = OUT + 4 * TILE;  // (f32: four tiles of 32 values)
 
 struct Smem {  // at SMALL
@@ -244,8 +244,9 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 //
 // V' enters as four bf16 terms that hold its product with an f32 factor, so
 // states are f32 sums of f32-grade products.  S and P enter the outputs' products as one: each
-// rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; both come
-// to 2.3e-3 at most, their shares of the output being 1 together).
+// rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; all come
+// to 2.4e-3, S's and P's shares of the output being 1 together).  Of up to eight
+// chunks, whose outputs are mostly P's, P enters as two terms.
 //
 // A value that is not finite would reach the outputs of earlier tokens of its
 // chunk, in its own column, through the zeros of P: it is taken out of the V
@@ -257,8 +258,8 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
 //
 // AGG: only the states, each time segment's end from a zero start (into
-// seg_end); no queries, no outputs.
-template <bool AGG>
+// seg_end); no queries, no outputs.  FINE: P in two terms.
+template <bool AGG, bool FINE>
 __global__ void __launch_bounds__(THREADS, 1)
 m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinMaps maps) {
   extern __shared__ unsigned char raw[];
@@ -436,6 +437,11 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
               tc_mma_ss(tm + T_O, vn + (ks * 2048 >> 4), pd + (ks * 32 >> 4), tc_idesc(128, 64, true, false), ks > 0);
+            if (FINE) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc_mma_ss(tm + T_O, vn + (ks * 2048 >> 4), pd + ((TILE + ks * 32) >> 4), tc_idesc(128, 64, true, false), true);
+            }
             tc_commit(&s.mbo);
             tc_commit(&s.empty[g.i]);
           }
@@ -704,9 +710,16 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           for (int c = 0; c < 8; ++c) x[c] = f2b(0.0f);
         }
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          stmatrix4<false>(st0 + PT + sw(i0 + (lane & 15), hf * 4 + p * 2 + (lane >> 4)), pack2(x[4 * p]), pack2(x[4 * p + 1]),
-                           pack2(x[4 * p + 2]), pack2(x[4 * p + 3]));
+        for (int p = 0; p < 2; ++p) {
+          const uint32_t at = st0 + PT + sw(i0 + (lane & 15), hf * 4 + p * 2 + (lane >> 4));
+          stmatrix4<false>(at, pack2(x[4 * p]), pack2(x[4 * p + 1]), pack2(x[4 * p + 2]), pack2(x[4 * p + 3]));
+          if (FINE) {
+            uint32_t hi, lo[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) split2(x[4 * p + c], hi, lo[c]);
+            stmatrix4<false>(at + TILE, lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
         fence_proxy_async();
         ready(&s.rdy_p);
       }
@@ -802,12 +815,13 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
   const int64_t items = (int64_t)a.np * a.B * a.Hv;
   cudaError_t e = cudaSuccess;
   if (a.segs > 1) {  // (the last segment's end is nobody's start)
-    e = cudaFuncSetAttribute(m3_lin_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    e = cudaFuncSetAttribute(m3_lin_tc_kernel<true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
     if (e == cudaSuccess)
-      e = launch_k(m3_lin_tc_kernel<true>, dim3((unsigned)items, (unsigned)(a.segs - 1)), THREADS, SMEM_BYTES, st, false, a, maps);
+      e = launch_k(m3_lin_tc_kernel<true, false>, dim3((unsigned)items, (unsigned)(a.segs - 1)), THREADS, SMEM_BYTES, st, false, a, maps);
     if (e == cudaSuccess) e = launch_lin_seg(a, st);
   }
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(m3_lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+  const auto kern = a.nc <= 8 ? m3_lin_tc_kernel<false, true> : m3_lin_tc_kernel<false, false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
   if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)items * 4, st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -825,7 +839,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = a.stream || a.segs > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, m3_lin_tc_kernel<false>, a, maps);
+  return cudaLaunchKernelEx(&cfg, kern, a, maps);
 }
 
 }  // namespace m3
