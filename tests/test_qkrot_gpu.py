@@ -8,6 +8,8 @@ values come to 1.7e-3).  To f32 it is 2^-24 on top of some 2^-22 of f32
 arithmetic (a few roundings of 2^-24 each, the cosines' 2^-22): 1e-6.  The weights' gradients are f32 sums: 2e-6 of the 2-norm of
 what is added, which for random signs is the sum's own size."""
 
+from fractions import Fraction
+
 import pytest
 import torch
 
@@ -94,6 +96,26 @@ def test_far_positions(il):
     # the reference's own angle is a product in 64 bits: off by 2^36 x 2^-53
     # radians at most
     _check(_run(x, il), rot_ref_grads(x, EPS, il), sums=1e-5)
+
+
+def test_angles_beyond_a_double():
+    """Angles of a far position against exact arithmetic: the frequency in
+    turns is off by 3 x 2^-65 at most, at 2^38 that is 1.4e-7 radians (and one
+    double's product would be off by some 1e-5)."""
+    pi = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+    x = rot_inputs(1, 6, 1, 1, 16, 16, torch.float32, seed=3, device="cuda")
+    x["inv_freq"] = torch.tensor([1.0, 0.9, -0.7, 0.11, 3.3, 1e-3, 42.5, 1e-9], device="cuda")
+    pos = [2 ** 38 + 1, 2 ** 38 - 12345, -(2 ** 37) - 77, 2 ** 36 + 5, 987654321987, 3]
+    x["positions"] = torch.tensor([pos], device="cuda")
+    turns = [[float(p * Fraction(f) / (2 * pi) % 1) for f in x["inv_freq"].tolist()] for p in pos]
+    ang = torch.tensor(turns, dtype=torch.float64) * float(2 * pi)
+    q, k = binding.m3scan_qkrot_fwd(*(x[n] for n in ("q", "k", "q_weight", "k_weight", "positions", "inv_freq")), eps=EPS)
+    for t, w, out in ((x["q"], x["q_weight"], q), (x["k"], x["k_weight"], k)):
+        t, w = t.double().cpu(), w.double().cpu()
+        n = t * torch.rsqrt(t.square().mean(-1, keepdim=True) + EPS) * w
+        a, b = n[..., :8], n[..., 8:]
+        c, s = ang.cos()[None, :, None], ang.sin()[None, :, None]
+        assert rel(out, torch.cat((a * c - b * s, a * s + b * c), -1)) <= TOL[torch.float32]
 
 
 def test_frequencies_of_every_size():
