@@ -94,6 +94,7 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
   // (a few tokens by the recurrence, without the chunks' latency)
   p->tc = act == M3_BF16 && p->T > 1;
   p->nc = (p->T + LIN_C - 1) / LIN_C;
+  if ((int64_t)3 * p->B * p->Hv * p->nc > 0x7FFFFFFF) return M3_ERR_DIMS;  // chunks are counted in 32 bits
   for (int i = 0; i < 2; ++i) {
     LinPlan::Walk& w = p->walk[i];
     const int64_t items = (int64_t)(i ? 3 : 1) * p->B * p->Hv;

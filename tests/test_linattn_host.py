@@ -64,7 +64,7 @@ def test_linattn_plan(lib, act):
     (dict(v_heads=3), 3), (dict(head_k=0), 3), (dict(head_k=12), 3), (dict(head_k=136), 3), (dict(head_v=136), 3),
     (dict(head_v=4), 3), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2), (dict(reserved=1), 2),
     (dict(q_stride=127), 2), (dict(q_stride=132), 4), (dict(v_stride=511), 2), (dict(dk_stride=-8), 2),
-    (dict(seq_len=(1 << 30) + 1), 2),
+    (dict(seq_len=(1 << 30) + 1), 2), (dict(batch=8, seq_len=1 << 30, k_heads=1, v_heads=64), 2),
 ])
 def test_linattn_refuses(lib, kw, status):
     assert _lin_plan(_lin(**kw))[0] == status
