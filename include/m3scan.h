@@ -548,7 +548,7 @@ m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const voi
  *   inv_freq  : [rot_dim / 2] float32, radians per position
  *
  * Angles are exact for every position up to the rounding of inv_freq / (2 pi)
- * to 2^-64 turns: far positions lose nothing.  Sums are f32.  head_dim 2 to
+ * to 2^-63 turns (inv_freq up to 2^22): far positions lose nothing.  Sums are f32.  head_dim 2 to
  * 256; tensors whose heads and tokens start on 16 bytes (and, not
  * interleaved, rot_dim / 2 a multiple of 8 for bf16, 4 for f32) run the vector
  * kernels.  The weights' gradients are fixed-order sums: identical bits on
@@ -608,7 +608,14 @@ m3_status m3scan_qkrot_bwd(const m3_qkrot_dims* dims, m3_dtype act, const void* 
  *
  * head_k and head_v are multiples of 8 up to 128.  Activation and state
  * pointers are 16-byte aligned.  All results are the same bits on every call.
- * States are f32.
+ *
+ * States are f32, and sums are.  f32 activations are computed in f32.  bf16
+ * sequences are products on the tensor cores: states are f32 sums of products
+ * with f32's own error, and for the outputs the state that a chunk of 64 tokens
+ * starts from and the weights between its tokens are each rounded to bf16 once
+ * (the weights to two bf16 terms where seq_len is at most 512), which is of the
+ * size of the outputs' own rounding.  The gradients are computed the same way.
+ * Outputs and states are not finite exactly where the recurrence's are not.
  */
 typedef struct {
     int64_t batch, seq_len, k_heads, v_heads, head_k, head_v;

@@ -243,10 +243,11 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // register work of the ones around it.
 //
 // V' enters as four bf16 terms that hold its product with an f32 factor, so
-// states are f32 sums of f32-grade products.  S and P enter the outputs' products as one: each
-// rounding is of the size of the outputs' own (1.7e-3 in the 2-norm; all come
-// to 2.4e-3, S's and P's shares of the output being 1 together).  Of up to eight
-// chunks, whose outputs are mostly P's, P enters as two terms.
+// states are f32 sums of f32-grade products.  S and P enter the outputs'
+// products as one term each: a rounding of the size of the outputs' own (1.7e-3
+// of them in the 2-norm; all together come to 2.4e-3).  Of up to eight chunks,
+// whose outputs are mostly P's, P enters as two terms (2 x 77 tokens: 1.8e-3
+// instead of 2.3e-3, for no measurable time).
 //
 // A value that is not finite would reach the outputs of earlier tokens of its
 // chunk, in its own column, through the zeros of P: it is taken out of the V
@@ -256,6 +257,19 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 //
 // Roles: warps 0-7 the state, 8-15 V', 16-23 the outputs (P, O^T), warp 24
 // issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
+//
+// Bound: a head of 128 x 128 moves 64 KB a chunk, 1.3 us at a full SM's share
+// of HBM, and a chunk takes 1.2 to 1.4 us, of which the tensor cores work a
+// quarter; issue slots are 46 to 58 % busy and shared memory under 50 %, so what
+// is left is the chain C -> X -> A and B -> P -> O within a chunk.  Measured: 4 x
+// 4096 x 40 heads, forward 112 us (650 MB: 86 % of HBM's rate), the three
+// backward passes side by side 290 us (1.56 GB, 79 %); 1 x 65536 x 16 heads in
+// nine segments 268 us, where its last part runs at 95 %.  One loop for all of
+// it, and each role's own code unrolled by tile, was bound by instruction
+// fetches (11000 instructions, 86 us for 8 x 2048 x 12 heads); rolled up it is
+// 3700 and takes 50.  A second warp issuing MMAs and prefetches of later chunks
+// into L2 made nothing faster.  The state's warps spill 70 bytes a thread, where
+// runs start and end.
 //
 // AGG: only the states, each time segment's end from a zero start (into
 // seg_end); no queries, no outputs.  FINE: P in two terms.
@@ -464,13 +478,14 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
         wait(&s.mbx[two(n - 1)], two_par(n - 1));
         tmem_fence_after_sync();
-        if (!idle)
+        if (!idle) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float2 x[8];
-          tc_ld16(tq + at_x(n - 1) + hf * 64 + q * 16, x);
+          for (int q = 0; q < 4; ++q) {
+            float2 x[8];
+            tc_ld16(tq + at_x(n - 1) + hf * 64 + q * 16, x);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
+            for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
+          }
         }
         ready(&s.rdy_x[two(n - 1)]);
         if (flags & F_LAST) {  // where the run leaves its state
@@ -543,17 +558,19 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         wait(&s.mbq, (n - 1) & 1);  // the last state is read
         tmem_fence_after_sync();
       }
-      if (!idle)
+      if (!idle) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {  // S into tensor memory
-        uint32_t x[8];
+        for (int p = 0; p < 4; ++p) {  // S into tensor memory
+          uint32_t x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = pack2(S[8 * p + k]);
-        tc_st8(tq + T_S + hf * 32 + p * 8, x);
+          for (int k = 0; k < 8; ++k) x[k] = pack2(S[8 * p + k]);
+          tc_st8(tq + T_S + hf * 32 + p * 8, x);
+        }
       }
       ready(&s.rdy_s);
     }
-  } else if (warp < 2 * GW) {  // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
+  } else if (warp < 2 * GW) {
+    // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RC));
     const int hf = (warp >> 2) & 1, row = quad * 32 + lane;  // half of the tokens
     const bool idle = (int)quad * 32 >= DV;
@@ -574,17 +591,18 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       const uint32_t vt = vl + g.i * STB;
       const LinVec& vec = s.vec[n & 7];
       __nv_bfloat162 chk = as_bf2(0);
-      if (!idle)
+      if (!idle) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int tp = 0; tp < 2; ++tp) {  // tokens 32 hf + 16 tp ..
-          // (values 0-7, tokens 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-          uint32_t (&z)[4] = reinterpret_cast<uint32_t(&)[4]>(x[h][tp * 4]);
-          ldmatrix4t(z, vt + (el ^ (h * 32)) + tp * 2048);
+          for (int tp = 0; tp < 2; ++tp) {  // tokens 32 hf + 16 tp ..
+            // (values 0-7, tokens 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+            uint32_t (&z)[4] = reinterpret_cast<uint32_t(&)[4]>(x[h][tp * 4]);
+            ldmatrix4t(z, vt + (el ^ (h * 32)) + tp * 2048);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) chk = __hfma2(as_bf2(z[i]), as_bf2(0), chk);  // 0 unless a value is not finite
-        }
+            for (int i = 0; i < 4; ++i) chk = __hfma2(as_bf2(z[i]), as_bf2(0), chk);  // 0 unless a value is not finite
+          }
+      }
       auto terms = [&](int h) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
@@ -621,18 +639,18 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         wait(&s.mbx[two(n)], two_par(n) ^ 1);
         tmem_fence_after_sync();
       }
-      if (!idle)
+      if (!idle) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h) terms(1);
+        for (int h = 0; h < 2; ++h) {
+          if (h) terms(1);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
+          for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
+        }
       }
       ready(&s.rdy_v[two(n)]);
     }
   } else {  // the outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RB));
-    if constexpr (!AGG) {
     const int hf = (warp >> 2) & 1;  // half of the tokens (of P: of its columns)
     const int i0 = quad * 16, j0 = hf * 32;
     const bool idle = (int)quad * 32 >= DV;  // (P's rows are tokens: no warp is idle there)
@@ -641,7 +659,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     const uint32_t op32 = st0 + OUT + quad * TILE + sw(j0 + 2 * (lane & 3), lane >> 4) + ((lane >> 2) & 3) * 4;
     const uint32_t op = st0 + OUT + (quad >> 1) * TILE + sw(j0 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
 #pragma unroll 1
-    for (int n = 0; n <= walk.n; ++n) {
+    for (int n = 0; n <= (AGG ? -1 : walk.n); ++n) {
       // O of the step before: values 32 quad .. of tokens 32 hf ..
       float2 o[2][8];  // [half of the lanes][block of 8 tokens][row + 8]
       if (n > 0) {
@@ -652,16 +670,17 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         for (int tb = 0; tb < 4; ++tb) f[tb] = *reinterpret_cast<const float2*>(fo + tb * 8);
         wait(&s.mbo, m & 1);  // (and S Q^T, which was issued before)
         tmem_fence_after_sync();
-        if (!idle)
+        if (!idle) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float2 q[8];
-          tc_ld_frag(tq + (h << 20) + T_Q + j0, q);
-          tc_ld_frag(tq + (h << 20) + T_O + j0, o[h]);
-          tc_wait_frag(q);
-          tc_wait_frag(o[h]);
+          for (int h = 0; h < 2; ++h) {
+            float2 q[8];
+            tc_ld_frag(tq + (h << 20) + T_Q + j0, q);
+            tc_ld_frag(tq + (h << 20) + T_O + j0, o[h]);
+            tc_wait_frag(q);
+            tc_wait_frag(o[h]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) o[h][c] = __ffma2_rn(f[c >> 1], q[c], o[h][c]);
+            for (int c = 0; c < 8; ++c) o[h][c] = __ffma2_rn(f[c >> 1], q[c], o[h][c]);
+          }
         }
         if (!idle && s.any_bad[m & 3] == (unsigned)n) {
           const bool rev = s.info[m & 7].flags & F_REV;
@@ -732,7 +751,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {  // value 16 h + 8 (c & 1) + lane / 4 of this warp's tile, tokens j0 + 8 (c >> 1) + 2 (lane & 3), + 1
+            for (int c = 0; c < 8; ++c) {
+              // value 16 h + 8 (c & 1) + lane / 4 of this warp's tile, tokens j0 + 8 (c >> 1) + 2 (lane & 3), + 1
               const uint32_t at = (op32 ^ ((4 * h + 2 * (c & 1)) << 4)) + (c >> 1) * 1024;
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(o[h][c].x) : "memory");
               asm volatile("st.shared.f32 [%0], %1;" ::"r"((at ^ 16u) + 128u), "f"(o[h][c].y) : "memory");
@@ -748,7 +768,6 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.rdy_o);
       }
-    }
     }
   }
   if (!wait.ok()) report_timeout(&g_lin_status, a.status);

@@ -278,6 +278,54 @@ def test_on_another_stream():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H", [(40, 200, 4), (1, 1500, 2)])
+def test_two_calls_at_once(dt, B, T, H):
+    xs = [lin_inputs(B, T, H, H, 64, 64, DT[dt], seed=s, device="cuda") for s in (3, 4)]
+    want = [_run(x) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[_run(x, stream=s) for x, s in zip(xs, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for g, w in zip(pair, want):
+            for n in w:
+                assert torch.equal(g[n], w[n]), n
+    assert binding.m3scan_device_status() == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,Hk,Hv", [(40, 200, 2, 4), (1, 1500, 1, 2), (2, 100, 2, 2)])
+def test_workspace_holds_anything(dt, B, T, Hk, Hv):
+    """What a workspace held past its status block changes nothing."""
+    x = lin_inputs(B, T, Hk, Hv, 64, 72, DT[dt], seed=5, device="cuda")
+    want = _run(x)
+    dims = binding.M3LinattnDims(B, T, Hk, Hv, 64, 72, 0, 0, 0, 0, 0, 0, 0.0, 0)
+    ws = binding.Workspace(binding.m3scan_linattn_plan(dims, binding.M3_BF16 if dt == "bf16" else binding.M3_F32).workspace_bytes, "cuda")
+    ws.buf[binding.STATUS_BYTES:] = 255
+    got = _run(x, workspace=ws)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    assert binding.m3scan_get_status(ws) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_decode_captured(dt):
+    """A captured token, replayed: the state moves on with every replay."""
+    x = lin_inputs(3, 1, 2, 4, 64, 64, DT[dt], seed=9, device="cuda")
+    args = [x[n] for n in ("q", "k", "v", "log_decay")]
+    state, want = x["state"].clone(), x["state"].clone()
+    binding.m3scan_linattn_decode(*args, x["state"].clone())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = binding.m3scan_linattn_decode(*args, state)
+    for _ in range(3):
+        g.replay()
+        ref = binding.m3scan_linattn_decode(*args, want)
+        torch.cuda.synchronize()
+        assert torch.equal(o, ref) and torch.equal(state, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_offsets_past_32_bits(dt):
     """Tokens a megabyte or more apart: the last ones lie past 2^31 elements."""
     T, stride = 2100, 1 << 20
