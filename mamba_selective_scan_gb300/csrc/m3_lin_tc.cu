@@ -41,7 +41,7 @@ enum { F_REV = 1, F_TAKE = 2, F_GIVE = 4, F_FIRST = 8, F_LAST = 16 };
 
 // A step's factors (lam the head's decay, n the chunk's tokens)
 struct LinVec {
-  uint4 fk[TC / 2];        // of two tokens' shares in the next state, as three bf16 terms
+  uint4 fk[TC / 2];        // of two tokens' shares in the next state: three bf16 terms, the first negated
   float fo[TC];            // of the start state in a token's output
   // of token j's share in token i's output: pz[0][64 + j - i], and one place
   // earlier in pz[1], so that the two of a pair of j lie on 8 bytes for every i
@@ -174,7 +174,7 @@ __device__ __forceinline__ void lin_factors(const LinArgs& a, const LinInfo& t, 
     fk[0] -= __low2float(f);
     fk[1] -= __high2float(f);
   }
-  v.fk[lane] = make_uint4(term[0], term[1], term[2], 0);
+  v.fk[lane] = make_uint4(term[0], term[1], term[2], term[0] ^ 0x80008000u);
 }
 // The decay of a chunk of n tokens, rounded to f32 now up and now down so that
 // the product over a run's chunks stays within a rounding of the true one (`acc`
@@ -431,7 +431,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
                 tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
-                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? TC_NEGATE_A : 0u), p + ks > 0);
+                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A), p + ks > 0);
             tc_commit(&s.mbx[two(n)]);
             if (AGG) tc_commit(&s.empty[g.i]);
           }
@@ -579,9 +579,9 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n < walk.n; ++n, g.next()) {
-      // v f to f32's grade, as terms: hi = v f1 rounded, its rest hi - v f1
-      // (exact, eight bits at most; negated), v f2 rounded, and its rest with
-      // v f3 (negated: the MMAs of these two negate their A).  Five packed bf16
+      // v f to f32's grade, as terms: hi = v f1 rounded (negated, for the rest's
+      // sake: its MMAs negate their A), the rest v f1 - hi (exact, eight bits at
+      // most), v f2 rounded (negated), and its rest with v f3.  Five packed bf16
       // instructions for two values, where three terms cut from the f32 product
       // take twelve.  (Three terms of this kind are 4 % faster, and 2e-6 off.)
       // Made while the X before runs; written as soon as that is done with the
@@ -600,27 +600,27 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             uint32_t (&z)[4] = reinterpret_cast<uint32_t(&)[4]>(x[h][tp * 4]);
             ldmatrix4t(z, vt + (el ^ (h * 32)) + tp * 2048);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) chk = __hfma2(as_bf2(z[i]), as_bf2(0), chk);  // 0 unless a value is not finite
+            for (int i = 0; i < 4; i += 2) chk = __hfma2(as_bf2(z[i]), as_bf2(z[i + 1]), chk);  // finite only if all values are
           }
       }
       auto terms = [&](int h) {
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
           const uint4 f = vec.fk[hf * 16 + tb * 4 + (lane & 3)];
-          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y), n1 = as_bf2(f.x ^ 0x80008000u);
-          const __nv_bfloat162 n2 = as_bf2(f.y ^ 0x80008000u), n3 = as_bf2(f.z ^ 0x80008000u);
+          const __nv_bfloat162 f1 = as_bf2(f.x), f2 = as_bf2(f.y), f3 = as_bf2(f.z), n1 = as_bf2(f.w);
+          const __nv_bfloat162 n2 = as_bf2(f.y ^ 0x80008000u);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, f1), t = __hmul2_rn(v, f2);
+            const __nv_bfloat162 v = as_bf2(x[h][tb * 2 + i]), hi = __hmul2_rn(v, n1), t = __hmul2_rn(v, n2);
             y[0][tb * 2 + i] = as_u32(hi);
-            y[1][tb * 2 + i] = as_u32(__hfma2(v, n1, hi));
+            y[1][tb * 2 + i] = as_u32(__hfma2(v, f1, hi));
             y[2][tb * 2 + i] = as_u32(t);
-            y[3][tb * 2 + i] = as_u32(__hfma2(v, n3, __hfma2(v, n2, t)));
+            y[3][tb * 2 + i] = as_u32(__hfma2(v, f3, __hfma2(v, f2, t)));
           }
         }
       };
       if (!idle) terms(0);
-      if (__any_sync(~0u, (as_u32(chk) & 0x7FFF7FFFu) != 0)) {
+      if (__any_sync(~0u, (as_u32(__hmul2(chk, as_bf2(0))) & 0x7FFF7FFFu) != 0)) {
         const bool rev = s.info[n & 7].flags & F_REV;
 #pragma unroll 1
         for (int tok = hf * 32; tok < hf * 32 + 32; ++tok) {
@@ -711,11 +711,12 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           tc_wait_frag(x);
           float2 chk = f2b(0.0f);
 #pragma unroll
+          for (int c = 0; c < 8; c += 2) chk = __ffma2_rn(x[c], x[c + 1], chk);  // finite only if all are
+#pragma unroll
           for (int c = 0; c < 8; ++c) {
-            chk = __ffma2_rn(x[c], f2b(0.0f), chk);
             x[c] = __fmul2_rn(x[c], *reinterpret_cast<const float2*>(pz + 8 * (c >> 1) - 8 * (c & 1)));
           }
-          if (!(chk.x + chk.y == 0.0f)) {  // what is not finite among pairs that do not count
+          if ((chk.x + chk.y) * 0.0f != 0.0f) {  // what is not finite among pairs that do not count
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const int d = i0 + (lane >> 2) + 8 * (c & 1) - j0 - 2 * (lane & 3) - 8 * (c >> 1);  // i - j
