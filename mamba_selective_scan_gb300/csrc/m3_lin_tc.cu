@@ -68,9 +68,9 @@ struct Smem {  // at SMALL
   unsigned any_bad[4];   // step + 1
   LinInfo info[8];       // (a step's stores come up to two steps later)
   uint64_t full[AGG_STAGES], empty[AGG_STAGES];
-  uint64_t mbx[2];           // (AGG: by step, for two X in flight)
+  uint64_t mbx[2], mbv[2];   // X made, by half of the keys; V' read, by half of the tokens
+  uint64_t rdy_v[2], rdy_x[2];  // (AGG: all three by step, for two X in flight)
   uint64_t mbp, mbq, mbo, o_free;
-  uint64_t rdy_v[2], rdy_x[2];
   uint64_t rdy_s, rdy_q, rdy_p, rdy_o;  // one arrival per warp of a group
   uint32_t tmem;
 };
@@ -258,18 +258,18 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // Roles: warps 0-7 the state, 8-15 V', 16-23 the outputs (P, O^T), warp 24
 // issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
 //
-// Bound: a head of 128 x 128 moves 64 KB a chunk, 1.3 us at a full SM's share
-// of HBM, and a chunk takes 1.2 to 1.4 us, of which the tensor cores work a
-// quarter; issue slots are 46 to 58 % busy and shared memory under 50 %, so what
-// is left is the chain C -> X -> A and B -> P -> O within a chunk.  Measured: 4 x
-// 4096 x 40 heads, forward 112 us (650 MB: 86 % of HBM's rate), the three
-// backward passes side by side 290 us (1.56 GB, 79 %); 1 x 65536 x 16 heads in
-// nine segments 268 us, where its last part runs at 95 %.  One loop for all of
-// it, and each role's own code unrolled by tile, was bound by instruction
-// fetches (11000 instructions, 86 us for 8 x 2048 x 12 heads); rolled up it is
-// 3700 and takes 50.  A second warp issuing MMAs and prefetches of later chunks
-// into L2 made nothing faster.  The state's warps spill 70 bytes a thread, where
-// runs start and end.
+// Bound: a chunk of a 128 x 128 head is 64 KB, 1.4 us at an SM's share of HBM's
+// rate, and takes 1.2 to 1.4 us (2400 cycles), in which the tensor cores work
+// 1500, issue slots are 55 % busy and shared memory 50 %: the outputs' warps go
+// through reading, weighing and writing one after the other, 2100 to 2400
+// cycles.  Measured: 4 x 4096 x 40 heads, forward 112 us (650 MB: 86 % of HBM's
+// rate), the three backward passes side by side 290 us (1.56 GB, 79 %); 1 x
+// 65536 x 16 heads in nine segments 268 us, where its last part runs at 95 %.
+// Each role's code unrolled by tile was bound by instruction fetches (11000
+// instructions, 86 us for 8 x 2048 x 12 heads); rolled up it is 3700 and takes
+// 50.  A second warp issuing MMAs, and prefetches of later chunks into L2, made
+// nothing faster.  The state's warps spill 70 bytes a thread, where runs start
+// and end.
 //
 // AGG: only the states, each time segment's end from a zero start (into
 // seg_end); no queries, no outputs.  FINE: P in two terms.
@@ -294,8 +294,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   const int DK = a.p[pass].DK, DV = a.p[pass].DV;
   const int nk = DK > 64 ? 2 : 1, nv = DV > 64 ? 2 : 1;
   constexpr int NST = AGG ? AGG_STAGES : STAGES, STB = AGG ? AGG_STAGE : STAGE;
-  // X, V' and their barriers: one of each, or two in turns
-  auto two = [](int n) { return AGG ? n & 1 : 0; };
+  // X, V' and their barriers: one of each, in halves, or (AGG) two in turns
+  auto two = [](int n, int half) { return AGG ? n & 1 : half; };
   auto two_par = [](int n) { return (uint32_t)(AGG ? n >> 1 : n) & 1u; };
   auto at_x = [&](int n) { return AGG ? A_X + (n & 1) * 128 : T_X; };
   auto at_v = [&](int n) { return AGG ? A_V + (n & 1) * 128 : T_V; };
@@ -306,8 +306,9 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       mbar_init(&s.full[i], 2);  // the copies, the factors
       mbar_init(&s.empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbp, &s.mbx[0], &s.mbx[1], &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy_v[0], &s.rdy_v[1], &s.rdy_x[0], &s.rdy_x[1], &s.rdy_s, &s.rdy_q, &s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
+    for (uint64_t* r : {&s.mbp, &s.mbx[0], &s.mbx[1], &s.mbv[0], &s.mbv[1], &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_v[0], &s.rdy_v[1], &s.rdy_x[0], &s.rdy_x[1]}) mbar_init(r, AGG ? GW : GW / 2);
+    for (uint64_t* r : {&s.rdy_s, &s.rdy_q, &s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
     mbar_init_fence();
   }
   if (tid < 512) reinterpret_cast<unsigned*>(s.bad)[tid] = 0;
@@ -396,6 +397,10 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.full[i]);
       }
+      // every product is done (and its arrivals are in) before the block ends
+#pragma unroll 1
+      for (int n = walk.n; n < walk.n + NST; ++n, g.next())
+        if (n >= NST) wait(&s.empty[g.i], g.par ^ 1);
       // after a wait ran out, copies still in flight land before the block's
       // shared memory is given up (bounded)
       if (!wait.ok())
@@ -422,20 +427,48 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             }
             tc_commit(&s.mbp);
           }
-          wait(&s.rdy_v[two(n)], two_par(n));      // V' is in tensor memory
-          if (n >= BACK) wait(&s.rdy_x[two(n)], two_par(n) ^ 1);  // the last X is read
-          if (wait.ok()) {
-            tmem_fence_after_sync();
+          if (AGG) {
+            wait(&s.rdy_v[n & 1], two_par(n));                  // V' is in tensor memory
+            if (n >= BACK) wait(&s.rdy_x[n & 1], two_par(n) ^ 1);  // the X before is read
+            if (wait.ok()) {
+              tmem_fence_after_sync();
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
+              for (int p = 0; p < 4; ++p)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
-                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A), p + ks > 0);
-            tc_commit(&s.mbx[two(n)]);
-            if (AGG) tc_commit(&s.empty[g.i]);
+                for (int ks = 0; ks < 4; ++ks)
+                  tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
+                            (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A),
+                            p + ks > 0);
+              tc_commit(&s.mbx[n & 1]);
+              tc_commit(&s.empty[g.i]);
+            }
+            continue;
           }
-          if (AGG) continue;
+          // X in quarters: half of the tokens of either half of the keys, then
+          // the other half.  So half of V' can be written, and half of X read,
+          // while the rest is multiplied.
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            wait(&s.rdy_v[kh], par);  // this half of V' is in tensor memory
+#pragma unroll
+            for (int nh = 0; nh < 2; ++nh) {
+              if (kh == 0 && n > 0) wait(&s.rdy_x[nh], par ^ 1);  // the last X is read (idle warps keep step here)
+              if (nh < nk && wait.ok()) {
+                tmem_fence_after_sync();
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+#pragma unroll
+                  for (int ks = 2 * kh; ks < 2 * kh + 2; ++ks)
+                    tc_mma_ts(tm + T_X + nh * 64, tm + T_V + p * 32 + ks * 8, kn + ((nh * 2 * TILE + ks * 2048) >> 4),
+                              tc_idesc(128, 64, false, true) | (p & 1 ? 0u : TC_NEGATE_A), p + ks > 0);
+                if (kh == 1) tc_commit(&s.mbx[nh]);
+              }
+            }
+            if (wait.ok()) {
+              tc_commit(&s.mbv[kh]);
+              if (kh == 1 && nk == 1) tc_commit(&s.mbx[1]);
+            }
+          }
           wait(&s.rdy_s, par);                     // S is in tensor memory
           if (n > 0) wait(&s.rdy_q, par ^ 1);      // the last outputs are read
           if (wait.ok()) {
@@ -476,7 +509,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     for (int n = 0; n <= walk.n; ++n, g.next()) {
       if (n > 0) {  // S = lam^n S + X of the step before
         const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
-        wait(&s.mbx[two(n - 1)], two_par(n - 1));
+        wait(&s.mbx[two(n - 1, hf)], two_par(n - 1));
         tmem_fence_after_sync();
         if (!idle) {
 #pragma unroll
@@ -487,7 +520,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
           }
         }
-        ready(&s.rdy_x[two(n - 1)]);
+        ready(&s.rdy_x[two(n - 1, hf)]);
         if (flags & F_LAST) {  // where the run leaves its state
           const LinInfo t = s.info[(n - 1) & 7];
           const LinPass& p = a.p[t.pass];
@@ -636,7 +669,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         fence_proxy_async();
       }
       if (n >= BACK) {
-        wait(&s.mbx[two(n)], two_par(n) ^ 1);
+        wait(AGG ? &s.mbx[n & 1] : &s.mbv[hf], two_par(n) ^ 1);
         tmem_fence_after_sync();
       }
       if (!idle) {
@@ -647,7 +680,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
         }
       }
-      ready(&s.rdy_v[two(n)]);
+      ready(&s.rdy_v[two(n, hf)]);
     }
   } else {  // the outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RB));
