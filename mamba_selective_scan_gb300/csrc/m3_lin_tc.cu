@@ -68,10 +68,12 @@ struct Smem {  // at SMALL
   unsigned any_bad[4];   // step + 1
   LinInfo info[8];       // (a step's stores come up to two steps later)
   uint64_t full[AGG_STAGES], empty[AGG_STAGES];
-  uint64_t mbx[2], mbv[2];   // X made, by half of the keys; V' read, by half of the tokens
-  uint64_t rdy_v[2], rdy_x[2];  // (AGG: all three by step, for two X in flight)
-  uint64_t mbp, mbq, mbo, o_free;
-  uint64_t rdy_s, rdy_q, rdy_p, rdy_o;  // one arrival per warp of a group
+  // products done: X (AGG: by step, for two in flight), its first half of the
+  // tokens, P, S Q^T, O
+  uint64_t mbx[2], mbv, mbp, mbq, mbo, o_free;
+  // ready for a step's products, one arrival per warp: V' is there and the X
+  // before read; S is there and the outputs before are read; P; the outputs
+  uint64_t rdy_x[2], rdy_s, rdy_p, rdy_o;
   uint32_t tmem;
 };
 constexpr size_t SMEM_BYTES = SMALL + sizeof(Smem) + 1024;
@@ -198,6 +200,13 @@ __device__ __forceinline__ void tc_ld_frag(uint32_t t, float2 (&v)[8]) {  // 16 
         "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y), "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
       : "r"(t) : "memory");
 }
+__device__ __forceinline__ void tc_ld_rows(uint32_t t, float2 (&v)[8]) {  // 32 lanes x 16 columns
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0].x), "=f"(v[0].y), "=f"(v[1].x), "=f"(v[1].y), "=f"(v[2].x), "=f"(v[2].y), "=f"(v[3].x), "=f"(v[3].y),
+        "=f"(v[4].x), "=f"(v[4].y), "=f"(v[5].x), "=f"(v[5].y), "=f"(v[6].x), "=f"(v[6].y), "=f"(v[7].x), "=f"(v[7].y)
+      : "r"(t) : "memory");
+}
 __device__ __forceinline__ void tc_wait_frag(float2 (&a)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(a[0].x), "+f"(a[0].y), "+f"(a[1].x), "+f"(a[1].y), "+f"(a[2].x), "+f"(a[2].y), "+f"(a[3].x), "+f"(a[3].y),
@@ -294,8 +303,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   const int DK = a.p[pass].DK, DV = a.p[pass].DV;
   const int nk = DK > 64 ? 2 : 1, nv = DV > 64 ? 2 : 1;
   constexpr int NST = AGG ? AGG_STAGES : STAGES, STB = AGG ? AGG_STAGE : STAGE;
-  // X, V' and their barriers: one of each, in halves, or (AGG) two in turns
-  auto two = [](int n, int half) { return AGG ? n & 1 : half; };
+  // X, V' and their barriers: one of each, or (AGG) two in turns
+  auto two = [](int n) { return AGG ? n & 1 : 0; };
   auto two_par = [](int n) { return (uint32_t)(AGG ? n >> 1 : n) & 1u; };
   auto at_x = [&](int n) { return AGG ? A_X + (n & 1) * 128 : T_X; };
   auto at_v = [&](int n) { return AGG ? A_V + (n & 1) * 128 : T_V; };
@@ -306,9 +315,9 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       mbar_init(&s.full[i], 2);  // the copies, the factors
       mbar_init(&s.empty[i], 1);
     }
-    for (uint64_t* r : {&s.mbp, &s.mbx[0], &s.mbx[1], &s.mbv[0], &s.mbv[1], &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
-    for (uint64_t* r : {&s.rdy_v[0], &s.rdy_v[1], &s.rdy_x[0], &s.rdy_x[1]}) mbar_init(r, AGG ? GW : GW / 2);
-    for (uint64_t* r : {&s.rdy_s, &s.rdy_q, &s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
+    for (uint64_t* r : {&s.mbx[0], &s.mbx[1], &s.mbv, &s.mbp, &s.mbq, &s.mbo, &s.o_free}) mbar_init(r, 1);
+    for (uint64_t* r : {&s.rdy_x[0], &s.rdy_x[1], &s.rdy_s}) mbar_init(r, 2 * GW);
+    for (uint64_t* r : {&s.rdy_p, &s.rdy_o}) mbar_init(r, GW);
     mbar_init_fence();
   }
   if (tid < 512) reinterpret_cast<unsigned*>(s.bad)[tid] = 0;
@@ -319,8 +328,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
   tmem_fence_after_sync();
   const uint32_t tm = __shfl_sync(~0u, s.tmem, 0);
   LinWait wait;
-  auto ready = [&](uint64_t* bar) {  // this warp's tensor-memory accesses so far are done
-    tmem_wait_st();
+  auto ready = [&](uint64_t* bar, bool wrote) {  // this warp's tensor-memory accesses so far are done
+    if (wrote) tmem_wait_st();
     tmem_fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
@@ -330,7 +339,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 
   // registers go to the warps that hold the state: (RA + RB + RC) x 256 + RM x
   // 128 is what the block was launched with
-  constexpr int LAUNCHED = 65536 / THREADS / 8 * 8, RA = 88, RB = 72, RC = 72, RM = 40;
+  constexpr int LAUNCHED = 65536 / THREADS / 8 * 8, RA = 104, RB = 64, RC = 64, RM = 40;
   static_assert((RA + RB + RC) * GROUP + RM * 128 <= LAUNCHED * THREADS, "registers of the block");
   static_assert(RA >= LAUNCHED && RB <= LAUNCHED && RC <= LAUNCHED && RM <= LAUNCHED, "inc only raises, dec only lowers");
   if (warp >= 3 * GW) {
@@ -416,9 +425,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           // (an address in a descriptor counts 16 bytes)
           const uint64_t kd = tc_desc(st, 16, 1024), qd = tc_desc(st + TILE, 16, 1024);  // K, Q by rows
           const uint64_t kn = tc_desc(st, (AGG ? 1 : 2) * TILE, 1024), vn = tc_desc(st + 4 * TILE, TILE, 1024);  // K, V by columns
-          wait(&s.full[g.i], g.par);
-          if (!AGG && n > 0) wait(&s.rdy_p, par ^ 1);  // the last chunk's P is read
-          if (!AGG && wait.ok()) {                     // Q K^T
+          wait(&s.rdy_x[two(n)], two_par(n));  // (whoever wrote V' has seen the step's tiles)
+          if (!AGG && wait.ok()) {  // Q K^T: the last P was read before its product
             tmem_fence_after_sync();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
@@ -427,50 +435,22 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             }
             tc_commit(&s.mbp);
           }
-          if (AGG) {
-            wait(&s.rdy_v[n & 1], two_par(n));                  // V' is in tensor memory
-            if (n >= BACK) wait(&s.rdy_x[n & 1], two_par(n) ^ 1);  // the X before is read
-            if (wait.ok()) {
-              tmem_fence_after_sync();
+          if (wait.ok()) {
+            tmem_fence_after_sync();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
 #pragma unroll
               for (int p = 0; p < 4; ++p)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
-                            (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A),
-                            p + ks > 0);
-              tc_commit(&s.mbx[n & 1]);
-              tc_commit(&s.empty[g.i]);
+                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
+                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A),
+                          p + ks > 0);
+              if (!AGG && ks == 1) tc_commit(&s.mbv);  // half of V' can be written again
             }
-            continue;
+            tc_commit(&s.mbx[two(n)]);
+            if (AGG) tc_commit(&s.empty[g.i]);
           }
-          // X in quarters: half of the tokens of either half of the keys, then
-          // the other half.  So half of V' can be written, and half of X read,
-          // while the rest is multiplied.
-#pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-            wait(&s.rdy_v[kh], par);  // this half of V' is in tensor memory
-#pragma unroll
-            for (int nh = 0; nh < 2; ++nh) {
-              if (kh == 0 && n > 0) wait(&s.rdy_x[nh], par ^ 1);  // the last X is read (idle warps keep step here)
-              if (nh < nk && wait.ok()) {
-                tmem_fence_after_sync();
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-#pragma unroll
-                  for (int ks = 2 * kh; ks < 2 * kh + 2; ++ks)
-                    tc_mma_ts(tm + T_X + nh * 64, tm + T_V + p * 32 + ks * 8, kn + ((nh * 2 * TILE + ks * 2048) >> 4),
-                              tc_idesc(128, 64, false, true) | (p & 1 ? 0u : TC_NEGATE_A), p + ks > 0);
-                if (kh == 1) tc_commit(&s.mbx[nh]);
-              }
-            }
-            if (wait.ok()) {
-              tc_commit(&s.mbv[kh]);
-              if (kh == 1 && nk == 1) tc_commit(&s.mbx[1]);
-            }
-          }
-          wait(&s.rdy_s, par);                     // S is in tensor memory
-          if (n > 0) wait(&s.rdy_q, par ^ 1);      // the last outputs are read
+          if (AGG) continue;
+          wait(&s.rdy_s, par);
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
@@ -478,7 +458,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
               if (ks < 4 * nk) tc_mma_ts(tm + T_Q, tm + T_S + ks * 8, qd + (((ks >> 2) * 2 * TILE + (ks & 3) * 32) >> 4), tc_idesc(128, 64, false, false), ks > 0);
             tc_commit(&s.mbq);
           }
-          wait(&s.rdy_p, par);                     // P is in shared memory
+          wait(&s.rdy_p, par);
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
@@ -503,24 +483,33 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     float2 S[32];  // S^T[row][64 hf + k]
 
     grid_dep_wait();  // the segments' states, too
-    int flags = 0;
+    if (lane == 0)  // no X before the first
+      for (int i = 0; i < BACK; ++i) mbar_arrive(&s.rdy_x[i]);
+    int flags = F_LAST;  // of the step before
     LinStage<NST> g;
 #pragma unroll 1
     for (int n = 0; n <= walk.n; ++n, g.next()) {
       if (n > 0) {  // S = lam^n S + X of the step before
-        const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
-        wait(&s.mbx[two(n - 1, hf)], two_par(n - 1));
+        wait(&s.mbx[two(n - 1)], two_par(n - 1));
         tmem_fence_after_sync();
+        // (the factors and the step's place are there: the products were issued behind them)
+        const float2 dec = f2b(s.vec[(n - 1) & 7].dec);
         if (!idle) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float2 x[8];
-            tc_ld16(tq + at_x(n - 1) + hf * 64 + q * 16, x);
+          for (int q = 0; q < 4; q += 2) {
+            float2 x[8], y[8];
+            tc_ld_rows(tq + at_x(n - 1) + hf * 64 + q * 16, x);
+            tc_ld_rows(tq + at_x(n - 1) + hf * 64 + q * 16 + 16, y);
+            tc_wait_frag(x);
+            tc_wait_frag(y);
 #pragma unroll
             for (int k = 0; k < 8; ++k) S[q * 8 + k] = __ffma2_rn(dec, S[q * 8 + k], x[k]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) S[q * 8 + 8 + k] = __ffma2_rn(dec, S[q * 8 + 8 + k], y[k]);
           }
         }
-        ready(&s.rdy_x[two(n - 1, hf)]);
+        ready(&s.rdy_x[two(n - 1)], false);
+        flags = s.info[(n - 1) & 7].flags;
         if (flags & F_LAST) {  // where the run leaves its state
           const LinInfo t = s.info[(n - 1) & 7];
           const LinPass& p = a.p[t.pass];
@@ -551,8 +540,6 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         }
         if (n == walk.n) break;
       }
-      wait(&s.full[g.i], g.par);
-      flags = s.info[n & 7].flags;
       if (AGG) {
         if (n == 0) {
 #pragma unroll
@@ -560,10 +547,11 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         }
         continue;
       }
-      if (flags & F_FIRST) {  // the state a run starts from
+      if (flags & F_LAST) {  // the state a run starts from
+        wait(&s.full[g.i], g.par);
         const LinInfo t = s.info[n & 7];
         const LinPass& p = a.p[t.pass];
-        if (flags & F_TAKE && wait.ok()) wait.tries = flag_wait(a.flags + t.item) ? wait.tries : 0;
+        if (t.flags & F_TAKE && wait.ok()) wait.tries = flag_wait(a.flags + t.item) ? wait.tries : 0;
         if (t.w > 0 || a.segs > 1) {
           const float* src = a.seg_start + (((size_t)t.item * a.segs + seg) * LIN_DMAX + hf * 64) * LIN_DMAX + row;
 #pragma unroll
@@ -600,7 +588,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           tc_st8(tq + T_S + hf * 32 + p * 8, x);
         }
       }
-      ready(&s.rdy_s);
+      ready(&s.rdy_s, true);
     }
   } else if (warp < 2 * GW) {
     // V': 32 values (this warp's lanes) of 32 tokens, transposed on their way out of shared memory
@@ -669,7 +657,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         fence_proxy_async();
       }
       if (n >= BACK) {
-        wait(AGG ? &s.mbx[n & 1] : &s.mbv[hf], two_par(n) ^ 1);
+        wait(AGG || hf ? &s.mbx[two(n)] : &s.mbv, two_par(n) ^ 1);
         tmem_fence_after_sync();
       }
       if (!idle) {
@@ -680,7 +668,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           for (int m = 0; m < 4; ++m) tc_st_frag(tq + (h << 20) + at_v(n) + m * 32 + hf * 16, y[m]);
         }
       }
-      ready(&s.rdy_v[two(n, hf)]);
+      ready(&s.rdy_x[two(n)], true);
     }
   } else {  // the outputs
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RB));
@@ -731,8 +719,8 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
               }
             }
         }
-        ready(&s.rdy_q);
       }
+      ready(&s.rdy_s, false);
       if (n < walk.n) {  // P: rows 16 quad .., columns 32 hf ..
         float2 x[8];  // [column block of 8][row + 8]
         wait(&s.mbp, n & 1);  // (and with it the factors, which the products were issued behind)
@@ -774,7 +762,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           }
         }
         fence_proxy_async();
-        ready(&s.rdy_p);
+        ready(&s.rdy_p, false);
       }
       if (n > 0) {
         if (n > 1) wait(&s.o_free, n & 1);
