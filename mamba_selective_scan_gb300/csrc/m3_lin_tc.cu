@@ -425,7 +425,7 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           // (an address in a descriptor counts 16 bytes)
           const uint64_t kd = tc_desc(st, 16, 1024), qd = tc_desc(st + TILE, 16, 1024);  // K, Q by rows
           const uint64_t kn = tc_desc(st, (AGG ? 1 : 2) * TILE, 1024), vn = tc_desc(st + 4 * TILE, TILE, 1024);  // K, V by columns
-          wait(&s.rdy_x[two(n)], two_par(n));  // (whoever wrote V' has seen the step's tiles)
+          wait(&s.full[g.i], g.par);
           if (!AGG && wait.ok()) {  // Q K^T: the last P was read before its product
             tmem_fence_after_sync();
 #pragma unroll
@@ -435,16 +435,16 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
             }
             tc_commit(&s.mbp);
           }
+          wait(&s.rdy_x[two(n)], two_par(n));
           if (wait.ok()) {
             tmem_fence_after_sync();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-#pragma unroll
-              for (int p = 0; p < 4; ++p)
-                tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
-                          (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A),
-                          p + ks > 0);
-              if (!AGG && ks == 1) tc_commit(&s.mbv);  // half of V' can be written again
+            for (int i = 0; i < 16; ++i) {
+              // half of the tokens after the other, and few changes of the kind of MMA
+              const int half = i >> 3, p = (i & 2) | ((i >> 2 ^ i >> 3) & 1), ks = half * 2 | (i & 1);
+              tc_mma_ts(tm + at_x(n), tm + at_v(n) + p * 32 + ks * 8, kn + (ks * 2048 >> 4),
+                        (nk > 1 ? tc_idesc(128, 128, false, true) : tc_idesc(128, 64, false, true)) | (p & 1 ? 0u : TC_NEGATE_A), i > 0);
+              if (!AGG && i == 7) tc_commit(&s.mbv);  // half of V' can be written again
             }
             tc_commit(&s.mbx[two(n)]);
             if (AGG) tc_commit(&s.empty[g.i]);
@@ -676,9 +676,10 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
     const int i0 = quad * 16, j0 = hf * 32;
     const bool idle = (int)quad * 32 >= DV;  // (P's rows are tokens: no warp is idle there)
     const int pz_at = TC + j0 + 2 * (lane & 3) - i0 - (lane >> 2) - ((lane >> 2) & 1);  // (even)
-    // where this thread's first value goes: bf16 (rows of 64 values), f32 (of 32)
-    const uint32_t op32 = st0 + OUT + quad * TILE + sw(j0 + 2 * (lane & 3), lane >> 4) + ((lane >> 2) & 3) * 4;
-    const uint32_t op = st0 + OUT + (quad >> 1) * TILE + sw(j0 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1));
+    const bool out_f32 = a.p[pass].out_f32;
+    // where this thread's first value goes: rows of 64 values (bf16), or of 32
+    const uint32_t op = st0 + OUT + (out_f32 ? quad * TILE + sw(j0 + 2 * (lane & 3), lane >> 4) + ((lane >> 2) & 3) * 4
+                                             : (quad >> 1) * TILE + sw(j0 + (lane & 7) + ((lane >> 4) << 3), (quad & 1) * 4 + ((lane >> 3) & 1)));
 #pragma unroll 1
     for (int n = 0; n <= (AGG ? -1 : walk.n); ++n) {
       // O of the step before: values 32 quad .. of tokens 32 hf ..
@@ -766,16 +767,14 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
       }
       if (n > 0) {
         if (n > 1) wait(&s.o_free, n & 1);
-        const LinInfo& t = s.info[(n - 1) & 7];
-        const LinPass& p = a.p[t.pass];
         if (idle) {
-        } else if (p.out_f32) {
+        } else if (out_f32) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               // value 16 h + 8 (c & 1) + lane / 4 of this warp's tile, tokens j0 + 8 (c >> 1) + 2 (lane & 3), + 1
-              const uint32_t at = (op32 ^ ((4 * h + 2 * (c & 1)) << 4)) + (c >> 1) * 1024;
+              const uint32_t at = (op ^ ((4 * h + 2 * (c & 1)) << 4)) + (c >> 1) * 1024;
               asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(o[h][c].x) : "memory");
               asm volatile("st.shared.f32 [%0], %1;" ::"r"((at ^ 16u) + 128u), "f"(o[h][c].y) : "memory");
             }
