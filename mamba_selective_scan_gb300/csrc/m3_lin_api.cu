@@ -55,11 +55,26 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 // 1024 chunks: nine segments, 269 us, where one takes 1225, four 522, 19 282;
 // 12 of 256 (2 x 8192): six, 71 us, where one takes 168 and nine 98; 48 heads of
 // 32: three, 46 us, where one takes 52.
-// f32: a unit is 64 tokens of the sequential kernel (13 us), four blocks of 32
-// columns per item, two blocks per SM.
+//
+// f32: a block takes 32 columns, so there are four per (item, segment).  A unit
+// is 64 tokens of an SM with three blocks at work for each of them, 7.6 us; one
+// or two alone take 1.5 and 2.4 units together, the ends half of that.  Training
+// passes: 1 x 2000 x 1 head, 32 segments: 76 us, one 692; 1 x 300 x 8, five: 87,
+// one 115; 4 x 1000 x 4, eight: 322, one 437; 2 x 512 x 16, one: 281, two 356;
+// 8 x 128 x 4, one: 80, two 108.
+double lin_cost(int64_t items, int m, int S, bool tc) {
+  if (tc) {
+    const double all = (double)((items * S + 151) / 152) * (m + 7.0);
+    return S > 1 ? all + (double)((items * (S - 1) + 151) / 152) * (m + 7.0) * 0.7 + 4.0 + 0.25 * S : all;
+  }
+  auto units = [&](int64_t parts) {
+    const int64_t blocks = (4 * parts + 151) / 152;  // of an SM
+    const double rest[3] = {0.0, 1.5, 2.4};
+    return (double)(blocks / 3 * 3) + rest[blocks % 3];
+  };
+  return S > 1 ? 1.03 * (units(items * S) + 0.5 * units(items * (S - 1))) * m + 0.8 + 0.03 * S : units(items) * m;
+}
 void lin_segments(int64_t items, int nc, bool tc, int* segs, int* seg_chunks) {
-  const int64_t at_once = tc ? 152 : 76;
-  const double up = tc ? 7.0 : 0.3, agg = tc ? 0.7 : 0.6, chain = tc ? 4.0 : 0.6, link = tc ? 0.25 : 0.03;
   const int least = tc ? 3 : 1;
   double best = 0.0;
   *segs = 1;
@@ -68,10 +83,9 @@ void lin_segments(int64_t items, int nc, bool tc, int* segs, int* seg_chunks) {
     const int m = (nc + want - 1) / want;
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
-    const double all = (double)((items * S + at_once - 1) / at_once) * (m + up);
-    const double ends = S > 1 ? (double)((items * (S - 1) + at_once - 1) / at_once) * (m + up) * agg + chain + link * S : 0.0;
-    if (want == 1 || all + ends < best - 1e-9) {
-      best = all + ends;
+    const double cost = lin_cost(items, m, S, tc);
+    if (want == 1 || cost < best - 1e-9) {
+      best = cost;
       *segs = S;
       *seg_chunks = m;
     }

@@ -74,11 +74,21 @@ __global__ void __launch_bounds__(256, 2) m3_lin_step_kernel(const __grid_consta
   }
 }
 
-// A sequence: 32 COLS columns of one head's state per block, eight lanes to
-// COLS neighbouring columns (a lane has rows 4 s .. 4 s + 3 of every 32).  16
-// tokens at a time are brought into shared memory, the next 16 in flight
-// meanwhile.  Within those 16 the state that they start from stays as it is and
-// what they add grows beside it from zero,
+// Four values into shared memory as f32: zeros where there are none
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(float* dst, const __nv_bfloat16* src, bool live) {
+  const uint2 x = live ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
+  *reinterpret_cast<float4*>(dst) = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                                                __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+}
+
+// A sequence: 32 columns of one head's state per block of four warps, eight
+// lanes to two neighbouring columns (a lane has rows 4 s .. 4 s + 3 of every
+// 32).  16 tokens at a time are brought into shared memory, the next 16 in
+// flight meanwhile.  Within those 16 the state that they start from stays as it
+// is and what they add grows beside it from zero,
 //
 //   o_i = scale (lam^{i+1} S0^T q_i + L_i^T q_i),  L_i = lam L_{i-1} + k_i v_i^T
 //
@@ -89,25 +99,28 @@ __global__ void __launch_bounds__(256, 2) m3_lin_step_kernel(const __grid_consta
 //
 // With every SM at work shared memory is the bound: a lane reads its 16 rows'
 // k and q of every token, 128 bytes, 32 wavefronts a warp whatever the lanes
-// share.  A second column per lane halves that (8 x 512 x 16 heads, training
-// pass: 1.05 instead of 1.34 ms); with few blocks the latency of a token counts,
-// 0.2 us with one column, 0.35 with two.
+// share.  A second column per lane halves that, a fourth needs more registers
+// than latency can spare (training passes, f32, heads of 128 x 128: 8 x 128 x 4
+// heads 82 us, with one column 99, with four 125; 8 x 512 x 16 heads 881, 1143,
+// 1037); blocks of eight warps are behind, too (101 and 891).
 //
 // blockIdx.z: time segments, from the chaining's start states.  AGG: only the
 // states, each segment's end from a zero start.
-template <typename T, int COLS, bool AGG>
-__global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constant__ LinArgs a) {
-  constexpr int NT = 16, TV = 32 * COLS;
-  __shared__ __align__(16) float kq[2][NT][LIN_DMAX];  // k, q
-  __shared__ float vs[NT][TV], os[NT][TV + 1];
+constexpr int SEQ_THREADS = 128, SEQ_COLS = 2;
+template <typename T, bool AGG>
+__global__ void __launch_bounds__(SEQ_THREADS, 3) m3_lin_seq_kernel(const __grid_constant__ LinArgs a) {
+  constexpr int NT = 16, COLS = SEQ_COLS, THREADS = SEQ_THREADS, TV = THREADS / 8 * COLS, KQ = AGG ? 1 : 2;
+  __shared__ __align__(16) float kq[2][KQ][NT][LIN_DMAX];  // k, q; of two tiles
+  __shared__ __align__(16) float vs[2][NT][TV];
+  __shared__ float os[NT][TV + 1];
   __shared__ float pw[NT];  // the start state's weight in each token's output
   const LinPass& p = a.p[blockIdx.y];
   constexpr int MAX_TILES = LIN_DMAX / TV;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int bh = blockIdx.x / MAX_TILES, v0 = (blockIdx.x % MAX_TILES) * TV;
   if (v0 >= p.DV) return;
   const int b = bh / a.Hv, h = bh % a.Hv;
-  const int s = lane & 7, col = (warp * 4 + (lane >> 3)) * COLS;
+  const int s = lane & 7, col = (tid >> 3) * COLS;
   // this segment's tokens, in the pass's order
   const int seg = blockIdx.z, seg_tok = a.seg_chunks * LIN_C, odd = p.rev ? a.nc * LIN_C - a.T : 0;
   const int first = seg ? seg * seg_tok - odd : 0, last = seg + 1 < a.segs ? (seg + 1) * seg_tok - odd : a.T;
@@ -116,6 +129,34 @@ __global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constan
   auto where = [&](int k, int c) { return p.st ? sbase + (size_t)(v0 + col + c) * p.DK + k : sbase + (size_t)k * p.DV + v0 + col + c; };
   auto row = [&](int i) { return (i >> 2) * 32 + s * 4 + (i & 3); };
 
+  const float ld = lin_ld(a.ld[h]);
+  const float fv = p.rev ? a.scale : 1.0f, fo = p.rev ? 1.0f : a.scale;
+  if (tid < NT) pw[tid] = expf(ld * (float)(p.rev ? tid : tid + 1));
+  const float2 lam = f2b(expf(ld));
+  const int64_t tok0 = (int64_t)b * a.T;
+  const T* kp = static_cast<const T*>(p.k) + tok0 * p.ks + (int64_t)(h / p.kh) * p.DK;
+  const T* qp = static_cast<const T*>(p.q) + tok0 * p.qs + (int64_t)(h / p.qh) * p.DK;
+  const T* vp = static_cast<const T*>(p.v) + tok0 * p.vs + (int64_t)(h / p.vh) * p.DV + v0;
+  const size_t ob = (size_t)tok0 * p.os + (size_t)(h / p.oh) * p.DV + v0;
+  auto time = [&](int i) { return (int64_t)(p.rev ? a.T - 1 - i : i); };  // of the pass's i-th token
+
+  // four values a thread on their way into a tile, zeros past the ends
+  auto fetch = [&](int buf, int t0) {
+#pragma unroll
+    for (int j = 0; j < KQ * NT * 32 / THREADS; ++j) {
+      const int e = tid + j * THREADS, which = e / (NT * 32), i = e / 32 % NT, c = e % 32 * 4;
+      const bool live = t0 + i < last && c < p.DK;
+      copy4(&kq[buf][which][i][c], live ? (which ? qp + time(t0 + i) * p.qs : kp + time(t0 + i) * p.ks) + c : kp, live);
+    }
+#pragma unroll
+    for (int j = 0; j < (NT * TV / 4 + THREADS - 1) / THREADS; ++j) {
+      const int e = tid + j * THREADS, i = e / (TV / 4), c = e % (TV / 4) * 4;
+      const bool live = t0 + i < last && v0 + c < p.DV;
+      if (i < NT) copy4(&vs[buf][i][c], live ? vp + time(t0 + i) * p.vs + c : vp, live);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(0, first);
   float2 S[COLS][8], L[COLS][8];  // rows row(2 i), row(2 i + 1)
   grid_dep_wait();
 #pragma unroll
@@ -130,40 +171,11 @@ __global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constan
       }
       (i & 1 ? S[c][i >> 1].y : S[c][i >> 1].x) = x;
     }
-  const float ld = lin_ld(a.ld[h]);
-  const float fv = p.rev ? a.scale : 1.0f, fo = p.rev ? 1.0f : a.scale;
-  if (tid < NT) pw[tid] = expf(ld * (float)(p.rev ? tid : tid + 1));
-  const float2 lam = f2b(expf(ld));
-  const int64_t tok0 = (int64_t)b * a.T;
-  const int c0 = tid & (LIN_DMAX - 1), which = tid >> 7;  // this thread brings column c0 of k (0) or q (1)
-  const int64_t xs = which ? p.qs : p.ks;
-  const T* xp = static_cast<const T*>(which ? p.q : p.k) + tok0 * xs + (int64_t)(h / (which ? p.qh : p.kh)) * p.DK + c0;
-  const T* vp = static_cast<const T*>(p.v) + tok0 * p.vs + (int64_t)(h / p.vh) * p.DV + v0;
-  const size_t ob = (size_t)tok0 * p.os + (size_t)(h / p.oh) * p.DV + v0;
-  auto time = [&](int i) { return (int64_t)(p.rev ? a.T - 1 - i : i); };  // of the pass's i-th token
-
-  float x[NT], v[2][COLS];
-  auto fetch = [&](int t0) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) x[i] = t0 + i < last && c0 < p.DK && !(AGG && which) ? Act<T>::ld(xp + time(t0 + i) * xs) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = t0 + warp + i * 8;
-#pragma unroll
-      for (int c = 0; c < COLS; ++c)
-        v[i][c] = t < last && v0 + lane + 32 * c < p.DV ? Act<T>::ld(vp + time(t) * p.vs + lane + 32 * c) : 0.0f;
-    }
-  };
-  fetch(first);
-  for (int t0 = first; t0 < last; t0 += NT) {
-#pragma unroll
-    for (int i = 0; i < NT; ++i) kq[which][i][c0] = x[i];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int c = 0; c < COLS; ++c) vs[warp + i * 8][lane + 32 * c] = v[i][c] * fv;
+  int buf = 0;
+  for (int t0 = first; t0 < last; t0 += NT, buf ^= 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    if (t0 + NT < last) fetch(t0 + NT);
+    if (t0 + NT < last) fetch(buf ^ 1, t0 + NT);
     const int n = min(NT, last - t0);
 #pragma unroll
     for (int c = 0; c < COLS; ++c)
@@ -178,17 +190,19 @@ __global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < COLS; ++c) old[c] = sum[c] = f2b(0.0f);
         if (g + j < n) {
+          float2 vv[COLS];
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) vv[c] = f2b(vs[buf][g + j][col + c] * fv);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 kk = *reinterpret_cast<const float4*>(&kq[0][g + j][i * 32 + s * 4]);
+            const float4 kk = *reinterpret_cast<const float4*>(&kq[buf][0][g + j][i * 32 + s * 4]);
             float4 q;
-            if (!AGG) q = *reinterpret_cast<const float4*>(&kq[1][g + j][i * 32 + s * 4]);
+            if (!AGG) q = *reinterpret_cast<const float4*>(&kq[buf][KQ - 1][g + j][i * 32 + s * 4]);
             const float2 q0 = make_float2(q.x, q.y), q1 = make_float2(q.z, q.w);
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
-              const float2 vv = f2b(vs[g + j][col + c]);
-              L[c][2 * i] = __ffma2_rn(lam, L[c][2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv));
-              L[c][2 * i + 1] = __ffma2_rn(lam, L[c][2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv));
+              L[c][2 * i] = __ffma2_rn(lam, L[c][2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv[c]));
+              L[c][2 * i + 1] = __ffma2_rn(lam, L[c][2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv[c]));
               if (AGG) continue;
               sum[c] = __ffma2_rn(L[c][2 * i], q0, sum[c]);
               old[c] = __ffma2_rn(S[c][2 * i], q0, old[c]);
@@ -224,17 +238,16 @@ __global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         S[c][i] = __ffma2_rn(f2b(d.near), S[c][i], __ffma2_rn(f2b(d.off), S[c][i], __fmul2_rn(fl, L[c][i])));
+    if (AGG) continue;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = warp + i * 8;
-#pragma unroll
-      for (int c = 0; c < (AGG ? 0 : COLS); ++c)
-        if (j < n && v0 + lane + 32 * c < p.DV) {
-          const size_t at = ob + (size_t)time(t0 + j) * p.os + lane + 32 * c;
-          if (p.out_f32) static_cast<float*>(p.out)[at] = os[j][lane + 32 * c];
-          else Act<T>::st(static_cast<T*>(p.out) + at, os[j][lane + 32 * c]);
-        }
+    for (int j = 0; j < NT * TV / THREADS; ++j) {
+      const int e = tid + j * THREADS, i = e / TV, c = e % TV;
+      if (i < n && v0 + c < p.DV) {
+        const size_t at = ob + (size_t)time(t0 + i) * p.os + c;
+        if (p.out_f32) static_cast<float*>(p.out)[at] = os[i][c];
+        else Act<T>::st(static_cast<T*>(p.out) + at, os[i][c]);
+      }
     }
   }
   if (AGG) {
@@ -251,20 +264,18 @@ __global__ void __launch_bounds__(256, 2) m3_lin_seq_kernel(const __grid_constan
   }
 }
 
-template <typename T, int COLS>
+template <typename T>
 cudaError_t launch_lin_seq(const LinArgs& a, cudaStream_t st) {
-  const unsigned x = (unsigned)((int64_t)a.B * a.Hv * (LIN_DMAX / (32 * COLS)));
+  const unsigned x = (unsigned)((int64_t)a.B * a.Hv * (LIN_DMAX / (SEQ_THREADS / 8 * SEQ_COLS)));
   cudaError_t e = cudaSuccess;
   if (a.segs > 1) {  // (the last segment's end is nobody's start)
-    e = launch_k(m3_lin_seq_kernel<T, COLS, true>, dim3(x, a.np, a.segs - 1), 256, 0, st, false, a);
+    e = launch_k(m3_lin_seq_kernel<T, true>, dim3(x, a.np, a.segs - 1), SEQ_THREADS, 0, st, false, a);
     if (e == cudaSuccess) e = launch_lin_seg(a, st);
   }
-  return e == cudaSuccess ? launch_k(m3_lin_seq_kernel<T, COLS, false>, dim3(x, a.np, a.segs), 256, 0, st, a.segs > 1, a) : e;
+  return e == cudaSuccess ? launch_k(m3_lin_seq_kernel<T, false>, dim3(x, a.np, a.segs), SEQ_THREADS, 0, st, a.segs > 1, a) : e;
 }
 
-// One token of one pass (decoding): wide blocks once there are two per SM.
-// Sequences: two columns per lane once blocks of one fill the SMs (two each)
-// more than twice.
+// One token of one pass (decoding): wide blocks once there are two per SM
 template <typename T>
 cudaError_t launch_lin_rec(LinArgs a, cudaStream_t st, int sms) {
   const int64_t heads = (int64_t)a.B * a.Hv;
@@ -279,8 +290,7 @@ cudaError_t launch_lin_rec(LinArgs a, cudaStream_t st, int sms) {
     a.segs = 1;
     a.nc = a.seg_chunks = (a.T + LIN_C - 1) / LIN_C;
   }
-  const int64_t blocks = heads * a.np * a.segs * ((a.p[0].DV + 31) / 32);
-  return blocks > 4 * (int64_t)sms ? launch_lin_seq<T, 2>(a, st) : launch_lin_seq<T, 1>(a, st);
+  return launch_lin_seq<T>(a, st);
 }
 template cudaError_t launch_lin_rec<float>(LinArgs, cudaStream_t, int);
 template cudaError_t launch_lin_rec<__nv_bfloat16>(LinArgs, cudaStream_t, int);
