@@ -1,5 +1,7 @@
 // m3_lin_rec.cu -- linear attention with a decay for each head, token by
 // token: decoding, and sequences of f32 activations.
+#include <type_traits>
+
 #include "m3_lin.cuh"
 
 namespace m3 {
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(256, 2) m3_lin_step_kernel(const __grid_consta
 
 // Four values into shared memory as f32: zeros where there are none
 __device__ __forceinline__ void copy4(float* dst, const float* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0) : "memory");
+  cp_async16(dst, src, live);
 }
 __device__ __forceinline__ void copy4(float* dst, const __nv_bfloat16* src, bool live) {
   const uint2 x = live ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
@@ -101,8 +103,9 @@ __device__ __forceinline__ void copy4(float* dst, const __nv_bfloat16* src, bool
 // k and q of every token, 128 bytes, 32 wavefronts a warp whatever the lanes
 // share.  A second column per lane halves that, a fourth needs more registers
 // than latency can spare (training passes, f32, heads of 128 x 128: 8 x 128 x 4
-// heads 82 us, with one column 99, with four 125; 8 x 512 x 16 heads 881, 1143,
-// 1037); blocks of eight warps are behind, too (101 and 891).
+// heads 78 us, 8 x 512 x 16 heads 849; before the last step 82 and 881, with one
+// column 99 and 1143, with four 125 and 1037, in blocks of eight warps 101 and
+// 891).
 //
 // blockIdx.z: time segments, from the chaining's start states.  AGG: only the
 // states, each segment's end from a zero start.
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 3) m3_lin_seq_kernel(const __grid
       const bool live = t0 + i < last && v0 + c < p.DV;
       if (i < NT) copy4(&vs[buf][i][c], live ? vp + time(t0 + i) * p.vs + c : vp, live);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    cp_async_commit();
   };
   fetch(0, first);
   float2 S[COLS][8], L[COLS][8];  // rows row(2 i), row(2 i + 1)
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 3) m3_lin_seq_kernel(const __grid
     }
   int buf = 0;
   for (int t0 = first; t0 < last; t0 += NT, buf ^= 1) {
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    cp_async_wait<0>();
     __syncthreads();
     if (t0 + NT < last) fetch(buf ^ 1, t0 + NT);
     const int n = min(NT, last - t0);
@@ -181,56 +184,60 @@ __global__ void __launch_bounds__(SEQ_THREADS, 3) m3_lin_seq_kernel(const __grid
     for (int c = 0; c < COLS; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) L[c][i] = f2b(0.0f);
+    auto tile = [&](auto whole) {  // (whole tiles without a condition for each token: 4 % faster)
 #pragma unroll
-    for (int g = 0; g < NT; g += 8) {
-      float o[COLS][8];
+      for (int g = 0; g < NT; g += 8) {
+        float o[COLS][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float2 old[COLS], sum[COLS];
+        for (int j = 0; j < 8; ++j) {
+          float2 old[COLS], sum[COLS];
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) old[c] = sum[c] = f2b(0.0f);
-        if (g + j < n) {
-          float2 vv[COLS];
+          for (int c = 0; c < COLS; ++c) old[c] = sum[c] = f2b(0.0f);
+          if (whole.value || g + j < n) {
+            float2 vv[COLS];
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) vv[c] = f2b(vs[buf][g + j][col + c] * fv);
+            for (int c = 0; c < COLS; ++c) vv[c] = f2b(vs[buf][g + j][col + c] * fv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 kk = *reinterpret_cast<const float4*>(&kq[buf][0][g + j][i * 32 + s * 4]);
-            float4 q;
-            if (!AGG) q = *reinterpret_cast<const float4*>(&kq[buf][KQ - 1][g + j][i * 32 + s * 4]);
-            const float2 q0 = make_float2(q.x, q.y), q1 = make_float2(q.z, q.w);
+            for (int i = 0; i < 4; ++i) {
+              const float4 kk = *reinterpret_cast<const float4*>(&kq[buf][0][g + j][i * 32 + s * 4]);
+              float4 q;
+              if (!AGG) q = *reinterpret_cast<const float4*>(&kq[buf][KQ - 1][g + j][i * 32 + s * 4]);
+              const float2 q0 = make_float2(q.x, q.y), q1 = make_float2(q.z, q.w);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-              L[c][2 * i] = __ffma2_rn(lam, L[c][2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv[c]));
-              L[c][2 * i + 1] = __ffma2_rn(lam, L[c][2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv[c]));
-              if (AGG) continue;
-              sum[c] = __ffma2_rn(L[c][2 * i], q0, sum[c]);
-              old[c] = __ffma2_rn(S[c][2 * i], q0, old[c]);
-              sum[c] = __ffma2_rn(L[c][2 * i + 1], q1, sum[c]);
-              old[c] = __ffma2_rn(S[c][2 * i + 1], q1, old[c]);
+              for (int c = 0; c < COLS; ++c) {
+                L[c][2 * i] = __ffma2_rn(lam, L[c][2 * i], __fmul2_rn(make_float2(kk.x, kk.y), vv[c]));
+                L[c][2 * i + 1] = __ffma2_rn(lam, L[c][2 * i + 1], __fmul2_rn(make_float2(kk.z, kk.w), vv[c]));
+                if (AGG) continue;
+                sum[c] = __ffma2_rn(L[c][2 * i], q0, sum[c]);
+                old[c] = __ffma2_rn(S[c][2 * i], q0, old[c]);
+                sum[c] = __ffma2_rn(L[c][2 * i + 1], q1, sum[c]);
+                old[c] = __ffma2_rn(S[c][2 * i + 1], q1, old[c]);
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) sum[c] = __ffma2_rn(f2b(pw[g + j]), old[c], sum[c]);
+          }
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) o[c][j] = sum[c].x + sum[c].y;
+        }
+        // lane s ends with the sum of token g + s
+#pragma unroll
+        for (int c = 0; c < (AGG ? 0 : COLS); ++c) {
+#pragma unroll
+          for (int m = 4; m > 0; m >>= 1) {
+            const bool up = s & m;
+#pragma unroll
+            for (int j = 0; j < m; ++j) {
+              const float give = up ? o[c][j] : o[c][j + m], keep = up ? o[c][j + m] : o[c][j];
+              o[c][j] = keep + __shfl_xor_sync(~0u, give, m);
             }
           }
-#pragma unroll
-          for (int c = 0; c < COLS; ++c) sum[c] = __ffma2_rn(f2b(pw[g + j]), old[c], sum[c]);
+          os[g + s][col + c] = o[c][0] * fo;
         }
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) o[c][j] = sum[c].x + sum[c].y;
       }
-      // lane s ends with the sum of token g + s
-#pragma unroll
-      for (int c = 0; c < (AGG ? 0 : COLS); ++c) {
-#pragma unroll
-        for (int m = 4; m > 0; m >>= 1) {
-          const bool up = s & m;
-#pragma unroll
-          for (int j = 0; j < m; ++j) {
-            const float give = up ? o[c][j] : o[c][j + m], keep = up ? o[c][j + m] : o[c][j];
-            o[c][j] = keep + __shfl_xor_sync(~0u, give, m);
-          }
-        }
-        os[g + s][col + c] = o[c][0] * fo;
-      }
-    }
+    };
+    if (n == NT) tile(std::true_type{});
+    else tile(std::false_type{});
     const LinDecay d = lin_decay(ld, n);
     const float2 fl = p.rev ? lam : f2b(1.0f);
 #pragma unroll
