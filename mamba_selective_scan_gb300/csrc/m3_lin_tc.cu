@@ -268,17 +268,23 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // issues the MMAs, 25 the loads (and makes the factors), 26 the stores.
 //
 // Bound: a chunk of a 128 x 128 head is 64 KB, 1.4 us at an SM's share of HBM's
-// rate, and takes 1.2 to 1.4 us (2400 cycles), in which the tensor cores work
-// 1500, issue slots are 55 % busy and shared memory 50 %: the outputs' warps go
-// through reading, weighing and writing one after the other, 2100 to 2400
-// cycles.  Measured: 4 x 4096 x 40 heads, forward 112 us (650 MB: 86 % of HBM's
-// rate), the three backward passes side by side 290 us (1.56 GB, 79 %); 1 x
-// 65536 x 16 heads in nine segments 268 us, where its last part runs at 95 %.
-// Each role's code unrolled by tile was bound by instruction fetches (11000
-// instructions, 86 us for 8 x 2048 x 12 heads); rolled up it is 3700 and takes
-// 50.  A second warp issuing MMAs, and prefetches of later chunks into L2, made
-// nothing faster.  The state's warps spill 70 bytes a thread, where runs start
-// and end.
+// rate, and takes some 2350 cycles (1.15 us at 2.07 GHz), of which the tensor
+// cores work 1670: 1024 on X, 256 on Q K^T (64 rows at half their rate), 256 on
+// S Q^T, 128 on O.  The rest is P: its products wait for X to be read, and O for
+// the outputs' warps, which read, weigh and write the chunk before first (2100
+// cycles a chunk, the longest of the roles).  Measured: 8 x 2048 x 12 heads 49
+// us; 4 x 4096 x 40 heads, forward 110 us (650 MB: 87 % of HBM's rate), the three
+// backward passes side by side 284 us (1.56 GB, 81 %); 1 x 65536 x 16 heads in
+// nine segments 263 us.  Minutes of such work meet the power limit: at 1.7 GHz
+// the latter two take 450 and 294.
+//
+// Tried: each role's code unrolled by tile (11000 instructions: bound by their
+// fetches, 86 us for 8 x 2048 x 12 heads; rolled up it is 3600); a second warp
+// issuing MMAs, and prefetches of later chunks into L2 (no faster); P by four
+// warps of its own (8 x 2048 x 12 heads 55 us, heads of 64 x 64 17 % slower), or by
+// the warps of V' (55): every wait and arrival takes its share of the issue slots,
+// so fewer and longer roles win; barriers polled without suspending (25 %
+// slower).
 //
 // AGG: only the states, each time segment's end from a zero start (into
 // seg_end); no queries, no outputs.  FINE: P in two terms.
