@@ -48,13 +48,14 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 }
 
 // Time segments of the tensor-core kernels for few items.  A block per (item,
-// segment) takes a unit of time per chunk (1.25 us) and seven to come up and to
-// end; with S segments, first the ends of the S - 1 earlier ones are found (0.7
-// units per chunk), then a kernel chains them, then all S run.  The count with
-// the least total is taken, with at least three chunks per segment.  16 heads of
-// 1024 chunks: nine segments, 269 us, where one takes 1225, four 522, 19 282;
-// 12 of 256 (2 x 8192): six, 71 us, where one takes 168 and nine 98; 48 heads of
-// 32: three, 46 us, where one takes 52.
+// segment) takes a unit of time per chunk (1.2 us) and eight to come up and to
+// end; with S segments, first the ends of the S - 1 earlier ones are found (0.8
+// units per chunk, two more), then a kernel chains them, then all S run.  The
+// count with the least total is taken, with at least three chunks per segment.
+// 16 heads of 1024 chunks: nine segments, 263 us, where one takes 1200 and eight
+// 282; 24 of 128: six, 70, where one takes 163 and seven 87; 12 of 16: five, 26,
+// where one takes 30; 48 of 32: three, 46, where one takes 49 and two 54; 72 of
+// 64: one, 88, where two take 93.
 //
 // f32: a block takes 32 columns, so there are four per (item, segment).  A unit
 // is 64 tokens of an SM with three blocks at work for each of them, 7.6 us; one
@@ -64,8 +65,8 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 // 8 x 128 x 4, one: 80, two 108.
 double lin_cost(int64_t items, int m, int S, bool tc) {
   if (tc) {
-    const double all = (double)((items * S + 151) / 152) * (m + 7.0);
-    return S > 1 ? all + (double)((items * (S - 1) + 151) / 152) * (m + 7.0) * 0.7 + 4.0 + 0.25 * S : all;
+    const double all = (double)((items * S + 151) / 152) * (m + 8.0);
+    return S > 1 ? all + (double)((items * (S - 1) + 151) / 152) * (0.8 * m + 2.0) + 4.0 + 0.3 * S : all;
   }
   auto units = [&](int64_t parts) {
     const int64_t blocks = (4 * parts + 151) / 152;  // of an SM
