@@ -615,7 +615,10 @@ m3_status m3scan_qkrot_bwd(const m3_qkrot_dims* dims, m3_dtype act, const void* 
  * starts from and the weights between its tokens are each rounded to bf16 once
  * (the weights to two bf16 terms where seq_len is at most 512), which is of the
  * size of the outputs' own rounding.  The gradients are computed the same way.
- * Outputs and states are not finite exactly where the recurrence's are not.
+ * Inputs that are not finite reach exactly the outputs and states that they reach
+ * in the recurrence.  Of a head that grows (log_decay > 0) exp(log_decay * seq_len)
+ * and the products q.k have to be within f32's range: powers of the decay of up to
+ * seq_len tokens are factors of their own.
  */
 typedef struct {
     int64_t batch, seq_len, k_heads, v_heads, head_k, head_v;

@@ -148,7 +148,9 @@ struct LinCursor : LinInfo {
 };
 
 // One warp: a step's factors.  Those of tokens stay in their slot while the
-// head and the chunk's length do; the state's decay is made anew.
+// head and the chunk's length do; the state's decay is made anew.  Factors of
+// as many tokens as the chunk does not have are 0: of a head that grows they
+// may pass f32's range, and what they would multiply are zeros.
 __device__ __forceinline__ void lin_factors(const LinArgs& a, const LinInfo& t, LinVec& v, int lane) {
   const bool rev = t.flags & F_REV;
   const float ld = lin_ld(a.ld[t.h]);
@@ -156,9 +158,10 @@ __device__ __forceinline__ void lin_factors(const LinArgs& a, const LinInfo& t, 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int j = 2 * lane + i;
+    const bool there = j < t.n;
     // in time: lam^{n-1-j} and scale lam^{j+1}; backwards: scale lam^{j+1} and lam^{n-1-j}
-    const float w = a.scale * expf(ld * (float)j);
-    const float up = a.scale * expf(ld * (float)(j + 1)), down = j < t.n ? expf(ld * (float)(t.n - 1 - j)) : 0.0f;
+    const float w = there ? a.scale * expf(ld * (float)j) : 0.0f;
+    const float up = there ? a.scale * expf(ld * (float)(j + 1)) : 0.0f, down = there ? expf(ld * (float)(t.n - 1 - j)) : 0.0f;
     fk[i] = rev ? up : down;
     v.fo[j] = rev ? down : up;
     const float before = rev && j ? 0.0f : w, after = rev || !j ? w : 0.0f;

@@ -365,3 +365,24 @@ def test_gradients_against_differences():
         want = (r[d].double() * u).sum().item()
         size = (r[d].double().norm() * u.double().norm()).item()
         assert abs((up - down) / (2 * h) - want) <= 1e-5 * size
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,ld", [(2, 2, 40.0), (2, 7, 2.0), (2, 7, 11.0), (1, 33, 2.4), (2, 45, 1.7), (60, 7, 9.0)])
+def test_growing_heads_of_short_sequences(dt, B, T, ld):
+    """A head that grows, beside one that fades: everything is finite where the
+    growth over the sequence is, whatever it would be over a whole chunk.
+    (exp of up to 80 rounds its argument: 2^-18 of the value, within the
+    tolerances.)"""
+    x = lin_inputs(B, T, 2, 4, 64, 72, DT[dt], seed=T, device="cuda", log_decay=[ld, -0.1])
+    _check_all(_run(x), lin_ref_grads(x, 64 ** -0.5), NAMES + ["d_state"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_growing_heads_behind_the_last_whole_chunk(dt):
+    """100 tokens that grow past f32's range: the first 36 in time and the last
+    36 backwards in time do not know of it."""
+    x = lin_inputs(1, 100, 1, 2, 64, 64, DT[dt], seed=1, device="cuda", log_decay=[1.5, -0.1])
+    got, ref = _run(x), lin_ref_grads(x, 64 ** -0.5)
+    part = {"o": slice(0, 36), "dq": slice(0, 36), "dk": slice(64, 100), "dv": slice(64, 100)}
+    _check_all({n: got[n][:, s, :1] for n, s in part.items()}, {n: ref[n][:, s, :1] for n, s in part.items()}, list(part))
