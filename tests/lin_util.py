@@ -36,12 +36,12 @@ def lin_ref(q, k, v, log_decay, state, scale):
     return (torch.stack(outs, 1) if outs else v.new_zeros(B, 0, Hv, dv)), S
 
 
-def lin_ref_grads(x, scale):
+def lin_ref_grads(x, scale, ref=lin_ref):
     """float64 results and gradients on x's values: dict with o, state_out, dq,
     dk, dv and d_state."""
     names = ["q", "k", "v"] + (["state"] if x["state"] is not None else [])
     f = {n: x[n].detach().double().clone().requires_grad_() for n in names}
-    o, S = lin_ref(f["q"], f["k"], f["v"], x["log_decay"].double(), f.get("state"), scale)
+    o, S = ref(f["q"], f["k"], f["v"], x["log_decay"].double(), f.get("state"), scale)
     loss = (o * x["d_o"].double()).sum()
     if x["d_state_out"] is not None:
         loss = loss + (S * x["d_state_out"].double()).sum()
@@ -105,3 +105,23 @@ def rel(got, ref):
         return float("inf")
     n = ref.norm().item()
     return (got - ref).norm().item() / (n if n > 0 else 1.0)
+
+
+def lin_ref_chunked(q, k, v, log_decay, state, scale, chunk=64):
+    """``lin_ref`` by chunks, for long sequences of finite values;
+    differentiable."""
+    B, T, Hv, dv = v.shape
+    Hk, dk = k.shape[2:]
+    q, k, v = (x.repeat_interleave(Hv // x.shape[2], 2).transpose(1, 2) for x in (q, k, v))  # [B, H, T, d]
+    S = torch.zeros(B, Hv, dk, dv, dtype=v.dtype, device=v.device) if state is None else state
+    i = torch.arange(chunk, device=v.device)
+    ld = log_decay[:, None, None]
+    pairs = torch.where(i[:, None] < i, 0.0, torch.exp(ld * (i[:, None] - i).clamp(min=0)))
+    outs = []
+    for t in range(0, T, chunk):
+        qc, kc, vc = (x[:, :, t:t + chunk] for x in (q, k, v))
+        n = vc.shape[2]
+        o = ((qc @ kc.transpose(-1, -2)) * pairs[:, :n, :n]) @ vc + torch.exp(ld * (i[:n, None] + 1)) * (qc @ S)
+        S = torch.exp(ld * n) * S + (kc * torch.exp(ld * (n - 1 - i[:n, None]))).transpose(-1, -2) @ vc
+        outs.append(scale * o)
+    return torch.cat(outs, 2).transpose(1, 2), S

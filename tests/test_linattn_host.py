@@ -7,7 +7,7 @@ import ctypes
 import pytest
 import torch
 
-from lin_util import lin_inputs, lin_ref, lin_ref_grads, rot_inputs, rot_ref, rot_ref_grads
+from lin_util import lin_inputs, lin_ref, lin_ref_chunked, lin_ref_grads, rel, rot_inputs, rot_ref, rot_ref_grads
 from mamba_selective_scan_gb300 import binding, build
 
 F32, BF16 = binding.M3_F32, binding.M3_BF16
@@ -183,3 +183,12 @@ def test_definitions_against_differences():
             num = (loss({**at, n: at[n] + eps * d}) - loss({**at, n: at[n] - eps * d})) / (2 * eps)
             ana = (want[g] * d).sum().item()
             assert abs(num - ana) <= 1e-6 * max(1.0, abs(ana)), n
+
+
+def test_definition_by_chunks():
+    """Whole and short chunks against the recurrence, gradients too; in 64 bits
+    both are sums of a few hundred roundings of 2^-53."""
+    for T in (64, 130, 9):
+        x = lin_inputs(2, T, 2, 4, 16, 24, torch.float32, seed=1)
+        a, b = lin_ref_grads(x, 0.3), lin_ref_grads(x, 0.3, lin_ref_chunked)
+        assert all(rel(b[n], a[n]) <= 1e-13 for n in a)
