@@ -552,7 +552,8 @@ m3_status m3scan_delta_decode(const m3_delta_dims* dims, m3_dtype act, const voi
  * 256; tensors whose heads and tokens start on 16 bytes (and, not
  * interleaved, rot_dim / 2 a multiple of 8 for bf16, 4 for f32) run the vector
  * kernels.  The weights' gradients are fixed-order sums: identical bits on
- * every call.
+ * every call.  A value or weight that is not finite reaches its pair where it
+ * turns, through the sums its head, and nothing else.
  */
 typedef struct {
     int64_t batch, seq_len, q_heads, k_heads, head_dim, rot_dim;

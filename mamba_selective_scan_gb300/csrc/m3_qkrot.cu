@@ -166,8 +166,11 @@ template <int VEC, bool IL> __device__ __forceinline__ void slot_at(const RotArg
 // group heads at a time, with the token's cosines and sines (and the weights)
 // in registers and the next groups' values on their way, across units.  A
 // warp makes its token's cosines and sines itself, so no barrier stands
-// between units.  Blocks take the queries or the keys.
-template <typename T, int VEC, int NS, bool IL, bool BWD>
+// between units.  Blocks take the queries or the keys.  PART: not all of a head
+// turns (4 x 4096 with 40 + 40 heads, half turned, 122 -> 124 us forward; as a
+// condition in one kernel for all it cost the backward of 8 x 2048 with 12 + 12
+// heads a third, 66 -> 86 us).
+template <typename T, int VEC, int NS, bool IL, bool BWD, bool PART>
 __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_constant__ RotArgs a) {
   constexpr int ROW = VEC > 1 ? ROT_DMAX / 2 : 32 * NS;  // pairs of a head, at most
   __shared__ __align__(16) float2 cs_all[ROT_WARPS][ROW];
@@ -208,6 +211,13 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_c
     }
   };
   if (BWD) weights();
+  // PART: x of slot i's pairs 2 j and 2 j + 1 that turn, 0 of those that do not: a
+  // value (or a weight) that is not finite stays out of the one it shares a pair with
+  auto turned = [&](int i, int j, float2 x) {
+    if (!PART) return x;
+    const int m = (u0 + i * group) * VEC + 2 * j;
+    return make_float2(m < a.R ? x.x : 0.0f, m + 1 < a.R ? x.y : 0.0f);
+  };
   P dw[BWD ? NS : 1];
 #pragma unroll
   for (int i = 0; i < (BWD ? NS : 1); ++i) dw[i].zero();
@@ -324,9 +334,9 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_c
         si[i][j] = make_float2(c0.y, c1.y);
         if constexpr (!BWD) {
           wc[i][j] = __fmul2_rn(w[i].q[j], co[i][j]);
-          ws[i][j] = neg2(__fmul2_rn(w[i].q[j], si[i][j]));
+          ws[i][j] = turned(i, j, neg2(__fmul2_rn(w[i].q[j], si[i][j])));
           co[i][j] = __fmul2_rn(w[i].p[j], co[i][j]);
-          si[i][j] = __fmul2_rn(w[i].p[j], si[i][j]);
+          si[i][j] = turned(i, j, __fmul2_rn(w[i].p[j], si[i][j]));
         }
       }
     }
@@ -358,8 +368,8 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             const float2 p = __fmul2_rn(v[i].p[j], r2), q = __fmul2_rn(v[i].q[j], r2);
-            v[i].p[j] = __ffma2_rn(p, co[i][j], __fmul2_rn(q, ws[i][j]));
-            v[i].q[j] = __ffma2_rn(p, si[i][j], __fmul2_rn(q, wc[i][j]));
+            v[i].p[j] = __ffma2_rn(p, co[i][j], __fmul2_rn(turned(i, j, q), ws[i][j]));
+            v[i].q[j] = __ffma2_rn(turned(i, j, p), si[i][j], __fmul2_rn(q, wc[i][j]));
           }
       } else {
         // u = r dn w,  dx = u - x r^2 mean(u x)
@@ -369,7 +379,8 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_c
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             const float2 p = __fmul2_rn(u[i].p[j], r2), q = __fmul2_rn(u[i].q[j], r2);
-            const float2 np = __ffma2_rn(p, co[i][j], __fmul2_rn(q, si[i][j])), nq = __ffma2_rn(q, co[i][j], __fmul2_rn(p, neg2(si[i][j])));
+            const float2 np = __ffma2_rn(p, co[i][j], __fmul2_rn(turned(i, j, q), si[i][j]));
+            const float2 nq = __ffma2_rn(q, co[i][j], __fmul2_rn(turned(i, j, p), neg2(si[i][j])));
             dw[i].p[j] = __ffma2_rn(np, v[i].p[j], dw[i].p[j]);
             dw[i].q[j] = __ffma2_rn(nq, v[i].q[j], dw[i].q[j]);
             u[i].p[j] = __fmul2_rn(np, w[i].p[j]);
@@ -495,9 +506,9 @@ RotArgs rot_args(const m3_qkrot_dims* d, const void* q, const void* k, const flo
   return a;
 }
 
-template <typename T, int VEC, int NS, bool IL, bool BWD>
+template <typename T, int VEC, int NS, bool IL, bool BWD, bool PART>
 cudaError_t rot_go(RotArgs& a, cudaStream_t s) {
-  auto kern = m3_qkrot_kernel<T, VEC, NS, IL, BWD>;
+  auto kern = m3_qkrot_kernel<T, VEC, NS, IL, BWD, PART>;
   int sms = 0, occ = 0;
   const size_t smem = BWD ? (size_t)ROT_WARPS * a.D * 4 : 0;
   cudaError_t e = sm_count(&sms);
@@ -529,18 +540,23 @@ cudaError_t rot_go(RotArgs& a, cudaStream_t s) {
   return e;
 }
 
-template <typename T, bool BWD>
-cudaError_t rot_launch(RotArgs a, bool vec, bool il, cudaStream_t s) {
+template <typename T, bool IL, bool BWD, bool PART>
+cudaError_t rot_pick(RotArgs& a, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int v = vec ? V : 1;
   a.np = (a.D + 2 * v - 1) / (2 * v);
   a.group = 1;
   while (a.group < a.np && a.group < 32) a.group *= 2;
   const int per = (a.np + a.group - 1) / a.group;
-  if (vec) return il ? rot_go<T, V, 1, true, BWD>(a, s) : rot_go<T, V, 1, false, BWD>(a, s);
-  if (per == 1) return il ? rot_go<T, 1, 1, true, BWD>(a, s) : rot_go<T, 1, 1, false, BWD>(a, s);
-  if (per == 2) return il ? rot_go<T, 1, 2, true, BWD>(a, s) : rot_go<T, 1, 2, false, BWD>(a, s);
-  return il ? rot_go<T, 1, 4, true, BWD>(a, s) : rot_go<T, 1, 4, false, BWD>(a, s);
+  if (vec) return rot_go<T, V, 1, IL, BWD, PART>(a, s);
+  if (per == 1) return rot_go<T, 1, 1, IL, BWD, PART>(a, s);
+  if (per == 2) return rot_go<T, 1, 2, IL, BWD, PART>(a, s);
+  return rot_go<T, 1, 4, IL, BWD, PART>(a, s);
+}
+template <typename T, bool BWD>
+cudaError_t rot_launch(RotArgs a, bool vec, bool il, cudaStream_t s) {
+  if (2 * a.R == a.D) return il ? rot_pick<T, true, BWD, false>(a, vec, s) : rot_pick<T, false, BWD, false>(a, vec, s);
+  return il ? rot_pick<T, true, BWD, true>(a, vec, s) : rot_pick<T, false, BWD, true>(a, vec, s);
 }
 
 // 16-byte vectors: heads and tokens of every tensor start on 16 bytes, and a

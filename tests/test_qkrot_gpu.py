@@ -249,3 +249,48 @@ def test_gradients_against_differences():
         want = (r[d].double() * u).sum().item()
         size = (r[d].double().norm() * u.double().norm()).item()
         assert abs(diff - want) <= 1e-3 * size
+
+
+@pytest.mark.parametrize("il", [False, True])
+@pytest.mark.parametrize("D,rot,dt", [(64, 32, "bf16"), (80, 48, "f32"), (80, 50, "bf16"), (37, 22, "f32"), (128, 4, "bf16"), (128, 126, "f32")])
+@pytest.mark.parametrize("name,value", [("q", float("inf")), ("q", float("nan")), ("dq_out", float("inf")), ("dq_out", float("nan")),
+                                        ("q_weight", float("-inf")), ("q_weight", float("nan"))])
+def test_not_finite_among_values_that_do_not_turn(name, value, D, rot, dt, il):
+    """A value or a weight behind the turned ones that is not finite reaches
+    what the definition says: its own output and the head's sums, not the
+    values that it lies beside."""
+    x = rot_inputs(2, 5, 3, 1, D, rot, DT[dt], seed=D, device="cuda")
+    for place in {rot, D - 1}:
+        y = dict(x)
+        y[name] = x[name].clone()
+        y[name][(..., place) if name == "q_weight" else (1, 3, 2, place)] = value
+        got, ref = _run(y, il), rot_ref_grads(y, EPS, il)
+        for n, want in ref.items():
+            fine = torch.isfinite(want)
+            assert torch.equal(torch.isfinite(got[n]).cpu(), fine), n
+            assert rel(got[n][fine.cuda()], want[fine]) <= (2e-6 if n.startswith("d_") else TOL[got[n].dtype]), n
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_not_finite_weight_of_a_pair(dt):
+    """The weight of a turned value reaches both values of its pair."""
+    x = rot_inputs(2, 5, 3, 1, 64, 32, DT[dt], seed=1, device="cuda")
+    x["k_weight"][21] = float("inf")
+    bad = (~torch.isfinite(_run(x)["k_out"])).flatten(0, 2).all(0).nonzero().flatten().tolist()
+    assert bad == [5, 21] and torch.equal(torch.isfinite(_run(x)["k_out"]).cpu(), torch.isfinite(rot_ref_grads(x, EPS, False)["k_out"]))
+
+
+@pytest.mark.parametrize("il", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_row_of_zeros_without_eps(dt, il):
+    """0 / 0 in that head alone: its outputs, its gradient, and the weight's
+    gradient, to which it adds."""
+    x = rot_inputs(2, 4, 3, 2, 64, 48, DT[dt], seed=1, device="cuda")
+    x["q"][1, 2, 1] = 0
+    got, ref = _run(x, il, eps=0.0), rot_ref_grads(x, 0.0, il)
+    for n, want in ref.items():
+        fine = torch.isfinite(want)
+        assert torch.equal(torch.isfinite(got[n]).cpu(), fine), n
+        if fine.any():
+            assert rel(got[n][fine.cuda()], want[fine]) <= (2e-6 if n.startswith("d_") else TOL[got[n].dtype]), n
+    assert not torch.isfinite(ref["q_out"]).all() and not torch.isfinite(ref["d_q_weight"]).any()
