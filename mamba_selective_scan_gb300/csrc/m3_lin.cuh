@@ -46,11 +46,15 @@ struct LinArgs {
   unsigned* status;
   int nc;                // chunks of a sequence
   bool stream;           // tensor-core kernels: equal shares of all items' chunks, one block per SM
-  unsigned* flags;       // stream: per item, set once its state was handed over (in seg_start)
+  unsigned* flags;       // stream: per block, set once it handed on its state (in seg_start)
   int segs, seg_chunks;  // else: time segments, chunks per segment
-  float *seg_end, *seg_start;  // [items][segs][128][128]: ends from a zero start, start states
+  float *seg_end, *seg_start;  // [items][segs][128][128]: ends from a zero start, start states; stream: seg_start [blocks][128][128]
 };
 constexpr int LIN_C = 64;  // tokens per chunk
+// The SMs of a GB300.  Plans are made for them, without a device, so that a
+// plan's bytes are the same wherever it is made; a launch takes the SMs that
+// there are, and no more blocks of equal shares than these.
+constexpr int LIN_SMS = 152;
 
 // (a comparison, not fmaxf: a decay that is NaN stays one)
 __device__ __forceinline__ float lin_ld(float x) { return x < LIN_LD_MIN ? LIN_LD_MIN : x; }

@@ -65,11 +65,11 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 // 8 x 128 x 4, one: 80, two 108.
 double lin_cost(int64_t items, int m, int S, bool tc) {
   if (tc) {
-    const double all = (double)((items * S + 151) / 152) * (m + 8.0);
-    return S > 1 ? all + (double)((items * (S - 1) + 151) / 152) * (0.8 * m + 2.0) + 4.0 + 0.3 * S : all;
+    const double all = (double)((items * S + LIN_SMS - 1) / LIN_SMS) * (m + 8.0);
+    return S > 1 ? all + (double)((items * (S - 1) + LIN_SMS - 1) / LIN_SMS) * (0.8 * m + 2.0) + 4.0 + 0.3 * S : all;
   }
   auto units = [&](int64_t parts) {
-    const int64_t blocks = (4 * parts + 151) / 152;  // of an SM
+    const int64_t blocks = (4 * parts + LIN_SMS - 1) / LIN_SMS;  // of an SM
     const double rest[3] = {0.0, 1.5, 2.4};
     return (double)(blocks / 3 * 3) + rest[blocks % 3];
   };
@@ -80,7 +80,7 @@ void lin_segments(int64_t items, int nc, bool tc, int* segs, int* seg_chunks) {
   double best = 0.0;
   *segs = 1;
   *seg_chunks = nc < 1 ? 1 : nc;
-  for (int want = 1; want <= 152 && want * least <= (nc > least ? nc : least); ++want) {
+  for (int want = 1; want <= LIN_SMS && want * least <= (nc > least ? nc : least); ++want) {
     const int m = (nc + want - 1) / want;
     if (m < 1) break;
     const int S = (nc + m - 1) / m;
@@ -115,12 +115,13 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     const int64_t items = (int64_t)(i ? 3 : 1) * p->B * p->Hv;
     w.segs = 1;
     w.seg_chunks = p->nc;
-    w.stream = p->tc && items > 152;
+    w.stream = p->tc && items > LIN_SMS;
     if (!w.stream && p->T > 1) lin_segments(items, p->nc, p->tc, &w.segs, &w.seg_chunks);
-    const size_t slots = (size_t)items * w.segs * LIN_DMAX * LIN_DMAX * 4;
-    w.o_start = take(w.stream || w.segs > 1 ? slots : 0);
-    w.o_end = take(w.segs > 1 ? slots : 0);
-    w.o_flags = take(w.stream ? (size_t)items * 4 : 0);
+    // a block of equal shares hands on one state at most; segments have their starts and their ends
+    const size_t slot = (size_t)LIN_DMAX * LIN_DMAX * 4, slots = w.segs > 1 ? (size_t)items * w.segs : 0;
+    w.o_start = take((w.stream ? LIN_SMS : slots) * slot);
+    w.o_end = take(slots * slot);
+    w.o_flags = take(w.stream ? LIN_SMS * 4 : 0);
     if (i == 0) p->fwd_ws_bytes = off > align_up(STATUS_BYTES, 256) ? off : 0;  // (no more than a status block: none at all)
   }
   // the backward's: shares of dq and dk where key heads are shared, and a

@@ -527,12 +527,12 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
 #pragma unroll
             for (int k = 0; k < 64; ++k) dst[k * LIN_DMAX] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
           } else if (t.flags & F_GIVE) {
-            float* dst = a.seg_start + ((size_t)t.item * LIN_DMAX + hf * 64) * LIN_DMAX + row;
+            float* dst = a.seg_start + ((size_t)blockIdx.x * LIN_DMAX + hf * 64) * LIN_DMAX + row;
 #pragma unroll
             for (int k = 0; k < 64; ++k) dst[k * LIN_DMAX] = k & 1 ? S[k >> 1].y : S[k >> 1].x;
             __threadfence();
             bar_sync(1, GROUP);
-            if (tid == 0) flag_set(a.flags + t.item);
+            if (tid == 0) flag_set(a.flags + blockIdx.x);
           } else if (p.s_out && t.w == a.nc - 1 && row < p.DV) {  // (never transposed)
             float* dst = p.s_out + (((size_t)t.b * a.Hv + t.h) * p.DK + hf * 64) * p.DV + row;
             const int live = p.DK - hf * 64;  // (a multiple of 8)
@@ -560,9 +560,11 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
         wait(&s.full[g.i], g.par);
         const LinInfo t = s.info[n & 7];
         const LinPass& p = a.p[t.pass];
-        if (t.flags & F_TAKE && wait.ok()) wait.tries = flag_wait(a.flags + t.item) ? wait.tries : 0;
+        // (handed on by the share before, of the same pass)
+        if (t.flags & F_TAKE && wait.ok()) wait.tries = flag_wait(a.flags + (blockIdx.x - np)) ? wait.tries : 0;
         if (t.w > 0 || a.segs > 1) {
-          const float* src = a.seg_start + (((size_t)t.item * a.segs + seg) * LIN_DMAX + hf * 64) * LIN_DMAX + row;
+          const size_t slot = t.flags & F_TAKE ? blockIdx.x - np : (size_t)t.item * a.segs + seg;
+          const float* src = a.seg_start + (slot * LIN_DMAX + hf * 64) * LIN_DMAX + row;
 #pragma unroll
           for (int k = 0; k < 64; ++k) (k & 1 ? S[k >> 1].y : S[k >> 1].x) = __ldcg(src + k * LIN_DMAX);
         } else {
@@ -871,10 +873,10 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
   }
   const auto kern = a.nc <= 8 ? m3_lin_tc_kernel<false, true> : m3_lin_tc_kernel<false, false>;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-  if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, (size_t)items * 4, st);
+  if (e == cudaSuccess && a.stream) e = cudaMemsetAsync(a.flags, 0, LIN_SMS * 4, st);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = a.stream ? dim3(delta_share_blocks((int64_t)a.B * a.Hv, sms / a.np) * a.np) : dim3((unsigned)items, (unsigned)a.segs);
+  cfg.gridDim = a.stream ? dim3(delta_share_blocks((int64_t)a.B * a.Hv, (sms < LIN_SMS ? sms : LIN_SMS) / a.np) * a.np) : dim3((unsigned)items, (unsigned)a.segs);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = st;

@@ -192,3 +192,14 @@ def test_definition_by_chunks():
         x = lin_inputs(2, T, 2, 4, 16, 24, torch.float32, seed=1)
         a, b = lin_ref_grads(x, 0.3), lin_ref_grads(x, 0.3, lin_ref_chunked)
         assert all(rel(b[n], a[n]) <= 1e-13 for n in a)
+
+
+def test_linattn_workspace_of_many_heads(lib):
+    """With more heads than SMs what a workspace holds for the heads handed on
+    does not grow with them: a state of 64 KB per SM and direction, and for the
+    backward a copy of d_state."""
+    for B, T in ((256, 512), (64, 4096), (1024, 130)):
+        st, p = _lin_plan(_lin(batch=B, seq_len=T, k_heads=40, v_heads=40, head_k=128))
+        hand = 152 * (64 << 10) + (64 << 10)
+        assert st == 0 and p.fwd_workspace_bytes <= hand
+        assert p.workspace_bytes <= 2 * hand + B * 40 * 128 * 128 * 4
