@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(ROT_THREADS, 2) m3_qkrot_kernel(const __grid_c
       work(g, 0);
       if constexpr (AHEAD > 1) {
         if (g + 1 < now.g1) work(g + 1, 1);
-        else if (then.g0 + 1 < then.g1) fetch(val[1], then.tok, then.g0 + 1);
+        else if (g == now.g0 && then.g0 + 1 < then.g1) fetch(val[1], then.tok, then.g0 + 1);  // (of more groups the last pair fetched it)
       }
     }
     now = then;
