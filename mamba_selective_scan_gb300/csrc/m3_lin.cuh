@@ -31,7 +31,7 @@ struct LinPass {
   const float* s_in;     // NULL = zero
   float* s_out;          // NULL = not wanted
   int64_t qs, ks, vs, os;  // elements between tokens
-  int qh, kh, vh, oh;      // value heads that share a head of each
+  int qh, kh, vh;          // value heads that share a head of each (outputs have one of their own)
   int DK, DV;              // sizes of the pass's keys and values
   bool rev;                // backwards in time
   bool st;                 // states are given transposed, [DV][DK]

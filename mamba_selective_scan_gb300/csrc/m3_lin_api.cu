@@ -106,7 +106,7 @@ m3_status lin_plan(const m3_linattn_dims* d, m3_dtype act, LinPlan* p) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  // (a few tokens by the recurrence, without the chunks' latency)
+  // (one token by the recurrence, without a chunk's latency)
   p->tc = act == M3_BF16 && p->T > 1;
   p->nc = (p->T + LIN_C - 1) / LIN_C;
   if ((int64_t)3 * p->B * p->Hv * p->nc > 0x7FFFFFFF) return M3_ERR_DIMS;  // chunks are counted in 32 bits
@@ -154,7 +154,7 @@ LinPass lin_fwd_pass(const m3_linattn_dims* d, const LinPlan& p, const void* q, 
   r.qs = or_dense(d->q_stride, kw); r.ks = or_dense(d->k_stride, kw); r.vs = or_dense(d->v_stride, vw);
   r.os = vw;
   r.qh = r.kh = p.share;
-  r.vh = r.oh = 1;
+  r.vh = 1;
   r.DK = p.DK; r.DV = p.DV;
   return r;
 }
@@ -293,7 +293,7 @@ m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const vo
   pk.s_in = d_state_out;
   pk.out = shared ? part[1] : dk;
   pk.os = shared ? pw : or_dense(dims->dk_stride, kw);
-  pk.oh = 1; pk.out_f32 = shared || act == M3_F32;
+  pk.out_f32 = shared || act == M3_F32;
   LinPass& pv = a.p[1];
   pv.q = k; pv.qs = f.ks; pv.qh = p.share;
   pv.k = q; pv.ks = f.qs; pv.kh = p.share;
@@ -301,7 +301,7 @@ m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const vo
   pv.DK = p.DK; pv.DV = p.DV;
   pv.rev = true;
   pv.s_in = d_state_out; pv.s_out = d_state;
-  pv.out = dv; pv.os = or_dense(dims->dv_stride, vw); pv.oh = 1;
+  pv.out = dv; pv.os = or_dense(dims->dv_stride, vw);
   LinPass& pq = a.p[2];
   pq.q = d_o; pq.qs = vw; pq.qh = 1;
   pq.k = v; pq.ks = f.vs; pq.kh = 1;
@@ -311,7 +311,7 @@ m3_status m3scan_linattn_bwd(const m3_linattn_dims* dims, m3_dtype act, const vo
   pq.s_in = state;
   pq.out = shared ? part[0] : dq;
   pq.os = shared ? pw : or_dense(dims->dq_stride, kw);
-  pq.oh = 1; pq.out_f32 = pk.out_f32;
+  pq.out_f32 = pk.out_f32;
   cudaError_t e = lin_launch(a, p, act, workspace, s);
   if (e == cudaSuccess && shared) {
     LinShare sh{};

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(SEQ_THREADS, 3) m3_lin_seq_kernel(const __grid
   const T* kp = static_cast<const T*>(p.k) + tok0 * p.ks + (int64_t)(h / p.kh) * p.DK;
   const T* qp = static_cast<const T*>(p.q) + tok0 * p.qs + (int64_t)(h / p.qh) * p.DK;
   const T* vp = static_cast<const T*>(p.v) + tok0 * p.vs + (int64_t)(h / p.vh) * p.DV + v0;
-  const size_t ob = (size_t)tok0 * p.os + (size_t)(h / p.oh) * p.DV + v0;
+  const size_t ob = (size_t)tok0 * p.os + (size_t)h * p.DV + v0;
   auto time = [&](int i) { return (int64_t)(p.rev ? a.T - 1 - i : i); };  // of the pass's i-th token
 
   // four values a thread on their way into a tile, zeros past the ends
@@ -275,9 +275,11 @@ template <typename T>
 cudaError_t launch_lin_seq(const LinArgs& a, cudaStream_t st) {
   const unsigned x = (unsigned)((int64_t)a.B * a.Hv * (LIN_DMAX / (SEQ_THREADS / 8 * SEQ_COLS)));
   cudaError_t e = cudaSuccess;
-  if (a.segs > 1) {  // (the last segment's end is nobody's start)
-    e = launch_k(m3_lin_seq_kernel<T, true>, dim3(x, a.np, a.segs - 1), SEQ_THREADS, 0, st, false, a);
-    if (e == cudaSuccess) e = launch_lin_seg(a, st);
+  if constexpr (sizeof(T) == 4) {  // (bf16 has segments on the tensor cores alone)
+    if (a.segs > 1) {  // (the last segment's end is nobody's start)
+      e = launch_k(m3_lin_seq_kernel<T, true>, dim3(x, a.np, a.segs - 1), SEQ_THREADS, 0, st, false, a);
+      if (e == cudaSuccess) e = launch_lin_seg(a, st);
+    }
   }
   return e == cudaSuccess ? launch_k(m3_lin_seq_kernel<T, false>, dim3(x, a.np, a.segs), SEQ_THREADS, 0, st, a.segs > 1, a) : e;
 }

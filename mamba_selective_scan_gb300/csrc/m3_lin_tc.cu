@@ -361,9 +361,9 @@ m3_lin_tc_kernel(const __grid_constant__ LinArgs a, const __grid_constant__ LinM
           const LinInfo& t = s.info[n & 7];
           const LinPass& p = a.p[t.pass];
           if (wait.ok()) {
-            const int h = p.oh == 1 ? t.h : t.h / p.oh, cols = p.out_f32 ? 32 : 64;
+            const int cols = p.out_f32 ? 32 : 64;
             for (int col = 0, at = OUT; col < p.DV; col += cols, at += TILE)
-              tma_tile_store(&maps.m[t.pass][3], st0 + at, col, h, t.tok, t.b);
+              tma_tile_store(&maps.m[t.pass][3], st0 + at, col, t.h, t.tok, t.b);
             bulk_commit();
             bulk_wait_read();
           }
@@ -861,7 +861,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, cudaStream_t st, int sms) {
         !delta_tile_map(&maps.m[i][1], p.k, p.DK, a.Hv / p.kh, a.T, a.B, p.ks) ||
         !delta_tile_map(&maps.m[i][2], p.v, p.DV, a.Hv / p.vh, a.T, a.B, p.vs))
       return cudaErrorInvalidValue;
-    if (!delta_tile_map(&maps.m[i][3], p.out, p.DV, a.Hv / p.oh, a.T, a.B, p.os, p.out_f32)) return cudaErrorInvalidValue;
+    if (!delta_tile_map(&maps.m[i][3], p.out, p.DV, a.Hv, a.T, a.B, p.os, p.out_f32)) return cudaErrorInvalidValue;
   }
   const int64_t items = (int64_t)a.np * a.B * a.Hv;
   cudaError_t e = cudaSuccess;
