@@ -632,7 +632,8 @@ typedef struct {
 } m3_linattn_dims;
 
 typedef struct {
-    int64_t workspace_bytes;     /* enough for both directions */
+    int64_t workspace_bytes;     /* enough for both directions, a backward whose d_state is
+                                    d_state_out too (which needs a copy of it) */
     int64_t fwd_workspace_bytes; /* enough for m3scan_linattn_fwd; 0: it may be NULL (such
                                     a call reports to m3scan_device_status only) */
     int32_t fwd_launches, bwd_launches;

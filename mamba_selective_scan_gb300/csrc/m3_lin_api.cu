@@ -52,7 +52,7 @@ m3_status lin_validate(const m3_linattn_dims* d, m3_dtype act) {
 // end; with S segments, first the ends of the S - 1 earlier ones are found (0.8
 // units per chunk, two more), then a kernel chains them, then all S run.  The
 // count with the least total is taken, with at least three chunks per segment.
-// 16 heads of 1024 chunks: nine segments, 263 us, where one takes 1200 and eight
+// 16 heads of 1024 chunks: nine segments, 266 us, where one takes 1200 and eight
 // 282; 24 of 128: six, 70, where one takes 163 and seven 87; 12 of 16: five, 26,
 // where one takes 30; 48 of 32: three, 46, where one takes 49 and two 54; 72 of
 // 64: one, 88, where two take 93.

@@ -278,11 +278,11 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 x) { return *reinterpr
 // cycles a chunk, the longest of the roles).  Measured: 8 x 2048 x 12 heads 49
 // us; 4 x 4096 x 40 heads, forward 110 us (650 MB: 87 % of HBM's rate), the three
 // backward passes side by side 284 us (1.56 GB, 81 %); 1 x 65536 x 16 heads in
-// nine segments 263 us.  Minutes of such work meet the power limit: at 1.7 GHz
-// the latter two take 450 and 294.
+// nine segments 266 us.  Seconds of such work meet the power limit: at 1.7 GHz a
+// forward and backward of the former take 457, the latter 302.
 //
 // Tried: each role's code unrolled by tile (11000 instructions: bound by their
-// fetches, 86 us for 8 x 2048 x 12 heads; rolled up it is 3600); a second warp
+// fetches, 86 us for 8 x 2048 x 12 heads; rolled up it is a third of that); a second warp
 // issuing MMAs, and prefetches of later chunks into L2 (no faster); P by four
 // warps of its own (8 x 2048 x 12 heads 55 us, heads of 64 x 64 17 % slower), or by
 // the warps of V' (55): every wait and arrival takes its share of the issue slots,
